@@ -7,10 +7,14 @@ indices a nondeterministic one.  Here the forward runs ``det_gather_rows`` and
 the adjoint runs ``det_scatter_add`` (1-D values) or ``det_scatter_add_rows``
 (row tables) of the library, so the gradient bits are the same on every run
 and at every launch shape.  Indices outside the source get zero outputs and
-send no gradient.  Argument marshalling only: every step runs in the
+send no gradient.  Two operators of language models follow the same rule: the log
+probabilities of given tokens, and the learned relative position bias, whose
+adjoint is a scatter-add on a few buckets.  Argument marshalling only: every step runs in the
 library's CUDA kernels (the gradient buffer is zero-filled by torch).
 """
 from __future__ import annotations
+
+from typing import Optional
 
 import torch
 
@@ -46,3 +50,60 @@ def gather(src: torch.Tensor, idx: torch.Tensor, row_offset: int = 0) -> torch.T
 
     ``src`` is float32 or float64 on CUDA, ``idx`` int32 on the same device."""
     return _Gather.apply(src, idx, int(row_offset))
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits: torch.Tensor, tokens: torch.Tensor):
+        r = det.det_token_logprobs(logits, tokens)
+        ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
+        ctx.set_materialize_grads(False)
+        return r.logprob, r.entropy
+
+    @staticmethod
+    def backward(ctx, grad_logprob, grad_entropy):
+        logits, tokens, lse, entropy = ctx.saved_tensors
+        if not ctx.needs_input_grad[0] or (grad_logprob is None and grad_entropy is None):
+            return None, None
+        return det.det_token_logprobs_backward(
+            logits, tokens, lse, entropy,
+            grad_logprob=None if grad_logprob is None else grad_logprob.contiguous(),
+            grad_entropy=None if grad_entropy is None else grad_entropy.contiguous()), None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """(log probability of each token, entropy of each row) under softmax(logits), float32.
+
+    logits is [..., vocab] (float32, bfloat16 or float16), tokens int32 of the leading shape; tokens outside the
+    vocabulary (padding) have log probability 0 and send no gradient."""
+    return _TokenLogprobs.apply(logits, tokens)
+
+
+class _RelativeBias(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, bounds, q_len, k_len, q_offset, bidirectional, batch, dtype):
+        ctx.save_for_backward(bounds)
+        ctx.how = dict(q_offset=q_offset, bidirectional=bidirectional, dtype=table.dtype)
+        out = det.det_relative_bias(table, bounds, q_len, k_len, q_offset=q_offset, bidirectional=bidirectional,
+                                    dtype=dtype)
+        return out if batch is None else out.expand(batch, *out.shape)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (bounds,) = ctx.saved_tensors
+        table_grad = None
+        if ctx.needs_input_grad[0]:
+            if grad.shape[-1] > 1 and grad.stride(-1) != 1:
+                grad = grad.contiguous()
+            table_grad = det.det_relative_bias_backward(grad, bounds, **ctx.how)
+        return (table_grad,) + (None,) * 7
+
+
+def relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_len: int, *, q_offset: int = 0,
+                  bidirectional: bool = False, batch: Optional[int] = None,
+                  dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """det.det_relative_bias with a deterministic gradient for the table.
+
+    With ``batch`` the result is expanded (not copied) to [batch, heads, q_len, k_len], and the gradient's sum over
+    the batch is taken with the buckets' sums, in one pass over the gradient."""
+    return _RelativeBias.apply(table, bounds, int(q_len), int(k_len), int(q_offset), bool(bidirectional), batch, dtype)

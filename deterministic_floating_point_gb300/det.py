@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -19,6 +20,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdet.so")
 
 F32, F64 = 0, 1
+BF16, F16 = 2, 3        # the language-model operators' 16-bit types (include/det_model.h)
+MAX_TOP_K, MAX_BOUNDS = 32, 2047
 OK = 0
 ERR_CUDA = 6   # DET_ERR_CUDA: a CUDA call or launch failed (detail: det_last_cuda_error)
 SCAN_INCLUSIVE, SCAN_EXCLUSIVE, SCAN_REVERSE = 0, 1, 2
@@ -29,7 +32,7 @@ SCAN_CHUNK = {torch.float32: 32768, torch.float64: 16384}
 _lock = threading.Lock()
 _lib = None
 
-_i64, _sz, _vp, _int = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int
+_i64, _sz, _vp, _int, _flt = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _SIGNATURES = {
     "det_sum_workspace_bytes": (_sz, [_i64, _int]),
     "det_sum": (_int, [_vp, _i64, _int, _vp, _vp, _sz, _int, _vp]),
@@ -54,6 +57,16 @@ _SIGNATURES = {
     "det_scan_i32": (_int, [_vp, _vp, _i64, _int, _vp, _vp, _sz, _int, _vp]),
     "det_slot_alloc_workspace_bytes": (_sz, [_i64, _i64]),
     "det_slot_alloc": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _int, _vp]),
+    "det_token_logprobs": (_int, [_vp, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp]),
+    "det_token_logprobs_backward": (_int, [_vp, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "det_relative_bias": (_int, [_vp, _int, _i64, _vp, _i64, _int, _i64, _i64, _i64, _vp, _int, _vp]),
+    "det_relative_bias_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _int]),
+    "det_relative_bias_backward": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _int, _i64,
+                                          _vp, _int, _vp, _sz, _vp]),
+    "det_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "det_paged_attention": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
+                                   _i64, _i64, _vp, _i64, _i64, _i64, _i64, _int, _flt, _vp, _int, _vp, _i64, _i64,
+                                   _vp, _vp, _vp, _sz, _vp]),
     "det_read_status": (_int, [_vp, _vp, ctypes.POINTER(_int)]),
     "det_status_string": (ctypes.c_char_p, [_int]),
     "det_last_cuda_error": (ctypes.c_char_p, []),
@@ -380,6 +393,295 @@ def det_segmented_scan(x: torch.Tensor, seg_offsets: torch.Tensor, y: torch.Tens
     _check(lib().det_segmented_scan(_ptr(x), _ptr(y), n, _ptr(seg_offsets), S, code, int(flags), _ptr(ws),
                                     ws.numel(), block_threads, _stream(stream)), "det_segmented_scan")
     return y
+
+
+# ---------------------------------------------------------------------------
+# operators of language models (include/det_model.h)
+
+_MODEL_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _model_code(t: torch.Tensor, name: str, codes=_MODEL_CODES) -> int:
+    code = codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {[str(d) for d in codes]}, got {t.dtype}")
+    return code
+
+
+def _on(device, dtype, name: str, t: torch.Tensor, shape=None, contiguous: bool = True) -> torch.Tensor:
+    """t, checked to be a tensor of this device, dtype and shape (each unless None)."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor on one device with the others")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _unit_stride(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return t
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that the work enqueued on `stream` writes: taken from that stream's memory (so no earlier work of
+    another stream still uses it), and kept from reuse while the caller's current stream works on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _model_ws(ws, nbytes, device, stream):
+    if ws is None:
+        # the allocator's blocks are 512-byte aligned
+        return _empty((max(int(nbytes), 256),), torch.uint8, device, stream)
+    if ws.numel() < nbytes:
+        raise DetError(4, "workspace")
+    return ws
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: Optional[torch.Tensor]
+    top_index: Optional[torch.Tensor]
+
+
+def _logit_rows(logits: torch.Tensor):
+    """(rows, vocab, elements from one row to the next) of [..., vocab] logits."""
+    _on(None, None, "logits", logits, contiguous=False)
+    if logits.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    vocab = logits.shape[-1]
+    _unit_stride(logits, "logits")
+    if logits.dim() == 2:
+        return logits.shape[0], vocab, logits.stride(0)
+    rows = logits.numel() // vocab if vocab else 0
+    if not logits.is_contiguous():
+        raise ValueError("logits of other than two dimensions must be contiguous")
+    return rows, vocab, vocab
+
+
+def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top_k: int = 0,
+                       stream=None) -> TokenLogprobs:
+    """Log probabilities of the tokens under softmax(logits), entropy, log-sum-exp and the top_k
+    alternatives of every row (see det_model.h).
+
+    logits is [..., vocab] (float32, bfloat16 or float16; two-dimensional logits may have any row stride), tokens
+    int32 of the leading shape, or None for the other results alone.  Results are float32 of the leading shape
+    (top_*: with top_k appended; top_index int32)."""
+    rows, vocab, stride = _logit_rows(logits)
+    code = _model_code(logits, "logits")
+    dev, lead = logits.device, logits.shape[:-1]
+    if tokens is not None:
+        _on(dev, torch.int32, "tokens", tokens, lead)
+    logprob = _empty(lead, torch.float32, dev, stream) if tokens is not None else None
+    entropy = _empty(lead, torch.float32, dev, stream)
+    lse = _empty(lead, torch.float32, dev, stream)
+    top_logprob = top_index = None
+    if top_k:
+        if not 0 < top_k <= min(vocab, MAX_TOP_K):
+            raise ValueError(f"top_k must be at most {MAX_TOP_K} and the vocabulary, got {top_k}")
+        top_logprob = _empty((*lead, top_k), torch.float32, dev, stream)
+        top_index = _empty((*lead, top_k), torch.int32, dev, stream)
+    _check(lib().det_token_logprobs(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob),
+                                    _ptr(entropy), _ptr(lse), int(top_k), _ptr(top_logprob), _ptr(top_index),
+                                    _stream(stream)), "det_token_logprobs")
+    return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
+
+
+def det_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], lse: torch.Tensor,
+                                entropy: Optional[torch.Tensor] = None, *,
+                                grad_logprob: Optional[torch.Tensor] = None,
+                                grad_entropy: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """The gradient for the logits of sum(grad_logprob * logprob + grad_entropy * entropy) (see det_model.h);
+    lse and entropy are det_token_logprobs' results.  Has the logits' dtype and shape."""
+    rows, vocab, stride = _logit_rows(logits)
+    code = _model_code(logits, "logits")
+    dev, lead = logits.device, logits.shape[:-1]
+    _on(dev, torch.float32, "lse", lse, lead)
+    for name, t in (("entropy", entropy), ("grad_logprob", grad_logprob), ("grad_entropy", grad_entropy)):
+        if t is not None:
+            _on(dev, torch.float32, name, t, lead)
+    if grad_logprob is not None and tokens is None:
+        raise ValueError("grad_logprob needs the tokens")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs the entropy")
+    if tokens is not None:
+        _on(dev, torch.int32, "tokens", tokens, lead)
+    if out is None:
+        out = _empty(logits.shape, logits.dtype, dev, stream)
+    else:
+        _on(dev, logits.dtype, "out", out, logits.shape, contiguous=out.dim() != 2)
+    _, _, out_stride = _logit_rows(out)
+    _check(lib().det_token_logprobs_backward(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
+                                             _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
+                                             out_stride, _stream(stream)), "det_token_logprobs_backward")
+    return out
+
+
+def det_relative_bounds(num_buckets: int, max_distance: int, *, bidirectional: bool = False,
+                        device="cuda") -> torch.Tensor:
+    """The bounds of the usual logarithmic buckets, for det_relative_bias: of the buckets of one direction the first
+    half (rounded down) hold one distance each, the others are logarithmic steps up to max_distance, and the
+    last one takes every distance from there.  Computed from the integers alone, so no distance moves between buckets by a
+    rounded logarithm."""
+    if num_buckets < 2 or (bidirectional and num_buckets % 2):
+        raise ValueError("num_buckets must be at least 2, and even when bidirectional")
+    n = num_buckets // 2 if bidirectional else num_buckets
+    exact = max(n // 2, 1)
+    if max_distance <= exact:
+        raise ValueError(f"max_distance must be above {exact}")
+    steps = n - exact
+    bounds = list(range(1, exact + 1))[:n - 1]
+    for j in range(1, steps):
+        # least d with log(d / exact) / log(max_distance / exact) * steps >= j
+        goal = max_distance ** j * exact ** (steps - j)
+        lo, hi = bounds[-1], max_distance
+        while lo < hi:
+            mid = (lo + hi) // 2
+            if mid ** steps >= goal:
+                hi = mid
+            else:
+                lo = mid + 1
+        bounds.append(lo)
+    return torch.tensor(bounds, dtype=torch.int32, device=device)
+
+
+def _bounds(bounds: torch.Tensor, device, bidirectional: bool):
+    """(number of bounds, number of buckets)"""
+    _on(device, torch.int32, "bounds", bounds)
+    if bounds.dim() != 1:
+        raise ValueError("bounds must have one dimension")
+    n = bounds.numel()
+    return n, (n + 1) * (2 if bidirectional else 1)
+
+
+def det_relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_len: int, *, q_offset: int = 0,
+                      bidirectional: bool = False, dtype: Optional[torch.dtype] = None,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[h, i, j] = table[bucket(j - i - q_offset), h], [heads, q_len, k_len] (see det_model.h).
+
+    table is [buckets, heads]; bounds int32, the least distance of each bucket after the first, in rising order
+    (det_relative_bounds); the result has the table's dtype unless dtype or out says otherwise."""
+    _on(None, None, "table", table)
+    if table.dim() != 2:
+        raise ValueError("table must be [buckets, heads]")
+    n, buckets = _bounds(bounds, table.device, bidirectional)
+    heads = table.shape[1]
+    if table.shape[0] != buckets:
+        raise ValueError(f"the table must have {buckets} rows for {n} bounds, got {table.shape[0]}")
+    table_code = _model_code(table, "table")
+    if out is None:
+        out = _empty((heads, q_len, k_len), dtype or table.dtype, table.device, stream)
+    else:
+        _on(table.device, dtype, "out", out, (heads, q_len, k_len))
+    _check(lib().det_relative_bias(_ptr(table), table_code, heads, _ptr(bounds), n, int(bidirectional), int(q_len),
+                                   int(k_len), int(q_offset), _ptr(out), _model_code(out, "out"), _stream(stream)),
+           "det_relative_bias")
+    return out
+
+
+def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_offset: int = 0,
+                               bidirectional: bool = False, dtype: torch.dtype = torch.float32,
+                               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient for det_relative_bias' table, [buckets, heads] of dtype: grad ([heads, q_len, k_len], or with a
+    batch in front over which the bias was broadcast) summed over the pairs of each bucket (see det_model.h).  grad
+    may have any strides but along the keys."""
+    _on(None, None, "grad", grad, contiguous=False)
+    if grad.dim() not in (3, 4):
+        raise ValueError("grad must be [heads, q_len, k_len] or [batch, heads, q_len, k_len]")
+    _unit_stride(grad, "grad")
+    n, buckets = _bounds(bounds, grad.device, bidirectional)
+    code = _model_code(grad, "grad")
+    batch, (heads, q_len, k_len) = (grad.shape[0] if grad.dim() == 4 else 1), grad.shape[-3:]
+    stride_b = grad.stride(0) if grad.dim() == 4 else 0
+    out = _empty((buckets, heads), dtype, grad.device, stream)
+    nbytes = lib().det_relative_bias_backward_workspace_bytes(batch, heads, q_len, k_len, n, int(bidirectional))
+    ws = _model_ws(workspace, nbytes, grad.device, stream)
+    _check(lib().det_relative_bias_backward(_ptr(grad), code, batch, heads, q_len, k_len, stride_b, grad.stride(-3),
+                                            grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset),
+                                            _ptr(out), _model_code(out, "dtype"), _ptr(ws), ws.numel(),
+                                            _stream(stream)), "det_relative_bias_backward")
+    return out
+
+
+class PagedAttention(NamedTuple):
+    out: torch.Tensor
+    lse: torch.Tensor
+
+
+def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                        lengths: torch.Tensor, *, scale: Optional[float] = None, max_len: Optional[int] = None,
+                        bias_table: Optional[torch.Tensor] = None, bias_bounds: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> PagedAttention:
+    """Attention of the last token of each sequence over its paged key-value cache (see det_model.h).
+
+    q is [batch, heads, head_dim] (bfloat16 or float16, head_dim 64, 128 or 256); the caches are [pages, page_size,
+    kv_heads, head_dim] views of any strides that are multiples of 8 elements; block_table is int32 [batch,
+    max_pages], lengths int32 [batch].  scale defaults to head_dim ** -0.5.  max_len, a bound on the lengths that
+    the host knows, saves launching for the whole table; longer sequences are cut at it.  bias_table
+    ([buckets, heads], with bias_bounds as in det_relative_bias) adds the learned relative position bias.
+    Returns the output, [batch, heads, head_dim] of q's dtype, and the log-sum-exp of the scores, float32 [batch, heads]."""
+    _on(None, None, "q", q, contiguous=False)
+    dev = q.device
+    code = _model_code(q, "q", {torch.bfloat16: BF16, torch.float16: F16})
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [batch, heads, head_dim] and the caches [pages, page_size, kv_heads, head_dim]")
+    batch, heads, dim = q.shape
+    pages, page_size, kv_heads = k_cache.shape[:3]
+    if dim not in (64, 128, 256):
+        raise ValueError(f"head_dim must be 64, 128 or 256, got {dim}")
+    if page_size < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError("page_size must be positive and heads a multiple of kv_heads")
+    _unit_stride(q, "q")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _on(dev, q.dtype, name, t, (pages, page_size, kv_heads, dim), contiguous=False)
+        _unit_stride(t, name)
+        if t.data_ptr() % 16 or any(st % 8 for st in t.stride()[:3]):
+            raise ValueError(f"{name} must be 16-byte aligned with strides that are multiples of 8 elements")
+    _on(dev, torch.int32, "block_table", block_table, contiguous=False)
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch, max_pages]")
+    _unit_stride(block_table, "block_table")
+    _on(dev, torch.int32, "lengths", lengths, (batch,))
+    bias_code = n_bounds = 0
+    if bias_table is not None:
+        if bias_bounds is None:
+            raise ValueError("bias_table needs bias_bounds")
+        n_bounds, buckets = _bounds(bias_bounds, dev, False)
+        bias_code = _model_code(bias_table, "bias_table")
+        _on(dev, None, "bias_table", bias_table)
+        if bias_table.dim() != 2 or bias_table.shape[1] != heads or bias_table.shape[0] not in (buckets, 2 * buckets):
+            raise ValueError(f"bias_table must be [{buckets} or {2 * buckets}, {heads}]")
+    capacity = min(block_table.shape[1] * page_size, (1 << 31) - 2048)
+    limit = capacity if max_len is None else min(int(max_len), capacity)
+    if limit < 0:
+        raise ValueError("max_len must not be negative")
+    if out is None:
+        out = _empty((batch, heads, dim), q.dtype, dev, stream)
+    else:
+        _on(dev, q.dtype, "out", out, (batch, heads, dim))
+    lse = _empty((batch, heads), torch.float32, dev, stream)
+    ws = _model_ws(workspace, lib().det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
+    _check(lib().det_paged_attention(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), *k_cache.stride()[:3], _ptr(v_cache), *v_cache.stride()[:3],
+        pages, page_size, _ptr(block_table), block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads,
+        kv_heads, dim, code, dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
+        _ptr(bias_bounds) if bias_table is not None else None, n_bounds, limit, _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel(), _stream(stream)), "det_paged_attention")
+    return PagedAttention(out, lse)
 
 
 # ---------------------------------------------------------------------------
