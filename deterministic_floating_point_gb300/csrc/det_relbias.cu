@@ -8,6 +8,7 @@
 #include "det_model.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace det {
 namespace {
@@ -54,93 +55,386 @@ struct Distances {
   }
 };
 
+// Few rows (at most kDirectRows): a thread per pair, its bucket searched.
+constexpr int kDirectRows = 8;
 template <typename T>
 __global__ void __launch_bounds__(256)
-relative_bias_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
-                     T* __restrict__ out) {
-  const int h = blockIdx.z, i = blockIdx.y;
-  for (int q = i; q < q_len; q += gridDim.y)
-    for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < k_len; j += gridDim.x * blockDim.x) {
-      const int k = dist.bucket(j - q + (q_len - 1) + dist.first);
-      out[((long long)h * q_len + q) * k_len + j] =
-          from_f32<T>(load_as_f32(table, (long long)k * heads + h, table_dtype));
+bias_direct_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
+                   T* __restrict__ out) {
+  const int j = blockIdx.x * blockDim.x + threadIdx.x, q = blockIdx.y, h = blockIdx.z;
+  if (j >= k_len) return;
+  const int k = dist.bucket(j - q + (q_len - 1) + dist.first);
+  out[((long long)h * q_len + q) * k_len + j] = from_f32<T>(load_as_f32(table, (long long)k * heads + h, table_dtype));
+}
+
+// Otherwise a CTA writes 128 rows by 128 eights of keys from the strip of
+// diagonals that they cross, kept in shared memory (in 16-bit types as the
+// pairs of diagonals d, d + 1 that make up a word of the output).  A row's
+// eights start where its memory is 16-byte aligned, so every store but those
+// at a row's ends is 16 bytes wide whatever the row length.  Word u of the
+// strip lies at u + u / 8: threads are 8 diagonals apart, which then are 9
+// banks.
+constexpr int kBiasThreads = 128;
+constexpr int kBiasRows = 128;
+constexpr int kStrip = 8 * kBiasThreads + kBiasRows + 16;
+
+template <typename T> struct Out16;
+template <> struct Out16<float> {
+  static __device__ __forceinline__ unsigned word(float a, float) { return __float_as_uint(a); }
+};
+template <> struct Out16<__nv_bfloat16> {
+  static __device__ __forceinline__ unsigned word(float a, float b) {
+    return (unsigned)__bfloat16_as_ushort(__float2bfloat16_rn(a)) | ((unsigned)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
+  }
+};
+template <> struct Out16<__half> {
+  static __device__ __forceinline__ unsigned word(float a, float b) {
+    return (unsigned)__half_as_ushort(__float2half_rn(a)) | ((unsigned)__half_as_ushort(__float2half_rn(b)) << 16);
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kBiasThreads)
+bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
+                  T* __restrict__ out) {
+  constexpr int E = 4 / sizeof(T);        // elements of a word
+  constexpr int kUnit = 16 / sizeof(T);   // elements of a store
+  __shared__ unsigned strip[kStrip + kStrip / 8 + 1];
+  __shared__ float value[kStrip + 1];
+  const int h = blockIdx.z, i0 = blockIdx.y * kBiasRows, c0 = blockIdx.x * kBiasThreads;
+  const int rows = min(kBiasRows, q_len - i0);
+  // strip[u] holds diagonal u + d0: key - query from 8 (c0 - 1) - (i0 + kBiasRows - 1) up
+  const int d0 = 8 * (c0 - 1) - (i0 + kBiasRows - 1);
+  const int base = d0 + (q_len - 1) + dist.first;   // distance of strip[0]
+  for (int u = threadIdx.x; u <= kStrip; u += kBiasThreads)
+    value[u] = load_as_f32(table, (long long)dist.bucket(base + u) * heads + h, table_dtype);
+  __syncthreads();
+  for (int u = threadIdx.x; u < kStrip; u += kBiasThreads) strip[u + (u >> 3)] = Out16<T>::word(value[u], value[u + 1]);
+  __syncthreads();
+  for (int y = 0; y < rows; ++y) {
+    const int i = i0 + y;
+    T* row = out + ((long long)h * q_len + i) * k_len;
+    // keys before the row's first 16-byte boundary
+    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
+    const int j = head + 8 * (c0 - 1 + (int)threadIdx.x);
+    if (j >= k_len || j + 8 <= 0) continue;
+    const int u = j - i - d0;
+    unsigned w[8 / E];
+#pragma unroll
+    for (int x = 0; x < 8 / E; ++x) {
+      const int at = u + x * E;
+      w[x] = strip[at + (at >> 3)];
     }
+    if (j >= 0 && j + 8 <= k_len) {
+#pragma unroll
+      for (int x = 0; x < 8 / kUnit; ++x)
+        *reinterpret_cast<uint4*>(row + j + x * kUnit) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        if (j + x < 0 || j + x >= k_len) continue;
+        if constexpr (E == 1) row[j + x] = __uint_as_float(w[x]);
+        else reinterpret_cast<unsigned short*>(row)[j + x] = (unsigned short)(w[x / 2] >> (16 * (x & 1)));
+      }
+    }
+  }
 }
 
 struct GradView {
   long long stride_b, stride_h, stride_q;
   int batch, q_len, k_len;
+  uintptr_t lo, hi;   // the bytes from the first element to the end of the last
 };
 
-// diag[h][d] = the sum of diagonal d of head h.
-template <typename T>
-__global__ void __launch_bounds__(256)
-diagonal_sums_kernel(const T* __restrict__ grad, GradView g, float* __restrict__ diag) {
-  const int d = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
-  const int count = g.q_len + g.k_len - 1;
-  if (d >= count) return;
-  const int shift = d - (g.q_len - 1);   // key - query index
-  const int i0 = max(0, -shift), i1 = min(g.q_len, g.k_len - shift);
-  float sum = 0.0f;
-  for (int b = 0; b < g.batch; ++b) {
-    float part = 0.0f;
-    const T* p = grad + b * g.stride_b + h * g.stride_h;
-    for (int i = i0; i < i1; ++i) part += to_f32(p[i * g.stride_q + i + shift]);
-    sum += part;
+// The gradient is cut into tiles of 64 queries by 256 diagonals, a warp each:
+// lane l takes 8 neighbouring keys of 8 queries at a time and moves 8 keys
+// on with every 8 queries, so its 64 pairs always lie on the same 15 diagonals
+// (the key within the eight less the query within the eight), whose sums
+// stay in registers.
+constexpr int kTileRows = 64;
+constexpr int kTileGroups = kTileRows / 8;
+constexpr int kTileDiags = 264;   // diagonals of a tile: 32 lanes x 8, and the 8 below
+constexpr int kTileWarps = 4;     // warps of a CTA
+
+struct TileGrid {
+  int row_blocks, strips;   // tiles along the queries and along the keys
+  __host__ __device__ TileGrid(int q_len, int k_len)
+      : row_blocks((q_len + kTileRows - 1) / kTileRows), strips(((k_len + 7) / 8 + kTileGroups + 31) / 32) {}
+  __host__ __device__ int per_matrix() const { return row_blocks * strips; }
+  // First key eight of lane 0 in the tile's first group.
+  __device__ __forceinline__ int first_eight(int strip) const { return strip * 32 - kTileGroups; }
+  // Key - query of the tile's diagonal 0.
+  __device__ __forceinline__ int first_diagonal(int row_block, int strip) const {
+    return 8 * first_eight(strip) - row_block * kTileRows - 8;
   }
-  diag[(long long)h * count + d] = sum;
+};
+
+template <typename T> struct Eight {   // 8 neighbouring elements as 32-bit words
+  static constexpr int W = 8 * sizeof(T) / 4;
+  unsigned w[W];
+  __device__ __forceinline__ float get(int x) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[x]);
+    const unsigned v = w[x >> 1];
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float((x & 1) ? (v & 0xffff0000u) : (v << 16));
+    return __half2float(__ushort_as_half((unsigned short)((x & 1) ? (v >> 16) : v)));
+  }
+};
+
+__device__ __forceinline__ uint4 load_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-// One warp per (bucket, head): lane l adds the bucket's diagonals l, l + 32,
-// ... of the interval, then the lanes are added by a tree.
-__global__ void __launch_bounds__(32)
-bucket_sums_kernel(const float* __restrict__ diag, Distances dist, int diagonals, int heads,
-                   void* __restrict__ grad_table, int table_dtype) {
+// The 8 elements at p, every such eight 16-byte aligned (ALIGNED), or any:
+// the 16-byte blocks that hold it are read and shifted into place.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ Eight<T> load_eight(const T* p) {
+  constexpr int W = Eight<T>::W;
+  Eight<T> e;
+  if constexpr (ALIGNED) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = load_16(reinterpret_cast<const char*>(p) + 4 * i);
+      e.w[i] = v.x, e.w[i + 1] = v.y, e.w[i + 2] = v.z, e.w[i + 3] = v.w;
+    }
+  } else {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), first = at & ~(uintptr_t)15;
+    unsigned v[W + 4];
+#pragma unroll
+    for (int i = 0; i < W + 4; i += 4) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(first) + i / 4);
+      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    }
+    const unsigned off = (unsigned)(at - first);
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = (off & 8) ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) v[i] = (off & 4) ? v[i + 1] : v[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) e.w[i] = sizeof(T) == 2 ? __funnelshift_r(v[i], v[i + 1], (off & 2) * 8) : v[i];
+  }
+  return e;
+}
+// Whether load_eight at p stays inside the matrices' memory.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ bool eight_inside(const T* p, const GradView& g) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+  return ALIGNED || (first >= g.lo && first + 4 * Eight<T>::W + 16 <= g.hi);
+}
+// Elements j .. j + 7 of a row one by one, 0 outside [0, k_len).
+template <typename T>
+__device__ __forceinline__ Eight<T> load_singly(const T* row, int j, int k_len) {
+  Eight<T> e;
+#pragma unroll
+  for (int i = 0; i < Eight<T>::W; ++i) e.w[i] = 0u;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    if (j + x < 0 || j + x >= k_len) continue;
+    if constexpr (sizeof(T) == 4) e.w[x] = __float_as_uint(__ldg(row + j + x));
+    else e.w[x >> 1] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(row) + j + x) << (16 * (x & 1));
+  }
+  return e;
+}
+
+// part[h][bucket][tile] = the tile's sum over the bucket, for the buckets
+// that the tile's diagonals reach.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kTileWarps, 4)
+bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_offset, int buckets,
+                  float* __restrict__ part) {
+  __shared__ float sh[kTileWarps][kTileDiags];
+  const TileGrid tiles(g.q_len, g.k_len);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_matrix = tiles.per_matrix(), per_head = per_matrix * g.batch;   // below 2^31: the launch checks
+  const int tile = blockIdx.x * kTileWarps + warp, h = blockIdx.y;
+  if (tile >= per_head) return;
+  const int b = tile / per_matrix, in_matrix = tile - b * per_matrix;
+  const int row_block = in_matrix / tiles.strips, strip = in_matrix - row_block * tiles.strips;
+
+  const T* matrix = grad + b * g.stride_b + h * g.stride_h;
+  const int i0 = row_block * kTileRows;
+  int j = 8 * (tiles.first_eight(strip) + lane);
+  float acc[15];
+#pragma unroll
+  for (int i = 0; i < 15; ++i) acc[i] = 0.0f;
+  for (int i = i0; i < min(i0 + kTileRows, g.q_len); i += 8, j += 8) {
+    if (j + 8 <= 0 || j >= g.k_len) continue;
+    const T* p = matrix + (long long)i * g.stride_q + j;
+    const int count = min(8, g.q_len - i);
+    if (count == 8 && j >= 0 && j + 8 <= g.k_len && eight_inside<T, ALIGNED>(p, g) &&
+        eight_inside<T, ALIGNED>(p + 7 * g.stride_q, g)) {
+      Eight<T> e[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) e[y] = load_eight<T, ALIGNED>(p + y * g.stride_q);
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x - y + 7] += e[y].get(x);
+    } else {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        if (y >= count) break;
+        const Eight<T> e = load_singly(p + y * g.stride_q - j, j, g.k_len);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x - y + 7] += e.get(x);
+      }
+    }
+  }
+  // the tile's diagonals: one's own 0 .. 7, then the 7 below on top of the
+  // neighbour's
+  float* diag = sh[warp];
+  if (lane < 8) diag[lane] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) diag[8 * (lane + 1) + s] = acc[s + 7];
+  __syncwarp();
+#pragma unroll
+  for (int s = 1; s < 8; ++s) diag[8 * lane + s] += acc[s - 1];
+  __syncwarp();
+  // The buckets of both signs, a lane each; a bucket of 32 diagonals or more
+  // is added by the whole warp.
+  const int from = tiles.first_diagonal(row_block, strip) - q_offset, to = from + kTileDiags;
+  float* out = part + (long long)h * buckets * per_head + tile;
+  for (int side = 0; side < 2; ++side) {
+    // the least and the largest |distance| on this side of the query
+    int k0, k1;
+    if (side == 0) {
+      if (from > 0 && dist.bidirectional) continue;
+      k0 = dist.bounds_at_most(to - 1 < 0 ? 1 - to : 0);
+      k1 = dist.bounds_at_most(from < 0 ? -from : 0);
+    } else {
+      if (to <= 1 || !dist.bidirectional) continue;
+      k0 = dist.bounds_at_most(from > 1 ? from : 1) + dist.num_bounds + 1;
+      k1 = dist.bounds_at_most(to - 1) + dist.num_bounds + 1;
+    }
+    for (int kb = k0; kb <= k1; kb += 32) {
+      const int k = kb + lane;
+      int lo = 0, hi = 0;
+      if (k <= k1) {
+        dist.interval(k, from, to, lo, hi);
+        lo -= from;
+        hi -= from;
+      }
+      unsigned wide = __ballot_sync(0xffffffffu, hi - lo >= 32);
+      if (hi - lo < 32 && hi > lo) {
+        float sum = 0.0f;
+        for (int d = lo; d < hi; ++d) sum += diag[d];
+        out[(long long)k * per_head] = sum;
+      }
+      while (wide) {
+        const int owner = __ffs(wide) - 1;
+        wide &= wide - 1;
+        const int l = __shfl_sync(0xffffffffu, lo, owner), u = __shfl_sync(0xffffffffu, hi, owner);
+        float sum = 0.0f;
+        for (int d = l + lane; d < u; d += 32) sum += diag[d];
+        sum = warp_pt(sum);
+        if (lane == 0) out[(long long)(kb + owner) * per_head] = sum;
+      }
+    }
+  }
+}
+
+// One CTA per (bucket, head): thread t adds the tiles t, t + 128, ... that
+// reach the bucket, then the threads are added by a tree.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads)
+bias_join_kernel(const float* __restrict__ part, int batch, int q_len, int k_len, Distances dist, int q_offset, int heads,
+                 int buckets, void* __restrict__ grad_table, int table_dtype) {
+  __shared__ float sh[kJoinThreads / 32];
+  dep_wait();
+  const TileGrid tiles(q_len, k_len);
+  const int per_matrix = tiles.per_matrix(), per_head = per_matrix * batch;
   const int k = blockIdx.x, h = blockIdx.y;
-  int lo, hi;
-  dist.interval(k, dist.first, dist.first + diagonals, lo, hi);
-  const float* p = diag + (long long)h * diagonals - dist.first;
+  const float* p = part + ((long long)h * buckets + k) * per_head;
   float sum = 0.0f;
-  for (int r = lo + (int)threadIdx.x; r < hi; r += 32) sum += p[r];
+  for (int t = threadIdx.x; t < per_head; t += kJoinThreads) {
+    const int in_matrix = t % per_matrix;
+    const int row_block = in_matrix / tiles.strips, strip = in_matrix - row_block * tiles.strips;
+    const int from = tiles.first_diagonal(row_block, strip) - q_offset;
+    int lo, hi;
+    dist.interval(k, from, from + kTileDiags, lo, hi);
+    if (lo < hi) sum += p[t];
+  }
   sum = warp_pt(sum);
-  if (threadIdx.x == 0) store_from_f32(grad_table, (long long)k * heads + h, sum, table_dtype);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) sum += sh[w];
+    store_from_f32(grad_table, (long long)k * heads + h, sum, table_dtype);
+  }
 }
 
 int check_shape(int64_t heads, int64_t num_bounds, int64_t q_len, int64_t k_len, int64_t q_offset) {
   if (heads < 0 || num_bounds < 0 || q_len < 0 || k_len < 0) return DET_ERR_INVALID_ARG;
-  const int64_t most = (1LL << 31) - 1;
+  const int64_t most = (1LL << 30);   // so that no distance, nor one of a tile past the edge, leaves 32 bits
   if (heads > 65535 || num_bounds > DET_MAX_BOUNDS || q_len > most || k_len > most || q_offset > most ||
       q_offset < -most || q_len + k_len + (q_offset < 0 ? -q_offset : q_offset) > most)
     return DET_ERR_TOO_LARGE;
   return DET_OK;
 }
 
+// Tiles of a head's gradient, or 2^31 when there are that many or more.
+inline int64_t tiles_of_head(int64_t batch, int64_t q_len, int64_t k_len) {
+  const int64_t rows = (q_len + kTileRows - 1) / kTileRows, strips = ((k_len + 7) / 8 + kTileGroups + 31) / 32;
+  if (rows * strips >= (1LL << 31) || (rows * strips > 0 && batch > (1LL << 31) / (rows * strips))) return 1LL << 31;
+  return rows * strips * batch;
+}
+
 template <typename T>
 int launch_bias(const void* table, int table_dtype, int heads, const Distances& dist, int q_len, int k_len, void* out,
                 cudaStream_t s) {
-  const dim3 grid((unsigned)std::min((k_len + 255) / 256, 1024), (unsigned)std::min(q_len, 65535), (unsigned)heads);
-  launch_begin("det_relative_bias", s);
-  relative_bias_kernel<T><<<grid, 256, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len, static_cast<T*>(out));
+  if (q_len <= kDirectRows) {
+    const dim3 grid((unsigned)((k_len + 255) / 256), (unsigned)q_len, (unsigned)heads);
+    launch_begin("det_relative_bias", s);
+    bias_direct_kernel<T><<<grid, 256, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len, static_cast<T*>(out));
+  } else {
+    // a row has eights from head - 8 up, head < 8
+    const int eights = (k_len + 7) / 8 + 1;
+    const dim3 grid((unsigned)((eights + kBiasThreads - 1) / kBiasThreads),
+                    (unsigned)((q_len + kBiasRows - 1) / kBiasRows), (unsigned)heads);
+    if (grid.y > 65535) return DET_ERR_TOO_LARGE;
+    launch_begin("det_relative_bias", s);
+    bias_strip_kernel<T><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
+                                                       static_cast<T*>(out));
+  }
   launch_end(s);
   return check_launch("det_relative_bias");
 }
 
-template <typename T>
-int launch_bias_grad(const void* grad, const GradView& g, const Distances& dist, int heads, int buckets, float* diag,
-                     void* grad_table, int table_dtype, cudaStream_t s) {
-  const int count = g.q_len > 0 && g.k_len > 0 ? g.q_len + g.k_len - 1 : 0;
-  if (count > 0) {
-    launch_begin("det_relative_bias_diagonals", s);
-    diagonal_sums_kernel<T><<<dim3((unsigned)((count + 255) / 256), (unsigned)heads), 256, 0, s>>>(
-        static_cast<const T*>(grad), g, diag);
-    launch_end(s);
-    if (const int rc = check_launch("det_relative_bias_diagonals")) return rc;
-  }
-  launch_begin("det_relative_bias_buckets", s);
-  bucket_sums_kernel<<<dim3((unsigned)buckets, (unsigned)heads), 32, 0, s>>>(diag, dist, count, heads, grad_table,
-                                                                             table_dtype);
+template <typename T, bool ALIGNED>
+int launch_tiles(const void* grad, const GradView& g, const Distances& dist, int q_offset, int buckets,
+                 float* part, dim3 grid, cudaStream_t s) {
+  launch_begin("det_relative_bias_tiles", s);
+  bias_tiles_kernel<T, ALIGNED><<<grid, 32 * kTileWarps, 0, s>>>(static_cast<const T*>(grad), g, dist, q_offset,
+                                                                 buckets, part);
   launch_end(s);
-  return check_launch("det_relative_bias_buckets");
+  return check_launch("det_relative_bias_tiles");
+}
+
+template <typename T>
+int launch_bias_grad(const void* grad, GradView g, const Distances& dist, int q_offset, int heads, int buckets,
+                     float* part, void* grad_table, int table_dtype, cudaStream_t s) {
+  const long long tiles = (long long)TileGrid(g.q_len, g.k_len).per_matrix() * g.batch;   // of a head
+  if (tiles > 0) {
+    const dim3 grid((unsigned)((tiles + kTileWarps - 1) / kTileWarps), (unsigned)heads);
+    g.lo = reinterpret_cast<uintptr_t>(grad);
+    g.hi = g.lo + sizeof(T) * (size_t)((g.batch - 1) * g.stride_b + (heads - 1) * g.stride_h +
+                                       (g.q_len - 1) * g.stride_q + g.k_len);
+    // an eight of keys starts on 16 bytes if every row does
+    const bool aligned = (g.lo | (uintptr_t)(sizeof(T) * (g.stride_b | g.stride_h | g.stride_q))) % 16 == 0;
+    const int rc = aligned ? launch_tiles<T, true>(grad, g, dist, q_offset, buckets, part, grid, s)
+                           : launch_tiles<T, false>(grad, g, dist, q_offset, buckets, part, grid, s);
+    if (rc) return rc;
+  }
+  launch_begin("det_relative_bias_join", s);
+  const cudaError_t e = launch_dep(bias_join_kernel, dim3((unsigned)buckets, (unsigned)heads), dim3(kJoinThreads), 0, s,
+                                   (const float*)part, tiles > 0 ? g.batch : 0, g.q_len, g.k_len, dist, q_offset, heads,
+                                   buckets, grad_table, table_dtype);
+  launch_end(s);
+  return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_relative_bias_join");
 }
 
 }  // namespace
@@ -169,9 +463,9 @@ extern "C" int det_relative_bias(const void* table, int table_dtype, int64_t hea
 
 extern "C" size_t det_relative_bias_backward_workspace_bytes(int64_t batch, int64_t heads, int64_t q_len,
                                                              int64_t k_len, int64_t num_bounds, int bidirectional) {
-  (void)bidirectional;
   if (batch < 0 || check_shape(heads, num_bounds, q_len, k_len, 0) != DET_OK) return 0;
-  return align_up((size_t)heads * (size_t)(q_len + k_len) * sizeof(float) + 256, 256);
+  const size_t buckets = (size_t)(num_bounds + 1) * (bidirectional ? 2 : 1);
+  return 256 + align_up((size_t)heads * buckets * (size_t)tiles_of_head(batch, q_len, k_len) * sizeof(float), 256);
 }
 
 extern "C" int det_relative_bias_backward(const void* grad, int dtype, int64_t batch, int64_t heads, int64_t q_len,
@@ -182,7 +476,7 @@ extern "C" int det_relative_bias_backward(const void* grad, int dtype, int64_t b
   if (!valid_model_dtype(dtype) || !valid_model_dtype(table_dtype)) return DET_ERR_DTYPE;
   if (batch < 0) return DET_ERR_INVALID_ARG;
   if (const int rc = check_shape(heads, num_bounds, q_len, k_len, q_offset)) return rc;
-  if (batch >= (1LL << 31)) return DET_ERR_TOO_LARGE;
+  if (batch >= (1LL << 31) || tiles_of_head(batch, q_len, k_len) >= (1LL << 31)) return DET_ERR_TOO_LARGE;
   if (heads == 0) return DET_OK;
   const bool none = batch == 0 || q_len == 0 || k_len == 0;
   if (!grad_table || (!none && !grad) || (num_bounds > 0 && !bounds)) return DET_ERR_INVALID_ARG;
@@ -192,14 +486,15 @@ extern "C" int det_relative_bias_backward(const void* grad, int dtype, int64_t b
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 ||
       workspace_bytes < det_relative_bias_backward_workspace_bytes(batch, heads, q_len, k_len, num_bounds, bidirectional))
     return DET_ERR_WORKSPACE;
-  const GradView g = {stride_b, stride_h, stride_q, (int)batch, none ? 0 : (int)q_len, none ? 0 : (int)k_len};
+  if (stride_b < 0 || stride_h < 0 || stride_q < 0) return DET_ERR_INVALID_ARG;
+  const GradView g = {stride_b, stride_h, stride_q, none ? 0 : (int)batch, (int)q_len, (int)k_len, 0, 0};
   const Distances dist = {bounds, (int)num_bounds, bidirectional ? 1 : 0, (int)(1 - q_len - q_offset)};
   const int buckets = (int)(num_bounds + 1) * (bidirectional ? 2 : 1);
-  float* diag = static_cast<float*>(workspace);
+  float* part = static_cast<float*>(workspace);
   const cudaStream_t s = as_stream(stream);
   if (dtype == DET_F32)
-    return launch_bias_grad<float>(grad, g, dist, (int)heads, buckets, diag, grad_table, table_dtype, s);
+    return launch_bias_grad<float>(grad, g, dist, (int)q_offset, (int)heads, buckets, part, grad_table, table_dtype, s);
   if (dtype == DET_BF16)
-    return launch_bias_grad<__nv_bfloat16>(grad, g, dist, (int)heads, buckets, diag, grad_table, table_dtype, s);
-  return launch_bias_grad<__half>(grad, g, dist, (int)heads, buckets, diag, grad_table, table_dtype, s);
+    return launch_bias_grad<__nv_bfloat16>(grad, g, dist, (int)q_offset, (int)heads, buckets, part, grad_table, table_dtype, s);
+  return launch_bias_grad<__half>(grad, g, dist, (int)q_offset, (int)heads, buckets, part, grad_table, table_dtype, s);
 }
