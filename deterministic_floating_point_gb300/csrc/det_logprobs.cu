@@ -24,12 +24,24 @@ template <> struct Word<float> {
   static constexpr int N = 1;
   static constexpr unsigned kMasked = 0xff800000u;   // -inf
   static __device__ __forceinline__ float get(unsigned w, int) { return __uint_as_float(w); }
+  static __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  }
 };
 template <> struct Word<__nv_bfloat16> {
   static constexpr int N = 2;
   static constexpr unsigned kMasked = 0xff80ff80u;
   static __device__ __forceinline__ float get(unsigned w, int j) {
     return __uint_as_float(j ? (w & 0xffff0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
+    unsigned r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ unsigned pack(float a, float b) {   // to nearest
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&v);
   }
 };
 template <> struct Word<__half> {
@@ -38,7 +50,44 @@ template <> struct Word<__half> {
   static __device__ __forceinline__ float get(unsigned w, int j) {
     return __half2float(__ushort_as_half((unsigned short)(j ? (w >> 16) : w)));
   }
+  static __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
+    unsigned r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ unsigned pack(float a, float b) {   // to nearest
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&v);
+  }
 };
+
+// Two 32-bit lanes in a 64-bit register.
+__device__ __forceinline__ unsigned long long pack_f32x2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b,
+                                                        unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // Word w of a row (elements N w, N w + 1), with masked logits past its end.
 template <typename T>
@@ -172,40 +221,119 @@ __device__ void top_alternatives(const T* row, long long vocab, bool words_align
   }
 }
 
+// A row in chunks of 512 threads x 16 words, a thread's word i of chunk c
+// being word (16 c + i) 512 + t: a warp reads 128 neighbouring bytes.  Words
+// are 4-byte aligned in memory, except in 16-bit rows that start at an odd
+// element (ODD): there a thread reads the aligned word that holds the first of
+// its two elements and gets the other from the next lane, whose word holds it
+// (the last lane's from an extra word a lane loads for each i).
+template <typename T>
+struct RowReader {
+  const T* row;
+  long long vocab, words;
+  bool odd;
+  const unsigned* base;   // the aligned word with (the first element of) the thread's word 0
+  const unsigned* extra;  // of the word behind the warp's last, for i = lane % 16
+
+  __device__ __forceinline__ RowReader(const T* row_, long long vocab_) : row(row_), vocab(vocab_) {
+    words = (vocab + Word<T>::N - 1) / Word<T>::N;
+    odd = Word<T>::N == 2 && (reinterpret_cast<uintptr_t>(row) & 3);
+    const unsigned* aligned = reinterpret_cast<const unsigned*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)3);
+    base = aligned + threadIdx.x;
+    extra = aligned + (threadIdx.x & 15) * kRowThreads + (threadIdx.x & ~31u) + 32;
+  }
+  // Raw words of the chunk whose first word is w0.  A word read here lies
+  // inside the row; what is not is left to finish().
+  __device__ __forceinline__ void start(long long w0, unsigned (&x)[kWords], unsigned& more) const {
+    // every aligned word up to index w0 + 16 * 512 is inside the row, and word 0 is not half outside
+    const bool inside = odd ? w0 > 0 && 2 * (w0 + kWords * kRowThreads) < vocab
+                            : Word<T>::N * (w0 + kWords * kRowThreads) <= vocab;
+    if (inside) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) x[i] = __ldg(base + w0 + i * kRowThreads);
+      if (odd) more = __ldg(extra + w0);
+    } else if (!odd) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) x[i] = load_word(row, w0 + threadIdx.x + i * kRowThreads, vocab, true);
+    }
+  }
+  __device__ __forceinline__ void finish(long long w0, unsigned (&x)[kWords], unsigned more) const {
+    if (!odd) return;
+    if (w0 > 0 && 2 * (w0 + kWords * kRowThreads) < vocab) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        unsigned next = __shfl_down_sync(0xffffffffu, x[i], 1);
+        const unsigned last = __shfl_sync(0xffffffffu, more, i);
+        if ((threadIdx.x & 31) == 31) next = last;
+        x[i] = __funnelshift_r(x[i], next, 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) x[i] = load_word(row, w0 + threadIdx.x + i * kRowThreads, vocab, false);
+    }
+  }
+};
+
+// The chunk's elements added to the thread's statistics.
+template <typename T>
+__device__ __forceinline__ void add_chunk(Stat& st, const unsigned (&x)[kWords]) {
+  constexpr int N = Word<T>::N;
+  unsigned mx[kWords / 2];
+#pragma unroll
+  for (int i = 0; i < kWords / 2; ++i) mx[i] = Word<T>::larger(x[i], x[i + kWords / 2]);
+#pragma unroll
+  for (int s = kWords / 4; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < s; ++i) mx[i] = Word<T>::larger(mx[i], mx[i + s]);
+  float m = Word<T>::get(mx[0], 0);
+  if (N == 2) m = max_nan(m, Word<T>::get(mx[0], 1));
+  if (!(m <= st.m)) {   // a new maximum (or NaN): the sums so far relative to it
+    if (st.m != kNegInf) {
+      const float d = st.m - m, f = exp2_approx(d * kLog2e);
+      st.t = f > 0.0f ? f * fmaf(st.s, d, st.t) : f;   // no 0 * inf
+      st.s *= f;
+    }
+    st.m = max_nan(st.m, m);
+  }
+  const float base = stat_base(st.m);
+  const unsigned long long minus = pack_f32x2(-base, -base), scale = pack_f32x2(kLog2e, kLog2e);
+  unsigned long long s2 = 0, t2 = 0;   // of elements 0 and 1 of the words (f32: even and odd words)
+#pragma unroll
+  for (int i = 0; i < kWords; i += 3 - N) {
+    const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % kWords], 0);
+    const float2 y = unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(a, b), minus), scale));
+    // 2^-150 is 0 already; without the bound 0 * inf for a masked logit
+    const float y0 = max_nan(y.x, -150.0f), y1 = max_nan(y.y, -150.0f);
+    const unsigned long long e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
+    s2 = add_f32x2(s2, e);
+    t2 = fma_f32x2(e, pack_f32x2(y0, y1), t2);
+  }
+  const float2 s = unpack_f32x2(s2), t = unpack_f32x2(t2);
+  st.s += s.x + s.y;
+  st.t = fmaf(t.x + t.y, kLn2, st.t);   // y is d in units of log 2
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 2)
 token_logprobs_kernel(const T* __restrict__ logits, long long vocab, long long row_stride,
                       const int32_t* __restrict__ tokens, int top_k, RowOut out) {
-  constexpr int N = Word<T>::N;
   __shared__ Stat sh[kRowWarps];
   const long long r = blockIdx.x;
   const T* row = logits + r * row_stride;
-  const bool aligned = (reinterpret_cast<uintptr_t>(row) & 3) == 0;
-  const long long words = (vocab + N - 1) / N;
+  const RowReader<T> reader(row, vocab);
+  const bool aligned = !reader.odd;
   Stat st = {kNegInf, 0.0f, 0.0f};
-  for (long long w0 = threadIdx.x; w0 < words; w0 += (long long)kRowThreads * kWords) {
-    unsigned x[kWords];
+  // the next chunk's loads are in flight while a chunk is added
+  constexpr long long kStep = (long long)kRowThreads * kWords;
+  unsigned x[kWords], ahead[kWords], more = 0, more_ahead = 0;
+  if (reader.words > 0) reader.start(0, x, more);
+  for (long long w0 = 0; w0 < reader.words; w0 += kStep) {
+    if (w0 + kStep < reader.words) reader.start(w0 + kStep, ahead, more_ahead);
+    reader.finish(w0, x, more);
+    add_chunk<T>(st, x);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const long long w = w0 + (long long)i * kRowThreads;
-      x[i] = w < words ? load_word(row, w, vocab, aligned) : Word<T>::kMasked;
-    }
-    Stat c = {kNegInf, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-      for (int j = 0; j < N; ++j) c.m = max_nan(c.m, Word<T>::get(x[i], j));
-    const float base = stat_base(c.m);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float d = Word<T>::get(x[i], j) - base;
-        const float e = exp2_approx(d * kLog2e);
-        c.s += e;
-        c.t = fmaf(e, d < -200.0f ? -200.0f : d, c.t);   // e is 0 there: no 0 * inf
-      }
-    st = stat_join(st, c);
+    for (int i = 0; i < kWords; ++i) x[i] = ahead[i];
+    more = more_ahead;
   }
   const float best = st.m;
 #pragma unroll
@@ -238,7 +366,7 @@ token_logprobs_kernel(const T* __restrict__ logits, long long vocab, long long r
 // The gradient: elementwise once lse and the entropy are known.
 
 constexpr int kGradThreads = 256;
-constexpr int kGradElems = 16;   // elements of a thread
+constexpr int kGradVecs = 4;   // 16-byte vectors of a thread
 // From this magnitude on 32 bits hold lse to 2^-14 or worse (nothing of log S
 // is left of it in a row at the types' lowest values): the row is summed again.
 constexpr float kLseFar = 1024.0f;
@@ -263,37 +391,92 @@ __device__ float2 row_max_and_log_sum(const T* row, long long vocab) {
   return make_float2(m, logf(s));
 }
 
-template <typename T>
+// grad[v] = [v == token] g_l - p (c + g_h log p) with c = g_l + g_h * entropy.
+struct GradRow {
+  float base, log_s;   // log p = (x - base) - log_s
+  float gl, gh, c;
+  __device__ __forceinline__ float at(float x) const {
+    // p is 0 from -150 on already; without the bound 0 * inf for a masked logit
+    const float lp = max_nan((x - base) - log_s, -150.0f);
+    return -exp2_approx(lp * kLog2e) * fmaf(gh, lp, c);
+  }
+};
+
+// A CTA takes 256 x 4 vectors of 16 bytes of a row, counted from the row's
+// first 16-byte boundary (the same one of both rows: SAME_PHASE), and the
+// row's first CTA the elements before it and behind the last vector.  Where
+// the rows' boundaries differ it goes by elements.
+template <typename T, bool SAME_PHASE>
 __global__ void __launch_bounds__(kGradThreads)
-token_logprobs_grad_kernel(const T* __restrict__ logits, long long vocab, long long row_stride,
+token_logprobs_grad_kernel(const T* __restrict__ logits, int vocab, long long row_stride,
                            const int32_t* __restrict__ tokens, const float* __restrict__ lse,
                            const float* __restrict__ entropy, const float* __restrict__ grad_logprob,
-                           const float* __restrict__ grad_entropy, T* __restrict__ grad, long long grad_stride) {
-  const long long r = blockIdx.x;
+                           const float* __restrict__ grad_entropy, T* __restrict__ grad, long long grad_stride,
+                           unsigned ctas_per_row) {
+  constexpr int E = 16 / sizeof(T), N = Word<T>::N;
+  const unsigned r = blockIdx.x / ctas_per_row, part = blockIdx.x - r * ctas_per_row;
   const T* row = logits + r * row_stride;
   T* g = grad + r * grad_stride;
+  const int head = SAME_PHASE ? min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T), vocab) : 0;
+  const int vecs = SAME_PHASE ? (vocab - head) / E : 0;
+  const int v0 = part * (kGradThreads * kGradVecs) + threadIdx.x;
+  uint4 x[kGradVecs];
+  if constexpr (SAME_PHASE) {
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i)
+      if (v0 + i * kGradThreads < vecs) x[i] = __ldg(reinterpret_cast<const uint4*>(row + head) + v0 + i * kGradThreads);
+  }
   const float l = lse[r];
-  long long tok = grad_logprob ? tokens[r] : -1;
-  const float gl = tok >= 0 && tok < vocab ? grad_logprob[r] : 0.0f;
-  const float gh = grad_entropy ? grad_entropy[r] : 0.0f;
-  const float h = grad_entropy ? entropy[r] : 0.0f;
-  // log p = (x - base) - log_s
-  float base = l, log_s = 0.0f;
+  const int tok = grad_logprob ? tokens[r] : -1;
+  GradRow q;
+  q.gl = tok >= 0 && tok < vocab ? grad_logprob[r] : 0.0f;
+  q.gh = grad_entropy ? grad_entropy[r] : 0.0f;
+  q.c = grad_entropy ? fmaf(q.gh, entropy[r], q.gl) : q.gl;
+  q.base = l;
+  q.log_s = 0.0f;
   if (fabsf(l) >= kLseFar && fabsf(l) < INFINITY) {
     const float2 ms = row_max_and_log_sum(row, vocab);
-    base = ms.x;
-    log_s = ms.y;
+    q.base = ms.x;
+    q.log_s = ms.y;
   }
-  const long long start = (long long)blockIdx.y * kGradThreads * kGradElems + threadIdx.x;
+  if (l == kNegInf) {   // a row without a logit above -inf: 0 throughout
+    q.gl = q.gh = q.c = 0.0f;
+    q.base = 0.0f;
+  }
+  if constexpr (SAME_PHASE) {
 #pragma unroll
-  for (int i = 0; i < kGradElems; ++i) {
-    const long long e = start + i * kGradThreads;
-    if (e >= vocab) return;
-    const float lp = (to_f32(row[e]) - base) - log_s;
-    const float p = l == kNegInf ? 0.0f : exp2_approx(lp * kLog2e);
-    float d = p == 0.0f ? 0.0f : -p * fmaf(gh, lp + h, gl);
-    if (e == tok) d += gl;
-    g[e] = from_f32<T>(l == kNegInf ? 0.0f : d);
+    for (int i = 0; i < kGradVecs; ++i) {
+      const int v = v0 + i * kGradThreads;
+      if (v >= vecs) break;
+      const unsigned w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float d[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) d[j] = q.at(Word<T>::get(w[j / N], j % N));
+      const int at = tok - head - v * E;   // the token's place in the vector
+      if (at >= 0 && at < E) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) d[j] += j == at ? q.gl : 0.0f;
+      }
+      uint4 o;
+      if constexpr (N == 1) {
+        o = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+      } else {
+        unsigned y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = Word<T>::pack(d[2 * j], d[2 * j + 1]);
+        o = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      reinterpret_cast<uint4*>(g + head)[v] = o;
+    }
+    if (part > 0) return;
+    for (int k = threadIdx.x; k < vocab - vecs * E; k += kGradThreads) {
+      const int e = k < head ? k : vecs * E + k;
+      g[e] = from_f32<T>(q.at(to_f32(row[e])) + (e == tok ? q.gl : 0.0f));
+    }
+  } else {
+    const int first = part * (kGradThreads * kGradVecs * E);
+    for (int e = first + threadIdx.x; e < min(first + kGradThreads * kGradVecs * E, vocab); e += kGradThreads)
+      g[e] = from_f32<T>(q.at(to_f32(row[e])) + (e == tok ? q.gl : 0.0f));
   }
 }
 
@@ -311,11 +494,20 @@ template <typename T>
 int launch_grad(const void* logits, long long rows, long long vocab, long long stride, const int32_t* tokens,
                 const float* lse, const float* entropy, const float* gl, const float* gh, void* grad,
                 long long grad_stride, cudaStream_t s) {
-  const long long per = (long long)kGradThreads * kGradElems;
-  const dim3 grid((unsigned)rows, (unsigned)((vocab + per - 1) / per));
+  const long long per = (long long)kGradThreads * kGradVecs * (16 / sizeof(T)), ctas = (vocab + per - 1) / per;
+  if (rows * ctas >= (1LL << 31)) return DET_ERR_TOO_LARGE;
+  // every row pair starts at the same place of a 16-byte block
+  const bool same = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(grad)) % 16 == 0) &&
+                    (rows == 1 || (stride - grad_stride) * (long long)sizeof(T) % 16 == 0);
   launch_begin("det_token_logprobs_backward", s);
-  token_logprobs_grad_kernel<T><<<grid, kGradThreads, 0, s>>>(static_cast<const T*>(logits), vocab, stride, tokens, lse,
-                                                              entropy, gl, gh, static_cast<T*>(grad), grad_stride);
+  if (same)
+    token_logprobs_grad_kernel<T, true><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
+        static_cast<const T*>(logits), (int)vocab, stride, tokens, lse, entropy, gl, gh, static_cast<T*>(grad),
+        grad_stride, (unsigned)ctas);
+  else
+    token_logprobs_grad_kernel<T, false><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
+        static_cast<const T*>(logits), (int)vocab, stride, tokens, lse, entropy, gl, gh, static_cast<T*>(grad),
+        grad_stride, (unsigned)ctas);
   launch_end(s);
   return check_launch("det_token_logprobs_backward");
 }

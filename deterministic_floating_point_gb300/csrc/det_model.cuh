@@ -11,6 +11,7 @@
 namespace det {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -93,7 +93,7 @@ template <> struct Out16<__half> {
   }
 };
 
-template <typename T>
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kBiasThreads)
 bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
                   T* __restrict__ out) {
@@ -111,6 +111,43 @@ bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Di
   __syncthreads();
   for (int u = threadIdx.x; u < kStrip; u += kBiasThreads) strip[u + (u >> 3)] = Out16<T>::word(value[u], value[u + 1]);
   __syncthreads();
+  if constexpr (ALIGNED) {
+    // Every row's eights start at the same keys.  Eight rows of a thread's
+    // eight cross 15 diagonals: two eights of the strip, and the next
+    // eight rows need one more.
+    const int j = 8 * (c0 - 1 + (int)threadIdx.x);
+    if (j < 0 || j >= k_len) return;
+    if (j + 8 <= k_len) {
+      unsigned lo[8], hi[8];
+      const unsigned* at = strip + 9 * (threadIdx.x + kBiasRows / 8);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) hi[x] = at[x];
+      T* p = out + ((long long)h * q_len + i0) * k_len + j;
+      for (int y0 = 0; y0 < rows; y0 += 8) {
+        at -= 9;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) lo[x] = at[x];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          if (y0 + y < rows) {
+            unsigned w[8 / E];
+#pragma unroll
+            for (int x = 0; x < 8 / E; ++x) {
+              const int k = 7 - y + x * E;
+              w[x] = k < 8 ? lo[k] : hi[k - 8];
+            }
+#pragma unroll
+            for (int x = 0; x < 8 / kUnit; ++x)
+              *reinterpret_cast<uint4*>(p + x * kUnit) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            p += k_len;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) hi[x] = lo[x];
+      }
+      return;
+    }
+  }
   for (int y = 0; y < rows; ++y) {
     const int i = i0 + y;
     T* row = out + ((long long)h * q_len + i) * k_len;
@@ -396,9 +433,14 @@ int launch_bias(const void* table, int table_dtype, int heads, const Distances& 
     const dim3 grid((unsigned)((eights + kBiasThreads - 1) / kBiasThreads),
                     (unsigned)((q_len + kBiasRows - 1) / kBiasRows), (unsigned)heads);
     if (grid.y > 65535) return DET_ERR_TOO_LARGE;
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)k_len * sizeof(T)) % 16 == 0;
     launch_begin("det_relative_bias", s);
-    bias_strip_kernel<T><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
-                                                       static_cast<T*>(out));
+    if (aligned)
+      bias_strip_kernel<T, true><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
+                                                               static_cast<T*>(out));
+    else
+      bias_strip_kernel<T, false><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
+                                                                static_cast<T*>(out));
   }
   launch_end(s);
   return check_launch("det_relative_bias");

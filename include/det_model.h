@@ -73,7 +73,8 @@ int det_token_logprobs(const void* logits, int64_t rows, int64_t vocab, int64_t 
  *   tokens         may be NULL when grad_logprob is
  *   grad_logits    device, rows x vocab of dtype (written), row r at element
  *                  r * grad_row_stride; must not overlap the inputs
- * Limits: as det_token_logprobs, vocab < 2^28.
+ * Limits: vocab < 2^28, rows x (vocab rounded up to 8,192) below 2^42 (4,096
+ * and 2^41 for DET_F32).
  */
 int det_token_logprobs_backward(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride,
                                 const int32_t* tokens, int dtype, const float* lse, const float* entropy,
