@@ -11,6 +11,7 @@
 #include "det_model.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace det {
 namespace {
@@ -27,6 +28,7 @@ template <> struct Word<float> {
   static __device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
     return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
+  static __device__ __forceinline__ unsigned pack(float a, float) { return __float_as_uint(a); }
 };
 template <> struct Word<__nv_bfloat16> {
   static constexpr int N = 2;
@@ -77,11 +79,6 @@ __device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, un
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b,
                                                         unsigned long long c) {
   unsigned long long r;
@@ -106,23 +103,34 @@ __device__ __forceinline__ unsigned load_word(const T* row, long long w, long lo
   }
 }
 
-// Running maximum and the two sums relative to it (relative to 0 while the
-// maximum is -inf: both sums are 0 then).
+// A thread's (or row's) statistics in units of log 2: the largest logit m,
+// and S = sum 2^y, T = sum 2^y y with y = x log2(e) - ref.  Where log2(e) m
+// is far from overflow (near()), ref is that product rounded, so y takes one
+// fused operation for an element; otherwise (the types' lowest values,
+// infinities, NaN) ref is the exact product, and y = (x - m) log2(e).
 struct Stat {
   float m, s, t;
 };
-__device__ __forceinline__ float stat_base(float m) { return m == kNegInf ? 0.0f : m; }
-// a and b joined, a's elements the earlier ones.
-__device__ __forceinline__ Stat stat_join(const Stat& a, const Stat& b) {
-  Stat r;
-  r.m = max_nan(a.m, b.m);
-  const float base = stat_base(r.m);
-  // a side without a logit above -inf has sums of 0; its maximum may not enter (0 * inf)
-  const float da = a.m == kNegInf ? 0.0f : a.m - base, db = b.m == kNegInf ? 0.0f : b.m - base;
-  const float ca = exp2_approx(da * kLog2e), cb = exp2_approx(db * kLog2e);
-  r.s = a.s * ca + b.s * cb;
-  r.t = (ca > 0.0f ? ca * fmaf(a.s, da, a.t) : ca) + (cb > 0.0f ? cb * fmaf(b.s, db, b.t) : cb);
-  return r;
+template <typename T> __device__ __forceinline__ bool near_max(float m) {
+  // in f16 also: the bound for masked logits, m - 150 and a little, is a finite value
+  return m > (std::is_same<T, __half>::value ? -60000.0f : -1e30f) && m < 1e30f;
+}
+// The reference of `from` less that of m, in units of log 2.
+template <typename T> __device__ __forceinline__ float ref_step(float from, float m) {
+  const bool a = near_max<T>(from), b = near_max<T>(m);
+  if (a && b) return from * kLog2e - m * kLog2e;
+  if (a) return -fmaf(m, kLog2e, -(from * kLog2e));
+  if (b) return fmaf(from, kLog2e, -(m * kLog2e));
+  return (from - m) * kLog2e;
+}
+// S and T brought to the reference of m, which is not below st.m.
+template <typename T> __device__ __forceinline__ void raise_to(Stat& st, float m) {
+  if (st.m != kNegInf) {
+    const float d = ref_step<T>(st.m, m), f = exp2_approx(d);
+    st.t = f > 0.0f ? f * fmaf(st.s, d, st.t) : f;   // no 0 * inf; NaN stays
+    st.s *= f;
+  }
+  st.m = m;
 }
 
 // The sorted list of a warp's best keys, the largest in lane 0; a key is the
@@ -140,143 +148,100 @@ struct RowOut {
   int32_t* top_index;
 };
 
-// The top_k largest of the row, after the pass: `best` is the thread's own
-// largest element.  The k-th largest of the two best threads of every warp is
-// a lower bound of the row's k-th largest element, so only threads whose best
-// reaches it are looked through again, each by its whole warp.
-template <typename T>
-__device__ void top_alternatives(const T* row, long long vocab, bool words_aligned, float best, int k, float m,
-                                 float log_s, long long r, const RowOut& out) {
-  __shared__ unsigned sh_best[2 * kRowWarps];
-  __shared__ unsigned sh_floor;
-  __shared__ unsigned long long sh_list[kRowWarps * DET_MAX_TOP_K];
-  __shared__ int sh_count[kRowWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned key = order_key(best);
-  const unsigned first = __reduce_max_sync(0xffffffffu, key);
-  const int owner = __ffs(__ballot_sync(0xffffffffu, key == first)) - 1;
-  const unsigned second = __reduce_max_sync(0xffffffffu, lane == owner ? 0u : key);
-  if (lane == 0) {
-    sh_best[2 * warp] = first;
-    sh_best[2 * warp + 1] = second;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const unsigned b = sh_best[lane];
-    int above = 0;
-    for (int j = 0; j < 32; ++j) {
-      const unsigned o = __shfl_sync(0xffffffffu, b, j);
-      above += (o > b || (o == b && j < lane)) ? 1 : 0;
-    }
-    if (above == k - 1) sh_floor = b;
-  }
-  __syncthreads();
-  const unsigned floor_key = sh_floor;
-  const long long words = (vocab + Word<T>::N - 1) / Word<T>::N;
-  unsigned long long mine = 0;   // below every key: an element's key has a nonzero complement of its index
-  unsigned todo = __ballot_sync(0xffffffffu, key >= floor_key);
-  while (todo) {
-    const int owner_lane = __ffs(todo) - 1;
-    todo &= todo - 1;
-    for (long long base = warp * 32 + owner_lane; base < words; base += 32LL * kRowThreads) {
-      const long long w = base + (long long)lane * kRowThreads;
-      const unsigned word = w < words ? load_word(row, w, vocab, words_aligned) : 0u;
-#pragma unroll
-      for (int j = 0; j < Word<T>::N; ++j) {
-        const long long e = w * Word<T>::N + j;
-        unsigned long long cand = 0;
-        if (e < vocab) {
-          const unsigned ek = order_key(Word<T>::get(word, j));
-          if (ek >= floor_key) cand = ((unsigned long long)ek << 32) | (unsigned)~(unsigned)e;
-        }
-        const unsigned long long worst = __shfl_sync(0xffffffffu, mine, k - 1);
-        unsigned hits = __ballot_sync(0xffffffffu, cand > worst);
-        while (hits) {
-          const int src = __ffs(hits) - 1;
-          hits &= hits - 1;
-          list_insert(mine, __shfl_sync(0xffffffffu, cand, src), lane);
-        }
-      }
-    }
-  }
-  const int count = min(k, __popc(__ballot_sync(0xffffffffu, mine != 0)));
-  if (lane == 0) sh_count[warp] = count;
-  __syncthreads();
-  int at = 0, total = 0;
-  for (int w = 0; w < kRowWarps; ++w) {
-    at += w < warp ? sh_count[w] : 0;
-    total += sh_count[w];
-  }
-  if (lane < count) sh_list[at + lane] = mine;
-  __syncthreads();
-  if (threadIdx.x < total) {
-    const unsigned long long c = sh_list[threadIdx.x];
-    int rank = 0;
-    for (int j = 0; j < total; ++j) rank += sh_list[j] > c ? 1 : 0;
-    if (rank < k) {
-      const float x = key_value((unsigned)(c >> 32));
-      if (out.top_index) out.top_index[r * k + rank] = (int32_t)~(unsigned)c;
-      if (out.top_logprob) out.top_logprob[r * k + rank] = (x - m) - log_s;
-    }
-  }
-}
+// A row streams through shared memory in chunks of 512 threads x 16 words,
+// word i of thread t of chunk c being word (16 c + i) 512 + t of the row (a
+// 4-byte word: two elements of the 16-bit types).  One bulk copy fetches a
+// chunk, kStages - 1 ahead of its use and across the ends of rows.  It takes the
+// 16-byte blocks that lie inside the row, and puts them where the row's bytes
+// have their place modulo 16, so that nothing outside a row is read; the few
+// words at a row's ends that no block holds (its edges) are fetched by their threads
+// a row ahead.  In a 16-bit row that starts at an odd element a thread's
+// word lies in two words of shared memory.
+constexpr int kChunkWords = kRowThreads * kWords;
+constexpr int kChunkBytes = kChunkWords * 4;
+constexpr int kStages = 3;
+constexpr int kStageBytes = kChunkBytes + 32;   // a row's start modulo 16, and the block behind the chunk
 
-// A row in chunks of 512 threads x 16 words, a thread's word i of chunk c
-// being word (16 c + i) 512 + t: a warp reads 128 neighbouring bytes.  Words
-// are 4-byte aligned in memory, except in 16-bit rows that start at an odd
-// element (ODD): there a thread reads the aligned word that holds the first of
-// its two elements and gets the other from the next lane, whose word holds it
-// (the last lane's from an extra word a lane loads for each i).
+struct Stream {
+  alignas(16) unsigned char stage[kStages][kStageBytes];
+  unsigned long long full[kStages], empty[kStages];
+};
+
+// Where the parts of a row lie.
 template <typename T>
-struct RowReader {
+struct RowMap {
+  static constexpr int N = Word<T>::N;
   const T* row;
-  long long vocab, words;
-  bool odd;
-  const unsigned* base;   // the aligned word with (the first element of) the thread's word 0
-  const unsigned* extra;  // of the word behind the warp's last, for i = lane % 16
+  int vocab, words;
+  long long bytes;        // of the row
+  int off;                // the row's start modulo 16
+  long long in0, in1;     // the bytes of the row's whole 16-byte blocks, from its start
+  int head, tail;         // words [0, head) and [tail, words) are edges
 
-  __device__ __forceinline__ RowReader(const T* row_, long long vocab_) : row(row_), vocab(vocab_) {
-    words = (vocab + Word<T>::N - 1) / Word<T>::N;
-    odd = Word<T>::N == 2 && (reinterpret_cast<uintptr_t>(row) & 3);
-    const unsigned* aligned = reinterpret_cast<const unsigned*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)3);
-    base = aligned + threadIdx.x;
-    extra = aligned + (threadIdx.x & 15) * kRowThreads + (threadIdx.x & ~31u) + 32;
+  __device__ __forceinline__ RowMap(const T* row_, int vocab_) : row(row_), vocab(vocab_) {
+    words = (vocab + N - 1) / N;
+    bytes = (long long)vocab * (int)sizeof(T);
+    off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    in0 = (16 - off) & 15;
+    in1 = max(in0, ((bytes + off) & ~15LL) - off);
+    tail = (int)(in1 >> 2);
+    head = min((int)((in0 + 3) >> 2), tail);
+    if (in1 == in0) head = tail = 0;   // no whole block: every word (at most 8) is an edge
   }
-  // Raw words of the chunk whose first word is w0.  A word read here lies
-  // inside the row; what is not is left to finish().
-  __device__ __forceinline__ void start(long long w0, unsigned (&x)[kWords], unsigned& more) const {
-    // every aligned word up to index w0 + 16 * 512 is inside the row, and word 0 is not half outside
-    const bool inside = odd ? w0 > 0 && 2 * (w0 + kWords * kRowThreads) < vocab
-                            : Word<T>::N * (w0 + kWords * kRowThreads) <= vocab;
-    if (inside) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) x[i] = __ldg(base + w0 + i * kRowThreads);
-      if (odd) more = __ldg(extra + w0);
-    } else if (!odd) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) x[i] = load_word(row, w0 + threadIdx.x + i * kRowThreads, vocab, true);
-    }
+  __device__ __forceinline__ bool odd() const { return N == 2 && (off & 2); }
+  // Whether chunk c has edges or masked words.
+  __device__ __forceinline__ bool ragged(int c) const {
+    return (c == 0 && head > 0) || (long long)(c + 1) * kChunkWords > tail;
   }
-  __device__ __forceinline__ void finish(long long w0, unsigned (&x)[kWords], unsigned more) const {
-    if (!odd) return;
-    if (w0 > 0 && 2 * (w0 + kWords * kRowThreads) < vocab) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        unsigned next = __shfl_down_sync(0xffffffffu, x[i], 1);
-        const unsigned last = __shfl_sync(0xffffffffu, more, i);
-        if ((threadIdx.x & 31) == 31) next = last;
-        x[i] = __funnelshift_r(x[i], next, 16);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) x[i] = load_word(row, w0 + threadIdx.x + i * kRowThreads, vocab, false);
-    }
+  // The thread's word among the last edges, or -1.
+  __device__ __forceinline__ int tail_word() const {
+    const int w = tail + (((int)threadIdx.x - tail) & (kRowThreads - 1));
+    return w < words ? w : -1;
+  }
+  // Fetch chunk c into a stage (one thread).
+  __device__ __forceinline__ void fetch(Stream& st, int stage, int c) const {
+    const long long lo = (long long)c * kChunkBytes;             // of the chunk, from the row's start
+    const long long from = c == 0 ? in0 : lo - off;              // a 16-byte boundary
+    const long long to = min(in1, lo - off + kStageBytes);
+    const unsigned n = to > from ? (unsigned)(to - from) : 0u;
+    mbar_arrive_expect_tx(&st.full[stage], n);
+    if (n)
+      bulk_copy_g2s(st.stage[stage] + (from - (lo - off)), reinterpret_cast<const char*>(row) + from, n, &st.full[stage]);
   }
 };
 
-// The chunk's elements added to the thread's statistics.
+// The thread's words of a chunk that has arrived.
+template <bool ODD>
+__device__ __forceinline__ void read_words(const unsigned char* stage, int off, unsigned (&x)[kWords]) {
+  const unsigned* p = reinterpret_cast<const unsigned*>(stage + (off & ~3)) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    x[i] = p[i * kRowThreads];
+    if (ODD) x[i] = __funnelshift_r(x[i], p[i * kRowThreads + 1], 16);
+  }
+}
+// Edges from where their threads hold them, and masked logits past the end.
 template <typename T>
-__device__ __forceinline__ void add_chunk(Stat& st, const unsigned (&x)[kWords]) {
+__device__ __forceinline__ void set_edges(const RowMap<T>& map, int c, unsigned head, unsigned tail, unsigned (&x)[kWords]) {
+  const int w0 = c * kChunkWords + threadIdx.x, tail_word = map.tail_word();
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int w = w0 + i * kRowThreads;
+    if (w < map.head) x[i] = head;
+    if (w >= map.tail) x[i] = w == tail_word ? tail : Word<T>::kMasked;
+  }
+}
+
+// Of a thread's elements: the chunk of the largest, and the largest of the
+// other chunks.
+struct Best {
+  int chunk;
+  float others;
+};
+
+// Chunk c's elements added to the thread's statistics.
+template <typename T>
+__device__ __forceinline__ void add_chunk(Stat& st, Best& best, int c, const unsigned (&x)[kWords]) {
   constexpr int N = Word<T>::N;
   unsigned mx[kWords / 2];
 #pragma unroll
@@ -287,79 +252,291 @@ __device__ __forceinline__ void add_chunk(Stat& st, const unsigned (&x)[kWords])
     for (int i = 0; i < s; ++i) mx[i] = Word<T>::larger(mx[i], mx[i + s]);
   float m = Word<T>::get(mx[0], 0);
   if (N == 2) m = max_nan(m, Word<T>::get(mx[0], 1));
-  if (!(m <= st.m)) {   // a new maximum (or NaN): the sums so far relative to it
-    if (st.m != kNegInf) {
-      const float d = st.m - m, f = exp2_approx(d * kLog2e);
-      st.t = f > 0.0f ? f * fmaf(st.s, d, st.t) : f;   // no 0 * inf
-      st.s *= f;
-    }
-    st.m = max_nan(st.m, m);
+  if (!(m <= st.m)) {   // a new maximum, or NaN
+    best.chunk = c;
+    best.others = st.m;
+    raise_to<T>(st, max_nan(st.m, m));
+  } else {
+    best.others = max_nan(best.others, m);
   }
-  const float base = stat_base(st.m);
-  const unsigned long long minus = pack_f32x2(-base, -base), scale = pack_f32x2(kLog2e, kLog2e);
   unsigned long long s2 = 0, t2 = 0;   // of elements 0 and 1 of the words (f32: even and odd words)
+  if (near_max<T>(st.m)) {
+    const float ref = -(st.m * kLog2e);
+    const unsigned long long c = pack_f32x2(kLog2e, kLog2e), minus = pack_f32x2(ref, ref);
+    // 2^y is 0 from y = -127 on: a bound of -150 for x - m changes no term, and
+    // without it 0 * inf for a masked logit.  16-bit logits are bounded in
+    // pairs, by a value below m - 150 in every rounding.
+    const float low = st.m - 150.0f - fabsf(st.m) * 0.015625f;
+    const unsigned low2 = Word<T>::N == 2 ? Word<T>::pack(low, low) : 0u;
 #pragma unroll
-  for (int i = 0; i < kWords; i += 3 - N) {
-    const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % kWords], 0);
-    const float2 y = unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(a, b), minus), scale));
-    // 2^-150 is 0 already; without the bound 0 * inf for a masked logit
-    const float y0 = max_nan(y.x, -150.0f), y1 = max_nan(y.y, -150.0f);
-    const unsigned long long e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
-    s2 = add_f32x2(s2, e);
-    t2 = fma_f32x2(e, pack_f32x2(y0, y1), t2);
+    for (int i = 0; i < kWords; i += 3 - N) {
+      unsigned long long v;
+      if constexpr (N == 2) {
+        const unsigned w = Word<T>::larger(x[i], low2);
+        v = pack_f32x2(Word<T>::get(w, 0), Word<T>::get(w, 1));
+      } else {
+        v = pack_f32x2(max_nan(__uint_as_float(x[i]), low), max_nan(__uint_as_float(x[i + 1]), low));
+      }
+      v = fma_f32x2(v, c, minus);
+      const float2 y = unpack_f32x2(v);
+      const unsigned long long e = pack_f32x2(exp2_approx(y.x), exp2_approx(y.y));
+      s2 = add_f32x2(s2, e);
+      t2 = fma_f32x2(e, v, t2);
+    }
+  } else {
+    const float base = st.m == kNegInf ? 0.0f : st.m;
+#pragma unroll
+    for (int i = 0; i < kWords; i += 3 - N) {
+      const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % kWords], 0);
+      const float y0 = max_nan((a - base) * kLog2e, -200.0f), y1 = max_nan((b - base) * kLog2e, -200.0f);
+      const unsigned long long e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
+      s2 = add_f32x2(s2, e);
+      t2 = fma_f32x2(e, pack_f32x2(y0, y1), t2);
+    }
   }
   const float2 s = unpack_f32x2(s2), t = unpack_f32x2(t2);
   st.s += s.x + s.y;
-  st.t = fmaf(t.x + t.y, kLn2, st.t);   // y is d in units of log 2
+  st.t += t.x + t.y;
 }
 
+// Shared memory of a row's end.
+struct RowEnd {
+  unsigned best[4 * kRowWarps];   // the order keys of every warp's four best threads
+  float s[kRowWarps], t[kRowWarps];
+  unsigned floor;
+  int count[kRowWarps];
+  unsigned long long list[kRowWarps * DET_MAX_TOP_K];
+};
+
+// The top_k largest of the row.  end.best holds the order keys of the four
+// best threads of every warp: the k-th largest of those 64 is a lower bound of
+// the row's k-th largest element, so only threads whose best reaches it are
+// looked through again, each by half of its warp, whose lanes keep the best in
+// order: the 16 words of the chunk with its best, and all its words only if
+// another chunk has such an element too.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 2)
-token_logprobs_kernel(const T* __restrict__ logits, long long vocab, long long row_stride,
-                      const int32_t* __restrict__ tokens, int top_k, RowOut out) {
-  __shared__ Stat sh[kRowWarps];
-  const long long r = blockIdx.x;
-  const T* row = logits + r * row_stride;
-  const RowReader<T> reader(row, vocab);
-  const bool aligned = !reader.odd;
-  Stat st = {kNegInf, 0.0f, 0.0f};
-  // the next chunk's loads are in flight while a chunk is added
-  constexpr long long kStep = (long long)kRowThreads * kWords;
-  unsigned x[kWords], ahead[kWords], more = 0, more_ahead = 0;
-  if (reader.words > 0) reader.start(0, x, more);
-  for (long long w0 = 0; w0 < reader.words; w0 += kStep) {
-    if (w0 + kStep < reader.words) reader.start(w0 + kStep, ahead, more_ahead);
-    reader.finish(w0, x, more);
-    add_chunk<T>(st, x);
+__device__ void top_alternatives(const T* row, int vocab, float largest, const Best& best, int k, float m, float log_s,
+                                 long long r, RowEnd& end, const RowOut& out) {
+  constexpr int N = Word<T>::N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  {
+    const unsigned a = end.best[lane], b = end.best[lane + 32];
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) x[i] = ahead[i];
-    more = more_ahead;
-  }
-  const float best = st.m;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    Stat o;
-    o.m = __shfl_xor_sync(0xffffffffu, st.m, s);
-    o.s = __shfl_xor_sync(0xffffffffu, st.s, s);
-    o.t = __shfl_xor_sync(0xffffffffu, st.t, s);
-    st = (threadIdx.x & s) ? stat_join(o, st) : stat_join(st, o);
-  }
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = st;
-  __syncthreads();
-  st = sh[0];
-  for (int w = 1; w < kRowWarps; ++w) st = stat_join(st, sh[w]);
-  const bool empty = st.m == kNegInf;
-  const float log_s = empty ? 0.0f : logf(st.s);
-  const float base = stat_base(st.m);
-  if (threadIdx.x == 0) {
-    if (out.lse) out.lse[r] = empty ? kNegInf : base + log_s;
-    if (out.entropy) out.entropy[r] = empty ? 0.0f : log_s - st.t / st.s;
-    if (out.logprob) {
-      const long long tok = tokens[r];
-      out.logprob[r] = tok >= 0 && tok < vocab ? (to_f32(row[tok]) - base) - log_s : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      const int at = 4 * warp + j;
+      const unsigned mine = end.best[at];
+      const int above = __popc(__ballot_sync(0xffffffffu, a > mine || (a == mine && lane < at))) +
+                        __popc(__ballot_sync(0xffffffffu, b > mine || (b == mine && lane + 32 < at)));
+      if (above == k - 1) end.floor = mine;
     }
   }
-  if (top_k > 0) top_alternatives(row, vocab, aligned, best, top_k, base, log_s, r, out);
+  __syncthreads();
+  const unsigned floor_key = end.floor;
+  const bool aligned = (reinterpret_cast<uintptr_t>(row) & 3) == 0;
+  const int words = (vocab + N - 1) / N, chunks = (words + kChunkWords - 1) / kChunkWords;
+  unsigned long long mine = 0;   // below every key
+  // the threads to look through: at one chunk, or at every one from 0 up
+  unsigned one = __ballot_sync(0xffffffffu, order_key(largest) >= floor_key);
+  unsigned all = __ballot_sync(0xffffffffu, order_key(largest) >= floor_key && order_key(best.others) >= floor_key);
+  one &= ~all;
+  int all_chunk = 0;
+  constexpr int kAhead = 4;      // loads in flight, each of two threads' chunks
+  while (one | all) {
+    unsigned word[kAhead];
+    int at[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      int owner[2], chunk[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        owner[half] = 0;
+        chunk[half] = chunks;   // none
+        if (one) {
+          owner[half] = __ffs(one) - 1;
+          one &= one - 1;
+          chunk[half] = __shfl_sync(0xffffffffu, best.chunk, owner[half]);
+        } else if (all) {
+          owner[half] = __ffs(all) - 1;
+          chunk[half] = all_chunk;
+          if (++all_chunk == chunks) {
+            all_chunk = 0;
+            all &= all - 1;
+          }
+        }
+      }
+      const int c = lane < 16 ? chunk[0] : chunk[1];
+      at[a] = words;
+      word[a] = 0u;
+      if (c < chunks) {
+        at[a] = c * kChunkWords + (lane & 15) * kRowThreads + warp * 32 + (lane < 16 ? owner[0] : owner[1]);
+        if (at[a] < words) word[a] = load_word(row, at[a], vocab, aligned);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int e = at[a] * N + j;
+        unsigned long long cand = 0;
+        if (at[a] < words && e < vocab) {
+          const unsigned ek = order_key(Word<T>::get(word[a], j));
+          if (ek >= floor_key) cand = ((unsigned long long)ek << 32) | (unsigned)~(unsigned)e;
+        }
+        if (!__any_sync(0xffffffffu, cand != 0)) continue;
+        const unsigned long long worst = __shfl_sync(0xffffffffu, mine, k - 1);
+        unsigned hits = __ballot_sync(0xffffffffu, cand > worst);
+        while (hits) {
+          const int src = __ffs(hits) - 1;
+          hits &= hits - 1;
+          list_insert(mine, __shfl_sync(0xffffffffu, cand, src), lane);
+        }
+      }
+  }
+  const int count = min(k, __popc(__ballot_sync(0xffffffffu, mine != 0)));
+  if (lane == 0) end.count[warp] = count;
+  __syncthreads();
+  int before = lane < warp && lane < kRowWarps ? end.count[lane] : 0, total = lane < kRowWarps ? end.count[lane] : 0;
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane < count) end.list[before + lane] = mine;
+  __syncthreads();
+  if (threadIdx.x < total) {
+    const unsigned long long c = end.list[threadIdx.x];
+    int rank = 0;
+    for (int j = 0; j < total; ++j) rank += end.list[j] > c ? 1 : 0;
+    if (rank < k) {
+      const float x = key_value((unsigned)(c >> 32));
+      if (out.top_index) out.top_index[r * k + rank] = (int32_t)~(unsigned)c;
+      if (out.top_logprob) out.top_logprob[r * k + rank] = (x - m) - log_s;
+    }
+  }
+}
+
+// The threads' statistics joined, and the row's results.
+template <typename T>
+__device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* row, int vocab, long long r,
+                                           const int32_t* tokens, int top_k, RowEnd& end, const RowOut& out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the token's logit is on its way meanwhile
+  int tok = -1;
+  float at = 0.0f;
+  if (threadIdx.x == 0 && out.logprob) {
+    tok = tokens[r];
+    if (tok >= 0 && tok < vocab) at = to_f32(row[tok]);
+  }
+  const float largest = st.m;
+  unsigned left = order_key(largest);
+  for (int j = 0; j < (top_k > 0 ? 4 : 1); ++j) {
+    const unsigned top = __reduce_max_sync(0xffffffffu, left);
+    if (lane == 0) end.best[4 * warp + j] = top;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, left == top)) - 1;
+    if (lane == owner) left = 0u;
+  }
+  __syncthreads();
+  const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[4 * (lane & (kRowWarps - 1))]));
+  raise_to<T>(st, m);
+  float s = warp_pt(st.s), t = warp_pt(st.t);
+  if (lane == 0) {
+    end.s[warp] = s;
+    end.t[warp] = t;
+  }
+  __syncthreads();
+  s = end.s[lane & (kRowWarps - 1)];
+  t = end.t[lane & (kRowWarps - 1)];
+#pragma unroll
+  for (int d = 1; d < kRowWarps; d <<= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, d);
+    t += __shfl_xor_sync(0xffffffffu, t, d);
+  }
+  const bool empty = m == kNegInf;
+  const float base = empty ? 0.0f : m;
+  // log of the sum relative to exp(m): the reference is m log2(e) up to its rounding
+  const float log_2s = empty ? 0.0f : logf(s);
+  const float log_s = near_max<T>(m) ? fmaf(-kLn2, fmaf(m, kLog2e, -(m * kLog2e)), log_2s) : log_2s;
+  if (threadIdx.x == 0) {
+    if (out.lse) out.lse[r] = empty ? kNegInf : base + log_s;
+    if (out.entropy) out.entropy[r] = empty ? 0.0f : log_2s - kLn2 * (t / s);
+    if (out.logprob) out.logprob[r] = tok >= 0 && tok < vocab ? (at - base) - log_s : 0.0f;
+  }
+  if (top_k > 0) top_alternatives(row, vocab, largest, best, top_k, base, log_s, r, end, out);
+}
+
+// Persistent: CTA b takes the rows b, b + gridDim.x, ...  A wait for a copy
+// that does not end within kWaitNs gives up: the row's results are NaN then.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 2)
+token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, long long row_stride,
+                      const int32_t* __restrict__ tokens, int top_k, RowOut out) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  Stream& stream = *reinterpret_cast<Stream*>(dynamic);
+  __shared__ RowEnd end;
+  const int lane = threadIdx.x & 31;
+  const int chunks = max(1, (int)(((long long)vocab + Word<T>::N * kChunkWords - 1) / (Word<T>::N * kChunkWords)));
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&stream.full[i], 1);
+      mbar_init(&stream.empty[i], kRowWarps);
+    }
+  __syncthreads();
+  // the next chunk to fetch, its stage and how often the stage was filled
+  long long next_row = blockIdx.x;
+  int next_chunk = 0, next_stage = 0, next_round = 0;
+  bool gave_up = false;
+  auto fetch_next = [&](bool mine) {
+    if (next_row >= rows) return;
+    if (mine) {
+      if (next_round > 0 && !gave_up) gave_up = !mbar_wait(&stream.empty[next_stage], (next_round - 1) & 1, kWaitNs);
+      if (!gave_up) RowMap<T>(logits + next_row * row_stride, vocab).fetch(stream, next_stage, next_chunk);
+    }
+    if (++next_chunk == chunks) {
+      next_chunk = 0;
+      next_row += gridDim.x;
+    }
+    if (++next_stage == kStages) {
+      next_stage = 0;
+      ++next_round;
+    }
+  };
+  for (int i = 0; i < kStages - 1; ++i) fetch_next(threadIdx.x == 0);
+  // a thread's edges of the row after the current one
+  unsigned head_ahead = 0, tail_ahead = 0;
+  auto load_edges = [&](long long r) {
+    if (r >= rows) return;
+    const RowMap<T> map(logits + r * row_stride, vocab);
+    const bool aligned = (map.off & 3) == 0;
+    if ((int)threadIdx.x < map.head) head_ahead = load_word(map.row, threadIdx.x, vocab, aligned);
+    const int w = map.tail_word();
+    if (w >= 0) tail_ahead = load_word(map.row, w, vocab, aligned);
+  };
+  load_edges(blockIdx.x);
+  int stage = 0, round = 0, turn = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    const RowMap<T> map(logits + r * row_stride, vocab);
+    const unsigned head = head_ahead, tail = tail_ahead;
+    load_edges(r + gridDim.x);
+    Stat st = {kNegInf, 0.0f, 0.0f};
+    Best best = {0, kNegInf};
+    for (int c = 0; c < chunks; ++c) {
+      // the warps take turns at waiting for the stage that all have read and filling it
+      fetch_next(threadIdx.x == turn * 32);
+      turn = (turn + 1) & (kRowWarps - 1);
+      if (!gave_up) gave_up = !mbar_wait(&stream.full[stage], round & 1, kWaitNs);
+      unsigned x[kWords];
+      const bool odd = map.odd(), ragged = map.ragged(c);
+      if (odd) read_words<true>(stream.stage[stage], map.off, x);
+      else read_words<false>(stream.stage[stage], map.off, x);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stream.empty[stage]);
+      if (ragged) set_edges(map, c, head, tail, x);
+      add_chunk<T>(st, best, c, x);
+      if (++stage == kStages) {
+        stage = 0;
+        ++round;
+      }
+    }
+    if (gave_up) st.m = __uint_as_float(0x7fc00000u);
+    finish_row(st, best, map.row, vocab, r, tokens, top_k, end, out);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -481,11 +658,14 @@ token_logprobs_grad_kernel(const T* __restrict__ logits, int vocab, long long ro
 }
 
 template <typename T>
-int launch_logprobs(const void* logits, long long rows, long long vocab, long long stride, const int32_t* tokens,
-                    int top_k, const RowOut& out, cudaStream_t s) {
+int launch_logprobs(const void* logits, long long rows, int vocab, long long stride, const int32_t* tokens, int top_k,
+                    const RowOut& out, cudaStream_t s) {
+  const void* kernel = reinterpret_cast<const void*>(&token_logprobs_kernel<T>);
+  if (const cudaError_t e = ensure_dyn_smem(kernel, sizeof(Stream))) return cuda_fail(e, "det_token_logprobs");
+  const long long grid = std::min(rows, 2LL * std::max(device_sm_count(), 1));
   launch_begin("det_token_logprobs", s);
-  token_logprobs_kernel<T><<<(unsigned)rows, kRowThreads, 0, s>>>(static_cast<const T*>(logits), vocab, stride, tokens,
-                                                                  top_k, out);
+  token_logprobs_kernel<T><<<(unsigned)grid, kRowThreads, sizeof(Stream), s>>>(static_cast<const T*>(logits), rows, vocab,
+                                                                             stride, tokens, top_k, out);
   launch_end(s);
   return check_launch("det_token_logprobs");
 }
@@ -524,15 +704,15 @@ extern "C" int det_token_logprobs(const void* logits, int64_t rows, int64_t voca
   if (!valid_model_dtype(dtype)) return DET_ERR_DTYPE;
   if (rows < 0 || vocab < 0 || row_stride < 0 || top_k < 0 || top_k > DET_MAX_TOP_K || top_k > vocab)
     return DET_ERR_INVALID_ARG;
-  if (rows >= (1LL << 31) || vocab >= (1LL << 31)) return DET_ERR_TOO_LARGE;
+  if (rows >= (1LL << 31) || vocab > (1LL << 30)) return DET_ERR_TOO_LARGE;
   if (rows == 0) return DET_OK;
   if ((vocab > 0 && !logits) || (logprob_out && !tokens)) return DET_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(logits) % model_elem_size(dtype)) return DET_ERR_INVALID_ARG;
   const RowOut out = {logprob_out, entropy_out, lse_out, top_logprob_out, top_index_out};
   const cudaStream_t s = as_stream(stream);
-  if (dtype == DET_F32) return launch_logprobs<float>(logits, rows, vocab, row_stride, tokens, top_k, out, s);
-  if (dtype == DET_BF16) return launch_logprobs<__nv_bfloat16>(logits, rows, vocab, row_stride, tokens, top_k, out, s);
-  return launch_logprobs<__half>(logits, rows, vocab, row_stride, tokens, top_k, out, s);
+  if (dtype == DET_F32) return launch_logprobs<float>(logits, rows, (int)vocab, row_stride, tokens, top_k, out, s);
+  if (dtype == DET_BF16) return launch_logprobs<__nv_bfloat16>(logits, rows, (int)vocab, row_stride, tokens, top_k, out, s);
+  return launch_logprobs<__half>(logits, rows, (int)vocab, row_stride, tokens, top_k, out, s);
 }
 
 extern "C" int det_token_logprobs_backward(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride,

@@ -53,7 +53,7 @@ extern "C" {
  *   *_out        device, rows floats each; each may be NULL
  *   top_logprob_out, top_index_out  device, rows x top_k (float, int32); each
  *                may be NULL; not used when top_k is 0
- * Limits: rows < 2^31, vocab < 2^31, top_k <= DET_MAX_TOP_K and <= vocab.
+ * Limits: rows < 2^31, vocab <= 2^30, top_k <= DET_MAX_TOP_K and <= vocab.
  */
 int det_token_logprobs(const void* logits, int64_t rows, int64_t vocab, int64_t row_stride, const int32_t* tokens,
                        int dtype, float* logprob_out, float* entropy_out, float* lse_out, int top_k,
