@@ -16,9 +16,11 @@
 namespace det {
 namespace {
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kWords = 16;   // 4-byte words of a thread's chunk
+constexpr int kWords = 32;      // 4-byte words of a thread's chunk
+constexpr int kPartWords = 4;   // a row's last chunk goes by this many
+constexpr int kBest = 64 / kRowWarps;   // threads of a warp that a bound for the alternatives is drawn from
 
 template <typename T> struct Word;   // what a 4-byte word of a row holds
 template <> struct Word<float> {
@@ -148,8 +150,8 @@ struct RowOut {
   int32_t* top_index;
 };
 
-// A row streams through shared memory in chunks of 512 threads x 16 words,
-// word i of thread t of chunk c being word (16 c + i) 512 + t of the row (a
+// A row streams through shared memory in chunks of 256 threads x 32 words,
+// word i of thread t of chunk c being word (32 c + i) 256 + t of the row (a
 // 4-byte word: two elements of the 16-bit types).  One bulk copy fetches a
 // chunk, kStages - 1 ahead of its use and across the ends of rows.  It takes the
 // 16-byte blocks that lie inside the row, and puts them where the row's bytes
@@ -210,22 +212,23 @@ struct RowMap {
   }
 };
 
-// The thread's words of a chunk that has arrived.
-template <bool ODD>
-__device__ __forceinline__ void read_words(const unsigned char* stage, int off, unsigned (&x)[kWords]) {
-  const unsigned* p = reinterpret_cast<const unsigned*>(stage + (off & ~3)) + threadIdx.x;
+// NW of the thread's words, from word i0 up, of a chunk that has arrived.
+template <bool ODD, int NW>
+__device__ __forceinline__ void read_words(const unsigned char* stage, int off, int i0, unsigned (&x)[NW]) {
+  const unsigned* p = reinterpret_cast<const unsigned*>(stage + (off & ~3)) + i0 * kRowThreads + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
+  for (int i = 0; i < NW; ++i) {
     x[i] = p[i * kRowThreads];
     if (ODD) x[i] = __funnelshift_r(x[i], p[i * kRowThreads + 1], 16);
   }
 }
-// Edges from where their threads hold them, and masked logits past the end.
-template <typename T>
-__device__ __forceinline__ void set_edges(const RowMap<T>& map, int c, unsigned head, unsigned tail, unsigned (&x)[kWords]) {
-  const int w0 = c * kChunkWords + threadIdx.x, tail_word = map.tail_word();
+// Edges from where their threads hold them, and masked logits past the end;
+// w0 is the thread's first of these words.
+template <typename T, int NW>
+__device__ __forceinline__ void set_edges(const RowMap<T>& map, int w0, unsigned head, unsigned tail, unsigned (&x)[NW]) {
+  const int tail_word = map.tail_word();
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
+  for (int i = 0; i < NW; ++i) {
     const int w = w0 + i * kRowThreads;
     if (w < map.head) x[i] = head;
     if (w >= map.tail) x[i] = w == tail_word ? tail : Word<T>::kMasked;
@@ -239,24 +242,24 @@ struct Best {
   float others;
 };
 
-// Chunk c's elements added to the thread's statistics.
-template <typename T>
-__device__ __forceinline__ void add_chunk(Stat& st, Best& best, int c, const unsigned (&x)[kWords]) {
+// NW words of chunk c added to the thread's statistics.
+template <typename T, int NW>
+__device__ __forceinline__ void add_words(Stat& st, Best& best, int c, const unsigned (&x)[NW]) {
   constexpr int N = Word<T>::N;
-  unsigned mx[kWords / 2];
+  unsigned mx[NW / 2];
 #pragma unroll
-  for (int i = 0; i < kWords / 2; ++i) mx[i] = Word<T>::larger(x[i], x[i + kWords / 2]);
+  for (int i = 0; i < NW / 2; ++i) mx[i] = Word<T>::larger(x[i], x[i + NW / 2]);
 #pragma unroll
-  for (int s = kWords / 4; s > 0; s >>= 1)
+  for (int s = NW / 4; s > 0; s >>= 1)
 #pragma unroll
     for (int i = 0; i < s; ++i) mx[i] = Word<T>::larger(mx[i], mx[i + s]);
   float m = Word<T>::get(mx[0], 0);
   if (N == 2) m = max_nan(m, Word<T>::get(mx[0], 1));
   if (!(m <= st.m)) {   // a new maximum, or NaN
+    if (c != best.chunk) best.others = st.m;   // else another part of the same chunk
     best.chunk = c;
-    best.others = st.m;
     raise_to<T>(st, max_nan(st.m, m));
-  } else {
+  } else if (c != best.chunk) {
     best.others = max_nan(best.others, m);
   }
   unsigned long long s2 = 0, t2 = 0;   // of elements 0 and 1 of the words (f32: even and odd words)
@@ -269,7 +272,7 @@ __device__ __forceinline__ void add_chunk(Stat& st, Best& best, int c, const uns
     const float low = st.m - 150.0f - fabsf(st.m) * 0.015625f;
     const unsigned low2 = Word<T>::N == 2 ? Word<T>::pack(low, low) : 0u;
 #pragma unroll
-    for (int i = 0; i < kWords; i += 3 - N) {
+    for (int i = 0; i < NW; i += 3 - N) {
       unsigned long long v;
       if constexpr (N == 2) {
         const unsigned w = Word<T>::larger(x[i], low2);
@@ -286,8 +289,8 @@ __device__ __forceinline__ void add_chunk(Stat& st, Best& best, int c, const uns
   } else {
     const float base = st.m == kNegInf ? 0.0f : st.m;
 #pragma unroll
-    for (int i = 0; i < kWords; i += 3 - N) {
-      const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % kWords], 0);
+    for (int i = 0; i < NW; i += 3 - N) {
+      const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % NW], 0);
       const float y0 = max_nan((a - base) * kLog2e, -200.0f), y1 = max_nan((b - base) * kLog2e, -200.0f);
       const unsigned long long e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
       s2 = add_f32x2(s2, e);
@@ -301,18 +304,18 @@ __device__ __forceinline__ void add_chunk(Stat& st, Best& best, int c, const uns
 
 // Shared memory of a row's end.
 struct RowEnd {
-  unsigned best[4 * kRowWarps];   // the order keys of every warp's four best threads
+  unsigned best[64];   // the order keys of every warp's best threads
   float s[kRowWarps], t[kRowWarps];
   unsigned floor;
   int count[kRowWarps];
   unsigned long long list[kRowWarps * DET_MAX_TOP_K];
 };
 
-// The top_k largest of the row.  end.best holds the order keys of the four
+// The top_k largest of the row.  end.best holds the order keys of the eight
 // best threads of every warp: the k-th largest of those 64 is a lower bound of
 // the row's k-th largest element, so only threads whose best reaches it are
-// looked through again, each by half of its warp, whose lanes keep the best in
-// order: the 16 words of the chunk with its best, and all its words only if
+// looked through again, each by its whole warp, whose lanes keep the best in
+// order: the 32 words of the chunk with its best, and all its words only if
 // another chunk has such an element too.
 template <typename T>
 __device__ void top_alternatives(const T* row, int vocab, float largest, const Best& best, int k, float m, float log_s,
@@ -322,8 +325,8 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
   {
     const unsigned a = end.best[lane], b = end.best[lane + 32];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = 4 * warp + j;
+    for (int j = 0; j < kBest; ++j) {
+      const int at = kBest * warp + j;
       const unsigned mine = end.best[at];
       const int above = __popc(__ballot_sync(0xffffffffu, a > mine || (a == mine && lane < at))) +
                         __popc(__ballot_sync(0xffffffffu, b > mine || (b == mine && lane + 32 < at)));
@@ -340,35 +343,30 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
   unsigned all = __ballot_sync(0xffffffffu, order_key(largest) >= floor_key && order_key(best.others) >= floor_key);
   one &= ~all;
   int all_chunk = 0;
-  constexpr int kAhead = 4;      // loads in flight, each of two threads' chunks
+  static_assert(kWords == 32, "a lane per word");
+  constexpr int kAhead = 4;      // loads in flight
   while (one | all) {
     unsigned word[kAhead];
     int at[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      int owner[2], chunk[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        owner[half] = 0;
-        chunk[half] = chunks;   // none
-        if (one) {
-          owner[half] = __ffs(one) - 1;
-          one &= one - 1;
-          chunk[half] = __shfl_sync(0xffffffffu, best.chunk, owner[half]);
-        } else if (all) {
-          owner[half] = __ffs(all) - 1;
-          chunk[half] = all_chunk;
-          if (++all_chunk == chunks) {
-            all_chunk = 0;
-            all &= all - 1;
-          }
+      int owner = 0, c = chunks;   // none
+      if (one) {
+        owner = __ffs(one) - 1;
+        one &= one - 1;
+        c = __shfl_sync(0xffffffffu, best.chunk, owner);
+      } else if (all) {
+        owner = __ffs(all) - 1;
+        c = all_chunk;
+        if (++all_chunk == chunks) {
+          all_chunk = 0;
+          all &= all - 1;
         }
       }
-      const int c = lane < 16 ? chunk[0] : chunk[1];
       at[a] = words;
       word[a] = 0u;
       if (c < chunks) {
-        at[a] = c * kChunkWords + (lane & 15) * kRowThreads + warp * 32 + (lane < 16 ? owner[0] : owner[1]);
+        at[a] = c * kChunkWords + lane * kRowThreads + warp * 32 + owner;
         if (at[a] < words) word[a] = load_word(row, at[a], vocab, aligned);
       }
     }
@@ -400,8 +398,8 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
   total = __reduce_add_sync(0xffffffffu, total);
   if (lane < count) end.list[before + lane] = mine;
   __syncthreads();
-  if (threadIdx.x < total) {
-    const unsigned long long c = end.list[threadIdx.x];
+  for (int at = threadIdx.x; at < total; at += kRowThreads) {   // at most 8 x 32
+    const unsigned long long c = end.list[at];
     int rank = 0;
     for (int j = 0; j < total; ++j) rank += end.list[j] > c ? 1 : 0;
     if (rank < k) {
@@ -426,14 +424,14 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   }
   const float largest = st.m;
   unsigned left = order_key(largest);
-  for (int j = 0; j < (top_k > 0 ? 4 : 1); ++j) {
+  for (int j = 0; j < (top_k > 0 ? kBest : 1); ++j) {
     const unsigned top = __reduce_max_sync(0xffffffffu, left);
-    if (lane == 0) end.best[4 * warp + j] = top;
+    if (lane == 0) end.best[kBest * warp + j] = top;
     const int owner = __ffs(__ballot_sync(0xffffffffu, left == top)) - 1;
     if (lane == owner) left = 0u;
   }
   __syncthreads();
-  const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[4 * (lane & (kRowWarps - 1))]));
+  const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[kBest * (lane & (kRowWarps - 1))]));
   raise_to<T>(st, m);
   float s = warp_pt(st.s), t = warp_pt(st.t);
   if (lane == 0) {
@@ -515,20 +513,44 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
     const unsigned head = head_ahead, tail = tail_ahead;
     load_edges(r + gridDim.x);
     Stat st = {kNegInf, 0.0f, 0.0f};
-    Best best = {0, kNegInf};
+    Best best = {-1, kNegInf};
     for (int c = 0; c < chunks; ++c) {
       // the warps take turns at waiting for the stage that all have read and filling it
       fetch_next(threadIdx.x == turn * 32);
       turn = (turn + 1) & (kRowWarps - 1);
       if (!gave_up) gave_up = !mbar_wait(&stream.full[stage], round & 1, kWaitNs);
-      unsigned x[kWords];
-      const bool odd = map.odd(), ragged = map.ragged(c);
-      if (odd) read_words<true>(stream.stage[stage], map.off, x);
-      else read_words<false>(stream.stage[stage], map.off, x);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&stream.empty[stage]);
-      if (ragged) set_edges(map, c, head, tail, x);
-      add_chunk<T>(st, best, c, x);
+      const unsigned char* words = stream.stage[stage];
+      auto release = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stream.empty[stage]);
+      };
+      if ((c + 1LL) * kChunkWords <= map.words) {
+        unsigned x[kWords];
+        if (map.odd()) {
+          read_words<true>(words, map.off, 0, x);
+          release();
+          if (map.ragged(c)) set_edges(map, c * kChunkWords + threadIdx.x, head, tail, x);
+          add_words<T>(st, best, c, x);
+        } else if (map.ragged(c)) {
+          read_words<false>(words, map.off, 0, x);
+          release();
+          set_edges(map, c * kChunkWords + threadIdx.x, head, tail, x);
+          add_words<T>(st, best, c, x);
+        } else {
+          read_words<false>(words, map.off, 0, x);
+          release();
+          add_words<T>(st, best, c, x);
+        }
+      } else {
+        for (int i0 = 0; i0 < kWords && c * kChunkWords + i0 * kRowThreads < map.words; i0 += kPartWords) {
+          unsigned x[kPartWords];
+          if (map.odd()) read_words<true>(words, map.off, i0, x);
+          else read_words<false>(words, map.off, i0, x);
+          set_edges(map, c * kChunkWords + i0 * kRowThreads + threadIdx.x, head, tail, x);
+          add_words<T>(st, best, c, x);
+        }
+        release();
+      }
       if (++stage == kStages) {
         stage = 0;
         ++round;
