@@ -212,21 +212,24 @@ struct RowMap {
   }
 };
 
-// NW of the thread's words, from word i0 up, of a chunk that has arrived.
-template <bool ODD, int NW>
-__device__ __forceinline__ void read_words(const unsigned char* stage, int off, int i0, unsigned (&x)[NW]) {
+// NW of the thread's words, from word i0 up, of a chunk that has arrived;
+// odd_shift is 16 in a row that starts at an odd element, else 0 (SHIFT: may be 16).
+template <bool SHIFT, int NW>
+__device__ __forceinline__ void read_words(const unsigned char* stage, int off, int i0, unsigned odd_shift,
+                                           unsigned (&x)[NW]) {
   const unsigned* p = reinterpret_cast<const unsigned*>(stage + (off & ~3)) + i0 * kRowThreads + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    x[i] = p[i * kRowThreads];
-    if (ODD) x[i] = __funnelshift_r(x[i], p[i * kRowThreads + 1], 16);
+  for (int i = 0; i < NW; ++i) x[i] = p[i * kRowThreads];
+  if (SHIFT) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) x[i] = __funnelshift_r(x[i], p[i * kRowThreads + 1], odd_shift);
   }
 }
 // Edges from where their threads hold them, and masked logits past the end;
 // w0 is the thread's first of these words.
 template <typename T, int NW>
-__device__ __forceinline__ void set_edges(const RowMap<T>& map, int w0, unsigned head, unsigned tail, unsigned (&x)[NW]) {
-  const int tail_word = map.tail_word();
+__device__ __forceinline__ void set_edges(const RowMap<T>& map, int w0, unsigned head, unsigned tail, int tail_word,
+                                          unsigned (&x)[NW]) {
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
     const int w = w0 + i * kRowThreads;
@@ -242,10 +245,9 @@ struct Best {
   float others;
 };
 
-// NW words of chunk c added to the thread's statistics.
+// The largest of NW words.
 template <typename T, int NW>
-__device__ __forceinline__ void add_words(Stat& st, Best& best, int c, const unsigned (&x)[NW]) {
-  constexpr int N = Word<T>::N;
+__device__ __forceinline__ float largest_of(const unsigned (&x)[NW]) {
   unsigned mx[NW / 2];
 #pragma unroll
   for (int i = 0; i < NW / 2; ++i) mx[i] = Word<T>::larger(x[i], x[i + NW / 2]);
@@ -253,8 +255,13 @@ __device__ __forceinline__ void add_words(Stat& st, Best& best, int c, const uns
   for (int s = NW / 4; s > 0; s >>= 1)
 #pragma unroll
     for (int i = 0; i < s; ++i) mx[i] = Word<T>::larger(mx[i], mx[i + s]);
-  float m = Word<T>::get(mx[0], 0);
-  if (N == 2) m = max_nan(m, Word<T>::get(mx[0], 1));
+  const float m = Word<T>::get(mx[0], 0);
+  return Word<T>::N == 2 ? max_nan(m, Word<T>::get(mx[0], 1)) : m;
+}
+
+// The statistics brought to the largest of words of chunk c, before they are added.
+template <typename T>
+__device__ __forceinline__ void raise_words(Stat& st, Best& best, int c, float m) {
   if (!(m <= st.m)) {   // a new maximum, or NaN
     if (c != best.chunk) best.others = st.m;   // else another part of the same chunk
     best.chunk = c;
@@ -262,44 +269,50 @@ __device__ __forceinline__ void add_words(Stat& st, Best& best, int c, const uns
   } else if (c != best.chunk) {
     best.others = max_nan(best.others, m);
   }
+}
+
+// NW words added; near_max(st.m).
+template <typename T, int NW>
+__device__ __forceinline__ void add_words(Stat& st, const unsigned (&x)[NW]) {
+  constexpr int N = Word<T>::N;
   unsigned long long s2 = 0, t2 = 0;   // of elements 0 and 1 of the words (f32: even and odd words)
-  if (near_max<T>(st.m)) {
-    const float ref = -(st.m * kLog2e);
-    const unsigned long long c = pack_f32x2(kLog2e, kLog2e), minus = pack_f32x2(ref, ref);
-    // 2^y is 0 from y = -127 on: a bound of -150 for x - m changes no term, and
-    // without it 0 * inf for a masked logit.  16-bit logits are bounded in
-    // pairs, by a value below m - 150 in every rounding.
-    const float low = st.m - 150.0f - fabsf(st.m) * 0.015625f;
-    const unsigned low2 = Word<T>::N == 2 ? Word<T>::pack(low, low) : 0u;
+  const float ref = -(st.m * kLog2e);
+  const unsigned long long c = pack_f32x2(kLog2e, kLog2e), minus = pack_f32x2(ref, ref);
+  // 2^y is 0 from y = -127 on: a bound of -150 for x - m changes no term, and
+  // without it 0 * inf for a masked logit.  16-bit logits are bounded in
+  // pairs, by a value below m - 150 in every rounding.
+  const float low = st.m - 150.0f - fabsf(st.m) * 0.015625f;
+  const unsigned low2 = N == 2 ? Word<T>::pack(low, low) : 0u;
 #pragma unroll
-    for (int i = 0; i < NW; i += 3 - N) {
-      unsigned long long v;
-      if constexpr (N == 2) {
-        const unsigned w = Word<T>::larger(x[i], low2);
-        v = pack_f32x2(Word<T>::get(w, 0), Word<T>::get(w, 1));
-      } else {
-        v = pack_f32x2(max_nan(__uint_as_float(x[i]), low), max_nan(__uint_as_float(x[i + 1]), low));
-      }
-      v = fma_f32x2(v, c, minus);
-      const float2 y = unpack_f32x2(v);
-      const unsigned long long e = pack_f32x2(exp2_approx(y.x), exp2_approx(y.y));
-      s2 = add_f32x2(s2, e);
-      t2 = fma_f32x2(e, v, t2);
+  for (int i = 0; i < NW; i += 3 - N) {
+    unsigned long long v;
+    if constexpr (N == 2) {
+      const unsigned w = Word<T>::larger(x[i], low2);
+      v = pack_f32x2(Word<T>::get(w, 0), Word<T>::get(w, 1));
+    } else {
+      v = pack_f32x2(max_nan(__uint_as_float(x[i]), low), max_nan(__uint_as_float(x[i + 1]), low));
     }
-  } else {
-    const float base = st.m == kNegInf ? 0.0f : st.m;
-#pragma unroll
-    for (int i = 0; i < NW; i += 3 - N) {
-      const float a = Word<T>::get(x[i], 0), b = N == 2 ? Word<T>::get(x[i], 1) : Word<T>::get(x[(i + 1) % NW], 0);
-      const float y0 = max_nan((a - base) * kLog2e, -200.0f), y1 = max_nan((b - base) * kLog2e, -200.0f);
-      const unsigned long long e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
-      s2 = add_f32x2(s2, e);
-      t2 = fma_f32x2(e, pack_f32x2(y0, y1), t2);
-    }
+    v = fma_f32x2(v, c, minus);
+    const float2 y = unpack_f32x2(v);
+    const unsigned long long e = pack_f32x2(exp2_approx(y.x), exp2_approx(y.y));
+    s2 = add_f32x2(s2, e);
+    t2 = fma_f32x2(e, v, t2);
   }
   const float2 s = unpack_f32x2(s2), t = unpack_f32x2(t2);
   st.s += s.x + s.y;
   st.t += t.x + t.y;
+}
+
+// The same for a maximum far from 0 (or -inf, inf, NaN), word by word.
+template <typename T>
+__device__ __forceinline__ void add_far_word(Stat& st, unsigned x) {
+  const float base = st.m == kNegInf ? 0.0f : st.m;
+#pragma unroll
+  for (int j = 0; j < Word<T>::N; ++j) {
+    const float y = max_nan((Word<T>::get(x, j) - base) * kLog2e, -200.0f), e = exp2_approx(y);
+    st.s += e;
+    st.t = fmaf(e, y, st.t);
+  }
 }
 
 // Shared memory of a row's end.
@@ -514,41 +527,55 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
     load_edges(r + gridDim.x);
     Stat st = {kNegInf, 0.0f, 0.0f};
     Best best = {-1, kNegInf};
+    const unsigned odd_shift = map.odd() ? 16u : 0u;
+    const int tail_word = map.tail_word();
     for (int c = 0; c < chunks; ++c) {
       // the warps take turns at waiting for the stage that all have read and filling it
       fetch_next(threadIdx.x == turn * 32);
       turn = (turn + 1) & (kRowWarps - 1);
       if (!gave_up) gave_up = !mbar_wait(&stream.full[stage], round & 1, kWaitNs);
       const unsigned char* words = stream.stage[stage];
+      // read words (all of the thread's, or kPartWords at a time in the row's
+      // last chunk if it is not whole), then bring the maximum up, then add
       auto release = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(&stream.empty[stage]);
       };
-      if ((c + 1LL) * kChunkWords <= map.words) {
-        unsigned x[kWords];
-        if (map.odd()) {
-          read_words<true>(words, map.off, 0, x);
-          release();
-          if (map.ragged(c)) set_edges(map, c * kChunkWords + threadIdx.x, head, tail, x);
-          add_words<T>(st, best, c, x);
-        } else if (map.ragged(c)) {
-          read_words<false>(words, map.off, 0, x);
-          release();
-          set_edges(map, c * kChunkWords + threadIdx.x, head, tail, x);
-          add_words<T>(st, best, c, x);
+      auto step = [&](auto shift, auto count, int i0, bool ragged) {
+        constexpr int NW = decltype(count)::value;
+        constexpr bool kAll = NW == kWords;   // the chunk's only step
+        const int w0 = c * kChunkWords + i0 * kRowThreads + threadIdx.x;
+        unsigned x[NW];
+        read_words<decltype(shift)::value>(words, map.off, i0, odd_shift, x);
+        if (ragged) set_edges(map, w0, head, tail, tail_word, x);
+        raise_words<T>(st, best, c, largest_of<T>(x));
+        const bool near = near_max<T>(st.m), all_near = __all_sync(0xffffffffu, near);
+        if (kAll && all_near) release();
+        if (near) {
+          add_words<T>(st, x);
         } else {
-          read_words<false>(words, map.off, 0, x);
-          release();
-          add_words<T>(st, best, c, x);
+#pragma unroll 1
+          for (int i = 0; i < NW; ++i) {
+            unsigned y[1];
+            read_words<true>(words, map.off, i0 + i, odd_shift, y);
+            set_edges(map, w0 + i * kRowThreads, head, tail, tail_word, y);
+            add_far_word<T>(st, y[0]);
+          }
+        }
+        if (kAll && !all_near) release();
+      };
+      using std::integral_constant;
+      if ((c + 1LL) * kChunkWords <= map.words) {
+        const bool ragged = map.ragged(c);
+        if (odd_shift == 0 && !ragged) {
+          step(integral_constant<bool, false>(), integral_constant<int, kWords>(), 0, false);
+        } else {
+          step(integral_constant<bool, true>(), integral_constant<int, kWords>(), 0, ragged);
         }
       } else {
-        for (int i0 = 0; i0 < kWords && c * kChunkWords + i0 * kRowThreads < map.words; i0 += kPartWords) {
-          unsigned x[kPartWords];
-          if (map.odd()) read_words<true>(words, map.off, i0, x);
-          else read_words<false>(words, map.off, i0, x);
-          set_edges(map, c * kChunkWords + i0 * kRowThreads + threadIdx.x, head, tail, x);
-          add_words<T>(st, best, c, x);
-        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < kWords && c * kChunkWords + i0 * kRowThreads < map.words; i0 += kPartWords)
+          step(integral_constant<bool, true>(), integral_constant<int, kPartWords>(), i0, true);
         release();
       }
       if (++stage == kStages) {
