@@ -3,8 +3,8 @@
 //
 // A sequence is cut into chunks whose size depends on its own length alone;
 // a CTA takes the query heads that share one key-value head over one chunk,
-// and a second kernel joins the chunks.  Inside a chunk warp w of 4 takes the
-// 16-token tiles w, w + 4, ... with a running maximum (softmax statistics
+// and a second kernel joins the chunks.  Inside a chunk warp w takes every
+// fourth (of 256 dims every third) tile of 16 tokens with a running maximum (softmax statistics
 // and the output are held in 32 bits), so the order of every addition is
 // fixed by token index and a sequence's bits do not depend on its batch.
 //
@@ -22,13 +22,14 @@
 namespace det {
 namespace {
 
-constexpr int kTile = 16;        // tokens of a tile
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kMaxChunk = 1024;  // most tokens of a chunk
 
-// Tokens of a chunk of a sequence of n tokens.
-__host__ __device__ inline int chunk_tokens(long long n) { return n <= 8192 ? 256 : n <= 32768 ? 512 : kMaxChunk; }
+// Tokens of a chunk of a sequence of n tokens: short chunks let a short
+// sequence use more SMs, long ones spend less on their start and on the join
+// (32 sequences of 8,192 tokens, 8 kv heads of 128: 183 us at 256, 179 at 512,
+// 175 at 1,024; one of 1,000 tokens: 14, 18 and 24 us).
+constexpr int kShort = 1024, kMedium = 16384;
+__host__ __device__ inline int chunk_tokens(int n) { return n <= kShort ? 256 : n <= kMedium ? 512 : kMaxChunk; }
 __host__ __device__ inline int chunk_count(int n) {
   const int c = chunk_tokens(n);
   return n <= 0 ? 1 : (n - 1) / c + 1;
@@ -36,15 +37,28 @@ __host__ __device__ inline int chunk_count(int n) {
 // Most chunks of a sequence of at most n tokens.
 inline int most_chunks(int n) {
   int most = chunk_count(n);
-  if (n > 8192) most = std::max(most, chunk_count(8192));
-  if (n > 32768) most = std::max(most, chunk_count(32768));
+  if (n > kShort) most = std::max(most, chunk_count(kShort));
+  if (n > kMedium) most = std::max(most, chunk_count(kMedium));
   return most;
 }
 
-template <int D> __host__ __device__ constexpr int attn_stages() { return D == 64 ? 6 : 3; }
-template <int D> __host__ __device__ constexpr size_t attn_smem() {
-  return (size_t)kAttnWarps * attn_stages<D>() * kTile * D * 2 * 2;
-}
+// A warp's tiles of 16 tokens, two of them in shared memory: the one it works
+// on and the next.  What hides the latency of loads and of a tile's chain of
+// products and exponentials is the number of warps on an SM, so tiles are as
+// short as the matrix instructions allow (measured, 32 sequences of 8,192
+// tokens, 8 kv heads: of 64 dims 101 us, three tiles 120, tiles of 32 tokens
+// 139; of 128 dims 182 us, three tiles 209).  Rows lie 16 bytes apart modulo
+// 128, so that eight rows of a matrix load hit 32 banks.
+template <int D> struct Tile {
+  static constexpr int kWarps = D == 256 ? 3 : 4;   // of a CTA: 2 CTAs of 3 warps, 3 or 6 of 4 fit an SM
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kTokens = 16;
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kPitch = kRowBytes + 16;
+  static constexpr int kBytes = kTokens * kPitch;   // of the keys, and of the values
+  static constexpr int kStages = 2;
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * 2 * kBytes;
+};
 
 struct AttnArgs {
   const void *q, *k, *v;
@@ -64,8 +78,8 @@ struct AttnArgs {
   float* lse;
 };
 
-__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async_16(unsigned dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
@@ -122,17 +136,20 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 }
 
 // NT tiles of 8 heads per CTA.  Grid: (chunks, kv heads x head tiles, batch).
+// A warp fetches its tiles itself, kStages - 1 ahead, the keys and the values
+// of a tile as two groups of asynchronous copies.  Where a page holds whole
+// blocks of 16 tokens the block's place is looked up once for the warp.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int S = attn_stages<D>();
-  constexpr int C = D / 8;              // 16-byte pieces of a row
-  constexpr int kRowBytes = D * 2;
-  constexpr int kTileBytes = kTile * kRowBytes;
+__global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
+  using L = Tile<D>;
+  constexpr int S = L::kStages, W = L::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int sh_page[kMaxChunk + 1];
-  __shared__ unsigned sh_mask[kAttnWarps][S];
-  __shared__ float sh_m[kAttnWarps][8 * NT], sh_l[kAttnWarps][8 * NT];
+  __shared__ long long sh_place[kMaxChunk / 16][2];   // of a block of 16 tokens: its keys and values; -1: token by token
+  __shared__ unsigned sh_mask[W][S];   // of a tile's tokens: those not skipped
+  __shared__ float sh_m[W][8 * NT], sh_l[W][8 * NT];
 
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x, b = blockIdx.z;
   const int g = blockIdx.y / a.head_tiles, h0 = (blockIdx.y % a.head_tiles) * 8 * NT;   // first head in the group
   const int n = min(max(a.lengths[b], 0), a.limit);
@@ -143,11 +160,17 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
   const int p0 = t0 / a.page_size;
   const int pages = t1 > t0 ? (t1 - 1) / a.page_size - p0 + 1 : 0;
   const int32_t* table = a.table + b * a.table_stride + p0;
-  for (int i = threadIdx.x; i < pages; i += kAttnThreads) {
+  for (int i = threadIdx.x; i < pages; i += L::kThreads) {
     const int p = table[i];
     sh_page[i] = p >= 0 && p < a.num_pages ? p : -1;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < (t1 - t0 + 15) / 16; i += L::kThreads) {
+    const int j = t0 + 16 * i, pj = j / a.page_size, slot = j - pj * a.page_size;
+    const int p = table[pj - p0];
+    const bool whole = a.page_size % 16 == 0 && j + 16 <= t1 && p >= 0 && p < a.num_pages;   // t0 is a multiple of 16
+    sh_place[i][0] = whole ? p * a.k_sp + slot * a.k_st : -1;
+    sh_place[i][1] = whole ? p * a.v_sp + slot * a.v_st : -1;
+  }
 
   // the queries as B operands: column = head (lane / 4), rows = dims
   unsigned qf[D / 16][NT][2];
@@ -168,45 +191,79 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
         qf[ks][nt][j] = w;
       }
   }
+  // with a bias: the distance from which on the last bucket holds, and its values
+  int far = 0;
+  float far_bias[NT][2];
+  if (a.bias) {
+    far = a.num_bounds > 0 ? __ldg(a.bounds + a.num_bounds - 1) : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
+        far_bias[nt][j] =
+            h < a.group ? kLog2e * load_as_f32(a.bias, (long long)a.num_bounds * a.heads + g * a.group + h, a.bias_dtype)
+                        : 0.0f;
+      }
+  }
   __syncthreads();
 
   const T* kbase = static_cast<const T*>(a.k) + g * a.k_sh;
   const T* vbase = static_cast<const T*>(a.v) + g * a.v_sh;
-  unsigned char* ring = smem + (size_t)warp * S * 2 * kTileBytes;
-  const int tiles = (t1 - t0 + kTile - 1) / kTile;
-  const int mine = (tiles - warp + kAttnWarps - 1) / kAttnWarps;   // tiles of this warp (warp <= tiles or <= 0)
+  unsigned char* ring = smem + (size_t)warp * S * 2 * L::kBytes;
+  const int tiles = (t1 - t0 + L::kTokens - 1) / L::kTokens;
+  const int mine = (tiles - warp + W - 1) / W;   // tiles of this warp
 
-  auto load = [&](int it) {
-    if (it < mine) {
-      const int stage = it % S;
-      const int j = t0 + (it * kAttnWarps + warp) * kTile + (lane & 15);
-      long long ko = 0, vo = 0;
-      int page = -1;
-      if (j < t1) {
-        const int pj = j / a.page_size, slot = j - pj * a.page_size;
-        page = sh_page[pj - p0];
-        ko = page * a.k_sp + slot * a.k_st;
-        vo = page * a.v_sp + slot * a.v_st;
-      }
-      const unsigned mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-      if (lane == 0) sh_mask[warp][stage] = mask;
-      unsigned char* ks = ring + (size_t)stage * 2 * kTileBytes;
-      unsigned char* vs = ks + kTileBytes;
+  // a lane copies 16 bytes of every (32 / C)-th row
+  constexpr int C = D / 8, kRows = 32 / C;
+  const int row0 = lane / C, col = lane % C;
+  const T* klane = kbase + row0 * a.k_st + col * 8;
+  const T* vlane = vbase + row0 * a.v_st + col * 8;
+  const unsigned dst_lane = smem_u32(ring) + row0 * L::kPitch + col * 16;
+  auto copy_block = [&](unsigned dst, const T* src, long long stride) {
 #pragma unroll
-      for (int i = 0; i < kTile * C / 32; ++i) {
-        const int at = i * 32 + lane, row = at / C, c = at % C;
-        const long long kr = __shfl_sync(0xffffffffu, ko, row), vr = __shfl_sync(0xffffffffu, vo, row);
-        const int dst = row * kRowBytes + ((c ^ (row & 7)) << 4);
-        if ((mask >> row) & 1) {
-          cp_async_16(ks + dst, kbase + kr + c * 8);
-          cp_async_16(vs + dst, vbase + vr + c * 8);
-        } else {   // nothing is read for a skipped token: 0, so that 0 * value is 0
-          *reinterpret_cast<uint4*>(ks + dst) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vs + dst) = make_uint4(0, 0, 0, 0);
-        }
-      }
+    for (int i = 0; i < 16 / kRows; ++i) cp_async_16(dst + i * kRows * L::kPitch, src + i * (kRows * stride));
+  };
+  // the rows of a block one by one, `from` the place of the lane's token's row
+  auto copy_rows = [&](unsigned dst, const T* base, long long from, unsigned mask) {
+#pragma unroll
+    for (int i = 0; i < 16 / kRows; ++i) {
+      const int row = i * kRows + row0;
+      const long long at = __shfl_sync(0xffffffffu, from, row);
+      // nothing is read for a skipped token: 0, so that 0 * value is 0
+      if ((mask >> row) & 1) cp_async_16(dst + i * kRows * L::kPitch, base + at + col * 8);
+      else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * kRows * L::kPitch), "r"(0u) : "memory");
     }
-    cp_async_commit();
+  };
+  auto fetch = [&](int it) {
+    if (it < mine) {
+      const int stage = it % S, tile = it * W + warp;
+      const unsigned kd = dst_lane + stage * (2 * L::kBytes), vd = kd + L::kBytes;
+      const long long ko = sh_place[tile][0];
+      if (ko >= 0) {
+        if (lane == 0) sh_mask[warp][stage] = 0xffffu;
+        copy_block(kd, klane + ko, a.k_st);
+        cp_async_commit();
+        copy_block(vd, vlane + sh_place[tile][1], a.v_st);
+      } else {
+        const int j = t0 + tile * 16 + (lane & 15);
+        int page = -1, slot = 0;
+        if (j < t1) {
+          const int pj = j / a.page_size;
+          slot = j - pj * a.page_size;
+          page = sh_page[pj - p0];
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+        if (lane == 0) sh_mask[warp][stage] = mask;
+        copy_rows(kd, kbase, page * a.k_sp + slot * a.k_st, mask);
+        cp_async_commit();
+        copy_rows(vd, vbase, page * a.v_sp + slot * a.v_st, mask);
+      }
+      cp_async_commit();
+    } else {
+      cp_async_commit();
+      cp_async_commit();
+    }
   };
 
   float o[D / 16][NT][4];
@@ -226,35 +283,57 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
     }
 
 #pragma unroll
-  for (int it = 0; it < S - 1; ++it) load(it);
+  for (int it = 0; it < S - 1; ++it) fetch(it);
   for (int it = 0; it < mine; ++it) {
-    load(it + S - 1);
-    cp_async_wait<S - 1>();
-    __syncwarp();
+    fetch(it + S - 1);
     const int stage = it % S;
-    const unsigned ks = smem_u32(ring + (size_t)stage * 2 * kTileBytes), vs = ks + kTileBytes;
-    float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
+    const unsigned ks = smem_u32(ring + (size_t)stage * 2 * L::kBytes), vs = ks + L::kBytes;
+    cp_async_wait<2 * S - 1>();   // this tile's keys
+    __syncwarp();
+    float s[NT][4] = {};
     {
-      const int row = lane & 15;
+      const unsigned row = ks + (lane & 15) * L::kPitch + ((lane >> 4) << 4);
+      // two chains, of the even and the odd sixteens of the dims
+      float odd[NT][4] = {};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         unsigned af[4];
-        ldmatrix_x4(af, ks + row * kRowBytes + (((2 * k + (lane >> 4)) ^ (row & 7)) << 4));
+        ldmatrix_x4(af, row + 32 * k);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816<T>(s[nt], af, qf[k][nt][0], qf[k][nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816<T>(k & 1 ? odd[nt] : s[nt], af, qf[k][nt][0], qf[k][nt][1]);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] += odd[nt][j];
     }
     // scores in units of log 2; masked tokens to -inf
     const unsigned mask = sh_mask[warp][stage] >> (lane >> 2);
-    const int j0 = t0 + (it * kAttnWarps + warp) * kTile + (lane >> 2);
-    int bucket0 = 0, bucket1 = 0;
-    if (a.bias) {
-      bucket0 = bounds_at_most(a.bounds, a.num_bounds, n - 1 - j0);
-      bucket1 = bounds_at_most(a.bounds, a.num_bounds, n - 9 - j0);
+    const int first = t0 + (it * W + warp) * L::kTokens;
+    if (a.bias && n - (first + L::kTokens) >= far) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(s[nt][j], a.scale_log2, far_bias[nt][j & 1]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const void* row = nullptr;
+        if (a.bias) {
+          const int distance = n - 1 - (first + r * 8 + (lane >> 2));
+          row = static_cast<const char*>(a.bias) + (long long)bounds_at_most(a.bounds, a.num_bounds, distance) *
+                                                       a.heads * (a.bias_dtype == DET_F32 ? 4 : 2);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
+            float x = s[nt][2 * r + j] * a.scale_log2;
+            if (a.bias && h < a.group) x = fmaf(load_as_f32(row, g * a.group + h, a.bias_dtype), kLog2e, x);
+            s[nt][2 * r + j] = x;
+          }
+      }
     }
     bool raise = false;
     float fresh[NT][2];
@@ -262,15 +341,8 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
-        float x0 = s[nt][j] * a.scale_log2, x1 = s[nt][2 + j] * a.scale_log2;
-        if (a.bias && h < a.group) {
-          const long long col = g * a.group + h;
-          x0 = fmaf(load_as_f32(a.bias, (long long)bucket0 * a.heads + col, a.bias_dtype), kLog2e, x0);
-          x1 = fmaf(load_as_f32(a.bias, (long long)bucket1 * a.heads + col, a.bias_dtype), kLog2e, x1);
-        }
-        s[nt][j] = (mask & 1) ? x0 : kNegInf;
-        s[nt][2 + j] = (mask & 256) ? x1 : kNegInf;
+        if (!(mask & 1)) s[nt][j] = kNegInf;
+        if (!(mask & 256)) s[nt][2 + j] = kNegInf;
         float mx = fmaxf(s[nt][j], s[nt][2 + j]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -299,27 +371,30 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
     unsigned ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float(&p)[4] = s[nt];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float base = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
-        s[nt][j] = exp2_approx(s[nt][j] - base);
-        s[nt][2 + j] = exp2_approx(s[nt][2 + j] - base);
-        l[nt][j] += s[nt][j] + s[nt][2 + j];
+        p[j] = exp2_approx(p[j] - base);
+        p[2 + j] = exp2_approx(p[2 + j] - base);
+        l[nt][j] += p[j] + p[2 + j];
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const unsigned hi = pack2<T>(s[nt][2 * half], s[nt][2 * half + 1]);
+        const unsigned hi = pack2<T>(p[2 * half], p[2 * half + 1]);
         const float2 r = unpack2<T>(hi);
         ph[nt][half] = movmatrix_trans(hi);
-        pl[nt][half] = movmatrix_trans(pack2<T>(s[nt][2 * half] - r.x, s[nt][2 * half + 1] - r.y));
+        pl[nt][half] = movmatrix_trans(pack2<T>(p[2 * half] - r.x, p[2 * half + 1] - r.y));
       }
     }
+    cp_async_wait<2 * S - 2>();   // and its values
+    __syncwarp();
     {
-      const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
+      const unsigned row = vs + ((lane & 7) + ((lane >> 4) & 1) * 8) * L::kPitch + (((lane >> 3) & 1) << 4);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         unsigned af[4];
-        ldmatrix_x4_trans(af, vs + row * kRowBytes + (((2 * i + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+        ldmatrix_x4_trans(af, row + 32 * i);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816<T>(o[i][nt], af, ph[nt][0], ph[nt][1]);
@@ -346,14 +421,14 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
   __syncthreads();
   constexpr int kPitch = D + 4;   // floats of a row of the joined outputs: the writes below hit 32 banks
   float* sh_o = reinterpret_cast<float*>(smem);
-  static_assert((size_t)kAttnWarps * 8 * NT * kPitch * 4 <= attn_smem<D>(), "the outputs fit the ring");
+  static_assert((size_t)W * 8 * NT * kPitch * 4 <= L::kSmem, "the outputs fit the ring");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = nt * 8 + 2 * (lane & 3) + j;
       float top = kNegInf;
-      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh_m[w][col]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
       const float f = m[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - top);
       float* dst = sh_o + (size_t)(warp * 8 * NT + col) * kPitch + (lane >> 2);
 #pragma unroll
@@ -363,12 +438,12 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
       }
     }
   __syncthreads();
-  for (int at = threadIdx.x; at < 8 * NT * D; at += kAttnThreads) {
+  for (int at = threadIdx.x; at < 8 * NT * D; at += L::kThreads) {
     const int col = at / D, d = at % D;
     if (h0 + col >= a.group) break;
     float top = kNegInf, sum = 0.0f, v = 0.0f;
-    for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh_m[w][col]);
-    for (int w = 0; w < kAttnWarps; ++w) {
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
+    for (int w = 0; w < W; ++w) {
       const float mw = sh_m[w][col];
       sum += mw == kNegInf ? sh_l[w][col] : sh_l[w][col] * exp2_approx(mw - top);
       v += sh_o[(size_t)(w * 8 * NT + col) * kPitch + d];
@@ -384,13 +459,14 @@ __global__ void __launch_bounds__(kAttnThreads) attention_chunks_kernel(const __
   }
 }
 
-// The chunks of one head of one sequence joined: warp w of 4 adds the chunks
-// w, w + 4, ..., then the warps are added in order.
+// The chunks of one head of one sequence joined: warp w of 8 adds the chunks
+// w, w + 8, ..., then the warps are added in order.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(kAttnThreads) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int E = D / 32;
-  __shared__ float sh_top[kAttnWarps], sh_sum[kAttnWarps];
-  __shared__ float sh_o[kAttnWarps][D];
+  __shared__ float sh_top[kJoinWarps], sh_sum[kJoinWarps];
+  __shared__ float sh_o[kJoinWarps][D];
   dep_wait();
   const int h = blockIdx.x, b = blockIdx.y;
   const int chunks = chunk_count(min(max(a.lengths[b], 0), a.limit));
@@ -398,34 +474,45 @@ __global__ void __launch_bounds__(kAttnThreads) attention_join_kernel(const __gr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long bh = (long long)b * a.heads + h;
   const float2* ml = a.part_ml + bh * a.max_chunks;
-  const float* part = a.part + bh * a.max_chunks * D;
+  const float* part = a.part + bh * a.max_chunks * D + lane;
   float top = kNegInf;
-  for (int c = threadIdx.x; c < chunks; c += kAttnThreads) top = fmaxf(top, ml[c].x);
+  for (int c = threadIdx.x; c < chunks; c += 32 * kJoinWarps) top = fmaxf(top, ml[c].x);
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) sh_top[warp] = top;
   __syncthreads();
-  for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sh_top[w]);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
   float v[E], sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
-#pragma unroll 4
-  for (int c = warp; c < chunks; c += kAttnWarps) {
-    const float2 x = ml[c];
-    const float f = x.x == kNegInf ? 1.0f : exp2_approx(x.x - top);   // a chunk without a score adds 0
-    sum = fmaf(x.y, f, sum);
+  constexpr int kAhead = 8;   // chunks in flight
+  for (int c0 = warp; c0 < chunks; c0 += kAhead * kJoinWarps) {
+    float2 x[kAhead];
+    float y[kAhead][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(part[(long long)c * D + e * 32 + lane], f, v[e]);
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = c0 + k * kJoinWarps;
+      x[k] = c < chunks ? ml[c] : make_float2(kNegInf, 0.0f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[k][e] = c < chunks ? part[(long long)c * D + e * 32] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const float f = x[k].x == kNegInf ? 1.0f : exp2_approx(x[k].x - top);   // a chunk without a score adds 0
+      sum = fmaf(x[k].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = fmaf(y[k][e], f, v[e]);
+    }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = v[e];
   if (lane == 0) sh_sum[warp] = sum;
   __syncthreads();
   sum = 0.0f;
-  for (int w = 0; w < kAttnWarps; ++w) sum += sh_sum[w];
+  for (int w = 0; w < kJoinWarps; ++w) sum += sh_sum[w];
   const bool none = top == kNegInf && sum == 0.0f;
-  for (int d = threadIdx.x; d < D; d += kAttnThreads) {
+  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
     float r = 0.0f;
-    for (int w = 0; w < kAttnWarps; ++w) r += sh_o[w][d];
+    for (int w = 0; w < kJoinWarps; ++w) r += sh_o[w][d];
     static_cast<T*>(a.out)[bh * D + d] = from_f32<T>(none ? 0.0f : r / sum);
   }
   if (a.lse && threadIdx.x == 0) a.lse[bh] = none ? kNegInf : (top + log2f(sum)) * (1.0f / kLog2e);
@@ -436,16 +523,16 @@ int launch_attention(AttnArgs a, int batch, int kv_heads, cudaStream_t s) {
   a.head_tiles = (a.group + 8 * NT - 1) / (8 * NT);
   if ((long long)kv_heads * a.head_tiles > 65535) return DET_ERR_TOO_LARGE;
   const void* kernel = reinterpret_cast<const void*>(&attention_chunks_kernel<T, D, NT>);
-  if (const cudaError_t e = ensure_dyn_smem(kernel, attn_smem<D>())) return cuda_fail(e, "det_paged_attention");
+  if (const cudaError_t e = ensure_dyn_smem(kernel, Tile<D>::kSmem)) return cuda_fail(e, "det_paged_attention");
   const dim3 grid((unsigned)a.max_chunks, (unsigned)(kv_heads * a.head_tiles), (unsigned)batch);
   launch_begin("det_paged_attention", s);
-  attention_chunks_kernel<T, D, NT><<<grid, kAttnThreads, attn_smem<D>(), s>>>(a);
+  attention_chunks_kernel<T, D, NT><<<grid, Tile<D>::kThreads, Tile<D>::kSmem, s>>>(a);
   launch_end(s);
   if (const int rc = check_launch("det_paged_attention")) return rc;
   if (a.max_chunks == 1) return DET_OK;
   launch_begin("det_paged_attention_join", s);
   const cudaError_t e = launch_dep(attention_join_kernel<T, D>, dim3((unsigned)a.heads, (unsigned)batch),
-                                   dim3(kAttnThreads), 0, s, a);
+                                   dim3(32 * kJoinWarps), 0, s, a);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_paged_attention_join");
 }

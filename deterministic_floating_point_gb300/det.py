@@ -652,11 +652,15 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if page_size < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError("page_size must be positive and heads a multiple of kv_heads")
     _unit_stride(q, "q")
+    strides = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _on(dev, q.dtype, name, t, (pages, page_size, kv_heads, dim), contiguous=False)
-        _unit_stride(t, name)
-        if t.data_ptr() % 16 or any(st % 8 for st in t.stride()[:3]):
+        s_page, s_token, s_head, s_dim = t.stride()
+        if s_dim != 1:
+            raise ValueError(f"{name} must be contiguous along its last dimension")
+        if (t.data_ptr() & 15) or ((s_page | s_token | s_head) & 7):
             raise ValueError(f"{name} must be 16-byte aligned with strides that are multiples of 8 elements")
+        strides.append((s_page, s_token, s_head))
     _on(dev, torch.int32, "block_table", block_table, contiguous=False)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, max_pages]")
@@ -680,11 +684,11 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     else:
         _on(dev, q.dtype, "out", out, (batch, heads, dim))
     lse = _empty((batch, heads), torch.float32, dev, stream)
-    ws = _model_ws(workspace, lib().det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
-    _check(lib().det_paged_attention(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), *k_cache.stride()[:3], _ptr(v_cache), *v_cache.stride()[:3],
-        pages, page_size, _ptr(block_table), block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads,
-        kv_heads, dim, code, dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
+    call = lib()
+    ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
+    _check(call.det_paged_attention(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), *strides[0], _ptr(v_cache), *strides[1], pages, page_size,
+        _ptr(block_table), block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads, kv_heads, dim, code, dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
         _ptr(bias_bounds) if bias_table is not None else None, n_bounds, limit, _ptr(out), _ptr(lse), _ptr(ws),
         ws.numel(), _stream(stream, dev)), "det_paged_attention")
     return PagedAttention(out, lse)
