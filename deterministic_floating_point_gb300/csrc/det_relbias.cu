@@ -67,16 +67,17 @@ bias_direct_kernel(const void* __restrict__ table, int table_dtype, int heads, D
   out[((long long)h * q_len + q) * k_len + j] = from_f32<T>(load_as_f32(table, (long long)k * heads + h, table_dtype));
 }
 
-// Otherwise a CTA writes 128 rows by 128 eights of keys from the strip of
-// diagonals that they cross, kept in shared memory (in 16-bit types as the
-// pairs of diagonals d, d + 1 that make up a word of the output).  A row's
-// eights start where its memory is 16-byte aligned, so every store but those
-// at a row's ends is 16 bytes wide whatever the row length.  Word u of the
-// strip lies at u + u / 8: threads are 8 diagonals apart, which then are 9
-// banks.
-constexpr int kBiasThreads = 128;
-constexpr int kBiasRows = 128;
-constexpr int kStrip = 8 * kBiasThreads + kBiasRows + 16;
+// Otherwise a CTA writes 32 rows by 128 units of 16 bytes (aligned rows in 32
+// bits: 16 by 256) from the strip of diagonals that they cross, kept
+// in shared memory (in 16-bit types as the pairs of diagonals d, d + 1 that make
+// up a word of the output).  A row's
+// units start where its memory is 16-byte aligned, so every store but those
+// at a row's ends is a whole unit, whatever the row length.  Word u of the strip
+// lies at u + u / U, U elements to a unit: threads are U diagonals apart, which
+// then is an odd number of banks.
+template <typename T, bool ALIGNED> struct BiasTile {
+  static constexpr int kThreads = sizeof(T) == 4 && ALIGNED ? 256 : 128, kRows = sizeof(T) == 4 && ALIGNED ? 16 : 32;
+};
 
 template <typename T> struct Out16;
 template <> struct Out16<float> {
@@ -94,84 +95,78 @@ template <> struct Out16<__half> {
 };
 
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kBiasThreads)
+__global__ void __launch_bounds__(BiasTile<T, ALIGNED>::kThreads)
 bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
                   T* __restrict__ out) {
-  constexpr int E = 4 / sizeof(T);        // elements of a word
-  constexpr int kUnit = 16 / sizeof(T);   // elements of a store
-  __shared__ unsigned strip[kStrip + kStrip / 8 + 1];
+  constexpr int E = 4 / sizeof(T);    // elements of a word
+  constexpr int U = 16 / sizeof(T);   // elements of a unit
+  constexpr int kBiasThreads = BiasTile<T, ALIGNED>::kThreads, kBiasRows = BiasTile<T, ALIGNED>::kRows;
+  constexpr int kStrip = U * kBiasThreads + kBiasRows + 2 * U;
+  __shared__ unsigned strip[kStrip + kStrip / U + 1];
   __shared__ float value[kStrip + 1];
   const int h = blockIdx.z, i0 = blockIdx.y * kBiasRows, c0 = blockIdx.x * kBiasThreads;
   const int rows = min(kBiasRows, q_len - i0);
-  // strip[u] holds diagonal u + d0: key - query from 8 (c0 - 1) - (i0 + kBiasRows - 1) up
-  const int d0 = 8 * (c0 - 1) - (i0 + kBiasRows - 1);
+  // strip[u] holds diagonal u + d0: key - query from U (c0 - 1) - (i0 + kBiasRows - 1) up
+  const int d0 = U * (c0 - 1) - (i0 + kBiasRows - 1);
   const int base = d0 + (q_len - 1) + dist.first;   // distance of strip[0]
   for (int u = threadIdx.x; u <= kStrip; u += kBiasThreads)
     value[u] = load_as_f32(table, (long long)dist.bucket(base + u) * heads + h, table_dtype);
   __syncthreads();
-  for (int u = threadIdx.x; u < kStrip; u += kBiasThreads) strip[u + (u >> 3)] = Out16<T>::word(value[u], value[u + 1]);
+  for (int u = threadIdx.x; u < kStrip; u += kBiasThreads) strip[u + u / U] = Out16<T>::word(value[u], value[u + 1]);
   __syncthreads();
   if constexpr (ALIGNED) {
-    // Every row's eights start at the same keys.  Eight rows of a thread's
-    // eight cross 15 diagonals: two eights of the strip, and the next
-    // eight rows need one more.
-    const int j = 8 * (c0 - 1 + (int)threadIdx.x);
-    if (j < 0 || j >= k_len) return;
-    if (j + 8 <= k_len) {
-      unsigned lo[8], hi[8];
-      const unsigned* at = strip + 9 * (threadIdx.x + kBiasRows / 8);
+    // Every row's units start at the same keys.  U rows of a thread's unit
+    // cross 2 U - 1 diagonals: two runs of U words of the strip, of which the
+    // next U rows need one more.
+    const int j = U * (c0 - 1 + (int)threadIdx.x);
+    if (j < 0 || j + U > k_len) return;   // a row holds whole units
+    unsigned lo[U], hi[U];
+    const unsigned* at = strip + (U + 1) * (threadIdx.x + kBiasRows / U);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) hi[x] = at[x];
-      T* p = out + ((long long)h * q_len + i0) * k_len + j;
-      for (int y0 = 0; y0 < rows; y0 += 8) {
-        at -= 9;
+    for (int x = 0; x < U; ++x) hi[x] = at[x];
+    T* p = out + ((long long)h * q_len + i0) * k_len + j;
+    for (int y0 = 0; y0 < rows; y0 += U) {
+      at -= U + 1;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) lo[x] = at[x];
+      for (int x = 0; x < U; ++x) lo[x] = at[x];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          if (y0 + y < rows) {
-            unsigned w[8 / E];
+      for (int y = 0; y < U; ++y) {
+        if (y0 + y < rows) {
+          unsigned w[4];
 #pragma unroll
-            for (int x = 0; x < 8 / E; ++x) {
-              const int k = 7 - y + x * E;
-              w[x] = k < 8 ? lo[k] : hi[k - 8];
-            }
-#pragma unroll
-            for (int x = 0; x < 8 / kUnit; ++x)
-              *reinterpret_cast<uint4*>(p + x * kUnit) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-            p += k_len;
+          for (int x = 0; x < 4; ++x) {
+            const int k = U - 1 - y + x * E;
+            w[x] = k < U ? lo[k] : hi[k - U];
           }
+          *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+          p += k_len;
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) hi[x] = lo[x];
       }
-      return;
+#pragma unroll
+      for (int x = 0; x < U; ++x) hi[x] = lo[x];
     }
-  }
-  for (int y = 0; y < rows; ++y) {
-    const int i = i0 + y;
-    T* row = out + ((long long)h * q_len + i) * k_len;
-    // keys before the row's first 16-byte boundary
-    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
-    const int j = head + 8 * (c0 - 1 + (int)threadIdx.x);
-    if (j >= k_len || j + 8 <= 0) continue;
-    const int u = j - i - d0;
-    unsigned w[8 / E];
+  } else {
+#pragma unroll 4
+    for (int y = 0; y < rows; ++y) {
+      const int i = i0 + y;
+      T* row = out + ((long long)h * q_len + i) * k_len;
+      // keys before the row's first 16-byte boundary
+      const int head = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
+      const int j = head + U * (c0 - 1 + (int)threadIdx.x);
+      if (j >= k_len || j + U <= 0) continue;
+      const int u = j - i - d0;
+      unsigned w[4];
 #pragma unroll
-    for (int x = 0; x < 8 / E; ++x) {
-      const int at = u + x * E;
-      w[x] = strip[at + (at >> 3)];
-    }
-    if (j >= 0 && j + 8 <= k_len) {
+      for (int x = 0; x < 4; ++x) w[x] = strip[u + x * E + (u + x * E) / U];
+      if (j >= 0 && j + U <= k_len) {
+        *reinterpret_cast<uint4*>(row + j) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
 #pragma unroll
-      for (int x = 0; x < 8 / kUnit; ++x)
-        *reinterpret_cast<uint4*>(row + j + x * kUnit) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-    } else {
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        if (j + x < 0 || j + x >= k_len) continue;
-        if constexpr (E == 1) row[j + x] = __uint_as_float(w[x]);
-        else reinterpret_cast<unsigned short*>(row)[j + x] = (unsigned short)(w[x / 2] >> (16 * (x & 1)));
+        for (int x = 0; x < U; ++x) {
+          if (j + x < 0 || j + x >= k_len) continue;
+          if constexpr (E == 1) row[j + x] = __uint_as_float(w[x]);
+          else reinterpret_cast<unsigned short*>(row)[j + x] = (unsigned short)(w[x / 2] >> (16 * (x & 1)));
+        }
       }
     }
   }
@@ -183,23 +178,27 @@ struct GradView {
   uintptr_t lo, hi;   // the bytes from the first element to the end of the last
 };
 
-// The gradient is cut into tiles of 64 queries by 256 diagonals, a warp each:
-// lane l takes 8 neighbouring keys of 8 queries at a time and moves 8 keys
+// The gradient is cut into tiles of 64 queries by 248 diagonals, a warp each:
+// lane l < 31 takes 8 neighbouring keys of 8 queries at a time and moves 8 keys
 // on with every 8 queries, so its 64 pairs always lie on the same 15 diagonals
 // (the key within the eight less the query within the eight), whose sums
-// stay in registers.
+// stay in registers.  Lane 31 takes no pairs: where eights are not 16-byte
+// aligned it reads what lane 30 lacks.
 constexpr int kTileRows = 64;
 constexpr int kTileGroups = kTileRows / 8;
-constexpr int kTileDiags = 264;   // diagonals of a tile: 32 lanes x 8, and the 8 below
-constexpr int kTileWarps = 4;     // warps of a CTA
+constexpr int kTileLanes = 31;
+constexpr int kStripDiags = 8 * kTileLanes;
+constexpr int kTileDiags = kStripDiags + 8;   // diagonals of a tile: the lanes' eights, and the 8 below
+constexpr int kTileWarps = 4;                 // warps of a CTA
 
 struct TileGrid {
   int row_blocks, strips;   // tiles along the queries and along the keys
   __host__ __device__ TileGrid(int q_len, int k_len)
-      : row_blocks((q_len + kTileRows - 1) / kTileRows), strips(((k_len + 7) / 8 + kTileGroups + 31) / 32) {}
+      : row_blocks((q_len + kTileRows - 1) / kTileRows),
+        strips(((k_len + 7) / 8 + kTileGroups + kTileLanes - 1) / kTileLanes) {}
   __host__ __device__ int per_matrix() const { return row_blocks * strips; }
   // First key eight of lane 0 in the tile's first group.
-  __device__ __forceinline__ int first_eight(int strip) const { return strip * 32 - kTileGroups; }
+  __device__ __forceinline__ int first_eight(int strip) const { return strip * kTileLanes - kTileGroups; }
   // Key - query of the tile's diagonal 0.
   __device__ __forceinline__ int first_diagonal(int row_block, int strip) const {
     return 8 * first_eight(strip) - row_block * kTileRows - 8;
@@ -225,41 +224,47 @@ __device__ __forceinline__ uint4 load_16(const void* p) {
   return v;
 }
 
-// The 8 elements at p, every such eight 16-byte aligned (ALIGNED), or any:
-// the 16-byte blocks that hold it are read and shifted into place.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ Eight<T> load_eight(const T* p) {
-  constexpr int W = Eight<T>::W;
+// The 16-byte blocks from `at` up that make an eight when they are aligned.
+template <typename T, bool ALIGNED> __device__ __forceinline__ Eight<T> load_blocks(uintptr_t at) {
   Eight<T> e;
-  if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const uint4 v = load_16(reinterpret_cast<const char*>(p) + 4 * i);
-      e.w[i] = v.x, e.w[i + 1] = v.y, e.w[i + 2] = v.z, e.w[i + 3] = v.w;
-    }
-  } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p), first = at & ~(uintptr_t)15;
-    unsigned v[W + 4];
-#pragma unroll
-    for (int i = 0; i < W + 4; i += 4) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(first) + i / 4);
-      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-    }
-    const unsigned off = (unsigned)(at - first);
-#pragma unroll
-    for (int i = 0; i < W + 2; ++i) v[i] = (off & 8) ? v[i + 2] : v[i];
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) v[i] = (off & 4) ? v[i + 1] : v[i];
-#pragma unroll
-    for (int i = 0; i < W; ++i) e.w[i] = sizeof(T) == 2 ? __funnelshift_r(v[i], v[i + 1], (off & 2) * 8) : v[i];
+  for (int i = 0; i < Eight<T>::W; i += 4) {
+    // (unaligned in 32 bits a sector is often halved between two of the loads:
+    // kept in L1; 3 x 12 x 509 x 1531: 40 -> 29 us)
+    const uint4 v = sizeof(T) == 4 && !ALIGNED ? __ldg(reinterpret_cast<const uint4*>(at) + i / 4)
+                                               : load_16(reinterpret_cast<const void*>(at + 4 * i));
+    e.w[i] = v.x, e.w[i + 1] = v.y, e.w[i + 2] = v.z, e.w[i + 3] = v.w;
   }
   return e;
 }
-// Whether load_eight at p stays inside the matrices' memory.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ bool eight_inside(const T* p, const GradView& g) {
-  const uintptr_t first = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
-  return ALIGNED || (first >= g.lo && first + 4 * Eight<T>::W + 16 <= g.hi);
+// The eight that starts `off` bytes (the same of every lane) into the lane's
+// blocks and ends in the next lane's first.
+template <typename T, int WORDS> __device__ __forceinline__ Eight<T> shift_eight_by(const Eight<T>& mine, bool half) {
+  constexpr int W = Eight<T>::W;
+  unsigned v[W + WORDS + 1];
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = mine.w[i];
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) v[W + i] = __shfl_down_sync(0xffffffffu, mine.w[i], 1);
+  Eight<T> e;
+  if (sizeof(T) == 2 && half) {
+    v[W + WORDS] = __shfl_down_sync(0xffffffffu, mine.w[WORDS], 1);
+#pragma unroll
+    for (int i = 0; i < W; ++i) e.w[i] = __funnelshift_r(v[WORDS + i], v[WORDS + i + 1], 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) e.w[i] = v[WORDS + i];
+  }
+  return e;
+}
+template <typename T> __device__ __forceinline__ Eight<T> shift_eight(const Eight<T>& mine, unsigned off) {
+  const bool half = off & 2;
+  switch (off >> 2) {
+    case 0: return shift_eight_by<T, 0>(mine, half);
+    case 1: return shift_eight_by<T, 1>(mine, half);
+    case 2: return shift_eight_by<T, 2>(mine, half);
+    default: return shift_eight_by<T, 3>(mine, half);
+  }
 }
 // Elements j .. j + 7 of a row one by one, 0 outside [0, k_len).
 template <typename T>
@@ -279,7 +284,7 @@ __device__ __forceinline__ Eight<T> load_singly(const T* row, int j, int k_len) 
 // part[h][bucket][tile] = the tile's sum over the bucket, for the buckets
 // that the tile's diagonals reach.
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kTileWarps, 4)
+__global__ void __launch_bounds__(32 * kTileWarps, ALIGNED ? 4 : sizeof(T) == 4 ? 3 : 5)
 bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_offset, int buckets,
                   float* __restrict__ part) {
   __shared__ float sh[kTileWarps][kTileDiags];
@@ -298,37 +303,67 @@ bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_
 #pragma unroll
   for (int i = 0; i < 15; ++i) acc[i] = 0.0f;
   for (int i = i0; i < min(i0 + kTileRows, g.q_len); i += 8, j += 8) {
-    if (j + 8 <= 0 || j >= g.k_len) continue;
     const T* p = matrix + (long long)i * g.stride_q + j;
     const int count = min(8, g.q_len - i);
-    if (count == 8 && j >= 0 && j + 8 <= g.k_len && eight_inside<T, ALIGNED>(p, g) &&
-        eight_inside<T, ALIGNED>(p + 7 * g.stride_q, g)) {
-      Eight<T> e[8];
+    const bool whole = j >= 0 && j + 8 <= g.k_len && lane < kTileLanes;
+    const bool some = j + 8 > 0 && j < g.k_len && lane < kTileLanes;
+    if constexpr (ALIGNED) {
+      if (whole && count == 8) {
+        Eight<T> e[8];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) e[y] = load_eight<T, ALIGNED>(p + y * g.stride_q);
+        for (int y = 0; y < 8; ++y) e[y] = load_blocks<T, true>(reinterpret_cast<uintptr_t>(p + y * g.stride_q));
 #pragma unroll
-      for (int y = 0; y < 8; ++y)
+        for (int y = 0; y < 8; ++y)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) acc[x - y + 7] += e[y].get(x);
-    } else {
+          for (int x = 0; x < 8; ++x) acc[x - y + 7] += e[y].get(x);
+        continue;
+      }
+    } else if (count == 8) {
+      // the blocks of all rows, where they hold some of the rows' keys and lie
+      // in the matrices' memory
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p), step = sizeof(T) * g.stride_q;
+      const uintptr_t top = at & ~(uintptr_t)15, bottom = (at + 7 * step) & ~(uintptr_t)15;
+      Eight<T> e[8] = {};
+      if (j > -16 && j < g.k_len + 8 && top >= g.lo && bottom + 4 * Eight<T>::W <= g.hi) {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = load_blocks<T, false>((at + y * step) & ~(uintptr_t)15);
+      }
+      // whether the next lane's do too
+      const bool shifted = whole && top >= g.lo && bottom + 8 * Eight<T>::W <= g.hi;
+      const unsigned off = __shfl_sync(0xffffffffu, (unsigned)at, 0);
+      const unsigned off_step = (unsigned)step;
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
-        if (y >= count) break;
-        const Eight<T> e = load_singly(p + y * g.stride_q - j, j, g.k_len);
+        const Eight<T> f = shift_eight(e[y], (off + y * off_step) & 15);
+        if (shifted) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) acc[x - y + 7] += e.get(x);
+          for (int x = 0; x < 8; ++x) acc[x - y + 7] += f.get(x);
+        }
       }
+      if (shifted) continue;
+    }
+    if (!some) continue;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      if (y >= count) break;
+      const Eight<T> e = load_singly(p + y * g.stride_q - j, j, g.k_len);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x - y + 7] += e.get(x);
     }
   }
   // the tile's diagonals: one's own 0 .. 7, then the 7 below on top of the
   // neighbour's
   float* diag = sh[warp];
   if (lane < 8) diag[lane] = 0.0f;
+  if (lane < kTileLanes) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s) diag[8 * (lane + 1) + s] = acc[s + 7];
+    for (int s = 0; s < 8; ++s) diag[8 * (lane + 1) + s] = acc[s + 7];
+  }
   __syncwarp();
+  if (lane < kTileLanes) {
 #pragma unroll
-  for (int s = 1; s < 8; ++s) diag[8 * lane + s] += acc[s - 1];
+    for (int s = 1; s < 8; ++s) diag[8 * lane + s] += acc[s - 1];
+  }
   __syncwarp();
   // The buckets of both signs, a lane each; a bucket of 32 diagonals or more
   // is added by the whole warp.
@@ -373,8 +408,9 @@ bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_
   }
 }
 
-// One CTA per (bucket, head): thread t adds the tiles t, t + 128, ... that
-// reach the bucket, then the threads are added by a tree.
+// One CTA per (bucket, head): thread t adds the tiles of the rows of tiles t,
+// t + 128, ... that reach the bucket (neighbours in the row), then the
+// threads are added by a tree.
 constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads)
 bias_join_kernel(const float* __restrict__ part, int batch, int q_len, int k_len, Distances dist, int q_offset, int heads,
@@ -382,17 +418,20 @@ bias_join_kernel(const float* __restrict__ part, int batch, int q_len, int k_len
   __shared__ float sh[kJoinThreads / 32];
   dep_wait();
   const TileGrid tiles(q_len, k_len);
-  const int per_matrix = tiles.per_matrix(), per_head = per_matrix * batch;
-  const int k = blockIdx.x, h = blockIdx.y;
-  const float* p = part + ((long long)h * buckets + k) * per_head;
+  const int k = blockIdx.x, h = blockIdx.y, rows = tiles.row_blocks * batch;
+  const float* p = part + ((long long)h * buckets + k) * rows * tiles.strips;
   float sum = 0.0f;
-  for (int t = threadIdx.x; t < per_head; t += kJoinThreads) {
-    const int in_matrix = t % per_matrix;
-    const int row_block = in_matrix / tiles.strips, strip = in_matrix - row_block * tiles.strips;
-    const int from = tiles.first_diagonal(row_block, strip) - q_offset;
+  for (int t = threadIdx.x; t < rows; t += kJoinThreads) {
+    // strip s holds the distances from + kStripDiags s up to kTileDiags more
+    const int from = tiles.first_diagonal(t % tiles.row_blocks, 0) - q_offset;
     int lo, hi;
-    dist.interval(k, from, from + kTileDiags, lo, hi);
-    if (lo < hi) sum += p[t];
+    dist.interval(k, from, from + kStripDiags * (tiles.strips - 1) + kTileDiags, lo, hi);
+    if (lo >= hi) continue;
+    lo -= from;
+    hi -= from;
+    const int s0 = lo < kTileDiags ? 0 : (lo - kTileDiags) / kStripDiags + 1;
+    const int s1 = min((hi - 1) / kStripDiags, tiles.strips - 1);
+    for (int s = s0; s <= s1; ++s) sum += p[(long long)t * tiles.strips + s];
   }
   sum = warp_pt(sum);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
@@ -415,7 +454,8 @@ int check_shape(int64_t heads, int64_t num_bounds, int64_t q_len, int64_t k_len,
 
 // Tiles of a head's gradient, or 2^31 when there are that many or more.
 inline int64_t tiles_of_head(int64_t batch, int64_t q_len, int64_t k_len) {
-  const int64_t rows = (q_len + kTileRows - 1) / kTileRows, strips = ((k_len + 7) / 8 + kTileGroups + 31) / 32;
+  const int64_t rows = (q_len + kTileRows - 1) / kTileRows;
+  const int64_t strips = ((k_len + 7) / 8 + kTileGroups + kTileLanes - 1) / kTileLanes;
   if (rows * strips >= (1LL << 31) || (rows * strips > 0 && batch > (1LL << 31) / (rows * strips))) return 1LL << 31;
   return rows * strips * batch;
 }
@@ -428,18 +468,19 @@ int launch_bias(const void* table, int table_dtype, int heads, const Distances& 
     launch_begin("det_relative_bias", s);
     bias_direct_kernel<T><<<grid, 256, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len, static_cast<T*>(out));
   } else {
-    // a row has eights from head - 8 up, head < 8
-    const int eights = (k_len + 7) / 8 + 1;
-    const dim3 grid((unsigned)((eights + kBiasThreads - 1) / kBiasThreads),
-                    (unsigned)((q_len + kBiasRows - 1) / kBiasRows), (unsigned)heads);
-    if (grid.y > 65535) return DET_ERR_TOO_LARGE;
+    // a row has units from the one before its first boundary up
+    const int unit = 16 / sizeof(T), units = (k_len + unit - 1) / unit + 1;
     const bool aligned = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)k_len * sizeof(T)) % 16 == 0;
+    const int threads = aligned ? BiasTile<T, true>::kThreads : BiasTile<T, false>::kThreads;
+    const int rows = aligned ? BiasTile<T, true>::kRows : BiasTile<T, false>::kRows;
+    const dim3 grid((unsigned)((units + threads - 1) / threads), (unsigned)((q_len + rows - 1) / rows), (unsigned)heads);
+    if (grid.y > 65535) return DET_ERR_TOO_LARGE;
     launch_begin("det_relative_bias", s);
     if (aligned)
-      bias_strip_kernel<T, true><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
+      bias_strip_kernel<T, true><<<grid, threads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
                                                                static_cast<T*>(out));
     else
-      bias_strip_kernel<T, false><<<grid, kBiasThreads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
+      bias_strip_kernel<T, false><<<grid, threads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
                                                                 static_cast<T*>(out));
   }
   launch_end(s);

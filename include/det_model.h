@@ -94,7 +94,7 @@ int det_token_logprobs_backward(const void* logits, int64_t rows, int64_t vocab,
  *   bounds  device, num_bounds int32 (NULL when num_bounds is 0)
  *   out     device, heads x q_len x k_len of dtype, contiguous (written); a
  *           table entry is converted to dtype once, to nearest
- * Limits: |q_offset| + q_len + k_len <= 2^30, q_len <= 2^22, num_bounds <=
+ * Limits: |q_offset| + q_len + k_len <= 2^30, q_len <= 2^20, num_bounds <=
  * DET_MAX_BOUNDS, heads <= 65,535.
  */
 #define DET_MAX_BOUNDS 2047
@@ -111,7 +111,7 @@ int det_relative_bias(const void* table, int table_dtype, int64_t heads, const i
  *               (in elements) but 1 along j; any alignment
  *   grad_table  device, buckets x heads of table_dtype, contiguous (written)
  * Limits: |q_offset| + q_len + k_len <= 2^30, num_bounds <= DET_MAX_BOUNDS,
- * heads <= 65,535, batch x (q_len / 64) x (k_len / 256 + 2) below 2^31;
+ * heads <= 65,535, batch x (q_len / 64 + 1) x (k_len / 248 + 2) below 2^31;
  * strides are not negative.
  */
 size_t det_relative_bias_backward_workspace_bytes(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len,
