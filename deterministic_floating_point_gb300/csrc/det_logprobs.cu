@@ -20,7 +20,7 @@ constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kWords = 32;      // 4-byte words of a thread's chunk
 constexpr int kPartWords = 4;   // a row's last chunk goes by this many
-constexpr int kBest = 64 / kRowWarps;   // threads of a warp that a bound for the alternatives is drawn from
+constexpr int kBest = 6;         // most threads of a warp that the bound for the alternatives is drawn from
 
 template <typename T> struct Word;   // what a 4-byte word of a row holds
 template <> struct Word<float> {
@@ -191,10 +191,8 @@ struct RowMap {
     if (in1 == in0) head = tail = 0;   // no whole block: every word (at most 8) is an edge
   }
   __device__ __forceinline__ bool odd() const { return N == 2 && (off & 2); }
-  // Whether chunk c has edges or masked words.
-  __device__ __forceinline__ bool ragged(int c) const {
-    return (c == 0 && head > 0) || (long long)(c + 1) * kChunkWords > tail;
-  }
+  // Whether chunk c has edges at the row's end, or masked words.
+  __device__ __forceinline__ bool ragged(int c) const { return (long long)(c + 1) * kChunkWords > tail; }
   // The thread's word among the last edges, or -1.
   __device__ __forceinline__ int tail_word() const {
     const int w = tail + (((int)threadIdx.x - tail) & (kRowThreads - 1));
@@ -317,15 +315,20 @@ __device__ __forceinline__ void add_far_word(Stat& st, unsigned x) {
 
 // Shared memory of a row's end.
 struct RowEnd {
-  unsigned best[64];   // the order keys of every warp's best threads
+  unsigned best[kBest * kRowWarps];   // the order keys of every warp's best threads
   float s[kRowWarps], t[kRowWarps];
   unsigned floor;
   int count[kRowWarps];
   unsigned long long list[kRowWarps * DET_MAX_TOP_K];
 };
 
-// The top_k largest of the row.  end.best holds the order keys of the eight
-// best threads of every warp: the k-th largest of those 64 is a lower bound of
+// Threads of a warp that the bound for k alternatives is drawn from: some more
+// than k in all the warps.
+__device__ __forceinline__ int best_per_warp(int k) { return k == 0 ? 1 : (k + kRowWarps - 1) / kRowWarps + 1 + (k > 8); }
+static_assert((DET_MAX_TOP_K + kRowWarps - 1) / kRowWarps + 2 <= kBest, "room for the largest k");
+
+// The top_k largest of the row.  end.best holds the order keys of the best
+// threads of every warp, `each` of them: the k-th largest is a lower bound of
 // the row's k-th largest element, so only threads whose best reaches it are
 // looked through again, each by its whole warp, whose lanes keep the best in
 // order: the 32 words of the chunk with its best, and all its words only if
@@ -334,12 +337,12 @@ template <typename T>
 __device__ void top_alternatives(const T* row, int vocab, float largest, const Best& best, int k, float m, float log_s,
                                  long long r, RowEnd& end, const RowOut& out) {
   constexpr int N = Word<T>::N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = best_per_warp(k);
   {
-    const unsigned a = end.best[lane], b = end.best[lane + 32];
-#pragma unroll
-    for (int j = 0; j < kBest; ++j) {
-      const int at = kBest * warp + j;
+    const unsigned a = lane < each * kRowWarps ? end.best[lane] : 0u;
+    const unsigned b = lane + 32 < each * kRowWarps ? end.best[lane + 32] : 0u;
+    for (int j = 0; j < each; ++j) {
+      const int at = each * warp + j;
       const unsigned mine = end.best[at];
       const int above = __popc(__ballot_sync(0xffffffffu, a > mine || (a == mine && lane < at))) +
                         __popc(__ballot_sync(0xffffffffu, b > mine || (b == mine && lane + 32 < at)));
@@ -357,10 +360,10 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
   one &= ~all;
   int all_chunk = 0;
   static_assert(kWords == 32, "a lane per word");
-  constexpr int kAhead = 4;      // loads in flight
+  constexpr int kAhead = 8;      // loads in flight
   while (one | all) {
     unsigned word[kAhead];
-    int at[kAhead];
+    int at[kAhead], loads = 0;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       int owner = 0, c = chunks;   // none
@@ -379,18 +382,19 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
       at[a] = words;
       word[a] = 0u;
       if (c < chunks) {
+        loads = a + 1;
         at[a] = c * kChunkWords + lane * kRowThreads + warp * 32 + owner;
         if (at[a] < words) word[a] = load_word(row, at[a], vocab, aligned);
       }
     }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+#pragma unroll 1
+    for (int a = 0; a < loads; ++a) {   // the first of the arrays, which move up
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int e = at[a] * N + j;
+        const int e = at[0] * N + j;
         unsigned long long cand = 0;
-        if (at[a] < words && e < vocab) {
-          const unsigned ek = order_key(Word<T>::get(word[a], j));
+        if (at[0] < words && e < vocab) {
+          const unsigned ek = order_key(Word<T>::get(word[0], j));
           if (ek >= floor_key) cand = ((unsigned long long)ek << 32) | (unsigned)~(unsigned)e;
         }
         if (!__any_sync(0xffffffffu, cand != 0)) continue;
@@ -402,6 +406,12 @@ __device__ void top_alternatives(const T* row, int vocab, float largest, const B
           list_insert(mine, __shfl_sync(0xffffffffu, cand, src), lane);
         }
       }
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) {
+        word[i] = word[i + 1];
+        at[i] = at[i + 1];
+      }
+    }
   }
   const int count = min(k, __popc(__ballot_sync(0xffffffffu, mine != 0)));
   if (lane == 0) end.count[warp] = count;
@@ -437,14 +447,15 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   }
   const float largest = st.m;
   unsigned left = order_key(largest);
-  for (int j = 0; j < (top_k > 0 ? kBest : 1); ++j) {
+  const int each = best_per_warp(top_k);
+  for (int j = 0; j < each; ++j) {
     const unsigned top = __reduce_max_sync(0xffffffffu, left);
-    if (lane == 0) end.best[kBest * warp + j] = top;
+    if (lane == 0) end.best[each * warp + j] = top;
     const int owner = __ffs(__ballot_sync(0xffffffffu, left == top)) - 1;
     if (lane == owner) left = 0u;
   }
   __syncthreads();
-  const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[kBest * (lane & (kRowWarps - 1))]));
+  const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[each * (lane & (kRowWarps - 1))]));
   raise_to<T>(st, m);
   float s = warp_pt(st.s), t = warp_pt(st.t);
   if (lane == 0) {
@@ -548,6 +559,7 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
         unsigned x[NW];
         read_words<decltype(shift)::value>(words, map.off, i0, odd_shift, x);
         if (ragged) set_edges(map, w0, head, tail, tail_word, x);
+        else if (w0 < map.head) x[0] = head;   // the first words of a row
         raise_words<T>(st, best, c, largest_of<T>(x));
         const bool near = near_max<T>(st.m), all_near = __all_sync(0xffffffffu, near);
         if (kAll && all_near) release();
