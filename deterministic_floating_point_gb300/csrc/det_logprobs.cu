@@ -243,6 +243,28 @@ struct Best {
   float others;
 };
 
+// A row is cut into at most four parts of whole chunks, and a thread joins
+// its statistics of the parts in order; so the parts may be the work of one
+// CTA after the other or of a cluster's CTAs at once, with the same bits.
+constexpr int kParts = 4;
+__host__ __device__ inline int chunks_per_part(int chunks) { return (chunks + kParts - 1) / kParts; }
+
+// A later part joined to the parts before it.
+template <typename T>
+__device__ __forceinline__ void join_part(Stat& st, Best& best, Stat part, const Best& part_best) {
+  const float m = max_nan(st.m, part.m);
+  if (!(part.m <= st.m)) {
+    best.chunk = part_best.chunk;
+    best.others = max_nan(part_best.others, st.m);
+  } else {
+    best.others = max_nan(best.others, part.m);
+  }
+  raise_to<T>(st, m);
+  raise_to<T>(part, m);
+  st.s += part.s;
+  st.t += part.t;
+}
+
 // The largest of NW words.
 template <typename T, int NW>
 __device__ __forceinline__ float largest_of(const unsigned (&x)[NW]) {
@@ -483,9 +505,16 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   if (top_k > 0) top_alternatives(row, vocab, largest, best, top_k, base, log_s, r, end, out);
 }
 
-// Persistent: CTA b takes the rows b, b + gridDim.x, ...  A wait for a copy
-// that does not end within kWaitNs gives up: the row's results are NaN then.
-template <typename T>
+// What a CTA of a cluster leaves of its part for the first one.
+struct PartStats {
+  float m[kRowThreads], s[kRowThreads], t[kRowThreads], others[kRowThreads], chunk[kRowThreads];
+};
+static_assert(sizeof(PartStats) <= sizeof(Stream::stage), "it fits the stages");
+
+// Persistent: CTA b takes the rows b, b + gridDim.x, ...; SPLIT: a cluster of a
+// CTA per part takes a row.  A wait for a copy that does not end within kWaitNs
+// gives up: the row's results are NaN then.
+template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kRowThreads, 2)
 token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, long long row_stride,
                       const int32_t* __restrict__ tokens, int top_k, RowOut out) {
@@ -494,6 +523,10 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
   __shared__ RowEnd end;
   const int lane = threadIdx.x & 31;
   const int chunks = max(1, (int)(((long long)vocab + Word<T>::N * kChunkWords - 1) / (Word<T>::N * kChunkWords)));
+  const int per_part = chunks_per_part(chunks), parts = (chunks + per_part - 1) / per_part;
+  const int rank = SPLIT ? blockIdx.x % parts : 0;
+  const int c0 = SPLIT ? rank * per_part : 0, c1 = SPLIT ? min(c0 + per_part, chunks) : chunks;
+  const long long row0 = SPLIT ? blockIdx.x / parts : blockIdx.x, row_step = SPLIT ? rows : gridDim.x;
   if (threadIdx.x == 0)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&stream.full[i], 1);
@@ -501,8 +534,8 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
     }
   __syncthreads();
   // the next chunk to fetch, its stage and how often the stage was filled
-  long long next_row = blockIdx.x;
-  int next_chunk = 0, next_stage = 0, next_round = 0;
+  long long next_row = row0;
+  int next_chunk = c0, next_stage = 0, next_round = 0;
   bool gave_up = false;
   auto fetch_next = [&](bool mine) {
     if (next_row >= rows) return;
@@ -510,9 +543,9 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
       if (next_round > 0 && !gave_up) gave_up = !mbar_wait(&stream.empty[next_stage], (next_round - 1) & 1, kWaitNs);
       if (!gave_up) RowMap<T>(logits + next_row * row_stride, vocab).fetch(stream, next_stage, next_chunk);
     }
-    if (++next_chunk == chunks) {
-      next_chunk = 0;
-      next_row += gridDim.x;
+    if (++next_chunk == c1) {
+      next_chunk = c0;
+      next_row += row_step;
     }
     if (++next_stage == kStages) {
       next_stage = 0;
@@ -530,17 +563,18 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
     const int w = map.tail_word();
     if (w >= 0) tail_ahead = load_word(map.row, w, vocab, aligned);
   };
-  load_edges(blockIdx.x);
+  load_edges(row0);
   int stage = 0, round = 0, turn = 0;
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+  for (long long r = row0; r < rows; r += row_step) {
     const RowMap<T> map(logits + r * row_stride, vocab);
     const unsigned head = head_ahead, tail = tail_ahead;
-    load_edges(r + gridDim.x);
-    Stat st = {kNegInf, 0.0f, 0.0f};
-    Best best = {-1, kNegInf};
+    load_edges(r + row_step);
+    Stat st = {kNegInf, 0.0f, 0.0f}, all = st;   // of the part, and of the parts before it
+    Best best = {-1, kNegInf}, all_best = best;
     const unsigned odd_shift = map.odd() ? 16u : 0u;
     const int tail_word = map.tail_word();
-    for (int c = 0; c < chunks; ++c) {
+    int part_end = per_part;
+    for (int c = c0; c < c1; ++c) {
       // the warps take turns at waiting for the stage that all have read and filling it
       fetch_next(threadIdx.x == turn * 32);
       turn = (turn + 1) & (kRowWarps - 1);
@@ -594,9 +628,36 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
         stage = 0;
         ++round;
       }
+      if (!SPLIT && (c + 1 == part_end || c + 1 == c1)) {
+        join_part<T>(all, all_best, st, best);
+        st = {kNegInf, 0.0f, 0.0f};
+        best = {-1, kNegInf};
+        part_end += per_part;
+      }
     }
-    if (gave_up) st.m = __uint_as_float(0x7fc00000u);
-    finish_row(st, best, map.row, vocab, r, tokens, top_k, end, out);
+    if (SPLIT) {
+      __syncthreads();   // the stages have been read
+      PartStats& left = *reinterpret_cast<PartStats*>(stream.stage);
+      left.m[threadIdx.x] = gave_up ? __uint_as_float(0x7fc00000u) : st.m;
+      left.s[threadIdx.x] = st.s;
+      left.t[threadIdx.x] = st.t;
+      left.others[threadIdx.x] = best.others;
+      left.chunk[threadIdx.x] = __int_as_float(best.chunk);
+      cluster_sync_all();
+      if (rank == 0)
+        for (int p = 0; p < parts; ++p) {
+          const Stat part = {ld_dsmem(&left.m[threadIdx.x], p), ld_dsmem(&left.s[threadIdx.x], p),
+                             ld_dsmem(&left.t[threadIdx.x], p)};
+          const Best part_best = {__float_as_int(ld_dsmem(&left.chunk[threadIdx.x], p)),
+                                  ld_dsmem(&left.others[threadIdx.x], p)};
+          join_part<T>(all, all_best, part, part_best);
+        }
+      cluster_sync_all();   // no CTA leaves before its part is read
+      if (rank != 0) return;
+    } else if (gave_up) {
+      all.m = __uint_as_float(0x7fc00000u);
+    }
+    finish_row(all, all_best, map.row, vocab, r, tokens, top_k, end, out);
   }
 }
 
@@ -721,14 +782,32 @@ token_logprobs_grad_kernel(const T* __restrict__ logits, int vocab, long long ro
 template <typename T>
 int launch_logprobs(const void* logits, long long rows, int vocab, long long stride, const int32_t* tokens, int top_k,
                     const RowOut& out, cudaStream_t s) {
-  const void* kernel = reinterpret_cast<const void*>(&token_logprobs_kernel<T>);
-  if (const cudaError_t e = ensure_dyn_smem(kernel, sizeof(Stream))) return cuda_fail(e, "det_token_logprobs");
-  const long long grid = std::min(rows, 2LL * std::max(device_sm_count(), 1));
+  const long long per_chunk = (long long)Word<T>::N * kChunkWords;
+  const int chunks = (int)std::max(1LL, (vocab + per_chunk - 1) / per_chunk);
+  const int per_part = chunks_per_part(chunks), parts = (chunks + per_part - 1) / per_part;
+  const long long resident = 2LL * std::max(device_sm_count(), 1);
+  // A row per cluster while every CTA is resident at once: SMs would stand idle
+  // otherwise.  With more rows the parts of a row gain nothing.
+  const bool split = parts > 1 && rows * parts <= resident;
+  auto kernel = split ? token_logprobs_kernel<T, true> : token_logprobs_kernel<T, false>;
+  if (const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), sizeof(Stream)))
+    return cuda_fail(e, "det_token_logprobs");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(split ? rows * parts : std::min(rows, resident)));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = sizeof(Stream);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split ? 1 : 0;
   launch_begin("det_token_logprobs", s);
-  token_logprobs_kernel<T><<<(unsigned)grid, kRowThreads, sizeof(Stream), s>>>(static_cast<const T*>(logits), rows, vocab,
-                                                                             stride, tokens, top_k, out);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(logits), rows, vocab, stride, tokens,
+                                           top_k, out);
   launch_end(s);
-  return check_launch("det_token_logprobs");
+  return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_token_logprobs");
 }
 
 template <typename T>

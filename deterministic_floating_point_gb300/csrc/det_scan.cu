@@ -317,25 +317,6 @@ __device__ void anchor_chain(const ScanArgs<T>& a) {
 // the tree over lanes L < c holding Agg(c - 1 - L), exactly as above.
 constexpr int kClusterChunks = 16;
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The value at `local` in the shared memory of cluster CTA `rank`.
-__device__ __forceinline__ float ld_dsmem(const float* local, unsigned rank) {
-  unsigned r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
-  return v;
-}
-__device__ __forceinline__ double ld_dsmem(const double* local, unsigned rank) {
-  unsigned r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(r) : "memory");
-  return v;
-}
-
 template <typename T, bool REV, bool EXCL>
 __global__ void __launch_bounds__(1024, 1) scan_cluster_kernel(const T* __restrict__ x, T* y, long long n,
                                                                T* total_out, unsigned int* status) {

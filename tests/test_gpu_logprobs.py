@@ -173,6 +173,27 @@ def test_a_row_does_not_depend_on_its_batch_or_alignment(det, dtype):
     assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("vocab", [16_385, 40_001, 65_536, 100_003])
+def test_few_rows_and_many_rows_give_the_same_bits(det, dtype, vocab):
+    """Few rows are split over several CTAs each, many are not."""
+    rng = np.random.default_rng(vocab)
+    rows = 170
+    x = logits(rng, rows, vocab, dtype)
+    x[3] = -np.inf
+    x[4, : vocab // 2] = -np.inf
+    x[5] = torch.finfo(x.dtype).min
+    x[6, 5] = float("nan")
+    x[7] = 1.5                                             # ties over all parts
+    tokens = torch.from_numpy(rng.integers(0, vocab, rows).astype(np.int32)).cuda()
+    many = det.det_token_logprobs(x, tokens, top_k=9)
+    for rs in ([0], [3, 4, 5, 6, 7], list(range(60, 100))):
+        few = det.det_token_logprobs(x[rs].contiguous(), tokens[rs].contiguous(), top_k=9)
+        for a, b in zip(many, few):
+            assert torch.equal(torch.nan_to_num(a[rs].float(), nan=12345.0), torch.nan_to_num(b.float(), nan=12345.0))
+    check(det, x[:9].contiguous(), tokens[:9].cpu().numpy(), 9)
+
+
 def test_empty_shapes_and_no_tokens(det):
     for shape in ((0, 100), (3, 0), (0, 0), (2, 0, 50)):
         x = torch.zeros(shape, device="cuda")
