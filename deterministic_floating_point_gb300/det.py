@@ -416,13 +416,13 @@ def _model_code(t: torch.Tensor, name: str, codes=_MODEL_CODES) -> int:
 
 def _on(device, dtype, name: str, t: torch.Tensor, shape=None, contiguous: bool = True) -> torch.Tensor:
     """t, checked to be a tensor of this device, dtype and shape (each unless None)."""
-    if not t.is_cuda or (device is not None and t.device != device):
+    if (not t.is_cuda) if device is None else (t.device != device or device.type != "cuda"):
         raise ValueError(f"{name} must be a CUDA tensor on one device with the others")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -499,9 +499,10 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
             raise ValueError(f"top_k must be at most {MAX_TOP_K} and the vocabulary, got {top_k}")
         top_logprob = _empty((*lead, top_k), torch.float32, dev, stream)
         top_index = _empty((*lead, top_k), torch.int32, dev, stream)
-    _check(lib().det_token_logprobs(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob),
-                                    _ptr(entropy), _ptr(lse), int(top_k), _ptr(top_logprob), _ptr(top_index),
-                                    _stream(stream, dev)), "det_token_logprobs")
+    rc = lib().det_token_logprobs(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob), _ptr(entropy),
+                                  _ptr(lse), top_k, _ptr(top_logprob), _ptr(top_index), _stream(stream, dev))
+    if rc:
+        raise DetError(rc, "det_token_logprobs")
     return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
 
 
@@ -622,6 +623,18 @@ def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_of
     return out
 
 
+def _cache(device, dtype, name: str, t: torch.Tensor, shape):
+    """(pointer, strides of pages, tokens and heads) of a key or value cache."""
+    _on(device, dtype, name, t, shape, contiguous=False)
+    s_page, s_token, s_head, s_dim = t.stride()
+    ptr = t.data_ptr()
+    if s_dim != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if (ptr | s_page * 2 | s_token * 2 | s_head * 2) & 15:
+        raise ValueError(f"{name} must be 16-byte aligned with strides that are multiples of 8 elements")
+    return ptr, (s_page, s_token, s_head)
+
+
 class PagedAttention(NamedTuple):
     out: torch.Tensor
     lse: torch.Tensor
@@ -652,15 +665,8 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if page_size < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError("page_size must be positive and heads a multiple of kv_heads")
     _unit_stride(q, "q")
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _on(dev, q.dtype, name, t, (pages, page_size, kv_heads, dim), contiguous=False)
-        s_page, s_token, s_head, s_dim = t.stride()
-        if s_dim != 1:
-            raise ValueError(f"{name} must be contiguous along its last dimension")
-        if (t.data_ptr() & 15) or ((s_page | s_token | s_head) & 7):
-            raise ValueError(f"{name} must be 16-byte aligned with strides that are multiples of 8 elements")
-        strides.append((s_page, s_token, s_head))
+    k_ptr, k_strides = _cache(dev, q.dtype, "k_cache", k_cache, (pages, page_size, kv_heads, dim))
+    v_ptr, v_strides = _cache(dev, q.dtype, "v_cache", v_cache, k_cache.shape)
     _on(dev, torch.int32, "block_table", block_table, contiguous=False)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, max_pages]")
@@ -687,8 +693,9 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     call = lib()
     ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
     _check(call.det_paged_attention(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), *strides[0], _ptr(v_cache), *strides[1], pages, page_size,
-        _ptr(block_table), block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads, kv_heads, dim, code, dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
+        _ptr(q), q.stride(0), q.stride(1), k_ptr, *k_strides, v_ptr, *v_strides, pages, page_size, _ptr(block_table),
+        block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads, kv_heads, dim, code,
+        dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
         _ptr(bias_bounds) if bias_table is not None else None, n_bounds, limit, _ptr(out), _ptr(lse), _ptr(ws),
         ws.numel(), _stream(stream, dev)), "det_paged_attention")
     return PagedAttention(out, lse)
