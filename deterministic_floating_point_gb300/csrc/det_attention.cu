@@ -24,12 +24,15 @@ namespace {
 
 constexpr int kMaxChunk = 1024;  // most tokens of a chunk
 
-// Tokens of a chunk of a sequence of n tokens: short chunks let a short
+// Tokens of a chunk of a sequence of n tokens.  Short chunks let a short
 // sequence use more SMs, long ones spend less on their start and on the join
 // (32 sequences of 8,192 tokens, 8 kv heads of 128: 183 us at 256, 179 at 512,
-// 175 at 1,024; one of 1,000 tokens: 14, 18 and 24 us).
-constexpr int kShort = 1024, kMedium = 16384;
-__host__ __device__ inline int chunk_tokens(int n) { return n <= kShort ? 256 : n <= kMedium ? 512 : kMaxChunk; }
+// 175 at 1,024; one of 1,000 tokens: 14, 18 and 24 us); a sequence of one chunk
+// needs no join (128 of 500 tokens: 65 us at 256, 58 at 512).
+constexpr int kOneChunk = 512, kShort = 1024, kMedium = 16384;
+__host__ __device__ inline int chunk_tokens(int n) {
+  return n <= kOneChunk ? kOneChunk : n <= kShort ? 256 : n <= kMedium ? 512 : kMaxChunk;
+}
 __host__ __device__ inline int chunk_count(int n) {
   const int c = chunk_tokens(n);
   return n <= 0 ? 1 : (n - 1) / c + 1;
