@@ -405,6 +405,7 @@ def det_segmented_scan(x: torch.Tensor, seg_offsets: torch.Tensor, y: torch.Tens
 # operators of language models (include/det_model.h)
 
 _MODEL_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_CACHE_CODES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
 def _model_code(t: torch.Tensor, name: str, codes=_MODEL_CODES) -> int:
@@ -433,12 +434,26 @@ def _unit_stride(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
+def _stream_object(stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _hold(stream, *tensors):
+    """Keeps the memory of a call's inputs until the work enqueued on `stream` has read them, should the caller drop
+    them before."""
+    if stream is not None:
+        s = _stream_object(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A tensor that the work enqueued on `stream` writes: taken from that stream's memory (so no earlier work of
     another stream still uses it), and kept from reuse while the caller's current stream works on it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    s = _stream_object(stream)
     with torch.cuda.stream(s):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
@@ -465,12 +480,13 @@ class TokenLogprobs(NamedTuple):
 def _logit_rows(logits: torch.Tensor):
     """(rows, vocab, elements from one row to the next) of [..., vocab] logits."""
     _on(None, None, "logits", logits, contiguous=False)
-    if logits.dim() < 1:
+    shape = logits.shape
+    if len(shape) < 1:
         raise ValueError("logits must have at least one dimension")
-    vocab = logits.shape[-1]
+    vocab = shape[-1]
     _unit_stride(logits, "logits")
-    if logits.dim() == 2:
-        return logits.shape[0], vocab, logits.stride(0)
+    if len(shape) == 2:
+        return shape[0], vocab, logits.stride(0)
     rows = logits.numel() // vocab if vocab else 0
     if not logits.is_contiguous():
         raise ValueError("logits of other than two dimensions must be contiguous")
@@ -499,10 +515,10 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
             raise ValueError(f"top_k must be at most {MAX_TOP_K} and the vocabulary, got {top_k}")
         top_logprob = _empty((*lead, top_k), torch.float32, dev, stream)
         top_index = _empty((*lead, top_k), torch.int32, dev, stream)
-    rc = lib().det_token_logprobs(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob), _ptr(entropy),
-                                  _ptr(lse), top_k, _ptr(top_logprob), _ptr(top_index), _stream(stream, dev))
-    if rc:
-        raise DetError(rc, "det_token_logprobs")
+    _check(lib().det_token_logprobs(logits.data_ptr(), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob),
+                                    entropy.data_ptr(), lse.data_ptr(), top_k, _ptr(top_logprob), _ptr(top_index),
+                                    _stream(stream, dev)), "det_token_logprobs")
+    _hold(stream, logits, tokens)
     return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
 
 
@@ -534,6 +550,7 @@ def det_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Ten
     _check(lib().det_token_logprobs_backward(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
                                              _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
                                              out_stride, _stream(stream, dev)), "det_token_logprobs_backward")
+    _hold(stream, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
     return out
 
 
@@ -593,9 +610,10 @@ def det_relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_l
         out = _empty((heads, q_len, k_len), dtype or table.dtype, table.device, stream)
     else:
         _on(table.device, dtype, "out", out, (heads, q_len, k_len))
-    _check(lib().det_relative_bias(_ptr(table), table_code, heads, _ptr(bounds), n, int(bidirectional), int(q_len),
-                                   int(k_len), int(q_offset), _ptr(out), _model_code(out, "out"), _stream(stream, table.device)),
-           "det_relative_bias")
+    _check(lib().det_relative_bias(table.data_ptr(), table_code, heads, bounds.data_ptr(), n, bool(bidirectional),
+                                   q_len, k_len, q_offset, out.data_ptr(), _model_code(out, "out"),
+                                   _stream(stream, table.device)), "det_relative_bias")
+    _hold(stream, table, bounds, out)
     return out
 
 
@@ -620,6 +638,7 @@ def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_of
                                             grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset),
                                             _ptr(out), _model_code(out, "dtype"), _ptr(ws), ws.numel(),
                                             _stream(stream, grad.device)), "det_relative_bias_backward")
+    _hold(stream, grad, bounds, workspace)
     return out
 
 
@@ -655,22 +674,25 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     Returns the output, [batch, heads, head_dim] of q's dtype, and the log-sum-exp of the scores, float32 [batch, heads]."""
     _on(None, None, "q", q, contiguous=False)
     dev = q.device
-    code = _model_code(q, "q", {torch.bfloat16: BF16, torch.float16: F16})
+    code = _model_code(q, "q", _CACHE_CODES)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [batch, heads, head_dim] and the caches [pages, page_size, kv_heads, head_dim]")
     batch, heads, dim = q.shape
-    pages, page_size, kv_heads = k_cache.shape[:3]
+    pages, page_size, kv_heads, _ = k_cache.shape
+    q_batch, q_head, q_dim = q.stride()
     if dim not in (64, 128, 256):
         raise ValueError(f"head_dim must be 64, 128 or 256, got {dim}")
     if page_size < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError("page_size must be positive and heads a multiple of kv_heads")
-    _unit_stride(q, "q")
+    if q_dim != 1:
+        raise ValueError("q must be contiguous along its last dimension")
     k_ptr, k_strides = _cache(dev, q.dtype, "k_cache", k_cache, (pages, page_size, kv_heads, dim))
     v_ptr, v_strides = _cache(dev, q.dtype, "v_cache", v_cache, k_cache.shape)
     _on(dev, torch.int32, "block_table", block_table, contiguous=False)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, max_pages]")
     _unit_stride(block_table, "block_table")
+    max_pages = block_table.shape[1]
     _on(dev, torch.int32, "lengths", lengths, (batch,))
     bias_code = n_bounds = 0
     if bias_table is not None:
@@ -681,7 +703,7 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         _on(dev, None, "bias_table", bias_table)
         if bias_table.dim() != 2 or bias_table.shape[1] != heads or bias_table.shape[0] not in (buckets, 2 * buckets):
             raise ValueError(f"bias_table must be [{buckets} or {2 * buckets}, {heads}]")
-    capacity = min(block_table.shape[1] * page_size, (1 << 31) - 2048)
+    capacity = min(max_pages * page_size, (1 << 31) - 2048)
     limit = capacity if max_len is None else min(int(max_len), capacity)
     if limit < 0:
         raise ValueError("max_len must not be negative")
@@ -693,11 +715,12 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     call = lib()
     ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
     _check(call.det_paged_attention(
-        _ptr(q), q.stride(0), q.stride(1), k_ptr, *k_strides, v_ptr, *v_strides, pages, page_size, _ptr(block_table),
-        block_table.stride(0), block_table.shape[1], _ptr(lengths), batch, heads, kv_heads, dim, code,
-        dim ** -0.5 if scale is None else float(scale), _ptr(bias_table), bias_code,
-        _ptr(bias_bounds) if bias_table is not None else None, n_bounds, limit, _ptr(out), _ptr(lse), _ptr(ws),
-        ws.numel(), _stream(stream, dev)), "det_paged_attention")
+        q.data_ptr(), q_batch, q_head, k_ptr, *k_strides, v_ptr, *v_strides, pages, page_size, block_table.data_ptr(),
+        block_table.stride(0), max_pages, lengths.data_ptr(), batch, heads, kv_heads, dim, code,
+        dim ** -0.5 if scale is None else scale, _ptr(bias_table), bias_code,
+        None if bias_table is None else bias_bounds.data_ptr(), n_bounds, limit, out.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream(stream, dev)), "det_paged_attention")
+    _hold(stream, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
     return PagedAttention(out, lse)
 
 
