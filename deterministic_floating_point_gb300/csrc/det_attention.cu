@@ -142,6 +142,15 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 // A warp fetches its tiles itself, kStages - 1 ahead, the keys and the values
 // of a tile as two groups of asynchronous copies.  Where a page holds whole
 // blocks of 16 tokens the block's place is looked up once for the warp.
+//
+// Bound by the reads of keys and values: 32 sequences of 8,192 tokens, 8 kv
+// heads of 128 dims for 32 heads 176 us (90% of the measured copy bandwidth), for 8
+// heads 168 us (94%); of 64 dims 99 us (80%), of 256 dims and 16 sequences 181 us
+// (88%).  With short chunks a CTA's start and end (length, table, first tile
+// and join of the warps, 5 us together against 1.3 us a tile) show:
+// 128 sequences of 500 tokens 56 us (69%), 64 ragged ones of up to 8,191 tokens
+// of 64 dims with the bias 66 us (64%).  Copying whole rows by the bulk engine was
+// slower (a copy of 256 bytes every 20 cycles an SM: 296 us for 32 x 8,192).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
   using L = Tile<D>;
@@ -463,7 +472,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
 }
 
 // The chunks of one head of one sequence joined: warp w of 8 adds the chunks
-// w, w + 8, ..., then the warps are added in order.
+// w, w + 8, ..., then the warps are added in order.  A dependent chain of two
+// reads of L2 and the sum, 2 to 9 us (128 chunks).
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnArgs a) {

@@ -2,12 +2,20 @@
 //
 // A row's statistics are S = sum exp(x - m) and T = sum exp(x - m) (x - m)
 // with m the row's maximum: lse = m + log S, entropy = log S - T / S, the log
-// probability of a token (x[token] - m) - log S.  One CTA takes a row and
-// reads it once.  The order of the additions is fixed by element index: thread
-// t of 512 takes the pairs (2t, 2t + 1), (2t + 1024, 2t + 1025), ... (single
-// elements in f32), keeps its own running maximum and sums relative to it,
-// and the 512 triples are joined by a tree.  So a row's bits depend neither on
-// the other rows nor on its alignment.
+// probability of a token (x[token] - m) - log S.  A row is read once.  The order
+// of the additions is fixed by element index: thread t of 256 takes the 4-byte
+// words t, t + 256, ... of the row (two elements of the 16-bit types), 32 of
+// them to a chunk; its sums over a chunk are relative to its own largest element
+// so far, chunks are added in order within a part of the row, parts in order,
+// and the threads by a tree.  So a row's bits depend neither on the other rows
+// nor on its alignment nor on how many CTAs share it.
+//
+// What bounds it: the bytes in 32 bits (4,096 x 49,152: 118 us, the measured
+// copy bandwidth), in 16 bits nearly as much the instructions, 7.6 an element at
+// 64% of the issue slots (4,096 x 98,304 bf16: 129 to 132 us, 90 to 92%).  Rows that
+// start at an odd element read each word of shared memory twice (4,096 x 100,003
+// bf16: 161 us, 75%).  With alternatives a CTA's row end takes 1 to 5 us more, half of it
+// hidden by the SM's other CTA (20 of them at 98,304: 197 us).
 #include "det_model.cuh"
 
 #include <algorithm>
@@ -512,8 +520,8 @@ struct PartStats {
 static_assert(sizeof(PartStats) <= sizeof(Stream::stage), "it fits the stages");
 
 // Persistent: CTA b takes the rows b, b + gridDim.x, ...; SPLIT: a cluster of a
-// CTA per part takes a row.  A wait for a copy that does not end within kWaitNs
-// gives up: the row's results are NaN then.
+// CTA per part takes a row (1 x 131,072 bf16: 17 us -> 12).  A wait for a copy that
+// does not end within kWaitNs gives up: the row's results are NaN then.
 template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kRowThreads, 2)
 token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, long long row_stride,
@@ -701,7 +709,9 @@ struct GradRow {
   }
 };
 
-// A CTA takes 256 x 4 vectors of 16 bytes of a row, counted from the row's
+// Bound by the bytes: each logit is read and its gradient written once (4,096 x
+// 65,536 bf16 154 us, 1,021 x 100,003 f32 119 us, both the measured copy
+// bandwidth).  A CTA takes 256 x 4 vectors of 16 bytes of a row, counted from the row's
 // first 16-byte boundary (the same one of both rows: SAME_PHASE), and the
 // row's first CTA the elements before it and behind the last vector.  Where
 // the rows' boundaries differ it goes by elements.

@@ -94,7 +94,7 @@ int det_token_logprobs_backward(const void* logits, int64_t rows, int64_t vocab,
  *   bounds  device, num_bounds int32 (NULL when num_bounds is 0)
  *   out     device, heads x q_len x k_len of dtype, contiguous (written); a
  *           table entry is converted to dtype once, to nearest
- * Limits: |q_offset| + q_len + k_len <= 2^30, q_len <= 2^20, num_bounds <=
+ * Limits: |q_offset| + q_len + k_len <= 2^30, q_len < 2^20, num_bounds <=
  * DET_MAX_BOUNDS, heads <= 65,535.
  */
 #define DET_MAX_BOUNDS 2047
