@@ -3,8 +3,8 @@
 //
 // A sequence is cut into chunks whose size depends on its own length alone;
 // a CTA takes the query heads that share one key-value head over one chunk,
-// and a second kernel joins the chunks.  Inside a chunk warp w takes every
-// fourth (of 256 dims every third) tile of 16 tokens with a running maximum (softmax statistics
+// and a second kernel joins the chunks.  Inside a chunk warp w of 4 takes the
+// 16-token tiles w, w + 4, ... with a running maximum (softmax statistics
 // and the output are held in 32 bits), so the order of every addition is
 // fixed by token index and a sequence's bits do not depend on its batch.
 //
@@ -26,9 +26,9 @@ constexpr int kMaxChunk = 1024;  // most tokens of a chunk
 
 // Tokens of a chunk of a sequence of n tokens.  Short chunks let a short
 // sequence use more SMs, long ones spend less on their start and on the join
-// (32 sequences of 8,192 tokens, 8 kv heads of 128: 183 us at 256, 179 at 512,
-// 175 at 1,024; one of 1,000 tokens: 14, 18 and 24 us); a sequence of one chunk
-// needs no join (128 of 500 tokens: 65 us at 256, 58 at 512).
+// (32 sequences of 8,192 tokens, 8 kv heads of 128, as two tiles were kept:
+// 183 us at 256, 179 at 512, 175 at 1,024; one of 1,000 tokens: 14, 18 and 24 us);
+// a sequence of one chunk needs no join (128 of 500 tokens: 65 us at 256, 58 at 512).
 constexpr int kOneChunk = 512, kShort = 1024, kMedium = 16384;
 __host__ __device__ inline int chunk_tokens(int n) {
   return n <= kOneChunk ? kOneChunk : n <= kShort ? 256 : n <= kMedium ? 512 : kMaxChunk;
@@ -45,22 +45,32 @@ inline int most_chunks(int n) {
   return most;
 }
 
-// A warp's tiles of 16 tokens, two of them in shared memory: the one it works
-// on and the next.  What hides the latency of loads and of a tile's chain of
-// products and exponentials is the number of warps on an SM, so tiles are as
-// short as the matrix instructions allow (measured, 32 sequences of 8,192
-// tokens, 8 kv heads: of 64 dims 101 us, three tiles 120, tiles of 32 tokens
-// 139; of 128 dims 182 us, three tiles 209).  Rows lie 16 bytes apart modulo
-// 128, so that eight rows of a matrix load hit 32 banks.
+// A warp's tiles of 16 tokens.  Its shared memory holds the keys of the tile it
+// works on and of the next one, and the values of the one it works on: what
+// hides the latency of loads and of a tile's chain of products and exponentials
+// is the number of warps on an SM, so tiles are as short as the matrix
+// instructions allow and no more is fetched ahead than keeps a warp going (32
+// sequences of 8,192 tokens, 8 kv heads of 128 dims: 172 us; with the next
+// tile's values too, and a CTA fewer on an SM, 177; three whole tiles 209; 128
+// sequences of 500 tokens: 51 and 56 us).  Rows lie 16 bytes apart modulo 128,
+// so that eight rows of a matrix load hit 32 banks.
 template <int D> struct Tile {
-  static constexpr int kWarps = D == 256 ? 3 : 4;   // of a CTA: 2 CTAs of 3 warps, 3 or 6 of 4 fit an SM
+  static constexpr int kWarps = 4;                  // of a CTA
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTokens = 16;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kPitch = kRowBytes + 16;
   static constexpr int kBytes = kTokens * kPitch;   // of the keys, and of the values
-  static constexpr int kStages = 2;
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * 2 * kBytes;
+  static constexpr size_t kWarpBytes = 3 * kBytes;  // keys, keys, values
+  static constexpr size_t kSmem = kWarps * kWarpBytes;
+  // the warps' outputs of 8 x nt heads when they are joined, in rows of floats
+  // 4 apart modulo 32, so that a warp's writes hit 32 banks
+  static constexpr int kOutPitch = D + 4;
+  // CTAs on an SM that registers are kept for, nt tiles of 8 heads in each
+  static constexpr int ctas(int nt) {
+    return D == 64 ? (nt == 1 ? 6 : nt == 2 ? 4 : 3) : D == 128 ? (nt == 1 ? 4 : 3) : 2;
+  }
+  static constexpr size_t out_bytes(int nt) { return (size_t)kWarps * 8 * nt * kOutPitch * sizeof(float); }
 };
 
 struct AttnArgs {
@@ -139,26 +149,24 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 }
 
 // NT tiles of 8 heads per CTA.  Grid: (chunks, kv heads x head tiles, batch).
-// A warp fetches its tiles itself, kStages - 1 ahead, the keys and the values
-// of a tile as two groups of asynchronous copies.  Where a page holds whole
-// blocks of 16 tokens the block's place is looked up once for the warp.
+// A warp fetches its tiles itself, as groups of asynchronous copies.  Where
+// pages hold whole blocks of 16 tokens a block's place is looked up once;
+// otherwise every token's.
 //
 // Bound by the reads of keys and values: 32 sequences of 8,192 tokens, 8 kv
-// heads of 128 dims for 32 heads 176 us (90% of the measured copy bandwidth), for 8
-// heads 168 us (94%); of 64 dims 99 us (80%), of 256 dims and 16 sequences 181 us
-// (88%).  With short chunks a CTA's start and end (length, table, first tile
+// heads of 128 dims for 32 heads 172 us (92% of the measured copy bandwidth), for 8
+// heads 163 us (97%); of 64 dims 98 us (81%), of 256 dims and 16 sequences 175 us
+// (90%).  With short chunks a CTA's start and end (length, table, first tile
 // and join of the warps, 5 us together against 1.3 us a tile) show:
-// 128 sequences of 500 tokens 56 us (69%), 64 ragged ones of up to 8,191 tokens
+// 128 sequences of 500 tokens 51 us (76%), 64 ragged ones of up to 8,191 tokens
 // of 64 dims with the bias 66 us (64%).  Copying whole rows by the bulk engine was
 // slower (a copy of 256 bytes every 20 cycles an SM: 296 us for 32 x 8,192).
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
   using L = Tile<D>;
-  constexpr int S = L::kStages, W = L::kWarps;
+  constexpr int W = L::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int sh_page[kMaxChunk + 1];
-  __shared__ long long sh_place[kMaxChunk / 16][2];   // of a block of 16 tokens: its keys and values; -1: token by token
-  __shared__ unsigned sh_mask[W][S];   // of a tile's tokens: those not skipped
+  __shared__ long long sh_place[kMaxChunk / 16][2];   // of a block of 16 tokens: its keys and values; -1: skipped
   __shared__ float sh_m[W][8 * NT], sh_l[W][8 * NT];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -172,16 +180,21 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
   const int p0 = t0 / a.page_size;
   const int pages = t1 > t0 ? (t1 - 1) / a.page_size - p0 + 1 : 0;
   const int32_t* table = a.table + b * a.table_stride + p0;
-  for (int i = threadIdx.x; i < pages; i += L::kThreads) {
-    const int p = table[i];
-    sh_page[i] = p >= 0 && p < a.num_pages ? p : -1;
-  }
-  for (int i = threadIdx.x; i < (t1 - t0 + 15) / 16; i += L::kThreads) {
-    const int j = t0 + 16 * i, pj = j / a.page_size, slot = j - pj * a.page_size;
-    const int p = table[pj - p0];
-    const bool whole = a.page_size % 16 == 0 && j + 16 <= t1 && p >= 0 && p < a.num_pages;   // t0 is a multiple of 16
-    sh_place[i][0] = whole ? p * a.k_sp + slot * a.k_st : -1;
-    sh_place[i][1] = whole ? p * a.v_sp + slot * a.v_st : -1;
+  int* sh_page = reinterpret_cast<int*>(smem + L::kSmem);   // of the chunk's pages, where blocks are not whole
+  const bool blocks = a.page_size % 16 == 0;                // t0 is a multiple of 16
+  if (blocks) {
+    for (int i = threadIdx.x; i < (t1 - t0 + 15) / 16; i += L::kThreads) {
+      const int j = t0 + 16 * i, pj = j / a.page_size, slot = j - pj * a.page_size;
+      const int p = table[pj - p0];
+      const bool valid = p >= 0 && p < a.num_pages;
+      sh_place[i][0] = valid ? p * a.k_sp + slot * a.k_st : -1;
+      sh_place[i][1] = valid ? p * a.v_sp + slot * a.v_st : -1;
+    }
+  } else {
+    for (int i = threadIdx.x; i < pages; i += L::kThreads) {
+      const int p = table[i];
+      sh_page[i] = p >= 0 && p < a.num_pages ? p : -1;
+    }
   }
 
   // the queries as B operands: column = head (lane / 4), rows = dims
@@ -222,60 +235,50 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
 
   const T* kbase = static_cast<const T*>(a.k) + g * a.k_sh;
   const T* vbase = static_cast<const T*>(a.v) + g * a.v_sh;
-  unsigned char* ring = smem + (size_t)warp * S * 2 * L::kBytes;
+  const unsigned ring = smem_u32(smem + warp * L::kWarpBytes);   // keys, keys, values
   const int tiles = (t1 - t0 + L::kTokens - 1) / L::kTokens;
   const int mine = (tiles - warp + W - 1) / W;   // tiles of this warp
 
   // a lane copies 16 bytes of every (32 / C)-th row
   constexpr int C = D / 8, kRows = 32 / C;
   const int row0 = lane / C, col = lane % C;
-  const T* klane = kbase + row0 * a.k_st + col * 8;
-  const T* vlane = vbase + row0 * a.v_st + col * 8;
-  const unsigned dst_lane = smem_u32(ring) + row0 * L::kPitch + col * 16;
-  auto copy_block = [&](unsigned dst, const T* src, long long stride) {
+  // The rows of the warp's tile `it`, of the keys or the values; a bit for
+  // each token that is not skipped.  Nothing is read for a skipped token: its
+  // row becomes 0, so that 0 * value is 0.
+  auto fetch = [&](int it, int which, unsigned to) -> unsigned {
+    const int tile = it * W + warp, j0 = t0 + 16 * tile;
+    const T* base = (which ? vbase : kbase) + col * 8;
+    const long long st = which ? a.v_st : a.k_st;
+    const unsigned dst = to + row0 * L::kPitch + col * 16;
+    unsigned mask = 0;
+    long long from = 0;   // of the block, or of the lane's token (lane % 16)
+    if (blocks) {
+      from = sh_place[tile][which];
+      mask = from < 0 ? 0u : j0 + 16 <= t1 ? 0xffffu : (1u << (t1 - j0)) - 1;
+      if (mask == 0xffffu) {
+        const T* src = base + from + row0 * st;
 #pragma unroll
-    for (int i = 0; i < 16 / kRows; ++i) cp_async_16(dst + i * kRows * L::kPitch, src + i * (kRows * stride));
-  };
-  // the rows of a block one by one, `from` the place of the lane's token's row
-  auto copy_rows = [&](unsigned dst, const T* base, long long from, unsigned mask) {
+        for (int i = 0; i < 16 / kRows; ++i) cp_async_16(dst + i * kRows * L::kPitch, src + i * (kRows * st));
+        return mask;
+      }
+    } else {
+      const int j = j0 + (lane & 15);
+      int page = -1;
+      if (j < t1) {
+        const int pj = j / a.page_size;
+        page = sh_page[pj - p0];
+        from = page * (which ? a.v_sp : a.k_sp) + (j - pj * a.page_size) * st;
+      }
+      mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+    }
 #pragma unroll
     for (int i = 0; i < 16 / kRows; ++i) {
       const int row = i * kRows + row0;
-      const long long at = __shfl_sync(0xffffffffu, from, row);
-      // nothing is read for a skipped token: 0, so that 0 * value is 0
-      if ((mask >> row) & 1) cp_async_16(dst + i * kRows * L::kPitch, base + at + col * 8);
+      const long long at = blocks ? from + row * st : __shfl_sync(0xffffffffu, from, row);
+      if ((mask >> row) & 1) cp_async_16(dst + i * kRows * L::kPitch, base + at);
       else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * kRows * L::kPitch), "r"(0u) : "memory");
     }
-  };
-  auto fetch = [&](int it) {
-    if (it < mine) {
-      const int stage = it % S, tile = it * W + warp;
-      const unsigned kd = dst_lane + stage * (2 * L::kBytes), vd = kd + L::kBytes;
-      const long long ko = sh_place[tile][0];
-      if (ko >= 0) {
-        if (lane == 0) sh_mask[warp][stage] = 0xffffu;
-        copy_block(kd, klane + ko, a.k_st);
-        cp_async_commit();
-        copy_block(vd, vlane + sh_place[tile][1], a.v_st);
-      } else {
-        const int j = t0 + tile * 16 + (lane & 15);
-        int page = -1, slot = 0;
-        if (j < t1) {
-          const int pj = j / a.page_size;
-          slot = j - pj * a.page_size;
-          page = sh_page[pj - p0];
-        }
-        const unsigned mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-        if (lane == 0) sh_mask[warp][stage] = mask;
-        copy_rows(kd, kbase, page * a.k_sp + slot * a.k_st, mask);
-        cp_async_commit();
-        copy_rows(vd, vbase, page * a.v_sp + slot * a.v_st, mask);
-      }
-      cp_async_commit();
-    } else {
-      cp_async_commit();
-      cp_async_commit();
-    }
+    return mask;
   };
 
   float o[D / 16][NT][4];
@@ -294,13 +297,16 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
       l[nt][j] = 0.0f;
     }
 
-#pragma unroll
-  for (int it = 0; it < S - 1; ++it) fetch(it);
+  unsigned next_mask = mine > 0 ? fetch(0, 0, ring) : 0u;
+  cp_async_commit();
   for (int it = 0; it < mine; ++it) {
-    fetch(it + S - 1);
-    const int stage = it % S;
-    const unsigned ks = smem_u32(ring + (size_t)stage * 2 * L::kBytes), vs = ks + L::kBytes;
-    cp_async_wait<2 * S - 1>();   // this tile's keys
+    const unsigned ks = ring + (it & 1) * L::kBytes, vs = ring + 2 * L::kBytes;
+    const unsigned mask = next_mask >> (lane >> 2);   // of this lane's tokens: bits 0 and 8
+    fetch(it, 1, vs);
+    cp_async_commit();
+    if (it + 1 < mine) next_mask = fetch(it + 1, 0, ring + ((it + 1) & 1) * L::kBytes);
+    cp_async_commit();
+    cp_async_wait<2>();   // this tile's keys
     __syncwarp();
     float s[NT][4] = {};
     {
@@ -320,7 +326,6 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
         for (int j = 0; j < 4; ++j) s[nt][j] += odd[nt][j];
     }
     // scores in units of log 2; masked tokens to -inf
-    const unsigned mask = sh_mask[warp][stage] >> (lane >> 2);
     const int first = t0 + (it * W + warp) * L::kTokens;
     if (a.bias && n - (first + L::kTokens) >= far) {
 #pragma unroll
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
         pl[nt][half] = movmatrix_trans(pack2<T>(p[2 * half] - r.x, p[2 * half + 1] - r.y));
       }
     }
-    cp_async_wait<2 * S - 2>();   // and its values
+    cp_async_wait<1>();   // and its values
     __syncwarp();
     {
       const unsigned row = vs + ((lane & 7) + ((lane >> 4) & 1) * 8) * L::kPitch + (((lane >> 3) & 1) << 4);
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
         }
       }
     }
-    __syncwarp();   // the stage is free
+    __syncwarp();   // its keys and values have been read
   }
   cp_async_wait<0>();
 
@@ -431,9 +436,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreads) attention_chunks_kernel(con
       }
     }
   __syncthreads();
-  constexpr int kPitch = D + 4;   // floats of a row of the joined outputs: the writes below hit 32 banks
-  float* sh_o = reinterpret_cast<float*>(smem);
-  static_assert((size_t)W * 8 * NT * kPitch * 4 <= L::kSmem, "the outputs fit the ring");
+  constexpr int kPitch = L::kOutPitch;
+  float* sh_o = reinterpret_cast<float*>(smem);   // in the place of the tiles
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -536,10 +540,14 @@ int launch_attention(AttnArgs a, int batch, int kv_heads, cudaStream_t s) {
   a.head_tiles = (a.group + 8 * NT - 1) / (8 * NT);
   if ((long long)kv_heads * a.head_tiles > 65535) return DET_ERR_TOO_LARGE;
   const void* kernel = reinterpret_cast<const void*>(&attention_chunks_kernel<T, D, NT>);
-  if (const cudaError_t e = ensure_dyn_smem(kernel, Tile<D>::kSmem)) return cuda_fail(e, "det_paged_attention");
+  // the ids of a chunk's pages are kept where a page is not made of whole blocks
+  const int longest = std::min(a.limit, kMaxChunk);
+  const size_t pages = a.page_size % 16 ? (size_t)(longest / a.page_size + 2) * sizeof(int) : 0;
+  const size_t smem = std::max(Tile<D>::kSmem + pages, Tile<D>::out_bytes(NT));
+  if (const cudaError_t e = ensure_dyn_smem(kernel, smem)) return cuda_fail(e, "det_paged_attention");
   const dim3 grid((unsigned)a.max_chunks, (unsigned)(kv_heads * a.head_tiles), (unsigned)batch);
   launch_begin("det_paged_attention", s);
-  attention_chunks_kernel<T, D, NT><<<grid, Tile<D>::kThreads, Tile<D>::kSmem, s>>>(a);
+  attention_chunks_kernel<T, D, NT><<<grid, Tile<D>::kThreads, smem, s>>>(a);
   launch_end(s);
   if (const int rc = check_launch("det_paged_attention")) return rc;
   if (a.max_chunks == 1) return DET_OK;
