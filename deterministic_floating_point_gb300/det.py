@@ -406,6 +406,7 @@ def det_segmented_scan(x: torch.Tensor, seg_offsets: torch.Tensor, y: torch.Tens
 
 _MODEL_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _CACHE_CODES = {torch.bfloat16: BF16, torch.float16: F16}
+_MOST_TOKENS = (1 << 31) - 2048
 
 
 def _model_code(t: torch.Tensor, name: str, codes=_MODEL_CODES) -> int:
@@ -417,7 +418,7 @@ def _model_code(t: torch.Tensor, name: str, codes=_MODEL_CODES) -> int:
 
 def _on(device, dtype, name: str, t: torch.Tensor, shape=None, contiguous: bool = True) -> torch.Tensor:
     """t, checked to be a tensor of this device, dtype and shape (each unless None)."""
-    if (not t.is_cuda) if device is None else (t.device != device or device.type != "cuda"):
+    if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a CUDA tensor on one device with the others")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -441,11 +442,10 @@ def _stream_object(stream):
 def _hold(stream, *tensors):
     """Keeps the memory of a call's inputs until the work enqueued on `stream` has read them, should the caller drop
     them before."""
-    if stream is not None:
-        s = _stream_object(stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+    s = _stream_object(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -464,6 +464,7 @@ def _model_ws(ws, nbytes, device, stream):
     if ws is None:
         # the allocator's blocks are 512-byte aligned
         return _empty((max(int(nbytes), 256),), torch.uint8, device, stream)
+    _on(device, torch.uint8, "workspace", ws)
     if ws.numel() < nbytes:
         raise DetError(4, "workspace")
     return ws
@@ -502,23 +503,32 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
     int32 of the leading shape, or None for the other results alone.  Results are float32 of the leading shape
     (top_*: with top_k appended; top_index int32)."""
     rows, vocab, stride = _logit_rows(logits)
-    code = _model_code(logits, "logits")
+    code = _MODEL_CODES.get(logits.dtype)
+    if code is None:
+        _model_code(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
+    f32 = torch.float32
+    logprob = token_ptr = logprob_ptr = top_logprob = top_index = top_lp_ptr = top_ix_ptr = None
     if tokens is not None:
         _on(dev, torch.int32, "tokens", tokens, lead)
-    logprob = _empty(lead, torch.float32, dev, stream) if tokens is not None else None
-    entropy = _empty(lead, torch.float32, dev, stream)
-    lse = _empty(lead, torch.float32, dev, stream)
-    top_logprob = top_index = None
+        logprob = _empty(lead, f32, dev, stream)
+        token_ptr, logprob_ptr = tokens.data_ptr(), logprob.data_ptr()
+    entropy = _empty(lead, f32, dev, stream)
+    lse = _empty(lead, f32, dev, stream)
     if top_k:
         if not 0 < top_k <= min(vocab, MAX_TOP_K):
             raise ValueError(f"top_k must be at most {MAX_TOP_K} and the vocabulary, got {top_k}")
-        top_logprob = _empty((*lead, top_k), torch.float32, dev, stream)
-        top_index = _empty((*lead, top_k), torch.int32, dev, stream)
-    _check(lib().det_token_logprobs(logits.data_ptr(), rows, vocab, stride, _ptr(tokens), code, _ptr(logprob),
-                                    entropy.data_ptr(), lse.data_ptr(), top_k, _ptr(top_logprob), _ptr(top_index),
-                                    _stream(stream, dev)), "det_token_logprobs")
-    _hold(stream, logits, tokens)
+        top_shape = (*lead, top_k)
+        top_logprob = _empty(top_shape, f32, dev, stream)
+        top_index = _empty(top_shape, torch.int32, dev, stream)
+        top_lp_ptr, top_ix_ptr = top_logprob.data_ptr(), top_index.data_ptr()
+    rc = lib().det_token_logprobs(logits.data_ptr(), rows, vocab, stride, token_ptr, code, logprob_ptr,
+                                  entropy.data_ptr(), lse.data_ptr(), top_k, top_lp_ptr, top_ix_ptr,
+                                  _stream(stream, dev))
+    if rc:
+        raise DetError(rc, "det_token_logprobs")
+    if stream is not None:
+        _hold(stream, logits, tokens)
     return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
 
 
@@ -550,7 +560,8 @@ def det_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Ten
     _check(lib().det_token_logprobs_backward(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
                                              _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
                                              out_stride, _stream(stream, dev)), "det_token_logprobs_backward")
-    _hold(stream, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
+    if stream is not None:
+        _hold(stream, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
     return out
 
 
@@ -558,8 +569,8 @@ def det_relative_bounds(num_buckets: int, max_distance: int, *, bidirectional: b
                         device="cuda") -> torch.Tensor:
     """The bounds of the usual logarithmic buckets, for det_relative_bias: of the buckets of one direction the first
     half (rounded down) hold one distance each, the others are logarithmic steps up to max_distance, and the
-    last one takes every distance from there.  Computed from the integers alone, so no distance moves between buckets by a
-    rounded logarithm."""
+    last one takes every distance from there.  Computed from the integers alone, so no distance moves between
+    buckets by a rounded logarithm."""
     if num_buckets < 2 or (bidirectional and num_buckets % 2):
         raise ValueError("num_buckets must be at least 2, and even when bidirectional")
     n = num_buckets // 2 if bidirectional else num_buckets
@@ -613,7 +624,8 @@ def det_relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_l
     _check(lib().det_relative_bias(table.data_ptr(), table_code, heads, bounds.data_ptr(), n, bool(bidirectional),
                                    q_len, k_len, q_offset, out.data_ptr(), _model_code(out, "out"),
                                    _stream(stream, table.device)), "det_relative_bias")
-    _hold(stream, table, bounds, out)
+    if stream is not None:
+        _hold(stream, table, bounds, out)
     return out
 
 
@@ -638,20 +650,21 @@ def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_of
                                             grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset),
                                             _ptr(out), _model_code(out, "dtype"), _ptr(ws), ws.numel(),
                                             _stream(stream, grad.device)), "det_relative_bias_backward")
-    _hold(stream, grad, bounds, workspace)
+    if stream is not None:
+        _hold(stream, grad, bounds, workspace)
     return out
 
 
 def _cache(device, dtype, name: str, t: torch.Tensor, shape):
     """(pointer, strides of pages, tokens and heads) of a key or value cache."""
-    _on(device, dtype, name, t, shape, contiguous=False)
+    _on(device, dtype, name, t, shape, False)
     s_page, s_token, s_head, s_dim = t.stride()
     ptr = t.data_ptr()
     if s_dim != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    if (ptr | s_page * 2 | s_token * 2 | s_head * 2) & 15:
+    if (ptr | (s_page | s_token | s_head) * 2) & 15:
         raise ValueError(f"{name} must be 16-byte aligned with strides that are multiples of 8 elements")
-    return ptr, (s_page, s_token, s_head)
+    return ptr, s_page, s_token, s_head
 
 
 class PagedAttention(NamedTuple):
@@ -671,29 +684,35 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     max_pages], lengths int32 [batch].  scale defaults to head_dim ** -0.5.  max_len, a bound on the lengths that
     the host knows, saves launching for the whole table; longer sequences are cut at it.  bias_table
     ([buckets, heads], with bias_bounds as in det_relative_bias) adds the learned relative position bias.
-    Returns the output, [batch, heads, head_dim] of q's dtype, and the log-sum-exp of the scores, float32 [batch, heads]."""
-    _on(None, None, "q", q, contiguous=False)
-    dev = q.device
-    code = _model_code(q, "q", _CACHE_CODES)
-    if q.dim() != 3 or k_cache.dim() != 4:
+    Returns the output, [batch, heads, head_dim] of q's dtype, and the scores' log-sum-exp, float32 [batch, heads]."""
+    dev, dtype = q.device, q.dtype
+    _on(None, None, "q", q, None, False)
+    code = _CACHE_CODES.get(dtype)
+    if code is None:
+        _model_code(q, "q", _CACHE_CODES)
+    cache_shape = k_cache.shape
+    if q.dim() != 3 or len(cache_shape) != 4:
         raise ValueError("q must be [batch, heads, head_dim] and the caches [pages, page_size, kv_heads, head_dim]")
     batch, heads, dim = q.shape
-    pages, page_size, kv_heads, _ = k_cache.shape
+    pages, page_size, kv_heads, cache_dim = cache_shape
     q_batch, q_head, q_dim = q.stride()
-    if dim not in (64, 128, 256):
-        raise ValueError(f"head_dim must be 64, 128 or 256, got {dim}")
+    if dim not in (64, 128, 256) or cache_dim != dim:
+        raise ValueError(f"head_dim must be 64, 128 or 256 and the caches', got {dim} and {cache_dim}")
     if page_size < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError("page_size must be positive and heads a multiple of kv_heads")
     if q_dim != 1:
         raise ValueError("q must be contiguous along its last dimension")
-    k_ptr, k_strides = _cache(dev, q.dtype, "k_cache", k_cache, (pages, page_size, kv_heads, dim))
-    v_ptr, v_strides = _cache(dev, q.dtype, "v_cache", v_cache, k_cache.shape)
-    _on(dev, torch.int32, "block_table", block_table, contiguous=False)
+    k_ptr, k_page, k_token, k_head = _cache(dev, dtype, "k_cache", k_cache, None)
+    v_ptr, v_page, v_token, v_head = _cache(dev, dtype, "v_cache", v_cache, cache_shape)
+    _on(dev, torch.int32, "block_table", block_table, None, False)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, max_pages]")
-    _unit_stride(block_table, "block_table")
     max_pages = block_table.shape[1]
+    table_stride, table_unit = block_table.stride()
+    if table_unit != 1 and max_pages > 1:
+        raise ValueError("block_table must be contiguous along its last dimension")
     _on(dev, torch.int32, "lengths", lengths, (batch,))
+    bias_ptr = bounds_ptr = None
     bias_code = n_bounds = 0
     if bias_table is not None:
         if bias_bounds is None:
@@ -703,24 +722,28 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         _on(dev, None, "bias_table", bias_table)
         if bias_table.dim() != 2 or bias_table.shape[1] != heads or bias_table.shape[0] not in (buckets, 2 * buckets):
             raise ValueError(f"bias_table must be [{buckets} or {2 * buckets}, {heads}]")
-    capacity = min(max_pages * page_size, (1 << 31) - 2048)
-    limit = capacity if max_len is None else min(int(max_len), capacity)
-    if limit < 0:
-        raise ValueError("max_len must not be negative")
+        bias_ptr, bounds_ptr = bias_table.data_ptr(), bias_bounds.data_ptr()
+    limit = min(max_pages * page_size, _MOST_TOKENS)
+    if max_len is not None and max_len < limit:
+        limit = int(max_len)
+        if limit < 0:
+            raise ValueError("max_len must not be negative")
     if out is None:
-        out = _empty((batch, heads, dim), q.dtype, dev, stream)
+        out = _empty((batch, heads, dim), dtype, dev, stream)
     else:
-        _on(dev, q.dtype, "out", out, (batch, heads, dim))
+        _on(dev, dtype, "out", out, (batch, heads, dim))
     lse = _empty((batch, heads), torch.float32, dev, stream)
     call = lib()
     ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
-    _check(call.det_paged_attention(
-        q.data_ptr(), q_batch, q_head, k_ptr, *k_strides, v_ptr, *v_strides, pages, page_size, block_table.data_ptr(),
-        block_table.stride(0), max_pages, lengths.data_ptr(), batch, heads, kv_heads, dim, code,
-        dim ** -0.5 if scale is None else scale, _ptr(bias_table), bias_code,
-        None if bias_table is None else bias_bounds.data_ptr(), n_bounds, limit, out.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(stream, dev)), "det_paged_attention")
-    _hold(stream, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
+    rc = call.det_paged_attention(
+        q.data_ptr(), q_batch, q_head, k_ptr, k_page, k_token, k_head, v_ptr, v_page, v_token, v_head, pages, page_size,
+        block_table.data_ptr(), table_stride, max_pages, lengths.data_ptr(), batch, heads, kv_heads, dim, code,
+        dim ** -0.5 if scale is None else scale, bias_ptr, bias_code, bounds_ptr, n_bounds, limit, out.data_ptr(),
+        lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev))
+    if rc:
+        raise DetError(rc, "det_paged_attention")
+    if stream is not None:
+        _hold(stream, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
     return PagedAttention(out, lse)
 
 
