@@ -426,7 +426,7 @@ bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_
 // threads are added by a tree.
 constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads)
-bias_join_kernel(const float* __restrict__ part, int batch, int q_len, int k_len, Distances dist, int q_offset, int heads,
+bias_join_kernel(const float* part, int batch, int q_len, int k_len, Distances dist, int q_offset, int heads,
                  int buckets, void* __restrict__ grad_table, int table_dtype) {
   __shared__ float sh[kJoinThreads / 32];
   dep_wait();
