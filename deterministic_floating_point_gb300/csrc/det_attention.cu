@@ -52,8 +52,10 @@ inline int most_chunks(int n) {
 // instructions allow and no more is fetched ahead than keeps a warp going (32
 // sequences of 8,192 tokens, 8 kv heads of 128 dims: 172 us; with the next
 // tile's values too, and a CTA fewer on an SM, 177; three whole tiles 209; 128
-// sequences of 500 tokens: 51 and 56 us).  Rows lie 16 bytes apart modulo 128,
-// so that eight rows of a matrix load hit 32 banks.
+// sequences of 500 tokens: 51 and 56 us).  With 64 dims and up to 8 heads the
+// next tile's values cost no CTA: they are kept too (one sequence of 131,072
+// tokens 58 us, without them 63; 128 of 512: 31 and 33).  Rows lie 16 bytes apart
+// modulo 128, so that eight rows of a matrix load hit 32 banks.
 template <int D> struct Tile {
   static constexpr int kWarps = 4;                  // of a CTA
   static constexpr int kThreads = 32 * kWarps;
@@ -61,12 +63,14 @@ template <int D> struct Tile {
   static constexpr int kRowBytes = D * 2;
   static constexpr int kPitch = kRowBytes + 16;
   static constexpr int kBytes = kTokens * kPitch;   // of the keys, and of the values
-  static constexpr size_t kWarpBytes = 3 * kBytes;  // keys, keys, values
-  static constexpr size_t kSmem = kWarps * kWarpBytes;
+  // nt tiles of 8 heads: tiles whose values are kept, bytes of a warp and of a CTA
+  __host__ __device__ static constexpr int values(int nt) { return D == 64 && nt == 1 ? 2 : 1; }
+  __host__ __device__ static constexpr size_t warp_bytes(int nt) { return (2 + values(nt)) * kBytes; }
+  __host__ __device__ static constexpr size_t smem_bytes(int nt) { return kWarps * warp_bytes(nt); }
   // the warps' outputs of 8 x nt heads when they are joined, in rows of floats
   // 4 apart modulo 32, so that a warp's writes hit 32 banks
   static constexpr int kOutPitch = D + 4;
-  // CTAs on an SM that registers are kept for, nt tiles of 8 heads in each
+  // CTAs on an SM that registers are kept for
   static constexpr int ctas(int nt) {
     return D == 64 ? (nt == 1 ? 6 : nt == 2 ? 4 : 3) : D == 128 ? (nt == 1 ? 4 : 3) : 2;
   }
@@ -142,7 +146,7 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
   int lo = 0, hi = count;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(bounds + mid) <= n) lo = mid + 1;
+    if (bounds[mid] <= n) lo = mid + 1;
     else hi = mid;
   }
   return lo;
@@ -153,18 +157,21 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 // pages hold whole blocks of 16 tokens a block's place is looked up once;
 // otherwise every token's.
 //
-// Bound by the reads of keys and values: 32 sequences of 8,192 tokens, 8 kv
-// heads of 128 dims for 32 heads 172 us (92% of the measured copy bandwidth), for 8
-// heads 163 us (97%); of 64 dims 98 us (81%), of 256 dims and 16 sequences 175 us
-// (90%).  With short chunks a CTA's start and end (length, table, first tile
-// and join of the warps, 5 us together against 1.3 us a tile) show:
-// 128 sequences of 500 tokens 51 us (76%), 64 ragged ones of up to 8,191 tokens
-// of 64 dims with the bias 66 us (64%).  Copying whole rows by the bulk engine was
+// Bound by the reads of keys and values (both kernels; fraction of the measured
+// copy bandwidth): 32 sequences of 8,192 tokens, 8 kv heads of 128 dims for 32
+// heads 171 us (92%), for 8 heads 167 us (95%); of 64 dims 95 us (83%), of 256 dims
+// and 16 sequences 175 us (90%).  About 10 us of a call are its own: the CTAs'
+// first tiles, the last ones, which do not fill the SMs, and the join (of 64 dims
+// 128 sequences 345 us, 92%).  With short chunks a CTA's start and end (length,
+// page, first tile and join of the warps, 4 us together against 1.3 us a tile) show:
+// 128 sequences of 500 tokens 48 us (80%), 64 ragged ones of up to 8,191 tokens
+// of 64 dims with the bias 59 us (72%).  Copying whole rows by the bulk engine was
 // slower (a copy of 256 bytes every 20 cycles an SM: 296 us for 32 x 8,192).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
   using L = Tile<D>;
-  constexpr int W = L::kWarps;
+  constexpr int W = L::kWarps, kValues = L::values(NT);
+  constexpr size_t kWarpBytes = L::warp_bytes(NT), kSmem = L::smem_bytes(NT);
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long sh_place[kMaxChunk / 16][2];   // of a block of 16 tokens: its keys and values; -1: skipped
   __shared__ float sh_m[W][8 * NT], sh_l[W][8 * NT];
@@ -172,70 +179,70 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x, b = blockIdx.z;
   const int g = blockIdx.y / a.head_tiles, h0 = (blockIdx.y % a.head_tiles) * 8 * NT;   // first head in the group
-  const int n = min(max(a.lengths[b], 0), a.limit);
+  const bool blocks = a.page_size % 16 == 0;   // chunks begin at multiples of 16
+  const int32_t* table = a.table + b * a.table_stride;
+  dep_wait();     // launched early: all loads come after, and none is a read-only one, which need not
+  dep_launch();   // the join's CTAs come as this kernel's run out
+  // A warp looks up its own blocks, a lane one.  The length, the queries and
+  // the page, which depends on the length through the chunk's size, are read
+  // at once: the page for the size that the longest sequence would have, and
+  // again where that was wrong (never in the first chunk).
+  static_assert(kMaxChunk / 16 <= 32 * W, "a lane places one block");
+  const int block = warp + W * lane;
+  const int guess = chunk * chunk_tokens(a.limit) + 16 * block;
+  const int length = a.lengths[b];
+  int page = -1;
+  if (blocks && lane < kMaxChunk / 16 / W && guess < a.limit) page = table[guess / a.page_size];
+
+  // the queries as B operands: column = head (lane / 4), rows = dims
+  unsigned qf[D / 16][NT][2];
+  const bool words = ((reinterpret_cast<uintptr_t>(a.q) | (a.q_sb | a.q_sh) * 2) & 3) == 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int h = h0 + nt * 8 + lane / 4;
+    const T* q = static_cast<const T*>(a.q) + b * a.q_sb + (long long)(g * a.group + h) * a.q_sh + 2 * (lane & 3);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        unsigned w = 0;
+        if (h < a.group) {
+          const unsigned short* p = reinterpret_cast<const unsigned short*>(q + ks * 16 + j * 8);
+          w = words ? *reinterpret_cast<const unsigned*>(p) : (unsigned)p[0] | ((unsigned)p[1] << 16);
+        }
+        qf[ks][nt][j] = w;
+      }
+  }
+
+  const int n = min(max(length, 0), a.limit);
   const int chunks = chunk_count(n);
   if (chunk >= chunks) return;
   const int size = chunk_tokens(n);
   const int t0 = chunk * size, t1 = min(n, t0 + size);
   const int p0 = t0 / a.page_size;
-  const int pages = t1 > t0 ? (t1 - 1) / a.page_size - p0 + 1 : 0;
-  const int32_t* table = a.table + b * a.table_stride + p0;
-  int* sh_page = reinterpret_cast<int*>(smem + L::kSmem);   // of the chunk's pages, where blocks are not whole
-  const bool blocks = a.page_size % 16 == 0;                // t0 is a multiple of 16
+  int* sh_page = reinterpret_cast<int*>(smem + kSmem);   // of the chunk's pages, where blocks are not whole
   if (blocks) {
-    for (int i = threadIdx.x; i < (t1 - t0 + 15) / 16; i += L::kThreads) {
-      const int j = t0 + 16 * i, pj = j / a.page_size, slot = j - pj * a.page_size;
-      const int p = table[pj - p0];
-      const bool valid = p >= 0 && p < a.num_pages;
-      sh_place[i][0] = valid ? p * a.k_sp + slot * a.k_st : -1;
-      sh_place[i][1] = valid ? p * a.v_sp + slot * a.v_st : -1;
+    const int j = t0 + 16 * block;
+    if (j < t1) {
+      const int pj = j / a.page_size, slot = j - pj * a.page_size;
+      if (j != guess) page = table[pj];
+      const bool valid = page >= 0 && page < a.num_pages;
+      sh_place[block][0] = valid ? page * a.k_sp + slot * a.k_st : -1;
+      sh_place[block][1] = valid ? page * a.v_sp + slot * a.v_st : -1;
     }
+    __syncwarp();
   } else {
+    const int pages = t1 > t0 ? (t1 - 1) / a.page_size - p0 + 1 : 0;
     for (int i = threadIdx.x; i < pages; i += L::kThreads) {
-      const int p = table[i];
+      const int p = table[p0 + i];
       sh_page[i] = p >= 0 && p < a.num_pages ? p : -1;
     }
+    __syncthreads();
   }
-
-  // the queries as B operands: column = head (lane / 4), rows = dims
-  unsigned qf[D / 16][NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int h = h0 + nt * 8 + lane / 4;
-    const T* q = static_cast<const T*>(a.q) + b * a.q_sb + (long long)(g * a.group + h) * a.q_sh;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int d = ks * 16 + j * 8 + 2 * (lane & 3);
-        unsigned w = 0;
-        if (h < a.group) {
-          const unsigned short* p = reinterpret_cast<const unsigned short*>(q + d);
-          w = (unsigned)__ldg(p) | ((unsigned)__ldg(p + 1) << 16);
-        }
-        qf[ks][nt][j] = w;
-      }
-  }
-  // with a bias: the distance from which on the last bucket holds, and its values
-  int far = 0;
-  float far_bias[NT][2];
-  if (a.bias) {
-    far = a.num_bounds > 0 ? __ldg(a.bounds + a.num_bounds - 1) : 0;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
-        far_bias[nt][j] =
-            h < a.group ? kLog2e * load_as_f32(a.bias, (long long)a.num_bounds * a.heads + g * a.group + h, a.bias_dtype)
-                        : 0.0f;
-      }
-  }
-  __syncthreads();
 
   const T* kbase = static_cast<const T*>(a.k) + g * a.k_sh;
   const T* vbase = static_cast<const T*>(a.v) + g * a.v_sh;
-  const unsigned ring = smem_u32(smem + warp * L::kWarpBytes);   // keys, keys, values
+  const unsigned ring = smem_u32(smem + warp * kWarpBytes);   // keys, keys, values
   const int tiles = (t1 - t0 + L::kTokens - 1) / L::kTokens;
   const int mine = (tiles - warp + W - 1) / W;   // tiles of this warp
 
@@ -299,14 +306,38 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 
   unsigned next_mask = mine > 0 ? fetch(0, 0, ring) : 0u;
   cp_async_commit();
+  if (kValues == 2 && mine > 0) fetch(0, 1, ring + 2 * L::kBytes);
+  if (kValues == 2) cp_async_commit();
+  // with a bias: the distance from which on the last bucket holds, and its values
+  int far = 0;
+  float far_bias[NT][2];
+  if (a.bias) {
+    far = a.num_bounds > 0 ? a.bounds[a.num_bounds - 1] : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
+        far_bias[nt][j] =
+            h < a.group ? kLog2e * load_as_f32(a.bias, (long long)a.num_bounds * a.heads + g * a.group + h, a.bias_dtype)
+                        : 0.0f;
+      }
+  }
   for (int it = 0; it < mine; ++it) {
-    const unsigned ks = ring + (it & 1) * L::kBytes, vs = ring + 2 * L::kBytes;
+    const unsigned ks = ring + (it & 1) * L::kBytes;
+    const unsigned vs = ring + (2 + (it & (kValues - 1))) * L::kBytes;
     const unsigned mask = next_mask >> (lane >> 2);   // of this lane's tokens: bits 0 and 8
-    fetch(it, 1, vs);
-    cp_async_commit();
+    if (kValues == 1) {
+      fetch(it, 1, vs);
+      cp_async_commit();
+    }
     if (it + 1 < mine) next_mask = fetch(it + 1, 0, ring + ((it + 1) & 1) * L::kBytes);
     cp_async_commit();
-    cp_async_wait<2>();   // this tile's keys
+    if (kValues == 2) {
+      if (it + 1 < mine) fetch(it + 1, 1, ring + (2 + ((it + 1) & 1)) * L::kBytes);
+      cp_async_commit();
+    }
+    cp_async_wait<1 + kValues>();   // this tile's keys
     __syncwarp();
     float s[NT][4] = {};
     {
@@ -404,7 +435,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
         pl[nt][half] = movmatrix_trans(pack2<T>(p[2 * half] - r.x, p[2 * half + 1] - r.y));
       }
     }
-    cp_async_wait<1>();   // and its values
+    cp_async_wait<kValues>();   // and its values
     __syncwarp();
     {
       const unsigned row = vs + ((lane & 7) + ((lane >> 4) & 1) * 8) * L::kPitch + (((lane >> 3) & 1) << 4);
@@ -475,36 +506,75 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
   }
 }
 
-// The chunks of one head of one sequence joined: warp w of 8 adds the chunks
-// w, w + 8, ..., then the warps are added in order.  A dependent chain of two
-// reads of L2 and the sum, 2 to 9 us (128 chunks).
+// The chunks of the heads of one sequence joined, in the order of the chunks:
+// of a few chunks a warp joins a head (a CTA 8 heads, and CTAs beyond the heads
+// have nothing to do); of more a CTA joins one, warp w of 8 the chunks w, w + 8,
+// ..., and the warps are added in order.  Its CTAs are on the SMs before the
+// first kernel ends.  A dependent chain of reads of L2 and the sum; what a CTA a
+// head costs is their number (256 sequences of up to 2,000 tokens, 32 heads of 64
+// dims, both kernels: 69 us, with a warp a head 58; 8 of 8,192, 128 dims: 49 and 50).
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int E = D / 32;
+  constexpr int kAhead = 8;                      // chunks in flight
+  constexpr int kWarpJoin = D <= 128 ? 16 : 8;   // most chunks that a warp joins
   __shared__ float sh_top[kJoinWarps], sh_sum[kJoinWarps];
   __shared__ float sh_o[kJoinWarps][D];
-  dep_wait();
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the first kernel had waited for all before it when it let this one start
   const int chunks = chunk_count(min(max(a.lengths[b], 0), a.limit));
-  if (chunks == 1) return;   // already in place
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool few = chunks <= kWarpJoin;
+  const bool idle = chunks == 1 || (few && blockIdx.x * kJoinWarps >= a.heads);   // 1: already in place
+  if (idle && (blockIdx.x | blockIdx.y)) return;
+  dep_wait();   // in one CTA at least, so that this kernel does not end before the first
+  dep_launch();
+  if (idle) return;
+  const int h = few ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const long long bh = (long long)b * a.heads + h;
   const float2* ml = a.part_ml + bh * a.max_chunks;
   const float* part = a.part + bh * a.max_chunks * D + lane;
-  float top = kNegInf;
-  for (int c = threadIdx.x; c < chunks; c += 32 * kJoinWarps) top = fmaxf(top, ml[c].x);
-  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (lane == 0) sh_top[warp] = top;
-  __syncthreads();
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
-  float v[E], sum = 0.0f;
+  float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.0f;
-  constexpr int kAhead = 8;   // chunks in flight
-  for (int c0 = warp; c0 < chunks; c0 += kAhead * kJoinWarps) {
-    float2 x[kAhead];
-    float y[kAhead][E];
+  float top = kNegInf, sum = 0.0f;
+
+  if (few) {
+    if (h >= a.heads) return;
+    const float2 x = lane < chunks ? ml[lane] : make_float2(kNegInf, 0.0f);   // a lane's chunk
+    float f = 0.0f;
+#pragma unroll
+    for (int c0 = 0; c0 < kWarpJoin; c0 += kAhead) {
+      if (c0 >= chunks) break;
+      float y[kAhead][E];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[k][e] = c0 + k < chunks ? part[(c0 + k) * D + e * 32] : 0.0f;
+      if (c0 == 0) {
+        top = x.x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        f = x.x == kNegInf ? 1.0f : exp2_approx(x.x - top);   // a chunk without a score adds 0
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, c0 + k);
+        sum = fmaf(__shfl_sync(0xffffffffu, x.y, c0 + k), fk, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf(y[k][e], fk, v[e]);
+      }
+    }
+    const bool none = top == kNegInf && sum == 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) static_cast<T*>(a.out)[bh * D + e * 32 + lane] = from_f32<T>(none ? 0.0f : v[e] / sum);
+    if (a.lse && lane == 0) a.lse[bh] = none ? kNegInf : (top + log2f(sum)) * (1.0f / kLog2e);
+    return;
+  }
+
+  float2 x[kAhead];
+  float y[kAhead][E];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int c = c0 + k * kJoinWarps;
@@ -512,13 +582,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
 #pragma unroll
       for (int e = 0; e < E; ++e) y[k][e] = c < chunks ? part[(long long)c * D + e * 32] : 0.0f;
     }
+  };
+  load(warp);
+  for (int c = threadIdx.x; c < chunks; c += 32 * kJoinWarps) top = fmaxf(top, ml[c].x);
+  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) sh_top[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
+  for (int c0 = warp;;) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float f = x[k].x == kNegInf ? 1.0f : exp2_approx(x[k].x - top);   // a chunk without a score adds 0
+      const float f = x[k].x == kNegInf ? 1.0f : exp2_approx(x[k].x - top);
       sum = fmaf(x[k].y, f, sum);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = fmaf(y[k][e], f, v[e]);
     }
+    c0 += kAhead * kJoinWarps;
+    if (c0 >= chunks) break;
+    load(c0);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = v[e];
@@ -543,13 +624,13 @@ int launch_attention(AttnArgs a, int batch, int kv_heads, cudaStream_t s) {
   // the ids of a chunk's pages are kept where a page is not made of whole blocks
   const int longest = std::min(a.limit, kMaxChunk);
   const size_t pages = a.page_size % 16 ? (size_t)(longest / a.page_size + 2) * sizeof(int) : 0;
-  const size_t smem = std::max(Tile<D>::kSmem + pages, Tile<D>::out_bytes(NT));
+  const size_t smem = std::max(Tile<D>::smem_bytes(NT) + pages, Tile<D>::out_bytes(NT));
   if (const cudaError_t e = ensure_dyn_smem(kernel, smem)) return cuda_fail(e, "det_paged_attention");
   const dim3 grid((unsigned)a.max_chunks, (unsigned)(kv_heads * a.head_tiles), (unsigned)batch);
   launch_begin("det_paged_attention", s);
-  attention_chunks_kernel<T, D, NT><<<grid, Tile<D>::kThreads, smem, s>>>(a);
+  const cudaError_t main = launch_dep(attention_chunks_kernel<T, D, NT>, grid, dim3(Tile<D>::kThreads), smem, s, a);
   launch_end(s);
-  if (const int rc = check_launch("det_paged_attention")) return rc;
+  if (main != cudaSuccess) return cuda_fail(main, "det_paged_attention");
   if (a.max_chunks == 1) return DET_OK;
   launch_begin("det_paged_attention_join", s);
   const cudaError_t e = launch_dep(attention_join_kernel<T, D>, dim3((unsigned)a.heads, (unsigned)batch),

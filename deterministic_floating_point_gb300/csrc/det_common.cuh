@@ -261,10 +261,14 @@ __device__ __forceinline__ double ld_dsmem(const double* local, unsigned rank) {
 // Programmatic dependent launch.  A kernel launched with launch_dep() may be
 // launched while the previous kernel of the stream is still running; it
 // calls dep_wait() before any global memory access, which returns once that
-// kernel has completed and its writes are visible.  What overlaps is the
+// kernel has completed and its writes are visible (to ordinary loads: a
+// read-only one may be moved before the wait).  What overlaps is the
 // launch itself (the CTAs are already resident when the wait returns), not
 // the work.  For a kernel launched the ordinary way dep_wait() is a no-op.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream, if it was launched with launch_dep(), be
+// launched once every CTA of this one has come here (or has ended).
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Host-side helpers -----------------------------------------------------------
 inline bool valid_block_threads(int bt) {

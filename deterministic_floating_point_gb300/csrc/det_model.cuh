@@ -49,9 +49,9 @@ __device__ __forceinline__ float key_value(unsigned k) {
 
 // The value at p of one of the three types.
 __device__ __forceinline__ float load_as_f32(const void* p, long long i, int dtype) {
-  if (dtype == DET_F32) return __ldg(static_cast<const float*>(p) + i);
-  if (dtype == DET_BF16) return to_f32(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
-  return to_f32(__ldg(static_cast<const __half*>(p) + i));
+  if (dtype == DET_F32) return static_cast<const float*>(p)[i];
+  if (dtype == DET_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+  return to_f32(static_cast<const __half*>(p)[i]);
 }
 __device__ __forceinline__ void store_from_f32(void* p, long long i, float v, int dtype) {
   if (dtype == DET_F32) static_cast<float*>(p)[i] = v;
