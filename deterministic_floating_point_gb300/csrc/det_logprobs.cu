@@ -100,15 +100,15 @@ __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, un
 template <typename T>
 __device__ __forceinline__ unsigned load_word(const T* row, long long w, long long vocab, bool words_aligned) {
   if constexpr (Word<T>::N == 1) {
-    return w < vocab ? __float_as_uint(__ldg(row + w)) : Word<T>::kMasked;
+    return w < vocab ? __float_as_uint(row[w]) : Word<T>::kMasked;
   } else {
     const long long e = 2 * w;
     const unsigned short* p = reinterpret_cast<const unsigned short*>(row);
     if (e + 1 < vocab) {
-      if (words_aligned) return __ldg(reinterpret_cast<const unsigned*>(p + e));
-      return (unsigned)__ldg(p + e) | ((unsigned)__ldg(p + e + 1) << 16);
+      if (words_aligned) return *reinterpret_cast<const unsigned*>(p + e);
+      return (unsigned)p[e] | ((unsigned)p[e + 1] << 16);
     }
-    if (e < vocab) return (unsigned)__ldg(p + e) | (Word<T>::kMasked & 0xffff0000u);
+    if (e < vocab) return (unsigned)p[e] | (Word<T>::kMasked & 0xffff0000u);
     return Word<T>::kMasked;
   }
 }
@@ -524,8 +524,8 @@ static_assert(sizeof(PartStats) <= sizeof(Stream::stage), "it fits the stages");
 // does not end within kWaitNs gives up: the row's results are NaN then.
 template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kRowThreads, 2)
-token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, long long row_stride,
-                      const int32_t* __restrict__ tokens, int top_k, RowOut out) {
+token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_stride, const int32_t* tokens, int top_k,
+                      RowOut out) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   Stream& stream = *reinterpret_cast<Stream*>(dynamic);
   __shared__ RowEnd end;
@@ -541,6 +541,8 @@ token_logprobs_kernel(const T* __restrict__ logits, long long rows, int vocab, l
       mbar_init(&stream.empty[i], kRowWarps);
     }
   __syncthreads();
+  dep_wait();   // launched early: all loads come after, and none is a read-only one, which need not
+  dep_launch();
   // the next chunk to fetch, its stage and how often the stage was filled
   long long next_row = row0;
   int next_chunk = c0, next_stage = 0, next_round = 0;
@@ -807,12 +809,14 @@ int launch_logprobs(const void* logits, long long rows, int vocab, long long str
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = sizeof(Stream);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)parts;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split ? 1 : 0;
+  cfg.numAttrs = split ? 2 : 1;
   launch_begin("det_token_logprobs", s);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(logits), rows, vocab, stride, tokens,
                                            top_k, out);
