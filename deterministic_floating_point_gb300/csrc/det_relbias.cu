@@ -25,7 +25,7 @@ struct Distances {
     int lo = 0, hi = num_bounds;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(bounds + mid) <= n) lo = mid + 1;
+      if (bounds[mid] <= n) lo = mid + 1;
       else hi = mid;
     }
     return lo;
@@ -38,8 +38,8 @@ struct Distances {
   __device__ __forceinline__ void interval(int k, int from, int to, int& lo, int& hi) const {
     const bool after = k > num_bounds;   // keys after the query (bidirectional)
     const int b = after ? k - num_bounds - 1 : k;
-    const int near = b > 0 ? max(__ldg(bounds + b - 1), 0) : 0;                  // least |distance|
-    const int far = b < num_bounds ? __ldg(bounds + b) : 0x7fffffff;   // first |distance| beyond
+    const int near = b > 0 ? max(bounds[b - 1], 0) : 0;                  // least |distance|
+    const int far = b < num_bounds ? bounds[b] : 0x7fffffff;   // first |distance| beyond
     if (far <= near) {
       lo = hi = from;
       return;
@@ -60,9 +60,11 @@ struct Distances {
 constexpr int kDirectRows = 8;
 template <typename T>
 __global__ void __launch_bounds__(256)
-bias_direct_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
+bias_direct_kernel(const void* table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
                    T* __restrict__ out) {
   const int j = blockIdx.x * blockDim.x + threadIdx.x, q = blockIdx.y, h = blockIdx.z;
+  dep_wait();   // launched early: all loads come after, and none is a read-only one, which need not
+  dep_launch();
   if (j >= k_len) return;
   const int k = dist.bucket(j - q + (q_len - 1) + dist.first);
   out[((long long)h * q_len + q) * k_len + j] = from_f32<T>(load_as_f32(table, (long long)k * heads + h, table_dtype));
@@ -103,7 +105,7 @@ template <> struct Out16<__half> {
 
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(BiasTile<T, ALIGNED>::kThreads)
-bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
+bias_strip_kernel(const void* table, int table_dtype, int heads, Distances dist, int q_len, int k_len,
                   T* __restrict__ out) {
   constexpr int E = 4 / sizeof(T);    // elements of a word
   constexpr int U = 16 / sizeof(T);   // elements of a unit
@@ -111,6 +113,8 @@ bias_strip_kernel(const void* __restrict__ table, int table_dtype, int heads, Di
   constexpr int kStrip = U * kBiasThreads + kBiasRows + 2 * U;
   __shared__ unsigned strip[kStrip + kStrip / U + 1];
   __shared__ float value[kStrip + 1];
+  dep_wait();
+  dep_launch();
   const int h = blockIdx.z, i0 = blockIdx.y * kBiasRows, c0 = blockIdx.x * kBiasThreads;
   const int rows = min(kBiasRows, q_len - i0);
   // strip[u] holds diagonal u + d0: key - query from U (c0 - 1) - (i0 + kBiasRows - 1) up
@@ -231,7 +235,7 @@ template <typename T> struct Eight {   // 8 neighbouring elements as 32-bit word
 
 __device__ __forceinline__ uint4 load_16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -244,7 +248,7 @@ template <typename T, bool ALIGNED> __device__ __forceinline__ Eight<T> load_blo
   for (int i = 0; i < Eight<T>::W; i += 4) {
     // (unaligned in 32 bits a sector is often halved between two of the loads:
     // kept in L1; 3 x 12 x 509 x 1531: 40 -> 29 us)
-    const uint4 v = sizeof(T) == 4 && !ALIGNED ? __ldg(reinterpret_cast<const uint4*>(at) + i / 4)
+    const uint4 v = sizeof(T) == 4 && !ALIGNED ? reinterpret_cast<const uint4*>(at)[i / 4]
                                                : load_16(reinterpret_cast<const void*>(at + 4 * i));
     e.w[i] = v.x, e.w[i + 1] = v.y, e.w[i + 2] = v.z, e.w[i + 3] = v.w;
   }
@@ -288,8 +292,8 @@ __device__ __forceinline__ Eight<T> load_singly(const T* row, int j, int k_len) 
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     if (j + x < 0 || j + x >= k_len) continue;
-    if constexpr (sizeof(T) == 4) e.w[x] = __float_as_uint(__ldg(row + j + x));
-    else e.w[x >> 1] |= (unsigned)__ldg(reinterpret_cast<const unsigned short*>(row) + j + x) << (16 * (x & 1));
+    if constexpr (sizeof(T) == 4) e.w[x] = __float_as_uint(row[j + x]);
+    else e.w[x >> 1] |= (unsigned)reinterpret_cast<const unsigned short*>(row)[j + x] << (16 * (x & 1));
   }
   return e;
 }
@@ -298,9 +302,10 @@ __device__ __forceinline__ Eight<T> load_singly(const T* row, int j, int k_len) 
 // that the tile's diagonals reach.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(32 * kTileWarps, ALIGNED ? 4 : sizeof(T) == 4 ? 3 : 5)
-bias_tiles_kernel(const T* __restrict__ grad, GradView g, Distances dist, int q_offset, int buckets,
-                  float* __restrict__ part) {
+bias_tiles_kernel(const T* grad, GradView g, Distances dist, int q_offset, int buckets, float* part) {
   __shared__ float sh[kTileWarps][kTileDiags];
+  dep_wait();
+  dep_launch();
   const TileGrid tiles(g.q_len, g.k_len);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_matrix = tiles.per_matrix(), per_head = per_matrix * g.batch;   // below 2^31: the launch checks
@@ -430,6 +435,7 @@ bias_join_kernel(const float* part, int batch, int q_len, int k_len, Distances d
                  int buckets, void* __restrict__ grad_table, int table_dtype) {
   __shared__ float sh[kJoinThreads / 32];
   dep_wait();
+  dep_launch();
   const TileGrid tiles(q_len, k_len);
   const int k = blockIdx.x, h = blockIdx.y, rows = tiles.row_blocks * batch;
   const float* p = part + ((long long)h * buckets + k) * rows * tiles.strips;
@@ -476,10 +482,12 @@ inline int64_t tiles_of_head(int64_t batch, int64_t q_len, int64_t k_len) {
 template <typename T>
 int launch_bias(const void* table, int table_dtype, int heads, const Distances& dist, int q_len, int k_len, void* out,
                 cudaStream_t s) {
+  cudaError_t e;
   if (q_len <= kDirectRows) {
     const dim3 grid((unsigned)((k_len + 255) / 256), (unsigned)q_len, (unsigned)heads);
     launch_begin("det_relative_bias", s);
-    bias_direct_kernel<T><<<grid, 256, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len, static_cast<T*>(out));
+    e = launch_dep(bias_direct_kernel<T>, grid, dim3(256), 0, s, table, table_dtype, heads, dist, q_len, k_len,
+                   static_cast<T*>(out));
   } else {
     // a row has units from the one before its first boundary up
     const int unit = 16 / sizeof(T), units = (k_len + unit - 1) / unit + 1;
@@ -489,25 +497,21 @@ int launch_bias(const void* table, int table_dtype, int heads, const Distances& 
     const dim3 grid((unsigned)((units + threads - 1) / threads), (unsigned)((q_len + rows - 1) / rows), (unsigned)heads);
     if (grid.y > 65535) return DET_ERR_TOO_LARGE;
     launch_begin("det_relative_bias", s);
-    if (aligned)
-      bias_strip_kernel<T, true><<<grid, threads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
-                                                               static_cast<T*>(out));
-    else
-      bias_strip_kernel<T, false><<<grid, threads, 0, s>>>(table, table_dtype, heads, dist, q_len, k_len,
-                                                                static_cast<T*>(out));
+    e = launch_dep(aligned ? bias_strip_kernel<T, true> : bias_strip_kernel<T, false>, grid, dim3(threads), 0, s, table,
+                   table_dtype, heads, dist, q_len, k_len, static_cast<T*>(out));
   }
   launch_end(s);
-  return check_launch("det_relative_bias");
+  return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_relative_bias");
 }
 
 template <typename T, bool ALIGNED>
 int launch_tiles(const void* grad, const GradView& g, const Distances& dist, int q_offset, int buckets,
                  float* part, dim3 grid, cudaStream_t s) {
   launch_begin("det_relative_bias_tiles", s);
-  bias_tiles_kernel<T, ALIGNED><<<grid, 32 * kTileWarps, 0, s>>>(static_cast<const T*>(grad), g, dist, q_offset,
-                                                                 buckets, part);
+  const cudaError_t e = launch_dep(bias_tiles_kernel<T, ALIGNED>, grid, dim3(32 * kTileWarps), 0, s,
+                                   static_cast<const T*>(grad), g, dist, q_offset, buckets, part);
   launch_end(s);
-  return check_launch("det_relative_bias_tiles");
+  return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_relative_bias_tiles");
 }
 
 template <typename T>
