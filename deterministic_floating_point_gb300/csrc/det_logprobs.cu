@@ -29,6 +29,7 @@ constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kWords = 32;      // 4-byte words of a thread's chunk
 constexpr int kPartWords = 4;   // a row's last chunk goes by this many
 constexpr int kBest = 6;         // most threads of a warp that the bound for the alternatives is drawn from
+constexpr int kMaxJobs = 128;    // reads for a row's alternatives that the warps share
 
 template <typename T> struct Word;   // what a 4-byte word of a row holds
 template <> struct Word<float> {
@@ -345,139 +346,174 @@ __device__ __forceinline__ void add_far_word(Stat& st, unsigned x) {
 
 // Shared memory of a row's end.
 struct RowEnd {
-  unsigned best[kBest * kRowWarps];   // the order keys of every warp's best threads
+  unsigned best[kBest * kRowWarps];        // the order keys of every warp's best threads
   float s[kRowWarps], t[kRowWarps];
-  unsigned floor;
-  int count[kRowWarps];
-  unsigned long long list[kRowWarps * DET_MAX_TOP_K];
+  int jobs[2];                             // of a first and a second list; 0 between the rows' ends
+  unsigned job[kMaxJobs];                  // chunk x 256 + thread: words to be read again
+  int count[kRowWarps];                    // of a warp's list
+  unsigned long long list[kRowWarps][32];  // elements that reach the bound, of a warp's jobs
 };
+static_assert(DET_MAX_TOP_K <= 32, "a lane per alternative");
 
 // Threads of a warp that the bound for k alternatives is drawn from: some more
 // than k in all the warps.
 __device__ __forceinline__ int best_per_warp(int k) { return k == 0 ? 1 : (k + kRowWarps - 1) / kRowWarps + 1 + (k > 8); }
 static_assert((DET_MAX_TOP_K + kRowWarps - 1) / kRowWarps + 2 <= kBest, "room for the largest k");
 
-// The top_k largest of the row.  end.best holds the order keys of the best
-// threads of every warp, `each` of them: the k-th largest is a lower bound of
-// the row's k-th largest element, so only threads whose best reaches it are
-// looked through again, each by its whole warp, whose lanes keep the best in
-// order: the 32 words of the chunk with its best, and all its words only if
-// another chunk has such an element too.
-template <typename T>
-__device__ void top_alternatives(const T* row, int vocab, float largest, const Best& best, int k, float m, float log_s,
-                                 long long r, RowEnd& end, const RowOut& out) {
-  constexpr int N = Word<T>::N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = best_per_warp(k);
-  {
-    const unsigned a = lane < each * kRowWarps ? end.best[lane] : 0u;
-    const unsigned b = lane + 32 < each * kRowWarps ? end.best[lane + 32] : 0u;
-    for (int j = 0; j < each; ++j) {
-      const int at = each * warp + j;
-      const unsigned mine = end.best[at];
-      const int above = __popc(__ballot_sync(0xffffffffu, a > mine || (a == mine && lane < at))) +
-                        __popc(__ballot_sync(0xffffffffu, b > mine || (b == mine && lane + 32 < at)));
-      if (above == k - 1) end.floor = mine;
-    }
-  }
-  __syncthreads();
-  const unsigned floor_key = end.floor;
-  const bool aligned = (reinterpret_cast<uintptr_t>(row) & 3) == 0;
-  const int words = (vocab + N - 1) / N, chunks = (words + kChunkWords - 1) / kChunkWords;
-  unsigned long long mine = 0;   // below every key
-  // the threads to look through: at one chunk, or at every one from 0 up
-  unsigned one = __ballot_sync(0xffffffffu, order_key(largest) >= floor_key);
-  unsigned all = __ballot_sync(0xffffffffu, order_key(largest) >= floor_key && order_key(best.others) >= floor_key);
-  one &= ~all;
-  int all_chunk = 0;
-  static_assert(kWords == 32, "a lane per word");
-  constexpr int kAhead = 8;      // loads in flight
-  while (one | all) {
-    unsigned word[kAhead];
-    int at[kAhead], loads = 0;
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      int owner = 0, c = chunks;   // none
-      if (one) {
-        owner = __ffs(one) - 1;
-        one &= one - 1;
-        c = __shfl_sync(0xffffffffu, best.chunk, owner);
-      } else if (all) {
-        owner = __ffs(all) - 1;
-        c = all_chunk;
-        if (++all_chunk == chunks) {
-          all_chunk = 0;
-          all &= all - 1;
-        }
-      }
-      at[a] = words;
-      word[a] = 0u;
-      if (c < chunks) {
-        loads = a + 1;
-        at[a] = c * kChunkWords + lane * kRowThreads + warp * 32 + owner;
-        if (at[a] < words) word[a] = load_word(row, at[a], vocab, aligned);
-      }
-    }
+// A lower bound of the row's k-th largest element: the k-th largest of the best
+// threads' order keys or a little less, by cutting the interval in which it is
+// to a quarter a few times.  Every warp finds it for itself.
+__device__ __forceinline__ unsigned kth_best(const RowEnd& end, int count, int k, int lane) {
+  static_assert(kBest * kRowWarps <= 64, "two keys a lane");
+  const bool in_a = lane < count, in_b = lane + 32 < count;
+  const unsigned a = in_a ? end.best[lane] : 0u, b = in_b ? end.best[lane + 32] : 0u;
+  // at least k keys reach low, and high is the largest
+  unsigned low = __reduce_min_sync(0xffffffffu, in_b ? min(a, b) : in_a ? a : 0xffffffffu);
+  const unsigned high = __reduce_max_sync(0xffffffffu, max(a, b));
+  unsigned width = high - low;
 #pragma unroll 1
-    for (int a = 0; a < loads; ++a) {   // the first of the arrays, which move up
+  for (int i = 0; i < 3 && width >= 4; ++i) {
+    width /= 4;
+    unsigned up = 0;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = at[0] * N + j;
-        unsigned long long cand = 0;
-        if (at[0] < words && e < vocab) {
-          const unsigned ek = order_key(Word<T>::get(word[0], j));
-          if (ek >= floor_key) cand = ((unsigned long long)ek << 32) | (unsigned)~(unsigned)e;
-        }
-        if (!__any_sync(0xffffffffu, cand != 0)) continue;
-        const unsigned long long worst = __shfl_sync(0xffffffffu, mine, k - 1);
-        unsigned hits = __ballot_sync(0xffffffffu, cand > worst);
-        while (hits) {
-          const int src = __ffs(hits) - 1;
-          hits &= hits - 1;
-          list_insert(mine, __shfl_sync(0xffffffffu, cand, src), lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i + 1 < kAhead; ++i) {
-        word[i] = word[i + 1];
-        at[i] = at[i + 1];
+    for (int q = 1; q < 4; ++q) {
+      const unsigned mid = low + q * width;
+      const int reach = __popc(__ballot_sync(0xffffffffu, in_a && a >= mid)) +
+                        __popc(__ballot_sync(0xffffffffu, in_b && b >= mid));
+      if (reach >= k) up = q * width;
+    }
+    low += up;
+  }
+  return low;
+}
+
+// The words that a warp reads again: of every 8th job, or, where there were too
+// many, of its own threads: the 32 words of the chunk with a thread's best, or those
+// of every chunk if another one has an element that reaches the bound too.
+struct Jobs {
+  const unsigned* list;
+  int next, count;             // of the list; count < 0: of the warp's threads
+  unsigned one, all;           // threads whose best chunk is to be read, or every chunk from `chunk` up
+  int chunk, chunks;
+
+  __device__ __forceinline__ bool any() const { return count < 0 ? (one | all) != 0 : next < count; }
+  // Chunk x 256 + thread of the next one; best_chunk: of the lane's thread.
+  __device__ __forceinline__ unsigned take(int best_chunk) {
+    const unsigned first = threadIdx.x & ~31u;   // of the warp's threads
+    if (count >= 0) {
+      const unsigned job = list[next];
+      next += kRowWarps;
+      return job;
+    }
+    if (one) {
+      const int owner = __ffs(one) - 1;
+      one &= one - 1;
+      // -1, in a row given up before the thread had an element: any chunk will do
+      return (unsigned)max(__shfl_sync(0xffffffffu, best_chunk, owner), 0) * kRowThreads + first + owner;
+    }
+    const unsigned job = (unsigned)chunk * kRowThreads + first + __ffs(all) - 1;
+    if (++chunk == chunks) {
+      chunk = 0;
+      all &= all - 1;
+    }
+    return job;
+  }
+};
+
+// The lane's word of a job and what it holds.
+template <typename T> struct Found {
+  const T* row;
+  int vocab, words;
+  bool aligned;
+  unsigned floor_key;
+
+  __device__ __forceinline__ int at(unsigned job) const {
+    return (int)((job / kRowThreads * kWords + (threadIdx.x & 31)) * kRowThreads + job % kRowThreads);
+  }
+  __device__ __forceinline__ unsigned load(int w) const { return w < words ? load_word(row, w, vocab, aligned) : 0u; }
+  // Element j of word w: its order key above the complement of its index if it reaches the bound, else 0.
+  __device__ __forceinline__ unsigned long long key(int w, unsigned word, int j) const {
+    const int e = w * Word<T>::N + j;
+    const unsigned ek = order_key(Word<T>::get(word, j));
+    return w < words && e < vocab && ek >= floor_key ? ((unsigned long long)ek << 32) | (unsigned)~(unsigned)e : 0ull;
+  }
+};
+
+// A warp whose elements do not fit its list (many equal ones): its k best, kept in order.
+template <typename T>
+__device__ __noinline__ int sorted_list(Jobs jobs, int best_chunk, Found<T> found, int k, unsigned long long* list) {
+  static_assert(kWords == 32, "a lane per word");
+  const int lane = threadIdx.x & 31;
+  unsigned long long mine = 0;   // below every key
+  while (jobs.any()) {
+    const int w = found.at(jobs.take(best_chunk));
+    const unsigned word = found.load(w);
+#pragma unroll 1
+    for (int j = 0; j < Word<T>::N; ++j) {
+      const unsigned long long key = found.key(w, word, j);
+      unsigned hits = __ballot_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1));
+      while (hits) {
+        const int src = __ffs(hits) - 1;
+        hits &= hits - 1;
+        list_insert(mine, __shfl_sync(0xffffffffu, key, src), lane);
       }
     }
   }
   const int count = min(k, __popc(__ballot_sync(0xffffffffu, mine != 0)));
-  if (lane == 0) end.count[warp] = count;
-  __syncthreads();
-  int before = lane < warp && lane < kRowWarps ? end.count[lane] : 0, total = lane < kRowWarps ? end.count[lane] : 0;
-  before = __reduce_add_sync(0xffffffffu, before);
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (lane < count) end.list[before + lane] = mine;
-  __syncthreads();
-  for (int at = threadIdx.x; at < total; at += kRowThreads) {   // at most 8 x 32
-    const unsigned long long c = end.list[at];
-    int rank = 0;
-    for (int j = 0; j < total; ++j) rank += end.list[j] > c ? 1 : 0;
-    if (rank < k) {
-      const float x = key_value((unsigned)(c >> 32));
-      if (out.top_index) out.top_index[r * k + rank] = (int32_t)~(unsigned)c;
-      if (out.top_logprob) out.top_logprob[r * k + rank] = (x - m) - log_s;
+  if (lane < count) list[lane] = mine;
+  return count;
+}
+
+// The last of the top_k alternatives, where only elements equal to the bound are
+// left: those of the lowest indices (one warp).
+template <typename T>
+__device__ __noinline__ void fill_equal(Found<T> found, unsigned equal, const RowEnd& end, int top_k, float base,
+                                        float log_s, long long r, const RowOut& out) {
+  const int lane = threadIdx.x & 31;
+  int rank = (int)__reduce_add_sync(0xffffffffu, lane < kRowWarps ? (unsigned)end.count[lane] : 0u);
+  const float log_p = (key_value(equal) - base) - log_s;
+  for (int w0 = 0; w0 < found.words && rank < top_k; w0 += 32) {
+    const unsigned word = found.load(w0 + lane);
+    unsigned hits[Word<T>::N];
+    int mine = rank;
+#pragma unroll
+    for (int j = 0; j < Word<T>::N; ++j) {
+      const bool is = w0 + lane < found.words && (w0 + lane) * Word<T>::N + j < found.vocab &&
+                      order_key(Word<T>::get(word, j)) == equal;
+      hits[j] = __ballot_sync(0xffffffffu, is);
+      mine += __popc(hits[j] & ((1u << lane) - 1));
+      rank += __popc(hits[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < Word<T>::N; ++j) {
+      if (!((hits[j] >> lane) & 1)) continue;
+      if (mine < top_k) {
+        if (out.top_index) out.top_index[r * top_k + mine] = (w0 + lane) * Word<T>::N + j;
+        if (out.top_logprob) out.top_logprob[r * top_k + mine] = log_p;
+      }
+      ++mine;
     }
   }
 }
 
-// The threads' statistics joined, and the row's results.
+// The threads' statistics joined, the row's results and its top_k largest
+// elements: only threads whose best reaches the k-th best of the warps' best
+// ones are looked through again, as jobs that the warps share.  raw is the
+// token's logit.
+//
+// It runs once a row: its instructions are mostly fetched anew, and it is one
+// chain of dependent steps, about half of which the SM's other CTA hides.  What
+// counts is little code, few steps, even shares, and reads of the row that
+// are on their way while the sums are joined.
 template <typename T>
-__device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* row, int vocab, long long r,
-                                           const int32_t* tokens, int top_k, RowEnd& end, const RowOut& out) {
+__device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* row, int vocab, long long r, int tok,
+                                           T raw, int top_k, RowEnd& end, const RowOut& out) {
+  constexpr int kAhead = 4;   // reads in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the token's logit is on its way meanwhile
-  int tok = -1;
-  float at = 0.0f;
-  if (threadIdx.x == 0 && out.logprob) {
-    tok = tokens[r];
-    if (tok >= 0 && tok < vocab) at = to_f32(row[tok]);
-  }
   const float largest = st.m;
   unsigned left = order_key(largest);
   const int each = best_per_warp(top_k);
+#pragma unroll 1
   for (int j = 0; j < each; ++j) {
     const unsigned top = __reduce_max_sync(0xffffffffu, left);
     if (lane == 0) end.best[each * warp + j] = top;
@@ -486,13 +522,97 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   }
   __syncthreads();
   const float m = key_value(__reduce_max_sync(0xffffffffu, end.best[each * (lane & (kRowWarps - 1))]));
+  Jobs jobs = {end.job, warp, 0, 0u, 0u, 0, 0};
+  Found<T> found = {row, vocab, 0, false, 0u};
+  unsigned floor_key = 0;
+  int at[kAhead];
+  unsigned word[kAhead];
+  if (top_k > 0) {
+    floor_key = kth_best(end, each * kRowWarps, top_k, lane);
+    found.words = (vocab + Word<T>::N - 1) / Word<T>::N;
+    found.aligned = (reinterpret_cast<uintptr_t>(row) & 3) == 0;
+    jobs.chunks = (found.words + kChunkWords - 1) / kChunkWords;
+    // With too many elements at the bound (the mask's value, in a row with
+    // fewer than k others) those above it are listed, and the lowest of the equal
+    // ones fill the rest; with too many above it the warps take their own threads.
+#pragma unroll 1
+    for (int list = 0; list < 3; ++list) {
+      found.floor_key = list == 1 ? floor_key + 1 : floor_key;
+      const bool reaches = order_key(largest) >= found.floor_key;
+      const bool others = reaches && order_key(best.others) >= found.floor_key;
+      jobs.one = __ballot_sync(0xffffffffu, reaches && !others);
+      jobs.all = __ballot_sync(0xffffffffu, others);
+      jobs.count = -1;
+      if (list == 2) break;
+      const int single = __popc(jobs.one), many = __popc(jobs.all);
+      if (single + many > 0) {
+        const long long wanted = single + (long long)many * jobs.chunks;
+        const int n = (int)min(wanted, (long long)kMaxJobs + 1);   // so that the sum of 8 stays small
+        int base = 0;
+        if (lane == 0) base = atomicAdd(&end.jobs[list], n);
+        base = __shfl_sync(0xffffffffu, base, 0);
+        if (base + n <= kMaxJobs) {
+          const unsigned before = (1u << lane) - 1;
+          if (reaches && !others)
+            end.job[base + __popc(jobs.one & before)] = (unsigned)max(best.chunk, 0) * kRowThreads + threadIdx.x;
+          if (others)
+            for (int c = 0; c < jobs.chunks; ++c)
+              end.job[base + single + __popc(jobs.all & before) * jobs.chunks + c] = (unsigned)c * kRowThreads + threadIdx.x;
+        }
+      }
+      __syncthreads();
+      jobs.count = end.jobs[list];
+      if (jobs.count <= kMaxJobs) break;
+      if (floor_key == 0xffffffffu) list = 1;   // nothing is above NaN
+    }
+  }
+  const Jobs from_the_start = jobs;
+  int loads = 0;
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    if (!jobs.any()) break;
+    at[a] = found.at(jobs.take(best.chunk));
+    word[a] = found.load(at[a]);
+    loads = a + 1;
+  }
   raise_to<T>(st, m);
   float s = warp_pt(st.s), t = warp_pt(st.t);
   if (lane == 0) {
     end.s[warp] = s;
     end.t[warp] = t;
   }
+  if (top_k > 0) {
+    int count = 0;
+    while (true) {
+#pragma unroll 1
+      for (int a = 0; a < loads; ++a) {   // the first of the arrays, which move up
+#pragma unroll 1
+        for (int j = 0; j < Word<T>::N; ++j) {
+          const unsigned long long key = found.key(at[0], word[0], j);
+          const unsigned hits = __ballot_sync(0xffffffffu, key != 0);
+          const int slot = count + __popc(hits & ((1u << lane) - 1));
+          if (key != 0 && slot < 32) end.list[warp][slot] = key;
+          count += __popc(hits);
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) {
+          word[i] = word[i + 1];
+          at[i] = at[i + 1];
+        }
+      }
+      if (!jobs.any() || count > 32) break;
+      at[0] = found.at(jobs.take(best.chunk));
+      word[0] = found.load(at[0]);
+      loads = 1;
+    }
+    if (count > 32) {
+      __syncwarp();
+      count = sorted_list(from_the_start, best.chunk, found, top_k, end.list[warp]);
+    }
+    if (lane == 0) end.count[warp] = count;
+  }
   __syncthreads();
+  if (threadIdx.x == 0) end.jobs[0] = end.jobs[1] = 0;
   s = end.s[lane & (kRowWarps - 1)];
   t = end.t[lane & (kRowWarps - 1)];
 #pragma unroll
@@ -508,9 +628,30 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   if (threadIdx.x == 0) {
     if (out.lse) out.lse[r] = empty ? kNegInf : base + log_s;
     if (out.entropy) out.entropy[r] = empty ? 0.0f : log_2s - kLn2 * (t / s);
-    if (out.logprob) out.logprob[r] = tok >= 0 && tok < vocab ? (at - base) - log_s : 0.0f;
+    if (out.logprob) out.logprob[r] = tok >= 0 && tok < vocab ? (to_f32(raw) - base) - log_s : 0.0f;
   }
-  if (top_k > 0) top_alternatives(row, vocab, largest, best, top_k, base, log_s, r, end, out);
+  if (top_k > 0) {
+    // the ranks of the warp's list among all lists, an element after the other
+    unsigned long long v[kRowWarps];
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) v[w] = lane < end.count[w] ? end.list[w][lane] : 0ull;
+    const int count = end.count[warp];
+    int rank = top_k;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const unsigned long long key = end.list[warp][i];
+      int above = 0;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) above += __popc(__ballot_sync(0xffffffffu, v[w] > key));
+      if (lane == i) rank = above;
+    }
+    if (rank < top_k) {
+      const unsigned long long key = end.list[warp][lane];
+      if (out.top_index) out.top_index[r * top_k + rank] = (int32_t)~(unsigned)key;
+      if (out.top_logprob) out.top_logprob[r * top_k + rank] = (key_value((unsigned)(key >> 32)) - base) - log_s;
+    }
+    if (found.floor_key != floor_key && warp == 0) fill_equal(found, floor_key, end, top_k, base, log_s, r, out);
+  }
 }
 
 // What a CTA of a cluster leaves of its part for the first one.
@@ -535,11 +676,13 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
   const int rank = SPLIT ? blockIdx.x % parts : 0;
   const int c0 = SPLIT ? rank * per_part : 0, c1 = SPLIT ? min(c0 + per_part, chunks) : chunks;
   const long long row0 = SPLIT ? blockIdx.x / parts : blockIdx.x, row_step = SPLIT ? rows : gridDim.x;
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
+    end.jobs[0] = end.jobs[1] = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&stream.full[i], 1);
       mbar_init(&stream.empty[i], kRowWarps);
     }
+  }
   __syncthreads();
   dep_wait();   // launched early: all loads come after, and none is a read-only one, which need not
   dep_launch();
@@ -565,8 +708,10 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
   for (int i = 0; i < kStages - 1; ++i) fetch_next(threadIdx.x == 0);
   // a thread's edges of the row after the current one
   unsigned head_ahead = 0, tail_ahead = 0;
+  int token_ahead = -1;   // of that row (one thread)
   auto load_edges = [&](long long r) {
     if (r >= rows) return;
+    if (threadIdx.x == 0 && out.logprob) token_ahead = tokens[r];
     const RowMap<T> map(logits + r * row_stride, vocab);
     const bool aligned = (map.off & 3) == 0;
     if ((int)threadIdx.x < map.head) head_ahead = load_word(map.row, threadIdx.x, vocab, aligned);
@@ -578,6 +723,9 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
   for (long long r = row0; r < rows; r += row_step) {
     const RowMap<T> map(logits + r * row_stride, vocab);
     const unsigned head = head_ahead, tail = tail_ahead;
+    const int token = token_ahead;
+    T token_logit = from_f32<T>(0.0f);
+    if (token >= 0 && token < vocab) token_logit = map.row[token];
     load_edges(r + row_step);
     Stat st = {kNegInf, 0.0f, 0.0f}, all = st;   // of the part, and of the parts before it
     Best best = {-1, kNegInf}, all_best = best;
@@ -667,7 +815,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     } else if (gave_up) {
       all.m = __uint_as_float(0x7fc00000u);
     }
-    finish_row(all, all_best, map.row, vocab, r, tokens, top_k, end, out);
+    finish_row(all, all_best, map.row, vocab, r, token, token_logit, top_k, end, out);
   }
 }
 

@@ -131,6 +131,36 @@ def test_masks_and_special_rows(det, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("vocab", [67, 4099, 131072])
+def test_fewer_tokens_left_than_alternatives(det, dtype, vocab):
+    """The mask's value (or a value that many share, anywhere in the row) fills the alternatives by index."""
+    rng = np.random.default_rng(vocab)
+    low = torch.finfo(DTYPES[dtype]).min
+    x = logits(rng, 12, vocab, dtype)
+    for row, (mask, left) in enumerate([(-np.inf, 2), (-np.inf, 19), (-np.inf, 31), (low, 3), (low, 20), (-3e4, 7)]):
+        keep = rng.permutation(vocab)[:left]
+        kept = x[row, keep].clone()
+        x[row] = mask
+        x[row, keep] = kept
+    x[6, : vocab // 2] = -20.0                       # a shared value in the row's second half, few above it
+    x[6, vocab // 2:] = 4.0
+    x[6, rng.permutation(vocab)[:9]] = 9.0
+    x[7] = -20.0
+    x[7, vocab - 40:] = 4.0                          # and at its end only
+    x[7, 3] = 5.0
+    x[8] = -np.inf
+    x[8, vocab - 33:] = low
+    x[9] = float("nan")
+    x[10] = 1.0
+    x[10, ::3] = float("nan")
+    x[11] = -np.inf
+    x[11, vocab - 1] = float("inf")
+    tokens = rng.integers(0, vocab, 12).astype(np.int32)
+    for k in (1, 20, 32):
+        check(det, x, tokens, k)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 def test_alternatives_with_many_ties(det, dtype):
     rng = np.random.default_rng(5)
     x = torch.from_numpy(rng.integers(0, 4, (6, 40_001)).astype(np.float32)).to(DTYPES[dtype]).cuda()
