@@ -12,10 +12,10 @@
 //
 // What bounds it: the bytes in 32 bits (4,096 x 49,152: 118 us, the measured
 // copy bandwidth), in 16 bits nearly as much the instructions, 7.6 an element at
-// 64% of the issue slots (4,096 x 98,304 bf16: 129 to 132 us, 90 to 92%).  Rows that
-// start at an odd element read each word of shared memory twice (4,096 x 100,003
-// bf16: 161 us, 75%).  With alternatives a CTA's row end takes 1 to 5 us more, half of it
-// hidden by the SM's other CTA (20 of them at 98,304: 197 us).
+// 64% of the issue slots (4,096 x 98,304 bf16: 124 us, 95%).  Rows that start at an
+// odd element read each word of shared memory twice (4,096 x 100,003 bf16: 161 us,
+// 75%).  With alternatives a CTA's row end takes 2 to 5 us more, half of it hidden
+// by the SM's other CTA (4,096 x 98,304: one of them 143 us, 20 of them 188).
 #include "det_model.cuh"
 
 #include <algorithm>
@@ -498,8 +498,7 @@ __device__ __noinline__ void fill_equal(Found<T> found, unsigned equal, const Ro
 
 // The threads' statistics joined, the row's results and its top_k largest
 // elements: only threads whose best reaches the k-th best of the warps' best
-// ones are looked through again, as jobs that the warps share.  raw is the
-// token's logit.
+// ones are looked through again, as jobs that the warps share.
 //
 // It runs once a row: its instructions are mostly fetched anew, and it is one
 // chain of dependent steps, about half of which the SM's other CTA hides.  What
@@ -507,9 +506,11 @@ __device__ __noinline__ void fill_equal(Found<T> found, unsigned equal, const Ro
 // are on their way while the sums are joined.
 template <typename T>
 __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* row, int vocab, long long r, int tok,
-                                           T raw, int top_k, RowEnd& end, const RowOut& out) {
+                                           int top_k, RowEnd& end, const RowOut& out) {
   constexpr int kAhead = 4;   // reads in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T raw = from_f32<T>(0.0f);   // the token's logit, used at the end
+  if (tok >= 0 && tok < vocab) raw = row[tok];
   const float largest = st.m;
   unsigned left = order_key(largest);
   const int each = best_per_warp(top_k);
@@ -708,7 +709,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
   for (int i = 0; i < kStages - 1; ++i) fetch_next(threadIdx.x == 0);
   // a thread's edges of the row after the current one
   unsigned head_ahead = 0, tail_ahead = 0;
-  int token_ahead = -1;   // of that row (one thread)
+  int token_ahead = -1;   // and its token (one thread)
   auto load_edges = [&](long long r) {
     if (r >= rows) return;
     if (threadIdx.x == 0 && out.logprob) token_ahead = tokens[r];
@@ -724,8 +725,6 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     const RowMap<T> map(logits + r * row_stride, vocab);
     const unsigned head = head_ahead, tail = tail_ahead;
     const int token = token_ahead;
-    T token_logit = from_f32<T>(0.0f);
-    if (token >= 0 && token < vocab) token_logit = map.row[token];
     load_edges(r + row_step);
     Stat st = {kNegInf, 0.0f, 0.0f}, all = st;   // of the part, and of the parts before it
     Best best = {-1, kNegInf}, all_best = best;
@@ -815,7 +814,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     } else if (gave_up) {
       all.m = __uint_as_float(0x7fc00000u);
     }
-    finish_row(all, all_best, map.row, vocab, r, token, token_logit, top_k, end, out);
+    finish_row(all, all_best, map.row, vocab, r, token, top_k, end, out);
   }
 }
 
