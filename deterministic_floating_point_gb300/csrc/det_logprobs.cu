@@ -756,7 +756,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
         if (kAll && all_near) release();
         if (near) {
           add_words<T>(st, x);
-        } else {
+        } else if (st.m != kNegInf) {   // masked logits alone add nothing
 #pragma unroll 1
           for (int i = 0; i < NW; ++i) {
             unsigned y[1];
