@@ -163,7 +163,7 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 // and 16 sequences 175 us (90%).  About 10 us of a call are its own: the CTAs'
 // first tiles, the last ones, which do not fill the SMs, and the join (of 64 dims
 // 128 sequences 345 us, 92%).  With short chunks a CTA's start and end (length,
-// page, first tile and join of the warps, 4 us together against 1.3 us a tile) show:
+// page, first tile and join of the warps, some 4 us against 1.3 us a tile) show:
 // 128 sequences of 500 tokens 48 us (80%), 64 ragged ones of up to 8,191 tokens
 // of 64 dims with the bias 59 us (72%).  Copying whole rows by the bulk engine was
 // slower (a copy of 256 bytes every 20 cycles an SM: 296 us for 32 x 8,192).

@@ -81,9 +81,9 @@ bias_direct_kernel(const void* table, int table_dtype, int heads, Distances dist
 //
 // Bound by the writes.  What matters is how much of the output is being
 // written at a time (16 x 4,096 x 4,096 bf16, threads x rows of a CTA: 128 x 128 117 us,
-// 256 x 64 98, 256 x 32 93, 128 x 32 86, 92% of the measured copy bandwidth;
-// 8 x 4,096 x 4,096 f32: 256 x 16 81 us, 98%; torch's fill of the same bytes
-// takes 136 us).  Rows of 4,097: 96 us.
+// 256 x 64 98, 256 x 32 93, 128 x 32 86, and launched early 83 to 85, 93 to 95% of
+// the measured copy bandwidth; 8 x 4,096 x 4,096 f32: 256 x 16 81 us, 98%; torch's
+// fill of the same bytes takes 136 us).  Rows of 4,097: 96 us.
 template <typename T, bool ALIGNED> struct BiasTile {
   static constexpr int kThreads = sizeof(T) == 4 && ALIGNED ? 256 : 128, kRows = sizeof(T) == 4 && ALIGNED ? 16 : 32;
 };
@@ -197,10 +197,10 @@ struct GradView {
 // aligned it reads what lane 30 lacks.
 //
 // Bound by the reads: one addition and one unpacking an element, 16 bytes a
-// load, 4 KB a warp in flight (8 x 16 x 2,048 x 2,048 bf16 with the join 164 us, 96% of
+// load, 4 KB a warp in flight (8 x 16 x 2,048 x 2,048 bf16 with the join 163 us, 97% of
 // the measured copy bandwidth).  Unaligned rows shift their eights across
 // lanes, 9 instructions an element instead of 4 (2,047 keys: 237 us;
-// 3 x 12 x 509 x 1,531 f32: 29 us, of which the launches are a third).
+// 3 x 12 x 509 x 1,531 f32: 28 us, of which the launches are a third).
 constexpr int kTileRows = 64;
 constexpr int kTileGroups = kTileRows / 8;
 constexpr int kTileLanes = 31;
