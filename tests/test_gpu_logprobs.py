@@ -161,6 +161,28 @@ def test_fewer_tokens_left_than_alternatives(det, dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+def test_alternatives_past_the_lists(det, dtype):
+    """More equal elements than a row's end lists: many threads' (some warps have none of them), or many of few threads."""
+    vocab = 40_003
+    per_word = 1 if dtype == "f32" else 2
+    thread = torch.arange(vocab, device="cuda") // per_word % 256
+    chunk = torch.arange(vocab, device="cuda") // per_word // 8192
+    x = torch.full((6, vocab), -1.0, device="cuda")
+    x[0] = torch.where(thread < 32, -20.0, 4.0)
+    x[0, 777] = 9.0
+    x[1] = torch.where(thread % 64 < 32, -20.0, 4.0)
+    x[1, 39_999] = 9.0
+    x[2] = torch.where((thread < 100) & (chunk == 0), 5.0, -1.0)
+    x[3] = torch.where((thread < 100) & (chunk == 1), 5.0, -1.0)
+    x[4] = torch.where((thread < 20) & (chunk == 0), 5.0, -1.0)
+    x[4, 6:40_000:3001] = 6.0
+    x[5] = torch.where(thread == 255, 3.0, -1.0)
+    x = x.to(DTYPES[dtype])
+    for k in (1, 7, 20, 32):
+        check(det, x, np.full(6, 777, np.int32), k)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 def test_alternatives_with_many_ties(det, dtype):
     rng = np.random.default_rng(5)
     x = torch.from_numpy(rng.integers(0, 4, (6, 40_001)).astype(np.float32)).to(DTYPES[dtype]).cuda()
