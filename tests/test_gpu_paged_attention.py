@@ -118,6 +118,24 @@ def test_long_lengths(det, lengths):
     check(det, make(len(lengths), lengths, 8, 8, 128, 16, "f16")) if max(lengths) < 40_000 else None
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 48, 20])
+def test_numbers_of_chunks(det, dim, page):
+    """Sequences of one to 33 chunks of every size in one call, whatever the longest one is."""
+    lengths = [512, 513, 768, 1024, 1025, 4096, 4097, 8192, 8193, 16_384, 16_385, 1, 0]
+    q, k, v, table, n = make(dim, lengths, 18, 2, dim, page, "bf16")
+    check(det, (q, k, v, table, n))
+    for longest in (1000, 8192):
+        r = det.det_paged_attention(q, k, v, table, n, max_len=longest)
+        cut = det.det_paged_attention(q, k, v, table, n.clamp(max=longest))
+        assert torch.equal(r.out, cut.out) and torch.equal(r.lse, cut.lse)
+    # queries at odd elements
+    odd = torch.zeros(len(lengths), 18, dim + 1, dtype=q.dtype, device="cuda")
+    odd[..., 1:] = q
+    r, want = det.det_paged_attention(odd[..., 1:], k, v, table, n), det.det_paged_attention(q, k, v, table, n)
+    assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("heads,kv_heads", [(8, 8), (8, 2), (12, 1)])
 def test_learned_bias(det, dtype, heads, kv_heads):
