@@ -332,6 +332,15 @@ __device__ __forceinline__ void add_words(Stat& st, const unsigned (&x)[NW]) {
   st.t += t.x + t.y;
 }
 
+// Whether NW words hold m alone, and it is neither +inf nor NaN.
+template <typename T, int NW>
+__device__ __forceinline__ bool all_equal(const unsigned (&x)[NW], float m) {
+  unsigned differ = 0;
+#pragma unroll
+  for (int i = 1; i < NW; ++i) differ |= x[i] ^ x[0];
+  return differ == 0 && Word<T>::get(x[0], 0) == m && Word<T>::get(x[0], Word<T>::N - 1) == m && m < -kNegInf;
+}
+
 // The same for a maximum far from 0 (or -inf, inf, NaN), word by word.
 template <typename T>
 __device__ __forceinline__ void add_far_word(Stat& st, unsigned x) {
@@ -756,7 +765,11 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
         if (kAll && all_near) release();
         if (near) {
           add_words<T>(st, x);
-        } else if (st.m != kNegInf) {   // masked logits alone add nothing
+        } else if (st.m == kNegInf) {
+          // masked logits alone add nothing
+        } else if (all_equal<T>(x, st.m)) {
+          st.s += (float)(NW * Word<T>::N);   // masked by the type's lowest value: 1 each, and nothing to T
+        } else {
 #pragma unroll 1
           for (int i = 0; i < NW; ++i) {
             unsigned y[1];
