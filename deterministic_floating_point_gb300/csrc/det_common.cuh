@@ -1,8 +1,10 @@
 // Shared device helpers for the deterministic reductions (sm_103a).
 //
-// Only IEEE round-to-nearest additions of the data type touch values.  The
-// build uses no fast-math and leaves flush-to-zero off; there are no
-// multiplies on any value path, so FMA contraction cannot arise.
+// Only IEEE round-to-nearest additions of the data type touch the values of the
+// calls of det.h.  The build uses no fast-math and leaves flush-to-zero off; there
+// are no multiplies on any of their value paths, so FMA contraction cannot arise.
+// The language-model operators do multiply: where a product has to be rounded
+// by itself they say so (__fmul_rn).
 #pragma once
 
 #include <cuda_runtime.h>

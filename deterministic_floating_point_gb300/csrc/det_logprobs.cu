@@ -126,13 +126,18 @@ template <typename T> __device__ __forceinline__ bool near_max(float m) {
   // in f16 also: the bound for masked logits, m - 150 and a little, is a finite value
   return m > (std::is_same<T, __half>::value ? -60000.0f : -1e30f) && m < 1e30f;
 }
-// The reference of `from` less that of m, in units of log 2.
+// The reference of a near maximum: the rounded product, the same number wherever
+// it is used.  As a plain product it may be fused with the addition that takes
+// it; a sum would then be scaled by 2 to the rounding's residue each time it is
+// brought to its own maximum (rows of equal logits, -1e9: log p was 25 to 62 off).
+__device__ __forceinline__ float near_ref(float m) { return __fmul_rn(m, kLog2e); }
+// The reference of `from` less that of m, in units of log 2 (0 where they are equal).
 template <typename T> __device__ __forceinline__ float ref_step(float from, float m) {
   const bool a = near_max<T>(from), b = near_max<T>(m);
-  if (a && b) return from * kLog2e - m * kLog2e;
-  if (a) return -fmaf(m, kLog2e, -(from * kLog2e));
-  if (b) return fmaf(from, kLog2e, -(m * kLog2e));
-  return (from - m) * kLog2e;
+  if (a && b) return __fsub_rn(near_ref(from), near_ref(m));
+  if (a) return -__fmaf_rn(m, kLog2e, -near_ref(from));
+  if (b) return __fmaf_rn(from, kLog2e, -near_ref(m));
+  return __fmul_rn(from - m, kLog2e);
 }
 // S and T brought to the reference of m, which is not below st.m.
 template <typename T> __device__ __forceinline__ void raise_to(Stat& st, float m) {
@@ -305,7 +310,7 @@ template <typename T, int NW>
 __device__ __forceinline__ void add_words(Stat& st, const unsigned (&x)[NW]) {
   constexpr int N = Word<T>::N;
   unsigned long long s2 = 0, t2 = 0;   // of elements 0 and 1 of the words (f32: even and odd words)
-  const float ref = -(st.m * kLog2e);
+  const float ref = -near_ref(st.m);
   const unsigned long long c = pack_f32x2(kLog2e, kLog2e), minus = pack_f32x2(ref, ref);
   // 2^y is 0 from y = -127 on: a bound of -150 for x - m changes no term, and
   // without it 0 * inf for a masked logit.  16-bit logits are bounded in
@@ -634,7 +639,7 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
   const float base = empty ? 0.0f : m;
   // log of the sum relative to exp(m): the reference is m log2(e) up to its rounding
   const float log_2s = empty ? 0.0f : logf(s);
-  const float log_s = near_max<T>(m) ? fmaf(-kLn2, fmaf(m, kLog2e, -(m * kLog2e)), log_2s) : log_2s;
+  const float log_s = near_max<T>(m) ? fmaf(-kLn2, __fmaf_rn(m, kLog2e, -near_ref(m)), log_2s) : log_2s;
   if (threadIdx.x == 0) {
     if (out.lse) out.lse[r] = empty ? kNegInf : base + log_s;
     if (out.entropy) out.entropy[r] = empty ? 0.0f : log_2s - kLn2 * (t / s);
