@@ -115,16 +115,21 @@ __device__ __forceinline__ unsigned load_word(const T* row, long long w, long lo
 }
 
 // A thread's (or row's) statistics in units of log 2: the largest logit m,
-// and S = sum 2^y, T = sum 2^y y with y = x log2(e) - ref.  Where log2(e) m
-// is far from overflow (near()), ref is that product rounded, so y takes one
-// fused operation for an element; otherwise (the types' lowest values,
-// infinities, NaN) ref is the exact product, and y = (x - m) log2(e).
+// and S = sum 2^y, T = sum 2^y y with y = x log2(e) - ref.  Where m is near 0
+// (near_max()), ref is the product m log2(e) rounded, so y takes one fused
+// operation for an element; otherwise (finite masks, infinities, NaN) ref is the
+// exact product, and y = (x - m) log2(e).
+//
+// Near: at x = m the former y is what the rounding of ref left, up to half a unit
+// of its last place.  It is 2^-4 at 2^20, and the logarithm of S takes it out again;
+// at -1e10 it would be 440, and 2^y overflows.
+constexpr float kNearMost = 1048576.0f;
 struct Stat {
   float m, s, t;
 };
 template <typename T> __device__ __forceinline__ bool near_max(float m) {
   // in f16 also: the bound for masked logits, m - 150 and a little, is a finite value
-  return m > (std::is_same<T, __half>::value ? -60000.0f : -1e30f) && m < 1e30f;
+  return m >= (std::is_same<T, __half>::value ? -60000.0f : -kNearMost) && m <= kNearMost;
 }
 // The reference of a near maximum: the rounded product, the same number wherever
 // it is used.  As a plain product it may be fused with the addition that takes
