@@ -141,6 +141,10 @@ template <typename T> __device__ __forceinline__ float2 unpack2(unsigned w) {
   return make_float2(to_f32(*reinterpret_cast<const T*>(&lo)), to_f32(*reinterpret_cast<const T*>(&hi)));
 }
 
+// What the weights are multiplied by in the second product, and the outputs
+// divided by at its end.
+template <typename T> constexpr float kWeightScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
+
 // Number of bounds <= n.
 __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, int n) {
   int lo = 0, hi = count;
@@ -415,7 +419,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
         }
     }
     // the weights as B operands (column = head), in two parts: the weight
-    // rounded to 16 bits and what the rounding left
+    // rounded to 16 bits and what the rounding left.  Held so to 2^-17 of
+    // themselves in bf16; in f16, whose smallest normal value is 2^-14, they are
+    // scaled by 2^15 (exact, and at most f16's 2^15): to 2^-22 of themselves from
+    // 2^-18 of the largest on, and to 2^-40 of the largest below.
     unsigned ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -429,10 +436,11 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const unsigned hi = pack2<T>(p[2 * half], p[2 * half + 1]);
+        const float p0 = p[2 * half] * kWeightScale<T>, p1 = p[2 * half + 1] * kWeightScale<T>;
+        const unsigned hi = pack2<T>(p0, p1);
         const float2 r = unpack2<T>(hi);
         ph[nt][half] = movmatrix_trans(hi);
-        pl[nt][half] = movmatrix_trans(pack2<T>(p[2 * half] - r.x, p[2 * half + 1] - r.y));
+        pl[nt][half] = movmatrix_trans(pack2<T>(p0 - r.x, p1 - r.y));
       }
     }
     cp_async_wait<kValues>();   // and its values
@@ -476,7 +484,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
       const int col = nt * 8 + 2 * (lane & 3) + j;
       float top = kNegInf;
       for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
-      const float f = m[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - top);
+      const float f = (m[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - top)) * (1.0f / kWeightScale<T>);
       float* dst = sh_o + (size_t)(warp * 8 * NT + col) * kPitch + (lane >> 2);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
