@@ -84,13 +84,13 @@ struct AttnArgs {
   long long table_stride;
   int num_pages, page_size, limit;   // limit: most tokens of a sequence
   int heads, group, head_tiles, max_chunks;
-  float scale_log2;
+  float scale;
   const void* bias;
   int bias_dtype;
   const int32_t* bounds;
   int num_bounds;
   float* part;      // [batch x heads][max_chunks][D]: the chunk's outputs, not yet divided
-  float2* part_ml;  // [batch x heads][max_chunks]: maximum (of log2 scores) and sum
+  float2* part_ml;  // [batch x heads][max_chunks]: maximum of the scores and sum
   void* out;
   float* lse;
 };
@@ -323,8 +323,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
       for (int j = 0; j < 2; ++j) {
         const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
         far_bias[nt][j] =
-            h < a.group ? kLog2e * load_as_f32(a.bias, (long long)a.num_bounds * a.heads + g * a.group + h, a.bias_dtype)
-                        : 0.0f;
+            h < a.group ? load_as_f32(a.bias, (long long)a.num_bounds * a.heads + g * a.group + h, a.bias_dtype) : 0.0f;
       }
   }
   for (int it = 0; it < mine; ++it) {
@@ -360,13 +359,14 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[nt][j] += odd[nt][j];
     }
-    // scores in units of log 2; masked tokens to -inf
+    // the scores, in units of the natural logarithm, since in units of log 2 a
+    // bias of the type's lowest value would be -inf; masked tokens to -inf
     const int first = t0 + (it * W + warp) * L::kTokens;
     if (a.bias && n - (first + L::kTokens) >= far) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(s[nt][j], a.scale_log2, far_bias[nt][j & 1]);
+        for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(s[nt][j], a.scale, far_bias[nt][j & 1]);
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -381,9 +381,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int h = h0 + nt * 8 + 2 * (lane & 3) + j;
-            float x = s[nt][2 * r + j] * a.scale_log2;
-            if (a.bias && h < a.group) x = fmaf(load_as_f32(row, g * a.group + h, a.bias_dtype), kLog2e, x);
-            s[nt][2 * r + j] = x;
+            const float bias = a.bias && h < a.group ? load_as_f32(row, g * a.group + h, a.bias_dtype) : 0.0f;
+            s[nt][2 * r + j] = fmaf(s[nt][2 * r + j], a.scale, bias);
           }
       }
     }
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           // nothing was added while the maximum was -inf: any factor will do
-          const float f = m[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - fresh[nt][j]);
+          const float f = m[nt][j] == kNegInf ? 1.0f : exp_approx(m[nt][j] - fresh[nt][j]);
           m[nt][j] = fresh[nt][j];
           l[nt][j] *= f;
 #pragma unroll
@@ -430,8 +429,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float base = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
-        p[j] = exp2_approx(p[j] - base);
-        p[2 + j] = exp2_approx(p[2 + j] - base);
+        p[j] = exp_approx(p[j] - base);
+        p[2 + j] = exp_approx(p[2 + j] - base);
         l[nt][j] += p[j] + p[2 + j];
       }
 #pragma unroll
@@ -484,7 +483,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
       const int col = nt * 8 + 2 * (lane & 3) + j;
       float top = kNegInf;
       for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
-      const float f = (m[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - top)) * (1.0f / kWeightScale<T>);
+      const float f = (m[nt][j] == kNegInf ? 1.0f : exp_approx(m[nt][j] - top)) * (1.0f / kWeightScale<T>);
       float* dst = sh_o + (size_t)(warp * 8 * NT + col) * kPitch + (lane >> 2);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -500,13 +499,13 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
     for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
     for (int w = 0; w < W; ++w) {
       const float mw = sh_m[w][col];
-      sum += mw == kNegInf ? sh_l[w][col] : sh_l[w][col] * exp2_approx(mw - top);
+      sum += mw == kNegInf ? sh_l[w][col] : sh_l[w][col] * exp_approx(mw - top);
       v += sh_o[(size_t)(w * 8 * NT + col) * kPitch + d];
     }
     const long long bh = (long long)b * a.heads + g * a.group + h0 + col;
     if (chunks == 1) {
       static_cast<T*>(a.out)[bh * D + d] = from_f32<T>(top == kNegInf && sum == 0.0f ? 0.0f : v / sum);
-      if (a.lse && d == 0) a.lse[bh] = top == kNegInf && sum == 0.0f ? kNegInf : (top + log2f(sum)) * (1.0f / kLog2e);
+      if (a.lse && d == 0) a.lse[bh] = top == kNegInf && sum == 0.0f ? kNegInf : top + logf(sum);
     } else {
       a.part[(bh * a.max_chunks + chunk) * D + d] = v;
       if (d == 0) a.part_ml[bh * a.max_chunks + chunk] = make_float2(top, sum);
@@ -563,7 +562,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
         top = x.x;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        f = x.x == kNegInf ? 1.0f : exp2_approx(x.x - top);   // a chunk without a score adds 0
+        f = x.x == kNegInf ? 1.0f : exp_approx(x.x - top);   // a chunk without a score adds 0
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     const bool none = top == kNegInf && sum == 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) static_cast<T*>(a.out)[bh * D + e * 32 + lane] = from_f32<T>(none ? 0.0f : v[e] / sum);
-    if (a.lse && lane == 0) a.lse[bh] = none ? kNegInf : (top + log2f(sum)) * (1.0f / kLog2e);
+    if (a.lse && lane == 0) a.lse[bh] = none ? kNegInf : top + logf(sum);
     return;
   }
 
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
   for (int c0 = warp;;) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float f = x[k].x == kNegInf ? 1.0f : exp2_approx(x[k].x - top);
+      const float f = x[k].x == kNegInf ? 1.0f : exp_approx(x[k].x - top);
       sum = fmaf(x[k].y, f, sum);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = fmaf(y[k][e], f, v[e]);
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     for (int w = 0; w < kJoinWarps; ++w) r += sh_o[w][d];
     static_cast<T*>(a.out)[bh * D + d] = from_f32<T>(none ? 0.0f : r / sum);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[bh] = none ? kNegInf : (top + log2f(sum)) * (1.0f / kLog2e);
+  if (a.lse && threadIdx.x == 0) a.lse[bh] = none ? kNegInf : top + logf(sum);
 }
 
 template <typename T, int D, int NT>
@@ -719,7 +718,7 @@ extern "C" int det_paged_attention(const void* q, int64_t q_stride_b, int64_t q_
   a.num_pages = (int)num_pages, a.page_size = (int)page_size, a.limit = limit;
   a.heads = (int)heads, a.group = (int)(heads / kv_heads);
   a.max_chunks = most_chunks(limit);
-  a.scale_log2 = scale * kLog2e;
+  a.scale = scale;
   a.bias = bias_table, a.bias_dtype = bias_dtype, a.bounds = bias_bounds, a.num_bounds = (int)num_bounds;
   unsigned char* ws = static_cast<unsigned char*>(workspace) + kHeaderBytes;
   a.part_ml = reinterpret_cast<float2*>(ws);

@@ -29,6 +29,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// e^x, for a difference of scores x <= 0.
+__device__ __forceinline__ float exp_approx(float x) { return exp2_approx(__fmul_rn(x, kLog2e)); }
 // The larger of two values, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

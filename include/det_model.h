@@ -131,6 +131,9 @@ int det_relative_bias_backward(const void* grad, int dtype, int64_t batch, int64
  * page_size].  The query is the sequence's last token (position n - 1), so
  * bias[j] = bias_table[number of bounds <= n - 1 - j][h] (see
  * det_relative_bias), or 0 without a table.
+ * Scores are 32-bit values in units of the natural logarithm: a finite bias,
+ * the types' lowest values included, is a finite score (what q . k adds to it is
+ * lost in the rounding), and -inf masks the token.
  * A length below 0 counts as 0, one above min(max_len, max_pages * page_size)
  * counts as that.  Tokens whose page is outside [0, num_pages) are skipped.
  * Slots past a sequence's length are not read.  Without a token, out is 0 and
