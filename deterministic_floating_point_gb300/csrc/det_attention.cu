@@ -529,14 +529,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
   __shared__ float sh_top[kJoinWarps], sh_sum[kJoinWarps];
   __shared__ float sh_o[kJoinWarps][D];
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the first kernel had waited for all before it when it let this one start
+  dep_wait();   // launched early: nothing is read before, the lengths neither
+  dep_launch();
   const int chunks = chunk_count(min(max(a.lengths[b], 0), a.limit));
   const bool few = chunks <= kWarpJoin;
-  const bool idle = chunks == 1 || (few && blockIdx.x * kJoinWarps >= a.heads);   // 1: already in place
-  if (idle && (blockIdx.x | blockIdx.y)) return;
-  dep_wait();   // in one CTA at least, so that this kernel does not end before the first
-  dep_launch();
-  if (idle) return;
+  if (chunks == 1 || (few && blockIdx.x * kJoinWarps >= a.heads)) return;   // 1: already in place
   const int h = few ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const long long bh = (long long)b * a.heads + h;
   const float2* ml = a.part_ml + bh * a.max_chunks;
