@@ -491,7 +491,10 @@ int launch_bias(const void* table, int table_dtype, int heads, const Distances& 
   } else {
     // a row has units from the one before its first boundary up
     const int unit = 16 / sizeof(T), units = (k_len + unit - 1) / unit + 1;
-    const bool aligned = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)k_len * sizeof(T)) % 16 == 0;
+    // (the tile of aligned rows in 32 bits has 16 rows, with which a grid ends a few
+    // queries before 2^20: from there on rows go 32 at a time as if unaligned)
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)k_len * sizeof(T)) % 16 == 0 &&
+                         q_len <= 65535LL * BiasTile<T, true>::kRows;
     const int threads = aligned ? BiasTile<T, true>::kThreads : BiasTile<T, false>::kThreads;
     const int rows = aligned ? BiasTile<T, true>::kRows : BiasTile<T, false>::kRows;
     const dim3 grid((unsigned)((units + threads - 1) / threads), (unsigned)((q_len + rows - 1) / rows), (unsigned)heads);
