@@ -488,7 +488,7 @@ def _logit_rows(logits: torch.Tensor):
     _unit_stride(logits, "logits")
     if len(shape) == 2:
         return shape[0], vocab, logits.stride(0)
-    rows = logits.numel() // vocab if vocab else 0
+    rows = shape[:-1].numel()   # without a vocabulary too: such rows have results
     if not logits.is_contiguous():
         raise ValueError("logits of other than two dimensions must be contiguous")
     return rows, vocab, vocab
