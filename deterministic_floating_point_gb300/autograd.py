@@ -75,7 +75,14 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor) -> tuple[torch.Te
     """(log probability of each token, entropy of each row) under softmax(logits), float32.
 
     logits is [..., vocab] (float32, bfloat16 or float16), tokens int32 of the leading shape; tokens outside the
-    vocabulary (padding) have log probability 0 and send no gradient."""
+    vocabulary (padding) have log probability 0 and send no gradient.  Any strides will do; logits whose rows do not lie at
+    one stride (logits[:, :-1] against tokens[:, 1:]) are copied, which whole logits with a token of -1 at each
+    sequence's end are not."""
+    if not tokens.is_contiguous():
+        tokens = tokens.contiguous()
+    if logits.dim() and not logits.is_contiguous() and (
+            (logits.shape[-1] > 1 and logits.stride(-1) != 1) or det._row_stride(logits) is None):
+        logits = logits.contiguous()
     return _TokenLogprobs.apply(logits, tokens)
 
 

@@ -489,9 +489,27 @@ def _logit_rows(logits: torch.Tensor):
     if len(shape) == 2:
         return shape[0], vocab, logits.stride(0)
     rows = shape[:-1].numel()   # without a vocabulary too: such rows have results
-    if not logits.is_contiguous():
-        raise ValueError("logits of other than two dimensions must be contiguous")
-    return rows, vocab, vocab
+    if logits.is_contiguous():
+        return rows, vocab, vocab
+    stride = _row_stride(logits)
+    if stride is None:
+        raise ValueError("logits of other than two dimensions must have one stride from each row to the next")
+    return rows, vocab, stride
+
+
+def _row_stride(logits: torch.Tensor) -> Optional[int]:
+    """The elements from each row of [..., vocab] logits to the next, or None if they differ (logits[:, :-1])."""
+    stride = None
+    for n, step in zip(reversed(logits.shape[:-1]), reversed(logits.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, after = step, step * n
+        elif step != after:
+            return None
+        else:
+            after *= n
+    return logits.shape[-1] if stride is None else stride
 
 
 def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top_k: int = 0,
@@ -499,7 +517,7 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
     """Log probabilities of the tokens under softmax(logits), entropy, log-sum-exp and the top_k
     alternatives of every row (see det_model.h).
 
-    logits is [..., vocab] (float32, bfloat16 or float16; two-dimensional logits may have any row stride), tokens
+    logits is [..., vocab] (float32, bfloat16 or float16) with any one stride from each row to the next, tokens
     int32 of the leading shape, or None for the other results alone.  Results are float32 of the leading shape
     (top_*: with top_k appended; top_index int32)."""
     rows, vocab, stride = _logit_rows(logits)
