@@ -17,6 +17,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import det
 
@@ -62,13 +63,25 @@ class _TokenLogprobs(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_logprob, grad_entropy):
-        logits, tokens, lse, entropy = ctx.saved_tensors
         if not ctx.needs_input_grad[0] or (grad_logprob is None and grad_entropy is None):
             return None, None
+        return _TokenLogprobsGrad.apply(*ctx.saved_tensors, grad_logprob, grad_entropy), None
+
+
+class _TokenLogprobsGrad(torch.autograd.Function):
+    """The gradient as a function of the logits, so that under create_graph its own derivative is asked for here and refused
+    (once_differentiable would notice only incoming gradients that need one)."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, lse, entropy, grad_logprob, grad_entropy):
         return det.det_token_logprobs_backward(
             logits, tokens, lse, entropy,
             grad_logprob=None if grad_logprob is None else grad_logprob.contiguous(),
-            grad_entropy=None if grad_entropy is None else grad_entropy.contiguous()), None
+            grad_entropy=None if grad_entropy is None else grad_entropy.contiguous())
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("token_logprobs has no second derivative")
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
@@ -77,7 +90,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor) -> tuple[torch.Te
     logits is [..., vocab] (float32, bfloat16 or float16), tokens int32 of the leading shape; tokens outside the
     vocabulary (padding) have log probability 0 and send no gradient.  Any strides will do; logits whose rows do not lie at
     one stride (logits[:, :-1] against tokens[:, 1:]) are copied, which whole logits with a token of -1 at each
-    sequence's end are not."""
+    sequence's end are not.  There is no second derivative."""
     if not tokens.is_contiguous():
         tokens = tokens.contiguous()
     if logits.dim() and not logits.is_contiguous() and (
@@ -96,6 +109,7 @@ class _RelativeBias(torch.autograd.Function):
         return out if batch is None else out.expand(batch, *out.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         (bounds,) = ctx.saved_tensors
         table_grad = None
@@ -112,5 +126,5 @@ def relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_len: 
     """det.det_relative_bias with a deterministic gradient for the table.
 
     With ``batch`` the result is expanded (not copied) to [batch, heads, q_len, k_len], and the gradient's sum over
-    the batch is taken with the buckets' sums, in one pass over the gradient."""
+    the batch is taken with the buckets' sums, in one pass over the gradient.  There is no second derivative."""
     return _RelativeBias.apply(table, bounds, int(q_len), int(k_len), int(q_offset), bool(bidirectional), batch, dtype)
