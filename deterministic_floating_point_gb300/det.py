@@ -435,14 +435,26 @@ def _unit_stride(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _stream_object(stream):
-    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+def _launch(device, name: str, *args):
+    """Call the library with the tensors' device as the current one: kernels are launched on that, whatever the stream, and
+    the library asks it for the number of SMs."""
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(lib(), name)(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), name)(*args)
+    if rc:
+        raise DetError(rc, name)
 
 
-def _hold(stream, *tensors):
+def _stream_object(stream, device):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _hold(stream, device, *tensors):
     """Keeps the memory of a call's inputs until the work enqueued on `stream` has read them, should the caller drop
     them before."""
-    s = _stream_object(stream)
+    s = _stream_object(stream, device)
     for t in tensors:
         if t is not None:
             t.record_stream(s)
@@ -453,7 +465,7 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     another stream still uses it), and kept from reuse while the caller's current stream works on it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    s = _stream_object(stream)
+    s = _stream_object(stream, device)
     with torch.cuda.stream(s):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
@@ -540,13 +552,10 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
         top_logprob = _empty(top_shape, f32, dev, stream)
         top_index = _empty(top_shape, torch.int32, dev, stream)
         top_lp_ptr, top_ix_ptr = top_logprob.data_ptr(), top_index.data_ptr()
-    rc = lib().det_token_logprobs(logits.data_ptr(), rows, vocab, stride, token_ptr, code, logprob_ptr,
-                                  entropy.data_ptr(), lse.data_ptr(), top_k, top_lp_ptr, top_ix_ptr,
-                                  _stream(stream, dev))
-    if rc:
-        raise DetError(rc, "det_token_logprobs")
+    _launch(dev, "det_token_logprobs", logits.data_ptr(), rows, vocab, stride, token_ptr, code, logprob_ptr,
+            entropy.data_ptr(), lse.data_ptr(), top_k, top_lp_ptr, top_ix_ptr, _stream(stream, dev))
     if stream is not None:
-        _hold(stream, logits, tokens)
+        _hold(stream, dev, logits, tokens)
     return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
 
 
@@ -575,11 +584,10 @@ def det_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Ten
     else:
         _on(dev, logits.dtype, "out", out, logits.shape, contiguous=out.dim() != 2)
     _, _, out_stride = _logit_rows(out)
-    _check(lib().det_token_logprobs_backward(_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
-                                             _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out),
-                                             out_stride, _stream(stream, dev)), "det_token_logprobs_backward")
+    _launch(dev, "det_token_logprobs_backward", _ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
+            _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out), out_stride, _stream(stream, dev))
     if stream is not None:
-        _hold(stream, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
+        _hold(stream, dev, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
     return out
 
 
@@ -639,11 +647,11 @@ def det_relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_l
         out = _empty((heads, q_len, k_len), dtype or table.dtype, table.device, stream)
     else:
         _on(table.device, dtype, "out", out, (heads, q_len, k_len))
-    _check(lib().det_relative_bias(table.data_ptr(), table_code, heads, bounds.data_ptr(), n, bool(bidirectional),
-                                   q_len, k_len, q_offset, out.data_ptr(), _model_code(out, "out"),
-                                   _stream(stream, table.device)), "det_relative_bias")
+    _launch(table.device, "det_relative_bias", table.data_ptr(), table_code, heads, bounds.data_ptr(), n,
+            bool(bidirectional), q_len, k_len, q_offset, out.data_ptr(), _model_code(out, "out"),
+            _stream(stream, table.device))
     if stream is not None:
-        _hold(stream, table, bounds, out)
+        _hold(stream, table.device, table, bounds, out)
     return out
 
 
@@ -664,12 +672,11 @@ def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_of
     out = _empty((buckets, heads), dtype, grad.device, stream)
     nbytes = lib().det_relative_bias_backward_workspace_bytes(batch, heads, q_len, k_len, n, int(bidirectional))
     ws = _model_ws(workspace, nbytes, grad.device, stream)
-    _check(lib().det_relative_bias_backward(_ptr(grad), code, batch, heads, q_len, k_len, stride_b, grad.stride(-3),
-                                            grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset),
-                                            _ptr(out), _model_code(out, "dtype"), _ptr(ws), ws.numel(),
-                                            _stream(stream, grad.device)), "det_relative_bias_backward")
+    _launch(grad.device, "det_relative_bias_backward", _ptr(grad), code, batch, heads, q_len, k_len, stride_b,
+            grad.stride(-3), grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset), _ptr(out),
+            _model_code(out, "dtype"), _ptr(ws), ws.numel(), _stream(stream, grad.device))
     if stream is not None:
-        _hold(stream, grad, bounds, workspace)
+        _hold(stream, grad.device, grad, bounds, workspace)
     return out
 
 
@@ -751,17 +758,15 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     else:
         _on(dev, dtype, "out", out, (batch, heads, dim))
     lse = _empty((batch, heads), torch.float32, dev, stream)
-    call = lib()
-    ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
-    rc = call.det_paged_attention(
+    ws = _model_ws(workspace, lib().det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
+    _launch(
+        dev, "det_paged_attention",
         q.data_ptr(), q_batch, q_head, k_ptr, k_page, k_token, k_head, v_ptr, v_page, v_token, v_head, pages, page_size,
         block_table.data_ptr(), table_stride, max_pages, lengths.data_ptr(), batch, heads, kv_heads, dim, code,
         dim ** -0.5 if scale is None else scale, bias_ptr, bias_code, bounds_ptr, n_bounds, limit, out.data_ptr(),
         lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev))
-    if rc:
-        raise DetError(rc, "det_paged_attention")
     if stream is not None:
-        _hold(stream, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
+        _hold(stream, dev, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
     return PagedAttention(out, lse)
 
 
