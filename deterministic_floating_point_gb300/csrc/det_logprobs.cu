@@ -186,7 +186,15 @@ constexpr int kStageBytes = kChunkBytes + 32;   // a row's start modulo 16, and 
 struct Stream {
   alignas(16) unsigned char stage[kStages][kStageBytes];
   unsigned long long full[kStages], empty[kStages];
+  int filled[kStages];   // the round of the stage's last copy, or -1
 };
+// The copies that are still on their way, waited for by one thread (each for at
+// most kWaitNs): after a wait has given up, before the stages serve anything else
+// or the CTA ends.  Round r of a stage completes phase r of its barrier.
+__device__ __noinline__ void land_copies(Stream& st) {
+  for (int i = 0; i < kStages; ++i)
+    if (st.filled[i] >= 0) mbar_wait(&st.full[i], st.filled[i] & 1, kWaitNs);
+}
 
 // Where the parts of a row lie.
 template <typename T>
@@ -515,6 +523,16 @@ __device__ __noinline__ void fill_equal(Found<T> found, unsigned equal, const Ro
   }
 }
 
+// The alternatives that were not found, in a row given up (one warp): index -1.
+__device__ __noinline__ void fill_missing(const RowEnd& end, int top_k, long long r, const RowOut& out) {
+  const int lane = threadIdx.x & 31;
+  const int found = (int)__reduce_add_sync(0xffffffffu, lane < kRowWarps ? (unsigned)end.count[lane] : 0u);
+  for (int rank = found + lane; rank < top_k; rank += 32) {
+    if (out.top_index) out.top_index[r * top_k + rank] = -1;
+    if (out.top_logprob) out.top_logprob[r * top_k + rank] = __uint_as_float(0x7fc00000u);
+  }
+}
+
 // The threads' statistics joined, the row's results and its top_k largest
 // elements: only threads whose best reaches the k-th best of the warps' best
 // ones are looked through again, as jobs that the warps share.
@@ -670,7 +688,10 @@ __device__ __forceinline__ void finish_row(Stat st, const Best& best, const T* r
       if (out.top_index) out.top_index[r * top_k + rank] = (int32_t)~(unsigned)key;
       if (out.top_logprob) out.top_logprob[r * top_k + rank] = (key_value((unsigned)(key >> 32)) - base) - log_s;
     }
-    if (found.floor_key != floor_key && warp == 0) fill_equal(found, floor_key, end, top_k, base, log_s, r, out);
+    if (warp == 0) {
+      if (found.floor_key != floor_key) fill_equal(found, floor_key, end, top_k, base, log_s, r, out);
+      else if (isnan(m)) fill_missing(end, top_k, r, out);
+    }
   }
 }
 
@@ -682,7 +703,8 @@ static_assert(sizeof(PartStats) <= sizeof(Stream::stage), "it fits the stages");
 
 // Persistent: CTA b takes the rows b, b + gridDim.x, ...; SPLIT: a cluster of a
 // CTA per part takes a row (1 x 131,072 bf16: 17 us -> 12).  A wait for a copy that
-// does not end within kWaitNs gives up: the row's results are NaN then.
+// does not end within kWaitNs gives up: the row's results, and those of the CTA's
+// rows after it, are NaN then.
 template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kRowThreads, 2)
 token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_stride, const int32_t* tokens, int top_k,
@@ -701,6 +723,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&stream.full[i], 1);
       mbar_init(&stream.empty[i], kRowWarps);
+      stream.filled[i] = -1;
     }
   }
   __syncthreads();
@@ -714,7 +737,10 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     if (next_row >= rows) return;
     if (mine) {
       if (next_round > 0 && !gave_up) gave_up = !mbar_wait(&stream.empty[next_stage], (next_round - 1) & 1, kWaitNs);
-      if (!gave_up) RowMap<T>(logits + next_row * row_stride, vocab).fetch(stream, next_stage, next_chunk);
+      if (!gave_up) {
+        stream.filled[next_stage] = next_round;
+        RowMap<T>(logits + next_row * row_stride, vocab).fetch(stream, next_stage, next_chunk);
+      }
     }
     if (++next_chunk == c1) {
       next_chunk = c0;
@@ -816,7 +842,10 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
       }
     }
     if (SPLIT) {
-      __syncthreads();   // the stages have been read
+      if (__syncthreads_or(gave_up)) {   // the stages have been read
+        if (threadIdx.x == 0) land_copies(stream);
+        __syncthreads();
+      }
       PartStats& left = *reinterpret_cast<PartStats*>(stream.stage);
       left.m[threadIdx.x] = gave_up ? __uint_as_float(0x7fc00000u) : st.m;
       left.s[threadIdx.x] = st.s;
@@ -839,6 +868,7 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
     }
     finish_row(all, all_best, map.row, vocab, r, token, top_k, end, out);
   }
+  if (!SPLIT && __syncthreads_or(gave_up) && threadIdx.x == 0) land_copies(stream);
 }
 
 // ---------------------------------------------------------------------------

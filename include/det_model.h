@@ -46,7 +46,9 @@ extern "C" {
  * A token outside [0, vocab) is skipped: its logprob is +0.0.  A logit of
  * -inf is a masked one (probability 0).  A row with no logit above -inf has
  * lse = logprob = -inf and entropy 0.  A row that holds NaN or +inf has NaN
- * results (top_index_out still names the largest).
+ * results (top_index_out still names the largest).  So does, as the only sign of
+ * it, a row whose logits could not be copied into shared memory in time (2 s; the
+ * kernel ends all the same); alternatives that were not found have index -1.
  *   logits       device, rows x vocab of dtype; row r starts at element
  *                r * row_stride, any alignment
  *   tokens       device, rows int32, or NULL when logprob_out is
