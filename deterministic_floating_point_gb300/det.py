@@ -435,16 +435,17 @@ def _unit_stride(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _launch(device, name: str, *args):
-    """Call the library with the tensors' device as the current one: kernels are launched on that, whatever the stream, and
-    the library asks it for the number of SMs."""
-    if torch.cuda.current_device() == device.index:
-        rc = getattr(lib(), name)(*args)
-    else:
-        with torch.cuda.device(device):
-            rc = getattr(lib(), name)(*args)
-    if rc:
-        raise DetError(rc, name)
+# torch.cuda.current_device() without its check that CUDA is initialized, which it is where there are CUDA tensors
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _run(device, fn, args):
+    """fn(*args), a call of the library, with the tensors' device as the current one: kernels are launched on that, whatever
+    the stream, and the library asks it for the number of SMs."""
+    if _current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _stream_object(stream, device):
@@ -552,8 +553,11 @@ def det_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = No
         top_logprob = _empty(top_shape, f32, dev, stream)
         top_index = _empty(top_shape, torch.int32, dev, stream)
         top_lp_ptr, top_ix_ptr = top_logprob.data_ptr(), top_index.data_ptr()
-    _launch(dev, "det_token_logprobs", logits.data_ptr(), rows, vocab, stride, token_ptr, code, logprob_ptr,
-            entropy.data_ptr(), lse.data_ptr(), top_k, top_lp_ptr, top_ix_ptr, _stream(stream, dev))
+    rc = _run(dev, lib().det_token_logprobs, (logits.data_ptr(), rows, vocab, stride, token_ptr, code, logprob_ptr,
+                                              entropy.data_ptr(), lse.data_ptr(), top_k, top_lp_ptr, top_ix_ptr,
+                                              _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_token_logprobs")
     if stream is not None:
         _hold(stream, dev, logits, tokens)
     return TokenLogprobs(logprob, entropy, lse, top_logprob, top_index)
@@ -584,8 +588,9 @@ def det_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Ten
     else:
         _on(dev, logits.dtype, "out", out, logits.shape, contiguous=out.dim() != 2)
     _, _, out_stride = _logit_rows(out)
-    _launch(dev, "det_token_logprobs_backward", _ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse),
-            _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), _ptr(out), out_stride, _stream(stream, dev))
+    _check(_run(dev, lib().det_token_logprobs_backward,
+                (_ptr(logits), rows, vocab, stride, _ptr(tokens), code, _ptr(lse), _ptr(entropy), _ptr(grad_logprob),
+                 _ptr(grad_entropy), _ptr(out), out_stride, _stream(stream, dev))), "det_token_logprobs_backward")
     if stream is not None:
         _hold(stream, dev, logits, tokens, lse, entropy, grad_logprob, grad_entropy, out)
     return out
@@ -647,11 +652,12 @@ def det_relative_bias(table: torch.Tensor, bounds: torch.Tensor, q_len: int, k_l
         out = _empty((heads, q_len, k_len), dtype or table.dtype, table.device, stream)
     else:
         _on(table.device, dtype, "out", out, (heads, q_len, k_len))
-    _launch(table.device, "det_relative_bias", table.data_ptr(), table_code, heads, bounds.data_ptr(), n,
-            bool(bidirectional), q_len, k_len, q_offset, out.data_ptr(), _model_code(out, "out"),
-            _stream(stream, table.device))
+    dev = table.device
+    _check(_run(dev, lib().det_relative_bias,
+                (table.data_ptr(), table_code, heads, bounds.data_ptr(), n, bool(bidirectional), q_len, k_len, q_offset,
+                 out.data_ptr(), _model_code(out, "out"), _stream(stream, dev))), "det_relative_bias")
     if stream is not None:
-        _hold(stream, table.device, table, bounds, out)
+        _hold(stream, dev, table, bounds, out)
     return out
 
 
@@ -672,11 +678,13 @@ def det_relative_bias_backward(grad: torch.Tensor, bounds: torch.Tensor, *, q_of
     out = _empty((buckets, heads), dtype, grad.device, stream)
     nbytes = lib().det_relative_bias_backward_workspace_bytes(batch, heads, q_len, k_len, n, int(bidirectional))
     ws = _model_ws(workspace, nbytes, grad.device, stream)
-    _launch(grad.device, "det_relative_bias_backward", _ptr(grad), code, batch, heads, q_len, k_len, stride_b,
-            grad.stride(-3), grad.stride(-2), _ptr(bounds), n, int(bidirectional), int(q_offset), _ptr(out),
-            _model_code(out, "dtype"), _ptr(ws), ws.numel(), _stream(stream, grad.device))
+    dev = grad.device
+    _check(_run(dev, lib().det_relative_bias_backward,
+                (_ptr(grad), code, batch, heads, q_len, k_len, stride_b, grad.stride(-3), grad.stride(-2), _ptr(bounds), n,
+                 int(bidirectional), int(q_offset), _ptr(out), _model_code(out, "dtype"), _ptr(ws), ws.numel(),
+                 _stream(stream, dev))), "det_relative_bias_backward")
     if stream is not None:
-        _hold(stream, grad.device, grad, bounds, workspace)
+        _hold(stream, dev, grad, bounds, workspace)
     return out
 
 
@@ -758,13 +766,15 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     else:
         _on(dev, dtype, "out", out, (batch, heads, dim))
     lse = _empty((batch, heads), torch.float32, dev, stream)
-    ws = _model_ws(workspace, lib().det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
-    _launch(
-        dev, "det_paged_attention",
+    call = lib()
+    ws = _model_ws(workspace, call.det_paged_attention_workspace_bytes(batch, heads, dim, limit), dev, stream)
+    rc = _run(dev, call.det_paged_attention, (
         q.data_ptr(), q_batch, q_head, k_ptr, k_page, k_token, k_head, v_ptr, v_page, v_token, v_head, pages, page_size,
         block_table.data_ptr(), table_stride, max_pages, lengths.data_ptr(), batch, heads, kv_heads, dim, code,
         dim ** -0.5 if scale is None else scale, bias_ptr, bias_code, bounds_ptr, n_bounds, limit, out.data_ptr(),
-        lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev))
+        lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_paged_attention")
     if stream is not None:
         _hold(stream, dev, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
     return PagedAttention(out, lse)

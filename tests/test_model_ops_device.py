@@ -41,7 +41,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(det, "lib", lambda: Library())
     monkeypatch.setattr(det, "_raw_stream", lambda index: 1000 + index)
     monkeypatch.setattr(det, "_empty", lambda shape, dtype, device, stream: on_device(torch.empty(shape, dtype=dtype)))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["current"])
+    monkeypatch.setattr(det, "_current_device", lambda: state["current"])
     monkeypatch.setattr(torch.cuda, "device", device)
     return state
 
