@@ -57,3 +57,19 @@ def test_shifted_logits(det, vocab):
     many = det.det_token_logprobs(x.repeat(40, 1), t.repeat(40))
     assert torch.equal(many.logprob.view(40, -1), r.logprob.expand(40, -1))
     assert torch.equal(many.entropy.view(40, -1), r.entropy.expand(40, -1))
+
+
+@pytest.mark.parametrize("vocab", [1000, 40_003])
+@pytest.mark.parametrize("spread", [0, 3, 40])
+def test_around_two_to_the_24(det, vocab, spread):
+    """Where 32-bit logits become 2 apart, and rows whose logits lie on both sides of it."""
+    rng = np.random.default_rng(spread)
+    at = np.asarray([1.6e7, -1.6e7, 2.0 ** 24, -2.0 ** 24, 2.0 ** 24 + 2, -2.0 ** 24 - 2, 2.0 ** 24 - 1, 1 - 2.0 ** 24, 5e7, -5e7])
+    x = torch.from_numpy((rng.integers(-spread, spread + 1, (len(at), vocab)) + at[:, None]).astype(np.float32)).cuda()
+    tokens = rng.integers(0, vocab, len(at)).astype(np.int32)
+    r = det.det_token_logprobs(x, torch.from_numpy(tokens).cuda())
+    check(r, x, tokens)
+    y = x.clone()                                   # a mask's size in most of a row
+    y[:, vocab // 4:] = torch.from_numpy(-np.abs(at).astype(np.float32)).cuda()[:, None]
+    y[:, 5] = 1.0
+    check(det.det_token_logprobs(y, torch.from_numpy(tokens).cuda()), y, tokens)
