@@ -141,8 +141,16 @@ template <typename T> __device__ __forceinline__ float2 unpack2(unsigned w) {
   return make_float2(to_f32(*reinterpret_cast<const T*>(&lo)), to_f32(*reinterpret_cast<const T*>(&hi)));
 }
 
-// What the weights are multiplied by in the second product, and the outputs
-// divided by at its end.
+// How the weights of the softmax, at most 1, enter the second product: as 16-bit
+// parts that add up to 32-bit accuracy, three of bf16's 8 bits or two of f16's 11.
+// f16's smallest normal value is 2^-14, so there they are scaled by 2^15 (exact; the
+// outputs are divided by it at the end): held to 2^-22 of themselves from 2^-18 of
+// the largest on, and to 2^-40 of the largest below.  A third part in bf16 costs 0 to
+// 1.5% with up to 8 heads in a group and 4% with 16 (32 sequences of 8,192 tokens, 32
+// heads on 8 x 128, 172.3 and 171.2 us; 32 of 32,768, 32 on 2, 202.4 and 194.4);
+// with two, 1.6e-3 to 2.7e-3 of the outputs are not the exact results rounded,
+// with three 3e-4 to 9e-4, and as many or more if all is done in 32 bits.
+template <typename T> constexpr int kWeightParts = std::is_same<T, __half>::value ? 2 : 3;
 template <typename T> constexpr float kWeightScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
 
 // Number of bounds <= n.
@@ -417,12 +425,9 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
           }
         }
     }
-    // the weights as B operands (column = head), in two parts: the weight
-    // rounded to 16 bits and what the rounding left.  Held so to 2^-17 of
-    // themselves in bf16; in f16, whose smallest normal value is 2^-14, they are
-    // scaled by 2^15 (exact, and at most f16's 2^15): to 2^-22 of themselves from
-    // 2^-18 of the largest on, and to 2^-40 of the largest below.
-    unsigned ph[NT][2], pl[NT][2];
+    // the weights as B operands (column = head), in parts: the weight rounded to
+    // 16 bits, and what the rounding left rounded again
+    unsigned pw[kWeightParts<T>][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float(&p)[4] = s[nt];
@@ -435,11 +440,14 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float p0 = p[2 * half] * kWeightScale<T>, p1 = p[2 * half + 1] * kWeightScale<T>;
-        const unsigned hi = pack2<T>(p0, p1);
-        const float2 r = unpack2<T>(hi);
-        ph[nt][half] = movmatrix_trans(hi);
-        pl[nt][half] = movmatrix_trans(pack2<T>(p0 - r.x, p1 - r.y));
+        float2 left = make_float2(p[2 * half] * kWeightScale<T>, p[2 * half + 1] * kWeightScale<T>);
+#pragma unroll
+        for (int part = 0; part < kWeightParts<T>; ++part) {
+          const unsigned w = pack2<T>(left.x, left.y);
+          const float2 r = unpack2<T>(w);
+          left = make_float2(left.x - r.x, left.y - r.y);   // exact
+          pw[part][nt][half] = movmatrix_trans(w);
+        }
       }
     }
     cp_async_wait<kValues>();   // and its values
@@ -451,10 +459,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
         unsigned af[4];
         ldmatrix_x4_trans(af, row + 32 * i);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816<T>(o[i][nt], af, ph[nt][0], ph[nt][1]);
-          mma_16816<T>(o[i][nt], af, pl[nt][0], pl[nt][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int part = 0; part < kWeightParts<T>; ++part)
+            mma_16816<T>(o[i][nt], af, pw[part][nt][0], pw[part][nt][1]);
       }
     }
     __syncwarp();   // its keys and values have been read
