@@ -149,7 +149,7 @@ template <typename T> __device__ __forceinline__ float2 unpack2(unsigned w) {
 // 1.5% with up to 8 heads in a group and 4% with 16 (32 sequences of 8,192 tokens, 32
 // heads on 8 x 128, 172.3 and 171.2 us; 32 of 32,768, 32 on 2, 202.4 and 194.4);
 // with two, 1.6e-3 to 2.7e-3 of the outputs are not the exact results rounded,
-// with three 3e-4 to 9e-4, and as many or more if all is done in 32 bits.
+// with three 3e-4 to 9e-4, and 2e-4 to 1.7e-3 if all is done in 32 bits.
 template <typename T> constexpr int kWeightParts = std::is_same<T, __half>::value ? 2 : 3;
 template <typename T> constexpr float kWeightScale = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
 
@@ -171,13 +171,13 @@ __device__ __forceinline__ int bounds_at_most(const int32_t* bounds, int count, 
 //
 // Bound by the reads of keys and values (both kernels; fraction of the measured
 // copy bandwidth): 32 sequences of 8,192 tokens, 8 kv heads of 128 dims for 32
-// heads 171 us (92%), for 8 heads 167 us (95%); of 64 dims 95 us (83%), of 256 dims
-// and 16 sequences 175 us (90%).  About 10 us of a call are its own: the CTAs'
+// heads 173 us (91%), for 8 heads 166 us (95%); of 64 dims 97 us (81%), of 256 dims
+// and 16 sequences 176 us (90%).  About 10 us of a call are its own: the CTAs'
 // first tiles, the last ones, which do not fill the SMs, and the join (of 64 dims
-// 128 sequences 345 us, 92%).  With short chunks a CTA's start and end (length,
+// 128 sequences 351 us, 90%).  With short chunks a CTA's start and end (length,
 // page, first tile and join of the warps, some 4 us against 1.3 us a tile) show:
-// 128 sequences of 500 tokens 48 us (80%), 64 ragged ones of up to 8,191 tokens
-// of 64 dims with the bias 59 us (72%).  Copying whole rows by the bulk engine was
+// 128 sequences of 500 tokens 49 us (79%), 64 ragged ones of up to 8,191 tokens
+// of 64 dims with the bias 60 us (70%).  Copying whole rows by the bulk engine was
 // slower (a copy of 256 bytes every 20 cycles an SM: 296 us for 32 x 8,192).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attention_chunks_kernel(const __grid_constant__ AttnArgs a) {
@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreads, Tile<D>::ctas(NT)) attentio
 // ..., and the warps are added in order.  Its CTAs are on the SMs before the
 // first kernel ends.  A dependent chain of reads of L2 and the sum; what a CTA a
 // head costs is their number (256 sequences of up to 2,000 tokens, 32 heads of 64
-// dims, both kernels: 69 us, with a warp a head 58; 8 of 8,192, 128 dims: 49 and 50).
+// dims, both kernels: 69 us, with a warp a head 58; 8 of 8,192, 128 dims: 49 and 50;
+// since lengths are read after the wait, 1 to 2 us more).
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnArgs a) {

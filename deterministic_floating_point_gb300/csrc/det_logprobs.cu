@@ -878,7 +878,9 @@ token_logprobs_kernel(const T* logits, long long rows, int vocab, long long row_
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;   // 16-byte vectors of a thread
 // From this magnitude on 32 bits hold lse to 2^-14 or worse (nothing of log S
-// is left of it in a row at the types' lowest values): the row is summed again.
+// is left of it in a row at the types' lowest values): the row is summed again, by
+// each of its CTAs, which read the whole row twice more.  Ten times the time where
+// every row is so (1,021 x 100,003 f32 1,176 us instead of 119; a tenth of them 230).
 constexpr float kLseFar = 1024.0f;
 
 // The maximum and the log of the sum relative to it of a whole row.

@@ -69,8 +69,9 @@ int det_token_logprobs(const void* logits, int64_t rows, int64_t vocab, int64_t 
  * rows without a logit above -inf get 0.
  *   lse, entropy   device, rows floats each: det_token_logprobs' results
  *                  (entropy may be NULL when grad_entropy is).  Where |lse| is
- *                  finite and 1024 or more, log p is taken from the row again:
- *                  32 bits do not hold lse well enough there
+ *                  finite and 1024 or more, log p is taken from the row again
+ *                  (up to ten times the time of such a row): 32 bits do not hold
+ *                  lse well enough there
  *   grad_logprob, grad_entropy  device, rows floats each; either may be NULL (0)
  *   tokens         may be NULL when grad_logprob is
  *   grad_logits    device, rows x vocab of dtype (written), row r at element
@@ -114,7 +115,9 @@ int det_relative_bias(const void* table, int table_dtype, int64_t heads, const i
  *   grad_table  device, buckets x heads of table_dtype, contiguous (written)
  * Limits: |q_offset| + q_len + k_len <= 2^30, num_bounds <= DET_MAX_BOUNDS,
  * heads <= 65,535, batch x (q_len / 64 + 1) x (k_len / 248 + 2) below 2^31;
- * strides are not negative.
+ * strides are not negative.  The workspace is heads x buckets x (the tiles of that
+ * product) floats: 4.7 MB for 8 x 16 x 2,048 x 2,048 and 32 buckets, 604 MB with
+ * 4,096 of them.
  */
 size_t det_relative_bias_backward_workspace_bytes(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len,
                                                   int64_t num_bounds, int bidirectional);
