@@ -1,5 +1,6 @@
 // Shared helpers of the language-model operators (det_logprobs.cu,
-// det_relbias.cu, det_attention.cu): the 16-bit types, and exponentials.
+// det_relbias.cu, det_attention.cu, det_embedding.cu, det_layernorm.cu,
+// det_recurrence.cu): the 16-bit types, exponentials, and eights of elements.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -59,6 +60,94 @@ __device__ __forceinline__ void store_from_f32(void* p, long long i, float v, in
   if (dtype == DET_F32) static_cast<float*>(p)[i] = v;
   else if (dtype == DET_BF16) static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
   else static_cast<__half*>(p)[i] = from_f32<__half>(v);
+}
+
+// Eight consecutive elements as they lie in memory: one 16-byte vector in 16
+// bits, two in 32.
+template <typename T> struct Eight { uint4 q; };
+template <> struct Eight<float> { uint4 q, r; };
+
+// n of the eight elements at p (the others 0).  VEC: p is 16-byte aligned and n is
+// 0 or 8 in 16 bits, 0, 4 or 8 in 32.
+template <bool VEC, typename T>
+__device__ __forceinline__ Eight<T> load_eight(const T* p, int n) {
+  Eight<T> e;
+  e.q = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (n > 0) e.q = *reinterpret_cast<const uint4*>(p);
+  } else {
+    unsigned w[4] = {0, 0, 0, 0};
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i >> 1] |= (unsigned)h[i] << (16 * (i & 1));
+    e.q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return e;
+}
+template <bool VEC>
+__device__ __forceinline__ Eight<float> load_eight(const float* p, int n) {
+  Eight<float> e;
+  e.q = e.r = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (n > 0) e.q = *reinterpret_cast<const uint4*>(p);
+    if (n > 4) e.r = *reinterpret_cast<const uint4*>(p + 4);
+  } else {
+    unsigned w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < n ? reinterpret_cast<const unsigned*>(p)[i] : 0u;
+    e.q = make_uint4(w[0], w[1], w[2], w[3]);
+    e.r = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  return e;
+}
+__device__ __forceinline__ void unpack_eight(const Eight<float>& e, float (&v)[8]) {
+  v[0] = __uint_as_float(e.q.x), v[1] = __uint_as_float(e.q.y), v[2] = __uint_as_float(e.q.z), v[3] = __uint_as_float(e.q.w);
+  v[4] = __uint_as_float(e.r.x), v[5] = __uint_as_float(e.r.y), v[6] = __uint_as_float(e.r.z), v[7] = __uint_as_float(e.r.w);
+}
+__device__ __forceinline__ void unpack_two(unsigned w, float& a, float& b, __nv_bfloat16) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_two(unsigned w, float& a, float& b, __half) {
+  a = __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+  b = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+template <typename T>
+__device__ __forceinline__ void unpack_eight(const Eight<T>& e, float (&v)[8]) {
+  unpack_two(e.q.x, v[0], v[1], T());
+  unpack_two(e.q.y, v[2], v[3], T());
+  unpack_two(e.q.z, v[4], v[5], T());
+  unpack_two(e.q.w, v[6], v[7], T());
+}
+__device__ __forceinline__ unsigned short bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+__device__ __forceinline__ unsigned short bits16(__half v) { return __half_as_ushort(v); }
+template <typename T>
+__device__ __forceinline__ unsigned pack_two(float a, float b) {
+  return (unsigned)bits16(from_f32<T>(a)) | (unsigned)bits16(from_f32<T>(b)) << 16;
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_eight(T* p, const float (&v)[8], int n) {
+  if constexpr (VEC) {
+    if (n > 0)
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack_two<T>(v[0], v[1]), pack_two<T>(v[2], v[3]), pack_two<T>(v[4], v[5]), pack_two<T>(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = from_f32<T>(v[i]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_eight(float* p, const float (&v)[8], int n) {
+  if constexpr (VEC) {
+    if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    if (n > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
 }
 
 inline bool valid_model_dtype(int dtype) { return dtype == DET_F32 || dtype == DET_BF16 || dtype == DET_F16; }

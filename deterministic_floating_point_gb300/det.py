@@ -67,6 +67,17 @@ _SIGNATURES = {
     "det_paged_attention": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
                                    _i64, _i64, _vp, _i64, _i64, _i64, _i64, _int, _flt, _vp, _int, _vp, _i64, _i64,
                                    _vp, _vp, _vp, _sz, _vp]),
+    "det_embedding": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _flt, _vp, _int, _vp]),
+    "det_embedding_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "det_embedding_backward": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _flt, _vp, _int, _i64, _int, _vp, _sz, _vp]),
+    "det_layer_norm": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _flt, _vp, _vp, _vp, _vp]),
+    "det_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "det_layer_norm_backward": (_int, [_vp, _i64, _vp, _i64, _int, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp,
+                                       _sz, _vp]),
+    "det_linear_recurrence": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _int, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
+                                     _vp, _vp]),
+    "det_linear_recurrence_backward": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _int, _int, _i64, _i64,
+                                              _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "det_read_status": (_int, [_vp, _vp, ctypes.POINTER(_int)]),
     "det_status_string": (ctypes.c_char_p, [_int]),
     "det_last_cuda_error": (ctypes.c_char_p, []),
@@ -778,6 +789,274 @@ def det_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if stream is not None:
         _hold(stream, dev, q, k_cache, v_cache, block_table, lengths, bias_table, bias_bounds, out, workspace)
     return PagedAttention(out, lse)
+
+
+def det_embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
+                  dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[..., :] = scale * table[tokens[...], :], rounded once (see det_model.h).
+
+    table is [vocab, dim] (float32, bfloat16 or float16) with any stride from row to row, tokens int32 of any shape; a
+    token outside the vocabulary gives a row of zeros.  The result has the table's dtype unless dtype or out says
+    otherwise."""
+    dev = table.device
+    _on(None, None, "table", table, None, False)
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, dim]")
+    vocab, dim = table.shape
+    _unit_stride(table, "table")
+    _on(dev, torch.int32, "tokens", tokens)
+    shape = (*tokens.shape, dim)
+    if out is None:
+        out = _empty(shape, dtype or table.dtype, dev, stream)
+    else:
+        _on(dev, dtype, "out", out, shape)
+    rc = _run(dev, lib().det_embedding, (table.data_ptr(), _model_code(table, "table"), vocab, dim, table.stride(0),
+                                         tokens.data_ptr(), tokens.numel(), scale, out.data_ptr(),
+                                         _model_code(out, "out"), _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_embedding")
+    if stream is not None:
+        _hold(stream, dev, table, tokens, out)
+    return out
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, elements from one row to the next) of a [..., columns] tensor."""
+    _on(None, None, name, t, None, False)
+    shape = t.shape
+    if len(shape) < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = shape[-1]
+    if t.is_contiguous():
+        return shape[:-1].numel(), cols, cols
+    _unit_stride(t, name)
+    stride = _row_stride(t)
+    if stride is None:
+        raise ValueError(f"{name} must have one stride from each row to the next")
+    return shape[:-1].numel(), cols, stride
+
+
+def det_embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, *, scale: float = 1.0,
+                           dtype: Optional[torch.dtype] = None, grad_table: Optional[torch.Tensor] = None,
+                           accumulate: bool = False, workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """The gradient for det_embedding's table, [vocab, dim] (see det_model.h): scale times the rows of grad ([..., dim])
+    summed over each token's places, in the order of det_scatter_add_rows.
+
+    It has grad's dtype unless dtype or grad_table says otherwise.  With accumulate it is added to what grad_table
+    holds."""
+    n, dim, stride = _rows(grad, "grad")
+    code, dev = _model_code(grad, "grad"), grad.device
+    _on(dev, torch.int32, "tokens", tokens, grad.shape[:-1])
+    if grad_table is None:
+        if accumulate:
+            raise ValueError("accumulate needs the grad_table to add to")
+        grad_table = _empty((vocab, dim), dtype or grad.dtype, dev, stream)
+    else:
+        _on(dev, dtype, "grad_table", grad_table, (vocab, dim))
+    call = lib()
+    ws = _model_ws(workspace, call.det_embedding_backward_workspace_bytes(n, vocab, dim), dev, stream)
+    rc = _run(dev, call.det_embedding_backward,
+              (grad.data_ptr(), code, n, dim, stride, tokens.data_ptr(), scale, grad_table.data_ptr(),
+               _model_code(grad_table, "grad_table"), vocab, bool(accumulate), ws.data_ptr(), ws.numel(),
+               _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_embedding_backward")
+    if stream is not None:
+        _hold(stream, dev, grad, tokens, grad_table, workspace)
+    return grad_table
+
+
+class LayerNorm(NamedTuple):
+    out: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+
+
+def _norm_param(dev, dtype, name: str, t: Optional[torch.Tensor], cols: int):
+    if t is None:
+        return None
+    return _on(dev, dtype, name, t, (cols,)).data_ptr()
+
+
+def det_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
+                   eps: float = 1e-5, out: Optional[torch.Tensor] = None, stream=None) -> LayerNorm:
+    """(x - mean) * rstd * weight + bias over the last dimension (see det_model.h), with the rows' mean and rstd (float32).
+
+    x is [..., cols] (float32, bfloat16 or float16, at most 16,384 columns) with one stride from each row to the
+    next; weight and bias are [cols], of x's or another of these types, but of one."""
+    rows, cols, stride = _rows(x, "x")
+    code, dev, lead = _model_code(x, "x"), x.device, x.shape[:-1]
+    param = weight if weight is not None else bias
+    param_code = code if param is None else _model_code(param, "weight")
+    weight_ptr = _norm_param(dev, None, "weight", weight, cols)
+    bias_ptr = _norm_param(dev, None if param is None else param.dtype, "bias", bias, cols)
+    if out is None:
+        out = _empty(x.shape, x.dtype, dev, stream)
+    else:
+        _on(dev, x.dtype, "out", out, x.shape)
+    mean = _empty(lead, torch.float32, dev, stream)
+    rstd = _empty(lead, torch.float32, dev, stream)
+    rc = _run(dev, lib().det_layer_norm, (x.data_ptr(), code, rows, cols, stride, weight_ptr, bias_ptr, param_code, eps,
+                                          out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_layer_norm")
+    if stream is not None:
+        _hold(stream, dev, x, weight, bias, out)
+    return LayerNorm(out, mean, rstd)
+
+
+class LayerNormGrads(NamedTuple):
+    x: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+
+
+def det_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                            weight: Optional[torch.Tensor] = None, *, dtype: Optional[torch.dtype] = None,
+                            want_x: bool = True, want_weight: bool = True, want_bias: bool = True,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> LayerNormGrads:
+    """The gradients for x, weight and bias of det_layer_norm (see det_model.h); mean and rstd are its results.
+
+    The weight's and the bias' gradients have the weight's dtype, or without a weight dtype (float32 by default).
+    Those that are not wanted are None."""
+    rows, cols, x_stride = _rows(x, "x")
+    code, dev, lead = _model_code(x, "x"), x.device, x.shape[:-1]
+    _on(dev, x.dtype, "grad", grad, x.shape, False)
+    _, _, grad_stride = _rows(grad, "grad")
+    _on(dev, torch.float32, "mean", mean, lead)
+    _on(dev, torch.float32, "rstd", rstd, lead)
+    weight_ptr = None
+    if weight is not None:
+        weight_ptr = _on(dev, dtype, "weight", weight, (cols,)).data_ptr()
+        dtype = weight.dtype
+    elif dtype is None:
+        dtype = torch.float32
+    param_code = _MODEL_CODES.get(dtype)
+    if param_code is None:
+        raise TypeError(f"dtype must be one of {[str(d) for d in _MODEL_CODES]}, got {dtype}")
+    grad_x = _empty(x.shape, x.dtype, dev, stream) if want_x else None
+    grad_weight = _empty((cols,), dtype, dev, stream) if want_weight else None
+    grad_bias = _empty((cols,), dtype, dev, stream) if want_bias else None
+    call, ws_ptr, ws_bytes = lib(), None, 0
+    if want_weight or want_bias:
+        ws = _model_ws(workspace, call.det_layer_norm_backward_workspace_bytes(rows, cols), dev, stream)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
+    rc = _run(dev, call.det_layer_norm_backward,
+              (grad.data_ptr(), grad_stride, x.data_ptr(), x_stride, code, rows, cols, mean.data_ptr(), rstd.data_ptr(),
+               weight_ptr, param_code, _ptr(grad_x), _ptr(grad_weight), _ptr(grad_bias), ws_ptr, ws_bytes,
+               _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_layer_norm_backward")
+    if stream is not None:
+        _hold(stream, dev, grad, x, mean, rstd, weight, workspace)
+    return LayerNormGrads(grad_x, grad_weight, grad_bias)
+
+
+GATE_FORMS = {"decay": 0, "sigmoid": 1}
+RECURRENCE_KEEP, RECURRENCE_SPAN = 128, 1024    # det_model.h
+
+
+class LinearRecurrence(NamedTuple):
+    out: torch.Tensor
+    final: torch.Tensor
+    states: Optional[torch.Tensor]
+
+
+def _steps(device, dtype, name: str, t: torch.Tensor, shape):
+    """(pointer, strides of sequences and steps) of a [batch, time, channels] tensor."""
+    _on(device, dtype, name, t, shape, False)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [batch, time, channels]")
+    _unit_stride(t, name)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _gate_form(form: str) -> int:
+    code = GATE_FORMS.get(form)
+    if code is None:
+        raise ValueError(f"form must be one of {sorted(GATE_FORMS)}, got {form!r}")
+    return code
+
+
+def det_linear_recurrence(x: torch.Tensor, gate: torch.Tensor, initial: Optional[torch.Tensor] = None, *,
+                          form: str = "sigmoid", lengths: Optional[torch.Tensor] = None, keep_states: bool = False,
+                          out: Optional[torch.Tensor] = None, final: Optional[torch.Tensor] = None,
+                          stream=None) -> LinearRecurrence:
+    """The gated linear recurrence h = a[t] * h + u[t] along time, for each sequence and channel (see det_model.h).
+
+    form "decay" takes gate as a and x as u, form "sigmoid" a = sigmoid(gate) and u = (1 - a) * x.  x and gate are
+    [batch, time, channels] of one dtype (float32, bfloat16 or float16) with any strides but along the channels; initial
+    is float32 [batch, channels], or None for zeros; lengths is int32 [batch], or None for whole sequences (past a
+    sequence's length nothing is read and out is 0).  Returns out like x, contiguous, final (float32 [batch, channels], the
+    states at the sequences' ends; final=initial updates them in place) and with keep_states what the gradient needs."""
+    dev, shape = x.device, x.shape
+    x_ptr, x_b, x_t = _steps(None, None, "x", x, None)
+    code = _model_code(x, "x")
+    gate_ptr, gate_b, gate_t = _steps(dev, x.dtype, "gate", gate, shape)
+    batch, time, channels = shape
+    initial_ptr = lengths_ptr = states = states_ptr = None
+    if initial is not None:
+        initial_ptr = _on(dev, torch.float32, "initial", initial, (batch, channels)).data_ptr()
+    if lengths is not None:
+        lengths_ptr = _on(dev, torch.int32, "lengths", lengths, (batch,)).data_ptr()
+    if out is None:
+        out = _empty(shape, x.dtype, dev, stream)
+    else:
+        _on(dev, x.dtype, "out", out, shape)
+    if final is None:
+        final = _empty((batch, channels), torch.float32, dev, stream)
+    else:
+        _on(dev, torch.float32, "final", final, (batch, channels))
+    if keep_states:
+        states = _empty((batch, -(-time // RECURRENCE_KEEP), channels), torch.float32, dev, stream)
+        states_ptr = states.data_ptr()
+    rc = _run(dev, lib().det_linear_recurrence,
+              (x_ptr, x_b, x_t, gate_ptr, gate_b, gate_t, code, _gate_form(form), batch, time, channels, initial_ptr,
+               lengths_ptr, out.data_ptr(), final.data_ptr(), states_ptr, _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_linear_recurrence")
+    if stream is not None:
+        _hold(stream, dev, x, gate, initial, lengths, out, final)
+    return LinearRecurrence(out, final, states)
+
+
+class LinearRecurrenceGrads(NamedTuple):
+    x: torch.Tensor
+    gate: torch.Tensor
+    initial: torch.Tensor
+
+
+def det_linear_recurrence_backward(grad: Optional[torch.Tensor], x: torch.Tensor, gate: torch.Tensor,
+                                   states: torch.Tensor, *, grad_final: Optional[torch.Tensor] = None,
+                                   form: str = "sigmoid", lengths: Optional[torch.Tensor] = None,
+                                   stream=None) -> LinearRecurrenceGrads:
+    """The gradients for x, gate and initial of det_linear_recurrence (see det_model.h), from those of out (grad) and
+    final (grad_final), each of which may be None; states are its kept ones, form and lengths the same."""
+    dev, shape = x.device, x.shape
+    x_ptr, x_b, x_t = _steps(None, None, "x", x, None)
+    code = _model_code(x, "x")
+    gate_ptr, gate_b, gate_t = _steps(dev, x.dtype, "gate", gate, shape)
+    batch, time, channels = shape
+    grad_ptr, grad_b, grad_t = (None, 0, 0) if grad is None else _steps(dev, x.dtype, "grad", grad, shape)
+    _on(dev, torch.float32, "states", states, (batch, -(-time // RECURRENCE_KEEP), channels))
+    grad_final_ptr = lengths_ptr = None
+    if grad_final is not None:
+        grad_final_ptr = _on(dev, torch.float32, "grad_final", grad_final, (batch, channels)).data_ptr()
+    if lengths is not None:
+        lengths_ptr = _on(dev, torch.int32, "lengths", lengths, (batch,)).data_ptr()
+    grad_x = _empty(shape, x.dtype, dev, stream)
+    grad_gate = _empty(shape, x.dtype, dev, stream)
+    grad_initial = _empty((batch, channels), torch.float32, dev, stream)
+    rc = _run(dev, lib().det_linear_recurrence_backward,
+              (grad_ptr, grad_b, grad_t, x_ptr, x_b, x_t, gate_ptr, gate_b, gate_t, code, _gate_form(form), batch, time,
+               channels, states.data_ptr(), grad_final_ptr, lengths_ptr, grad_x.data_ptr(), grad_gate.data_ptr(),
+               grad_initial.data_ptr(), _stream(stream, dev)))
+    if rc:
+        raise DetError(rc, "det_linear_recurrence_backward")
+    if stream is not None:
+        _hold(stream, dev, grad, x, gate, states, grad_final, lengths)
+    return LinearRecurrenceGrads(grad_x, grad_gate, grad_initial)
 
 
 # ---------------------------------------------------------------------------

@@ -1,8 +1,10 @@
 /*
  * det_model.h -- operators of language models whose sums are taken in a fixed
  * order: log probabilities of given tokens (with entropy, top alternatives and
- * the gradient), the learned relative position bias (with its gradient), and
- * the attention of one new token over a paged key-value cache.
+ * the gradient), the learned relative position bias (with its gradient), the
+ * attention of one new token over a paged key-value cache, and the token
+ * embedding, the layer norm and the gated linear recurrence, each with its
+ * gradient.
  *
  * The conventions of det.h hold (device pointers, caller-owned buffers and
  * workspace, a cudaStream_t as void*, return codes, nothing allocated and
@@ -167,6 +169,135 @@ int det_paged_attention(const void* q, int64_t q_stride_b, int64_t q_stride_h, c
                         int dtype, float scale, const void* bias_table, int bias_dtype, const int32_t* bias_bounds,
                         int64_t num_bounds, int64_t max_len, void* out, float* lse_out, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_embedding -- out[i][0..dim) = scale * table[tokens[i]][0..dim), the
+ * product in 32 bits, rounded once to dtype.  A token outside [0, vocab) gives a
+ * row of +0.0.
+ *   table   device, vocab x dim of table_dtype; row v starts at element
+ *           v * table_stride
+ *   tokens  device, n int32
+ *   out     device, n x dim of dtype, contiguous (written)
+ * Limits: n < 2^31, vocab < 2^31, dim <= 2^21.
+ */
+int det_embedding(const void* table, int table_dtype, int64_t vocab, int64_t dim, int64_t table_stride,
+                  const int32_t* tokens, int64_t n, float scale, void* out, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_embedding_backward -- the gradient of det_embedding's table:
+ *   grad_table[v] = scale * PT(grad[i] : tokens[i] = v, i rising), per column,
+ * the canonical pairwise tree of det_scatter_add_rows in 32 bits, times scale,
+ * rounded once to table_dtype: with DET_F32 and a scale of 1 the bits of
+ * det_scatter_add_rows on a table of zeros.  Rows of no token are +0.0.  With
+ * accumulate, what the row holds is added (in 32 bits, before the rounding), and
+ * rows of no token are neither read nor written.
+ *   grad        device, n x dim of dtype; row i starts at element i * grad_stride.
+ *               Rows of tokens outside [0, vocab) are not read
+ *   grad_table  device, vocab x dim of table_dtype, contiguous (written); must
+ *               not overlap the inputs
+ * Limits: n < 2^31, vocab < 2^31, dim <= 2^21.  The workspace is that of a sort of n
+ * records and up to n / 16 rows of dim floats.
+ */
+size_t det_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+int det_embedding_backward(const void* grad, int dtype, int64_t n, int64_t dim, int64_t grad_stride,
+                           const int32_t* tokens, float scale, void* grad_table, int table_dtype, int64_t vocab,
+                           int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_layer_norm -- for every row x[0..cols)
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   out[c] = (x[c] - mean) * rstd * weight[c] + bias[c]
+ *   x       device, rows x cols of dtype; row r starts at element r * x_stride
+ *   weight, bias  device, cols of param_dtype; either may be NULL (1, 0)
+ *   out     device, rows x cols of dtype, contiguous (written); may be x where
+ *           x_stride is cols
+ *   mean_out, rstd_out  device, rows floats each; either may be NULL
+ * A row that holds NaN or an infinity has NaN results.  So may one whose sum, or whose
+ * sum of squares, passes the range of 32 bits.
+ * Limits: rows < 2^31, 1 <= cols <= DET_MAX_NORM_COLS (rows of no columns are
+ * refused unless there is no row), eps >= 0.
+ */
+#define DET_MAX_NORM_COLS 16384
+int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
+                   const void* bias, int param_dtype, float eps, void* out, float* mean_out, float* rstd_out,
+                   void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_layer_norm_backward -- with xh = (x - mean) * rstd and gw = grad * weight
+ *   grad_x = rstd * (gw - sum(gw) / cols - xh * sum(gw * xh) / cols)
+ *   grad_weight[c] = sum_r grad[r][c] * xh[r][c],  grad_bias[c] = sum_r grad[r][c]
+ * The sums over rows are taken in an order that rows and cols alone decide.
+ *   grad, x     device, rows x cols of dtype, rows at their strides
+ *   mean, rstd  device, rows floats: det_layer_norm's
+ *   weight      device, cols of param_dtype, or NULL (1)
+ *   grad_x      device, rows x cols of dtype, contiguous (written), or NULL; may be grad where grad_stride is cols
+ *   grad_weight, grad_bias  device, cols of param_dtype (written); either may be
+ *               NULL.  Without rows they are +0.0
+ * Limits: as det_layer_norm's.
+ */
+size_t det_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype,
+                            int64_t rows, int64_t cols, const float* mean, const float* rstd, const void* weight,
+                            int param_dtype, void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_linear_recurrence -- for every sequence b and channel c, with h = the
+ * initial state,
+ *   h = a[t] * h + u[t],  out[t] = h,   t = 0..length-1
+ *   DET_GATE_DECAY:    a = gate[t], u = x[t]
+ *   DET_GATE_SIGMOID:  a = 1 / (1 + exp(-gate[t])), u = (1 - a) * x[t]
+ * in 32 bits; out is rounded once.  The bits of out[t] are a function of the initial
+ * state and of the steps up to t alone: a sequence gives the same bits whatever
+ * follows.  (One that is cut and resumed from its final state gives other roundings.)
+ *   x, gate   device, batch x time x channels of dtype; strides in elements, 1
+ *             along channels
+ *   initial   device, batch x channels floats, contiguous, or NULL (0)
+ *   lengths   device, batch int32, or NULL (time).  One below 0 counts as 0, one above
+ *             time as time.  Steps from a sequence's length on are not read, and
+ *             their outputs are +0.0
+ *   out       device, batch x time x channels of dtype, contiguous (written); must
+ *             not overlap the inputs
+ *   final_out device, batch x channels floats: the states at the sequences' ends,
+ *             or NULL; may be initial
+ *   states_out  device, batch x ceil(time / DET_RECURRENCE_KEEP) x channels floats:
+ *             the state before every DET_RECURRENCE_KEEP-th step, for the gradient
+ *             (past a sequence's end: its final state), or NULL
+ * Products of up to DET_RECURRENCE_SPAN decays are formed: where one passes the
+ * range of 32 bits (decays well above 1), states may become infinite or NaN before they
+ * would step by step.  A state that is infinite or NaN leaves later states infinite or NaN.
+ * Limits: batch <= 65,535, time < 2^31 - 2^16, channels < 2^31 - 2^16; strides are not negative.
+ */
+#define DET_GATE_DECAY 0
+#define DET_GATE_SIGMOID 1
+#define DET_RECURRENCE_KEEP 128
+#define DET_RECURRENCE_SPAN 1024
+int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t x_stride_t, const void* gate,
+                          int64_t gate_stride_b, int64_t gate_stride_t, int dtype, int form, int64_t batch,
+                          int64_t time, int64_t channels, const float* initial, const int32_t* lengths, void* out,
+                          float* final_out, float* states_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * det_linear_recurrence_backward -- the gradient of sum grad * out +
+ * grad_final * final.  With l = grad_final at a sequence's end and from its last step
+ * back l = grad[t] + a[t + 1] * l (a = 1 after the end):
+ *   DET_GATE_DECAY:    grad_gate[t] = l * h[t - 1],  grad_x[t] = l
+ *   DET_GATE_SIGMOID:  grad_gate[t] = l * (h[t - 1] - x[t]) * a * (1 - a),
+ *                      grad_x[t] = l * (1 - a)
+ * and grad_initial = a[0] * l of the first step.
+ *   grad      device, batch x time x channels of dtype, strided as x is, or NULL (0)
+ *   states    device: det_linear_recurrence's states_out
+ *   grad_final  device, batch x channels floats, or NULL (0)
+ *   grad_x, grad_gate  device, batch x time x channels of dtype, contiguous (written; +0.0
+ *             from a sequence's length on); must not overlap the inputs
+ *   grad_initial  device, batch x channels floats (written), or NULL
+ */
+int det_linear_recurrence_backward(const void* grad, int64_t grad_stride_b, int64_t grad_stride_t, const void* x,
+                                   int64_t x_stride_b, int64_t x_stride_t, const void* gate, int64_t gate_stride_b,
+                                   int64_t gate_stride_t, int dtype, int form, int64_t batch, int64_t time,
+                                   int64_t channels, const float* states, const float* grad_final,
+                                   const int32_t* lengths, void* grad_x, void* grad_gate, float* grad_initial,
+                                   void* stream);
 
 #ifdef __cplusplus
 }
