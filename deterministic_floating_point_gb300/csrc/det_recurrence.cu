@@ -3,28 +3,32 @@
 //
 // A step is the map h -> a h + u; a run of steps is a map of the same kind,
 // h -> A h + H with A the product of its decays and H its result from 0.  Time
-// is cut into pieces (a warp), the pieces of a CTA's 8 warps and those of a
-// cluster's 8 CTAs.  A warp reads its piece of 32 words of channels into
-// registers once, forms (A, H), the CTA's warps and then the cluster's CTAs
-// exchange these through (distributed) shared memory, and each warp runs
-// through its piece again, in registers, from the state it now knows.  A
-// cluster goes through its sequence from one such span to the next and carries
-// the state in registers; the next span's words are on their way meanwhile.  So
-// every input is read once and every output written once, and nothing waits on
-// memory that another CTA writes.  Pieces are joined in the order of time, always
-// from the same borders, so the bits of a step are a function of the steps before
-// it.
+// is cut into blocks of 128 steps (a CTA) and these into pieces of 8 (a warp, over
+// 32 words of channels).  A warp forms its piece's (A, H).  A further warp of the
+// CTA joins them and tells the other CTAs of the cluster, which hold the
+// sequence's other blocks; another one hears of theirs and tells each warp the
+// state its piece begins with.  The warp then runs through its piece again.  Every
+// input is read from memory once (copied into shared memory up to three rounds
+// ahead, kept in registers between the two passes) and every output written once.
+//
+// Nothing waits for the chain of states but the second pass: (A, H) of a round do
+// not depend on the states, so warps form those of the next round, and CTAs send
+// theirs, before the states of this one are known.  Without that the CTAs of a
+// cluster spent half of their time on waiting for each other.
+//
+// Blocks and pieces have fixed borders and are joined one after the other in the
+// order of time, by the same operations whatever the number of CTAs that share a
+// sequence; so the bits of a step are a function of the steps before it.
 //
 // The gradient runs the same way from the end.  With m = a[t] l the value that
 // step t hands to step t - 1, l = grad[t] + m, and a piece is m -> A m + M.  The
-// states inside a span are formed again from those kept before every 128th step,
-// so that the gates' gradients see 32-bit states and x, not h, is read.
+// states inside a block are formed again from the one kept before it, so that the
+// gates' gradients see 32-bit states and x, not h, is read.
 //
 // What bounds it: bytes, once an element costs few enough instructions (at the
 // copy's rate an SM's schedulers have 33 slots for each element forward and
 // twice that backward).  So two 16-bit channels of a word are worked on by packed
-// 32-bit instructions, whole pieces have no conditions, and gates are computed
-// once.
+// 32-bit instructions, and whole pieces have no conditions.
 #include "det_model.cuh"
 
 #include <algorithm>
@@ -33,13 +37,12 @@
 namespace det {
 namespace {
 
-constexpr int kWarps = 8;                   // pieces of a CTA
+constexpr int kBlock = DET_RECURRENCE_KEEP;  // steps of a CTA; a kept state stands before each
 constexpr int kMaxCluster = 8;
-constexpr int kStepsForward = 16;           // of a piece
-constexpr int kStepsBackward = 8;           // three inputs, and three values a step between the passes: registers
-static_assert(kStepsForward * kWarps * kMaxCluster == DET_RECURRENCE_SPAN, "the documented span");
-static_assert(kStepsForward * kWarps == DET_RECURRENCE_KEEP, "states are kept at the forward CTAs' spans");
-static_assert(2 * kStepsBackward * kWarps == DET_RECURRENCE_KEEP, "backward every second CTA begins with a kept state");
+constexpr int kSteps = 8;                    // of a piece: two rounds' pieces are in registers at a time
+constexpr int kWorkers = kBlock / kSteps;
+constexpr int kStages = 3;                   // rounds whose inputs are in shared memory or on their way
+static_assert(kBlock == DET_RECURRENCE_SPAN, "decays are multiplied over blocks");
 
 struct View {
   const void* p;
@@ -49,7 +52,6 @@ struct Shape {
   int time, channels;
   const int32_t* lengths;
   int log2_ranks;     // CTAs of a cluster
-  int near;           // a span of a cluster lies within 2^31 bytes in every operand
 };
 
 // ---------------------------------------------------------------------------
@@ -249,81 +251,179 @@ __device__ __forceinline__ void put(Map<float>* local, unsigned long long* bar, 
                "r"(__float_as_uint(v.A)), "r"(__float_as_uint(v.H)), "r"(remote(bar, rank))
                : "memory");
 }
-// Waits for a phase of messages, for at most kWaitNs.
+// Waits for a phase of messages, for about kWaitNs at most.  (The timer is read after
+// many polls only: reading it takes as long as a message.)
+template <bool CLUSTER>
 __device__ __forceinline__ bool messages_in(unsigned long long* bar, unsigned phase) {
   unsigned long long t0 = 0;
-  for (unsigned polls = 0;; ++polls) {
+  for (unsigned polls = 1;; ++polls) {
     unsigned done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(phase)
-        : "memory");
+    if (CLUSTER) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(smem_u32(bar)), "r"(phase)
+          : "memory");
+    } else {
+      done = mbar_try_wait(bar, phase);
+    }
     if (done) return true;
-    if (polls == 0) t0 = globaltimer();
-    else if ((polls & 255u) == 0 && globaltimer() - t0 > kWaitNs) return false;
-  }
-}
-
-// Where a thread works.
-template <typename T, bool SHORT>
-struct Place {
-  int warp, lane, b, c, n;         // n: its channels, from c on
-  int rank, ranks;
-  int len;                         // of the sequence
-  bool whole;                      // every lane of the warp has all its channels, and 32-bit offsets will do
-  __device__ __forceinline__ explicit Place(const Shape& s) {
-    constexpr int CH = Lane<T>::CH;
-    warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    lane = threadIdx.x & 31;
-    b = blockIdx.y;
-    ranks = SHORT ? 1 : 1 << s.log2_ranks;
-    rank = SHORT ? 0 : blockIdx.x & (ranks - 1);             // clusters lie along x
-    const int tile = SHORT ? blockIdx.x * kWarps + warp : blockIdx.x >> s.log2_ranks;
-    c = (tile * 32 + lane) * CH;
-    n = max(0, min(CH, s.channels - c));
-    whole = s.near && (tile + 1) * 32 * CH <= s.channels;
-    len = s.time;
-    if (s.lengths) len = max(0, min(len, (int)s.lengths[b]));
-  }
-};
-
-// The words of steps s0 + at .. s0 + at + STEPS - 1 below len.  A full piece is read
-// at 32-bit offsets from one base, the same for all threads: one addition a word.
-template <typename T, bool VEC, int STEPS>
-__device__ __forceinline__ void load_piece(unsigned (&w)[STEPS], const View& v, int b, int c, int n, int s0, int at,
-                                           int len, bool full) {
-  const T* base = static_cast<const T*>(v.p) + (b * v.sb + s0 * v.st);
-  if (full) {
-    const unsigned step = (unsigned)v.st * (unsigned)sizeof(T);
-    unsigned o = (unsigned)at * step + (unsigned)c * (unsigned)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i, o += step)
-      w[i] = load_word<T, VEC>(reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + o), Lane<T>::CH);
-  } else {
-    const T* p = base + at * v.st + c;
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      w[i] = 0;
-      if (n > 0 && s0 + at + i < len) w[i] = load_word<T, VEC>(p + i * v.st, n);
+    if ((polls & 1023u) == 0) {
+      const unsigned long long now = globaltimer();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitNs) return false;
     }
   }
 }
 
+// Between warps of a CTA: arrive() does not wait, join() waits until all of the
+// barrier's threads have come.
+__device__ __forceinline__ void arrive(int barrier, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void join(int barrier, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+}
+constexpr int kMapsIn = 1, kStatesIn = 3;      // named barriers, two each for odd and even rounds
+
+// ---------------------------------------------------------------------------
+// Where a CTA works: blocks rank, rank + ranks, ... of a sequence, 32 words of
+// channels.
+template <typename T>
+struct Place {
+  int warp, lane, b, c0, c, n;     // c0: of the tile; n: the lane's channels, from c on
+  int rank, ranks, stride, workers;
+  int len, rounds;                 // of the sequence
+  bool whole;                      // the tile has all its channels
+  __device__ __forceinline__ explicit Place(const Shape& s) {
+    constexpr int CH = Lane<T>::CH;
+    warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    lane = threadIdx.x & 31;
+    workers = (blockDim.x >> 5) - 2;
+    b = blockIdx.y;
+    ranks = 1 << s.log2_ranks;
+    stride = ranks * kBlock;
+    rank = blockIdx.x & (ranks - 1);             // clusters lie along x
+    c0 = (blockIdx.x >> s.log2_ranks) * 32 * CH;
+    c = c0 + lane * CH;
+    n = max(0, min(CH, s.channels - c));
+    whole = c0 + 32 * CH <= s.channels;
+    len = s.time;
+    if (s.lengths) len = max(0, min(len, (int)s.lengths[b]));
+    rounds = (int)(((long long)len + stride - 1) / stride);
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  if (VEC == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last one or two committed groups of this thread's copies have arrived.
+__device__ __forceinline__ void copies_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_but_two() { asm volatile("cp.async.wait_group 2;" ::: "memory"); }
+static_assert(kStages == 3, "so many groups are asked for after the one that is waited for");
+
+// Copies a warp's pieces of one operand into its part of shared memory, [kSteps][32]
+// words, 0 past the sequence and the channels, round after round.  VEC 2: rows of 16-byte
+// vectors; 1: of words; 0: 16-bit elements at any address, through registers.
+template <typename T, int VEC>
+struct Reader {
+  const T* p;            // the lane's first element of the next piece
+  static constexpr int kRows = VEC == 2 ? 4 : 1;             // that a copy of the warp takes
+  static __device__ __forceinline__ int first_channel(const Place<T>& me) {
+    return VEC == 2 ? me.c0 + (me.lane & 7) * (4 * Lane<T>::CH) : me.c;
+  }
+  // first: step of the first round's piece
+  __device__ __forceinline__ Reader(const View& v, const Place<T>& me, int first) {
+    p = static_cast<const T*>(v.p) + (me.b * v.sb + (first + (VEC == 2 ? me.lane >> 3 : 0)) * v.st + first_channel(me));
+  }
+  // the piece from step t0 on; by: steps to the next round's
+  __device__ __forceinline__ void next(unsigned (*to)[32], const View& v, const Place<T>& me, int t0, int by, int channels) {
+    const bool full = me.whole && t0 + kSteps <= me.len;
+    const long long step = kRows * v.st;
+    if constexpr (VEC == 0) {
+      unsigned w[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        w[i] = 0;
+        if (me.n > 0 && t0 + i < me.len) w[i] = load_word<T, false>(p + i * step, me.n);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) to[i][me.lane] = w[i];
+    } else {
+      unsigned* dst = VEC == 2 ? &to[me.lane >> 3][(me.lane & 7) * 4] : &to[0][me.lane];
+      const int row = VEC == 2 ? me.lane >> 3 : 0;
+      const T* q = p;
+#pragma unroll
+      for (int j = 0; j < kSteps / kRows; ++j, q += step) {
+        if (full) {
+          copy_async<VEC>(dst + j * kRows * 32, q, VEC == 2 ? 16 : 4);
+        } else {
+          const bool ok = first_channel(me) < channels && t0 + row + j * kRows < me.len;
+          copy_async<VEC>(dst + j * kRows * 32, ok ? q : v.p, ok ? VEC == 2 ? 16 : 4 : 0);   // (0 bytes are read)
+        }
+      }
+    }
+    p += by * v.st;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// What CTAs of a cluster tell each other: the map of each one's block.  Messages of
+// four rounds have places: a CTA may be told of round k + 2 while it still reads those
+// of k and k - 1.
+template <typename V>
+struct Messages {
+  Map<V> from[4][kMaxCluster][32];
+  unsigned long long bar[4];
+};
+template <typename V, typename PLACE>
+__device__ __forceinline__ void send(Messages<V>& box, const PLACE& me, int round, const Map<V>& map) {
+  const int k = round & 3;
+  if (me.ranks == 1) {                 // no cluster: its instructions must not be used
+    box.from[k][0][me.lane] = map;
+    __syncwarp();
+    if (me.lane == 0) mbar_arrive(&box.bar[k]);
+    return;
+  }
+  if (me.lane == 0) mbar_arrive_expect_tx(&box.bar[k], me.ranks * 32 * (unsigned)sizeof(Map<V>));
+  for (int r = 0; r < me.ranks; ++r) put(&box.from[k][me.rank][me.lane], &box.bar[k], r, map);
+}
+// The state (or what comes back) at the CTA's block, from the one at the cluster's
+// blocks, v, which moves on past them.  BACK: from the last block to the first.
+template <int FORM, bool BACK, typename V, typename PLACE>
+__device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int round, V& v, bool& lost) {
+  const int k = round & 3;
+  const unsigned phase = round >> 2 & 1;
+  lost = lost || !(me.ranks == 1 ? messages_in<false>(&box.bar[k], phase) : messages_in<true>(&box.bar[k], phase));
+  if (lost) both(v, __int_as_float(0x7fffffff));
+  V here = v;
+  const int first = BACK ? me.ranks - 1 : 0, by = BACK ? -1 : 1;
+  for (int j = 0, r = first; j < me.ranks; ++j, r += by) {
+    if (r == me.rank) here = v;
+    const Map<V> q = box.from[k][r][me.lane];
+    v = after<FORM>(v, q.A, q.H);
+  }
+  return here;
+}
+
 // ---------------------------------------------------------------------------
 
-// The decays and additions of a piece and its map.  A step past the end is
+// A piece's decays and what its steps add, and its map.  A step past the end is
 // (1, 0).
 template <typename T, int FORM, bool FULL>
-__device__ __forceinline__ void forward_maps(const Gates<T, FORM>& gates, const unsigned (&rg)[kStepsForward],
-                                             const unsigned (&rx)[kStepsForward], LaneV<T> (&a)[kStepsForward],
-                                             LaneV<T> (&u)[kStepsForward], Map<LaneV<T>>& map, int steps) {
+__device__ __forceinline__ Map<LaneV<T>> piece_map(const Gates<T, FORM>& gates, const unsigned (*gate)[32],
+                                                   const unsigned (*x)[32], LaneV<T> (&a)[kSteps], LaneV<T> (&u)[kSteps],
+                                                   int steps) {
+  Map<LaneV<T>> map;
 #pragma unroll
-  for (int i = 0; i < kStepsForward; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     LaneV<T> rest;
-    gates(rg[i], a[i], rest);
-    u[i] = gates.input(rest, unpack<T>(rx[i]));
+    gates(gate[i][threadIdx.x & 31], a[i], rest);
+    u[i] = gates.input(rest, unpack<T>(x[i][threadIdx.x & 31]));
     if (!FULL && i >= steps) {
       both(a[i], 1.0f);
       both(u[i], 0.0f);
@@ -331,374 +431,534 @@ __device__ __forceinline__ void forward_maps(const Gates<T, FORM>& gates, const 
     map.H = i ? fma(a[i], map.H, u[i]) : u[i];
     map.A = i ? mul(map.A, a[i]) : a[i];
   }
+  return map;
 }
 
-// SHORT: at most 16 steps, a piece for each sequence and warp of channels, and
-// nothing to exchange; the bits are those of the long form.
-template <typename T, int FORM, bool VEC, bool SHORT>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+template <typename T, int FORM, int VEC>
+__global__ void __launch_bounds__(32 * (kWorkers + 2), 1)
 recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, float* final_out, float* states) {
   using V = LaneV<T>;
-  constexpr int CH = Lane<T>::CH, STEPS = kStepsForward, SPAN = STEPS * kWarps;
-  __shared__ Map<V> s_warp[2][kWarps][32];
-  __shared__ Map<V> s_cta[2][kMaxCluster][32];
-  __shared__ unsigned long long s_bar[2];
-  if (!SHORT) {
-    if (threadIdx.x < 2) mbar_init(&s_bar[threadIdx.x], 1);
-    cluster_arrive();                    // the others' shared memory is written only after they have come here
-  }
+  constexpr int CH = Lane<T>::CH;
+  extern __shared__ __align__(128) unsigned s_raw[];     // [stages][workers][gate, x][kSteps][32]
+  __shared__ Map<V> s_map[2][kWorkers][32];              // of the pieces; then A: the state a piece begins with
+  __shared__ Messages<V> s_box;
+  if (threadIdx.x < 4) mbar_init(&s_box.bar[threadIdx.x], 1);
+  if (shape.log2_ranks > 0) cluster_arrive();            // a box is written only after its CTA has come here
   dep_wait();
   dep_launch();
-  const Gates<T, FORM> gates;
-  const Place<T, SHORT> me(shape);
-  const int len = me.len, time = shape.time, channels = shape.channels;
+  const Place<T> me(shape);
+  const int len = me.len, time = shape.time, channels = shape.channels, threads = blockDim.x;
   const long long row = (long long)me.b * channels + me.c;   // of the sequence's states
   V carry;
-  load_state<CH>(carry, initial + row, initial ? me.n : 0);
-  const int stride = SHORT ? STEPS : me.ranks * SPAN;
-  const int at = SHORT ? 0 : me.rank * SPAN + me.warp * STEPS;
-  const int kept = (time + SPAN - 1) / SPAN;
-  unsigned rg[STEPS], rx[STEPS];
-  bool full = me.whole && at + STEPS <= len;
-  load_piece<T, VEC>(rg, gate, me.b, me.c, me.n, 0, at, len, full);
-  load_piece<T, VEC>(rx, x, me.b, me.c, me.n, 0, at, len, full);
-  if (!SHORT) cluster_wait();
-  int round = 0;
-  bool lost = false;                     // a wait gave up: results are NaN from there on
-  long long s0 = 0;
-  for (; s0 < len; s0 += stride, ++round) {
-    const int parity = round & 1;
-    const int t0 = (int)s0 + at;
-    V a[STEPS], u[STEPS];
-    Map<V> map;
-    const bool all_in = full;
-    if (all_in) forward_maps<T, FORM, true>(gates, rg, rx, a, u, map, STEPS);
-    else forward_maps<T, FORM, false>(gates, rg, rx, a, u, map, len - t0);
-    // the next piece is on its way while the states are exchanged
-    if (!SHORT && s0 + stride < len) {
-      full = me.whole && s0 + stride + at + STEPS <= len;
-      load_piece<T, VEC>(rg, gate, me.b, me.c, me.n, (int)s0 + stride, at, len, full);
-      load_piece<T, VEC>(rx, x, me.b, me.c, me.n, (int)s0 + stride, at, len, full);
-    }
-    V h = carry;
-    if (!SHORT) {
-      s_warp[parity][me.warp][me.lane] = map;
-      __syncthreads();
-      if (me.ranks > 1) {
-        if (me.warp < me.ranks) {        // warp r tells CTA r
-          map = s_warp[parity][0][me.lane];
+  load_state<CH>(carry, initial + row, initial && me.warp >= me.workers ? me.n : 0);
+  // (the shuffle waits for it: a CTA that has heard of all may write the final state to the same place)
+  carry = __shfl_sync(0xffffffffu, carry, me.lane);
+  if (shape.log2_ranks > 0) cluster_wait();
+  else __syncthreads();
+
+  if (me.warp == me.workers) {
+    // tells of the CTA's blocks
+    for (int k = 0; k < me.rounds; ++k) {
+      join(kMapsIn + (k & 1), threads);
+      Map<V> map = s_map[k & 1][0][me.lane];
 #pragma unroll
-          for (int w = 1; w < kWarps; ++w) {
-            const Map<V> q = s_warp[parity][w][me.lane];
-            map.H = after<FORM>(map.H, q.A, q.H);
-            map.A = mul(map.A, q.A);
+      for (int w = 1; w < kWorkers; ++w) {
+        if (w >= me.workers) break;
+        const Map<V> q = s_map[k & 1][w][me.lane];
+        map.H = after<FORM>(map.H, q.A, q.H);
+        map.A = mul(map.A, q.A);
+      }
+      send(s_box, me, k, map);
+    }
+  } else if (me.warp > me.workers) {
+    // hears of the cluster's, and hands out states
+    const int kept = (time + kBlock - 1) / kBlock;
+    bool lost = false;                 // a wait gave up: states are NaN from there on
+    for (int k = 0; k < me.rounds; ++k) {
+      join(kMapsIn + (k & 1), threads);
+      V h = receive<FORM, false>(s_box, me, k, carry, lost);
+      const int block = k * me.ranks + me.rank;
+      if (states && block < kept) store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, h, me.n);
+#pragma unroll 1
+      for (int w0 = 0; w0 < me.workers; w0 += 4) {
+        Map<V> q[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) q[w] = s_map[k & 1][w0 + w][me.lane];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) {
+            s_map[k & 1][w0 + w][me.lane].A = h;
+            h = after<FORM>(h, q[w].A, q[w].H);
           }
-          if (!lost) put(&s_cta[parity][me.rank][me.lane], &s_bar[parity], me.warp, map);
-        }
-        if (threadIdx.x == 0 && !lost) mbar_arrive_expect_tx(&s_bar[parity], me.ranks * 32 * (unsigned)sizeof(Map<V>));
-        lost = lost || !messages_in(&s_bar[parity], round >> 1 & 1);
-        if (lost) both(h, __int_as_float(0x7fffffff));
-        int r = 0;
-        for (; r < me.rank; ++r) {
-          const Map<V> q = s_cta[parity][r][me.lane];
-          h = after<FORM>(h, q.A, q.H);
-        }
-        carry = h;
-        for (; r < me.ranks; ++r) {
-          const Map<V> q = s_cta[parity][r][me.lane];
-          carry = after<FORM>(carry, q.A, q.H);
-        }
       }
-      // (a CTA by itself makes one round and needs no carry)
-      if (states && me.warp == 0 && t0 < time)
-        store_state<CH>(states + ((long long)me.b * kept + t0 / SPAN) * channels + me.c, h, me.n);
-      for (int w = 0; w < me.warp; ++w) {
-        const Map<V> q = s_warp[parity][w][me.lane];
-        h = after<FORM>(h, q.A, q.H);
-      }
-    } else if (states) {
-      store_state<CH>(states + row, h, me.n);
+      arrive(kStatesIn + (k & 1), threads - 32);
     }
-    T* base = out + ((long long)me.b * time + s0) * channels;
-    const unsigned step = (unsigned)channels * (unsigned)sizeof(T);
-    if (all_in) {
-      unsigned o = (unsigned)at * step + (unsigned)me.c * (unsigned)sizeof(T);
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i, o += step) {
-        h = fma(a[i], h, u[i]);
-        store_word<T, VEC>(reinterpret_cast<T*>(reinterpret_cast<char*>(base) + o), pack<T>(h), CH);
+    if (states)                        // past the sequence's last round
+      for (int block = me.rounds * me.ranks + me.rank; block < kept; block += me.ranks)
+        store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, carry, me.n);
+    if (final_out && len == 0 && me.rank == 0) store_state<CH>(final_out + row, carry, me.n);
+  } else {
+    const Gates<T, FORM> gates;
+    const int at = me.rank * kBlock + me.warp * kSteps;
+    auto raw = [&](int k) {
+      return reinterpret_cast<unsigned(*)[kSteps][32]>(s_raw + (k % kStages * me.workers + me.warp) * (2 * kSteps * 32));
+    };
+    Reader<T, VEC> read_gate(gate, me, at), read_x(x, me, at);
+    auto ask = [&](int k) {            // for the piece of round k, if there is one; in the rounds' order
+      if (k < me.rounds) {
+        read_gate.next(raw(k)[0], gate, me, k * me.stride + at, me.stride, channels);
+        read_x.next(raw(k)[1], x, me, k * me.stride + at, me.stride, channels);
       }
-    } else {
-      T* o = base + (long long)at * channels + me.c;
+      copies_commit();
+    };
+    auto take = [&](int k, V (&a)[kSteps], V (&u)[kSteps]) {
+      copies_wait_but_two();
+      __syncwarp();
+      const int t0 = k * me.stride + at;
+      unsigned(*w)[kSteps][32] = raw(k);
+      s_map[k & 1][me.warp][me.lane] = me.whole && t0 + kSteps <= len
+                                           ? piece_map<T, FORM, true>(gates, w[0], w[1], a, u, kSteps)
+                                           : piece_map<T, FORM, false>(gates, w[0], w[1], a, u, len - t0);
+      __syncwarp();
+      arrive(kMapsIn + (k & 1), threads);
+      ask(k + kStages);
+    };
+    auto give = [&](int k, const V (&a)[kSteps], const V (&u)[kSteps]) {
+      join(kStatesIn + (k & 1), threads - 32);
+      V h = s_map[k & 1][me.warp][me.lane].A;
+      const int t0 = k * me.stride + at;
+      T* o = out + ((long long)me.b * time + t0) * channels + me.c;
+      if (me.whole && t0 + kSteps <= len) {
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        h = fma(a[i], h, u[i]);
-        if (me.n > 0 && t0 + i < time) store_word<T, VEC>(o + (long long)i * channels, t0 + i < len ? pack<T>(h) : 0u, me.n);
+        for (int i = 0; i < kSteps; ++i, o += channels) {
+          h = fma(a[i], h, u[i]);
+          store_word<T, VEC != 0>(o, pack<T>(h), CH);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i, o += channels) {
+          h = fma(a[i], h, u[i]);
+          if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(o, t0 + i < len ? pack<T>(h) : 0u, me.n);
+        }
       }
+      // the state at the end is that of the last step (steps past it have kept it); the
+      // initial state has been read everywhere by now, so it may lie in the same place
+      if (final_out && t0 < len && len <= t0 + kSteps) store_state<CH>(final_out + row, h, me.n);
+    };
+    V a0[kSteps], u0[kSteps], a1[kSteps], u1[kSteps];
+    if (me.rounds > 0) {
+      for (int k = 0; k < kStages; ++k) ask(k);
+      take(0, a0, u0);
     }
-    // the state at the end is that of the last step (steps past it have kept it); the
-    // initial state has been read everywhere by now, so it may lie in the same place
-    if (final_out && t0 < len && len <= t0 + STEPS) store_state<CH>(final_out + row, h, me.n);
-    if (SHORT) carry = h;
+    for (int k = 0; k < me.rounds; k += 2) {
+      if (k + 1 < me.rounds) take(k + 1, a1, u1);
+      give(k, a0, u0);
+      if (k + 1 == me.rounds) break;
+      if (k + 2 < me.rounds) take(k + 2, a0, u0);
+      give(k + 1, a1, u1);
+    }
+    // past the sequence's last round
+    for (long long t0 = (long long)me.rounds * me.stride + at; t0 < time; t0 += me.stride)
+      for (int i = 0; i < kSteps; ++i)
+        if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(out + ((long long)me.b * time + t0 + i) * channels + me.c, 0u, me.n);
   }
-  if (final_out && len == 0 && (SHORT || (me.rank == 0 && me.warp == 0))) store_state<CH>(final_out + row, carry, me.n);
-  if (!SHORT && me.ranks > 1) {            // no CTA leaves before what it was sent has come
+  if (shape.log2_ranks > 0) {          // no CTA leaves before what it was sent has come
     cluster_arrive();
     cluster_wait();
   }
-  // past the sequence's last span
-  for (; s0 < time; s0 += stride) {
-    const int t0 = (int)s0 + at;
-    if (states && (SHORT || me.warp == 0) && t0 < time)
-      store_state<CH>(states + ((long long)me.b * kept + t0 / SPAN) * channels + me.c, carry, me.n);
-    T* o = out + ((long long)me.b * time + t0) * channels + me.c;
-    for (int i = 0; i < STEPS; ++i)
-      if (me.n > 0 && t0 + i < time) store_word<T, VEC>(o + (long long)i * channels, 0u, me.n);
+}
+
+// A thread's word of channels of a sequence of at most one piece: the same
+// operations, without an exchange.
+struct Word {
+  int b, c, n, len;
+  template <typename T>
+  __device__ __forceinline__ Word(const Shape& s, T) {
+    b = blockIdx.y;
+    c = (blockIdx.x * blockDim.x + threadIdx.x) * Lane<T>::CH;
+    n = max(0, min(Lane<T>::CH, s.channels - c));
+    len = s.time;
+    if (s.lengths) len = max(0, min(len, (int)s.lengths[b]));
   }
+};
+template <typename T, bool VEC, int STEPS>
+__device__ __forceinline__ void load_words(unsigned (&w)[STEPS], const View& v, const Word& me) {
+  const T* p = static_cast<const T*>(v.p) + (me.b * v.sb + me.c);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    w[i] = 0;
+    if (i < me.len) w[i] = load_word<T, VEC>(p + i * v.st, me.n);
+  }
+}
+
+template <typename T, int FORM, bool VEC>
+__global__ void __launch_bounds__(128)
+recurrence_short_kernel(View x, View gate, Shape shape, const float* initial, T* out, float* final_out, float* states) {
+  using V = LaneV<T>;
+  constexpr int CH = Lane<T>::CH, STEPS = kSteps;
+  dep_wait();
+  dep_launch();
+  const Gates<T, FORM> gates;
+  const Word me(shape, T());
+  if (me.n <= 0) return;
+  const long long row = (long long)me.b * shape.channels + me.c;
+  V h;
+  load_state<CH>(h, initial + row, initial ? me.n : 0);
+  unsigned rg[STEPS], rx[STEPS];
+  load_words<T, VEC>(rg, gate, me);
+  load_words<T, VEC>(rx, x, me);
+  if (states && shape.time > 0) store_state<CH>(states + row, h, me.n);
+  T* o = out + (long long)me.b * shape.time * shape.channels + me.c;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i, o += shape.channels) {
+    if (i >= shape.time) break;
+    V a, rest;
+    gates(rg[i], a, rest);
+    if (i < me.len) h = fma(a, h, gates.input(rest, unpack<T>(rx[i])));
+    store_word<T, VEC>(o, i < me.len ? pack<T>(h) : 0u, me.n);
+  }
+  if (final_out) store_state<CH>(final_out + row, h, me.n);
 }
 
 // ---------------------------------------------------------------------------
 // gradient
 
+// A piece's forward map, and back M of m -> A m + M.
 template <typename T, int FORM, bool FULL>
-__device__ __forceinline__ void backward_maps(const Gates<T, FORM>& gates, const unsigned (&rg)[kStepsBackward],
-                                              const unsigned (&xs)[kStepsBackward], const unsigned (&gs)[kStepsBackward],
-                                              LaneV<T> (&a)[kStepsBackward], LaneV<T> (&rest)[kStepsBackward],
-                                              Map<LaneV<T>>& map, LaneV<T>& M, int steps) {
+__device__ __forceinline__ Map<LaneV<T>> piece_maps(const Gates<T, FORM>& gates, const unsigned (*raw)[kSteps][32],
+                                                    bool graded, LaneV<T>& M, int steps) {
+  using V = LaneV<T>;
+  const int lane = threadIdx.x & 31;
+  Map<V> map;
 #pragma unroll
-  for (int i = 0; i < kStepsBackward; ++i) {
-    gates(rg[i], a[i], rest[i]);
+  for (int i = 0; i < kSteps; ++i) {
+    V a, rest;
+    gates(raw[0][i][lane], a, rest);
+    V u = gates.input(rest, unpack<T>(raw[1][i][lane]));
     if (!FULL && i >= steps) {
-      both(a[i], 1.0f);
-      both(rest[i], 0.0f);
+      both(a, 1.0f);
+      both(u, 0.0f);
     }
-    const LaneV<T> u = gates.input(rest[i], unpack<T>(xs[i]));
-    map.H = i ? fma(a[i], map.H, u) : u;
-    map.A = i ? mul(map.A, a[i]) : a[i];
-    M = i ? fma(map.A, unpack<T>(gs[i]), M) : mul(map.A, unpack<T>(gs[i]));
+    map.H = i ? fma(a, map.H, u) : u;
+    map.A = i ? mul(map.A, a) : a;
+    const V d = unpack<T>(graded ? raw[2][i][lane] : 0u);
+    M = i ? fma(map.A, d, M) : mul(map.A, d);
+  }
+  return map;
+}
+
+// A lane's words of a piece: gate (0), x (1) and gradient (2), in shared memory or in
+// registers.
+struct Words {
+  const unsigned (*raw)[kSteps][32];
+  int lane;
+  bool graded;
+  __device__ __forceinline__ unsigned operator()(int which, int i) const {
+    return which < 2 || graded ? raw[which][i][lane] : 0u;
+  }
+};
+struct WordsHeld {
+  const unsigned (&w)[3][kSteps];
+  __device__ __forceinline__ unsigned operator()(int which, int i) const { return w[which][i]; }
+};
+
+// The gradients of a piece's steps from the state h before it and what comes back
+// behind it, m; m is what it hands back.
+template <typename T, int FORM, bool VEC, bool FULL, typename WORDS>
+__device__ __forceinline__ void piece_gradients(const Gates<T, FORM>& gates, const WORDS& words, LaneV<T> h,
+                                                LaneV<T>& m, T* ox, T* og, int channels, int n, int steps, int rows) {
+  using V = LaneV<T>;
+  constexpr int STEPS = kSteps;
+  V a[STEPS], rest[STEPS], factor[STEPS];      // factor: what l (1 - a) is multiplied by for the gate
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    gates(words(0, i), a[i], rest[i]);
+    const V xi = unpack<T>(words(1, i));
+    factor[i] = FORM == DET_GATE_DECAY ? h : mul(a[i], minus(h, xi));
+    h = fma(a[i], h, gates.input(rest[i], xi));
+  }
+  ox += (long long)(STEPS - 1) * channels;
+  og += (long long)(STEPS - 1) * channels;
+#pragma unroll
+  for (int i = STEPS - 1; i >= 0; --i, ox -= channels, og -= channels) {
+    const V l = add(unpack<T>(words(2, i)), m);
+    const V dx = gates.input(rest[i], l);
+    if (FULL || i < steps) m = mul(a[i], l);
+    if (FULL || i < rows) {
+      store_word<T, VEC>(ox, FULL || i < steps ? pack<T>(dx) : 0u, FULL ? Lane<T>::CH : n);
+      store_word<T, VEC>(og, FULL || i < steps ? pack<T>(mul(dx, factor[i])) : 0u, FULL ? Lane<T>::CH : n);
+    }
   }
 }
 
-template <typename T, int FORM, bool VEC, bool SHORT>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+template <typename T, int FORM, int VEC>
+__global__ void __launch_bounds__(32 * (kWorkers + 2), 1)
 recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* states, const float* grad_final,
                        T* grad_x, T* grad_gate, float* grad_initial) {
   using V = LaneV<T>;
-  constexpr int CH = Lane<T>::CH, STEPS = kStepsBackward, SPAN = STEPS * kWarps;
-  __shared__ Map<V> s_warp[2][kWarps][32];       // (A, H)
-  __shared__ V s_back[2][kWarps][32];            // M
-  __shared__ Map<V> s_cta[2][kMaxCluster][32];   // (A, M)
-  __shared__ Map<V> s_pair[2][32];               // (A, H) of the CTA before an odd one, which begins with no kept state
-  __shared__ unsigned long long s_bar[2];
-  if (!SHORT) {
-    if (threadIdx.x < 2) mbar_init(&s_bar[threadIdx.x], 1);
-    cluster_arrive();
-  }
+  constexpr int CH = Lane<T>::CH;
+  extern __shared__ __align__(128) unsigned s_raw[];     // [stages][workers][gate, x, grad][kSteps][32]
+  __shared__ Map<V> s_map[2][kWorkers][32];              // (A, H) of the pieces; then H: the state before a piece
+  __shared__ V s_back[2][kWorkers][32];                  // M; then what comes back behind a piece
+  __shared__ Messages<V> s_box;                          // (A, M) of the CTAs' blocks
+  if (threadIdx.x < 4) mbar_init(&s_box.bar[threadIdx.x], 1);
+  if (shape.log2_ranks > 0) cluster_arrive();
   dep_wait();
   dep_launch();
-  const Gates<T, FORM> gates;
-  const Place<T, SHORT> me(shape);
-  const int len = me.len, time = shape.time, channels = shape.channels;
+  const Place<T> me(shape);
+  const int len = me.len, time = shape.time, channels = shape.channels, threads = blockDim.x;
   const long long row = (long long)me.b * channels + me.c;
-  V carry;
-  load_state<CH>(carry, grad_final + row, grad_final ? me.n : 0);
-  V first = carry;                               // what the sequence's first step hands back
-  const int stride = SHORT ? STEPS : me.ranks * SPAN;
-  const int at = SHORT ? 0 : me.rank * SPAN + me.warp * STEPS;
-  const int kept = (time + DET_RECURRENCE_KEEP - 1) / DET_RECURRENCE_KEEP;
-  // from the sequence's last span back
-  const int last = len > 0 ? (len - 1) / stride * stride : -stride;
-  for (long long s0 = (long long)last + stride; s0 < time; s0 += stride)
-    for (int i = 0; i < STEPS; ++i)
-      if (me.n > 0 && s0 + at + i < time) {
-        const long long o = ((long long)me.b * time + s0 + at + i) * channels + me.c;
-        store_word<T, VEC>(grad_x + o, 0u, me.n);
-        store_word<T, VEC>(grad_gate + o, 0u, me.n);
+  if (shape.log2_ranks > 0) cluster_wait();
+  else __syncthreads();
+  // round k takes the blocks from (rounds - 1 - k) * ranks on
+
+  if (me.warp == me.workers) {
+    for (int k = 0; k < me.rounds; ++k) {
+      join(kMapsIn + (k & 1), threads);
+      Map<V> map;
+      both(map.A, 1.0f);
+      both(map.H, 0.0f);
+#pragma unroll
+      for (int w = kWorkers - 1; w >= 0; --w) {
+        if (w >= me.workers) continue;
+        const V A = s_map[k & 1][w][me.lane].A, M = s_back[k & 1][w][me.lane];
+        map.H = after<FORM>(map.H, A, M);
+        map.A = mul(map.A, A);
       }
-  unsigned rg[STEPS], rx[STEPS], rd[STEPS];
-  bool full = false;
-  auto load = [&](int s0) {
-    full = me.whole && s0 + at + STEPS <= len;
-    load_piece<T, VEC>(rg, gate, me.b, me.c, me.n, s0, at, len, full);
-    load_piece<T, VEC>(rx, x, me.b, me.c, me.n, s0, at, len, full);
-    if (grad.p) {
-      load_piece<T, VEC>(rd, grad, me.b, me.c, me.n, s0, at, len, full);
-    } else {
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) rd[i] = 0;
+      send(s_box, me, k, map);
     }
-  };
-  if (last >= 0) load(last);
-  if (!SHORT) cluster_wait();
-  int round = 0;
-  bool lost = false;
-  for (int s0 = last; s0 >= 0; s0 -= stride, ++round) {
-    const int parity = round & 1;
-    const int t0 = s0 + at;
-    V a[STEPS], rest[STEPS], M;
-    Map<V> map;
-    const bool all_in = full;
-    unsigned xs[STEPS], gs[STEPS];
+  } else if (me.warp > me.workers) {
+    const int kept = (time + kBlock - 1) / kBlock;
+    V carry;
+    load_state<CH>(carry, grad_final + row, grad_final ? me.n : 0);
+    bool lost = false;
+    auto before = [&](int k) {         // the state kept before the CTA's block of round k
+      const int block = (me.rounds - 1 - k) * me.ranks + me.rank;
+      V h;
+      load_state<CH>(h, states + ((long long)me.b * kept + block) * channels + me.c, k < me.rounds && block < kept ? me.n : 0);
+      return h;
+    };
+    V next = before(0);
+    for (int k = 0; k < me.rounds; ++k) {
+      V h = next;
+      next = before(k + 1);
+      join(kMapsIn + (k & 1), threads);
+#pragma unroll 1
+      for (int w0 = 0; w0 < me.workers; w0 += 4) {
+        Map<V> q[4];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) xs[i] = rx[i], gs[i] = rd[i];
-    V h;
-    load_state<CH>(h, states + ((long long)me.b * kept + t0 / DET_RECURRENCE_KEEP) * channels + me.c, t0 < len ? me.n : 0);
-    if (all_in) backward_maps<T, FORM, true>(gates, rg, xs, gs, a, rest, map, M, STEPS);
-    else backward_maps<T, FORM, false>(gates, rg, xs, gs, a, rest, map, M, len - t0);
-    if (!SHORT && s0 > 0) load(s0 - stride);
-    V m = carry;
-    if (!SHORT) {
-      s_warp[parity][me.warp][me.lane] = map;
-      s_back[parity][me.warp][me.lane] = M;
-      __syncthreads();
-      if (me.ranks > 1) {
-        if (me.warp < me.ranks) {                // warp r tells CTA r
-          map.A = s_warp[parity][kWarps - 1][me.lane].A;
-          map.H = s_back[parity][kWarps - 1][me.lane];
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) q[w] = s_map[k & 1][w0 + w][me.lane];
 #pragma unroll
-          for (int w = kWarps - 2; w >= 0; --w) {
-            const V A = s_warp[parity][w][me.lane].A;
-            map.H = after<FORM>(map.H, A, s_back[parity][w][me.lane]);
-            map.A = mul(map.A, A);
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) {
+            s_map[k & 1][w0 + w][me.lane].H = h;
+            h = after<FORM>(h, q[w].A, q[w].H);
           }
-          if (!lost) put(&s_cta[parity][me.rank][me.lane], &s_bar[parity], me.warp, map);
-        }
-        if (me.warp == 0 && me.rank % 2 == 0 && !lost) {
-          map = s_warp[parity][0][me.lane];
+      }
+      V m = receive<FORM, true>(s_box, me, k, carry, lost);
+#pragma unroll 1
+      for (int w0 = (me.workers - 1) & ~3; w0 >= 0; w0 -= 4) {
+        V A[4], M[4];
 #pragma unroll
-          for (int w = 1; w < kWarps; ++w) {
-            const Map<V> q = s_warp[parity][w][me.lane];
-            map.H = after<FORM>(map.H, q.A, q.H);
-            map.A = mul(map.A, q.A);
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) {
+            A[w] = s_map[k & 1][w0 + w][me.lane].A;
+            M[w] = s_back[k & 1][w0 + w][me.lane];
           }
-          put(&s_pair[parity][me.lane], &s_bar[parity], me.rank + 1, map);
-        }
-        if (threadIdx.x == 0 && !lost)
-          mbar_arrive_expect_tx(&s_bar[parity], (me.ranks + me.rank % 2) * 32 * (unsigned)sizeof(Map<V>));
-        lost = lost || !messages_in(&s_bar[parity], round >> 1 & 1);
-        if (lost) both(m, __int_as_float(0x7fffffff));
-        int r = me.ranks - 1;
-        for (; r > me.rank; --r) {
-          const Map<V> q = s_cta[parity][r][me.lane];
-          m = after<FORM>(m, q.A, q.H);
-        }
-        carry = m;
-        for (; r >= 0; --r) {
-          const Map<V> q = s_cta[parity][r][me.lane];
-          carry = after<FORM>(carry, q.A, q.H);
-        }
-        if (me.rank % 2) {
-          const Map<V> q = s_pair[parity][me.lane];
-          h = after<FORM>(h, q.A, q.H);
-        }
+#pragma unroll
+        for (int w = 3; w >= 0; --w)
+          if (w0 + w < me.workers) {
+            s_back[k & 1][w0 + w][me.lane] = m;
+            m = after<FORM>(m, A[w], M[w]);
+          }
       }
-      for (int w = 0; w < me.warp; ++w) {
-        const Map<V> q = s_warp[parity][w][me.lane];
-        h = after<FORM>(h, q.A, q.H);
-      }
-      for (int w = kWarps - 1; w > me.warp; --w) m = after<FORM>(m, s_warp[parity][w][me.lane].A, s_back[parity][w][me.lane]);
+      arrive(kStatesIn + (k & 1), threads - 32);
     }
-    // forward again: what l is multiplied by for the gate, without 1 - a
-    V factor[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const V xi = unpack<T>(xs[i]);
-      factor[i] = FORM == DET_GATE_DECAY ? h : mul(a[i], minus(h, xi));
-      h = fma(a[i], h, gates.input(rest[i], xi));
-    }
-    const long long base = ((long long)me.b * time + s0) * channels;
-    if (all_in) {
-      const unsigned step = (unsigned)channels * (unsigned)sizeof(T);
-      unsigned o = (unsigned)(at + STEPS) * step + (unsigned)me.c * (unsigned)sizeof(T);
-      char* bx = reinterpret_cast<char*>(grad_x + base);
-      char* bg = reinterpret_cast<char*>(grad_gate + base);
-#pragma unroll
-      for (int i = STEPS - 1; i >= 0; --i) {
-        o -= step;
-        const V l = add(unpack<T>(gs[i]), m);
-        const V dx = gates.input(rest[i], l);
-        m = mul(a[i], l);
-        store_word<T, VEC>(reinterpret_cast<T*>(bx + o), pack<T>(dx), CH);
-        store_word<T, VEC>(reinterpret_cast<T*>(bg + o), pack<T>(mul(dx, factor[i])), CH);
+    if (grad_initial && len == 0 && me.rank == 0) store_state<CH>(grad_initial + row, carry, me.n);
+  } else {
+    const Gates<T, FORM> gates;
+    const int at = me.rank * kBlock + me.warp * kSteps;
+    auto start = [&](int k) { return (me.rounds - 1 - k) * me.stride + at; };
+    auto raw = [&](int k) {
+      return reinterpret_cast<unsigned(*)[kSteps][32]>(s_raw + (k % kStages * me.workers + me.warp) * (3 * kSteps * 32));
+    };
+    Reader<T, VEC> read_gate(gate, me, start(0)), read_x(x, me, start(0)), read_grad(grad, me, start(0));
+    auto ask = [&](int k) {
+      if (k < me.rounds) {
+        read_gate.next(raw(k)[0], gate, me, start(k), -me.stride, channels);
+        read_x.next(raw(k)[1], x, me, start(k), -me.stride, channels);
+        if (grad.p) read_grad.next(raw(k)[2], grad, me, start(k), -me.stride, channels);
       }
-    } else {
-      const long long o = base + (long long)at * channels + me.c;
-#pragma unroll
-      for (int i = STEPS - 1; i >= 0; --i) {
-        const V l = add(unpack<T>(gs[i]), m);
-        const V dx = gates.input(rest[i], l);
-        const bool inside = t0 + i < len;
-        if (inside) m = mul(a[i], l);
+      copies_commit();
+    };
+    auto take = [&](int k) {
+      copies_wait_but_one();
+      __syncwarp();
+      const int t0 = start(k);
+      V M;
+      s_map[k & 1][me.warp][me.lane] = me.whole && t0 + kSteps <= len
+                                           ? piece_maps<T, FORM, true>(gates, raw(k), grad.p != nullptr, M, kSteps)
+                                           : piece_maps<T, FORM, false>(gates, raw(k), grad.p != nullptr, M, len - t0);
+      s_back[k & 1][me.warp][me.lane] = M;
+      __syncwarp();
+      arrive(kMapsIn + (k & 1), threads);
+    };
+    auto give = [&](int k) {
+      join(kStatesIn + (k & 1), threads - 32);
+      const V h = s_map[k & 1][me.warp][me.lane].H;
+      V m = s_back[k & 1][me.warp][me.lane];
+      const int t0 = start(k);
+      const long long o = ((long long)me.b * time + t0) * channels + me.c;
+      if (me.whole && t0 + kSteps <= len)
+        piece_gradients<T, FORM, VEC != 0, true>(gates, Words{raw(k), me.lane, grad.p != nullptr}, h, m, grad_x + o,
+                                                 grad_gate + o, channels, CH, kSteps, kSteps);
+      else
+        piece_gradients<T, FORM, VEC != 0, false>(gates, Words{raw(k), me.lane, grad.p != nullptr}, h, m, grad_x + o,
+                                                  grad_gate + o, channels, me.n, len - t0, me.n > 0 ? time - t0 : 0);
+      if (grad_initial && t0 == 0) store_state<CH>(grad_initial + row, m, me.n);
+      __syncwarp();
+      ask(k + kStages);
+    };
+    // past the sequence's last round
+    for (long long t0 = (long long)me.rounds * me.stride + at; t0 < time; t0 += me.stride)
+      for (int i = 0; i < kSteps; ++i)
         if (me.n > 0 && t0 + i < time) {
-          store_word<T, VEC>(grad_x + o + (long long)i * channels, inside ? pack<T>(dx) : 0u, me.n);
-          store_word<T, VEC>(grad_gate + o + (long long)i * channels, inside ? pack<T>(mul(dx, factor[i])) : 0u, me.n);
+          const long long o = ((long long)me.b * time + t0 + i) * channels + me.c;
+          store_word<T, VEC != 0>(grad_x + o, 0u, me.n);
+          store_word<T, VEC != 0>(grad_gate + o, 0u, me.n);
         }
-      }
+    if (me.rounds > 0) {
+      ask(0);
+      ask(1);
+      take(0);
+      ask(2);
     }
-    first = m;
+    for (int k = 0; k < me.rounds; ++k) {
+      if (k + 1 < me.rounds) take(k + 1);
+      give(k);
+    }
   }
-  if (!SHORT && me.ranks > 1) {
+  if (shape.log2_ranks > 0) {
     cluster_arrive();
     cluster_wait();
   }
-  if (grad_initial && (SHORT || (me.rank == 0 && me.warp == 0))) store_state<CH>(grad_initial + row, first, me.n);
 }
 
-// A launch over channel tiles and sequences: a single piece without clusters, else
-// with as many CTAs a cluster as a sequence fills, at most 8.
-template <typename T, int STEPS, typename... KArgs, typename... Args>
+template <typename T, int FORM, bool VEC>
+__global__ void __launch_bounds__(128)
+recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const float* states, const float* grad_final,
+                             T* grad_x, T* grad_gate, float* grad_initial) {
+  using V = LaneV<T>;
+  constexpr int CH = Lane<T>::CH, STEPS = kSteps;
+  dep_wait();
+  dep_launch();
+  const Gates<T, FORM> gates;
+  const Word me(shape, T());
+  if (me.n <= 0) return;
+  const long long row = (long long)me.b * shape.channels + me.c;
+  V h, m;
+  load_state<CH>(h, states + row, me.len > 0 ? me.n : 0);
+  load_state<CH>(m, grad_final + row, grad_final ? me.n : 0);
+  unsigned w[3][STEPS];
+  load_words<T, VEC>(w[0], gate, me);
+  load_words<T, VEC>(w[1], x, me);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) w[2][i] = 0;
+  if (grad.p) load_words<T, VEC>(w[2], grad, me);
+  const long long o = (long long)me.b * shape.time * shape.channels + me.c;
+  piece_gradients<T, FORM, VEC, false>(gates, WordsHeld{w}, h, m, grad_x + o, grad_gate + o, shape.channels, me.n, me.len,
+                                       shape.time);
+  if (grad_initial) store_state<CH>(grad_initial + row, m, me.n);
+}
+
+// ---------------------------------------------------------------------------
+
+// CTAs that share a sequence (a cluster), as a logarithm: what costs the least in
+// rounds of blocks, with two more for a CTA's start, over the waves of CTAs that the SMs
+// take at a time.  The bits do not depend on it.
+int choose_ranks(long long sequences, int time) {
+  const long long slots = std::max(device_sm_count(), 1);
+  int best = 0;
+  long long least = -1;
+  for (int l = 0; (1 << l) <= kMaxCluster && (l == 0 || (kBlock << (l - 1)) < time); ++l) {
+    const long long waves = ((sequences << l) + slots - 1) / slots;
+    const long long rounds = ((long long)time + (kBlock << l) - 1) / (kBlock << l);
+    const long long cost = waves * (rounds + 2);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = l;
+    }
+  }
+  return best;
+}
+
+// A launch over channel tiles and sequences, a thread a word for single pieces.
+template <typename T, int OPERANDS, typename... KArgs, typename... Args>
 int launch_recurrence(const char* name, void (*short_kernel)(KArgs...), void (*kernel)(KArgs...), int batch,
                       const Shape& shape, cudaStream_t s, Args... args) {
   const int words = (shape.channels + Lane<T>::CH - 1) / Lane<T>::CH;
-  const bool brief = shape.time <= STEPS;
-  const int ranks = 1 << shape.log2_ranks;
-  const int tiles = (words + 31) / 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = brief ? dim3((unsigned)((tiles + kWarps - 1) / kWarps), (unsigned)batch)
-                      : dim3((unsigned)tiles * ranks, (unsigned)batch);
-  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (shape.time <= kSteps) {
+    cfg.gridDim = dim3((unsigned)((words + 127) / 128), (unsigned)batch);
+    cfg.blockDim = dim3(128);
+    launch_begin(name, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, short_kernel, args...);
+    launch_end(s);
+    return e == cudaSuccess ? DET_OK : cuda_fail(e, name);
+  }
+  const int ranks = 1 << shape.log2_ranks, workers = std::min(kWorkers, (shape.time + kSteps - 1) / kSteps);
+  cfg.gridDim = dim3((unsigned)((words + 31) / 32) * ranks, (unsigned)batch);
+  cfg.blockDim = dim3(32 * (workers + 2));
+  const size_t round_bytes = (size_t)workers * OPERANDS * kSteps * 32 * 4;
+  cfg.dynamicSmemBytes = std::min<long long>(kStages, (shape.time + (long long)ranks * kBlock - 1) / (ranks * kBlock)) * round_bytes;
+  // allowed for the largest at once: a small ring may pass the default limit too, with the static arrays
+  cudaError_t e = ensure_dyn_smem((const void*)kernel, (size_t)kStages * kBlock * OPERANDS * 32 * 4);
+  if (e != cudaSuccess) return cuda_fail(e, name);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)ranks;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = brief ? 1 : 2;
+  if (ranks > 1) cfg.numAttrs = 2;
   launch_begin(name, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, brief ? short_kernel : kernel, args...);
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, name);
 }
 
-// The shape with the cluster's size, and whether 32-bit offsets reach over its spans.
-template <typename T, int STEPS>
-Shape with_ranks(Shape shape, std::initializer_list<long long> strides) {
-  while ((1 << shape.log2_ranks) < kMaxCluster && (STEPS * kWarps << shape.log2_ranks) < shape.time) ++shape.log2_ranks;
-  shape.near = 1;
-  for (const long long st : strides)
-    if (st >= (1LL << 31) || (st * (STEPS * kWarps << shape.log2_ranks) + shape.channels) * (long long)sizeof(T) >= (1LL << 31))
-      shape.near = 0;
-  return shape;
+template <typename T, int FORM, int VEC>
+int forward(const View& x, const View& gate, Shape shape, int batch, const float* initial, void* out, float* final_out,
+            float* states, cudaStream_t s) {
+  shape.log2_ranks = choose_ranks((long long)batch * ((shape.channels + 32 * Lane<T>::CH - 1) / (32 * Lane<T>::CH)),
+                                  shape.time);
+  return launch_recurrence<T, 2>("det_linear_recurrence", recurrence_short_kernel<T, FORM, VEC != 0>,
+                                                recurrence_kernel<T, FORM, VEC>, batch, shape, s, x, gate, shape, initial,
+                                                static_cast<T*>(out), final_out, states);
+}
+template <typename T, int FORM, int VEC>
+int backward(const View& grad, const View& x, const View& gate, Shape shape, int batch, const float* states,
+             const float* grad_final, void* grad_x, void* grad_gate, float* grad_initial, cudaStream_t s) {
+  shape.log2_ranks = choose_ranks((long long)batch * ((shape.channels + 32 * Lane<T>::CH - 1) / (32 * Lane<T>::CH)),
+                                  shape.time);
+  return launch_recurrence<T, 3>(
+      "det_linear_recurrence_backward", recurrence_grad_short_kernel<T, FORM, VEC != 0>,
+      recurrence_grad_kernel<T, FORM, VEC>, batch, shape, s, grad, x, gate, shape, states, grad_final,
+      static_cast<T*>(grad_x), static_cast<T*>(grad_gate), grad_initial);
 }
 
-template <typename T, int FORM, bool VEC>
-int forward(const View& x, const View& gate, const Shape& shape, int batch, const float* initial, void* out,
-            float* final_out, float* states, cudaStream_t s) {
-  const Shape sh = with_ranks<T, kStepsForward>(shape, {x.st, gate.st, shape.channels});
-  return launch_recurrence<T, kStepsForward>("det_linear_recurrence", recurrence_kernel<T, FORM, VEC, true>,
-                                             recurrence_kernel<T, FORM, VEC, false>, batch, sh, s, x, gate, sh, initial,
-                                             static_cast<T*>(out), final_out, states);
-}
-template <typename T, int FORM, bool VEC>
-int backward(const View& grad, const View& x, const View& gate, const Shape& shape, int batch, const float* states,
-             const float* grad_final, void* grad_x, void* grad_gate, float* grad_initial, cudaStream_t s) {
-  const Shape sh = with_ranks<T, kStepsBackward>(shape, {grad.st, x.st, gate.st, shape.channels});
-  return launch_recurrence<T, kStepsBackward>(
-      "det_linear_recurrence_backward", recurrence_grad_kernel<T, FORM, VEC, true>,
-      recurrence_grad_kernel<T, FORM, VEC, false>, batch, sh, s, grad, x, gate, sh, states, grad_final,
-      static_cast<T*>(grad_x), static_cast<T*>(grad_gate), grad_initial);
+// How rows are read: 2 where all start on 16 bytes and are whole vectors, 1 where all
+// start on a word and are whole words, 0 else.
+int reading(int dtype, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> strides) {
+  uintptr_t all = 0;
+  for (const void* p : pointers) all |= reinterpret_cast<uintptr_t>(p);
+  for (const int64_t st : strides) all |= (uintptr_t)st * model_elem_size(dtype);
+  return all % 16 == 0 ? 2 : all % 4 == 0 ? 1 : 0;
 }
 
 int check_shape(int dtype, int form, int64_t batch, int64_t time, int64_t channels) {
@@ -717,22 +977,17 @@ bool misaligned_floats(const void* p) { return reinterpret_cast<uintptr_t>(p) % 
 
 using namespace det;
 
-// Two channels a lane go as one word where every row of every operand starts on one.
-#define DET_RECURRENCE_PICK(fn, ...)                                                                                  \
-  do {                                                                                                               \
-    if (dtype == DET_F32)                                                                                            \
-      return form == DET_GATE_DECAY ? fn<float, DET_GATE_DECAY, true>(__VA_ARGS__)                                   \
-                                    : fn<float, DET_GATE_SIGMOID, true>(__VA_ARGS__);                                \
-    if (dtype == DET_BF16)                                                                                           \
-      return form == DET_GATE_DECAY ? (words ? fn<__nv_bfloat16, DET_GATE_DECAY, true>(__VA_ARGS__)                  \
-                                             : fn<__nv_bfloat16, DET_GATE_DECAY, false>(__VA_ARGS__))                \
-                                    : (words ? fn<__nv_bfloat16, DET_GATE_SIGMOID, true>(__VA_ARGS__)                \
-                                             : fn<__nv_bfloat16, DET_GATE_SIGMOID, false>(__VA_ARGS__));             \
-    return form == DET_GATE_DECAY                                                                                    \
-               ? (words ? fn<__half, DET_GATE_DECAY, true>(__VA_ARGS__) : fn<__half, DET_GATE_DECAY, false>(__VA_ARGS__)) \
-               : (words ? fn<__half, DET_GATE_SIGMOID, true>(__VA_ARGS__)                                            \
-                        : fn<__half, DET_GATE_SIGMOID, false>(__VA_ARGS__));                                         \
-  } while (0)
+#define DET_RECURRENCE_FORM(fn, T, VEC, ...) \
+  (form == DET_GATE_DECAY ? fn<T, DET_GATE_DECAY, VEC>(__VA_ARGS__) : fn<T, DET_GATE_SIGMOID, VEC>(__VA_ARGS__))
+#define DET_RECURRENCE_16(fn, T, ...)                                       \
+  (how == 2   ? DET_RECURRENCE_FORM(fn, T, 2, __VA_ARGS__)                  \
+   : how == 1 ? DET_RECURRENCE_FORM(fn, T, 1, __VA_ARGS__)                  \
+              : DET_RECURRENCE_FORM(fn, T, 0, __VA_ARGS__))
+#define DET_RECURRENCE_PICK(fn, ...)                                         \
+  (dtype == DET_F32    ? (how == 2 ? DET_RECURRENCE_FORM(fn, float, 2, __VA_ARGS__)  \
+                                   : DET_RECURRENCE_FORM(fn, float, 1, __VA_ARGS__)) \
+   : dtype == DET_BF16 ? DET_RECURRENCE_16(fn, __nv_bfloat16, __VA_ARGS__)   \
+                       : DET_RECURRENCE_16(fn, __half, __VA_ARGS__))
 
 extern "C" int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t x_stride_t, const void* gate,
                                      int64_t gate_stride_b, int64_t gate_stride_t, int dtype, int form, int64_t batch,
@@ -745,13 +1000,11 @@ extern "C" int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t 
   if (misaligned(x, dtype) || misaligned(gate, dtype) || misaligned(out, dtype) || misaligned_floats(initial) ||
       misaligned_floats(lengths) || misaligned_floats(final_out) || misaligned_floats(states_out))
     return DET_ERR_INVALID_ARG;
-  const bool words = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gate) |
-                       reinterpret_cast<uintptr_t>(out)) % 4 == 0) &&
-                     ((x_stride_b | x_stride_t | gate_stride_b | gate_stride_t | channels) % 2 == 0);
+  const int how = reading(dtype, {x, gate, out}, {x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vx = {x, x_stride_b, x_stride_t}, vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0, 0};
+  const Shape shape = {(int)time, (int)channels, lengths, 0};
   const cudaStream_t s = as_stream(stream);
-  DET_RECURRENCE_PICK(forward, vx, vg, shape, (int)batch, initial, out, final_out, states_out, s);
+  return DET_RECURRENCE_PICK(forward, vx, vg, shape, (int)batch, initial, out, final_out, states_out, s);
 }
 
 extern "C" int det_linear_recurrence_backward(const void* grad, int64_t grad_stride_b, int64_t grad_stride_t,
@@ -769,13 +1022,11 @@ extern "C" int det_linear_recurrence_backward(const void* grad, int64_t grad_str
       misaligned(grad_gate, dtype) || misaligned_floats(states) || misaligned_floats(grad_final) ||
       misaligned_floats(lengths) || misaligned_floats(grad_initial))
     return DET_ERR_INVALID_ARG;
-  const bool words =
-      ((reinterpret_cast<uintptr_t>(grad) | reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gate) |
-        reinterpret_cast<uintptr_t>(grad_x) | reinterpret_cast<uintptr_t>(grad_gate)) % 4 == 0) &&
-      ((grad_stride_b | grad_stride_t | x_stride_b | x_stride_t | gate_stride_b | gate_stride_t | channels) % 2 == 0);
+  const int how = reading(dtype, {grad, x, gate, grad_x, grad_gate},
+                          {grad_stride_b, grad_stride_t, x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vd = {grad, grad_stride_b, grad_stride_t}, vx = {x, x_stride_b, x_stride_t},
              vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0, 0};
+  const Shape shape = {(int)time, (int)channels, lengths, 0};
   const cudaStream_t s = as_stream(stream);
-  DET_RECURRENCE_PICK(backward, vd, vx, vg, shape, (int)batch, states, grad_final, grad_x, grad_gate, grad_initial, s);
+  return DET_RECURRENCE_PICK(backward, vd, vx, vg, shape, (int)batch, states, grad_final, grad_x, grad_gate, grad_initial, s);
 }

@@ -954,7 +954,7 @@ def det_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Ten
 
 
 GATE_FORMS = {"decay": 0, "sigmoid": 1}
-RECURRENCE_KEEP, RECURRENCE_SPAN = 128, 1024    # det_model.h
+RECURRENCE_KEEP = 128    # det_model.h
 
 
 class LinearRecurrence(NamedTuple):

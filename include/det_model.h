@@ -271,7 +271,7 @@ int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x
 #define DET_GATE_DECAY 0
 #define DET_GATE_SIGMOID 1
 #define DET_RECURRENCE_KEEP 128
-#define DET_RECURRENCE_SPAN 1024
+#define DET_RECURRENCE_SPAN 128
 int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t x_stride_t, const void* gate,
                           int64_t gate_stride_b, int64_t gate_stride_t, int dtype, int form, int64_t batch,
                           int64_t time, int64_t channels, const float* initial, const int32_t* lengths, void* out,
