@@ -66,6 +66,11 @@ __device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, un
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ unsigned long long sub_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // A 32-bit key in the order of the values: -0 and +0 are equal, NaN is above
 // +inf.
@@ -148,11 +153,15 @@ __device__ __forceinline__ void unpack_eight(const Eight<T>& e, float (&v)[8]) {
   unpack_two(e.q.z, v[4], v[5], T());
   unpack_two(e.q.w, v[6], v[7], T());
 }
-__device__ __forceinline__ unsigned short bits16(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
-__device__ __forceinline__ unsigned short bits16(__half v) { return __half_as_ushort(v); }
-template <typename T>
-__device__ __forceinline__ unsigned pack_two(float a, float b) {
-  return (unsigned)bits16(from_f32<T>(a)) | (unsigned)bits16(from_f32<T>(b)) << 16;
+// Two values rounded to 16 bits each, a in the lower half.
+template <typename T> __device__ __forceinline__ unsigned pack_two(float a, float b);
+template <> __device__ __forceinline__ unsigned pack_two<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&v);
+}
+template <> __device__ __forceinline__ unsigned pack_two<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&v);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_eight(T* p, const float (&v)[8], int n) {

@@ -67,7 +67,7 @@ __device__ __forceinline__ Two fma(Two a, Two b, Two c) { return fma_f32x2(a, b,
 __device__ __forceinline__ void both(float& v, float x) { v = x; }
 __device__ __forceinline__ void both(Two& v, float x) { v = pack_f32x2(x, x); }
 __device__ __forceinline__ float minus(float a, float b) { return __fsub_rn(a, b); }
-__device__ __forceinline__ Two minus(Two a, Two b) { return fma_f32x2(b, pack_f32x2(-1.0f, -1.0f), a); }
+__device__ __forceinline__ Two minus(Two a, Two b) { return sub_f32x2(a, b); }
 
 template <typename T> struct Lane {
   static constexpr int CH = 2;
@@ -340,9 +340,9 @@ struct Reader {
   __device__ __forceinline__ Reader(const View& v, const Place<T>& me, int first) {
     p = static_cast<const T*>(v.p) + (me.b * v.sb + (first + (VEC == 2 ? me.lane >> 3 : 0)) * v.st + first_channel(me));
   }
-  // the piece from step t0 on; by: steps to the next round's
-  __device__ __forceinline__ void next(unsigned (*to)[32], const View& v, const Place<T>& me, int t0, int by, int channels) {
-    const bool full = me.whole && t0 + kSteps <= me.len;
+  // the piece from step t0 on, with all its steps and channels if full; by: steps to the next round's
+  __device__ __forceinline__ void next(unsigned (*to)[32], const View& v, const Place<T>& me, bool full, int t0, int by,
+                                       int channels) {
     const long long step = kRows * v.st;
     if constexpr (VEC == 0) {
       unsigned w[kSteps];
@@ -368,6 +368,15 @@ struct Reader {
       }
     }
     p += by * v.st;
+  }
+};
+
+// A warp's part of the stages.
+struct Ring {
+  unsigned* first;
+  int words;             // from one stage to the next
+  __device__ __forceinline__ unsigned (*at(int stage) const)[kSteps][32] {
+    return reinterpret_cast<unsigned(*)[kSteps][32]>(first + stage * words);
   }
 };
 
@@ -501,54 +510,59 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
   } else {
     const Gates<T, FORM> gates;
     const int at = me.rank * kBlock + me.warp * kSteps;
-    auto raw = [&](int k) {
-      return reinterpret_cast<unsigned(*)[kSteps][32]>(s_raw + (k % kStages * me.workers + me.warp) * (2 * kSteps * 32));
-    };
+    // the rounds before this one have whole pieces here
+    const int whole = me.whole && len >= at + kSteps ? (len - at - kSteps) / me.stride + 1 : 0;
+    // and this one has the sequence's last step
+    const int end = len > at && (len - 1 - at) % me.stride < kSteps ? (len - 1 - at) / me.stride : -1;
+    const Ring ring{s_raw + me.warp * (2 * kSteps * 32), me.workers * (2 * kSteps * 32)};
     Reader<T, VEC> read_gate(gate, me, at), read_x(x, me, at);
-    auto ask = [&](int k) {            // for the piece of round k, if there is one; in the rounds' order
+    auto ask = [&](int k, unsigned (*to)[kSteps][32]) {       // for the piece of round k, if there is one; in the rounds' order
       if (k < me.rounds) {
-        read_gate.next(raw(k)[0], gate, me, k * me.stride + at, me.stride, channels);
-        read_x.next(raw(k)[1], x, me, k * me.stride + at, me.stride, channels);
+        read_gate.next(to[0], gate, me, k < whole, k * me.stride + at, me.stride, channels);
+        read_x.next(to[1], x, me, k < whole, k * me.stride + at, me.stride, channels);
       }
       copies_commit();
     };
+    int taken = 0;                     // stage of the next piece
     auto take = [&](int k, V (&a)[kSteps], V (&u)[kSteps]) {
       copies_wait_but_two();
       __syncwarp();
-      const int t0 = k * me.stride + at;
-      unsigned(*w)[kSteps][32] = raw(k);
-      s_map[k & 1][me.warp][me.lane] = me.whole && t0 + kSteps <= len
+      unsigned(*w)[kSteps][32] = ring.at(taken);
+      s_map[k & 1][me.warp][me.lane] = k < whole
                                            ? piece_map<T, FORM, true>(gates, w[0], w[1], a, u, kSteps)
-                                           : piece_map<T, FORM, false>(gates, w[0], w[1], a, u, len - t0);
+                                           : piece_map<T, FORM, false>(gates, w[0], w[1], a, u, len - at - k * me.stride);
       __syncwarp();
       arrive(kMapsIn + (k & 1), threads);
-      ask(k + kStages);
+      ask(k + kStages, w);             // into the same stage
+      taken = taken + 1 == kStages ? 0 : taken + 1;
     };
+    T* o = out + ((long long)me.b * time + at) * channels + me.c;
     auto give = [&](int k, const V (&a)[kSteps], const V (&u)[kSteps]) {
       join(kStatesIn + (k & 1), threads - 32);
       V h = s_map[k & 1][me.warp][me.lane].A;
-      const int t0 = k * me.stride + at;
-      T* o = out + ((long long)me.b * time + t0) * channels + me.c;
-      if (me.whole && t0 + kSteps <= len) {
+      T* q = o;
+      if (k < whole) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i, o += channels) {
+        for (int i = 0; i < kSteps; ++i, q += channels) {
           h = fma(a[i], h, u[i]);
-          store_word<T, VEC != 0>(o, pack<T>(h), CH);
+          store_word<T, VEC != 0>(q, pack<T>(h), CH);
         }
       } else {
+        const int t0 = k * me.stride + at;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i, o += channels) {
+        for (int i = 0; i < kSteps; ++i, q += channels) {
           h = fma(a[i], h, u[i]);
-          if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(o, t0 + i < len ? pack<T>(h) : 0u, me.n);
+          if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(q, t0 + i < len ? pack<T>(h) : 0u, me.n);
         }
       }
+      o += (long long)me.stride * channels;
       // the state at the end is that of the last step (steps past it have kept it); the
       // initial state has been read everywhere by now, so it may lie in the same place
-      if (final_out && t0 < len && len <= t0 + kSteps) store_state<CH>(final_out + row, h, me.n);
+      if (k == end && final_out) store_state<CH>(final_out + row, h, me.n);
     };
     V a0[kSteps], u0[kSteps], a1[kSteps], u1[kSteps];
     if (me.rounds > 0) {
-      for (int k = 0; k < kStages; ++k) ask(k);
+      for (int k = 0; k < kStages; ++k) ask(k, ring.at(k));
       take(0, a0, u0);
     }
     for (int k = 0; k < me.rounds; k += 2) {
@@ -779,47 +793,54 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
     if (grad_initial && len == 0 && me.rank == 0) store_state<CH>(grad_initial + row, carry, me.n);
   } else {
     const Gates<T, FORM> gates;
-    const int at = me.rank * kBlock + me.warp * kSteps;
-    auto start = [&](int k) { return (me.rounds - 1 - k) * me.stride + at; };
-    auto raw = [&](int k) {
-      return reinterpret_cast<unsigned(*)[kSteps][32]>(s_raw + (k % kStages * me.workers + me.warp) * (3 * kSteps * 32));
-    };
-    Reader<T, VEC> read_gate(gate, me, start(0)), read_x(x, me, start(0)), read_grad(grad, me, start(0));
-    auto ask = [&](int k) {
+    const int at = me.rank * kBlock + me.warp * kSteps, last = (me.rounds - 1) * me.stride + at;
+    // from this round on the pieces are whole
+    const int whole = me.whole && len >= at + kSteps ? me.rounds - 1 - (len - at - kSteps) / me.stride : me.rounds;
+    const Ring ring{s_raw + me.warp * (3 * kSteps * 32), me.workers * (3 * kSteps * 32)};
+    const bool graded = grad.p != nullptr;
+    Reader<T, VEC> read_gate(gate, me, last), read_x(x, me, last), read_grad(grad, me, last);
+    auto ask = [&](int k, unsigned (*to)[kSteps][32]) {
       if (k < me.rounds) {
-        read_gate.next(raw(k)[0], gate, me, start(k), -me.stride, channels);
-        read_x.next(raw(k)[1], x, me, start(k), -me.stride, channels);
-        if (grad.p) read_grad.next(raw(k)[2], grad, me, start(k), -me.stride, channels);
+        const int t0 = last - k * me.stride;
+        read_gate.next(to[0], gate, me, k >= whole, t0, -me.stride, channels);
+        read_x.next(to[1], x, me, k >= whole, t0, -me.stride, channels);
+        if (graded) read_grad.next(to[2], grad, me, k >= whole, t0, -me.stride, channels);
       }
       copies_commit();
     };
+    int taken = 0, given = 0;          // stages
     auto take = [&](int k) {
       copies_wait_but_one();
       __syncwarp();
-      const int t0 = start(k);
       V M;
-      s_map[k & 1][me.warp][me.lane] = me.whole && t0 + kSteps <= len
-                                           ? piece_maps<T, FORM, true>(gates, raw(k), grad.p != nullptr, M, kSteps)
-                                           : piece_maps<T, FORM, false>(gates, raw(k), grad.p != nullptr, M, len - t0);
+      unsigned(*w)[kSteps][32] = ring.at(taken);
+      s_map[k & 1][me.warp][me.lane] =
+          k >= whole ? piece_maps<T, FORM, true>(gates, w, graded, M, kSteps)
+                     : piece_maps<T, FORM, false>(gates, w, graded, M, len - (last - k * me.stride));
       s_back[k & 1][me.warp][me.lane] = M;
       __syncwarp();
       arrive(kMapsIn + (k & 1), threads);
+      taken = taken + 1 == kStages ? 0 : taken + 1;
     };
+    long long o = ((long long)me.b * time + last) * channels + me.c;
     auto give = [&](int k) {
       join(kStatesIn + (k & 1), threads - 32);
       const V h = s_map[k & 1][me.warp][me.lane].H;
       V m = s_back[k & 1][me.warp][me.lane];
-      const int t0 = start(k);
-      const long long o = ((long long)me.b * time + t0) * channels + me.c;
-      if (me.whole && t0 + kSteps <= len)
-        piece_gradients<T, FORM, VEC != 0, true>(gates, Words{raw(k), me.lane, grad.p != nullptr}, h, m, grad_x + o,
-                                                 grad_gate + o, channels, CH, kSteps, kSteps);
-      else
-        piece_gradients<T, FORM, VEC != 0, false>(gates, Words{raw(k), me.lane, grad.p != nullptr}, h, m, grad_x + o,
-                                                  grad_gate + o, channels, me.n, len - t0, me.n > 0 ? time - t0 : 0);
-      if (grad_initial && t0 == 0) store_state<CH>(grad_initial + row, m, me.n);
+      unsigned(*w)[kSteps][32] = ring.at(given);
+      if (k >= whole) {
+        piece_gradients<T, FORM, VEC != 0, true>(gates, Words{w, me.lane, graded}, h, m, grad_x + o, grad_gate + o, channels,
+                                                 CH, kSteps, kSteps);
+      } else {
+        const int t0 = last - k * me.stride;
+        piece_gradients<T, FORM, VEC != 0, false>(gates, Words{w, me.lane, graded}, h, m, grad_x + o, grad_gate + o,
+                                                  channels, me.n, len - t0, me.n > 0 ? time - t0 : 0);
+      }
+      o -= (long long)me.stride * channels;
+      if (at == 0 && k + 1 == me.rounds && grad_initial) store_state<CH>(grad_initial + row, m, me.n);
       __syncwarp();
-      ask(k + kStages);
+      ask(k + kStages, w);
+      given = given + 1 == kStages ? 0 : given + 1;
     };
     // past the sequence's last round
     for (long long t0 = (long long)me.rounds * me.stride + at; t0 < time; t0 += me.stride)
@@ -830,10 +851,10 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
           store_word<T, VEC != 0>(grad_gate + o, 0u, me.n);
         }
     if (me.rounds > 0) {
-      ask(0);
-      ask(1);
+      ask(0, ring.at(0));
+      ask(1, ring.at(1));
       take(0);
-      ask(2);
+      ask(2, ring.at(2));
     }
     for (int k = 0; k < me.rounds; ++k) {
       if (k + 1 < me.rounds) take(k + 1);
