@@ -33,6 +33,10 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <map>
+#include <mutex>
+#include <tuple>
+#include <type_traits>
 
 namespace det {
 namespace {
@@ -205,19 +209,22 @@ struct Gates {
   __device__ __forceinline__ V input(V rest, V x) const { return FORM == DET_GATE_DECAY ? x : mul(rest, x); }
 };
 
-// The state h after a piece (A, H).  Decays above 1 may take A out of the range of
-// 32 bits where the states stay in it: from 0 the state is H whatever A is.
+// The state h after a run of steps (A, H).
+template <typename V>
+__device__ __forceinline__ V after(V h, V A, V H) { return fma(A, h, H); }
+// After whole blocks.  Decays above 1 may take a block's A out of the range of 32 bits
+// where the states stay in it: from 0 the state is H whatever A is.
 template <int FORM>
-__device__ __forceinline__ float after(float h, float A, float H) {
+__device__ __forceinline__ float after_block(float h, float A, float H) {
   return FORM == DET_GATE_DECAY && h == 0.0f ? H : fmaf(A, h, H);
 }
 template <int FORM>
-__device__ __forceinline__ Two after(Two h, Two A, Two H) {
+__device__ __forceinline__ Two after_block(Two h, Two A, Two H) {
   if constexpr (FORM == DET_GATE_SIGMOID) {
     return fma(A, h, H);
   } else {
     const float2 g = unpack_f32x2(h), a = unpack_f32x2(A), b = unpack_f32x2(H);
-    return pack_f32x2(after<FORM>(g.x, a.x, b.x), after<FORM>(g.y, a.y, b.y));
+    return pack_f32x2(after_block<FORM>(g.x, a.x, b.x), after_block<FORM>(g.y, a.y, b.y));
   }
 }
 
@@ -230,27 +237,19 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 template <typename V> struct alignas(2 * sizeof(V)) Map {
   V A, H;
 };
-// v to the place of `local` in the shared memory of the cluster's CTA `rank`, counted
-// there on the barrier at the place of `bar`.  (A barrier of the whole cluster
-// would first wait for the stores of outputs in flight: 1 x 65,536 x 2,048 in bf16
-// took 239 us with it, 202 without.)
-__device__ __forceinline__ unsigned remote(const void* local, int rank) {
-  unsigned r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void put(Map<Two>* local, unsigned long long* bar, int rank, const Map<Two>& v) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
-                   remote(local, rank)),
-               "l"(v.A), "l"(v.H), "r"(remote(bar, rank))
+// `bytes` from `from` to the place of `to` in the shared memory of the cluster's CTA `rank`,
+// counted there on the barrier at the place of `bar`.  (A barrier of the whole cluster
+// in its place would wait for all stores of outputs in flight.)
+__device__ __forceinline__ void copy_to(int rank, void* to, const void* from, unsigned bytes, unsigned long long* bar) {
+  unsigned dst, remote_bar;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote_bar) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(from)), "r"(bytes), "r"(remote_bar)
                : "memory");
 }
-__device__ __forceinline__ void put(Map<float>* local, unsigned long long* bar, int rank, const Map<float>& v) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
-                   remote(local, rank)),
-               "r"(__float_as_uint(v.A)), "r"(__float_as_uint(v.H)), "r"(remote(bar, rank))
-               : "memory");
-}
+// Writes to shared memory before it are seen by copies after it.
+__device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Waits for a phase of messages, for about kWaitNs at most.  (The timer is read after
 // many polls only: reading it takes as long as a message.)
 template <bool CLUSTER>
@@ -279,13 +278,23 @@ __device__ __forceinline__ bool messages_in(unsigned long long* bar, unsigned ph
 
 // Between warps of a CTA: arrive() does not wait, join() waits until all of the
 // barrier's threads have come.
-__device__ __forceinline__ void arrive(int barrier, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+template <int BARRIER>
+__device__ __forceinline__ void arrive(int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"n"(BARRIER), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void join(int barrier, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+template <int BARRIER>
+__device__ __forceinline__ void join(int threads) {
+  asm volatile("bar.sync %0, %1;" ::"n"(BARRIER), "r"(threads) : "memory");
 }
-constexpr int kMapsIn = 1, kStatesIn = 3;      // named barriers, two each for odd and even rounds
+constexpr int kMapsIn = 1, kStatesIn = 3;      // named barriers, two each for even and odd rounds
+// f(0 or 1, k) for every round k, with k's parity as a constant.
+template <typename F>
+__device__ __forceinline__ void each_round(int rounds, F&& f) {
+  for (int k = 0; k < rounds; k += 2) {
+    f(std::integral_constant<int, 0>(), k);
+    if (k + 1 < rounds) f(std::integral_constant<int, 1>(), k + 1);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // Where a CTA works: blocks rank, rank + ranks, ... of a sequence, 32 words of
@@ -383,9 +392,11 @@ struct Ring {
 // ---------------------------------------------------------------------------
 // What CTAs of a cluster tell each other: the map of each one's block.  Messages of
 // four rounds have places: a CTA may be told of round k + 2 while it still reads those
-// of k and k - 1.
+// of k and k - 1.  (A CTA sends round k + 4 after it has heard of everyone's round k + 2, which
+// is sent after round k has been heard: by then its own place is free too.)
 template <typename V>
 struct Messages {
+  alignas(16) Map<V> mine[4][32];
   Map<V> from[4][kMaxCluster][32];
   unsigned long long bar[4];
 };
@@ -398,8 +409,12 @@ __device__ __forceinline__ void send(Messages<V>& box, const PLACE& me, int roun
     if (me.lane == 0) mbar_arrive(&box.bar[k]);
     return;
   }
+  box.mine[k][me.lane] = map;
+  fence_copies();
   if (me.lane == 0) mbar_arrive_expect_tx(&box.bar[k], me.ranks * 32 * (unsigned)sizeof(Map<V>));
-  for (int r = 0; r < me.ranks; ++r) put(&box.from[k][me.rank][me.lane], &box.bar[k], r, map);
+  __syncwarp();
+  if (me.lane < me.ranks)
+    copy_to(me.lane, &box.from[k][me.rank][0], &box.mine[k][0], 32 * (unsigned)sizeof(Map<V>), &box.bar[k]);
 }
 // The state (or what comes back) at the CTA's block, from the one at the cluster's
 // blocks, v, which moves on past them.  BACK: from the last block to the first.
@@ -414,7 +429,7 @@ __device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int roun
   for (int j = 0, r = first; j < me.ranks; ++j, r += by) {
     if (r == me.rank) here = v;
     const Map<V> q = box.from[k][r][me.lane];
-    v = after<FORM>(v, q.A, q.H);
+    v = after_block<FORM>(v, q.A, q.H);
   }
   return here;
 }
@@ -467,24 +482,34 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
 
   if (me.warp == me.workers) {
     // tells of the CTA's blocks
-    for (int k = 0; k < me.rounds; ++k) {
-      join(kMapsIn + (k & 1), threads);
-      Map<V> map = s_map[k & 1][0][me.lane];
+    each_round(me.rounds, [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
+      join<kMapsIn + P>(threads);
+      Map<V> map;
+      both(map.A, 1.0f);
+      both(map.H, 0.0f);
+#pragma unroll 1
+      for (int w0 = 0; w0 < me.workers; w0 += 4) {           // four at a time are on their way
+        Map<V> q[4];
 #pragma unroll
-      for (int w = 1; w < kWorkers; ++w) {
-        if (w >= me.workers) break;
-        const Map<V> q = s_map[k & 1][w][me.lane];
-        map.H = after<FORM>(map.H, q.A, q.H);
-        map.A = mul(map.A, q.A);
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) q[w] = s_map[P][w0 + w][me.lane];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) {
+            map.H = after(map.H, q[w].A, q[w].H);
+            map.A = mul(map.A, q[w].A);
+          }
       }
       send(s_box, me, k, map);
-    }
+    });
   } else if (me.warp > me.workers) {
     // hears of the cluster's, and hands out states
     const int kept = (time + kBlock - 1) / kBlock;
     bool lost = false;                 // a wait gave up: states are NaN from there on
-    for (int k = 0; k < me.rounds; ++k) {
-      join(kMapsIn + (k & 1), threads);
+    each_round(me.rounds, [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
+      join<kMapsIn + P>(threads);
       V h = receive<FORM, false>(s_box, me, k, carry, lost);
       const int block = k * me.ranks + me.rank;
       if (states && block < kept) store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, h, me.n);
@@ -493,16 +518,16 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
         Map<V> q[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          if (w0 + w < me.workers) q[w] = s_map[k & 1][w0 + w][me.lane];
+          if (w0 + w < me.workers) q[w] = s_map[P][w0 + w][me.lane];
 #pragma unroll
         for (int w = 0; w < 4; ++w)
           if (w0 + w < me.workers) {
-            s_map[k & 1][w0 + w][me.lane].A = h;
-            h = after<FORM>(h, q[w].A, q[w].H);
+            s_map[P][w0 + w][me.lane].A = h;
+            h = after(h, q[w].A, q[w].H);
           }
       }
-      arrive(kStatesIn + (k & 1), threads - 32);
-    }
+      arrive<kStatesIn + P>(threads - 32);
+    });
     if (states)                        // past the sequence's last round
       for (int block = me.rounds * me.ranks + me.rank; block < kept; block += me.ranks)
         store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, carry, me.n);
@@ -524,22 +549,24 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
       copies_commit();
     };
     int taken = 0;                     // stage of the next piece
-    auto take = [&](int k, V (&a)[kSteps], V (&u)[kSteps]) {
+    auto take = [&](auto parity, int k, V (&a)[kSteps], V (&u)[kSteps]) {
+      constexpr int P = decltype(parity)::value;
       copies_wait_but_two();
       __syncwarp();
       unsigned(*w)[kSteps][32] = ring.at(taken);
-      s_map[k & 1][me.warp][me.lane] = k < whole
+      s_map[P][me.warp][me.lane] = k < whole
                                            ? piece_map<T, FORM, true>(gates, w[0], w[1], a, u, kSteps)
                                            : piece_map<T, FORM, false>(gates, w[0], w[1], a, u, len - at - k * me.stride);
       __syncwarp();
-      arrive(kMapsIn + (k & 1), threads);
+      arrive<kMapsIn + P>(threads);
       ask(k + kStages, w);             // into the same stage
       taken = taken + 1 == kStages ? 0 : taken + 1;
     };
     T* o = out + ((long long)me.b * time + at) * channels + me.c;
-    auto give = [&](int k, const V (&a)[kSteps], const V (&u)[kSteps]) {
-      join(kStatesIn + (k & 1), threads - 32);
-      V h = s_map[k & 1][me.warp][me.lane].A;
+    auto give = [&](auto parity, int k, const V (&a)[kSteps], const V (&u)[kSteps]) {
+      constexpr int P = decltype(parity)::value;
+      join<kStatesIn + P>(threads - 32);
+      V h = s_map[P][me.warp][me.lane].A;
       T* q = o;
       if (k < whole) {
 #pragma unroll
@@ -560,17 +587,19 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
       // initial state has been read everywhere by now, so it may lie in the same place
       if (k == end && final_out) store_state<CH>(final_out + row, h, me.n);
     };
+    constexpr std::integral_constant<int, 0> even;
+    constexpr std::integral_constant<int, 1> odd;
     V a0[kSteps], u0[kSteps], a1[kSteps], u1[kSteps];
     if (me.rounds > 0) {
       for (int k = 0; k < kStages; ++k) ask(k, ring.at(k));
-      take(0, a0, u0);
+      take(even, 0, a0, u0);
     }
     for (int k = 0; k < me.rounds; k += 2) {
-      if (k + 1 < me.rounds) take(k + 1, a1, u1);
-      give(k, a0, u0);
+      if (k + 1 < me.rounds) take(odd, k + 1, a1, u1);
+      give(even, k, a0, u0);
       if (k + 1 == me.rounds) break;
-      if (k + 2 < me.rounds) take(k + 2, a0, u0);
-      give(k + 1, a1, u1);
+      if (k + 2 < me.rounds) take(even, k + 2, a0, u0);
+      give(odd, k + 1, a1, u1);
     }
     // past the sequence's last round
     for (long long t0 = (long long)me.rounds * me.stride + at; t0 < time; t0 += me.stride)
@@ -728,20 +757,30 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
   // round k takes the blocks from (rounds - 1 - k) * ranks on
 
   if (me.warp == me.workers) {
-    for (int k = 0; k < me.rounds; ++k) {
-      join(kMapsIn + (k & 1), threads);
+    each_round(me.rounds, [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
+      join<kMapsIn + P>(threads);
       Map<V> map;
       both(map.A, 1.0f);
       both(map.H, 0.0f);
+#pragma unroll 1
+      for (int w0 = (me.workers - 1) & ~3; w0 >= 0; w0 -= 4) {
+        V A[4], M[4];
 #pragma unroll
-      for (int w = kWorkers - 1; w >= 0; --w) {
-        if (w >= me.workers) continue;
-        const V A = s_map[k & 1][w][me.lane].A, M = s_back[k & 1][w][me.lane];
-        map.H = after<FORM>(map.H, A, M);
-        map.A = mul(map.A, A);
+        for (int w = 0; w < 4; ++w)
+          if (w0 + w < me.workers) {
+            A[w] = s_map[P][w0 + w][me.lane].A;
+            M[w] = s_back[P][w0 + w][me.lane];
+          }
+#pragma unroll
+        for (int w = 3; w >= 0; --w)
+          if (w0 + w < me.workers) {
+            map.H = after(map.H, A[w], M[w]);
+            map.A = mul(map.A, A[w]);
+          }
       }
       send(s_box, me, k, map);
-    }
+    });
   } else if (me.warp > me.workers) {
     const int kept = (time + kBlock - 1) / kBlock;
     V carry;
@@ -754,21 +793,22 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
       return h;
     };
     V next = before(0);
-    for (int k = 0; k < me.rounds; ++k) {
+    each_round(me.rounds, [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
       V h = next;
       next = before(k + 1);
-      join(kMapsIn + (k & 1), threads);
+      join<kMapsIn + P>(threads);
 #pragma unroll 1
       for (int w0 = 0; w0 < me.workers; w0 += 4) {
         Map<V> q[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          if (w0 + w < me.workers) q[w] = s_map[k & 1][w0 + w][me.lane];
+          if (w0 + w < me.workers) q[w] = s_map[P][w0 + w][me.lane];
 #pragma unroll
         for (int w = 0; w < 4; ++w)
           if (w0 + w < me.workers) {
-            s_map[k & 1][w0 + w][me.lane].H = h;
-            h = after<FORM>(h, q[w].A, q[w].H);
+            s_map[P][w0 + w][me.lane].H = h;
+            h = after(h, q[w].A, q[w].H);
           }
       }
       V m = receive<FORM, true>(s_box, me, k, carry, lost);
@@ -778,18 +818,18 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
 #pragma unroll
         for (int w = 0; w < 4; ++w)
           if (w0 + w < me.workers) {
-            A[w] = s_map[k & 1][w0 + w][me.lane].A;
-            M[w] = s_back[k & 1][w0 + w][me.lane];
+            A[w] = s_map[P][w0 + w][me.lane].A;
+            M[w] = s_back[P][w0 + w][me.lane];
           }
 #pragma unroll
         for (int w = 3; w >= 0; --w)
           if (w0 + w < me.workers) {
-            s_back[k & 1][w0 + w][me.lane] = m;
-            m = after<FORM>(m, A[w], M[w]);
+            s_back[P][w0 + w][me.lane] = m;
+            m = after(m, A[w], M[w]);
           }
       }
-      arrive(kStatesIn + (k & 1), threads - 32);
-    }
+      arrive<kStatesIn + P>(threads - 32);
+    });
     if (grad_initial && len == 0 && me.rank == 0) store_state<CH>(grad_initial + row, carry, me.n);
   } else {
     const Gates<T, FORM> gates;
@@ -809,24 +849,26 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
       copies_commit();
     };
     int taken = 0, given = 0;          // stages
-    auto take = [&](int k) {
+    auto take = [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
       copies_wait_but_one();
       __syncwarp();
       V M;
       unsigned(*w)[kSteps][32] = ring.at(taken);
-      s_map[k & 1][me.warp][me.lane] =
+      s_map[P][me.warp][me.lane] =
           k >= whole ? piece_maps<T, FORM, true>(gates, w, graded, M, kSteps)
                      : piece_maps<T, FORM, false>(gates, w, graded, M, len - (last - k * me.stride));
-      s_back[k & 1][me.warp][me.lane] = M;
+      s_back[P][me.warp][me.lane] = M;
       __syncwarp();
-      arrive(kMapsIn + (k & 1), threads);
+      arrive<kMapsIn + P>(threads);
       taken = taken + 1 == kStages ? 0 : taken + 1;
     };
     long long o = ((long long)me.b * time + last) * channels + me.c;
-    auto give = [&](int k) {
-      join(kStatesIn + (k & 1), threads - 32);
-      const V h = s_map[k & 1][me.warp][me.lane].H;
-      V m = s_back[k & 1][me.warp][me.lane];
+    auto give = [&](auto parity, int k) {
+      constexpr int P = decltype(parity)::value;
+      join<kStatesIn + P>(threads - 32);
+      const V h = s_map[P][me.warp][me.lane].H;
+      V m = s_back[P][me.warp][me.lane];
       unsigned(*w)[kSteps][32] = ring.at(given);
       if (k >= whole) {
         piece_gradients<T, FORM, VEC != 0, true>(gates, Words{w, me.lane, graded}, h, m, grad_x + o, grad_gate + o, channels,
@@ -853,13 +895,13 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
     if (me.rounds > 0) {
       ask(0, ring.at(0));
       ask(1, ring.at(1));
-      take(0);
+      take(std::integral_constant<int, 0>(), 0);
       ask(2, ring.at(2));
     }
-    for (int k = 0; k < me.rounds; ++k) {
-      if (k + 1 < me.rounds) take(k + 1);
-      give(k);
-    }
+    each_round(me.rounds, [&](auto parity, int k) {
+      if (k + 1 < me.rounds) take(std::integral_constant<int, 1 - decltype(parity)::value>(), k + 1);
+      give(parity, k);
+    });
   }
   if (shape.log2_ranks > 0) {
     cluster_arrive();
@@ -897,14 +939,38 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
 // ---------------------------------------------------------------------------
 
 // CTAs that share a sequence (a cluster), as a logarithm: what costs the least in
-// rounds of blocks, with two more for a CTA's start, over the waves of CTAs that the SMs
-// take at a time.  The bits do not depend on it.
-int choose_ranks(long long sequences, int time) {
-  const long long slots = std::max(device_sm_count(), 1);
+// rounds of blocks, with two more for a CTA's start, over the waves of clusters that
+// are resident at a time.  (Of 8 CTAs fewer clusters fit than the SMs' number lets
+// expect: 16 of them took two waves.)  The bits do not depend on it.
+int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences, int time) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, unsigned>, int> cache;
+  int dev = 0;
+  cudaGetDevice(&dev);
   int best = 0;
   long long least = -1;
   for (int l = 0; (1 << l) <= kMaxCluster && (l == 0 || (kBlock << (l - 1)) < time); ++l) {
-    const long long waves = ((sequences << l) + slots - 1) / slots;
+    int clusters = 0;
+    {
+      std::lock_guard<std::mutex> lk(mu);
+      int& known = cache[{kernel, dev, l, cfg.blockDim.x}];
+      if (known == 0) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << l;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(1u << l);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&known, kernel, &cfg) != cudaSuccess || known <= 0) {
+          cudaGetLastError();
+          known = -1;
+        }
+      }
+      clusters = known;
+    }
+    if (clusters <= 0) continue;
+    const long long waves = (sequences + clusters - 1) / clusters;
     const long long rounds = ((long long)time + (kBlock << l) - 1) / (kBlock << l);
     const long long cost = waves * (rounds + 2);
     if (least < 0 || cost < least) {
@@ -916,9 +982,8 @@ int choose_ranks(long long sequences, int time) {
 }
 
 // A launch over channel tiles and sequences, a thread a word for single pieces.
-template <typename T, int OPERANDS, typename... KArgs, typename... Args>
-int launch_recurrence(const char* name, void (*short_kernel)(KArgs...), void (*kernel)(KArgs...), int batch,
-                      const Shape& shape, cudaStream_t s, Args... args) {
+template <typename T, int OPERANDS, typename K, typename ARGS>
+int launch_recurrence(const char* name, K* short_kernel, K* kernel, int batch, Shape shape, cudaStream_t s, ARGS with) {
   const int words = (shape.channels + Lane<T>::CH - 1) / Lane<T>::CH;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
@@ -931,46 +996,51 @@ int launch_recurrence(const char* name, void (*short_kernel)(KArgs...), void (*k
     cfg.gridDim = dim3((unsigned)((words + 127) / 128), (unsigned)batch);
     cfg.blockDim = dim3(128);
     launch_begin(name, s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, short_kernel, args...);
+    const cudaError_t e = with(cfg, short_kernel, shape);
     launch_end(s);
     return e == cudaSuccess ? DET_OK : cuda_fail(e, name);
   }
-  const int ranks = 1 << shape.log2_ranks, workers = std::min(kWorkers, (shape.time + kSteps - 1) / kSteps);
-  cfg.gridDim = dim3((unsigned)((words + 31) / 32) * ranks, (unsigned)batch);
+  const int workers = std::min(kWorkers, (shape.time + kSteps - 1) / kSteps);
+  const long long tiles = (words + 31) / 32;
   cfg.blockDim = dim3(32 * (workers + 2));
   const size_t round_bytes = (size_t)workers * OPERANDS * kSteps * 32 * 4;
-  cfg.dynamicSmemBytes = std::min<long long>(kStages, (shape.time + (long long)ranks * kBlock - 1) / (ranks * kBlock)) * round_bytes;
+  cfg.dynamicSmemBytes = std::min<long long>(kStages, (shape.time + kBlock - 1) / kBlock) * round_bytes;
   // allowed for the largest at once: a small ring may pass the default limit too, with the static arrays
   cudaError_t e = ensure_dyn_smem((const void*)kernel, (size_t)kStages * kBlock * OPERANDS * 32 * 4);
   if (e != cudaSuccess) return cuda_fail(e, name);
+  shape.log2_ranks = choose_ranks((const void*)kernel, cfg, tiles * batch, shape.time);
+  const int ranks = 1 << shape.log2_ranks;
+  cfg.gridDim = dim3((unsigned)tiles * ranks, (unsigned)batch);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)ranks;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   if (ranks > 1) cfg.numAttrs = 2;
   launch_begin(name, s);
-  e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  e = with(cfg, kernel, shape);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, name);
 }
 
 template <typename T, int FORM, int VEC>
-int forward(const View& x, const View& gate, Shape shape, int batch, const float* initial, void* out, float* final_out,
-            float* states, cudaStream_t s) {
-  shape.log2_ranks = choose_ranks((long long)batch * ((shape.channels + 32 * Lane<T>::CH - 1) / (32 * Lane<T>::CH)),
-                                  shape.time);
+int forward(const View& x, const View& gate, const Shape& shape, int batch, const float* initial, void* out,
+            float* final_out, float* states, cudaStream_t s) {
   return launch_recurrence<T, 2>("det_linear_recurrence", recurrence_short_kernel<T, FORM, VEC != 0>,
-                                                recurrence_kernel<T, FORM, VEC>, batch, shape, s, x, gate, shape, initial,
-                                                static_cast<T*>(out), final_out, states);
+                                 recurrence_kernel<T, FORM, VEC>, batch, shape, s,
+                                 [&](const cudaLaunchConfig_t& cfg, auto* kernel, const Shape& sh) {
+                                   return cudaLaunchKernelEx(&cfg, kernel, x, gate, sh, initial, static_cast<T*>(out),
+                                                             final_out, states);
+                                 });
 }
 template <typename T, int FORM, int VEC>
-int backward(const View& grad, const View& x, const View& gate, Shape shape, int batch, const float* states,
+int backward(const View& grad, const View& x, const View& gate, const Shape& shape, int batch, const float* states,
              const float* grad_final, void* grad_x, void* grad_gate, float* grad_initial, cudaStream_t s) {
-  shape.log2_ranks = choose_ranks((long long)batch * ((shape.channels + 32 * Lane<T>::CH - 1) / (32 * Lane<T>::CH)),
-                                  shape.time);
-  return launch_recurrence<T, 3>(
-      "det_linear_recurrence_backward", recurrence_grad_short_kernel<T, FORM, VEC != 0>,
-      recurrence_grad_kernel<T, FORM, VEC>, batch, shape, s, grad, x, gate, shape, states, grad_final,
-      static_cast<T*>(grad_x), static_cast<T*>(grad_gate), grad_initial);
+  return launch_recurrence<T, 3>("det_linear_recurrence_backward", recurrence_grad_short_kernel<T, FORM, VEC != 0>,
+                                 recurrence_grad_kernel<T, FORM, VEC>, batch, shape, s,
+                                 [&](const cudaLaunchConfig_t& cfg, auto* kernel, const Shape& sh) {
+                                   return cudaLaunchKernelEx(&cfg, kernel, grad, x, gate, sh, states, grad_final,
+                                                             static_cast<T*>(grad_x), static_cast<T*>(grad_gate),
+                                                             grad_initial);
+                                 });
 }
 
 // How rows are read: 2 where all start on 16 bytes and are whole vectors, 1 where all
