@@ -335,9 +335,12 @@ __device__ __forceinline__ void copies_wait_but_one() { asm volatile("cp.async.w
 __device__ __forceinline__ void copies_wait_but_two() { asm volatile("cp.async.wait_group 2;" ::: "memory"); }
 static_assert(kStages == 3, "so many groups are asked for after the one that is waited for");
 
-// Copies a warp's pieces of one operand into its part of shared memory, [kSteps][32]
+// Copies a warp's pieces of one operand into its part of shared memory, [kSteps][pitch]
 // words, 0 past the sequence and the channels, round after round.  VEC 2: rows of 16-byte
-// vectors; 1: of words; 0: 16-bit elements at any address, through registers.
+// vectors; 1: of words; 0: of 16-bit elements at any address: the words that hold them,
+// one more than the row's if it starts in the middle of one.  (Such a first word's lower half is
+// not the row's, but lies beside it in a word.)
+__host__ __device__ constexpr int pitch(int vec) { return vec == 0 ? 33 : 32; }
 template <typename T, int VEC>
 struct Reader {
   const T* p;            // the lane's first element of the next piece
@@ -350,18 +353,21 @@ struct Reader {
     p = static_cast<const T*>(v.p) + (me.b * v.sb + (first + (VEC == 2 ? me.lane >> 3 : 0)) * v.st + first_channel(me));
   }
   // the piece from step t0 on, with all its steps and channels if full; by: steps to the next round's
-  __device__ __forceinline__ void next(unsigned (*to)[32], const View& v, const Place<T>& me, bool full, int t0, int by,
-                                       int channels) {
+  __device__ __forceinline__ void next(unsigned (*to)[pitch(VEC)], const View& v, const Place<T>& me, bool full, int t0,
+                                       int by, int channels) {
     const long long step = kRows * v.st;
     if constexpr (VEC == 0) {
-      unsigned w[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        w[i] = 0;
-        if (me.n > 0 && t0 + i < me.len) w[i] = load_word<T, false>(p + i * step, me.n);
+        const uintptr_t q = reinterpret_cast<uintptr_t>(p + i * step);
+        const int odd = (int)(q >> 1 & 1);
+        copy_part(&to[i][me.lane], q & ~(uintptr_t)3, channels - (me.c - odd), t0 + i < me.len, v);
       }
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) to[i][me.lane] = w[i];
+      if (me.lane < kSteps) {           // the rows' last words, a lane a row
+        const uintptr_t q = reinterpret_cast<uintptr_t>(p + me.lane * step + (31 - me.lane) * 2);
+        const int odd = (int)(q >> 1 & 1);
+        copy_part(&to[me.lane][32], (q & ~(uintptr_t)3) + 4, channels - (me.c0 + 64 - odd), t0 + me.lane < me.len, v);
+      }
     } else {
       unsigned* dst = VEC == 2 ? &to[me.lane >> 3][(me.lane & 7) * 4] : &to[0][me.lane];
       const int row = VEC == 2 ? me.lane >> 3 : 0;
@@ -378,14 +384,60 @@ struct Reader {
     }
     p += by * v.st;
   }
+  // A word of which `left` elements are of the tensor.
+  static __device__ __forceinline__ void copy_part(unsigned* dst, uintptr_t src, int left, bool valid, const View& v) {
+    const int bytes = valid ? max(0, min(2, left)) * 2 : 0;
+    copy_async<1>(dst, bytes ? reinterpret_cast<const void*>(src) : reinterpret_cast<const void*>(
+                                 reinterpret_cast<uintptr_t>(v.p) & ~(uintptr_t)3), bytes);
+  }
 };
 
+// A lane's words of a piece, operand `which` of the stage at raw.
+template <int VEC> struct Words {
+  const unsigned (*raw)[kSteps][pitch(VEC)];
+  unsigned odd;          // VEC 0: bits 2 which and 2 which + 1: even and odd rows start in the middle of a word
+  int lane;
+  bool graded;           // there is an operand 2
+  __device__ __forceinline__ unsigned operator()(int which, int i) const {
+    if (which == 2 && !graded) return 0u;
+    const unsigned w = raw[which][i][lane];
+    if constexpr (VEC == 0) return __funnelshift_r(w, raw[which][i][lane + 1], (odd >> (2 * which + (i & 1)) & 1) * 16);
+    return w;
+  }
+  // pieces start at multiples of 8 steps, tiles at even channels: a row's place in its word is a matter of its number
+  static __device__ __forceinline__ unsigned odd_rows(const View& v, int b, int which) {
+    const unsigned first = (unsigned)((reinterpret_cast<uintptr_t>(v.p) >> 1) + b * v.sb) & 1u;
+    return (first | (first ^ ((unsigned)v.st & 1u)) << 1) << (2 * which);
+  }
+};
+
+// A row of a tile of the outputs.  VEC 0, 16 bits: at an odd element the lanes' words are
+// shifted by one element, and the first and the last element go by themselves.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(T* p, unsigned w, int n, bool valid) {
+  if constexpr (VEC != 0 || sizeof(T) == 4) {        // (-1: element by element)
+    if (valid && n > 0) store_word<T, (VEC > 0)>(p, w, n);
+  } else {
+    const unsigned before = __shfl_up_sync(0xffffffffu, w, 1);
+    const int after = __shfl_down_sync(0xffffffffu, n, 1), lane = threadIdx.x & 31;
+    if (!valid || n <= 0) return;
+    unsigned short* q = reinterpret_cast<unsigned short*>(p);
+    if (reinterpret_cast<uintptr_t>(p) % 4 == 0) {
+      store_word<T, true>(p, w, n);
+    } else {
+      if (lane == 0) q[0] = (unsigned short)w;
+      else *reinterpret_cast<unsigned*>(q - 1) = before >> 16 | w << 16;
+      if (n == 2 && (lane == 31 || after <= 0)) q[1] = (unsigned short)(w >> 16);
+    }
+  }
+}
+
 // A warp's part of the stages.
-struct Ring {
+template <int VEC> struct Ring {
   unsigned* first;
   int words;             // from one stage to the next
-  __device__ __forceinline__ unsigned (*at(int stage) const)[kSteps][32] {
-    return reinterpret_cast<unsigned(*)[kSteps][32]>(first + stage * words);
+  __device__ __forceinline__ unsigned (*at(int stage) const)[kSteps][pitch(VEC)] {
+    return reinterpret_cast<unsigned(*)[kSteps][pitch(VEC)]>(first + stage * words);
   }
 };
 
@@ -438,16 +490,15 @@ __device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int roun
 
 // A piece's decays and what its steps add, and its map.  A step past the end is
 // (1, 0).
-template <typename T, int FORM, bool FULL>
-__device__ __forceinline__ Map<LaneV<T>> piece_map(const Gates<T, FORM>& gates, const unsigned (*gate)[32],
-                                                   const unsigned (*x)[32], LaneV<T> (&a)[kSteps], LaneV<T> (&u)[kSteps],
-                                                   int steps) {
+template <typename T, int FORM, bool FULL, typename WORDS>
+__device__ __forceinline__ Map<LaneV<T>> piece_map(const Gates<T, FORM>& gates, const WORDS& words, LaneV<T> (&a)[kSteps],
+                                                   LaneV<T> (&u)[kSteps], int steps) {
   Map<LaneV<T>> map;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     LaneV<T> rest;
-    gates(gate[i][threadIdx.x & 31], a[i], rest);
-    u[i] = gates.input(rest, unpack<T>(x[i][threadIdx.x & 31]));
+    gates(words(0, i), a[i], rest);
+    u[i] = gates.input(rest, unpack<T>(words(1, i)));
     if (!FULL && i >= steps) {
       both(a[i], 1.0f);
       both(u[i], 0.0f);
@@ -539,9 +590,10 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
     const int whole = me.whole && len >= at + kSteps ? (len - at - kSteps) / me.stride + 1 : 0;
     // and this one has the sequence's last step
     const int end = len > at && (len - 1 - at) % me.stride < kSteps ? (len - 1 - at) / me.stride : -1;
-    const Ring ring{s_raw + me.warp * (2 * kSteps * 32), me.workers * (2 * kSteps * 32)};
+    const Ring<VEC> ring{s_raw + me.warp * (2 * kSteps * pitch(VEC)), me.workers * (2 * kSteps * pitch(VEC))};
+    const unsigned odd = VEC == 0 ? Words<VEC>::odd_rows(gate, me.b, 0) | Words<VEC>::odd_rows(x, me.b, 1) : 0u;
     Reader<T, VEC> read_gate(gate, me, at), read_x(x, me, at);
-    auto ask = [&](int k, unsigned (*to)[kSteps][32]) {       // for the piece of round k, if there is one; in the rounds' order
+    auto ask = [&](int k, unsigned (*to)[kSteps][pitch(VEC)]) {       // for the piece of round k, if there is one; in the rounds' order
       if (k < me.rounds) {
         read_gate.next(to[0], gate, me, k < whole, k * me.stride + at, me.stride, channels);
         read_x.next(to[1], x, me, k < whole, k * me.stride + at, me.stride, channels);
@@ -553,10 +605,11 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
       constexpr int P = decltype(parity)::value;
       copies_wait_but_two();
       __syncwarp();
-      unsigned(*w)[kSteps][32] = ring.at(taken);
+      unsigned(*w)[kSteps][pitch(VEC)] = ring.at(taken);
+      const Words<VEC> words{w, odd, me.lane, false};
       s_map[P][me.warp][me.lane] = k < whole
-                                           ? piece_map<T, FORM, true>(gates, w[0], w[1], a, u, kSteps)
-                                           : piece_map<T, FORM, false>(gates, w[0], w[1], a, u, len - at - k * me.stride);
+                                           ? piece_map<T, FORM, true>(gates, words, a, u, kSteps)
+                                           : piece_map<T, FORM, false>(gates, words, a, u, len - at - k * me.stride);
       __syncwarp();
       arrive<kMapsIn + P>(threads);
       ask(k + kStages, w);             // into the same stage
@@ -572,14 +625,14 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
 #pragma unroll
         for (int i = 0; i < kSteps; ++i, q += channels) {
           h = fma(a[i], h, u[i]);
-          store_word<T, VEC != 0>(q, pack<T>(h), CH);
+          store_row<T, VEC>(q, pack<T>(h), CH, true);
         }
       } else {
         const int t0 = k * me.stride + at;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i, q += channels) {
           h = fma(a[i], h, u[i]);
-          if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(q, t0 + i < len ? pack<T>(h) : 0u, me.n);
+          store_row<T, VEC>(q, t0 + i < len ? pack<T>(h) : 0u, me.n, t0 + i < time);
         }
       }
       o += (long long)me.stride * channels;
@@ -587,19 +640,19 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
       // initial state has been read everywhere by now, so it may lie in the same place
       if (k == end && final_out) store_state<CH>(final_out + row, h, me.n);
     };
-    constexpr std::integral_constant<int, 0> even;
-    constexpr std::integral_constant<int, 1> odd;
+    constexpr std::integral_constant<int, 0> first;
+    constexpr std::integral_constant<int, 1> second;
     V a0[kSteps], u0[kSteps], a1[kSteps], u1[kSteps];
     if (me.rounds > 0) {
       for (int k = 0; k < kStages; ++k) ask(k, ring.at(k));
-      take(even, 0, a0, u0);
+      take(first, 0, a0, u0);
     }
     for (int k = 0; k < me.rounds; k += 2) {
-      if (k + 1 < me.rounds) take(odd, k + 1, a1, u1);
-      give(even, k, a0, u0);
+      if (k + 1 < me.rounds) take(second, k + 1, a1, u1);
+      give(first, k, a0, u0);
       if (k + 1 == me.rounds) break;
-      if (k + 2 < me.rounds) take(even, k + 2, a0, u0);
-      give(odd, k + 1, a1, u1);
+      if (k + 2 < me.rounds) take(first, k + 2, a0, u0);
+      give(second, k + 1, a1, u1);
     }
     // past the sequence's last round
     for (long long t0 = (long long)me.rounds * me.stride + at; t0 < time; t0 += me.stride)
@@ -668,39 +721,28 @@ recurrence_short_kernel(View x, View gate, Shape shape, const float* initial, T*
 // gradient
 
 // A piece's forward map, and back M of m -> A m + M.
-template <typename T, int FORM, bool FULL>
-__device__ __forceinline__ Map<LaneV<T>> piece_maps(const Gates<T, FORM>& gates, const unsigned (*raw)[kSteps][32],
-                                                    bool graded, LaneV<T>& M, int steps) {
+template <typename T, int FORM, bool FULL, typename WORDS>
+__device__ __forceinline__ Map<LaneV<T>> piece_maps(const Gates<T, FORM>& gates, const WORDS& words, LaneV<T>& M, int steps) {
   using V = LaneV<T>;
-  const int lane = threadIdx.x & 31;
   Map<V> map;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     V a, rest;
-    gates(raw[0][i][lane], a, rest);
-    V u = gates.input(rest, unpack<T>(raw[1][i][lane]));
+    gates(words(0, i), a, rest);
+    V u = gates.input(rest, unpack<T>(words(1, i)));
     if (!FULL && i >= steps) {
       both(a, 1.0f);
       both(u, 0.0f);
     }
     map.H = i ? fma(a, map.H, u) : u;
     map.A = i ? mul(map.A, a) : a;
-    const V d = unpack<T>(graded ? raw[2][i][lane] : 0u);
+    const V d = unpack<T>(words(2, i));
     M = i ? fma(map.A, d, M) : mul(map.A, d);
   }
   return map;
 }
 
-// A lane's words of a piece: gate (0), x (1) and gradient (2), in shared memory or in
-// registers.
-struct Words {
-  const unsigned (*raw)[kSteps][32];
-  int lane;
-  bool graded;
-  __device__ __forceinline__ unsigned operator()(int which, int i) const {
-    return which < 2 || graded ? raw[which][i][lane] : 0u;
-  }
-};
+// A thread's words of a piece, held in registers.
 struct WordsHeld {
   const unsigned (&w)[3][kSteps];
   __device__ __forceinline__ unsigned operator()(int which, int i) const { return w[which][i]; }
@@ -708,7 +750,7 @@ struct WordsHeld {
 
 // The gradients of a piece's steps from the state h before it and what comes back
 // behind it, m; m is what it hands back.
-template <typename T, int FORM, bool VEC, bool FULL, typename WORDS>
+template <typename T, int FORM, int VEC, bool FULL, typename WORDS>
 __device__ __forceinline__ void piece_gradients(const Gates<T, FORM>& gates, const WORDS& words, LaneV<T> h,
                                                 LaneV<T>& m, T* ox, T* og, int channels, int n, int steps, int rows) {
   using V = LaneV<T>;
@@ -728,10 +770,8 @@ __device__ __forceinline__ void piece_gradients(const Gates<T, FORM>& gates, con
     const V l = add(unpack<T>(words(2, i)), m);
     const V dx = gates.input(rest[i], l);
     if (FULL || i < steps) m = mul(a[i], l);
-    if (FULL || i < rows) {
-      store_word<T, VEC>(ox, FULL || i < steps ? pack<T>(dx) : 0u, FULL ? Lane<T>::CH : n);
-      store_word<T, VEC>(og, FULL || i < steps ? pack<T>(mul(dx, factor[i])) : 0u, FULL ? Lane<T>::CH : n);
-    }
+    store_row<T, VEC>(ox, FULL || i < steps ? pack<T>(dx) : 0u, FULL ? Lane<T>::CH : n, FULL || i < rows);
+    store_row<T, VEC>(og, FULL || i < steps ? pack<T>(mul(dx, factor[i])) : 0u, FULL ? Lane<T>::CH : n, FULL || i < rows);
   }
 }
 
@@ -836,10 +876,13 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
     const int at = me.rank * kBlock + me.warp * kSteps, last = (me.rounds - 1) * me.stride + at;
     // from this round on the pieces are whole
     const int whole = me.whole && len >= at + kSteps ? me.rounds - 1 - (len - at - kSteps) / me.stride : me.rounds;
-    const Ring ring{s_raw + me.warp * (3 * kSteps * 32), me.workers * (3 * kSteps * 32)};
+    const Ring<VEC> ring{s_raw + me.warp * (3 * kSteps * pitch(VEC)), me.workers * (3 * kSteps * pitch(VEC))};
+    const unsigned odd = VEC == 0 ? Words<VEC>::odd_rows(gate, me.b, 0) | Words<VEC>::odd_rows(x, me.b, 1) |
+                                        Words<VEC>::odd_rows(grad, me.b, 2)
+                                  : 0u;
     const bool graded = grad.p != nullptr;
     Reader<T, VEC> read_gate(gate, me, last), read_x(x, me, last), read_grad(grad, me, last);
-    auto ask = [&](int k, unsigned (*to)[kSteps][32]) {
+    auto ask = [&](int k, unsigned (*to)[kSteps][pitch(VEC)]) {
       if (k < me.rounds) {
         const int t0 = last - k * me.stride;
         read_gate.next(to[0], gate, me, k >= whole, t0, -me.stride, channels);
@@ -854,10 +897,11 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
       copies_wait_but_one();
       __syncwarp();
       V M;
-      unsigned(*w)[kSteps][32] = ring.at(taken);
+      unsigned(*w)[kSteps][pitch(VEC)] = ring.at(taken);
+      const Words<VEC> words{w, odd, me.lane, graded};
       s_map[P][me.warp][me.lane] =
-          k >= whole ? piece_maps<T, FORM, true>(gates, w, graded, M, kSteps)
-                     : piece_maps<T, FORM, false>(gates, w, graded, M, len - (last - k * me.stride));
+          k >= whole ? piece_maps<T, FORM, true>(gates, words, M, kSteps)
+                     : piece_maps<T, FORM, false>(gates, words, M, len - (last - k * me.stride));
       s_back[P][me.warp][me.lane] = M;
       __syncwarp();
       arrive<kMapsIn + P>(threads);
@@ -869,14 +913,14 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
       join<kStatesIn + P>(threads - 32);
       const V h = s_map[P][me.warp][me.lane].H;
       V m = s_back[P][me.warp][me.lane];
-      unsigned(*w)[kSteps][32] = ring.at(given);
+      unsigned(*w)[kSteps][pitch(VEC)] = ring.at(given);
       if (k >= whole) {
-        piece_gradients<T, FORM, VEC != 0, true>(gates, Words{w, me.lane, graded}, h, m, grad_x + o, grad_gate + o, channels,
+        piece_gradients<T, FORM, VEC, true>(gates, Words<VEC>{w, odd, me.lane, graded}, h, m, grad_x + o, grad_gate + o, channels,
                                                  CH, kSteps, kSteps);
       } else {
         const int t0 = last - k * me.stride;
-        piece_gradients<T, FORM, VEC != 0, false>(gates, Words{w, me.lane, graded}, h, m, grad_x + o, grad_gate + o,
-                                                  channels, me.n, len - t0, me.n > 0 ? time - t0 : 0);
+        piece_gradients<T, FORM, VEC, false>(gates, Words<VEC>{w, odd, me.lane, graded}, h, m, grad_x + o, grad_gate + o,
+                                                  channels, me.n, len - t0, time - t0);
       }
       o -= (long long)me.stride * channels;
       if (at == 0 && k + 1 == me.rounds && grad_initial) store_state<CH>(grad_initial + row, m, me.n);
@@ -931,8 +975,8 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
   for (int i = 0; i < STEPS; ++i) w[2][i] = 0;
   if (grad.p) load_words<T, VEC>(w[2], grad, me);
   const long long o = (long long)me.b * shape.time * shape.channels + me.c;
-  piece_gradients<T, FORM, VEC, false>(gates, WordsHeld{w}, h, m, grad_x + o, grad_gate + o, shape.channels, me.n, me.len,
-                                       shape.time);
+  piece_gradients<T, FORM, VEC ? 1 : -1, false>(gates, WordsHeld{w}, h, m, grad_x + o, grad_gate + o, shape.channels, me.n,
+                                                me.len, shape.time);
   if (grad_initial) store_state<CH>(grad_initial + row, m, me.n);
 }
 
@@ -983,7 +1027,8 @@ int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences
 
 // A launch over channel tiles and sequences, a thread a word for single pieces.
 template <typename T, int OPERANDS, typename K, typename ARGS>
-int launch_recurrence(const char* name, K* short_kernel, K* kernel, int batch, Shape shape, cudaStream_t s, ARGS with) {
+int launch_recurrence(const char* name, K* short_kernel, K* kernel, int row_words, int batch, Shape shape, cudaStream_t s,
+                      ARGS with) {
   const int words = (shape.channels + Lane<T>::CH - 1) / Lane<T>::CH;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
@@ -1003,10 +1048,10 @@ int launch_recurrence(const char* name, K* short_kernel, K* kernel, int batch, S
   const int workers = std::min(kWorkers, (shape.time + kSteps - 1) / kSteps);
   const long long tiles = (words + 31) / 32;
   cfg.blockDim = dim3(32 * (workers + 2));
-  const size_t round_bytes = (size_t)workers * OPERANDS * kSteps * 32 * 4;
+  const size_t round_bytes = (size_t)workers * OPERANDS * kSteps * row_words * 4;
   cfg.dynamicSmemBytes = std::min<long long>(kStages, (shape.time + kBlock - 1) / kBlock) * round_bytes;
   // allowed for the largest at once: a small ring may pass the default limit too, with the static arrays
-  cudaError_t e = ensure_dyn_smem((const void*)kernel, (size_t)kStages * kBlock * OPERANDS * 32 * 4);
+  cudaError_t e = ensure_dyn_smem((const void*)kernel, (size_t)kStages * kBlock * OPERANDS * row_words * 4);
   if (e != cudaSuccess) return cuda_fail(e, name);
   shape.log2_ranks = choose_ranks((const void*)kernel, cfg, tiles * batch, shape.time);
   const int ranks = 1 << shape.log2_ranks;
@@ -1025,7 +1070,7 @@ template <typename T, int FORM, int VEC>
 int forward(const View& x, const View& gate, const Shape& shape, int batch, const float* initial, void* out,
             float* final_out, float* states, cudaStream_t s) {
   return launch_recurrence<T, 2>("det_linear_recurrence", recurrence_short_kernel<T, FORM, VEC != 0>,
-                                 recurrence_kernel<T, FORM, VEC>, batch, shape, s,
+                                 recurrence_kernel<T, FORM, VEC>, pitch(VEC), batch, shape, s,
                                  [&](const cudaLaunchConfig_t& cfg, auto* kernel, const Shape& sh) {
                                    return cudaLaunchKernelEx(&cfg, kernel, x, gate, sh, initial, static_cast<T*>(out),
                                                              final_out, states);
@@ -1035,7 +1080,7 @@ template <typename T, int FORM, int VEC>
 int backward(const View& grad, const View& x, const View& gate, const Shape& shape, int batch, const float* states,
              const float* grad_final, void* grad_x, void* grad_gate, float* grad_initial, cudaStream_t s) {
   return launch_recurrence<T, 3>("det_linear_recurrence_backward", recurrence_grad_short_kernel<T, FORM, VEC != 0>,
-                                 recurrence_grad_kernel<T, FORM, VEC>, batch, shape, s,
+                                 recurrence_grad_kernel<T, FORM, VEC>, pitch(VEC), batch, shape, s,
                                  [&](const cudaLaunchConfig_t& cfg, auto* kernel, const Shape& sh) {
                                    return cudaLaunchKernelEx(&cfg, kernel, grad, x, gate, sh, states, grad_final,
                                                              static_cast<T*>(grad_x), static_cast<T*>(grad_gate),
