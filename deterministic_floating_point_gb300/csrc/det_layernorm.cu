@@ -19,22 +19,31 @@
 namespace det {
 namespace {
 
+using Two = unsigned long long;    // two adjacent columns, for packed 32-bit instructions
+
 // The lanes' sums of a group, in every thread: a tree over lanes, then over
 // warps through `slot` (one float a warp).  A group of one warp needs no barrier.
 __device__ __forceinline__ void put_warp(float* slot, float v, int warp, int lane) {
   if (lane == 0) slot[warp] = v;
 }
 __device__ __forceinline__ float over_warps(const float* slot, int first_warp, int warps, int lane) {
+  if (warps == 8) {                    // the same tree, without shuffles
+    const float4 a = *reinterpret_cast<const float4*>(slot + first_warp), b = *reinterpret_cast<const float4*>(slot + first_warp + 4);
+    return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  }
   float v = slot[first_warp + (lane & (warps - 1))];
   for (int s = 1; s < warps; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
-template <int N>
-__device__ __forceinline__ float tree(const float (&v)[N]) {
-  float t[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) t[i] = v[i];
-  return thread_pt(t);
+__device__ __forceinline__ float lanes(Two v) {
+  const float2 f = unpack_f32x2(v);
+  return __fadd_rn(f.x, f.y);
+}
+
+// 1 / sqrt(v) from the hardware's approximation by a step of Newton's method.
+__device__ __forceinline__ float inverse_root(float v) {
+  const float r = rsqrtf(v), e = fmaf(-0.5f * v * r, r, 0.5f);
+  return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0, infinite and NaN as they are
 }
 
 // A group's place: `threads` (a power of two) of them take a row.
@@ -52,13 +61,93 @@ struct Group {
   }
 };
 
+// ---------------------------------------------------------------------------
+// Rows.  A thread's columns are eights, `threads` eights apart.  Where every row
+// starts on 16 bytes (VEC) it reads and writes them as vectors.  Else the 256
+// columns of a warp's eights go element by element, lane after lane, and turn into
+// eights in the warp's kilobyte of shared memory; eight single elements a thread at
+// one address after the other took 33 us for 4,099 x 1,021 in 32 bits.
+template <typename T> struct Bits { using U = unsigned short; };
+template <> struct Bits<float> { using U = unsigned; };
+
+template <typename T, bool VEC, int K> struct Row {
+  Eight<T> e[K];
+};
+template <typename T, int K> struct Row<T, false, K> {
+  typename Bits<T>::U w[K][8];
+};
+
 template <typename T, bool VEC, int K>
-__device__ __forceinline__ void load_row(Eight<T> (&e)[K], const T* row, const Group& g, int cols, bool valid) {
+__device__ __forceinline__ void load_row(Row<T, VEC, K>& r, const T* row, const Group& g, int cols, bool valid) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (g.me + k * g.threads) * 8;
-    e[k] = load_eight<VEC>(row + c, valid ? max(0, min(8, cols - c)) : 0);
+    if constexpr (VEC) {
+      const int c = (g.me + k * g.threads) * 8;
+      r.e[k] = load_eight<true>(row + c, valid ? max(0, min(8, cols - c)) : 0);
+    } else {
+      const int c = ((g.me & ~31) + k * g.threads) * 8 + g.lane;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        r.w[k][j] = valid && c + 32 * j < cols ? reinterpret_cast<const typename Bits<T>::U*>(row)[c + 32 * j] : 0;
+    }
   }
+}
+template <typename T, bool VEC, int K>
+__device__ __forceinline__ void to_eights(Eight<T> (&e)[K], const Row<T, VEC, K>& r, void* warp_kb, int lane) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if constexpr (VEC) {
+      e[k] = r.e[k];
+    } else {
+      typename Bits<T>::U* s = static_cast<typename Bits<T>::U*>(warp_kb);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[32 * j + lane] = r.w[k][j];
+      __syncwarp();
+      e[k] = load_eight<true>(static_cast<const T*>(warp_kb) + 8 * lane, 8);
+      __syncwarp();
+    }
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_columns(T* row, const float (&v)[8], const Group& g, int k, int cols, bool valid,
+                                              void* warp_kb) {
+  if constexpr (VEC) {
+    const int c = (g.me + k * g.threads) * 8;
+    if (valid) store_eight<true>(row + c, v, max(0, min(8, cols - c)));
+  } else {
+    using U = typename Bits<T>::U;
+    store_eight<true>(static_cast<T*>(warp_kb) + 8 * g.lane, v, 8);
+    __syncwarp();
+    const int c = ((g.me & ~31) + k * g.threads) * 8 + g.lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (valid && c + 32 * j < cols) reinterpret_cast<U*>(row)[c + 32 * j] = static_cast<const U*>(warp_kb)[32 * j + g.lane];
+    __syncwarp();
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Eight<T>& e, Two (&v)[4]) {
+  float f[8];
+  unpack_eight(e, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+}
+// The first n of eight values, the others 0.
+__device__ __forceinline__ void keep_first(Two (&v)[4], int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f32x2(v[i]);
+    v[i] = pack_f32x2(2 * i < n ? f.x : 0.0f, 2 * i + 1 < n ? f.y : 0.0f);
+  }
+}
+__device__ __forceinline__ Two twice(float x) { return pack_f32x2(x, x); }
+// Columns c .. c + 7 of a weight or bias, `other` without one.
+__device__ __forceinline__ void load_param(Two (&v)[4], const void* p, int c, int cols, int dtype, float other) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack_f32x2(p && c + 2 * i < cols ? load_as_f32(p, c + 2 * i, dtype) : other,
+                      p && c + 2 * i + 1 < cols ? load_as_f32(p, c + 2 * i + 1, dtype) : other);
 }
 
 constexpr int kThreads = 256;       // a CTA's, unless a row takes more
@@ -67,181 +156,207 @@ template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 4 : 3)
 layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void* weight, const void* bias,
                   int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int log2_threads) {
-  __shared__ float s_sum[32], s_sq[32];
+  __shared__ __align__(16) float s_sum[32], s_sq[32];
+  __shared__ __align__(16) char s_turn[VEC ? 1 : MOST / 32][VEC ? 16 : 1024];
   dep_wait();
   dep_launch();
   const Group g(log2_threads);
-  float w[K][8], b[K][8];
+  char* turn = s_turn[VEC ? 0 : g.warp];
+  Two w[K][4], b[K][4];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = (g.me + k * g.threads) * 8 + i;
-      w[k][i] = weight && c < cols ? load_as_f32(weight, c, param_dtype) : 1.0f;
-      b[k][i] = bias && c < cols ? load_as_f32(bias, c, param_dtype) : 0.0f;
-    }
+  for (int k = 0; k < K; ++k) {
+    load_param(w[k], weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
+    load_param(b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
+  }
+  const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;   // all of the thread's columns are there
   const long long step = (long long)gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
   long long first = (long long)blockIdx.x * g.count;       // of the CTA's rows: every thread makes as many rounds
   long long r = first + g.index;
-  Eight<T> cur[K];
-  load_row<T, VEC>(cur, x + r * x_stride, g, cols, r < rows);
+  Row<T, VEC, K> next;
+  load_row(next, x + r * x_stride, g, cols, r < rows);
   for (; first < rows; first += step, r += step) {
-    Eight<T> next[K];
-    load_row<T, VEC>(next, x + (r + step) * x_stride, g, cols, r + step < rows);
-    float v[K][8], part[K];
+    Eight<T> e[K];
+    to_eights(e, next, turn, g.lane);
+    load_row(next, x + (r + step) * x_stride, g, cols, r + step < rows);
+    Two v[K][4], t[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack_eight(cur[k], v[k]);
-      part[k] = tree(v[k]);
+      pairs_of(e[k], v[k]);
+      t[k] = add_f32x2(add_f32x2(v[k][0], v[k][1]), add_f32x2(v[k][2], v[k][3]));
     }
-    float sum = warp_pt(tree(part));
+    if (K == 2) t[0] = add_f32x2(t[0], t[K - 1]);
+    float sum = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
       put_warp(s_sum, sum, g.warp, g.lane);
       __syncthreads();
       sum = over_warps(s_sum, g.first_warp, g.warps, g.lane);
     }
     const float mean = sum * of;
+    const Two mean2 = twice(mean);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int n = cols - (g.me + k * g.threads) * 8;
-      float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[k][i] -= mean;
-        q[i] = i < n ? v[k][i] * v[k][i] : 0.0f;
-      }
-      part[k] = tree(q);
+      for (int i = 0; i < 4; ++i) v[k][i] = sub_f32x2(v[k][i], mean2);
+      if (!whole) keep_first(v[k], cols - (g.me + k * g.threads) * 8);
+      t[k] = mul_f32x2(v[k][0], v[k][0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) t[k] = fma_f32x2(v[k][i], v[k][i], t[k]);
     }
-    float sq = warp_pt(tree(part));
+    if (K == 2) t[0] = add_f32x2(t[0], t[K - 1]);
+    float sq = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
       put_warp(s_sq, sq, g.warp, g.lane);
       __syncthreads();
       sq = over_warps(s_sq, g.first_warp, g.warps, g.lane);
     }
-    const float rstd = 1.0f / sqrtf(fmaf(sq, of, eps));
-    if (r < rows) {
+    const float rstd = inverse_root(fmaf(sq, of, eps));
+    const Two rstd2 = twice(rstd);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (g.me + k * g.threads) * 8;
-        float y[8];
+    for (int k = 0; k < K; ++k) {
+      float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
-        store_eight<VEC>(out + r * cols + c, y, max(0, min(8, cols - c)));
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_f32x2(fma_f32x2(mul_f32x2(v[k][i], rstd2), w[k][i], b[k][i]));
+        y[2 * i] = f.x;
+        y[2 * i + 1] = f.y;
       }
-      if (g.me == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
-      }
+      store_columns<VEC>(out + r * cols, y, g, k, cols, r < rows, turn);
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) cur[k] = next[k];
+    if (g.me == 0 && r < rows) {
+      if (mean_out) mean_out[r] = mean;
+      if (rstd_out) rstd_out[r] = rstd;
+    }
   }
 }
 
 // part: [gridDim.x][2][cols] sums of the weight's and the bias' gradients, or NULL.
 template <typename T, int K, bool VEC, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == 256 ? 2 : 1)
+__global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
 layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, int rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
                        float* part, int log2_threads) {
-  __shared__ float s_one[2][32], s_two[2][32];
-  extern __shared__ float s_acc[];
+  __shared__ float2 s_sums[2][32];
+  __shared__ __align__(16) char s_turn[VEC ? 1 : MOST / 32][VEC ? 16 : 1024];
+  extern __shared__ __align__(16) char s_dynamic[];
+  float* s_acc = reinterpret_cast<float*>(s_dynamic);
+  // the weight: registers hold two gradients for each column; halves of eights, so that a warp reads 512 bytes in a row
+  ulonglong2* s_w = reinterpret_cast<ulonglong2*>(s_dynamic);
   dep_wait();
   dep_launch();
   const Group g(log2_threads);
-  float w[K][8], aw[K][8], ab[K][8];
+  char* turn = s_turn[VEC ? 0 : g.warp];
+  Two aw[K][4], ab[K][4];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = (g.me + k * g.threads) * 8 + i;
-      w[k][i] = weight && c < cols ? load_as_f32(weight, c, param_dtype) : 1.0f;
-      aw[k][i] = ab[k][i] = 0.0f;
+  for (int k = 0; k < K; ++k) {
+    if (g.index == 0) {
+      Two w[4];
+      load_param(w, weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
+      s_w[(2 * k) * g.threads + g.me] = make_ulonglong2(w[0], w[1]);
+      s_w[(2 * k + 1) * g.threads + g.me] = make_ulonglong2(w[2], w[3]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = 0;
+  }
+  __syncthreads();
+  auto weights = [&](int k, Two (&w)[4]) {
+    const ulonglong2 a = s_w[(2 * k) * g.threads + g.me], b = s_w[(2 * k + 1) * g.threads + g.me];
+    w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+  };
+  const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
   const long long step = (long long)gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
   long long first = (long long)blockIdx.x * g.count;
   long long r = first + g.index;
-  Eight<T> cx[K], cg[K];
-  load_row<T, VEC>(cx, x + r * x_stride, g, cols, r < rows);
-  load_row<T, VEC>(cg, grad + r * grad_stride, g, cols, r < rows);
-  float cm = r < rows ? means[r] : 0.0f, cr = r < rows ? rstds[r] : 0.0f;
+  Row<T, VEC, K> nx, ng;
+  load_row(nx, x + r * x_stride, g, cols, r < rows);
+  load_row(ng, grad + r * grad_stride, g, cols, r < rows);
+  float nm = r < rows ? means[r] : 0.0f, nr = r < rows ? rstds[r] : 0.0f;
   int parity = 0;
   for (; first < rows; first += step, r += step, parity ^= 1) {
-    Eight<T> nx[K], ng[K];
+    Eight<T> cx[K], cg[K];
+    to_eights(cx, nx, turn, g.lane);
+    to_eights(cg, ng, turn, g.lane);
+    const Two mean2 = twice(nm), rstd2 = twice(nr);
     const bool more = r + step < rows;
-    load_row<T, VEC>(nx, x + (r + step) * x_stride, g, cols, more);
-    load_row<T, VEC>(ng, grad + (r + step) * grad_stride, g, cols, more);
-    const float nm = more ? means[r + step] : 0.0f, nr = more ? rstds[r + step] : 0.0f;
-    float p1[K], p2[K];
+    load_row(nx, x + (r + step) * x_stride, g, cols, more);
+    load_row(ng, grad + (r + step) * grad_stride, g, cols, more);
+    nm = more ? means[r + step] : 0.0f;
+    nr = more ? rstds[r + step] : 0.0f;
+    Two t1[K], t2[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float xh[8], d[8], q1[8], q2[8];
-      unpack_eight(cx[k], xh);
-      unpack_eight(cg[k], d);
-      const int n = cols - (g.me + k * g.threads) * 8;
+      Two xh[4], d[4], w[4];
+      weights(k, w);
+      pairs_of(cx[k], xh);
+      pairs_of(cg[k], d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xh[i] = i < n ? (xh[i] - cm) * cr : 0.0f;
-        aw[k][i] = fmaf(d[i], xh[i], aw[k][i]);
-        ab[k][i] += d[i];
-        q1[i] = d[i] * w[k][i];
-        q2[i] = q1[i] * xh[i];
+      for (int i = 0; i < 4; ++i) xh[i] = mul_f32x2(sub_f32x2(xh[i], mean2), rstd2);
+      if (!whole) keep_first(xh, cols - (g.me + k * g.threads) * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        aw[k][i] = fma_f32x2(d[i], xh[i], aw[k][i]);
+        ab[k][i] = add_f32x2(ab[k][i], d[i]);
+        d[i] = mul_f32x2(d[i], w[i]);
+        t1[k] = i ? add_f32x2(t1[k], d[i]) : d[i];
+        t2[k] = i ? fma_f32x2(d[i], xh[i], t2[k]) : mul_f32x2(d[i], xh[i]);
       }
-      p1[k] = tree(q1);
-      p2[k] = tree(q2);
     }
-    float one = warp_pt(tree(p1)), two = warp_pt(tree(p2));
+    if (K == 2) {
+      t1[0] = add_f32x2(t1[0], t1[K - 1]);
+      t2[0] = add_f32x2(t2[0], t2[K - 1]);
+    }
+    float one = warp_pt(lanes(t1[0])), two = warp_pt(lanes(t2[0]));
     if (g.warps > 1) {
-      put_warp(s_one[parity], one, g.warp, g.lane);
-      put_warp(s_two[parity], two, g.warp, g.lane);
+      if (g.lane == 0) s_sums[parity][g.warp] = make_float2(one, two);
       __syncthreads();
-      one = over_warps(s_one[parity], g.first_warp, g.warps, g.lane);
-      two = over_warps(s_two[parity], g.first_warp, g.warps, g.lane);
+      const float2 q = s_sums[parity][g.first_warp + (g.lane & (g.warps - 1))];
+      one = q.x;
+      two = q.y;
+      for (int s = 1; s < g.warps; s <<= 1) {
+        one += __shfl_xor_sync(0xffffffffu, one, s);
+        two += __shfl_xor_sync(0xffffffffu, two, s);
+      }
     }
-    if (grad_x && r < rows) {
-      one *= of;
-      two *= of;
+    if (grad_x) {
+      const Two minus_one = twice(-one * of), minus_two = twice(-two * of);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = (g.me + k * g.threads) * 8;
-        float xh[8], d[8];
-        unpack_eight(cx[k], xh);
-        unpack_eight(cg[k], d);
+        Two xh[4], d[4], w[4];
+        weights(k, w);
+        pairs_of(cx[k], xh);
+        pairs_of(cg[k], d);
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = cr * (fmaf(d[i], w[k][i], -one) - (xh[i] - cm) * cr * two);
-        store_eight<VEC>(grad_x + r * cols + c, d, max(0, min(8, cols - c)));
+        for (int i = 0; i < 4; ++i) {
+          xh[i] = mul_f32x2(sub_f32x2(xh[i], mean2), rstd2);
+          d[i] = fma_f32x2(xh[i], minus_two, fma_f32x2(d[i], w[i], minus_one));
+          const float2 f = unpack_f32x2(mul_f32x2(d[i], rstd2));
+          y[2 * i] = f.x;
+          y[2 * i + 1] = f.y;
+        }
+        store_columns<VEC>(grad_x + r * cols, y, g, k, cols, r < rows, turn);
       }
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) cx[k] = nx[k], cg[k] = ng[k];
-    cm = nm;
-    cr = nr;
   }
   if (!part) return;
+  __syncthreads();                     // the weight has been read
   float* mine = part + (long long)blockIdx.x * 2 * cols;
-  if (g.count == 1) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (g.me + k * g.threads) * 8 + i;
-        if (c < cols) mine[c] = aw[k][i], mine[cols + c] = ab[k][i];
-      }
-    return;
-  }
   // several rows at a time: the groups' sums in the groups' order
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+    if (g.count > 1 && which) __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (g.me + k * g.threads) * 8 + i;
-        if (c < cols) s_acc[g.index * cols + c] = which ? ab[k][i] : aw[k][i];
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_f32x2(which ? ab[k][i] : aw[k][i]);
+        const int c = (g.me + k * g.threads) * 8 + 2 * i;
+        float* to = g.count > 1 ? s_acc + g.index * cols : mine + which * cols;
+        if (c < cols) to[c] = f.x;
+        if (c + 1 < cols) to[c + 1] = f.y;
       }
+    if (g.count == 1) continue;
     __syncthreads();
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
       float t = s_acc[c];
@@ -274,18 +389,22 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
   if (lane == 0 && of < cols) store_from_f32(to, of, total, param_dtype);
 }
 
-// Threads that take a row, as a logarithm: two eights each, one of up to 256 columns.
-int row_threads(int64_t cols) {
+// Eights of columns a thread takes, and the threads that take a row, as a logarithm.
+// In 16 bits two eights keep a row's sums over lanes and warps short; in 32 one, because
+// two would need more registers than leave two CTAs on an SM.
+int eights(int64_t cols, int dtype) { return cols > (dtype == DET_F32 ? 8192 : 256) ? 2 : 1; }
+int row_threads(int64_t cols, int dtype) {
   int l = 5;
-  while ((16LL << l) < cols) ++l;
+  while ((8LL * eights(cols, dtype) << l) < cols) ++l;
   return l;
 }
 // CTAs of the gradient, each of which leaves a partial sum: as many as run at once on
 // the 152 SMs, by a constant, because the sums' order hangs on it.
-int grad_parts(int64_t rows, int64_t cols) {
-  const int l = row_threads(cols);
+int grad_parts(int64_t rows, int64_t cols, int dtype) {
+  const int l = row_threads(cols, dtype);
   const int64_t at_a_time = std::max<int64_t>(1, kThreads >> l);
-  return (int)std::min<int64_t>((rows + at_a_time - 1) / at_a_time, l <= 8 ? 304 : 152);
+  const int at_once = 152 * (l > 8 ? 1 : eights(cols, dtype) == 1 ? 3 : 2);
+  return (int)std::min<int64_t>((rows + at_a_time - 1) / at_a_time, at_once);
 }
 
 template <typename T>
@@ -295,8 +414,8 @@ bool vectors(const void* p, int64_t stride, int64_t cols) {
 
 template <typename T, int K, bool VEC, int MOST>
 int forward(const void* x, int rows, int cols, int64_t x_stride, const void* weight, const void* bias, int param_dtype,
-            float eps, void* out, float* mean_out, float* rstd_out, cudaStream_t s) {
-  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+            float eps, void* out, float* mean_out, float* rstd_out, int dtype, cudaStream_t s) {
+  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
   auto* k = layer_norm_kernel<T, K, VEC, MOST>;
   const int per_sm = kernel_occupancy((const void*)k, threads, 0);
   if (per_sm <= 0) return cuda_fail(cudaErrorUnknown, "det_layer_norm");
@@ -313,12 +432,16 @@ int forward(const void* x, int rows, int cols, int64_t x_stride, const void* wei
 template <typename T, int K, bool VEC, int MOST>
 int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int rows, int cols,
              const float* mean, const float* rstd, const void* weight, int param_dtype, void* grad_x, float* part,
-             cudaStream_t s) {
-  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+             int dtype, cudaStream_t s) {
+  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
   auto* k = layer_norm_grad_kernel<T, K, VEC, MOST>;
-  const size_t smem = part && at_a_time > 1 ? (size_t)at_a_time * cols * sizeof(float) : 0;
+  // the weight, and in its place later the groups' sums
+  const size_t smem = std::max((size_t)K * 8 << l, (size_t)(at_a_time > 1 ? at_a_time * cols : 0)) * sizeof(float);
+  // (at least 40 KB: with the static arrays less may pass the default limit too)
+  const cudaError_t se = ensure_dyn_smem((const void*)k, std::max(smem, (size_t)40 * 1024));
+  if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm_backward");
   launch_begin("det_layer_norm_backward", s);
-  const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols)), dim3(threads), smem, s,
+  const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols, dtype)), dim3(threads), smem, s,
                                    static_cast<const T*>(grad), (long long)grad_stride, static_cast<const T*>(x),
                                    (long long)x_stride, rows, cols, mean, rstd, weight, param_dtype,
                                    static_cast<T*>(grad_x), part, l);
@@ -339,32 +462,38 @@ bool misaligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p
 
 using namespace det;
 
-// One eight a thread up to 256 columns, two above; CTAs of more than 256 threads where a
-// row takes them.
-#define DET_NORM_PICK_T(fn, T, ...)                                                                      \
+// The kernels for eights() and row_threads().
+#define DET_NORM_PICK_16(fn, T, ...)                                                                     \
   do {                                                                                                   \
     if (cols <= 256) return vec ? fn<T, 1, true, 256>(__VA_ARGS__) : fn<T, 1, false, 256>(__VA_ARGS__);  \
     if (cols <= 4096) return vec ? fn<T, 2, true, 256>(__VA_ARGS__) : fn<T, 2, false, 256>(__VA_ARGS__); \
     if (cols <= 8192) return vec ? fn<T, 2, true, 512>(__VA_ARGS__) : fn<T, 2, false, 512>(__VA_ARGS__); \
     return vec ? fn<T, 2, true, 1024>(__VA_ARGS__) : fn<T, 2, false, 1024>(__VA_ARGS__);                 \
   } while (0)
+#define DET_NORM_PICK_32(fn, ...)                                                                                \
+  do {                                                                                                           \
+    if (cols <= 2048) return vec ? fn<float, 1, true, 256>(__VA_ARGS__) : fn<float, 1, false, 256>(__VA_ARGS__); \
+    if (cols <= 4096) return vec ? fn<float, 1, true, 512>(__VA_ARGS__) : fn<float, 1, false, 512>(__VA_ARGS__); \
+    if (cols <= 8192) return vec ? fn<float, 1, true, 1024>(__VA_ARGS__) : fn<float, 1, false, 1024>(__VA_ARGS__); \
+    return vec ? fn<float, 2, true, 1024>(__VA_ARGS__) : fn<float, 2, false, 1024>(__VA_ARGS__);                 \
+  } while (0)
 #define DET_NORM_PICK(fn, ...)                                                 \
   do {                                                                         \
-    if (dtype == DET_F32) DET_NORM_PICK_T(fn, float, __VA_ARGS__);             \
-    if (dtype == DET_BF16) DET_NORM_PICK_T(fn, __nv_bfloat16, __VA_ARGS__);    \
-    DET_NORM_PICK_T(fn, __half, __VA_ARGS__);                                  \
+    if (dtype == DET_F32) DET_NORM_PICK_32(fn, __VA_ARGS__);                   \
+    if (dtype == DET_BF16) DET_NORM_PICK_16(fn, __nv_bfloat16, __VA_ARGS__);   \
+    DET_NORM_PICK_16(fn, __half, __VA_ARGS__);                                 \
   } while (0)
 
 static int norm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
                         const void* bias, int param_dtype, float eps, void* out, float* mean_out, float* rstd_out,
                         bool vec, cudaStream_t s) {
-  DET_NORM_PICK(forward, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, s);
+  DET_NORM_PICK(forward, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, dtype, s);
 }
 static int norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype, int64_t rows,
                          int64_t cols, const float* mean, const float* rstd, const void* weight, int param_dtype,
                          void* grad_x, float* part, bool vec, cudaStream_t s) {
   DET_NORM_PICK(backward, grad, grad_stride, x, x_stride, (int)rows, (int)cols, mean, rstd, weight, param_dtype, grad_x,
-                part, s);
+                part, dtype, s);
 }
 
 extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride,
@@ -385,7 +514,8 @@ extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t co
 
 extern "C" size_t det_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (check_rows(DET_F32, DET_F32, rows, cols) != DET_OK || rows == 0) return 256;
-  return 256 + align_up((size_t)grad_parts(rows, cols) * 2 * (size_t)cols * sizeof(float), 256);
+  const int parts = std::max(grad_parts(rows, cols, DET_F32), grad_parts(rows, cols, DET_BF16));
+  return 256 + align_up((size_t)parts * 2 * (size_t)cols * sizeof(float), 256);
 }
 
 extern "C" int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype,
@@ -417,7 +547,7 @@ extern "C" int det_layer_norm_backward(const void* grad, int64_t grad_stride, co
   if (!params) return DET_OK;
   launch_begin("det_layer_norm_join", s);
   const cudaError_t e = launch_dep(layer_norm_join_kernel, dim3((unsigned)((cols + 31) / 32), 2), dim3(1024), 0, s,
-                                   (const float*)part, rows > 0 ? grad_parts(rows, cols) : 0, (int)cols, grad_weight,
+                                   (const float*)part, rows > 0 ? grad_parts(rows, cols, dtype) : 0, (int)cols, grad_weight,
                                    grad_bias, param_dtype);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm_join");
