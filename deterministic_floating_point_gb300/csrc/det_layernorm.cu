@@ -19,7 +19,7 @@
 namespace det {
 namespace {
 
-using Two = unsigned long long;    // two adjacent columns, for packed 32-bit instructions
+// (A Two holds two adjacent columns.)
 
 // The lanes' sums of a group, in every thread: a tree over lanes, then over
 // warps through `slot` (one float a warp).  A group of one warp needs no barrier.
@@ -36,8 +36,7 @@ __device__ __forceinline__ float over_warps(const float* slot, int first_warp, i
   return v;
 }
 __device__ __forceinline__ float lanes(Two v) {
-  const float2 f = unpack_f32x2(v);
-  return __fadd_rn(f.x, f.y);
+  return __fadd_rn(v.x, v.y);
 }
 
 // 1 / sqrt(v) from the hardware's approximation by a step of Newton's method.
@@ -131,22 +130,20 @@ __device__ __forceinline__ void pairs_of(const Eight<T>& e, Two (&v)[4]) {
   float f[8];
   unpack_eight(e, f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) v[i] = two(f[2 * i], f[2 * i + 1]);
 }
 // The first n of eight values, the others 0.
 __device__ __forceinline__ void keep_first(Two (&v)[4], int n) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_f32x2(v[i]);
-    v[i] = pack_f32x2(2 * i < n ? f.x : 0.0f, 2 * i + 1 < n ? f.y : 0.0f);
+    v[i] = two(2 * i < n ? v[i].x : 0.0f, 2 * i + 1 < n ? v[i].y : 0.0f);
   }
 }
-__device__ __forceinline__ Two twice(float x) { return pack_f32x2(x, x); }
 // Columns c .. c + 7 of a weight or bias, `other` without one.
 __device__ __forceinline__ void load_param(Two (&v)[4], const void* p, int c, int cols, int dtype, float other) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = pack_f32x2(p && c + 2 * i < cols ? load_as_f32(p, c + 2 * i, dtype) : other,
+    v[i] = two(p && c + 2 * i < cols ? load_as_f32(p, c + 2 * i, dtype) : other,
                       p && c + 2 * i + 1 < cols ? load_as_f32(p, c + 2 * i + 1, dtype) : other);
 }
 
@@ -183,9 +180,9 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       pairs_of(e[k], v[k]);
-      t[k] = add_f32x2(add_f32x2(v[k][0], v[k][1]), add_f32x2(v[k][2], v[k][3]));
+      t[k] = add(add(v[k][0], v[k][1]), add(v[k][2], v[k][3]));
     }
-    if (K == 2) t[0] = add_f32x2(t[0], t[K - 1]);
+    if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sum = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
       put_warp(s_sum, sum, g.warp, g.lane);
@@ -193,17 +190,17 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
       sum = over_warps(s_sum, g.first_warp, g.warps, g.lane);
     }
     const float mean = sum * of;
-    const Two mean2 = twice(mean);
+    const Two minus_mean = twice(-mean);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[k][i] = sub_f32x2(v[k][i], mean2);
+      for (int i = 0; i < 4; ++i) v[k][i] = add(v[k][i], minus_mean);
       if (!whole) keep_first(v[k], cols - (g.me + k * g.threads) * 8);
-      t[k] = mul_f32x2(v[k][0], v[k][0]);
+      t[k] = mul(v[k][0], v[k][0]);
 #pragma unroll
-      for (int i = 1; i < 4; ++i) t[k] = fma_f32x2(v[k][i], v[k][i], t[k]);
+      for (int i = 1; i < 4; ++i) t[k] = fma(v[k][i], v[k][i], t[k]);
     }
-    if (K == 2) t[0] = add_f32x2(t[0], t[K - 1]);
+    if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sq = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
       put_warp(s_sq, sq, g.warp, g.lane);
@@ -217,7 +214,7 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
       float y[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_f32x2(fma_f32x2(mul_f32x2(v[k][i], rstd2), w[k][i], b[k][i]));
+        const float2 f = (fma(mul(v[k][i], rstd2), w[k][i], b[k][i]));
         y[2 * i] = f.x;
         y[2 * i + 1] = f.y;
       }
@@ -241,7 +238,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   extern __shared__ __align__(16) char s_dynamic[];
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
   // the weight: registers hold two gradients for each column; halves of eights, so that a warp reads 512 bytes in a row
-  ulonglong2* s_w = reinterpret_cast<ulonglong2*>(s_dynamic);
+  float4* s_w = reinterpret_cast<float4*>(s_dynamic);
   dep_wait();
   dep_launch();
   const Group g(log2_threads);
@@ -252,16 +249,16 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     if (g.index == 0) {
       Two w[4];
       load_param(w, weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
-      s_w[(2 * k) * g.threads + g.me] = make_ulonglong2(w[0], w[1]);
-      s_w[(2 * k + 1) * g.threads + g.me] = make_ulonglong2(w[2], w[3]);
+      s_w[(2 * k) * g.threads + g.me] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+      s_w[(2 * k + 1) * g.threads + g.me] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = 0;
+    for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = twice(0.0f);
   }
   __syncthreads();
   auto weights = [&](int k, Two (&w)[4]) {
-    const ulonglong2 a = s_w[(2 * k) * g.threads + g.me], b = s_w[(2 * k + 1) * g.threads + g.me];
-    w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+    const float4 a = s_w[(2 * k) * g.threads + g.me], b = s_w[(2 * k + 1) * g.threads + g.me];
+    w[0] = two(a.x, a.y), w[1] = two(a.z, a.w), w[2] = two(b.x, b.y), w[3] = two(b.z, b.w);
   };
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
   const long long step = (long long)gridDim.x * g.count;
@@ -277,7 +274,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     Eight<T> cx[K], cg[K];
     to_eights(cx, nx, turn, g.lane);
     to_eights(cg, ng, turn, g.lane);
-    const Two mean2 = twice(nm), rstd2 = twice(nr);
+    const Two minus_mean = twice(-nm), rstd2 = twice(nr);
     const bool more = r + step < rows;
     load_row(nx, x + (r + step) * x_stride, g, cols, more);
     load_row(ng, grad + (r + step) * grad_stride, g, cols, more);
@@ -291,20 +288,20 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       pairs_of(cx[k], xh);
       pairs_of(cg[k], d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = mul_f32x2(sub_f32x2(xh[i], mean2), rstd2);
+      for (int i = 0; i < 4; ++i) xh[i] = mul(add(xh[i], minus_mean), rstd2);
       if (!whole) keep_first(xh, cols - (g.me + k * g.threads) * 8);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        aw[k][i] = fma_f32x2(d[i], xh[i], aw[k][i]);
-        ab[k][i] = add_f32x2(ab[k][i], d[i]);
-        d[i] = mul_f32x2(d[i], w[i]);
-        t1[k] = i ? add_f32x2(t1[k], d[i]) : d[i];
-        t2[k] = i ? fma_f32x2(d[i], xh[i], t2[k]) : mul_f32x2(d[i], xh[i]);
+        aw[k][i] = fma(d[i], xh[i], aw[k][i]);
+        ab[k][i] = add(ab[k][i], d[i]);
+        d[i] = mul(d[i], w[i]);
+        t1[k] = i ? add(t1[k], d[i]) : d[i];
+        t2[k] = i ? fma(d[i], xh[i], t2[k]) : mul(d[i], xh[i]);
       }
     }
     if (K == 2) {
-      t1[0] = add_f32x2(t1[0], t1[K - 1]);
-      t2[0] = add_f32x2(t2[0], t2[K - 1]);
+      t1[0] = add(t1[0], t1[K - 1]);
+      t2[0] = add(t2[0], t2[K - 1]);
     }
     float one = warp_pt(lanes(t1[0])), two = warp_pt(lanes(t2[0]));
     if (g.warps > 1) {
@@ -329,9 +326,9 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          xh[i] = mul_f32x2(sub_f32x2(xh[i], mean2), rstd2);
-          d[i] = fma_f32x2(xh[i], minus_two, fma_f32x2(d[i], w[i], minus_one));
-          const float2 f = unpack_f32x2(mul_f32x2(d[i], rstd2));
+          xh[i] = mul(add(xh[i], minus_mean), rstd2);
+          d[i] = fma(xh[i], minus_two, fma(d[i], w[i], minus_one));
+          const float2 f = (mul(d[i], rstd2));
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
         }
@@ -350,7 +347,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_f32x2(which ? ab[k][i] : aw[k][i]);
+        const float2 f = which ? ab[k][i] : aw[k][i];
         const int c = (g.me + k * g.threads) * 8 + 2 * i;
         float* to = g.count > 1 ? s_acc + g.index * cols : mine + which * cols;
         if (c < cols) to[c] = f.x;

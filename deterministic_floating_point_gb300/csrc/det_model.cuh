@@ -61,16 +61,15 @@ __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, un
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ unsigned long long sub_f32x2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+
+// Two values worked on by one packed instruction.
+using Two = float2;
+__device__ __forceinline__ Two two(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ Two twice(float a) { return make_float2(a, a); }
+__device__ __forceinline__ Two add(Two a, Two b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ Two mul(Two a, Two b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ Two minus(Two a, Two b) { return __ffma2_rn(b, twice(-1.0f), a); }
 
 // A 32-bit key in the order of the values: -0 and +0 are equal, NaN is above
 // +inf.

@@ -61,17 +61,16 @@ struct Shape {
 // ---------------------------------------------------------------------------
 // A lane's values: two 16-bit channels of a word as a packed pair, one of 32 bits.
 
-using Two = unsigned long long;
+using det::add;
+using det::fma;
+using det::minus;
+using det::mul;
 __device__ __forceinline__ float add(float a, float b) { return __fadd_rn(a, b); }
 __device__ __forceinline__ float mul(float a, float b) { return __fmul_rn(a, b); }
 __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ Two add(Two a, Two b) { return add_f32x2(a, b); }
-__device__ __forceinline__ Two mul(Two a, Two b) { return mul_f32x2(a, b); }
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) { return fma_f32x2(a, b, c); }
 __device__ __forceinline__ void both(float& v, float x) { v = x; }
-__device__ __forceinline__ void both(Two& v, float x) { v = pack_f32x2(x, x); }
+__device__ __forceinline__ void both(Two& v, float x) { v = twice(x); }
 __device__ __forceinline__ float minus(float a, float b) { return __fsub_rn(a, b); }
-__device__ __forceinline__ Two minus(Two a, Two b) { return sub_f32x2(a, b); }
 
 template <typename T> struct Lane {
   static constexpr int CH = 2;
@@ -90,7 +89,7 @@ __device__ __forceinline__ LaneV<T> unpack(unsigned w) {
   } else {
     float a, b;
     unpack_two(w, a, b, T());
-    return pack_f32x2(a, b);
+    return two(a, b);
   }
 }
 template <typename T>
@@ -98,7 +97,7 @@ __device__ __forceinline__ unsigned pack(LaneV<T> v) {
   if constexpr (sizeof(T) == 4) {
     return __float_as_uint(v);
   } else {
-    const float2 f = unpack_f32x2(v);
+    const float2 f = (v);
     return pack_two<T>(f.x, f.y);
   }
 }
@@ -131,18 +130,24 @@ __device__ __forceinline__ void store_word(T* p, unsigned w, int n) {
   }
 }
 
+// v, after it has arrived: a shuffle needs its value.
+__device__ __forceinline__ float here_by_now(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+__device__ __forceinline__ Two here_by_now(Two v, int lane) {
+  return two(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane));
+}
+
 // 32-bit state of a lane's channels in [.., channels] floats at p.
 template <int CH, typename V>
 __device__ __forceinline__ void load_state(V& v, const float* p, int n) {
   if constexpr (CH == 1) v = n > 0 ? p[0] : 0.0f;
-  else v = pack_f32x2(n > 0 ? p[0] : 0.0f, n > 1 ? p[1] : 0.0f);
+  else v = two(n > 0 ? p[0] : 0.0f, n > 1 ? p[1] : 0.0f);
 }
 template <int CH, typename V>
 __device__ __forceinline__ void store_state(float* p, V v, int n) {
   if constexpr (CH == 1) {
     if (n > 0) p[0] = v;
   } else {
-    const float2 f = unpack_f32x2(v);
+    const float2 f = (v);
     if (n > 0) p[0] = f.x;
     if (n > 1) p[1] = f.y;
   }
@@ -182,7 +187,7 @@ struct Gates {
     if constexpr (FORM == DET_GATE_SIGMOID && sizeof(T) == 2) {
       const float e = exp2_approx(__fmul_rn(kLowestGate, -kLog2e));
       const float a = -rcp_approx(__fadd_rn(e, 1.0f));
-      floor = pack_f32x2(a, a);
+      floor = two(a, a);
     }
   }
   __device__ __forceinline__ void operator()(unsigned w, V& a, V& rest) const {
@@ -190,11 +195,11 @@ struct Gates {
       a = unpack<T>(w);
       both(rest, 1.0f);
     } else if constexpr (sizeof(T) == 2) {
-      const Two t = mul(unpack<T>(at_least(w, kLowestGate, T())), pack_f32x2(-kLog2e, -kLog2e));
-      const float2 f = unpack_f32x2(t);
-      const Two e = pack_f32x2(exp2_approx(f.x), exp2_approx(f.y));
-      const float2 d = unpack_f32x2(add(e, pack_f32x2(1.0f, 1.0f)));
-      a = pack_f32x2(rcp_approx(d.x), rcp_approx(d.y));
+      const Two t = mul(unpack<T>(at_least(w, kLowestGate, T())), two(-kLog2e, -kLog2e));
+      const float2 f = (t);
+      const Two e = two(exp2_approx(f.x), exp2_approx(f.y));
+      const float2 d = (add(e, two(1.0f, 1.0f)));
+      a = two(rcp_approx(d.x), rcp_approx(d.y));
       rest = mul(e, a);
       a = add(a, floor);
     } else {
@@ -223,8 +228,8 @@ __device__ __forceinline__ Two after_block(Two h, Two A, Two H) {
   if constexpr (FORM == DET_GATE_SIGMOID) {
     return fma(A, h, H);
   } else {
-    const float2 g = unpack_f32x2(h), a = unpack_f32x2(A), b = unpack_f32x2(H);
-    return pack_f32x2(after_block<FORM>(g.x, a.x, b.x), after_block<FORM>(g.y, a.y, b.y));
+    const float2 g = (h), a = (A), b = (H);
+    return two(after_block<FORM>(g.x, a.x, b.x), after_block<FORM>(g.y, a.y, b.y));
   }
 }
 
@@ -527,7 +532,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
   V carry;
   load_state<CH>(carry, initial + row, initial && me.warp >= me.workers ? me.n : 0);
   // (the shuffle waits for it: a CTA that has heard of all may write the final state to the same place)
-  carry = __shfl_sync(0xffffffffu, carry, me.lane);
+  carry = here_by_now(carry, me.lane);
   if (shape.log2_ranks > 0) cluster_wait();
   else __syncthreads();
 
