@@ -76,18 +76,33 @@ template <typename T, int K> struct Row<T, false, K> {
   typename Bits<T>::U w[K][8];
 };
 
+// Where a thread reads and writes in a row: its first column, and how many of each
+// of its eights there are.
+template <bool VEC, int K> struct Columns {
+  int first, step;       // step: from one eight to the next
+  int n[K];              // VEC: columns; else columns of the row from the thread's first element on
+  __device__ __forceinline__ Columns(const Group& g, int cols) {
+    first = VEC ? g.me * 8 : (g.me & ~31) * 8 + g.lane;
+    step = g.threads * 8;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      n[k] = cols - first - k * step;
+      if (VEC) n[k] = max(0, min(8, n[k]));
+    }
+  }
+};
+
+// at: the row, from the thread's first column on
 template <typename T, bool VEC, int K>
-__device__ __forceinline__ void load_row(Row<T, VEC, K>& r, const T* row, const Group& g, int cols, bool valid) {
+__device__ __forceinline__ void load_row(Row<T, VEC, K>& r, const T* at, const Columns<VEC, K>& c, bool valid) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if constexpr (VEC) {
-      const int c = (g.me + k * g.threads) * 8;
-      r.e[k] = load_eight<true>(row + c, valid ? max(0, min(8, cols - c)) : 0);
+      r.e[k] = load_eight<true>(at + k * c.step, valid ? c.n[k] : 0);
     } else {
-      const int c = ((g.me & ~31) + k * g.threads) * 8 + g.lane;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        r.w[k][j] = valid && c + 32 * j < cols ? reinterpret_cast<const typename Bits<T>::U*>(row)[c + 32 * j] : 0;
+        r.w[k][j] = valid && 32 * j < c.n[k] ? reinterpret_cast<const typename Bits<T>::U*>(at)[k * c.step + 32 * j] : 0;
     }
   }
 }
@@ -107,20 +122,19 @@ __device__ __forceinline__ void to_eights(Eight<T> (&e)[K], const Row<T, VEC, K>
     }
   }
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_columns(T* row, const float (&v)[8], const Group& g, int k, int cols, bool valid,
-                                              void* warp_kb) {
+template <typename T, bool VEC, int K>
+__device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<VEC, K>& c, int k, bool valid,
+                                              void* warp_kb, int lane) {
   if constexpr (VEC) {
-    const int c = (g.me + k * g.threads) * 8;
-    if (valid) store_eight<true>(row + c, v, max(0, min(8, cols - c)));
+    if (valid) store_eight<true>(at + k * c.step, v, c.n[k]);
   } else {
     using U = typename Bits<T>::U;
-    store_eight<true>(static_cast<T*>(warp_kb) + 8 * g.lane, v, 8);
+    store_eight<true>(static_cast<T*>(warp_kb) + 8 * lane, v, 8);
     __syncwarp();
-    const int c = ((g.me & ~31) + k * g.threads) * 8 + g.lane;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (valid && c + 32 * j < cols) reinterpret_cast<U*>(row)[c + 32 * j] = static_cast<const U*>(warp_kb)[32 * j + g.lane];
+      if (valid && 32 * j < c.n[k])
+        reinterpret_cast<U*>(at)[k * c.step + 32 * j] = static_cast<const U*>(warp_kb)[32 * j + lane];
     __syncwarp();
   }
 }
@@ -151,7 +165,7 @@ constexpr int kThreads = 256;       // a CTA's, unless a row takes more
 
 template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 4 : 3)
-layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void* weight, const void* bias,
+layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const void* weight, const void* bias,
                   int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int log2_threads) {
   __shared__ __align__(16) float s_sum[32], s_sq[32];
   __shared__ __align__(16) char s_turn[VEC ? 1 : MOST / 32][VEC ? 16 : 1024];
@@ -166,22 +180,26 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
     load_param(b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
   }
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;   // all of the thread's columns are there
-  const long long step = (long long)gridDim.x * g.count;
+  const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
-  long long first = (long long)blockIdx.x * g.count;       // of the CTA's rows: every thread makes as many rounds
-  long long r = first + g.index;
+  const Columns<VEC, K> c(g, cols);
+  unsigned r = blockIdx.x * g.count + g.index;
+  const T* from = x + r * x_stride + c.first;
+  T* to = out + (long long)r * cols + c.first;
   Row<T, VEC, K> next;
-  load_row(next, x + r * x_stride, g, cols, r < rows);
-  for (; first < rows; first += step, r += step) {
+  load_row(next, from, c, r < rows);
+  // (every thread of the CTA makes as many rounds)
+  for (unsigned first = blockIdx.x * g.count; first < rows; first += step, r += step, to += (long long)step * cols) {
     Eight<T> e[K];
     to_eights(e, next, turn, g.lane);
-    load_row(next, x + (r + step) * x_stride, g, cols, r + step < rows);
     Two v[K][4], t[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       pairs_of(e[k], v[k]);
       t[k] = add(add(v[k][0], v[k][1]), add(v[k][2], v[k][3]));
     }
+    from += step * x_stride;
+    load_row(next, from, c, r + step < rows);
     if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sum = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
@@ -218,7 +236,7 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
         y[2 * i] = f.x;
         y[2 * i + 1] = f.y;
       }
-      store_columns<VEC>(out + r * cols, y, g, k, cols, r < rows, turn);
+      store_columns(to, y, c, k, r < rows, turn, g.lane);
     }
     if (g.me == 0 && r < rows) {
       if (mean_out) mean_out[r] = mean;
@@ -230,7 +248,7 @@ layer_norm_kernel(const T* x, int rows, int cols, long long x_stride, const void
 // part: [gridDim.x][2][cols] sums of the weight's and the bias' gradients, or NULL.
 template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
-layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, int rows, int cols,
+layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, unsigned rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
                        float* part, int log2_threads) {
   __shared__ float2 s_sums[2][32];
@@ -261,23 +279,29 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     w[0] = two(a.x, a.y), w[1] = two(a.z, a.w), w[2] = two(b.x, b.y), w[3] = two(b.z, b.w);
   };
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
-  const long long step = (long long)gridDim.x * g.count;
+  const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
-  long long first = (long long)blockIdx.x * g.count;
-  long long r = first + g.index;
+  const Columns<VEC, K> c(g, cols);
+  unsigned r = blockIdx.x * g.count + g.index;
+  const T* from_x = x + r * x_stride + c.first;
+  const T* from_grad = grad + r * grad_stride + c.first;
+  T* to = grad_x + (long long)r * cols + c.first;
   Row<T, VEC, K> nx, ng;
-  load_row(nx, x + r * x_stride, g, cols, r < rows);
-  load_row(ng, grad + r * grad_stride, g, cols, r < rows);
+  load_row(nx, from_x, c, r < rows);
+  load_row(ng, from_grad, c, r < rows);
   float nm = r < rows ? means[r] : 0.0f, nr = r < rows ? rstds[r] : 0.0f;
   int parity = 0;
-  for (; first < rows; first += step, r += step, parity ^= 1) {
+  for (unsigned first = blockIdx.x * g.count; first < rows;
+       first += step, r += step, parity ^= 1, to += (long long)step * cols) {
     Eight<T> cx[K], cg[K];
     to_eights(cx, nx, turn, g.lane);
     to_eights(cg, ng, turn, g.lane);
     const Two minus_mean = twice(-nm), rstd2 = twice(nr);
     const bool more = r + step < rows;
-    load_row(nx, x + (r + step) * x_stride, g, cols, more);
-    load_row(ng, grad + (r + step) * grad_stride, g, cols, more);
+    from_x += step * x_stride;
+    from_grad += step * grad_stride;
+    load_row(nx, from_x, c, more);
+    load_row(ng, from_grad, c, more);
     nm = more ? means[r + step] : 0.0f;
     nr = more ? rstds[r + step] : 0.0f;
     Two t1[K], t2[K];
@@ -332,7 +356,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
         }
-        store_columns<VEC>(grad_x + r * cols, y, g, k, cols, r < rows, turn);
+        store_columns(to, y, c, k, r < rows, turn, g.lane);
       }
     }
   }
@@ -419,7 +443,7 @@ int forward(const void* x, int rows, int cols, int64_t x_stride, const void* wei
   const long long grid = std::min<long long>((rows + (long long)at_a_time - 1) / at_a_time,
                                              (long long)per_sm * std::max(device_sm_count(), 1));
   launch_begin("det_layer_norm", s);
-  const cudaError_t e = launch_dep(k, dim3((unsigned)grid), dim3(threads), 0, s, static_cast<const T*>(x), rows, cols,
+  const cudaError_t e = launch_dep(k, dim3((unsigned)grid), dim3(threads), 0, s, static_cast<const T*>(x), (unsigned)rows, cols,
                                    (long long)x_stride, weight, bias, param_dtype, eps, static_cast<T*>(out), mean_out,
                                    rstd_out, l);
   launch_end(s);
@@ -440,7 +464,7 @@ int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_str
   launch_begin("det_layer_norm_backward", s);
   const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols, dtype)), dim3(threads), smem, s,
                                    static_cast<const T*>(grad), (long long)grad_stride, static_cast<const T*>(x),
-                                   (long long)x_stride, rows, cols, mean, rstd, weight, param_dtype,
+                                   (long long)x_stride, (unsigned)rows, cols, mean, rstd, weight, param_dtype,
                                    static_cast<T*>(grad_x), part, l);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm_backward");
