@@ -61,20 +61,16 @@ struct Group {
 };
 
 // ---------------------------------------------------------------------------
-// Rows.  A thread's columns are eights, `threads` eights apart.  Where every row
-// starts on 16 bytes (VEC) it reads and writes them as vectors.  Else the 256
-// columns of a warp's eights go element by element, lane after lane, and turn into
-// eights in the warp's kilobyte of shared memory; eight single elements a thread at
-// one address after the other took 33 us for 4,099 x 1,021 in 32 bits.
+// Rows.  A thread's columns are eights, `threads` eights apart.  Rows are copied into
+// shared memory up to two rounds ahead of their turn, each warp the 256 columns of
+// its eights: as 16-byte vectors where every row starts on 16 bytes (VEC), else in 32
+// bits element by element.  (Rows ahead in registers instead left an SM with two CTAs.)
+// 16-bit rows at other addresses go through registers, element after element across the
+// lanes, and turn into eights in the warp's part of shared memory; eight single elements a
+// thread at one address after the other took 33 us for 4,099 x 1,021 in 32 bits, this
+// way 20.
 template <typename T> struct Bits { using U = unsigned short; };
 template <> struct Bits<float> { using U = unsigned; };
-
-template <typename T, bool VEC, int K> struct Row {
-  Eight<T> e[K];
-};
-template <typename T, int K> struct Row<T, false, K> {
-  typename Bits<T>::U w[K][8];
-};
 
 // Where a thread reads and writes in a row: its first column, and how many of each
 // of its eights there are.
@@ -92,36 +88,78 @@ template <bool VEC, int K> struct Columns {
   }
 };
 
-// at: the row, from the thread's first column on
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool valid) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last `ahead` (0 or 1) groups have arrived.
+__device__ __forceinline__ void copies_wait(int ahead) {
+  if (ahead) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
+
+// A warp's rows of one operand: asked for, and taken in the same order.
 template <typename T, bool VEC, int K>
-__device__ __forceinline__ void load_row(Row<T, VEC, K>& r, const T* at, const Columns<VEC, K>& c, bool valid) {
+struct Feed {
+  static constexpr bool kCopies = VEC || sizeof(T) == 4;
+  enum : int { kHalves = sizeof(T) / 2, kStage = K * 256 * sizeof(T) };   // 16-byte vectors of an eight; bytes of a warp's columns
+  char* s;               // the warp's stages; without copies the place where eights are made
+  typename Bits<T>::U w[kCopies ? 1 : K][8];
+  __device__ __forceinline__ explicit Feed(char* stages) : s(stages) {}
+  // at: the row, from the thread's first column on; `any` may be read
+  __device__ __forceinline__ void ask(int stage, const T* at, const T* any, const Columns<VEC, K>& c, bool valid, int lane) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if constexpr (VEC) {
-      r.e[k] = load_eight<true>(at + k * c.step, valid ? c.n[k] : 0);
-    } else {
+    for (int k = 0; k < K; ++k) {
+      if constexpr (VEC) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        r.w[k][j] = valid && 32 * j < c.n[k] ? reinterpret_cast<const typename Bits<T>::U*>(at)[k * c.step + 32 * j] : 0;
+        for (int h = 0; h < kHalves; ++h) {
+          const bool ok = valid && c.n[k] > 4 * h;
+          copy_async<16>(s + stage * kStage + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 4 * h : any, ok);
+        }
+      } else if constexpr (kCopies) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool ok = valid && 32 * j < c.n[k];
+          copy_async<4>(s + stage * kStage + (k * 256 + 32 * j + lane) * 4, ok ? at + k * c.step + 32 * j : any, ok);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[k][j] = valid && 32 * j < c.n[k] ? reinterpret_cast<const typename Bits<T>::U*>(at)[k * c.step + 32 * j] : 0;
+      }
     }
   }
-}
-template <typename T, bool VEC, int K>
-__device__ __forceinline__ void to_eights(Eight<T> (&e)[K], const Row<T, VEC, K>& r, void* warp_kb, int lane) {
+  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], int lane) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if constexpr (VEC) {
-      e[k] = r.e[k];
-    } else {
-      typename Bits<T>::U* s = static_cast<typename Bits<T>::U*>(warp_kb);
+    for (int k = 0; k < K; ++k) {
+      if constexpr (VEC) {
+        const uint4* q = reinterpret_cast<const uint4*>(s + stage * kStage) + k * kHalves * 32 + lane;
+        e[k].q = q[0];
+        if constexpr (kHalves == 2) e[k].r = q[32];
+      } else if constexpr (kCopies) {
+        e[k] = load_eight<true>(reinterpret_cast<const T*>(s + stage * kStage) + k * 256 + 8 * lane, 8);
+      } else {
+        typename Bits<T>::U* turn = reinterpret_cast<typename Bits<T>::U*>(s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[32 * j + lane] = r.w[k][j];
-      __syncwarp();
-      e[k] = load_eight<true>(static_cast<const T*>(warp_kb) + 8 * lane, 8);
-      __syncwarp();
+        for (int j = 0; j < 8; ++j) turn[32 * j + lane] = w[k][j];
+        __syncwarp();
+        e[k] = load_eight<true>(reinterpret_cast<const T*>(s) + 8 * lane, 8);
+        __syncwarp();
+      }
     }
+    if constexpr (kCopies) __syncwarp();                 // the stage may be written again
   }
+};
+// Bytes of a warp's stages, and of the place where its outputs turn into rows.
+template <typename T, bool VEC, int K>
+__host__ __device__ constexpr int feed_bytes(int stages) {
+  return VEC || sizeof(T) == 4 ? stages * K * 256 * (int)sizeof(T) : 512;
 }
+template <typename T, bool VEC>
+__host__ __device__ constexpr int turn_bytes() { return VEC ? 0 : 256 * (int)sizeof(T); }
 template <typename T, bool VEC, int K>
 __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<VEC, K>& c, int k, bool valid,
                                               void* warp_kb, int lane) {
@@ -163,43 +201,76 @@ __device__ __forceinline__ void load_param(Two (&v)[4], const void* p, int c, in
 
 constexpr int kThreads = 256;       // a CTA's, unless a row takes more
 
+// A weight or bias in shared memory, where they leave registers for rows: halves of
+// eights, so that a warp reads 512 bytes in a row.
+__device__ __forceinline__ void keep_param(float4* s, const void* p, const Group& g, int k, int cols, int dtype, float other) {
+  Two v[4];
+  load_param(v, p, (g.me + k * g.threads) * 8, cols, dtype, other);
+  s[(2 * k) * g.threads + g.me] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  s[(2 * k + 1) * g.threads + g.me] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void param(Two (&v)[4], const float4* s, const Group& g, int k) {
+  const float4 a = s[(2 * k) * g.threads + g.me], b = s[(2 * k + 1) * g.threads + g.me];
+  v[0] = two(a.x, a.y), v[1] = two(a.z, a.w), v[2] = two(b.x, b.y), v[3] = two(b.z, b.w);
+}
+
 template <typename T, int K, bool VEC, int MOST>
-__global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 4 : 3)
+__global__ void __launch_bounds__(MOST, MOST > 256 ? 1024 / MOST : K == 1 ? 4 : 3)
 layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const void* weight, const void* bias,
-                  int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int log2_threads) {
+                  int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int log2_threads, int stages) {
   __shared__ __align__(16) float s_sum[32], s_sq[32];
-  __shared__ __align__(16) char s_turn[VEC ? 1 : MOST / 32][VEC ? 16 : 1024];
+  extern __shared__ __align__(16) char s_dynamic[];
   dep_wait();
   dep_launch();
   const Group g(log2_threads);
-  char* turn = s_turn[VEC ? 0 : g.warp];
-  Two w[K][4], b[K][4];
+  // weight and bias are in registers where CTAs of 256 threads leave enough of them (48 us for 16,384 x 4,096 in bf16 against
+  // 52 with shared memory), else in shared memory
+  constexpr bool HELD = MOST == 256;
+  Two held_w[HELD ? K : 1][4], held_b[HELD ? K : 1][4];
+  float4* s_w = reinterpret_cast<float4*>(s_dynamic);
+  float4* s_b = s_w + (HELD ? 0 : 2 * K * g.threads);
+  char* mine = reinterpret_cast<char*>(s_b + (HELD ? 0 : 2 * K * g.threads)) +
+               g.warp * (feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
+  char* turn = mine + feed_bytes<T, VEC, K>(stages);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    load_param(w[k], weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
-    load_param(b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
+    if constexpr (HELD) {
+      load_param(held_w[k], weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
+      load_param(held_b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
+    } else {
+      keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);       // (read again by the same thread)
+      keep_param(s_b, bias, g, k, cols, param_dtype, 0.0f);
+    }
   }
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;   // all of the thread's columns are there
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
   const Columns<VEC, K> c(g, cols);
-  unsigned r = blockIdx.x * g.count + g.index;
+  unsigned r = blockIdx.x * g.count + g.index, asked = r;
   const T* from = x + r * x_stride + c.first;
   T* to = out + (long long)r * cols + c.first;
-  Row<T, VEC, K> next;
-  load_row(next, from, c, r < rows);
+  Feed<T, VEC, K> feed(mine);
+  for (int i = 0; i < stages; ++i, asked += step, from += step * x_stride) {
+    feed.ask(i, from, x, c, asked < rows, g.lane);
+    copies_commit();
+  }
+  int stage = 0;
   // (every thread of the CTA makes as many rounds)
   for (unsigned first = blockIdx.x * g.count; first < rows; first += step, r += step, to += (long long)step * cols) {
     Eight<T> e[K];
-    to_eights(e, next, turn, g.lane);
+    copies_wait(stages - 1);
+    feed.take(stage, e, g.lane);
+    feed.ask(stage, from, x, c, asked < rows, g.lane);
+    copies_commit();
+    asked += step;
+    from += step * x_stride;
+    stage = stage + 1 == stages ? 0 : stage + 1;
     Two v[K][4], t[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       pairs_of(e[k], v[k]);
       t[k] = add(add(v[k][0], v[k][1]), add(v[k][2], v[k][3]));
     }
-    from += step * x_stride;
-    load_row(next, from, c, r + step < rows);
     if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sum = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
@@ -230,9 +301,14 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float y[8];
+      Two w[4], b[4];
+      if constexpr (!HELD) {
+        param(w, s_w, g, k);
+        param(b, s_b, g, k);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = (fma(mul(v[k][i], rstd2), w[k][i], b[k][i]));
+        const float2 f = fma(mul(v[k][i], rstd2), HELD ? held_w[HELD ? k : 0][i] : w[i], HELD ? held_b[HELD ? k : 0][i] : b[i]);
         y[2 * i] = f.x;
         y[2 * i + 1] = f.y;
       }
@@ -250,65 +326,62 @@ template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
 layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, unsigned rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
-                       float* part, int log2_threads) {
+                       float* part, int log2_threads, int stages) {
   __shared__ float2 s_sums[2][32];
-  __shared__ __align__(16) char s_turn[VEC ? 1 : MOST / 32][VEC ? 16 : 1024];
   extern __shared__ __align__(16) char s_dynamic[];
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
-  // the weight: registers hold two gradients for each column; halves of eights, so that a warp reads 512 bytes in a row
-  float4* s_w = reinterpret_cast<float4*>(s_dynamic);
   dep_wait();
   dep_launch();
   const Group g(log2_threads);
-  char* turn = s_turn[VEC ? 0 : g.warp];
+  float4* s_w = reinterpret_cast<float4*>(s_dynamic);
+  char* mine_x = reinterpret_cast<char*>(s_w + 2 * K * g.threads) +
+                 g.warp * (2 * feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
   Two aw[K][4], ab[K][4];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (g.index == 0) {
-      Two w[4];
-      load_param(w, weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
-      s_w[(2 * k) * g.threads + g.me] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
-      s_w[(2 * k + 1) * g.threads + g.me] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
-    }
+    if (g.index == 0) keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = twice(0.0f);
   }
   __syncthreads();
-  auto weights = [&](int k, Two (&w)[4]) {
-    const float4 a = s_w[(2 * k) * g.threads + g.me], b = s_w[(2 * k + 1) * g.threads + g.me];
-    w[0] = two(a.x, a.y), w[1] = two(a.z, a.w), w[2] = two(b.x, b.y), w[3] = two(b.z, b.w);
-  };
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
   const Columns<VEC, K> c(g, cols);
-  unsigned r = blockIdx.x * g.count + g.index;
+  unsigned r = blockIdx.x * g.count + g.index, asked = r;
   const T* from_x = x + r * x_stride + c.first;
   const T* from_grad = grad + r * grad_stride + c.first;
   T* to = grad_x + (long long)r * cols + c.first;
-  Row<T, VEC, K> nx, ng;
-  load_row(nx, from_x, c, r < rows);
-  load_row(ng, from_grad, c, r < rows);
+  Feed<T, VEC, K> feed_x(mine_x), feed_grad(mine_x + feed_bytes<T, VEC, K>(stages));
+  char* turn = mine_x + 2 * feed_bytes<T, VEC, K>(stages);
+  auto ask = [&](int stage) {
+    feed_x.ask(stage, from_x, x, c, asked < rows, g.lane);
+    feed_grad.ask(stage, from_grad, grad, c, asked < rows, g.lane);
+    copies_commit();
+    asked += step;
+    from_x += step * x_stride;
+    from_grad += step * grad_stride;
+  };
+  for (int i = 0; i < stages; ++i) ask(i);
   float nm = r < rows ? means[r] : 0.0f, nr = r < rows ? rstds[r] : 0.0f;
-  int parity = 0;
+  int parity = 0, stage = 0;
   for (unsigned first = blockIdx.x * g.count; first < rows;
        first += step, r += step, parity ^= 1, to += (long long)step * cols) {
     Eight<T> cx[K], cg[K];
-    to_eights(cx, nx, turn, g.lane);
-    to_eights(cg, ng, turn, g.lane);
+    copies_wait(stages - 1);
+    feed_x.take(stage, cx, g.lane);
+    feed_grad.take(stage, cg, g.lane);
+    ask(stage);
+    stage = stage + 1 == stages ? 0 : stage + 1;
     const Two minus_mean = twice(-nm), rstd2 = twice(nr);
     const bool more = r + step < rows;
-    from_x += step * x_stride;
-    from_grad += step * grad_stride;
-    load_row(nx, from_x, c, more);
-    load_row(ng, from_grad, c, more);
     nm = more ? means[r + step] : 0.0f;
     nr = more ? rstds[r + step] : 0.0f;
     Two t1[K], t2[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       Two xh[4], d[4], w[4];
-      weights(k, w);
+      param(w, s_w, g, k);
       pairs_of(cx[k], xh);
       pairs_of(cg[k], d);
 #pragma unroll
@@ -344,7 +417,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Two xh[4], d[4], w[4];
-        weights(k, w);
+        param(w, s_w, g, k);
         pairs_of(cx[k], xh);
         pairs_of(cg[k], d);
         float y[8];
@@ -361,7 +434,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     }
   }
   if (!part) return;
-  __syncthreads();                     // the weight has been read
+  __syncthreads();                     // weight and rows have been read
   float* mine = part + (long long)blockIdx.x * 2 * cols;
   // several rows at a time: the groups' sums in the groups' order
 #pragma unroll
@@ -433,19 +506,36 @@ bool vectors(const void* p, int64_t stride, int64_t cols) {
   return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * sizeof(T)) | (uintptr_t)(cols * sizeof(T))) % 16 == 0;
 }
 
+// Rows that are copied ahead, and the dynamic shared memory: two, or one where 32-bit
+// rows of more than 8,192 columns leave no room.
+template <typename T, bool VEC, int K>
+size_t room(int params, int operands, int log2_threads, int threads, int* stages) {
+  size_t bytes = 0;
+  for (*stages = VEC || sizeof(T) == 4 ? 2 : 1; *stages > 0; --*stages) {
+    bytes = ((size_t)params * K * 32 << log2_threads) +
+            threads / 32 * (size_t)(operands * feed_bytes<T, VEC, K>(*stages) + turn_bytes<T, VEC>());
+    if (bytes <= 226 * 1024 || *stages == 1) break;
+  }
+  return bytes;
+}
+
 template <typename T, int K, bool VEC, int MOST>
 int forward(const void* x, int rows, int cols, int64_t x_stride, const void* weight, const void* bias, int param_dtype,
             float eps, void* out, float* mean_out, float* rstd_out, int dtype, cudaStream_t s) {
   const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
   auto* k = layer_norm_kernel<T, K, VEC, MOST>;
-  const int per_sm = kernel_occupancy((const void*)k, threads, 0);
+  int stages = 1;
+  const size_t smem = room<T, VEC, K>(MOST == 256 ? 0 : 2, 1, l, threads, &stages);
+  const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
+  if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm");
+  const int per_sm = kernel_occupancy((const void*)k, threads, smem);
   if (per_sm <= 0) return cuda_fail(cudaErrorUnknown, "det_layer_norm");
   const long long grid = std::min<long long>((rows + (long long)at_a_time - 1) / at_a_time,
                                              (long long)per_sm * std::max(device_sm_count(), 1));
   launch_begin("det_layer_norm", s);
-  const cudaError_t e = launch_dep(k, dim3((unsigned)grid), dim3(threads), 0, s, static_cast<const T*>(x), (unsigned)rows, cols,
-                                   (long long)x_stride, weight, bias, param_dtype, eps, static_cast<T*>(out), mean_out,
-                                   rstd_out, l);
+  const cudaError_t e = launch_dep(k, dim3((unsigned)grid), dim3(threads), smem, s, static_cast<const T*>(x),
+                                   (unsigned)rows, cols, (long long)x_stride, weight, bias, param_dtype, eps,
+                                   static_cast<T*>(out), mean_out, rstd_out, l, stages);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm");
 }
@@ -454,18 +544,19 @@ template <typename T, int K, bool VEC, int MOST>
 int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int rows, int cols,
              const float* mean, const float* rstd, const void* weight, int param_dtype, void* grad_x, float* part,
              int dtype, cudaStream_t s) {
-  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l);
   auto* k = layer_norm_grad_kernel<T, K, VEC, MOST>;
-  // the weight, and in its place later the groups' sums
-  const size_t smem = std::max((size_t)K * 8 << l, (size_t)(at_a_time > 1 ? at_a_time * cols : 0)) * sizeof(float);
-  // (at least 40 KB: with the static arrays less may pass the default limit too)
-  const cudaError_t se = ensure_dyn_smem((const void*)k, std::max(smem, (size_t)40 * 1024));
+  int stages = 1;
+  // weight and rows; the groups' sums take their place at the end
+  const size_t sums = (threads >> l) > 1 ? (size_t)(threads >> l) * cols * sizeof(float) : 0;
+  const size_t smem = std::max(room<T, VEC, K>(1, 2, l, threads, &stages), sums);
+  const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm_backward");
   launch_begin("det_layer_norm_backward", s);
   const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols, dtype)), dim3(threads), smem, s,
                                    static_cast<const T*>(grad), (long long)grad_stride, static_cast<const T*>(x),
                                    (long long)x_stride, (unsigned)rows, cols, mean, rstd, weight, param_dtype,
-                                   static_cast<T*>(grad_x), part, l);
+                                   static_cast<T*>(grad_x), part, l, stages);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm_backward");
 }

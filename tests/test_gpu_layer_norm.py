@@ -75,7 +75,7 @@ def column_depth(rows, cols, dtype):
     eights = 2 if cols > (8192 if dtype == torch.float32 else 256) else 1
     threads = max(32, 1 << max(0, math.ceil(math.log2(cols / (8 * eights)))))
     at_a_time = max(1, 256 // threads)
-    parts = max(1, min(-(-rows // at_a_time), 152 * (1 if threads > 256 else 3 if eights == 1 else 2)))
+    parts = max(1, min(-(-rows // at_a_time), 152 * (1 if threads > 256 else 3)))
     return -(-rows // (parts * at_a_time)) + at_a_time + -(-parts // 32) + 6
 
 
