@@ -65,20 +65,19 @@ struct Group {
 // shared memory up to two rounds ahead of their turn, each warp the 256 columns of
 // its eights: as 16-byte vectors where every row starts on 16 bytes (VEC), else in 32
 // bits element by element.  (Rows ahead in registers instead left an SM with two CTAs.)
-// 16-bit rows at other addresses go through registers, element after element across the
-// lanes, and turn into eights in the warp's part of shared memory; eight single elements a
-// thread at one address after the other took 33 us for 4,099 x 1,021 in 32 bits, this
-// way 20.
-template <typename T> struct Bits { using U = unsigned short; };
-template <> struct Bits<float> { using U = unsigned; };
+// 16-bit rows at other addresses are copied by the words that hold them and shifted by an
+// element where they start in the middle of one (such a first word's lower half is not
+// the row's, but lies beside it in a word); outputs are shifted back and go through the
+// warp's part of shared memory.  (Element after element across the lanes instead: 176 us for the gradient of
+// 16,384 x 4,095 in bf16.)
 
 // Where a thread reads and writes in a row: its first column, and how many of each
 // of its eights there are.
-template <bool VEC, int K> struct Columns {
+template <typename T, bool VEC, int K> struct Columns {
   int first, step;       // step: from one eight to the next
-  int n[K];              // VEC: columns; else columns of the row from the thread's first element on
+  int n[K];              // VEC: columns; else columns of the row from the first one on
   __device__ __forceinline__ Columns(const Group& g, int cols) {
-    first = VEC ? g.me * 8 : (g.me & ~31) * 8 + g.lane;
+    first = VEC ? g.me * 8 : (g.me & ~31) * 8 + (sizeof(T) == 4 ? g.lane : 0);   // (16 bits: the warp's first)
     step = g.threads * 8;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -89,9 +88,9 @@ template <bool VEC, int K> struct Columns {
 };
 
 template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool valid) {
-  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the last `ahead` (0 or 1) groups have arrived.
@@ -102,77 +101,124 @@ __device__ __forceinline__ void copies_wait(int ahead) {
 }
 
 // A warp's rows of one operand: asked for, and taken in the same order.
+constexpr int kSpanWords = 132;          // 256 elements of 16 bits from the middle of a word on, and to 16 bytes
 template <typename T, bool VEC, int K>
 struct Feed {
-  static constexpr bool kCopies = VEC || sizeof(T) == 4;
-  enum : int { kHalves = sizeof(T) / 2, kStage = K * 256 * sizeof(T) };   // 16-byte vectors of an eight; bytes of a warp's columns
-  char* s;               // the warp's stages; without copies the place where eights are made
-  typename Bits<T>::U w[kCopies ? 1 : K][8];
+  enum : int {
+    kHalves = sizeof(T) / 2,             // 16-byte vectors of an eight
+    kSpan = !VEC && sizeof(T) == 2 ? kSpanWords * 4 : 256 * (int)sizeof(T),
+    kStage = K * kSpan                   // bytes of a warp's columns
+  };
+  char* s;               // the warp's stages
   __device__ __forceinline__ explicit Feed(char* stages) : s(stages) {}
-  // at: the row, from the thread's first column on; `any` may be read
-  __device__ __forceinline__ void ask(int stage, const T* at, const T* any, const Columns<VEC, K>& c, bool valid, int lane) {
+  // at: the row, from the thread's first column on; `any` is aligned to what is copied at a time
+  __device__ __forceinline__ void ask(int stage, const T* at, const void* any, const Columns<T, VEC, K>& c, bool valid, int lane) {
+    char* to = s + stage * kStage;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (VEC) {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           const bool ok = valid && c.n[k] > 4 * h;
-          copy_async<16>(s + stage * kStage + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 4 * h : any, ok);
+          copy_async<16>(to + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 4 * h : any, ok ? 16 : 0);
         }
-      } else if constexpr (kCopies) {
+      } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const bool ok = valid && 32 * j < c.n[k];
-          copy_async<4>(s + stage * kStage + (k * 256 + 32 * j + lane) * 4, ok ? at + k * c.step + 32 * j : any, ok);
+          copy_async<4>(to + (k * 256 + 32 * j + lane) * 4, ok ? at + k * c.step + 32 * j : any, ok ? 4 : 0);
         }
       } else {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(at + k * c.step);
+        const int odd = (int)(p >> 1 & 1);
+        const char* words = reinterpret_cast<const char*>(p & ~(uintptr_t)3);
+        const int left = valid ? c.n[k] + odd : 0;       // elements from the first word on
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[k][j] = valid && 32 * j < c.n[k] ? reinterpret_cast<const typename Bits<T>::U*>(at)[k * c.step + 32 * j] : 0;
+        for (int j = 0; j < 5; ++j) {
+          const int i = 32 * j + lane;
+          const int bytes = max(0, min(4, 2 * (left - 2 * i)));
+          if (j < 4 || lane == 0) copy_async<4>(to + k * kSpan + 4 * i, bytes ? words + 4 * i : any, bytes);
+        }
       }
     }
   }
-  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], int lane) {
+  // odd: the row starts in the middle of a word (16-bit rows at any address)
+  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], bool odd, int lane) {
+    const char* from = s + stage * kStage;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (VEC) {
-        const uint4* q = reinterpret_cast<const uint4*>(s + stage * kStage) + k * kHalves * 32 + lane;
+        const uint4* q = reinterpret_cast<const uint4*>(from) + k * kHalves * 32 + lane;
         e[k].q = q[0];
         if constexpr (kHalves == 2) e[k].r = q[32];
-      } else if constexpr (kCopies) {
-        e[k] = load_eight<true>(reinterpret_cast<const T*>(s + stage * kStage) + k * 256 + 8 * lane, 8);
+      } else if constexpr (sizeof(T) == 4) {
+        e[k] = load_eight<true>(reinterpret_cast<const T*>(from) + k * 256 + 8 * lane, 8);
       } else {
-        typename Bits<T>::U* turn = reinterpret_cast<typename Bits<T>::U*>(s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) turn[32 * j + lane] = w[k][j];
-        __syncwarp();
-        e[k] = load_eight<true>(reinterpret_cast<const T*>(s) + 8 * lane, 8);
-        __syncwarp();
+        const unsigned* w = reinterpret_cast<const unsigned*>(from + k * kSpan) + 4 * lane;
+        uint4 q = *reinterpret_cast<const uint4*>(w);
+        if (odd) {
+          const unsigned next = w[4];
+          q = make_uint4(__funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16), __funnelshift_r(q.z, q.w, 16),
+                         __funnelshift_r(q.w, next, 16));
+        }
+        e[k].q = q;
       }
     }
-    if constexpr (kCopies) __syncwarp();                 // the stage may be written again
+    __syncwarp();                                        // the stage may be written again
+  }
+  // Whether row r of rows at p, stride elements apart, starts in the middle of a word.
+  static __device__ __forceinline__ bool odd_row(const T* p, unsigned r, long long stride) {
+    return !VEC && sizeof(T) == 2 && (((unsigned)(reinterpret_cast<uintptr_t>(p) >> 1) ^ (r & (unsigned)stride)) & 1);
+  }
+  static __device__ __forceinline__ const void* aligned(const T* p) {
+    return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
   }
 };
 // Bytes of a warp's stages, and of the place where its outputs turn into rows.
 template <typename T, bool VEC, int K>
-__host__ __device__ constexpr int feed_bytes(int stages) {
-  return VEC || sizeof(T) == 4 ? stages * K * 256 * (int)sizeof(T) : 512;
-}
+__host__ __device__ constexpr int feed_bytes(int stages) { return stages * Feed<T, VEC, K>::kStage; }
 template <typename T, bool VEC>
-__host__ __device__ constexpr int turn_bytes() { return VEC ? 0 : 256 * (int)sizeof(T); }
+__host__ __device__ constexpr int turn_bytes() { return VEC ? 0 : sizeof(T) == 2 ? kSpanWords * 4 : 1024; }
+
 template <typename T, bool VEC, int K>
-__device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<VEC, K>& c, int k, bool valid,
-                                              void* warp_kb, int lane) {
+__device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<T, VEC, K>& c, int k, bool valid,
+                                              char* turn, int lane) {
   if constexpr (VEC) {
     if (valid) store_eight<true>(at + k * c.step, v, c.n[k]);
-  } else {
-    using U = typename Bits<T>::U;
-    store_eight<true>(static_cast<T*>(warp_kb) + 8 * lane, v, 8);
+  } else if constexpr (sizeof(T) == 4) {
+    float* s = reinterpret_cast<float*>(turn);
+    store_eight<true>(s + 8 * lane, v, 8);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (valid && 32 * j < c.n[k])
-        reinterpret_cast<U*>(at)[k * c.step + 32 * j] = static_cast<const U*>(warp_kb)[32 * j + lane];
+      if (valid && 32 * j < c.n[k]) at[k * c.step + 32 * j] = s[32 * j + lane];
+    __syncwarp();
+  } else {
+    // the span's words: at an odd element each holds the element before its own first
+    unsigned* s = reinterpret_cast<unsigned*>(turn);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(at + k * c.step);
+    const int odd = (int)(p >> 1 & 1);
+    uint4 q = make_uint4(pack_two<T>(v[0], v[1]), pack_two<T>(v[2], v[3]), pack_two<T>(v[4], v[5]), pack_two<T>(v[6], v[7]));
+    if (odd) {
+      const unsigned before = __shfl_up_sync(0xffffffffu, q.w, 1);
+      if (lane == 31) s[128] = q.w >> 16;
+      q = make_uint4(__funnelshift_r(before, q.x, 16), __funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16),
+                     __funnelshift_r(q.z, q.w, 16));
+    }
+    *reinterpret_cast<uint4*>(s + 4 * lane) = q;
+    __syncwarp();
+    char* words = reinterpret_cast<char*>(p & ~(uintptr_t)3);
+    const int end = valid ? min(256, c.n[k]) + odd : 0;   // halves of words from `odd` on
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const int i = 32 * j + lane;
+      if (j == 4 && lane > 0) break;
+      const bool low = 2 * i < end && 2 * i >= odd, high = 2 * i + 1 < end;
+      unsigned short* h = reinterpret_cast<unsigned short*>(words + 4 * i);
+      if (low && high) *reinterpret_cast<unsigned*>(h) = s[i];
+      else if (low) h[0] = (unsigned short)s[i];
+      else if (high) h[1] = (unsigned short)(s[i] >> 16);
+    }
     __syncwarp();
   }
 }
@@ -245,13 +291,13 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;   // all of the thread's columns are there
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
-  const Columns<VEC, K> c(g, cols);
+  const Columns<T, VEC, K> c(g, cols);
   unsigned r = blockIdx.x * g.count + g.index, asked = r;
   const T* from = x + r * x_stride + c.first;
   T* to = out + (long long)r * cols + c.first;
   Feed<T, VEC, K> feed(mine);
   for (int i = 0; i < stages; ++i, asked += step, from += step * x_stride) {
-    feed.ask(i, from, x, c, asked < rows, g.lane);
+    feed.ask(i, from, feed.aligned(x), c, asked < rows, g.lane);
     copies_commit();
   }
   int stage = 0;
@@ -259,8 +305,8 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   for (unsigned first = blockIdx.x * g.count; first < rows; first += step, r += step, to += (long long)step * cols) {
     Eight<T> e[K];
     copies_wait(stages - 1);
-    feed.take(stage, e, g.lane);
-    feed.ask(stage, from, x, c, asked < rows, g.lane);
+    feed.take(stage, e, feed.odd_row(x, r, x_stride), g.lane);
+    feed.ask(stage, from, feed.aligned(x), c, asked < rows, g.lane);
     copies_commit();
     asked += step;
     from += step * x_stride;
@@ -327,7 +373,7 @@ __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
 layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, unsigned rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
                        float* part, int log2_threads, int stages) {
-  __shared__ float2 s_sums[2][32];
+  __shared__ __align__(16) Two s_sums[2][32];
   extern __shared__ __align__(16) char s_dynamic[];
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
   dep_wait();
@@ -347,7 +393,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
-  const Columns<VEC, K> c(g, cols);
+  const Columns<T, VEC, K> c(g, cols);
   unsigned r = blockIdx.x * g.count + g.index, asked = r;
   const T* from_x = x + r * x_stride + c.first;
   const T* from_grad = grad + r * grad_stride + c.first;
@@ -355,8 +401,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   Feed<T, VEC, K> feed_x(mine_x), feed_grad(mine_x + feed_bytes<T, VEC, K>(stages));
   char* turn = mine_x + 2 * feed_bytes<T, VEC, K>(stages);
   auto ask = [&](int stage) {
-    feed_x.ask(stage, from_x, x, c, asked < rows, g.lane);
-    feed_grad.ask(stage, from_grad, grad, c, asked < rows, g.lane);
+    feed_x.ask(stage, from_x, feed_x.aligned(x), c, asked < rows, g.lane);
+    feed_grad.ask(stage, from_grad, feed_grad.aligned(grad), c, asked < rows, g.lane);
     copies_commit();
     asked += step;
     from_x += step * x_stride;
@@ -369,8 +415,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
        first += step, r += step, parity ^= 1, to += (long long)step * cols) {
     Eight<T> cx[K], cg[K];
     copies_wait(stages - 1);
-    feed_x.take(stage, cx, g.lane);
-    feed_grad.take(stage, cg, g.lane);
+    feed_x.take(stage, cx, feed_x.odd_row(x, r, x_stride), g.lane);
+    feed_grad.take(stage, cg, feed_grad.odd_row(grad, r, grad_stride), g.lane);
     ask(stage);
     stage = stage + 1 == stages ? 0 : stage + 1;
     const Two minus_mean = twice(-nm), rstd2 = twice(nr);
@@ -400,20 +446,28 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       t1[0] = add(t1[0], t1[K - 1]);
       t2[0] = add(t2[0], t2[K - 1]);
     }
-    float one = warp_pt(lanes(t1[0])), two = warp_pt(lanes(t2[0]));
+    Two sums = two(lanes(t1[0]), lanes(t2[0]));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+      sums = add(sums, two(__shfl_xor_sync(0xffffffffu, sums.x, d), __shfl_xor_sync(0xffffffffu, sums.y, d)));
     if (g.warps > 1) {
-      if (g.lane == 0) s_sums[parity][g.warp] = make_float2(one, two);
+      if (g.lane == 0) s_sums[parity][g.warp] = sums;
       __syncthreads();
-      const float2 q = s_sums[parity][g.first_warp + (g.lane & (g.warps - 1))];
-      one = q.x;
-      two = q.y;
-      for (int s = 1; s < g.warps; s <<= 1) {
-        one += __shfl_xor_sync(0xffffffffu, one, s);
-        two += __shfl_xor_sync(0xffffffffu, two, s);
+      if (g.warps == 8) {              // the same tree, without shuffles
+        const float4* q = reinterpret_cast<const float4*>(&s_sums[parity][g.first_warp]);
+        Two t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = add(two(q[i].x, q[i].y), two(q[i].z, q[i].w));
+        sums = add(add(t[0], t[1]), add(t[2], t[3]));
+      } else {
+        sums = s_sums[parity][g.first_warp + (g.lane & (g.warps - 1))];
+        for (int d = 1; d < g.warps; d <<= 1)
+          sums = add(sums, two(__shfl_xor_sync(0xffffffffu, sums.x, d), __shfl_xor_sync(0xffffffffu, sums.y, d)));
       }
     }
     if (grad_x) {
-      const Two minus_one = twice(-one * of), minus_two = twice(-two * of);
+      // rstd (gw - sums.x / cols) - (x - mean) rstd^2 sums.y / cols
+      const Two minus_one = twice(-sums.x * of * rstd2.x), minus_two = twice(-sums.y * of * rstd2.x * rstd2.x);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Two xh[4], d[4], w[4];
@@ -423,9 +477,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          xh[i] = mul(add(xh[i], minus_mean), rstd2);
-          d[i] = fma(xh[i], minus_two, fma(d[i], w[i], minus_one));
-          const float2 f = (mul(d[i], rstd2));
+          const float2 f = fma(add(xh[i], minus_mean), minus_two, fma(mul(d[i], w[i]), rstd2, minus_one));
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
         }
@@ -483,21 +535,20 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
   if (lane == 0 && of < cols) store_from_f32(to, of, total, param_dtype);
 }
 
-// Eights of columns a thread takes, and the threads that take a row, as a logarithm.
-// In 16 bits two eights keep a row's sums over lanes and warps short; in 32 one, because
-// two would need more registers than leave two CTAs on an SM.
-int eights(int64_t cols, int dtype) { return cols > (dtype == DET_F32 ? 8192 : 256) ? 2 : 1; }
-int row_threads(int64_t cols, int dtype) {
+// Eights of columns a thread takes (two keep a row's sums over lanes and warps short), and
+// the threads that take a row, as a logarithm.
+int eights(int64_t cols) { return cols > 256 ? 2 : 1; }
+int row_threads(int64_t cols) {
   int l = 5;
-  while ((8LL * eights(cols, dtype) << l) < cols) ++l;
+  while ((8LL * eights(cols) << l) < cols) ++l;
   return l;
 }
 // CTAs of the gradient, each of which leaves a partial sum: as many as run at once on
 // the 152 SMs, by a constant, because the sums' order hangs on it.
-int grad_parts(int64_t rows, int64_t cols, int dtype) {
-  const int l = row_threads(cols, dtype);
+int grad_parts(int64_t rows, int64_t cols) {
+  const int l = row_threads(cols);
   const int64_t at_a_time = std::max<int64_t>(1, kThreads >> l);
-  const int at_once = 152 * (l > 8 ? 1 : eights(cols, dtype) == 1 ? 3 : 2);
+  const int at_once = 152 * (l > 8 ? 1 : eights(cols) == 1 ? 3 : 2);
   return (int)std::min<int64_t>((rows + at_a_time - 1) / at_a_time, at_once);
 }
 
@@ -511,7 +562,7 @@ bool vectors(const void* p, int64_t stride, int64_t cols) {
 template <typename T, bool VEC, int K>
 size_t room(int params, int operands, int log2_threads, int threads, int* stages) {
   size_t bytes = 0;
-  for (*stages = VEC || sizeof(T) == 4 ? 2 : 1; *stages > 0; --*stages) {
+  for (*stages = 2; *stages > 0; --*stages) {
     bytes = ((size_t)params * K * 32 << log2_threads) +
             threads / 32 * (size_t)(operands * feed_bytes<T, VEC, K>(*stages) + turn_bytes<T, VEC>());
     if (bytes <= 226 * 1024 || *stages == 1) break;
@@ -521,8 +572,8 @@ size_t room(int params, int operands, int log2_threads, int threads, int* stages
 
 template <typename T, int K, bool VEC, int MOST>
 int forward(const void* x, int rows, int cols, int64_t x_stride, const void* weight, const void* bias, int param_dtype,
-            float eps, void* out, float* mean_out, float* rstd_out, int dtype, cudaStream_t s) {
-  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+            float eps, void* out, float* mean_out, float* rstd_out, cudaStream_t s) {
+  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
   auto* k = layer_norm_kernel<T, K, VEC, MOST>;
   int stages = 1;
   const size_t smem = room<T, VEC, K>(MOST == 256 ? 0 : 2, 1, l, threads, &stages);
@@ -543,8 +594,8 @@ int forward(const void* x, int rows, int cols, int64_t x_stride, const void* wei
 template <typename T, int K, bool VEC, int MOST>
 int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int rows, int cols,
              const float* mean, const float* rstd, const void* weight, int param_dtype, void* grad_x, float* part,
-             int dtype, cudaStream_t s) {
-  const int l = row_threads(cols, dtype), threads = std::max(kThreads, 1 << l);
+             cudaStream_t s) {
+  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l);
   auto* k = layer_norm_grad_kernel<T, K, VEC, MOST>;
   int stages = 1;
   // weight and rows; the groups' sums take their place at the end
@@ -553,7 +604,7 @@ int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_str
   const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm_backward");
   launch_begin("det_layer_norm_backward", s);
-  const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols, dtype)), dim3(threads), smem, s,
+  const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols)), dim3(threads), smem, s,
                                    static_cast<const T*>(grad), (long long)grad_stride, static_cast<const T*>(x),
                                    (long long)x_stride, (unsigned)rows, cols, mean, rstd, weight, param_dtype,
                                    static_cast<T*>(grad_x), part, l, stages);
@@ -575,37 +626,30 @@ bool misaligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p
 using namespace det;
 
 // The kernels for eights() and row_threads().
-#define DET_NORM_PICK_16(fn, T, ...)                                                                     \
+#define DET_NORM_PICK_T(fn, T, ...)                                                                     \
   do {                                                                                                   \
     if (cols <= 256) return vec ? fn<T, 1, true, 256>(__VA_ARGS__) : fn<T, 1, false, 256>(__VA_ARGS__);  \
     if (cols <= 4096) return vec ? fn<T, 2, true, 256>(__VA_ARGS__) : fn<T, 2, false, 256>(__VA_ARGS__); \
     if (cols <= 8192) return vec ? fn<T, 2, true, 512>(__VA_ARGS__) : fn<T, 2, false, 512>(__VA_ARGS__); \
     return vec ? fn<T, 2, true, 1024>(__VA_ARGS__) : fn<T, 2, false, 1024>(__VA_ARGS__);                 \
   } while (0)
-#define DET_NORM_PICK_32(fn, ...)                                                                                \
-  do {                                                                                                           \
-    if (cols <= 2048) return vec ? fn<float, 1, true, 256>(__VA_ARGS__) : fn<float, 1, false, 256>(__VA_ARGS__); \
-    if (cols <= 4096) return vec ? fn<float, 1, true, 512>(__VA_ARGS__) : fn<float, 1, false, 512>(__VA_ARGS__); \
-    if (cols <= 8192) return vec ? fn<float, 1, true, 1024>(__VA_ARGS__) : fn<float, 1, false, 1024>(__VA_ARGS__); \
-    return vec ? fn<float, 2, true, 1024>(__VA_ARGS__) : fn<float, 2, false, 1024>(__VA_ARGS__);                 \
-  } while (0)
 #define DET_NORM_PICK(fn, ...)                                                 \
   do {                                                                         \
-    if (dtype == DET_F32) DET_NORM_PICK_32(fn, __VA_ARGS__);                   \
-    if (dtype == DET_BF16) DET_NORM_PICK_16(fn, __nv_bfloat16, __VA_ARGS__);   \
-    DET_NORM_PICK_16(fn, __half, __VA_ARGS__);                                 \
+    if (dtype == DET_F32) DET_NORM_PICK_T(fn, float, __VA_ARGS__);                   \
+    if (dtype == DET_BF16) DET_NORM_PICK_T(fn, __nv_bfloat16, __VA_ARGS__);   \
+    DET_NORM_PICK_T(fn, __half, __VA_ARGS__);                                 \
   } while (0)
 
 static int norm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
                         const void* bias, int param_dtype, float eps, void* out, float* mean_out, float* rstd_out,
                         bool vec, cudaStream_t s) {
-  DET_NORM_PICK(forward, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, dtype, s);
+  DET_NORM_PICK(forward, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, s);
 }
 static int norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype, int64_t rows,
                          int64_t cols, const float* mean, const float* rstd, const void* weight, int param_dtype,
                          void* grad_x, float* part, bool vec, cudaStream_t s) {
   DET_NORM_PICK(backward, grad, grad_stride, x, x_stride, (int)rows, (int)cols, mean, rstd, weight, param_dtype, grad_x,
-                part, dtype, s);
+                part, s);
 }
 
 extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride,
@@ -626,8 +670,7 @@ extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t co
 
 extern "C" size_t det_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (check_rows(DET_F32, DET_F32, rows, cols) != DET_OK || rows == 0) return 256;
-  const int parts = std::max(grad_parts(rows, cols, DET_F32), grad_parts(rows, cols, DET_BF16));
-  return 256 + align_up((size_t)parts * 2 * (size_t)cols * sizeof(float), 256);
+  return 256 + align_up((size_t)grad_parts(rows, cols) * 2 * (size_t)cols * sizeof(float), 256);
 }
 
 extern "C" int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype,
@@ -659,7 +702,7 @@ extern "C" int det_layer_norm_backward(const void* grad, int64_t grad_stride, co
   if (!params) return DET_OK;
   launch_begin("det_layer_norm_join", s);
   const cudaError_t e = launch_dep(layer_norm_join_kernel, dim3((unsigned)((cols + 31) / 32), 2), dim3(1024), 0, s,
-                                   (const float*)part, rows > 0 ? grad_parts(rows, cols, dtype) : 0, (int)cols, grad_weight,
+                                   (const float*)part, rows > 0 ? grad_parts(rows, cols) : 0, (int)cols, grad_weight,
                                    grad_bias, param_dtype);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm_join");

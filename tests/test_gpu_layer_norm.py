@@ -70,18 +70,17 @@ def check_forward(r, x, w, b, eps):
           + smallest(x.dtype), "out")
 
 
-def column_depth(rows, cols, dtype):
+def column_depth(rows, cols):
     """Additions on a column's way: a register's, the groups of a CTA, a strand of the join and its tree."""
-    eights = 2 if cols > (8192 if dtype == torch.float32 else 256) else 1
+    eights = 2 if cols > 256 else 1
     threads = max(32, 1 << max(0, math.ceil(math.log2(cols / (8 * eights)))))
     at_a_time = max(1, 256 // threads)
-    parts = max(1, min(-(-rows // at_a_time), 152 * (1 if threads > 256 else 3)))
+    parts = max(1, min(-(-rows // at_a_time), 152 * (1 if threads > 256 else 3 if eights == 1 else 2)))
     return -(-rows // (parts * at_a_time)) + at_a_time + -(-parts // 32) + 6
 
 
 def check_backward(r, g, x, mean, rstd, w, param_dtype):
     rows, cols = x.shape
-    x_dtype = x.dtype
     g, x, m, s = g.double(), x.double(), mean.double()[:, None], rstd.double()[:, None]
     wd = torch.ones(cols).double() if w is None else w.double()
     xh = (x - m) * s
@@ -96,7 +95,7 @@ def check_backward(r, g, x, mean, rstd, w, param_dtype):
         tol = s * (e_one + xh.abs() * e_two + (e_xh * two.abs()) + 6 * U * big) * 1.01
         dt = r.x.dtype
         close(r.x, want, tol + half_step(dt) * want.abs() * 1.01 + smallest(dt), "x")
-    depth = column_depth(rows, cols, x_dtype)
+    depth = column_depth(rows, cols)
     for got, terms in ((r.weight, g * xh), (r.bias, g)):
         if got is not None:
             want = terms.sum(0)
