@@ -75,14 +75,19 @@ struct Group {
 // of its eights there are.
 template <typename T, bool VEC, int K> struct Columns {
   int first, step;       // step: from one eight to the next
-  int n[K];              // VEC: columns; else columns of the row from the first one on
+  int read;              // the first column that the thread copies: in 32 bits vectors lie lane after lane
+  int n[K];              // VEC: columns of the thread's eights; else columns of the row from the first one on
+  int span[K];           // columns of the row from the first one that it copies on
   __device__ __forceinline__ Columns(const Group& g, int cols) {
-    first = VEC ? g.me * 8 : (g.me & ~31) * 8 + (sizeof(T) == 4 ? g.lane : 0);   // (16 bits: the warp's first)
+    const int warp = (g.me & ~31) * 8;                   // the warp's first
+    first = VEC ? g.me * 8 : sizeof(T) == 4 ? warp + g.lane : warp;
+    read = VEC && sizeof(T) == 4 ? warp + 4 * g.lane : first;
     step = g.threads * 8;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       n[k] = cols - first - k * step;
       if (VEC) n[k] = max(0, min(8, n[k]));
+      span[k] = cols - read - k * step;
     }
   }
 };
@@ -111,16 +116,17 @@ struct Feed {
   };
   char* s;               // the warp's stages
   __device__ __forceinline__ explicit Feed(char* stages) : s(stages) {}
-  // at: the row, from the thread's first column on; `any` is aligned to what is copied at a time
+  // at: the row, from the first column that the thread copies on; `any` is aligned to what is copied at a time
   __device__ __forceinline__ void ask(int stage, const T* at, const void* any, const Columns<T, VEC, K>& c, bool valid, int lane) {
     char* to = s + stage * kStage;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (VEC) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          const bool ok = valid && c.n[k] > 4 * h;
-          copy_async<16>(to + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 4 * h : any, ok ? 16 : 0);
+        for (int h = 0; h < kHalves; ++h) {              // (in 32 bits: vector v of the span to place v / 2 of the odd or even ones)
+          const bool ok = valid && c.span[k] > 128 * h;
+          const int place = kHalves == 1 ? lane : 32 * (lane & 1) + 16 * h + (lane >> 1);
+          copy_async<16>(to + (k * kHalves * 32 + place) * 16, ok ? at + k * c.step + 128 * h : any, ok ? 16 : 0);
         }
       } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -133,6 +139,12 @@ struct Feed {
         const int odd = (int)(p >> 1 & 1);
         const char* words = reinterpret_cast<const char*>(p & ~(uintptr_t)3);
         const int left = valid ? c.n[k] + odd : 0;       // elements from the first word on
+        if (left >= 258) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) copy_async<4>(to + k * kSpan + 4 * (32 * j + lane), words + 4 * (32 * j + lane), 4);
+          if (odd && lane == 0) copy_async<4>(to + k * kSpan + 512, words + 512, 4);
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < 5; ++j) {
           const int i = 32 * j + lane;
@@ -184,6 +196,12 @@ template <typename T, bool VEC, int K>
 __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<T, VEC, K>& c, int k, bool valid,
                                               char* turn, int lane) {
   if constexpr (VEC) {
+    if constexpr (sizeof(T) == 4) {
+      if (valid && c.n[k] == 8 && reinterpret_cast<uintptr_t>(at) % 32 == 0) {
+        st_256(at + k * c.step, v);                      // whole sectors
+        return;
+      }
+    }
     if (valid) store_eight<true>(at + k * c.step, v, c.n[k]);
   } else if constexpr (sizeof(T) == 4) {
     float* s = reinterpret_cast<float*>(turn);
@@ -209,6 +227,19 @@ __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const 
     __syncwarp();
     char* words = reinterpret_cast<char*>(p & ~(uintptr_t)3);
     const int end = valid ? min(256, c.n[k]) + odd : 0;   // halves of words from `odd` on
+    if (end >= 256 + odd) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 32 * j + lane;
+        if (j > 0 || lane >= odd) *reinterpret_cast<unsigned*>(words + 4 * i) = s[i];
+      }
+      if (odd && lane == 0) {
+        *reinterpret_cast<unsigned short*>(words + 2) = (unsigned short)(s[0] >> 16);
+        *reinterpret_cast<unsigned short*>(words + 512) = (unsigned short)s[128];
+      }
+      __syncwarp();
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < 5; ++j) {
       const int i = 32 * j + lane;
@@ -293,7 +324,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   const float of = 1.0f / (float)cols;
   const Columns<T, VEC, K> c(g, cols);
   unsigned r = blockIdx.x * g.count + g.index, asked = r;
-  const T* from = x + r * x_stride + c.first;
+  const T* from = x + r * x_stride + c.read;
   T* to = out + (long long)r * cols + c.first;
   Feed<T, VEC, K> feed(mine);
   for (int i = 0; i < stages; ++i, asked += step, from += step * x_stride) {
@@ -395,8 +426,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   const float of = 1.0f / (float)cols;
   const Columns<T, VEC, K> c(g, cols);
   unsigned r = blockIdx.x * g.count + g.index, asked = r;
-  const T* from_x = x + r * x_stride + c.first;
-  const T* from_grad = grad + r * grad_stride + c.first;
+  const T* from_x = x + r * x_stride + c.read;
+  const T* from_grad = grad + r * grad_stride + c.read;
   T* to = grad_x + (long long)r * cols + c.first;
   Feed<T, VEC, K> feed_x(mine_x), feed_grad(mine_x + feed_bytes<T, VEC, K>(stages));
   char* turn = mine_x + 2 * feed_bytes<T, VEC, K>(stages);
