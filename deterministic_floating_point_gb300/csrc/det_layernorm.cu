@@ -123,10 +123,9 @@ struct Feed {
     for (int k = 0; k < K; ++k) {
       if constexpr (VEC) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {              // (in 32 bits: vector v of the span to place v / 2 of the odd or even ones)
+        for (int h = 0; h < kHalves; ++h) {              // (a warp's copies go to one place after the other, or take longer)
           const bool ok = valid && c.span[k] > 128 * h;
-          const int place = kHalves == 1 ? lane : 32 * (lane & 1) + 16 * h + (lane >> 1);
-          copy_async<16>(to + (k * kHalves * 32 + place) * 16, ok ? at + k * c.step + 128 * h : any, ok ? 16 : 0);
+          copy_async<16>(to + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 128 * h : any, ok ? 16 : 0);
         }
       } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -160,9 +159,9 @@ struct Feed {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (VEC) {
-        const uint4* q = reinterpret_cast<const uint4*>(from) + k * kHalves * 32 + lane;
+        const uint4* q = reinterpret_cast<const uint4*>(from) + kHalves * (k * 32 + lane);
         e[k].q = q[0];
-        if constexpr (kHalves == 2) e[k].r = q[32];
+        if constexpr (kHalves == 2) e[k].r = q[1];
       } else if constexpr (sizeof(T) == 4) {
         e[k] = load_eight<true>(reinterpret_cast<const T*>(from) + k * 256 + 8 * lane, 8);
       } else {
