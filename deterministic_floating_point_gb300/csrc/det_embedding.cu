@@ -3,10 +3,12 @@
 // The gradient is the row scatter-add of det_scatter_add_rows on tokens, for
 // 16-bit inputs too and without its slow case, a destination that many rows
 // aim at (the most frequent token of a text is met in every twentieth place):
-//   1. the tokens are sorted stably (payload: the position);
-//   2. every run of one token is cut into blocks of 32 by rank; a warp reduces
-//      256 columns of every block that begins among its positions of the sorted
-//      order, streaming through them eight rows at a time whatever runs they
+//   1. the positions are sorted by token, stably.  Up to 16,384 of them one CTA
+//      sorts in its shared memory, in two passes of 9 bits; the other SMs clear the
+//      table meanwhile.  (More: the library's sort, after a clear.)
+//   2. every run of one token is cut into blocks of 32 by rank; a warp reduces a
+//      slice of the columns of every block that begins among its positions of the
+//      sorted order, streaming through them eight rows at a time whatever runs they
 //      belong to, and writes the row (or for a run of more than a block the block's
 //      node);
 //   3. the nodes of long runs are joined, eight warps a run and 64 columns.
@@ -35,6 +37,20 @@ embedding_kernel(const T* table, int vocab, int dim, long long stride, const int
   const int token = tokens[i];
   const bool known = (unsigned)token < (unsigned)vocab;
   const T* row = table + (known ? token * stride : 0);
+  if constexpr (!VEC) {
+    // element after element across the row's threads
+    constexpr int N = 8;
+    const int end = min(dim, (int)(blockIdx.y + 1) * threads * kEights * 8);
+    for (int c = blockIdx.y * threads * kEights * 8 + me; c < end; c += N * threads) {
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = known && c + j * threads < end ? to_f32(row[c + j * threads]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c + j * threads < end) out[i * dim + c + j * threads] = from_f32<O>(known ? __fmul_rn(v[j], scale) : 0.0f);
+    }
+    return;
+  }
   const int c0 = (blockIdx.y * threads * kEights + me) * 8;
   Eight<T> e[kEights];
 #pragma unroll
@@ -54,24 +70,193 @@ embedding_kernel(const T* table, int vocab, int dim, long long stride, const int
 }
 
 // ---------------------------------------------------------------------------
-// gradient
+// gradient: positions by token
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSortPer = 16;                                       // most positions a thread
+constexpr int kSortMost = kSortThreads * kSortPer, kPositionBits = 14;
+constexpr int kSortVocab = 1 << (2 * kDigitBits);
+static_assert(kSortMost == 1 << kPositionBits && kPositionBits + 2 * kDigitBits == 32, "a record is a word");
+
+struct SortArgs {
+  const int32_t* tokens;
+  int n, vocab, per;             // per: positions a thread
+  int32_t *perm, *run_start, *run_end;
+  unsigned *n_valid, *long_runs;
+  char* table;                   // to be cleared, or NULL
+  long long bytes;
+};
+
+struct SortShared {
+  unsigned short warp_digits[kSortWarps][kDigits];
+  unsigned start[kDigits];       // of the digits' records
+  unsigned scan[kSortWarps];
+  unsigned total;
+  unsigned pad_[3];
+  // then two orders of the records (token above position)
+};
+
+// A stable pass over the records, which lie in the order of warps, steps and lanes, by
+// the digit of their tokens at `shift`.
+__device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned (&record)[kSortPer], unsigned valid,
+                                          int shift, unsigned* to) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned short* mine = s.warp_digits[warp];
+  for (int d = lane; d < kDigits / 2; d += 32) reinterpret_cast<unsigned*>(mine)[d] = 0;
+  __syncwarp();
+  unsigned in_warp[kSortPer];
+#pragma unroll
+  for (int k = 0; k < kSortPer; ++k) {
+    if (k >= per) break;
+    const bool ok = valid >> k & 1;
+    const unsigned digit = ok ? record[k] >> (kPositionBits + shift) & (kDigits - 1) : kDigits;
+    const unsigned same = __match_any_sync(0xffffffffu, digit);
+    const unsigned ahead = __popc(same & ((1u << lane) - 1));
+    in_warp[k] = ok ? mine[digit] + ahead : 0;
+    __syncwarp();
+    if (ok && ahead == 0) mine[digit] += (unsigned short)__popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // a digit a thread: over the warps
+  unsigned all = 0;
+  if (threadIdx.x < kDigits) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const unsigned c = s.warp_digits[w][threadIdx.x];
+      s.warp_digits[w][threadIdx.x] = (unsigned short)all;
+      all += c;
+    }
+  }
+  // over the digits
+  unsigned scan = all;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned v = __shfl_up_sync(0xffffffffu, scan, d);
+    if (lane >= d) scan += v;
+  }
+  if (lane == 31) s.scan[warp] = scan;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned v = s.scan[lane];
+    const unsigned own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += u;
+    }
+    s.scan[lane] = v - own;
+    if (lane == 31) s.total = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < kDigits) s.start[threadIdx.x] = s.scan[warp] + scan - all;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortPer; ++k) {
+    if (k >= per) break;
+    if (!(valid >> k & 1)) continue;
+    const unsigned digit = record[k] >> (kPositionBits + shift) & (kDigits - 1);
+    to[s.start[digit] + mine[digit] + in_warp[k]] = record[k];
+  }
+  __syncthreads();
+}
+
+// The first CTA sorts; the others clear the table.
+__global__ void __launch_bounds__(kSortThreads, 1)
+embedding_sort_kernel(SortArgs a) {
+  extern __shared__ __align__(16) char s_raw[];
+  dep_wait();
+  dep_launch();
+  if (blockIdx.x > 0) {
+    const float zero[8] = {};
+    char* const lo = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.table) + 31) & ~(uintptr_t)31);
+    char* const hi = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(a.table + a.bytes) & ~(uintptr_t)31);
+    const long long thread = (long long)(blockIdx.x - 1) * kSortThreads + threadIdx.x;
+    const long long threads = (long long)(gridDim.x - 1) * kSortThreads;
+    if (hi <= lo) {
+      for (long long i = thread; i < a.bytes; i += threads) a.table[i] = 0;
+      return;
+    }
+    if (thread < 32 && a.table + thread < lo) a.table[thread] = 0;
+    if (thread < 32 && hi + thread < a.table + a.bytes) hi[thread] = 0;
+    for (char* p = lo + thread * 32; p < hi; p += threads * 32) st_256(reinterpret_cast<float*>(p), zero);
+    return;
+  }
+  SortShared& s = *reinterpret_cast<SortShared*>(s_raw);
+  unsigned* order = reinterpret_cast<unsigned*>(s_raw + sizeof(SortShared));
+  const int per = a.per, size = per * kSortThreads;
+  const int first = (threadIdx.x >> 5) * 32 * per + (threadIdx.x & 31);
+  unsigned record[kSortPer], valid = 0;
+#pragma unroll
+  for (int k = 0; k < kSortPer; ++k) {
+    const int i = first + 32 * k;
+    const int token = k < per && i < a.n ? a.tokens[i] : -1;
+    if ((unsigned)token < (unsigned)a.vocab) valid |= 1u << k;
+    record[k] = (unsigned)token << kPositionBits | (unsigned)i;
+  }
+  sort_pass(s, per, record, valid, 0, order);
+  const int total = (int)s.total;
+  valid = 0;
+#pragma unroll
+  for (int k = 0; k < kSortPer; ++k) {
+    const int q = first + 32 * k;
+    if (k < per && q < total) {
+      valid |= 1u << k;
+      record[k] = order[q];
+    }
+  }
+  unsigned* sorted = order + size;
+  sort_pass(s, per, record, valid, kDigitBits, sorted);
+  // the order, and where runs begin and end in it
+  for (int q = threadIdx.x; q < total; q += kSortThreads) {
+    const unsigned t = sorted[q] >> kPositionBits;
+    a.perm[q] = (int32_t)(sorted[q] & (kSortMost - 1));
+    if (q == 0 || sorted[q - 1] >> kPositionBits != t) a.run_start[t] = q;
+    if (q + 1 == total || sorted[q + 1] >> kPositionBits != t) a.run_end[t] = q + 1;
+  }
+  if (threadIdx.x == 0) {
+    *a.n_valid = (unsigned)total;
+    *a.long_runs = 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradient: sums
 
 constexpr int kBlock = 32;       // ranks of a block
-constexpr int kRound = 8;        // rows in flight
-constexpr int kSlice = 256;      // columns of a warp
+constexpr int kAhead = 16, kGroup = 4;   // rows on their way to a warp, and how many are asked for at a time
+// columns of a lane, a 16-byte vector, and of a warp
+template <typename T> constexpr int kCols = 16 / sizeof(T);
+template <typename T> constexpr int kSlice = 32 * kCols<T>;
 
 // A run of more than one block, for the join.
 struct LongRun {
   int token, start, end;
 };
 
-// The workspace after the sort's.
+// The workspace: that of the library's sort, or a header and the order and runs of the
+// CTA's; then long runs and nodes.
 struct EmbedPlan {
-  size_t runs, nodes, total;
+  bool one_cta;
+  SortPlan sort;
+  size_t perm, run_start, run_end, runs, nodes, total;
 };
-EmbedPlan embed_plan(const SortPlan& sort, long long n, long long dim) {
+EmbedPlan embed_plan(long long n, long long vocab, long long dim) {
   EmbedPlan p;
-  p.runs = align_up(sort.total, 256);
+  p.one_cta = n <= kSortMost && vocab <= kSortVocab;
+  size_t at;
+  if (p.one_cta) {
+    p.perm = kHeaderBytes;
+    p.run_start = align_up(p.perm + (size_t)n * 4, 256);
+    p.run_end = align_up(p.run_start + (size_t)vocab * 4, 256);
+    at = p.run_end + (size_t)vocab * 4;
+  } else {
+    p.sort = make_sort_plan(n, vocab, 0, true, 0);
+    p.perm = p.run_start = p.run_end = 0;
+    at = p.sort.total;
+  }
+  p.runs = align_up(at, 256);
   p.nodes = align_up(p.runs + (size_t)(n / kBlock + 1) * sizeof(LongRun), 256);
   // a window of 32 sorted positions holds at most two beginnings of a long run's blocks: of one that ends
   // in it or passes it, and of one that starts in it (two blocks of one run begin 32 positions apart,
@@ -85,7 +270,7 @@ __host__ __device__ inline long long node_slot(long long q, bool first) { return
 struct GradArgs {
   const int32_t* tokens;
   const int32_t* perm;           // positions in the order of their tokens
-  const int32_t* seg;            // where a token's run starts in it
+  const int32_t *run_start, *run_end;   // a token's run in it; of tokens that occur
   const unsigned* n_valid;
   unsigned* long_runs;           // how many
   LongRun* runs;
@@ -101,10 +286,89 @@ __device__ __forceinline__ float finish(float sum, float scale, const O* old, bo
   return accumulate ? __fadd_rn(to_f32(*old), v) : v;
 }
 
+// A lane's columns of a row: 16 bytes of T.  VEC: aligned, and all or none of them.
+template <typename T> struct Vec16 { uint4 q; };
+template <bool VEC, typename T>
+__device__ __forceinline__ Vec16<T> load_vec(const T* p, int n) {
+  Vec16<T> v;
+  v.q = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (n > 0) v.q = *reinterpret_cast<const uint4*>(p);
+  } else if constexpr (sizeof(T) == 4) {
+    const unsigned* u = reinterpret_cast<const unsigned*>(p);
+    if (n > 0) v.q.x = u[0];
+    if (n > 1) v.q.y = u[1];
+    if (n > 2) v.q.z = u[2];
+    if (n > 3) v.q.w = u[3];
+  } else {
+    v.q = load_eight<false>(p, n).q;
+  }
+  return v;
+}
+__device__ __forceinline__ void pairs_of(const Vec16<float>& e, Two (&v)[2]) {
+  v[0] = two(__uint_as_float(e.q.x), __uint_as_float(e.q.y));
+  v[1] = two(__uint_as_float(e.q.z), __uint_as_float(e.q.w));
+}
+// n of a lane's columns at p to its place in shared memory, the others 0: asynchronously
+// where all are there and aligned; `any` is aligned.
+template <bool VEC, typename T>
+__device__ __forceinline__ void copy_row(uint4* to, const T* p, const T* any, int n) {
+  if constexpr (VEC) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(n > 0 ? p : any), "r"(n > 0 ? 16 : 0)
+                 : "memory");
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to) + 4 * i), "l"(i < n ? p + i : any),
+                   "r"(i < n ? 4 : 0)
+                   : "memory");
+  } else {
+    *to = load_vec<false>(p, n).q;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Vec16<T>& e, Two (&v)[4]) {
+  const unsigned w[4] = {e.q.x, e.q.y, e.q.z, e.q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack_two(w[i], v[i].x, v[i].y, T());
+}
+template <int N> __device__ __forceinline__ void set(Two (&to)[N], const Two (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) to[i] = v[i];
+}
+template <int N> __device__ __forceinline__ void join(Two (&v)[N], const Two (&node)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = add(node[i], v[i]);
+}
+// The first n of N columns.
+template <bool VEC, typename O, int N>
+__device__ __forceinline__ void load_cols(float (&v)[N], const O* p, int n) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+}
+template <bool VEC, typename O, int N>
+__device__ __forceinline__ void store_cols(O* p, const float (&v)[N], int n) {
+  if (VEC && n == N) {
+    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else if constexpr (N == 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_two<O>(v[0], v[1]), pack_two<O>(v[2], v[3]), pack_two<O>(v[4], v[5]),
+                                                pack_two<O>(v[6], v[7]));
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_two<O>(v[0], v[1]), pack_two<O>(v[2], v[3]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = from_f32<O>(v[i]);
+  }
+}
+
 // A warp: the blocks that begin at sorted positions [w * window, (w + 1) *
-// window), columns blockIdx.y * 256 and on.
+// window), columns blockIdx.y * kSlice and on.
 template <typename T, typename O, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int window) {
   dep_wait();
   dep_launch();
@@ -123,8 +387,8 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
     in = in && (unsigned)from[h] < (unsigned)a.n;      // what follows an unfinished sort (its waits are bounded)
     token[h] = in ? a.tokens[from[h]] : 0;
     in = in && (unsigned)token[h] < (unsigned)a.vocab; // is left out
-    run0[h] = in ? a.seg[token[h]] : 0;
-    run1[h] = in ? a.seg[token[h] + 1] : 0;
+    run0[h] = in ? a.run_start[token[h]] : 0;
+    run1[h] = in ? a.run_end[token[h]] : 0;
     in = in && run0[h] >= 0 && run0[h] <= q && q < run1[h] && run1[h] <= valid;
     const int rank = (int)q - run0[h];
     begins[h] = __ballot_sync(0xffffffffu, in && rank % kBlock == 0);
@@ -134,56 +398,57 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   const unsigned long long end = ends[0] | (unsigned long long)ends[1] << 32;
   const unsigned long long here = begin & ((window == 32 ? 0xffffffffull : (1ull << window) - 1));
   if (here == 0) return;
-  const int c = blockIdx.y * kSlice + lane * 8;
-  const int nc = max(0, min(8, a.dim - c));
+  constexpr int COLS = kCols<T>, PAIRS = COLS / 2;
+  const int c = blockIdx.y * kSlice<T> + lane * COLS;
+  const int nc = max(0, min(COLS, a.dim - c));
   const int p0 = __ffsll((long long)here) - 1;
   // the last block that begins here ends at the first end behind its beginning
   const int last = 63 - __clzll((long long)here);
   const int p1 = __ffsll((long long)(end >> last << last)) - 1;
   if (p1 < 0) return;
-  float st[5][8];                // pending nodes of a block's tree: 1, 2, 4, 8, 16 rows
-  int rank = 0;
-  for (int p = p0; p <= p1; p += kRound) {
-    Eight<T> e[kRound];
+  // rows come through the warp's ring, kAhead before their turn, in groups of kGroup; a lane
+  // reads what it has copied itself.  (Eight rows in registers, unrolled, ran from the
+  // instruction cache at a quarter of the schedulers' rate.)
+  __shared__ __align__(16) uint4 s_rows[256 / 32][kAhead][32];
+  uint4(*rows)[32] = s_rows[threadIdx.x >> 5];
+  auto ask = [&](int p) {
 #pragma unroll
-    for (int j = 0; j < kRound; ++j) {
+    for (int j = 0; j < kGroup; ++j) {
       const int q = p + j;
       const int f = __shfl_sync(0xffffffffu, q < 32 ? from[0] : from[1], q & 31);
-      e[j] = load_eight<VEC>(grad + f * a.stride + c, q <= p1 ? nc : 0);
+      copy_row<VEC>(&rows[q & (kAhead - 1)][lane], grad + f * a.stride + c, grad, q <= p1 ? nc : 0);
     }
-#pragma unroll
-    for (int j = 0; j < kRound; ++j) {
-      const int q = p + j;
-      if (q > p1) break;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int g = 0; g < kAhead / kGroup; ++g) ask(p0 + g * kGroup);
+  Two st[5][PAIRS];              // pending nodes of a block's tree: 1, 2, 4, 8, 16 rows
+  int rank = 0;
+  for (int p = p0; p <= p1; p += kGroup) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / kGroup - 1) : "memory");
+#pragma unroll 1
+    for (int q = p; q < p + kGroup && q <= p1; ++q) {
       if (begin >> q & 1) rank = 0;
-      float v[8];
-      unpack_eight(e[j], v);
+      Two v[PAIRS];
+      pairs_of(Vec16<T>{rows[q & (kAhead - 1)][lane]}, v);
       // a binary counter: the new leaf is added to the pending node of each level it completes
-      int level = 0;
-#pragma unroll
-      for (int l = 0; l < 5; ++l) {
-        if (level == l && (rank >> l & 1)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = st[l][i] + v[i];
-          level = l + 1;
-        }
+      switch (__ffs(~rank) - 1) {
+        case 0: set(st[0], v); break;
+        case 1: join(v, st[0]); set(st[1], v); break;
+        case 2: join(v, st[0]); join(v, st[1]); set(st[2], v); break;
+        case 3: join(v, st[0]); join(v, st[1]); join(v, st[2]); set(st[3], v); break;
+        case 4: join(v, st[0]); join(v, st[1]); join(v, st[2]); join(v, st[3]); set(st[4], v); break;
+        default: join(v, st[0]); join(v, st[1]); join(v, st[2]); join(v, st[3]); join(v, st[4]);
       }
-#pragma unroll
-      for (int l = 0; l < 5; ++l)
-        if (level == l) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) st[l][i] = v[i];
-        }
       ++rank;
       if (!(end >> q & 1)) continue;
-      // the block's node: the pending ones from the smallest up
-      if (rank < kBlock) {
+      // the block's node: the pending ones from the smallest up (a full block's, and a leaf alone, are there)
+      if (rank > 1 && rank < kBlock) {
         bool have = false;
 #pragma unroll
         for (int l = 0; l < 5; ++l)
           if (rank >> l & 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = have ? st[l][i] + v[i] : st[l][i];
+            if (have) join(v, st[l]);
+            else set(v, st[l]);
             have = true;
           }
       }
@@ -191,30 +456,32 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       const int lo = __shfl_sync(0xffffffffu, q < 32 ? run0[0] : run0[1], src);
       const int hi = __shfl_sync(0xffffffffu, q < 32 ? run1[0] : run1[1], src);
       const int tok = __shfl_sync(0xffffffffu, q < 32 ? token[0] : token[1], src);
+      float sum[COLS];
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) sum[2 * i] = v[i].x, sum[2 * i + 1] = v[i].y;
       if (hi - lo <= kBlock) {
         O* to = out + (long long)tok * a.dim + c;
         if (accumulate) {
-          float old[8];
-          unpack_eight(load_eight<VEC>(to, nc), old);
+          float old[COLS];
+          load_cols<VEC>(old, to, nc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(old[i], __fmul_rn(v[i], a.scale));
+          for (int i = 0; i < COLS; ++i) sum[i] = __fadd_rn(old[i], __fmul_rn(sum[i], a.scale));
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], a.scale);
+          for (int i = 0; i < COLS; ++i) sum[i] = __fmul_rn(sum[i], a.scale);
         }
-        store_eight<VEC>(to, v, nc);
+        store_cols<VEC>(to, sum, nc);
       } else {
         const long long start = w0 + q - (rank - 1);
         float* to = a.nodes + node_slot(start, start == lo) * a.dim + c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < nc) to[i] = v[i];
+        store_cols<VEC>(to, sum, nc);
         if (start == lo && blockIdx.y == 0 && lane == 0) {
           const unsigned k = atomicAdd(a.long_runs, 1u);       // in any order: runs do not meet
           if (k <= (unsigned)(a.n / kBlock)) a.runs[k] = {tok, lo, hi};
         }
       }
     }
+    ask(p + kAhead);
   }
 }
 
@@ -298,8 +565,9 @@ int forward(const void* table, int vocab, int dim, int64_t stride, const int32_t
 
 template <typename T, typename O>
 int blocks(const void* grad, const GradArgs& a, int n, void* out, int accumulate, cudaStream_t s) {
+  // vectors where every row of every operand starts on 16 bytes (rows of nodes do in the workspace then)
   const bool vec = vectors<T>(grad, a.stride) && vectors<O>(out, a.dim) && a.dim * sizeof(T) % 16 == 0;
-  const unsigned slices = (unsigned)((a.dim + kSlice - 1) / kSlice);
+  const unsigned slices = (unsigned)((a.dim + kSlice<T> - 1) / kSlice<T>);
   // windows of 32 positions, shorter ones while they leave SMs without a warp
   int window = 32;
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
@@ -321,6 +589,31 @@ int join(const GradArgs& a, int n, void* out, int accumulate, cudaStream_t s) {
                                    static_cast<O*>(out), accumulate);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_join");
+}
+
+int cta_sort(const GradArgs& a, int n, int vocab, void* table, size_t bytes, cudaStream_t s) {
+  SortArgs g;
+  g.tokens = a.tokens;
+  g.n = n;
+  g.vocab = vocab;
+  g.per = (n + kSortThreads - 1) / kSortThreads;
+  g.perm = const_cast<int32_t*>(a.perm);
+  g.run_start = const_cast<int32_t*>(a.run_start);
+  g.run_end = const_cast<int32_t*>(a.run_end);
+  g.n_valid = const_cast<unsigned*>(a.n_valid);
+  g.long_runs = a.long_runs;
+  g.table = static_cast<char*>(table);
+  g.bytes = (long long)bytes;
+  const cudaError_t se = ensure_dyn_smem((const void*)embedding_sort_kernel, sizeof(SortShared) + (size_t)2 * kSortMost * 4);
+  if (se != cudaSuccess) return cuda_fail(se, "det_embedding_sort");
+  // CTAs that clear: one on each other SM, fewer for small tables
+  const long long clear =
+      table ? std::min<long long>(std::max(device_sm_count() - 1, 1), (long long)(bytes / (kSortThreads * 32)) + 1) : 0;
+  launch_begin("det_embedding_sort", s);
+  const cudaError_t e = launch_dep(embedding_sort_kernel, dim3((unsigned)(1 + clear)), dim3(kSortThreads),
+                                   sizeof(SortShared) + (size_t)2 * g.per * kSortThreads * 4, s, g);
+  launch_end(s);
+  return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_sort");
 }
 
 int check_table(int dtype, int table_dtype, int64_t n, int64_t vocab, int64_t dim) {
@@ -367,7 +660,7 @@ extern "C" int det_embedding(const void* table, int table_dtype, int64_t vocab, 
 
 extern "C" size_t det_embedding_backward_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
   if (check_table(DET_F32, DET_F32, n, vocab, dim) != DET_OK) return 0;
-  return embed_plan(make_sort_plan(n, vocab, 0, true, 0), n, dim).total;
+  return embed_plan(n, vocab, dim).total;
 }
 
 extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, int64_t dim, int64_t grad_stride,
@@ -380,24 +673,33 @@ extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, in
   if (!grad_table || (n > 0 && (!grad || !tokens))) return DET_ERR_INVALID_ARG;
   if (misaligned(grad, dtype) || misaligned(grad_table, table_dtype) || misaligned(tokens, DET_F32))
     return DET_ERR_INVALID_ARG;
-  const SortPlan sort = make_sort_plan(n, vocab, 0, true, 0);
-  const EmbedPlan plan = embed_plan(sort, n, dim);
+  const EmbedPlan plan = embed_plan(n, vocab, dim);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < plan.total) return DET_ERR_WORKSPACE;
   const cudaStream_t s = as_stream(stream);
-  if (!accumulate) {
-    const cudaError_t e = cudaMemsetAsync(grad_table, 0, (size_t)vocab * dim * model_elem_size(table_dtype), s);
+  const size_t table_bytes = (size_t)vocab * dim * model_elem_size(table_dtype);
+  if (!accumulate && (n == 0 || !plan.one_cta)) {
+    const cudaError_t e = cudaMemsetAsync(grad_table, 0, table_bytes, s);
     if (e != cudaSuccess) return cuda_fail(e, "det_embedding_backward: clear");
   }
   if (n == 0) return DET_OK;
-  int buffer = 0;
-  if (const int rc = enqueue_sort(sort, workspace, tokens, 0, nullptr, nullptr, s, &buffer)) return rc;
   char* w = static_cast<char*>(workspace);
+  SortHdr* header = reinterpret_cast<SortHdr*>(w);
   GradArgs a;
   a.tokens = tokens;
-  a.perm = reinterpret_cast<const int32_t*>(w + sort.idx[buffer]);
-  a.seg = reinterpret_cast<const int32_t*>(w + sort.seg);
-  a.n_valid = &reinterpret_cast<SortHdr*>(w)->n_valid;
-  a.long_runs = &reinterpret_cast<SortHdr*>(w)->long_segs;       // cleared by the sort, which does not use it
+  a.n_valid = &header->n_valid;
+  a.long_runs = &header->long_segs;                              // cleared by either sort, neither of which uses it
+  if (plan.one_cta) {
+    a.perm = reinterpret_cast<int32_t*>(w + plan.perm);
+    a.run_start = reinterpret_cast<int32_t*>(w + plan.run_start);
+    a.run_end = reinterpret_cast<int32_t*>(w + plan.run_end);
+    if (const int rc = cta_sort(a, (int)n, (int)vocab, accumulate ? nullptr : grad_table, table_bytes, s)) return rc;
+  } else {
+    int buffer = 0;
+    if (const int rc = enqueue_sort(plan.sort, workspace, tokens, 0, nullptr, nullptr, s, &buffer)) return rc;
+    a.perm = reinterpret_cast<const int32_t*>(w + plan.sort.idx[buffer]);
+    a.run_start = reinterpret_cast<const int32_t*>(w + plan.sort.seg);
+    a.run_end = a.run_start + 1;
+  }
   a.runs = reinterpret_cast<LongRun*>(w + plan.runs);
   a.nodes = reinterpret_cast<float*>(w + plan.nodes);
   a.n = (int)n;
