@@ -3,9 +3,11 @@
 // The gradient is the row scatter-add of det_scatter_add_rows on tokens, for
 // 16-bit inputs too and without its slow case, a destination that many rows
 // aim at (the most frequent token of a text is met in every twentieth place):
-//   1. the positions are sorted by token, stably.  Up to 16,384 of them one CTA
-//      sorts in its shared memory, in two passes of 9 bits; the other SMs clear the
-//      table meanwhile.  (More: the library's sort, after a clear.)
+//   1. the positions are put in the order of their tokens, stably.  Up to 16,384 of
+//      them 8 CTAs do so for an eighth of the tokens each (those with the same low
+//      bits), in shared memory, in two passes of 8 bits, and without a word to each
+//      other; the other SMs clear the table meanwhile.  (More: the library's sort,
+//      after a clear.)
 //   2. every run of one token is cut into blocks of 32 by rank; a warp reduces a
 //      slice of the columns of every block that begins among its positions of the
 //      sorted order, streaming through them eight rows at a time whatever runs they
@@ -73,11 +75,12 @@ embedding_kernel(const T* table, int vocab, int dim, long long stride, const int
 // gradient: positions by token
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kClassBits = 3, kClasses = 1 << kClassBits;          // CTAs: tokens by their low bits
+constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;           // of what is left of a token
 constexpr int kSortPer = 16;                                       // most positions a thread
 constexpr int kSortMost = kSortThreads * kSortPer, kPositionBits = 14;
-constexpr int kSortVocab = 1 << (2 * kDigitBits);
-static_assert(kSortMost == 1 << kPositionBits && kPositionBits + 2 * kDigitBits == 32, "a record is a word");
+constexpr int kSortVocab = 1 << (2 * kDigitBits + kClassBits - 1); // (31 bits of a record are used)
+static_assert(kSortMost == 1 << kPositionBits && kPositionBits + 2 * kDigitBits <= 32, "a record is a word");
 
 struct SortArgs {
   const int32_t* tokens;
@@ -91,9 +94,9 @@ struct SortArgs {
 struct SortShared {
   unsigned short warp_digits[kSortWarps][kDigits];
   unsigned start[kDigits];       // of the digits' records
-  unsigned scan[kSortWarps];
-  unsigned total;
-  unsigned pad_[3];
+  unsigned scan[kSortWarps], below[kSortWarps];
+  unsigned total, total_below;
+  unsigned pad_[2];
   // then two orders of the records (token above position)
 };
 
@@ -110,12 +113,19 @@ __device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned
   for (int k = 0; k < kSortPer; ++k) {
     if (k >= per) break;
     const bool ok = valid >> k & 1;
-    const unsigned digit = ok ? record[k] >> (kPositionBits + shift) & (kDigits - 1) : kDigits;
-    const unsigned same = __match_any_sync(0xffffffffu, digit);
+    const unsigned digit = record[k] >> (kPositionBits + shift) & (kDigits - 1);
+    // the lanes with the same digit, bit by bit
+    unsigned same = __ballot_sync(0xffffffffu, ok);
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+      const unsigned ones = __ballot_sync(0xffffffffu, digit >> b & 1);
+      same &= digit >> b & 1 ? ones : ~ones;
+    }
     const unsigned ahead = __popc(same & ((1u << lane) - 1));
-    in_warp[k] = ok ? mine[digit] + ahead : 0;
+    const unsigned before = ok ? mine[digit] : 0;
+    in_warp[k] = before + ahead;
     __syncwarp();
-    if (ok && ahead == 0) mine[digit] += (unsigned short)__popc(same);
+    if (ok && ahead == 0) mine[digit] = (unsigned short)(before + __popc(same));
     __syncwarp();
   }
   __syncthreads();
@@ -162,18 +172,18 @@ __device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned
   __syncthreads();
 }
 
-// The first CTA sorts; the others clear the table.
+// The first CTAs sort a class of tokens each; the others clear the table.
 __global__ void __launch_bounds__(kSortThreads, 1)
 embedding_sort_kernel(SortArgs a) {
   extern __shared__ __align__(16) char s_raw[];
   dep_wait();
   dep_launch();
-  if (blockIdx.x > 0) {
+  if (blockIdx.x >= kClasses) {
     const float zero[8] = {};
     char* const lo = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.table) + 31) & ~(uintptr_t)31);
     char* const hi = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(a.table + a.bytes) & ~(uintptr_t)31);
-    const long long thread = (long long)(blockIdx.x - 1) * kSortThreads + threadIdx.x;
-    const long long threads = (long long)(gridDim.x - 1) * kSortThreads;
+    const long long thread = (long long)(blockIdx.x - kClasses) * kSortThreads + threadIdx.x;
+    const long long threads = (long long)(gridDim.x - kClasses) * kSortThreads;
     if (hi <= lo) {
       for (long long i = thread; i < a.bytes; i += threads) a.table[i] = 0;
       return;
@@ -185,38 +195,79 @@ embedding_sort_kernel(SortArgs a) {
   }
   SortShared& s = *reinterpret_cast<SortShared*>(s_raw);
   unsigned* order = reinterpret_cast<unsigned*>(s_raw + sizeof(SortShared));
-  const int per = a.per, size = per * kSortThreads;
-  const int first = (threadIdx.x >> 5) * 32 * per + (threadIdx.x & 31);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, size = a.per * kSortThreads;
   unsigned record[kSortPer], valid = 0;
+  {
+    // the class' records in the order of their positions, and how many records lower classes have
+    const int first = warp * 32 * a.per + lane;
+    unsigned mine = 0, below = 0;
 #pragma unroll
-  for (int k = 0; k < kSortPer; ++k) {
-    const int i = first + 32 * k;
-    const int token = k < per && i < a.n ? a.tokens[i] : -1;
-    if ((unsigned)token < (unsigned)a.vocab) valid |= 1u << k;
-    record[k] = (unsigned)token << kPositionBits | (unsigned)i;
-  }
-  sort_pass(s, per, record, valid, 0, order);
-  const int total = (int)s.total;
-  valid = 0;
-#pragma unroll
-  for (int k = 0; k < kSortPer; ++k) {
-    const int q = first + 32 * k;
-    if (k < per && q < total) {
-      valid |= 1u << k;
-      record[k] = order[q];
+    for (int k = 0; k < kSortPer; ++k) {
+      const int i = first + 32 * k;
+      const int token = k < a.per && i < a.n ? a.tokens[i] : -1;
+      record[k] = (unsigned)token >> kClassBits << kPositionBits | (unsigned)i;
+      const bool known = (unsigned)token < (unsigned)a.vocab;
+      if (known && (token & (kClasses - 1)) == (int)blockIdx.x) valid |= 1u << k;
+      mine += __popc(__ballot_sync(0xffffffffu, valid >> k & 1));
+      below += __popc(__ballot_sync(0xffffffffu, known && (token & (kClasses - 1)) < (int)blockIdx.x));
     }
+    if (lane == 0) {
+      s.scan[warp] = mine;
+      s.below[warp] = below;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      unsigned v = s.scan[lane], u = s.below[lane];
+      const unsigned own = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += up;
+        u += __shfl_xor_sync(0xffffffffu, u, d);
+      }
+      s.scan[lane] = v - own;
+      if (lane == 31) {
+        s.total = v;
+        s.total_below = u;
+      }
+    }
+    __syncthreads();
+    unsigned at = s.scan[warp];
+#pragma unroll
+    for (int k = 0; k < kSortPer; ++k) {
+      const unsigned ok = __ballot_sync(0xffffffffu, valid >> k & 1);
+      if (valid >> k & 1) order[at + __popc(ok & ((1u << lane) - 1))] = record[k];
+      at += __popc(ok);
+    }
+    __syncthreads();
   }
-  unsigned* sorted = order + size;
-  sort_pass(s, per, record, valid, kDigitBits, sorted);
+  const int total = (int)s.total, base = (int)s.total_below;
+  const int per = (total + kSortThreads - 1) / kSortThreads, first = warp * 32 * per + lane;
+  auto load = [&](const unsigned* from) {
+    valid = 0;
+#pragma unroll
+    for (int k = 0; k < kSortPer; ++k) {
+      const int q = first + 32 * k;
+      if (k < per && q < total) {
+        valid |= 1u << k;
+        record[k] = from[q];
+      }
+    }
+  };
+  load(order);
+  sort_pass(s, per, record, valid, 0, order + size);
+  load(order + size);
+  sort_pass(s, per, record, valid, kDigitBits, order);
   // the order, and where runs begin and end in it
   for (int q = threadIdx.x; q < total; q += kSortThreads) {
-    const unsigned t = sorted[q] >> kPositionBits;
-    a.perm[q] = (int32_t)(sorted[q] & (kSortMost - 1));
-    if (q == 0 || sorted[q - 1] >> kPositionBits != t) a.run_start[t] = q;
-    if (q + 1 == total || sorted[q + 1] >> kPositionBits != t) a.run_end[t] = q + 1;
+    const unsigned t = order[q] >> kPositionBits;
+    const int token = (int)(t << kClassBits | blockIdx.x);
+    a.perm[base + q] = (int32_t)(order[q] & (kSortMost - 1));
+    if (q == 0 || order[q - 1] >> kPositionBits != t) a.run_start[token] = base + q;
+    if (q + 1 == total || order[q + 1] >> kPositionBits != t) a.run_end[token] = base + q + 1;
   }
-  if (threadIdx.x == 0) {
-    *a.n_valid = (unsigned)total;
+  if (threadIdx.x == 0 && blockIdx.x == kClasses - 1) {
+    *a.n_valid = (unsigned)(base + total);
     *a.long_runs = 0;
   }
 }
@@ -228,6 +279,7 @@ constexpr int kBlock = 32;       // ranks of a block
 constexpr int kAhead = 16, kGroup = 4;   // rows on their way to a warp, and how many are asked for at a time
 // columns of a lane, a 16-byte vector, and of a warp
 template <typename T> constexpr int kCols = 16 / sizeof(T);
+
 template <typename T> constexpr int kSlice = 32 * kCols<T>;
 
 // A run of more than one block, for the join.
@@ -332,41 +384,41 @@ __device__ __forceinline__ void pairs_of(const Vec16<T>& e, Two (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack_two(w[i], v[i].x, v[i].y, T());
 }
-template <int N> __device__ __forceinline__ void set(Two (&to)[N], const Two (&v)[N]) {
+// to = node + v, the earlier one on the left
+template <int N> __device__ __forceinline__ void join(const Two (&v)[N], const Two (&node)[N], Two (&to)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) to[i] = v[i];
+  for (int i = 0; i < N; ++i) to[i] = add(node[i], v[i]);
 }
-template <int N> __device__ __forceinline__ void join(Two (&v)[N], const Two (&node)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = add(node[i], v[i]);
-}
-// The first n of N columns.
+// The first n of 2 P columns.
 template <bool VEC, typename O, int N>
 __device__ __forceinline__ void load_cols(float (&v)[N], const O* p, int n) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
 }
-template <bool VEC, typename O, int N>
-__device__ __forceinline__ void store_cols(O* p, const float (&v)[N], int n) {
-  if (VEC && n == N) {
+template <bool VEC, typename O, int P>
+__device__ __forceinline__ void store_cols(O* p, const Two (&v)[P], int n) {
+  if (VEC && n == 2 * P) {
     if constexpr (sizeof(O) == 4) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else if constexpr (N == 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_two<O>(v[0], v[1]), pack_two<O>(v[2], v[3]), pack_two<O>(v[4], v[5]),
-                                                pack_two<O>(v[6], v[7]));
+      for (int i = 0; i < P; i += 2) *reinterpret_cast<float4*>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+    } else if constexpr (P == 4) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_two<O>(v[0].x, v[0].y), pack_two<O>(v[1].x, v[1].y),
+                                                pack_two<O>(v[2].x, v[2].y), pack_two<O>(v[3].x, v[3].y));
     } else {
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack_two<O>(v[0], v[1]), pack_two<O>(v[2], v[3]));
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_two<O>(v[0].x, v[0].y), pack_two<O>(v[1].x, v[1].y));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = from_f32<O>(v[i]);
+    for (int i = 0; i < P; ++i) {
+      if (2 * i < n) p[2 * i] = from_f32<O>(v[i].x);
+      if (2 * i + 1 < n) p[2 * i + 1] = from_f32<O>(v[i].y);
+    }
   }
 }
 
 // A warp: the blocks that begin at sorted positions [w * window, (w + 1) *
 // window), columns blockIdx.y * kSlice and on.
+constexpr int kEnd = 32, kLong = 64, kFirst = 128;     // of a position: it ends its block, its run is long, its block is the run's first
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(256, 3)
 embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int window) {
@@ -377,23 +429,28 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   const long long w0 = ((long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * window;
   if (w0 >= valid) return;
   // 64 positions from w0 on, two a lane: what they hold, and where blocks begin and end
-  int from[2], token[2], run0[2], run1[2];
+  __shared__ int4 s_meta[256 / 32][64];          // position, token, rank in its block and flags
+  int4* meta = s_meta[threadIdx.x >> 5];
   unsigned begins[2], ends[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const long long q = w0 + h * 32 + lane;
     bool in = q < valid;
-    from[h] = in ? a.perm[q] : 0;
-    in = in && (unsigned)from[h] < (unsigned)a.n;      // what follows an unfinished sort (its waits are bounded)
-    token[h] = in ? a.tokens[from[h]] : 0;
-    in = in && (unsigned)token[h] < (unsigned)a.vocab; // is left out
-    run0[h] = in ? a.run_start[token[h]] : 0;
-    run1[h] = in ? a.run_end[token[h]] : 0;
-    in = in && run0[h] >= 0 && run0[h] <= q && q < run1[h] && run1[h] <= valid;
-    const int rank = (int)q - run0[h];
-    begins[h] = __ballot_sync(0xffffffffu, in && rank % kBlock == 0);
-    ends[h] = __ballot_sync(0xffffffffu, in && (rank % kBlock == kBlock - 1 || q + 1 == run1[h]));
+    const int from = in ? a.perm[q] : 0;
+    in = in && (unsigned)from < (unsigned)a.n;         // what follows an unfinished sort (its waits are bounded)
+    const int token = in ? a.tokens[from] : 0;
+    in = in && (unsigned)token < (unsigned)a.vocab;    // is left out
+    const int lo = in ? a.run_start[token] : 0;
+    const int hi = in ? a.run_end[token] : 0;
+    in = in && lo >= 0 && lo <= q && q < hi && hi <= valid;
+    const int rank = (int)q - lo;
+    const bool begin = in && rank % kBlock == 0, end = in && (rank % kBlock == kBlock - 1 || q + 1 == hi);
+    begins[h] = __ballot_sync(0xffffffffu, begin);
+    ends[h] = __ballot_sync(0xffffffffu, end);
+    meta[h * 32 + lane] = make_int4(in ? from : 0, token, rank % kBlock | (end ? kEnd : 0) | (hi - lo > kBlock ? kLong : 0) |
+                                                              (rank < kBlock ? kFirst : 0), 0);
   }
+  __syncwarp();
   const unsigned long long begin = begins[0] | (unsigned long long)begins[1] << 32;
   const unsigned long long end = ends[0] | (unsigned long long)ends[1] << 32;
   const unsigned long long here = begin & ((window == 32 ? 0xffffffffull : (1ull << window) - 1));
@@ -409,75 +466,74 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   // rows come through the warp's ring, kAhead before their turn, in groups of kGroup; a lane
   // reads what it has copied itself.  (Eight rows in registers, unrolled, ran from the
   // instruction cache at a quarter of the schedulers' rate.)
-  __shared__ __align__(16) uint4 s_rows[256 / 32][kAhead][32];
-  uint4(*rows)[32] = s_rows[threadIdx.x >> 5];
+  extern __shared__ __align__(16) uint4 s_rows[];        // [warps][kAhead][32]
+  uint4(*rows)[32] = reinterpret_cast<uint4(*)[32]>(s_rows) + (threadIdx.x >> 5) * kAhead;
   auto ask = [&](int p) {
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) {
       const int q = p + j;
-      const int f = __shfl_sync(0xffffffffu, q < 32 ? from[0] : from[1], q & 31);
+      const int f = meta[q & 63].x;
       copy_row<VEC>(&rows[q & (kAhead - 1)][lane], grad + f * a.stride + c, grad, q <= p1 ? nc : 0);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (int g = 0; g < kAhead / kGroup; ++g) ask(p0 + g * kGroup);
   Two st[5][PAIRS];              // pending nodes of a block's tree: 1, 2, 4, 8, 16 rows
-  int rank = 0;
+  const Two scale = twice(a.scale);
   for (int p = p0; p <= p1; p += kGroup) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / kGroup - 1) : "memory");
 #pragma unroll 1
     for (int q = p; q < p + kGroup && q <= p1; ++q) {
-      if (begin >> q & 1) rank = 0;
+      const int4 m = meta[q];
+      const int rank = m.z & (kBlock - 1);
+      const Vec16<T> row{rows[q & (kAhead - 1)][lane]};
+      // a binary counter: the new leaf is added to the pending node of each level it completes.  (The
+      // row is unpacked in each case, where its place is known: values that change places cost more
+      // instructions than the sums.)
       Two v[PAIRS];
-      pairs_of(Vec16<T>{rows[q & (kAhead - 1)][lane]}, v);
-      // a binary counter: the new leaf is added to the pending node of each level it completes
       switch (__ffs(~rank) - 1) {
-        case 0: set(st[0], v); break;
-        case 1: join(v, st[0]); set(st[1], v); break;
-        case 2: join(v, st[0]); join(v, st[1]); set(st[2], v); break;
-        case 3: join(v, st[0]); join(v, st[1]); join(v, st[2]); set(st[3], v); break;
-        case 4: join(v, st[0]); join(v, st[1]); join(v, st[2]); join(v, st[3]); set(st[4], v); break;
-        default: join(v, st[0]); join(v, st[1]); join(v, st[2]); join(v, st[3]); join(v, st[4]);
+        case 0: pairs_of(row, st[0]); break;
+        case 1: pairs_of(row, v); join(v, st[0], st[1]); break;
+        case 2: pairs_of(row, v); join(v, st[0], v); join(v, st[1], st[2]); break;
+        case 3: pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], st[3]); break;
+        case 4: pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], v); join(v, st[3], st[4]); break;
+        default:                     // the whole block's, to the first place
+          pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], v); join(v, st[3], v); join(v, st[4], st[0]);
       }
-      ++rank;
-      if (!(end >> q & 1)) continue;
-      // the block's node: the pending ones from the smallest up (a full block's, and a leaf alone, are there)
-      if (rank > 1 && rank < kBlock) {
-        bool have = false;
+      if (!(m.z & kEnd)) continue;
+      // the block's node: the pending ones from the smallest up
+      const int count = rank + 1 == kBlock ? 1 : rank + 1;
+      bool have = false;
 #pragma unroll
-        for (int l = 0; l < 5; ++l)
-          if (rank >> l & 1) {
-            if (have) join(v, st[l]);
-            else set(v, st[l]);
-            have = true;
+      for (int l = 0; l < 5; ++l)
+        if (count >> l & 1) {
+          if (have) {
+            join(v, st[l], v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) v[i] = st[l][i];
           }
-      }
-      const int src = q & 31;
-      const int lo = __shfl_sync(0xffffffffu, q < 32 ? run0[0] : run0[1], src);
-      const int hi = __shfl_sync(0xffffffffu, q < 32 ? run1[0] : run1[1], src);
-      const int tok = __shfl_sync(0xffffffffu, q < 32 ? token[0] : token[1], src);
-      float sum[COLS];
+          have = true;
+        }
+      const bool whole = !(m.z & kLong);
+      const long long start = w0 + q - rank;
+      O* to = out + (long long)m.y * a.dim + c;
+      float* node = a.nodes + node_slot(start, m.z & kFirst) * a.dim + c;
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) sum[2 * i] = v[i].x, sum[2 * i + 1] = v[i].y;
-      if (hi - lo <= kBlock) {
-        O* to = out + (long long)tok * a.dim + c;
+        for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
         if (accumulate) {
           float old[COLS];
           load_cols<VEC>(old, to, nc);
 #pragma unroll
-          for (int i = 0; i < COLS; ++i) sum[i] = __fadd_rn(old[i], __fmul_rn(sum[i], a.scale));
-        } else {
-#pragma unroll
-          for (int i = 0; i < COLS; ++i) sum[i] = __fmul_rn(sum[i], a.scale);
+          for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);
         }
-        store_cols<VEC>(to, sum, nc);
+        store_cols<VEC>(to, v, nc);
       } else {
-        const long long start = w0 + q - (rank - 1);
-        float* to = a.nodes + node_slot(start, start == lo) * a.dim + c;
-        store_cols<VEC>(to, sum, nc);
-        if (start == lo && blockIdx.y == 0 && lane == 0) {
+        store_cols<VEC>(node, v, nc);
+        if ((m.z & kFirst) && blockIdx.y == 0 && lane == 0) {
           const unsigned k = atomicAdd(a.long_runs, 1u);       // in any order: runs do not meet
-          if (k <= (unsigned)(a.n / kBlock)) a.runs[k] = {tok, lo, hi};
+          if (k <= (unsigned)(a.n / kBlock)) a.runs[k] = {m.y, (int)start, a.run_end[m.y]};
         }
       }
     }
@@ -572,9 +628,12 @@ int blocks(const void* grad, const GradArgs& a, int n, void* out, int accumulate
   int window = 32;
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
   const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 ? 1 : 8;
+  auto* kernel = vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>;
+  const size_t smem = (size_t)per_cta * kAhead * 32 * 16;
+  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kAhead * 32 * 16);
+  if (se != cudaSuccess) return cuda_fail(se, "det_embedding_blocks");
   launch_begin("det_embedding_blocks", s);
-  const cudaError_t e = launch_dep(vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>,
-                                   dim3((warps + per_cta - 1) / per_cta, slices), dim3(32 * per_cta), 0, s,
+  const cudaError_t e = launch_dep(kernel, dim3((warps + per_cta - 1) / per_cta, slices), dim3(32 * per_cta), smem, s,
                                    static_cast<const T*>(grad), a, static_cast<O*>(out), accumulate, window);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_blocks");
@@ -608,9 +667,9 @@ int cta_sort(const GradArgs& a, int n, int vocab, void* table, size_t bytes, cud
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_sort");
   // CTAs that clear: one on each other SM, fewer for small tables
   const long long clear =
-      table ? std::min<long long>(std::max(device_sm_count() - 1, 1), (long long)(bytes / (kSortThreads * 32)) + 1) : 0;
+      table ? std::min<long long>(std::max(device_sm_count() - kClasses, 1), (long long)(bytes / (kSortThreads * 32)) + 1) : 0;
   launch_begin("det_embedding_sort", s);
-  const cudaError_t e = launch_dep(embedding_sort_kernel, dim3((unsigned)(1 + clear)), dim3(kSortThreads),
+  const cudaError_t e = launch_dep(embedding_sort_kernel, dim3((unsigned)(kClasses + clear)), dim3(kSortThreads),
                                    sizeof(SortShared) + (size_t)2 * g.per * kSortThreads * 4, s, g);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_sort");
