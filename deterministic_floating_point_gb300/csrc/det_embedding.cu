@@ -276,7 +276,8 @@ embedding_sort_kernel(SortArgs a) {
 // gradient: sums
 
 constexpr int kBlock = 32;       // ranks of a block
-constexpr int kAhead = 16, kGroup = 4;   // rows on their way to a warp, and how many are asked for at a time
+constexpr int kEight = 8;        // rows that a warp asks for at a time, and of a whole subtree
+constexpr int kStages = 3;       // such groups in shared memory or on their way
 // columns of a lane, a 16-byte vector, and of a warp
 template <typename T> constexpr int kCols = 16 / sizeof(T);
 
@@ -420,7 +421,7 @@ __device__ __forceinline__ void store_cols(O* p, const Two (&v)[P], int n) {
 // window), columns blockIdx.y * kSlice and on.
 constexpr int kEnd = 32, kLong = 64, kFirst = 128;     // of a position: it ends its block, its run is long, its block is the run's first
 template <typename T, typename O, bool VEC>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 2)
 embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int window) {
   dep_wait();
   dep_launch();
@@ -431,7 +432,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   // 64 positions from w0 on, two a lane: what they hold, and where blocks begin and end
   __shared__ int4 s_meta[256 / 32][64];          // position, token, rank in its block and flags
   int4* meta = s_meta[threadIdx.x >> 5];
-  unsigned begins[2], ends[2];
+  unsigned begins[2], ends[2], wholes[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const long long q = w0 + h * 32 + lane;
@@ -447,12 +448,14 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
     const bool begin = in && rank % kBlock == 0, end = in && (rank % kBlock == kBlock - 1 || q + 1 == hi);
     begins[h] = __ballot_sync(0xffffffffu, begin);
     ends[h] = __ballot_sync(0xffffffffu, end);
+    wholes[h] = __ballot_sync(0xffffffffu, in && rank % kEight == 0 && q + kEight <= hi);   // eight rows of one block
     meta[h * 32 + lane] = make_int4(in ? from : 0, token, rank % kBlock | (end ? kEnd : 0) | (hi - lo > kBlock ? kLong : 0) |
                                                               (rank < kBlock ? kFirst : 0), 0);
   }
   __syncwarp();
   const unsigned long long begin = begins[0] | (unsigned long long)begins[1] << 32;
   const unsigned long long end = ends[0] | (unsigned long long)ends[1] << 32;
+  const unsigned long long whole = wholes[0] | (unsigned long long)wholes[1] << 32;
   const unsigned long long here = begin & ((window == 32 ? 0xffffffffull : (1ull << window) - 1));
   if (here == 0) return;
   constexpr int COLS = kCols<T>, PAIRS = COLS / 2;
@@ -463,42 +466,73 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   const int last = 63 - __clzll((long long)here);
   const int p1 = __ffsll((long long)(end >> last << last)) - 1;
   if (p1 < 0) return;
-  // rows come through the warp's ring, kAhead before their turn, in groups of kGroup; a lane
-  // reads what it has copied itself.  (Eight rows in registers, unrolled, ran from the
-  // instruction cache at a quarter of the schedulers' rate.)
-  extern __shared__ __align__(16) uint4 s_rows[];        // [warps][kAhead][32]
-  uint4(*rows)[32] = reinterpret_cast<uint4(*)[32]>(s_rows) + (threadIdx.x >> 5) * kAhead;
-  auto ask = [&](int p) {
+  // rows come through the warp's ring in groups: eight of one block that are a subtree, or up to
+  // eight up to the next such; a lane reads what it has copied itself
+  extern __shared__ __align__(16) uint4 s_rows[];        // [warps][kStages][kEight][32]
+  uint4(*rows)[kEight][32] = reinterpret_cast<uint4(*)[kEight][32]>(s_rows) + (threadIdx.x >> 5) * kStages;
+  auto group = [&](int p) {
+    if (whole >> p & 1) return kEight;
+    const int to_next = (whole >> p) ? __ffsll((long long)(whole >> p)) - 1 : kEight;
+    return min(kEight, min(to_next, p1 + 1 - p));
+  };
+  auto ask = [&](int p, int stage) {
+    if (p <= p1) {
+      const int n = group(p);
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      const int q = p + j;
-      const int f = meta[q & 63].x;
-      copy_row<VEC>(&rows[q & (kAhead - 1)][lane], grad + f * a.stride + c, grad, q <= p1 ? nc : 0);
+      for (int j = 0; j < kEight; ++j)
+        if (j < n) copy_row<VEC>(&rows[stage][j][lane], grad + meta[p + j].x * a.stride + c, grad, nc);
+      p += n;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return p;
   };
-  for (int g = 0; g < kAhead / kGroup; ++g) ask(p0 + g * kGroup);
+  int asked = p0;
+#pragma unroll
+  for (int g = 0; g < kStages; ++g) asked = ask(asked, g);
   Two st[5][PAIRS];              // pending nodes of a block's tree: 1, 2, 4, 8, 16 rows
   const Two scale = twice(a.scale);
-  for (int p = p0; p <= p1; p += kGroup) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / kGroup - 1) : "memory");
-#pragma unroll 1
-    for (int q = p; q < p + kGroup && q <= p1; ++q) {
+  int stage = 0;
+  for (int p = p0; p <= p1;) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    const uint4(*row)[32] = rows[stage];
+    const int n = group(p);
+    const bool eight = whole >> p & 1;
+    for (int q = eight ? p + kEight - 1 : p; q < p + n; ++q) {
       const int4 m = meta[q];
       const int rank = m.z & (kBlock - 1);
-      const Vec16<T> row{rows[q & (kAhead - 1)][lane]};
-      // a binary counter: the new leaf is added to the pending node of each level it completes.  (The
-      // row is unpacked in each case, where its place is known: values that change places cost more
-      // instructions than the sums.)
+      // a binary counter: the new node, a row or eight, is added to the pending node of each level it
+      // completes; the whole block's goes to the first place.  (A row is unpacked in each case, where its place is
+      // known: values that change places cost more instructions than the sums.)
       Two v[PAIRS];
-      switch (__ffs(~rank) - 1) {
-        case 0: pairs_of(row, st[0]); break;
-        case 1: pairs_of(row, v); join(v, st[0], st[1]); break;
-        case 2: pairs_of(row, v); join(v, st[0], v); join(v, st[1], st[2]); break;
-        case 3: pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], st[3]); break;
-        case 4: pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], v); join(v, st[3], st[4]); break;
-        default:                     // the whole block's, to the first place
-          pairs_of(row, v); join(v, st[0], v); join(v, st[1], v); join(v, st[2], v); join(v, st[3], v); join(v, st[4], st[0]);
+      if (eight) {
+        Two x[PAIRS], y[PAIRS];
+        pairs_of(Vec16<T>{row[0][lane]}, x);
+        pairs_of(Vec16<T>{row[1][lane]}, v);
+        join(v, x, x);
+        pairs_of(Vec16<T>{row[2][lane]}, y);
+        pairs_of(Vec16<T>{row[3][lane]}, v);
+        join(v, y, y);
+        join(y, x, x);
+        pairs_of(Vec16<T>{row[4][lane]}, y);
+        pairs_of(Vec16<T>{row[5][lane]}, v);
+        join(v, y, y);
+        Two z[PAIRS];
+        pairs_of(Vec16<T>{row[6][lane]}, z);
+        pairs_of(Vec16<T>{row[7][lane]}, v);
+        join(v, z, z);
+        join(z, y, y);
+        switch (rank / kEight) {
+          case 1: join(y, x, v); join(v, st[3], st[4]); break;
+          case 3: join(y, x, v); join(v, st[3], v); join(v, st[4], st[0]); break;
+          default: join(y, x, st[3]);
+        }
+      } else {
+        const Vec16<T> one{row[q - p][lane]};
+        switch (__ffs(~rank) - 1) {
+          case 0: pairs_of(one, st[0]); break;
+          case 1: pairs_of(one, v); join(v, st[0], st[1]); break;
+          default: pairs_of(one, v); join(v, st[0], v); join(v, st[1], st[2]);      // 2: an eighth row comes with its eight
+        }
       }
       if (!(m.z & kEnd)) continue;
       // the block's node: the pending ones from the smallest up
@@ -515,11 +549,11 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
           }
           have = true;
         }
-      const bool whole = !(m.z & kLong);
+      const bool last_node = !(m.z & kLong);
       const long long start = w0 + q - rank;
       O* to = out + (long long)m.y * a.dim + c;
       float* node = a.nodes + node_slot(start, m.z & kFirst) * a.dim + c;
-      if (whole) {
+      if (last_node) {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
         if (accumulate) {
@@ -537,7 +571,9 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
         }
       }
     }
-    ask(p + kAhead);
+    asked = ask(asked, stage);
+    p += n;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 }
 
@@ -629,8 +665,8 @@ int blocks(const void* grad, const GradArgs& a, int n, void* out, int accumulate
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
   const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 ? 1 : 8;
   auto* kernel = vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>;
-  const size_t smem = (size_t)per_cta * kAhead * 32 * 16;
-  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kAhead * 32 * 16);
+  const size_t smem = (size_t)per_cta * kStages * kEight * 32 * 16;
+  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kStages * kEight * 32 * 16);
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_blocks");
   launch_begin("det_embedding_blocks", s);
   const cudaError_t e = launch_dep(kernel, dim3((warps + per_cta - 1) / per_cta, slices), dim3(32 * per_cta), smem, s,
