@@ -6,13 +6,13 @@
 //   1. the positions are put in the order of their tokens, stably.  Up to 16,384 of
 //      them 8 CTAs do so for an eighth of the tokens each (those with the same low
 //      bits), in shared memory, in two passes of 8 bits, and without a word to each
-//      other; the other SMs clear the table meanwhile.  (More: the library's sort,
-//      after a clear.)
+//      other; the other SMs clear the first 96 MB of the table meanwhile.  (More: the
+//      library's sort, after a clear of all.)
 //   2. every run of one token is cut into blocks of 32 by rank; a warp reduces a
 //      slice of the columns of every block that begins among its positions of the
 //      sorted order, streaming through them eight rows at a time whatever runs they
 //      belong to, and writes the row (or for a run of more than a block the block's
-//      node);
+//      node); CTAs among these clear the rest of the table, but for the rows that others write;
 //   3. the nodes of long runs are joined, eight warps a run and 64 columns.
 // Blocks are subtrees of the canonical pairwise tree over a run's ranks, so the
 // sums are those of det_scatter_add_rows bit for bit.
@@ -331,6 +331,8 @@ struct GradArgs {
   int n, vocab, dim;
   long long stride;
   float scale;
+  int sum_ctas, slices, clear_ctas;   // CTAs that sum (a number of windows each, times slices of the columns) and that clear
+  int clear_from;                     // the first row that is still to be cleared
 };
 
 template <typename O>
@@ -417,17 +419,54 @@ __device__ __forceinline__ void store_cols(O* p, const Two (&v)[P], int n) {
   }
 }
 
+// Rows of a warp that clears.
+constexpr int kClearRows = 16;
+template <typename O>
+__device__ __forceinline__ void clear_rows(O* out, const GradArgs& a, long long warp) {
+  const int lane = threadIdx.x & 31;
+  const int valid = min((int)*a.n_valid, a.n);
+  const long long r0 = a.clear_from + warp * kClearRows, r = r0 + lane;
+  // A row that a token names is written by its sum.  run_start is written for such rows only: what it holds for another
+  // leads to no position of that token.
+  bool skip = r >= a.vocab || lane >= kClearRows;
+  if (!skip) {
+    const int q = a.run_start[r];
+    const int from = (unsigned)q < (unsigned)valid ? a.perm[q] : -1;
+    skip = (unsigned)from < (unsigned)a.n && a.tokens[from] == (int)r;
+  }
+  const unsigned mask = __ballot_sync(0xffffffffu, !skip);
+  const size_t bytes = (size_t)a.dim * sizeof(O);
+  const bool vectors = (reinterpret_cast<uintptr_t>(out) | bytes) % 16 == 0;
+  for (int i = 0; i < kClearRows; ++i) {
+    if (!(mask >> i & 1)) continue;
+    O* row = out + (r0 + i) * a.dim;
+    if (vectors) {
+      for (int c = lane; c < (int)(bytes / 16); c += 32) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = lane; c < a.dim; c += 32) row[c] = from_f32<O>(0.0f);
+    }
+  }
+}
+
 // A warp: the blocks that begin at sorted positions [w * window, (w + 1) *
-// window), columns blockIdx.y * kSlice and on.
+// window), columns slice * kSlice and on.
 constexpr int kEnd = 32, kLong = 64, kFirst = 128;     // of a position: it ends its block, its run is long, its block is the run's first
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(256, 2)
 embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int window) {
   dep_wait();
   dep_launch();
+  // CTAs that clear are spread among those that sum
+  const long long ctas = (long long)a.sum_ctas + a.clear_ctas;
+  const int cleared = (int)(blockIdx.x * (long long)a.clear_ctas / ctas);
+  if ((blockIdx.x + 1LL) * a.clear_ctas / ctas > cleared) {
+    clear_rows(out, a, (long long)cleared * (blockDim.x >> 5) + (threadIdx.x >> 5));
+    return;
+  }
+  const int cta = blockIdx.x - cleared, slice = cta % a.slices;
   const int lane = threadIdx.x & 31;
   const int valid = min((int)*a.n_valid, a.n);
-  const long long w0 = ((long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * window;
+  const long long w0 = ((long long)(cta / a.slices) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * window;
   if (w0 >= valid) return;
   // 64 positions from w0 on, two a lane: what they hold, and where blocks begin and end
   __shared__ int4 s_meta[256 / 32][64];          // position, token, rank in its block and flags
@@ -459,7 +498,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   const unsigned long long here = begin & ((window == 32 ? 0xffffffffull : (1ull << window) - 1));
   if (here == 0) return;
   constexpr int COLS = kCols<T>, PAIRS = COLS / 2;
-  const int c = blockIdx.y * kSlice<T> + lane * COLS;
+  const int c = slice * kSlice<T> + lane * COLS;
   const int nc = max(0, min(COLS, a.dim - c));
   const int p0 = __ffsll((long long)here) - 1;
   // the last block that begins here ends at the first end behind its beginning
@@ -526,6 +565,8 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
           case 3: join(y, x, v); join(v, st[3], v); join(v, st[4], st[0]); break;
           default: join(y, x, st[3]);
         }
+      } else if (rank == 0 && (m.z & kEnd)) {
+        pairs_of(Vec16<T>{row[q - p][lane]}, v);              // a token that occurs once, or a run's last row by itself
       } else {
         const Vec16<T> one{row[q - p][lane]};
         switch (__ffs(~rank) - 1) {
@@ -536,24 +577,24 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       }
       if (!(m.z & kEnd)) continue;
       // the block's node: the pending ones from the smallest up
-      const int count = rank + 1 == kBlock ? 1 : rank + 1;
-      bool have = false;
+      if (rank > 0) {
+        const int count = rank + 1 == kBlock ? 1 : rank + 1;
+        bool have = false;
 #pragma unroll
-      for (int l = 0; l < 5; ++l)
-        if (count >> l & 1) {
-          if (have) {
-            join(v, st[l], v);
-          } else {
+        for (int l = 0; l < 5; ++l)
+          if (count >> l & 1) {
+            if (have) {
+              join(v, st[l], v);
+            } else {
 #pragma unroll
-            for (int i = 0; i < PAIRS; ++i) v[i] = st[l][i];
+              for (int i = 0; i < PAIRS; ++i) v[i] = st[l][i];
+            }
+            have = true;
           }
-          have = true;
-        }
+      }
       const bool last_node = !(m.z & kLong);
-      const long long start = w0 + q - rank;
-      O* to = out + (long long)m.y * a.dim + c;
-      float* node = a.nodes + node_slot(start, m.z & kFirst) * a.dim + c;
       if (last_node) {
+        O* to = out + (long long)m.y * a.dim + c;
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
         if (accumulate) {
@@ -564,8 +605,9 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
         }
         store_cols<VEC>(to, v, nc);
       } else {
-        store_cols<VEC>(node, v, nc);
-        if ((m.z & kFirst) && blockIdx.y == 0 && lane == 0) {
+        const long long start = w0 + q - rank;
+        store_cols<VEC>(a.nodes + node_slot(start, m.z & kFirst) * a.dim + c, v, nc);
+        if ((m.z & kFirst) && slice == 0 && lane == 0) {
           const unsigned k = atomicAdd(a.long_runs, 1u);       // in any order: runs do not meet
           if (k <= (unsigned)(a.n / kBlock)) a.runs[k] = {m.y, (int)start, a.run_end[m.y]};
         }
@@ -630,6 +672,9 @@ embedding_join_kernel(GradArgs a, O* out, int accumulate) {
   }
 }
 
+// Bytes that are cleared beside the sort, in the 18 us that it takes.
+constexpr size_t kClearWithSort = 96 << 20;
+
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kMostDim = 1 << 21;       // 64 columns a CTA: the grid's second dimension
@@ -656,20 +701,26 @@ int forward(const void* table, int vocab, int dim, int64_t stride, const int32_t
 }
 
 template <typename T, typename O>
-int blocks(const void* grad, const GradArgs& a, int n, void* out, int accumulate, cudaStream_t s) {
+int blocks(const void* grad, GradArgs a, int n, void* out, int accumulate, cudaStream_t s) {
   // vectors where every row of every operand starts on 16 bytes (rows of nodes do in the workspace then)
   const bool vec = vectors<T>(grad, a.stride) && vectors<O>(out, a.dim) && a.dim * sizeof(T) % 16 == 0;
   const unsigned slices = (unsigned)((a.dim + kSlice<T> - 1) / kSlice<T>);
   // windows of 32 positions, shorter ones while they leave SMs without a warp
   int window = 32;
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
-  const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 ? 1 : 8;
+  const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 && a.clear_from == a.vocab ? 1 : 8;
   auto* kernel = vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>;
   const size_t smem = (size_t)per_cta * kStages * kEight * 32 * 16;
   const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kStages * kEight * 32 * 16);
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_blocks");
+  const long long sums = (long long)((warps + per_cta - 1) / per_cta) * slices;
+  const long long clears = (a.vocab - a.clear_from + (long long)kClearRows * per_cta - 1) / (kClearRows * per_cta);
+  if (sums + clears >= (1LL << 31)) return DET_ERR_TOO_LARGE;
+  a.slices = (int)slices;
+  a.sum_ctas = (int)sums;
+  a.clear_ctas = (int)clears;
   launch_begin("det_embedding_blocks", s);
-  const cudaError_t e = launch_dep(kernel, dim3((warps + per_cta - 1) / per_cta, slices), dim3(32 * per_cta), smem, s,
+  const cudaError_t e = launch_dep(kernel, dim3((unsigned)(sums + clears)), dim3(32 * per_cta), smem, s,
                                    static_cast<const T*>(grad), a, static_cast<O*>(out), accumulate, window);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_blocks");
@@ -782,12 +833,15 @@ extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, in
   GradArgs a;
   a.tokens = tokens;
   a.n_valid = &header->n_valid;
+  a.clear_from = (int)vocab;                                     // nothing
   a.long_runs = &header->long_segs;                              // cleared by either sort, neither of which uses it
   if (plan.one_cta) {
     a.perm = reinterpret_cast<int32_t*>(w + plan.perm);
     a.run_start = reinterpret_cast<int32_t*>(w + plan.run_start);
     a.run_end = reinterpret_cast<int32_t*>(w + plan.run_end);
-    if (const int rc = cta_sort(a, (int)n, (int)vocab, accumulate ? nullptr : grad_table, table_bytes, s)) return rc;
+    const size_t row_bytes = (size_t)dim * model_elem_size(table_dtype);
+    if (!accumulate) a.clear_from = (int)std::min<int64_t>(vocab, (int64_t)(kClearWithSort / row_bytes) + 1);
+    if (const int rc = cta_sort(a, (int)n, (int)vocab, accumulate ? nullptr : grad_table, a.clear_from * row_bytes, s)) return rc;
   } else {
     int buffer = 0;
     if (const int rc = enqueue_sort(plan.sort, workspace, tokens, 0, nullptr, nullptr, s, &buffer)) return rc;
