@@ -277,7 +277,7 @@ embedding_sort_kernel(SortArgs a) {
 
 constexpr int kBlock = 32;       // ranks of a block
 constexpr int kEight = 8;        // rows that a warp asks for at a time, and of a whole subtree
-constexpr int kStages = 3;       // such groups in shared memory or on their way
+constexpr int kStages = 2;       // such groups in shared memory or on their way
 // columns of a lane, a 16-byte vector, and of a warp
 template <typename T> constexpr int kCols = 16 / sizeof(T);
 
@@ -343,43 +343,53 @@ __device__ __forceinline__ float finish(float sum, float scale, const O* old, bo
 
 // A lane's columns of a row: 16 bytes of T.  VEC: aligned, and all or none of them.
 template <typename T> struct Vec16 { uint4 q; };
-template <bool VEC, typename T>
-__device__ __forceinline__ Vec16<T> load_vec(const T* p, int n) {
-  Vec16<T> v;
-  v.q = make_uint4(0, 0, 0, 0);
-  if constexpr (VEC) {
-    if (n > 0) v.q = *reinterpret_cast<const uint4*>(p);
-  } else if constexpr (sizeof(T) == 4) {
-    const unsigned* u = reinterpret_cast<const unsigned*>(p);
-    if (n > 0) v.q.x = u[0];
-    if (n > 1) v.q.y = u[1];
-    if (n > 2) v.q.z = u[2];
-    if (n > 3) v.q.w = u[3];
-  } else {
-    v.q = load_eight<false>(p, n).q;
-  }
-  return v;
-}
 __device__ __forceinline__ void pairs_of(const Vec16<float>& e, Two (&v)[2]) {
   v[0] = two(__uint_as_float(e.q.x), __uint_as_float(e.q.y));
   v[1] = two(__uint_as_float(e.q.z), __uint_as_float(e.q.w));
 }
-// n of a lane's columns at p to its place in shared memory, the others 0: asynchronously
-// where all are there and aligned; `any` is aligned.
+// A warp's columns of a row, from p on, `left` of them, to a place in shared memory; those
+// that are not there 0.  VEC: 16-byte vectors; else in 32 bits element by element and in 16 bits the
+// words that hold them (the lower half of the first may be an element before them, beside them in a
+// word); `any` is aligned.
+constexpr int kPlace = 33;               // 16-byte units of a place: 256 elements of 16 bits from the middle of a word on
 template <bool VEC, typename T>
-__device__ __forceinline__ void copy_row(uint4* to, const T* p, const T* any, int n) {
+__device__ __forceinline__ void copy_row(uint4* to, const T* p, const void* any, int left, int lane) {
+  const unsigned dst = smem_u32(to);
+  auto copy4 = [&](int word, const void* from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * word), "l"(bytes > 0 ? from : any), "r"(bytes)
+                 : "memory");
+  };
   if constexpr (VEC) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(n > 0 ? p : any), "r"(n > 0 ? 16 : 0)
+    const bool ok = lane * kCols<T> < left;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * lane), "l"(ok ? p + lane * kCols<T> : any),
+                 "r"(ok ? 16 : 0)
                  : "memory");
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to) + 4 * i), "l"(i < n ? p + i : any),
-                   "r"(i < n ? 4 : 0)
-                   : "memory");
+    for (int j = 0; j < 4; ++j) copy4(32 * j + lane, p + 32 * j + lane, 32 * j + lane < left ? 4 : 0);
   } else {
-    *to = load_vec<false>(p, n).q;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const int halves = left + (int)(at >> 1 & 1);         // from the first word on
+    const char* words = reinterpret_cast<const char*>(at & ~(uintptr_t)3);
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const int i = 32 * j + lane;
+      if (j < 4 || lane == 0) copy4(i, words + 4 * i, max(0, min(2, halves - 2 * i)) * 2);
+    }
   }
+}
+// A lane's columns of it; odd: the row starts in the middle of a word.
+template <bool VEC, typename T>
+__device__ __forceinline__ Vec16<T> take_row(const uint4* from, bool odd, int lane) {
+  Vec16<T> v{from[lane]};
+  if constexpr (!VEC && sizeof(T) == 2) {
+    if (odd) {
+      const unsigned next = reinterpret_cast<const unsigned*>(from + lane)[4];
+      v.q = make_uint4(__funnelshift_r(v.q.x, v.q.y, 16), __funnelshift_r(v.q.y, v.q.z, 16),
+                       __funnelshift_r(v.q.z, v.q.w, 16), __funnelshift_r(v.q.w, next, 16));
+    }
+  }
+  return v;
 }
 template <typename T>
 __device__ __forceinline__ void pairs_of(const Vec16<T>& e, Two (&v)[4]) {
@@ -506,9 +516,13 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   const int p1 = __ffsll((long long)(end >> last << last)) - 1;
   if (p1 < 0) return;
   // rows come through the warp's ring in groups: eight of one block that are a subtree, or up to
-  // eight up to the next such; a lane reads what it has copied itself
-  extern __shared__ __align__(16) uint4 s_rows[];        // [warps][kStages][kEight][32]
-  uint4(*rows)[kEight][32] = reinterpret_cast<uint4(*)[kEight][32]>(s_rows) + (threadIdx.x >> 5) * kStages;
+  // eight up to the next such
+  extern __shared__ __align__(16) uint4 s_rows[];        // [warps][kStages][kEight][kPlace]
+  uint4(*rows)[kEight][kPlace] = reinterpret_cast<uint4(*)[kEight][kPlace]>(s_rows) + (threadIdx.x >> 5) * kStages;
+  const uintptr_t grad_odd = reinterpret_cast<uintptr_t>(grad) >> 1;
+  const T* slice_grad = grad + slice * kSlice<T>;
+  const int left = a.dim - slice * kSlice<T>;
+  const void* any = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(grad) & ~(uintptr_t)3);
   auto group = [&](int p) {
     if (whole >> p & 1) return kEight;
     const int to_next = (whole >> p) ? __ffsll((long long)(whole >> p)) - 1 : kEight;
@@ -519,7 +533,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       const int n = group(p);
 #pragma unroll
       for (int j = 0; j < kEight; ++j)
-        if (j < n) copy_row<VEC>(&rows[stage][j][lane], grad + meta[p + j].x * a.stride + c, grad, nc);
+        if (j < n) copy_row<VEC>(rows[stage][j], slice_grad + meta[p + j].x * a.stride, VEC ? grad : any, left, lane);
       p += n;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -533,7 +547,11 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
   int stage = 0;
   for (int p = p0; p <= p1;) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    const uint4(*row)[32] = rows[stage];
+    if (!VEC) __syncwarp();            // (a lane reads what others have copied)
+    const uint4(*row)[kPlace] = rows[stage];
+    auto take = [&](int j) {
+      return take_row<VEC, T>(row[j], (grad_odd ^ (meta[p + j].x & (unsigned)a.stride)) & 1, lane);
+    };
     const int n = group(p);
     const bool eight = whole >> p & 1;
     for (int q = eight ? p + kEight - 1 : p; q < p + n; ++q) {
@@ -545,19 +563,19 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       Two v[PAIRS];
       if (eight) {
         Two x[PAIRS], y[PAIRS];
-        pairs_of(Vec16<T>{row[0][lane]}, x);
-        pairs_of(Vec16<T>{row[1][lane]}, v);
+        pairs_of(take(0), x);
+        pairs_of(take(1), v);
         join(v, x, x);
-        pairs_of(Vec16<T>{row[2][lane]}, y);
-        pairs_of(Vec16<T>{row[3][lane]}, v);
+        pairs_of(take(2), y);
+        pairs_of(take(3), v);
         join(v, y, y);
         join(y, x, x);
-        pairs_of(Vec16<T>{row[4][lane]}, y);
-        pairs_of(Vec16<T>{row[5][lane]}, v);
+        pairs_of(take(4), y);
+        pairs_of(take(5), v);
         join(v, y, y);
         Two z[PAIRS];
-        pairs_of(Vec16<T>{row[6][lane]}, z);
-        pairs_of(Vec16<T>{row[7][lane]}, v);
+        pairs_of(take(6), z);
+        pairs_of(take(7), v);
         join(v, z, z);
         join(z, y, y);
         switch (rank / kEight) {
@@ -566,9 +584,9 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
           default: join(y, x, st[3]);
         }
       } else if (rank == 0 && (m.z & kEnd)) {
-        pairs_of(Vec16<T>{row[q - p][lane]}, v);              // a token that occurs once, or a run's last row by itself
+        pairs_of(take(q - p), v);              // a token that occurs once, or a run's last row by itself
       } else {
-        const Vec16<T> one{row[q - p][lane]};
+        const Vec16<T> one = take(q - p);
         switch (__ffs(~rank) - 1) {
           case 0: pairs_of(one, st[0]); break;
           case 1: pairs_of(one, v); join(v, st[0], st[1]); break;
@@ -613,6 +631,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
         }
       }
     }
+    if (!VEC) __syncwarp();
     asked = ask(asked, stage);
     p += n;
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -710,8 +729,8 @@ int blocks(const void* grad, GradArgs a, int n, void* out, int accumulate, cudaS
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
   const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 && a.clear_from == a.vocab ? 1 : 8;
   auto* kernel = vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>;
-  const size_t smem = (size_t)per_cta * kStages * kEight * 32 * 16;
-  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kStages * kEight * 32 * 16);
+  const size_t smem = (size_t)per_cta * kStages * kEight * kPlace * 16;
+  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kStages * kEight * kPlace * 16);
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_blocks");
   const long long sums = (long long)((warps + per_cta - 1) / per_cta) * slices;
   const long long clears = (a.vocab - a.clear_from + (long long)kClearRows * per_cta - 1) / (kClearRows * per_cta);
