@@ -516,7 +516,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     }
   }
   if (!part) return;
-  __syncthreads();                     // weight and rows have been read
+  copies_wait(0);                      // (those past the last row write zeros)
+  __syncthreads();                     // weight and rows have been read: the groups' sums take their place
   float* mine = part + (long long)blockIdx.x * 2 * cols;
   // several rows at a time: the groups' sums in the groups' order
 #pragma unroll
