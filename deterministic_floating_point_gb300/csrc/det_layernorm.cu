@@ -1,7 +1,7 @@
 // det_layer_norm and its gradients.
 //
-// A row lies in the registers of a group of threads: 32 to 1,024 of them, eight or
-// sixteen columns each (eights, the group's threads apart), so it is read once.
+// A row lies in the registers of a group of threads: 32 to 1,024 of them, eight to
+// 32 columns each (eights, the group's threads apart), so it is read once.
 // The mean is the rows' sum, the variance the sum of squares of what the mean
 // leaves -- two trees over the same columns, across lanes by shuffles and across
 // warps through shared memory -- and never a difference of two large sums.
@@ -153,28 +153,31 @@ struct Feed {
       }
     }
   }
-  // odd: the row starts in the middle of a word (16-bit rows at any address)
-  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], bool odd, int lane) {
+  // An eight of the row in a stage.  odd: the row starts in the middle of a word (16-bit rows at any address)
+  __device__ __forceinline__ Eight<T> eight(int stage, int k, bool odd, int lane) const {
     const char* from = s + stage * kStage;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if constexpr (VEC) {
-        const uint4* q = reinterpret_cast<const uint4*>(from) + kHalves * (k * 32 + lane);
-        e[k].q = q[0];
-        if constexpr (kHalves == 2) e[k].r = q[1];
-      } else if constexpr (sizeof(T) == 4) {
-        e[k] = load_eight<true>(reinterpret_cast<const T*>(from) + k * 256 + 8 * lane, 8);
-      } else {
-        const unsigned* w = reinterpret_cast<const unsigned*>(from + k * kSpan) + 4 * lane;
-        uint4 q = *reinterpret_cast<const uint4*>(w);
-        if (odd) {
-          const unsigned next = w[4];
-          q = make_uint4(__funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16), __funnelshift_r(q.z, q.w, 16),
-                         __funnelshift_r(q.w, next, 16));
-        }
-        e[k].q = q;
+    Eight<T> e;
+    if constexpr (VEC) {
+      const uint4* q = reinterpret_cast<const uint4*>(from) + kHalves * (k * 32 + lane);
+      e.q = q[0];
+      if constexpr (kHalves == 2) e.r = q[1];
+    } else if constexpr (sizeof(T) == 4) {
+      e = load_eight<true>(reinterpret_cast<const T*>(from) + k * 256 + 8 * lane, 8);
+    } else {
+      const unsigned* w = reinterpret_cast<const unsigned*>(from + k * kSpan) + 4 * lane;
+      uint4 q = *reinterpret_cast<const uint4*>(w);
+      if (odd) {
+        const unsigned next = w[4];
+        q = make_uint4(__funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16), __funnelshift_r(q.z, q.w, 16),
+                       __funnelshift_r(q.w, next, 16));
       }
+      e.q = q;
     }
+    return e;
+  }
+  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], bool odd, int lane) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) e[k] = eight(stage, k, odd, lane);
     __syncwarp();                                        // the stage may be written again
   }
   // Whether row r of rows at p, stride elements apart, starts in the middle of a word.
@@ -268,14 +271,27 @@ __device__ __forceinline__ void keep_first(Two (&v)[4], int n) {
   }
 }
 // Columns c .. c + 7 of a weight or bias, `other` without one.
+template <typename P>
+__device__ __forceinline__ void load_param(Two (&v)[4], const P* p, int c, int cols) {
+  const int n = max(0, min(8, cols - c));
+  pairs_of(n == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0 ? load_eight<true>(p + c, 8) : load_eight<false>(p + c, n), v);
+}
 __device__ __forceinline__ void load_param(Two (&v)[4], const void* p, int c, int cols, int dtype, float other) {
+  if (!p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = two(p && c + 2 * i < cols ? load_as_f32(p, c + 2 * i, dtype) : other,
-                      p && c + 2 * i + 1 < cols ? load_as_f32(p, c + 2 * i + 1, dtype) : other);
+    for (int i = 0; i < 4; ++i) v[i] = twice(other);
+  } else if (dtype == DET_F32) {
+    load_param(v, static_cast<const float*>(p), c, cols);
+  } else if (dtype == DET_BF16) {
+    load_param(v, static_cast<const __nv_bfloat16*>(p), c, cols);
+  } else {
+    load_param(v, static_cast<const __half*>(p), c, cols);
+  }
 }
 
 constexpr int kThreads = 256;       // a CTA's, unless a row takes more
+// Of a row of partial sums, so that eights lie on 16 bytes.
+__host__ __device__ constexpr int whole_eights(int cols) { return (cols + 7) / 8 * 8; }
 
 // A weight or bias in shared memory, where they leave registers for rows: halves of
 // eights, so that a warp reads 512 bytes in a row.
@@ -308,16 +324,6 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   char* mine = reinterpret_cast<char*>(s_b + (HELD ? 0 : 2 * K * g.threads)) +
                g.warp * (feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
   char* turn = mine + feed_bytes<T, VEC, K>(stages);
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if constexpr (HELD) {
-      load_param(held_w[k], weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
-      load_param(held_b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
-    } else {
-      keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);       // (read again by the same thread)
-      keep_param(s_b, bias, g, k, cols, param_dtype, 0.0f);
-    }
-  }
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;   // all of the thread's columns are there
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
@@ -329,6 +335,16 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   for (int i = 0; i < stages; ++i, asked += step, from += step * x_stride) {
     feed.ask(i, from, feed.aligned(x), c, asked < rows, g.lane);
     copies_commit();
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if constexpr (HELD) {
+      load_param(held_w[k], weight, (g.me + k * g.threads) * 8, cols, param_dtype, 1.0f);
+      load_param(held_b[k], bias, (g.me + k * g.threads) * 8, cols, param_dtype, 0.0f);
+    } else {
+      keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);       // (read again by the same thread)
+      keep_param(s_b, bias, g, k, cols, param_dtype, 0.0f);
+    }
   }
   int stage = 0;
   // (every thread of the CTA makes as many rounds)
@@ -397,13 +413,15 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   }
 }
 
-// part: [gridDim.x][2][cols] sums of the weight's and the bias' gradients, or NULL.
+// part: [gridDim.x][2][whole_eights(cols)] sums of the weight's and the bias' gradients, or NULL.
 template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
 layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, unsigned rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
                        float* part, int log2_threads, int stages) {
   __shared__ __align__(16) Two s_sums[2][32];
+  // where the columns' sums take half of the registers, rows are read from shared memory twice
+  constexpr bool LATE = K == 4;
   extern __shared__ __align__(16) char s_dynamic[];
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
   dep_wait();
@@ -413,13 +431,6 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   char* mine_x = reinterpret_cast<char*>(s_w + 2 * K * g.threads) +
                  g.warp * (2 * feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
   Two aw[K][4], ab[K][4];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (g.index == 0) keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = twice(0.0f);
-  }
-  __syncthreads();
   const bool whole = (g.me + (K - 1) * g.threads) * 8 + 8 <= cols;
   const unsigned step = gridDim.x * g.count;
   const float of = 1.0f / (float)cols;
@@ -439,16 +450,26 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     from_grad += step * grad_stride;
   };
   for (int i = 0; i < stages; ++i) ask(i);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (g.index == 0) keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) aw[k][i] = ab[k][i] = twice(0.0f);
+  }
+  __syncthreads();
   float nm = r < rows ? means[r] : 0.0f, nr = r < rows ? rstds[r] : 0.0f;
   int parity = 0, stage = 0;
   for (unsigned first = blockIdx.x * g.count; first < rows;
        first += step, r += step, parity ^= 1, to += (long long)step * cols) {
     Eight<T> cx[K], cg[K];
     copies_wait(stages - 1);
-    feed_x.take(stage, cx, feed_x.odd_row(x, r, x_stride), g.lane);
-    feed_grad.take(stage, cg, feed_grad.odd_row(grad, r, grad_stride), g.lane);
-    ask(stage);
-    stage = stage + 1 == stages ? 0 : stage + 1;
+    const bool odd_x = feed_x.odd_row(x, r, x_stride), odd_grad = feed_grad.odd_row(grad, r, grad_stride);
+    if (!LATE) {
+      feed_x.take(stage, cx, odd_x, g.lane);
+      feed_grad.take(stage, cg, odd_grad, g.lane);
+      ask(stage);
+      stage = stage + 1 == stages ? 0 : stage + 1;
+    }
     const Two minus_mean = twice(-nm), rstd2 = twice(nr);
     const bool more = r + step < rows;
     nm = more ? means[r + step] : 0.0f;
@@ -458,8 +479,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     for (int k = 0; k < K; ++k) {
       Two xh[4], d[4], w[4];
       param(w, s_w, g, k);
-      pairs_of(cx[k], xh);
-      pairs_of(cg[k], d);
+      pairs_of(LATE ? feed_x.eight(stage, k, odd_x, g.lane) : cx[k], xh);
+      pairs_of(LATE ? feed_grad.eight(stage, k, odd_grad, g.lane) : cg[k], d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) xh[i] = mul(add(xh[i], minus_mean), rstd2);
       if (!whole) keep_first(xh, cols - (g.me + k * g.threads) * 8);
@@ -472,10 +493,13 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         t2[k] = i ? fma(d[i], xh[i], t2[k]) : mul(d[i], xh[i]);
       }
     }
-    if (K == 2) {
-      t1[0] = add(t1[0], t1[K - 1]);
-      t2[0] = add(t2[0], t2[K - 1]);
-    }
+#pragma unroll
+    for (int d = 1; d < K; d *= 2)
+#pragma unroll
+      for (int k = 0; k < K; k += 2 * d) {
+        t1[k] = add(t1[k], t1[k + d]);
+        t2[k] = add(t2[k], t2[k + d]);
+      }
     Two sums = two(lanes(t1[0]), lanes(t2[0]));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1)
@@ -502,8 +526,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       for (int k = 0; k < K; ++k) {
         Two xh[4], d[4], w[4];
         param(w, s_w, g, k);
-        pairs_of(cx[k], xh);
-        pairs_of(cg[k], d);
+        pairs_of(LATE ? feed_x.eight(stage, k, odd_x, g.lane) : cx[k], xh);
+        pairs_of(LATE ? feed_grad.eight(stage, k, odd_grad, g.lane) : cg[k], d);
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -514,31 +538,37 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         store_columns(to, y, c, k, r < rows, turn, g.lane);
       }
     }
+    if (LATE) {
+      __syncwarp();
+      ask(stage);
+      stage = stage + 1 == stages ? 0 : stage + 1;
+    }
   }
   if (!part) return;
   copies_wait(0);                      // (those past the last row write zeros)
   __syncthreads();                     // weight and rows have been read: the groups' sums take their place
-  float* mine = part + (long long)blockIdx.x * 2 * cols;
+  const int pitch = whole_eights(cols);
+  float* mine = part + (long long)blockIdx.x * 2 * pitch;
   // several rows at a time: the groups' sums in the groups' order
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (g.count > 1 && which) __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = which ? ab[k][i] : aw[k][i];
-        const int c = (g.me + k * g.threads) * 8 + 2 * i;
-        float* to = g.count > 1 ? s_acc + g.index * cols : mine + which * cols;
-        if (c < cols) to[c] = f.x;
-        if (c + 1 < cols) to[c + 1] = f.y;
+    for (int k = 0; k < K; ++k) {
+      const Two(&v)[4] = which ? ab[k] : aw[k];
+      const int c = (g.me + k * g.threads) * 8;
+      float4* to = reinterpret_cast<float4*>((g.count > 1 ? s_acc + g.index * pitch : mine + which * pitch) + c);
+      if (c < cols) {
+        to[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        to[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
       }
+    }
     if (g.count == 1) continue;
     __syncthreads();
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
       float t = s_acc[c];
-      for (int j = 1; j < g.count; ++j) t += s_acc[j * cols + c];
-      mine[which * cols + c] = t;
+      for (int j = 1; j < g.count; ++j) t += s_acc[j * pitch + c];
+      mine[which * pitch + c] = t;
     }
   }
 }
@@ -555,9 +585,10 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
   const int c = blockIdx.x * 32 + lane;
   float t = 0.0f;
   if (c < cols) {
-    const float* p = part + (long long)blockIdx.y * cols + c;
+    const int pitch = whole_eights(cols);
+    const float* p = part + (long long)blockIdx.y * pitch + c;
 #pragma unroll 4
-    for (int j = warp; j < parts; j += 32) t += p[(long long)j * 2 * cols];
+    for (int j = warp; j < parts; j += 32) t += p[(long long)j * 2 * pitch];
   }
   s[warp][lane] = t;
   __syncthreads();
@@ -567,19 +598,21 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
 }
 
 // Eights of columns a thread takes (two keep a row's sums over lanes and warps short), and
-// the threads that take a row, as a logarithm.
+// the threads that take a row, as a logarithm.  The gradient of wide rows takes four: 1,024 threads
+// of 64 registers each spill (4,096 x 16,384 in bf16: 182 us, 82 with 512 that take twice as much).
 int eights(int64_t cols) { return cols > 256 ? 2 : 1; }
-int row_threads(int64_t cols) {
+int grad_eights(int64_t cols) { return cols > 8192 ? 4 : eights(cols); }
+int row_threads(int64_t cols, int eights) {
   int l = 5;
-  while ((8LL * eights(cols) << l) < cols) ++l;
+  while ((8LL * eights << l) < cols) ++l;
   return l;
 }
 // CTAs of the gradient, each of which leaves a partial sum: as many as run at once on
 // the 152 SMs, by a constant, because the sums' order hangs on it.
 int grad_parts(int64_t rows, int64_t cols) {
-  const int l = row_threads(cols);
+  const int l = row_threads(cols, grad_eights(cols));
   const int64_t at_a_time = std::max<int64_t>(1, kThreads >> l);
-  const int at_once = 152 * (l > 8 ? 1 : eights(cols) == 1 ? 3 : 2);
+  const int at_once = 152 * (l > 8 ? 1 : grad_eights(cols) == 1 ? 3 : 2);
   return (int)std::min<int64_t>((rows + at_a_time - 1) / at_a_time, at_once);
 }
 
@@ -604,7 +637,7 @@ size_t room(int params, int operands, int log2_threads, int threads, int* stages
 template <typename T, int K, bool VEC, int MOST>
 int forward(const void* x, int rows, int cols, int64_t x_stride, const void* weight, const void* bias, int param_dtype,
             float eps, void* out, float* mean_out, float* rstd_out, cudaStream_t s) {
-  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+  const int l = row_threads(cols, K), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
   auto* k = layer_norm_kernel<T, K, VEC, MOST>;
   int stages = 1;
   const size_t smem = room<T, VEC, K>(MOST == 256 ? 0 : 2, 1, l, threads, &stages);
@@ -626,11 +659,11 @@ template <typename T, int K, bool VEC, int MOST>
 int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int rows, int cols,
              const float* mean, const float* rstd, const void* weight, int param_dtype, void* grad_x, float* part,
              cudaStream_t s) {
-  const int l = row_threads(cols), threads = std::max(kThreads, 1 << l);
+  const int l = row_threads(cols, K), threads = std::max(kThreads, 1 << l);
   auto* k = layer_norm_grad_kernel<T, K, VEC, MOST>;
   int stages = 1;
   // weight and rows; the groups' sums take their place at the end
-  const size_t sums = (threads >> l) > 1 ? (size_t)(threads >> l) * cols * sizeof(float) : 0;
+  const size_t sums = (threads >> l) > 1 ? (size_t)(threads >> l) * whole_eights(cols) * sizeof(float) : 0;
   const size_t smem = std::max(room<T, VEC, K>(1, 2, l, threads, &stages), sums);
   const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm_backward");
@@ -656,30 +689,30 @@ bool misaligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p
 
 using namespace det;
 
-// The kernels for eights() and row_threads().
-#define DET_NORM_PICK_T(fn, T, ...)                                                                     \
+// The kernels for eights() or grad_eights() and row_threads().
+#define DET_NORM_PICK_T(fn, T, WIDE_K, ...)                                                                     \
   do {                                                                                                   \
     if (cols <= 256) return vec ? fn<T, 1, true, 256>(__VA_ARGS__) : fn<T, 1, false, 256>(__VA_ARGS__);  \
     if (cols <= 4096) return vec ? fn<T, 2, true, 256>(__VA_ARGS__) : fn<T, 2, false, 256>(__VA_ARGS__); \
     if (cols <= 8192) return vec ? fn<T, 2, true, 512>(__VA_ARGS__) : fn<T, 2, false, 512>(__VA_ARGS__); \
-    return vec ? fn<T, 2, true, 1024>(__VA_ARGS__) : fn<T, 2, false, 1024>(__VA_ARGS__);                 \
+    return vec ? fn<T, WIDE_K, true, 2048 / WIDE_K>(__VA_ARGS__) : fn<T, WIDE_K, false, 2048 / WIDE_K>(__VA_ARGS__); \
   } while (0)
-#define DET_NORM_PICK(fn, ...)                                                 \
+#define DET_NORM_PICK(fn, WIDE_K, ...)                                                 \
   do {                                                                         \
-    if (dtype == DET_F32) DET_NORM_PICK_T(fn, float, __VA_ARGS__);                   \
-    if (dtype == DET_BF16) DET_NORM_PICK_T(fn, __nv_bfloat16, __VA_ARGS__);   \
-    DET_NORM_PICK_T(fn, __half, __VA_ARGS__);                                 \
+    if (dtype == DET_F32) DET_NORM_PICK_T(fn, float, WIDE_K, __VA_ARGS__);                   \
+    if (dtype == DET_BF16) DET_NORM_PICK_T(fn, __nv_bfloat16, WIDE_K, __VA_ARGS__);   \
+    DET_NORM_PICK_T(fn, __half, WIDE_K, __VA_ARGS__);                                 \
   } while (0)
 
 static int norm_forward(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
                         const void* bias, int param_dtype, float eps, void* out, float* mean_out, float* rstd_out,
                         bool vec, cudaStream_t s) {
-  DET_NORM_PICK(forward, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, s);
+  DET_NORM_PICK(forward, 2, x, (int)rows, (int)cols, x_stride, weight, bias, param_dtype, eps, out, mean_out, rstd_out, s);
 }
 static int norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype, int64_t rows,
                          int64_t cols, const float* mean, const float* rstd, const void* weight, int param_dtype,
                          void* grad_x, float* part, bool vec, cudaStream_t s) {
-  DET_NORM_PICK(backward, grad, grad_stride, x, x_stride, (int)rows, (int)cols, mean, rstd, weight, param_dtype, grad_x,
+  DET_NORM_PICK(backward, 4, grad, grad_stride, x, x_stride, (int)rows, (int)cols, mean, rstd, weight, param_dtype, grad_x,
                 part, s);
 }
 
@@ -701,7 +734,7 @@ extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t co
 
 extern "C" size_t det_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (check_rows(DET_F32, DET_F32, rows, cols) != DET_OK || rows == 0) return 256;
-  return 256 + align_up((size_t)grad_parts(rows, cols) * 2 * (size_t)cols * sizeof(float), 256);
+  return 256 + align_up((size_t)grad_parts(rows, cols) * 2 * (size_t)whole_eights((int)cols) * sizeof(float), 256);
 }
 
 extern "C" int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int dtype,
