@@ -63,13 +63,12 @@ struct Group {
 // ---------------------------------------------------------------------------
 // Rows.  A thread's columns are eights, `threads` eights apart.  Rows are copied into
 // shared memory up to two rounds ahead of their turn, each warp the 256 columns of
-// its eights: as 16-byte vectors where every row starts on 16 bytes (VEC), else in 32
-// bits element by element.  (Rows ahead in registers instead left an SM with two CTAs.)
-// 16-bit rows at other addresses are copied by the words that hold them and shifted by an
-// element where they start in the middle of one (such a first word's lower half is not
-// the row's, but lies beside it in a word); outputs are shifted back and go through the
-// warp's part of shared memory.  (Element after element across the lanes instead: 176 us for the gradient of
-// 16,384 x 4,095 in bf16.)
+// its eights, as 16-byte vectors.  (Rows ahead in registers instead left an SM with two CTAs.)
+// Where rows or outputs do not all start on 16 bytes (VEC is false), the vectors that hold a
+// row's columns are copied and shifted as they are taken (what else such a first vector holds
+// is not the row's, but lies beside it in 16 bytes); outputs go through the warp's part of
+// shared memory to words in the order of memory.  (Gradient of 16,384 x 4,095 in bf16: 127 us; rows copied
+// word by word 133, read and written element by element 176.  16,384 x 4,096: 78.)
 
 // Where a thread reads and writes in a row: its first column, and how many of each
 // of its eights there are.
@@ -80,7 +79,7 @@ template <typename T, bool VEC, int K> struct Columns {
   int span[K];           // columns of the row from the first one that it copies on
   __device__ __forceinline__ Columns(const Group& g, int cols) {
     const int warp = (g.me & ~31) * 8;                   // the warp's first
-    first = VEC ? g.me * 8 : sizeof(T) == 4 ? warp + g.lane : warp;
+    first = VEC ? g.me * 8 : warp;
     read = VEC && sizeof(T) == 4 ? warp + 4 * g.lane : first;
     step = g.threads * 8;
 #pragma unroll
@@ -92,10 +91,8 @@ template <typename T, bool VEC, int K> struct Columns {
   }
 };
 
-template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
-  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the last `ahead` (0 or 1) groups have arrived.
@@ -106,12 +103,11 @@ __device__ __forceinline__ void copies_wait(int ahead) {
 }
 
 // A warp's rows of one operand: asked for, and taken in the same order.
-constexpr int kSpanWords = 132;          // 256 elements of 16 bits from the middle of a word on, and to 16 bytes
 template <typename T, bool VEC, int K>
 struct Feed {
   enum : int {
     kHalves = sizeof(T) / 2,             // 16-byte vectors of an eight
-    kSpan = !VEC && sizeof(T) == 2 ? kSpanWords * 4 : 256 * (int)sizeof(T),
+    kSpan = 256 * (int)sizeof(T) + (VEC ? 0 : 16),       // from the vector that holds the first column on
     kStage = K * kSpan                   // bytes of a warp's columns
   };
   char* s;               // the warp's stages
@@ -125,78 +121,85 @@ struct Feed {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {              // (a warp's copies go to one place after the other, or take longer)
           const bool ok = valid && c.span[k] > 128 * h;
-          copy_async<16>(to + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 128 * h : any, ok ? 16 : 0);
-        }
-      } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool ok = valid && 32 * j < c.n[k];
-          copy_async<4>(to + (k * 256 + 32 * j + lane) * 4, ok ? at + k * c.step + 32 * j : any, ok ? 4 : 0);
+          copy_async(to + ((k * kHalves + h) * 32 + lane) * 16, ok ? at + k * c.step + 128 * h : any, ok ? 16 : 0);
         }
       } else {
         const uintptr_t p = reinterpret_cast<uintptr_t>(at + k * c.step);
-        const int odd = (int)(p >> 1 & 1);
-        const char* words = reinterpret_cast<const char*>(p & ~(uintptr_t)3);
-        const int left = valid ? c.n[k] + odd : 0;       // elements from the first word on
-        if (left >= 258) {
+        const int off = (int)(p & 15);
+        const char* vectors = reinterpret_cast<const char*>(p & ~(uintptr_t)15);
+        const int left = valid && c.n[k] > 0 ? c.n[k] * (int)sizeof(T) + off : 0;       // bytes from the first vector on
+        if (left >= kSpan) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) copy_async<4>(to + k * kSpan + 4 * (32 * j + lane), words + 4 * (32 * j + lane), 4);
-          if (odd && lane == 0) copy_async<4>(to + k * kSpan + 512, words + 512, 4);
-          continue;
-        }
+          for (int h = 0; h < kHalves; ++h) copy_async(to + k * kSpan + 16 * (32 * h + lane), vectors + 16 * (32 * h + lane), 16);
+          if (off && lane == 0) copy_async(to + k * kSpan + kSpan - 16, vectors + kSpan - 16, 16);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 5; ++j) {
-          const int i = 32 * j + lane;
-          const int bytes = max(0, min(4, 2 * (left - 2 * i)));
-          if (j < 4 || lane == 0) copy_async<4>(to + k * kSpan + 4 * i, bytes ? words + 4 * i : any, bytes);
+          for (int h = 0; h <= kHalves; ++h) {
+            const int i = 32 * h + lane, bytes = max(0, min(16, left - 16 * i));
+            if (h < kHalves || lane == 0) copy_async(to + k * kSpan + 16 * i, bytes ? vectors + 16 * i : any, bytes);
+          }
         }
       }
     }
   }
-  // An eight of the row in a stage.  odd: the row starts in the middle of a word (16-bit rows at any address)
-  __device__ __forceinline__ Eight<T> eight(int stage, int k, bool odd, int lane) const {
-    const char* from = s + stage * kStage;
+  // An eight of the row in a stage.  off: bytes from the vector that holds the row's first column to that
+  __device__ __forceinline__ Eight<T> eight(int stage, int k, int off, int lane) const {
     Eight<T> e;
     if constexpr (VEC) {
-      const uint4* q = reinterpret_cast<const uint4*>(from) + kHalves * (k * 32 + lane);
+      const uint4* q = reinterpret_cast<const uint4*>(s + stage * kStage) + kHalves * (k * 32 + lane);
       e.q = q[0];
       if constexpr (kHalves == 2) e.r = q[1];
-    } else if constexpr (sizeof(T) == 4) {
-      e = load_eight<true>(reinterpret_cast<const T*>(from) + k * 256 + 8 * lane, 8);
     } else {
-      const unsigned* w = reinterpret_cast<const unsigned*>(from + k * kSpan) + 4 * lane;
-      uint4 q = *reinterpret_cast<const uint4*>(w);
-      if (odd) {
-        const unsigned next = w[4];
-        q = make_uint4(__funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16), __funnelshift_r(q.z, q.w, 16),
-                       __funnelshift_r(q.w, next, 16));
+      const uint4* q = reinterpret_cast<const uint4*>(s + stage * kStage + k * kSpan) + kHalves * lane;
+      unsigned w[4 * kHalves + 4];
+#pragma unroll
+      for (int h = 0; h <= kHalves; ++h) {
+        const uint4 v = h < kHalves || off ? q[h] : make_uint4(0, 0, 0, 0);
+        w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
       }
-      e.q = q;
+      // (off is the same for the whole warp)
+      if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves + 2; ++i) w[i] = w[i + 2];
+      }
+      if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves + 1; ++i) w[i] = w[i + 1];
+      }
+      if (sizeof(T) == 2 && (off & 2)) {
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+      }
+      e.q = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (kHalves == 2) e.r = make_uint4(w[4], w[5], w[6], w[7]);
     }
     return e;
   }
-  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], bool odd, int lane) const {
+  __device__ __forceinline__ void take(int stage, Eight<T> (&e)[K], int off, int lane) const {
 #pragma unroll
-    for (int k = 0; k < K; ++k) e[k] = eight(stage, k, odd, lane);
+    for (int k = 0; k < K; ++k) e[k] = eight(stage, k, off, lane);
     __syncwarp();                                        // the stage may be written again
   }
-  // Whether row r of rows at p, stride elements apart, starts in the middle of a word.
-  static __device__ __forceinline__ bool odd_row(const T* p, unsigned r, long long stride) {
-    return !VEC && sizeof(T) == 2 && (((unsigned)(reinterpret_cast<uintptr_t>(p) >> 1) ^ (r & (unsigned)stride)) & 1);
+  // Where row r of rows at p, stride elements apart, starts in 16 bytes.
+  static __device__ __forceinline__ int offset(const T* p, unsigned r, long long stride) {
+    return VEC ? 0 : ((unsigned)reinterpret_cast<uintptr_t>(p) + r * (unsigned)stride * (unsigned)sizeof(T)) & 15;
   }
   static __device__ __forceinline__ const void* aligned(const T* p) {
-    return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+    return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
   }
 };
 // Bytes of a warp's stages, and of the place where its outputs turn into rows.
 template <typename T, bool VEC, int K>
 __host__ __device__ constexpr int feed_bytes(int stages) { return stages * Feed<T, VEC, K>::kStage; }
 template <typename T, bool VEC>
-__host__ __device__ constexpr int turn_bytes() { return VEC ? 0 : sizeof(T) == 2 ? kSpanWords * 4 : 1024; }
+__host__ __device__ constexpr int turn_bytes() { return VEC ? 0 : sizeof(T) == 2 ? 528 : 1024; }
 
 template <typename T, bool VEC, int K>
 __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const Columns<T, VEC, K>& c, int k, bool valid,
                                               char* turn, int lane) {
+  // a warp's lanes are of one row and start at one column.  (With four eights the branch costs registers that are
+  // not there: 4,096 x 12,001 in 32 bits 235 us against 209.)
+  if (!VEC && K < 4 && (!valid || c.n[k] <= 0)) return;
   if constexpr (VEC) {
     if constexpr (sizeof(T) == 4) {
       if (valid && c.n[k] == 8 && reinterpret_cast<uintptr_t>(at) % 32 == 0) {
@@ -211,7 +214,7 @@ __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const 
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (valid && 32 * j < c.n[k]) at[k * c.step + 32 * j] = s[32 * j + lane];
+      if (valid && 32 * j + lane < c.n[k]) at[k * c.step + 32 * j + lane] = s[32 * j + lane];
     __syncwarp();
   } else {
     // the span's words: at an odd element each holds the element before its own first
@@ -351,7 +354,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   for (unsigned first = blockIdx.x * g.count; first < rows; first += step, r += step, to += (long long)step * cols) {
     Eight<T> e[K];
     copies_wait(stages - 1);
-    feed.take(stage, e, feed.odd_row(x, r, x_stride), g.lane);
+    feed.take(stage, e, feed.offset(x, r, x_stride), g.lane);
     feed.ask(stage, from, feed.aligned(x), c, asked < rows, g.lane);
     copies_commit();
     asked += step;
@@ -463,10 +466,10 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
        first += step, r += step, parity ^= 1, to += (long long)step * cols) {
     Eight<T> cx[K], cg[K];
     copies_wait(stages - 1);
-    const bool odd_x = feed_x.odd_row(x, r, x_stride), odd_grad = feed_grad.odd_row(grad, r, grad_stride);
+    const int off_x = feed_x.offset(x, r, x_stride), off_grad = feed_grad.offset(grad, r, grad_stride);
     if (!LATE) {
-      feed_x.take(stage, cx, odd_x, g.lane);
-      feed_grad.take(stage, cg, odd_grad, g.lane);
+      feed_x.take(stage, cx, off_x, g.lane);
+      feed_grad.take(stage, cg, off_grad, g.lane);
       ask(stage);
       stage = stage + 1 == stages ? 0 : stage + 1;
     }
@@ -479,8 +482,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     for (int k = 0; k < K; ++k) {
       Two xh[4], d[4], w[4];
       param(w, s_w, g, k);
-      pairs_of(LATE ? feed_x.eight(stage, k, odd_x, g.lane) : cx[k], xh);
-      pairs_of(LATE ? feed_grad.eight(stage, k, odd_grad, g.lane) : cg[k], d);
+      pairs_of(LATE ? feed_x.eight(stage, k, off_x, g.lane) : cx[k], xh);
+      pairs_of(LATE ? feed_grad.eight(stage, k, off_grad, g.lane) : cg[k], d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) xh[i] = mul(add(xh[i], minus_mean), rstd2);
       if (!whole) keep_first(xh, cols - (g.me + k * g.threads) * 8);
@@ -526,8 +529,8 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       for (int k = 0; k < K; ++k) {
         Two xh[4], d[4], w[4];
         param(w, s_w, g, k);
-        pairs_of(LATE ? feed_x.eight(stage, k, odd_x, g.lane) : cx[k], xh);
-        pairs_of(LATE ? feed_grad.eight(stage, k, odd_grad, g.lane) : cg[k], d);
+        pairs_of(LATE ? feed_x.eight(stage, k, off_x, g.lane) : cx[k], xh);
+        pairs_of(LATE ? feed_grad.eight(stage, k, off_grad, g.lane) : cg[k], d);
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
