@@ -51,23 +51,23 @@ embedding_kernel(const T* table, int vocab, int dim, long long stride, const int
       for (int j = 0; j < N; ++j)
         if (c + j * threads < end) out[i * dim + c + j * threads] = from_f32<O>(known ? __fmul_rn(v[j], scale) : 0.0f);
     }
-    return;
-  }
-  const int c0 = (blockIdx.y * threads * kEights + me) * 8;
-  Eight<T> e[kEights];
+  } else {
+    const int c0 = (blockIdx.y * threads * kEights + me) * 8;
+    Eight<T> e[kEights];
 #pragma unroll
-  for (int k = 0; k < kEights; ++k) {
-    const int c = c0 + k * threads * 8;
-    e[k] = load_eight<VEC>(row + c, known ? max(0, min(8, dim - c)) : 0);
-  }
+    for (int k = 0; k < kEights; ++k) {
+      const int c = c0 + k * threads * 8;
+      e[k] = load_eight<true>(row + c, known ? max(0, min(8, dim - c)) : 0);
+    }
 #pragma unroll
-  for (int k = 0; k < kEights; ++k) {
-    const int c = c0 + k * threads * 8;
-    float v[8];
-    unpack_eight(e[k], v);
+    for (int k = 0; k < kEights; ++k) {
+      const int c = c0 + k * threads * 8;
+      float v[8];
+      unpack_eight(e[k], v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = known ? __fmul_rn(v[j], scale) : 0.0f;
-    store_eight<VEC>(out + i * dim + c, v, max(0, min(8, dim - c)));
+      for (int j = 0; j < 8; ++j) v[j] = known ? __fmul_rn(v[j], scale) : 0.0f;
+      store_eight(out + i * dim + c, v, max(0, min(8, dim - c)));
+    }
   }
 }
 
@@ -403,7 +403,7 @@ template <int N> __device__ __forceinline__ void join(const Two (&v)[N], const T
   for (int i = 0; i < N; ++i) to[i] = add(node[i], v[i]);
 }
 // The first n of 2 P columns.
-template <bool VEC, typename O, int N>
+template <typename O, int N>
 __device__ __forceinline__ void load_cols(float (&v)[N], const O* p, int n) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
@@ -617,7 +617,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
         for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
         if (accumulate) {
           float old[COLS];
-          load_cols<VEC>(old, to, nc);
+          load_cols(old, to, nc);
 #pragma unroll
           for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);
         }

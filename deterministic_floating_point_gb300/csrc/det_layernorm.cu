@@ -207,10 +207,10 @@ __device__ __forceinline__ void store_columns(T* at, const float (&v)[8], const 
         return;
       }
     }
-    if (valid) store_eight<true>(at + k * c.step, v, c.n[k]);
+    if (valid) store_eight(at + k * c.step, v, c.n[k]);
   } else if constexpr (sizeof(T) == 4) {
     float* s = reinterpret_cast<float*>(turn);
-    store_eight<true>(s + 8 * lane, v, 8);
+    store_eight(s + 8 * lane, v, 8);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)

@@ -162,28 +162,15 @@ template <> __device__ __forceinline__ unsigned pack_two<__half>(float a, float 
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const unsigned*>(&v);
 }
-template <bool VEC, typename T>
+template <typename T>
 __device__ __forceinline__ void store_eight(T* p, const float (&v)[8], int n) {
-  if constexpr (VEC) {
-    if (n > 0)
-      *reinterpret_cast<uint4*>(p) =
-          make_uint4(pack_two<T>(v[0], v[1]), pack_two<T>(v[2], v[3]), pack_two<T>(v[4], v[5]), pack_two<T>(v[6], v[7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
-  }
+  if (n > 0)
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_two<T>(v[0], v[1]), pack_two<T>(v[2], v[3]), pack_two<T>(v[4], v[5]), pack_two<T>(v[6], v[7]));
 }
-template <bool VEC>
 __device__ __forceinline__ void store_eight(float* p, const float (&v)[8], int n) {
-  if constexpr (VEC) {
-    if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    if (n > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = v[i];
-  }
+  if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  if (n > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 inline bool valid_model_dtype(int dtype) { return dtype == DET_F32 || dtype == DET_BF16 || dtype == DET_F16; }

@@ -993,7 +993,7 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
 // expect: 16 of them took two waves.)  The bits do not depend on it.
 int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences, int time) {
   static std::mutex mu;
-  static std::map<std::tuple<const void*, int, int, unsigned>, int> cache;
+  static std::map<std::tuple<const void*, int, int, unsigned, size_t>, int> cache;
   int dev = 0;
   cudaGetDevice(&dev);
   int best = 0;
@@ -1002,7 +1002,7 @@ int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences
     int clusters = 0;
     {
       std::lock_guard<std::mutex> lk(mu);
-      int& known = cache[{kernel, dev, l, cfg.blockDim.x}];
+      int& known = cache[{kernel, dev, l, cfg.blockDim.x, cfg.dynamicSmemBytes}];
       if (known == 0) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
