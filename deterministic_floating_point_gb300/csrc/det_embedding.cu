@@ -3,7 +3,7 @@
 // The gradient is the row scatter-add of det_scatter_add_rows on tokens, for
 // 16-bit inputs too and without its slow case, a destination that many rows
 // aim at (the most frequent token of a text is met in every twentieth place):
-//   1. the positions are put in the order of their tokens, stably.  Up to 16,384 of
+//   1. the positions are put in the order of their tokens, stably.  Up to 32,768 of
 //      them 8 CTAs do so for an eighth of the tokens each (those with the same low
 //      bits), in shared memory, in two passes of 8 bits, and without a word to each
 //      other; the other SMs clear the first 96 MB of the table meanwhile.  (More: the
@@ -77,8 +77,9 @@ embedding_kernel(const T* table, int vocab, int dim, long long stride, const int
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kClassBits = 3, kClasses = 1 << kClassBits;          // CTAs: tokens by their low bits
 constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;           // of what is left of a token
-constexpr int kSortPer = 16;                                       // most positions a thread
-constexpr int kSortMost = kSortThreads * kSortPer, kPositionBits = 14;
+constexpr int kSortPer = 32;                                       // most positions a thread (a kernel for half of them
+                                                                   // takes 6 us less where it is enough)
+constexpr int kSortMost = kSortThreads * kSortPer, kPositionBits = 15;
 constexpr int kSortVocab = 1 << (2 * kDigitBits + kClassBits - 1); // (31 bits of a record are used)
 static_assert(kSortMost == 1 << kPositionBits && kPositionBits + 2 * kDigitBits <= 32, "a record is a word");
 
@@ -97,20 +98,21 @@ struct SortShared {
   unsigned scan[kSortWarps], below[kSortWarps];
   unsigned total, total_below;
   unsigned pad_[2];
-  // then two orders of the records (token above position)
+  // then the records in an order (token above position)
 };
 
 // A stable pass over the records, which lie in the order of warps, steps and lanes, by
-// the digit of their tokens at `shift`.
-__device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned (&record)[kSortPer], unsigned valid,
+// the digit of their tokens at `shift`, to `to`, where they may have come from.
+template <int PER>
+__device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned (&record)[PER], unsigned valid,
                                           int shift, unsigned* to) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned short* mine = s.warp_digits[warp];
   for (int d = lane; d < kDigits / 2; d += 32) reinterpret_cast<unsigned*>(mine)[d] = 0;
   __syncwarp();
-  unsigned in_warp[kSortPer];
+  unsigned in_warp[PER / 2];          // two a word: as many as a warp has records
 #pragma unroll
-  for (int k = 0; k < kSortPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     if (k >= per) break;
     const bool ok = valid >> k & 1;
     const unsigned digit = record[k] >> (kPositionBits + shift) & (kDigits - 1);
@@ -123,7 +125,7 @@ __device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned
     }
     const unsigned ahead = __popc(same & ((1u << lane) - 1));
     const unsigned before = ok ? mine[digit] : 0;
-    in_warp[k] = before + ahead;
+    in_warp[k / 2] = k % 2 ? in_warp[k / 2] | (before + ahead) << 16 : before + ahead;
     __syncwarp();
     if (ok && ahead == 0) mine[digit] = (unsigned short)(before + __popc(same));
     __syncwarp();
@@ -163,16 +165,17 @@ __device__ __forceinline__ void sort_pass(SortShared& s, int per, const unsigned
   if (threadIdx.x < kDigits) s.start[threadIdx.x] = s.scan[warp] + scan - all;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kSortPer; ++k) {
+  for (int k = 0; k < PER; ++k) {
     if (k >= per) break;
     if (!(valid >> k & 1)) continue;
     const unsigned digit = record[k] >> (kPositionBits + shift) & (kDigits - 1);
-    to[s.start[digit] + mine[digit] + in_warp[k]] = record[k];
+    to[s.start[digit] + mine[digit] + (in_warp[k / 2] >> 16 * (k % 2) & 0xffff)] = record[k];
   }
   __syncthreads();
 }
 
 // The first CTAs sort a class of tokens each; the others clear the table.
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads, 1)
 embedding_sort_kernel(SortArgs a) {
   extern __shared__ __align__(16) char s_raw[];
@@ -195,14 +198,14 @@ embedding_sort_kernel(SortArgs a) {
   }
   SortShared& s = *reinterpret_cast<SortShared*>(s_raw);
   unsigned* order = reinterpret_cast<unsigned*>(s_raw + sizeof(SortShared));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, size = a.per * kSortThreads;
-  unsigned record[kSortPer], valid = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned record[PER], valid = 0;
   {
     // the class' records in the order of their positions, and how many records lower classes have
     const int first = warp * 32 * a.per + lane;
     unsigned mine = 0, below = 0;
 #pragma unroll
-    for (int k = 0; k < kSortPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
       const int i = first + 32 * k;
       const int token = k < a.per && i < a.n ? a.tokens[i] : -1;
       record[k] = (unsigned)token >> kClassBits << kPositionBits | (unsigned)i;
@@ -234,7 +237,7 @@ embedding_sort_kernel(SortArgs a) {
     __syncthreads();
     unsigned at = s.scan[warp];
 #pragma unroll
-    for (int k = 0; k < kSortPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
       const unsigned ok = __ballot_sync(0xffffffffu, valid >> k & 1);
       if (valid >> k & 1) order[at + __popc(ok & ((1u << lane) - 1))] = record[k];
       at += __popc(ok);
@@ -246,7 +249,7 @@ embedding_sort_kernel(SortArgs a) {
   auto load = [&](const unsigned* from) {
     valid = 0;
 #pragma unroll
-    for (int k = 0; k < kSortPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
       const int q = first + 32 * k;
       if (k < per && q < total) {
         valid |= 1u << k;
@@ -255,8 +258,8 @@ embedding_sort_kernel(SortArgs a) {
     }
   };
   load(order);
-  sort_pass(s, per, record, valid, 0, order + size);
-  load(order + size);
+  sort_pass(s, per, record, valid, 0, order);
+  load(order);
   sort_pass(s, per, record, valid, kDigitBits, order);
   // the order, and where runs begin and end in it
   for (int q = threadIdx.x; q < total; q += kSortThreads) {
@@ -297,6 +300,8 @@ struct EmbedPlan {
 };
 EmbedPlan embed_plan(long long n, long long vocab, long long dim) {
   EmbedPlan p;
+  // (gradient of 20,000 x 2,048 in bf16 for 65,536 rows: 97 us, 134 by the library's sort; of 32,768 places of one
+  // token, which one CTA sorts alone, 107 against 48.)
   p.one_cta = n <= kSortMost && vocab <= kSortVocab;
   size_t at;
   if (p.one_cta) {
@@ -691,7 +696,8 @@ embedding_join_kernel(GradArgs a, O* out, int accumulate) {
   }
 }
 
-// Bytes that are cleared beside the sort, in the 18 us that it takes.
+// Bytes that are cleared beside the sort, in the 18 us that it takes for 16,384 positions.  (All of a table of 268 MB
+// before the sort: 42 us more.)
 constexpr size_t kClearWithSort = 96 << 20;
 
 // ---------------------------------------------------------------------------
@@ -724,13 +730,15 @@ int blocks(const void* grad, GradArgs a, int n, void* out, int accumulate, cudaS
   // vectors where every row of every operand starts on 16 bytes (rows of nodes do in the workspace then)
   const bool vec = vectors<T>(grad, a.stride) && vectors<O>(out, a.dim) && a.dim * sizeof(T) % 16 == 0;
   const unsigned slices = (unsigned)((a.dim + kSlice<T> - 1) / kSlice<T>);
-  // windows of 32 positions, shorter ones while they leave SMs without a warp
+  // windows of 32 positions, shorter ones while there are fewer than 8 warps an SM (500 x 1,024 in bf16: 26 us, with
+  // 32 positions 32; 16,384 x 2,048: 87 us with 16 positions, 79 with 32)
   int window = 32;
   while (window > 8 && (long long)slices * (n / window) < 8LL * 152) window /= 2;
-  const unsigned warps = (unsigned)((n + (long long)window - 1) / window), per_cta = warps < 8 && a.clear_from == a.vocab ? 1 : 8;
+  const unsigned warps = (unsigned)((n + (long long)window - 1) / window);
+  constexpr unsigned per_cta = 8;
   auto* kernel = vec ? embedding_blocks_kernel<T, O, true> : embedding_blocks_kernel<T, O, false>;
   const size_t smem = (size_t)per_cta * kStages * kEight * kPlace * 16;
-  const cudaError_t se = ensure_dyn_smem((const void*)kernel, 8 * kStages * kEight * kPlace * 16);
+  const cudaError_t se = ensure_dyn_smem((const void*)kernel, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_blocks");
   const long long sums = (long long)((warps + per_cta - 1) / per_cta) * slices;
   const long long clears = (a.vocab - a.clear_from + (long long)kClearRows * per_cta - 1) / (kClearRows * per_cta);
@@ -769,14 +777,15 @@ int cta_sort(const GradArgs& a, int n, int vocab, void* table, size_t bytes, cud
   g.long_runs = a.long_runs;
   g.table = static_cast<char*>(table);
   g.bytes = (long long)bytes;
-  const cudaError_t se = ensure_dyn_smem((const void*)embedding_sort_kernel, sizeof(SortShared) + (size_t)2 * kSortMost * 4);
+  auto* kernel = g.per > kSortPer / 2 ? embedding_sort_kernel<kSortPer> : embedding_sort_kernel<kSortPer / 2>;
+  const cudaError_t se = ensure_dyn_smem((const void*)kernel, sizeof(SortShared) + (size_t)kSortMost * 4);
   if (se != cudaSuccess) return cuda_fail(se, "det_embedding_sort");
   // CTAs that clear: one on each other SM, fewer for small tables
   const long long clear =
       table ? std::min<long long>(std::max(device_sm_count() - kClasses, 1), (long long)(bytes / (kSortThreads * 32)) + 1) : 0;
   launch_begin("det_embedding_sort", s);
-  const cudaError_t e = launch_dep(embedding_sort_kernel, dim3((unsigned)(kClasses + clear)), dim3(kSortThreads),
-                                   sizeof(SortShared) + (size_t)2 * g.per * kSortThreads * 4, s, g);
+  const cudaError_t e = launch_dep(kernel, dim3((unsigned)(kClasses + clear)), dim3(kSortThreads),
+                                   sizeof(SortShared) + (size_t)g.per * kSortThreads * 4, s, g);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_sort");
 }

