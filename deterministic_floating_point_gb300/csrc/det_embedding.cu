@@ -7,7 +7,7 @@
 //      them 8 CTAs do so for an eighth of the tokens each (those with the same low
 //      bits), in shared memory, in two passes of 8 bits, and without a word to each
 //      other; the other SMs clear the first 96 MB of the table meanwhile.  (More: the
-//      library's sort, after a clear of all.)
+//      library's sort.)
 //   2. every run of one token is cut into blocks of 32 by rank; a warp reduces a
 //      slice of the columns of every block that begins among its positions of the
 //      sorted order, streaming through them eight rows at a time whatever runs they
@@ -85,7 +85,7 @@ constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;           // of what is
 constexpr int kSortPer = 32;                                       // most positions a thread (a kernel for half of them
                                                                    // takes 6 us less where it is enough)
 constexpr int kSortMost = kSortThreads * kSortPer, kPositionBits = 15;
-constexpr int kSortVocab = 1 << (2 * kDigitBits + kClassBits - 1); // (31 bits of a record are used)
+constexpr int kSortVocab = 1 << (2 * kDigitBits + kClassBits);     // (31 bits of a record are used)
 static_assert(kSortMost == 1 << kPositionBits && kPositionBits + 2 * kDigitBits <= 32, "a record is a word");
 
 struct SortArgs {
@@ -857,7 +857,7 @@ extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, in
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < plan.total) return DET_ERR_WORKSPACE;
   const cudaStream_t s = as_stream(stream);
   const size_t table_bytes = (size_t)vocab * dim * model_elem_size(table_dtype);
-  if (!accumulate && (n == 0 || !plan.one_cta)) {
+  if (!accumulate && n == 0) {
     const cudaError_t e = cudaMemsetAsync(grad_table, 0, table_bytes, s);
     if (e != cudaSuccess) return cuda_fail(e, "det_embedding_backward: clear");
   }
@@ -882,6 +882,7 @@ extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, in
     a.perm = reinterpret_cast<const int32_t*>(w + plan.sort.idx[buffer]);
     a.run_start = reinterpret_cast<const int32_t*>(w + plan.sort.seg);
     a.run_end = a.run_start + 1;
+    if (!accumulate) a.clear_from = 0;
   }
   a.runs = reinterpret_cast<LongRun*>(w + plan.runs);
   a.nodes = reinterpret_cast<float*>(w + plan.nodes);

@@ -244,7 +244,8 @@ def test_empty_sizes(det):
 
 
 @pytest.mark.parametrize("n,vocab", [(70_000, 3), (16_384, 300_000), (16_385, 40), (200_000, 300_000),
-                                     (32_768, 3), (32_768, 200_000), (32_769, 3), (20_001, 262_144)])
+                                     (32_768, 3), (32_768, 200_000), (32_769, 3), (20_001, 262_144),
+                                     (5_000, 524_288), (5_000, 524_289)])
 def test_embedding_gradients_of_either_sort(det, n, vocab):
     """Runs of one token as long as the call, tables past the small sort's, tokens outside at both ends, values that are not
     finite: a column of NaN is the token's own."""
