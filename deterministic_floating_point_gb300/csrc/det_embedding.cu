@@ -413,10 +413,30 @@ template <int N> __device__ __forceinline__ void join(const Two (&v)[N], const T
   for (int i = 0; i < N; ++i) to[i] = add(node[i], v[i]);
 }
 // The first n of 2 P columns.
-template <typename O, int N>
+template <bool VEC, typename O, int N>
 __device__ __forceinline__ void load_cols(float (&v)[N], const O* p, int n) {
+  if (VEC && n == N) {
+    constexpr int W = N * (int)sizeof(O) / 4;
+    unsigned w[W];
+    if constexpr (W % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+      for (int i = 0; i < W; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned*>(p) + i);
+        w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+      }
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x, w[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(O) == 4) v[i] = __uint_as_float(w[i]);
+      else unpack_two(w[i], v[2 * i], v[2 * i + 1], O());
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+  }
 }
 template <bool VEC, typename O, int P>
 __device__ __forceinline__ void store_cols(O* p, const Two (&v)[P], int n) {
@@ -625,7 +645,7 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
         for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
         if (accumulate) {
           float old[COLS];
-          load_cols(old, to, nc);
+          load_cols<VEC>(old, to, nc);
 #pragma unroll
           for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);
         }
