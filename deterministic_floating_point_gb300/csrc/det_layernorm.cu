@@ -1,6 +1,6 @@
 // det_layer_norm and its gradients.
 //
-// A row lies in the registers of a group of threads: 32 to 1,024 of them, eight to
+// A row lies in the registers of a group of threads: whole warps, 1 to 32, eight to
 // 32 columns each (eights, the group's threads apart), so it is read once.
 // The mean is the rows' sum, the variance the sum of squares of what the mean
 // leaves -- two trees over the same columns, across lanes by shuffles and across
@@ -25,18 +25,26 @@ namespace {
 
 // (A Two holds two adjacent columns.)
 
+// Leaves of the tree over a row's warps: the least power of two of that many and more.  MOST: threads of a
+// CTA, which a row takes more than half of if there may be more than 256.
+template <int MOST>
+__device__ __forceinline__ int leaves_of(int warps) { return MOST > 256 ? MOST / 32 : 1 << (32 - __clz(warps - 1)); }
+
 // The lanes' sums of a group, in every thread: a tree over lanes, then over
 // warps through `slot` (one float a warp).  A group of one warp needs no barrier.
 __device__ __forceinline__ void put_warp(float* slot, float v, int warp, int lane) {
   if (lane == 0) slot[warp] = v;
 }
+template <int MOST>
 __device__ __forceinline__ float over_warps(const float* slot, int first_warp, int warps, int lane) {
-  if (warps == 8) {                    // the same tree, without shuffles
+  if (MOST == 256 && warps == 8) {                    // the same tree as below, without shuffles
     const float4 a = *reinterpret_cast<const float4*>(slot + first_warp), b = *reinterpret_cast<const float4*>(slot + first_warp + 4);
     return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
   }
-  float v = slot[first_warp + (lane & (warps - 1))];
-  for (int s = 1; s < warps; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  const int leaves = leaves_of<MOST>(warps), j = lane & (leaves - 1);
+  float v = j < warps ? slot[first_warp + j] : 0.0f;
+#pragma unroll
+  for (int s = 1; s < leaves; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
 __device__ __forceinline__ float lanes(Two v) {
@@ -49,18 +57,19 @@ __device__ __forceinline__ float inverse_root(float v) {
   return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0, infinite and NaN as they are
 }
 
-// A group's place: `threads` (a power of two) of them take a row.
+// A group's place: `threads` of them, whole warps, take a row.  ONE: it is the CTA.
+template <bool ONE>
 struct Group {
   int me, threads, warps, warp, first_warp, lane, index, count;
-  __device__ __forceinline__ explicit Group(int log2_threads) {
-    threads = 1 << log2_threads;
-    me = threadIdx.x & (threads - 1);
+  __device__ __forceinline__ explicit Group(int threads_of_a_row) {
+    threads = threads_of_a_row;
     warps = threads >> 5;
     warp = threadIdx.x >> 5;
+    index = ONE ? 0 : warp / warps;
+    me = threadIdx.x - index * threads;
     lane = threadIdx.x & 31;
-    index = threadIdx.x >> log2_threads;
     first_warp = index * warps;
-    count = blockDim.x >> log2_threads;
+    count = ONE ? 1 : (blockDim.x >> 5) / warps;
   }
 };
 
@@ -81,7 +90,8 @@ template <typename T, bool VEC, int K> struct Columns {
   int read;              // the first column that the thread copies: in 32 bits vectors lie lane after lane
   int n[K];              // VEC: columns of the thread's eights; else columns of the row from the first one on
   int span[K];           // columns of the row from the first one that it copies on
-  __device__ __forceinline__ Columns(const Group& g, int cols) {
+  template <typename G>
+  __device__ __forceinline__ Columns(const G& g, int cols) {
     const int warp = (g.me & ~31) * 8;                   // the warp's first
     first = VEC ? g.me * 8 : warp;
     read = VEC && sizeof(T) == 4 ? warp + 4 * g.lane : first;
@@ -302,13 +312,15 @@ __host__ __device__ constexpr int whole_eights(int cols) { return (cols + 7) / 8
 
 // A weight or bias in shared memory, where they leave registers for rows: halves of
 // eights, so that a warp reads 512 bytes in a row.
-__device__ __forceinline__ void keep_param(float4* s, const void* p, const Group& g, int k, int cols, int dtype, float other) {
+template <typename G>
+__device__ __forceinline__ void keep_param(float4* s, const void* p, const G& g, int k, int cols, int dtype, float other) {
   Two v[4];
   load_param(v, p, (g.me + k * g.threads) * 8, cols, dtype, other);
   s[(2 * k) * g.threads + g.me] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   s[(2 * k + 1) * g.threads + g.me] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
-__device__ __forceinline__ void param(Two (&v)[4], const float4* s, const Group& g, int k) {
+template <typename G>
+__device__ __forceinline__ void param(Two (&v)[4], const float4* s, const G& g, int k) {
   const float4 a = s[(2 * k) * g.threads + g.me], b = s[(2 * k + 1) * g.threads + g.me];
   v[0] = two(a.x, a.y), v[1] = two(a.z, a.w), v[2] = two(b.x, b.y), v[3] = two(b.z, b.w);
 }
@@ -316,12 +328,12 @@ __device__ __forceinline__ void param(Two (&v)[4], const float4* s, const Group&
 template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1024 / MOST : K == 1 ? 4 : 3)
 layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const void* weight, const void* bias,
-                  int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int log2_threads, int stages) {
+                  int param_dtype, float eps, T* out, float* mean_out, float* rstd_out, int threads, int stages) {
   __shared__ __align__(16) float s_sum[32], s_sq[32];
   extern __shared__ __align__(16) char s_dynamic[];
   dep_wait();
   dep_launch();
-  const Group g(log2_threads);
+  const Group<(MOST > 256)> g(threads);
   // weight and bias are in registers where CTAs of 256 threads leave enough of them (48 us for 16,384 x 4,096 in bf16 against
   // 52 with shared memory), else in shared memory
   constexpr bool HELD = MOST == 256;
@@ -375,7 +387,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
     if (g.warps > 1) {
       put_warp(s_sum, sum, g.warp, g.lane);
       __syncthreads();
-      sum = over_warps(s_sum, g.first_warp, g.warps, g.lane);
+      sum = over_warps<MOST>(s_sum, g.first_warp, g.warps, g.lane);
     }
     const float mean = sum * of;
     const Two minus_mean = twice(-mean);
@@ -393,7 +405,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
     if (g.warps > 1) {
       put_warp(s_sq, sq, g.warp, g.lane);
       __syncthreads();
-      sq = over_warps(s_sq, g.first_warp, g.warps, g.lane);
+      sq = over_warps<MOST>(s_sq, g.first_warp, g.warps, g.lane);
     }
     const float rstd = inverse_root(fmaf(sq, of, eps));
     const Two rstd2 = twice(rstd);
@@ -425,7 +437,7 @@ template <typename T, int K, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : K == 1 ? 3 : 2)
 layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long long x_stride, unsigned rows, int cols,
                        const float* means, const float* rstds, const void* weight, int param_dtype, T* grad_x,
-                       float* part, int log2_threads, int stages) {
+                       float* part, int threads, int stages) {
   __shared__ __align__(16) Two s_sums[2][32];
   // where the columns' sums take half of the registers, rows are read from shared memory twice
   constexpr bool LATE = K == 4;
@@ -433,7 +445,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
   dep_wait();
   dep_launch();
-  const Group g(log2_threads);
+  const Group<false> g(threads);
   float4* s_w = reinterpret_cast<float4*>(s_dynamic);
   char* mine_x = reinterpret_cast<char*>(s_w + 2 * K * g.threads) +
                  g.warp * (2 * feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
@@ -521,8 +533,9 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         for (int i = 0; i < 4; ++i) t[i] = add(two(q[i].x, q[i].y), two(q[i].z, q[i].w));
         sums = add(add(t[0], t[1]), add(t[2], t[3]));
       } else {
-        sums = s_sums[parity][g.first_warp + (g.lane & (g.warps - 1))];
-        for (int d = 1; d < g.warps; d <<= 1)
+        const int leaves = leaves_of<256>(g.warps), j = g.lane & (leaves - 1);
+        sums = j < g.warps ? s_sums[parity][g.first_warp + j] : twice(0.0f);
+        for (int d = 1; d < leaves; d <<= 1)
           sums = add(sums, two(__shfl_xor_sync(0xffffffffu, sums.x, d), __shfl_xor_sync(0xffffffffu, sums.y, d)));
       }
     }
@@ -606,21 +619,20 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
 }
 
 // Eights of columns a thread takes (two keep a row's sums over lanes and warps short), and
-// the threads that take a row, as a logarithm.  The gradient of wide rows takes four: 1,024 threads
-// of 64 registers each spill (4,096 x 16,384 in bf16: 182 us, 82 with 512 that take twice as much).
+// the threads that take a row: as many warps as its columns need (13,107 x 5,120 in bf16, 10 warps: 53 and 98 us; with
+// the next power of two, 16 of them: 86 and 113).  The gradient of wide rows takes four eights: 1,024 threads of 64
+// registers each spill (4,096 x 16,384 in bf16: 182 us, 98 with 512 that take twice as much).
 int eights(int64_t cols) { return cols > 256 ? 2 : 1; }
 int grad_eights(int64_t cols) { return cols > 8192 ? 4 : eights(cols); }
 int row_threads(int64_t cols, int eights) {
-  int l = 5;
-  while ((8LL * eights << l) < cols) ++l;
-  return l;
+  return (int)std::max<int64_t>(1, (cols + 256 * eights - 1) / (256 * eights)) * 32;
 }
 // CTAs of the gradient, each of which leaves a partial sum: as many as run at once on
 // the 152 SMs, by a constant, because the sums' order hangs on it.
 int grad_parts(int64_t rows, int64_t cols) {
-  const int l = row_threads(cols, grad_eights(cols));
-  const int64_t at_a_time = std::max<int64_t>(1, kThreads >> l);
-  const int at_once = 152 * (l > 8 ? 1 : grad_eights(cols) == 1 ? 3 : 2);
+  const int threads = row_threads(cols, grad_eights(cols));
+  const int64_t at_a_time = std::max(1, kThreads / threads);
+  const int at_once = 152 * (threads > kThreads ? 1 : grad_eights(cols) == 1 ? 3 : 2);
   return (int)std::min<int64_t>((rows + at_a_time - 1) / at_a_time, at_once);
 }
 
@@ -632,10 +644,10 @@ bool vectors(const void* p, int64_t stride, int64_t cols) {
 // Rows that are copied ahead, and the dynamic shared memory: two, or one where 32-bit
 // rows of more than 8,192 columns leave no room.
 template <typename T, bool VEC, int K>
-size_t room(int params, int operands, int log2_threads, int threads, int* stages) {
+size_t room(int params, int operands, int row_threads, int threads, int* stages) {
   size_t bytes = 0;
   for (*stages = 2; *stages > 0; --*stages) {
-    bytes = ((size_t)params * K * 32 << log2_threads) +
+    bytes = (size_t)params * K * 32 * row_threads +
             threads / 32 * (size_t)(operands * feed_bytes<T, VEC, K>(*stages) + turn_bytes<T, VEC>());
     if (bytes <= 226 * 1024 || *stages == 1) break;
   }
@@ -645,10 +657,10 @@ size_t room(int params, int operands, int log2_threads, int threads, int* stages
 template <typename T, int K, bool VEC, int MOST>
 int forward(const void* x, int rows, int cols, int64_t x_stride, const void* weight, const void* bias, int param_dtype,
             float eps, void* out, float* mean_out, float* rstd_out, cudaStream_t s) {
-  const int l = row_threads(cols, K), threads = std::max(kThreads, 1 << l), at_a_time = threads >> l;
+  const int of_a_row = row_threads(cols, K), at_a_time = std::max(1, kThreads / of_a_row), threads = at_a_time * of_a_row;
   auto* k = layer_norm_kernel<T, K, VEC, MOST>;
   int stages = 1;
-  const size_t smem = room<T, VEC, K>(MOST == 256 ? 0 : 2, 1, l, threads, &stages);
+  const size_t smem = room<T, VEC, K>(MOST == 256 ? 0 : 2, 1, of_a_row, threads, &stages);
   const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm");
   const int per_sm = kernel_occupancy((const void*)k, threads, smem);
@@ -658,7 +670,7 @@ int forward(const void* x, int rows, int cols, int64_t x_stride, const void* wei
   launch_begin("det_layer_norm", s);
   const cudaError_t e = launch_dep(k, dim3((unsigned)grid), dim3(threads), smem, s, static_cast<const T*>(x),
                                    (unsigned)rows, cols, (long long)x_stride, weight, bias, param_dtype, eps,
-                                   static_cast<T*>(out), mean_out, rstd_out, l, stages);
+                                   static_cast<T*>(out), mean_out, rstd_out, of_a_row, stages);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm");
 }
@@ -667,19 +679,19 @@ template <typename T, int K, bool VEC, int MOST>
 int backward(const void* grad, int64_t grad_stride, const void* x, int64_t x_stride, int rows, int cols,
              const float* mean, const float* rstd, const void* weight, int param_dtype, void* grad_x, float* part,
              cudaStream_t s) {
-  const int l = row_threads(cols, K), threads = std::max(kThreads, 1 << l);
+  const int of_a_row = row_threads(cols, K), groups = std::max(1, kThreads / of_a_row), threads = groups * of_a_row;
   auto* k = layer_norm_grad_kernel<T, K, VEC, MOST>;
   int stages = 1;
   // weight and rows; the groups' sums take their place at the end
-  const size_t sums = (threads >> l) > 1 ? (size_t)(threads >> l) * whole_eights(cols) * sizeof(float) : 0;
-  const size_t smem = std::max(room<T, VEC, K>(1, 2, l, threads, &stages), sums);
+  const size_t sums = groups > 1 ? (size_t)groups * whole_eights(cols) * sizeof(float) : 0;
+  const size_t smem = std::max(room<T, VEC, K>(1, 2, of_a_row, threads, &stages), sums);
   const cudaError_t se = ensure_dyn_smem((const void*)k, smem);
   if (se != cudaSuccess) return cuda_fail(se, "det_layer_norm_backward");
   launch_begin("det_layer_norm_backward", s);
   const cudaError_t e = launch_dep(k, dim3((unsigned)grad_parts(rows, cols)), dim3(threads), smem, s,
                                    static_cast<const T*>(grad), (long long)grad_stride, static_cast<const T*>(x),
                                    (long long)x_stride, (unsigned)rows, cols, mean, rstd, weight, param_dtype,
-                                   static_cast<T*>(grad_x), part, l, stages);
+                                   static_cast<T*>(grad_x), part, of_a_row, stages);
   launch_end(s);
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_layer_norm_backward");
 }
