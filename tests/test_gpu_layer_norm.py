@@ -71,7 +71,8 @@ def check_forward(r, x, w, b, eps):
 
 
 def column_depth(rows, cols):
-    """Additions on a column's way: a register's, the groups of a CTA, a strand of the join and its tree."""
+    """Additions on a column's way: a register's, the groups of a CTA, a strand of the join and its tree.  (A row takes the
+    warps it needs, here rounded up to a power of two: 256 threads hold as many groups of 3 warps as of 4, of 5 as of 8.)"""
     eights = 2 if cols > 256 else 1
     threads = max(32, 1 << max(0, math.ceil(math.log2(cols / (8 * eights)))))
     at_a_time = max(1, 256 // threads)
@@ -114,7 +115,7 @@ def make(rows, cols, dtype, seed, offset=1.0):
 
 SIZES = [(0, 8), (1, 1), (3, 2), (5, 7), (8, 8), (9, 31), (33, 32), (2, 255), (3, 256), (3, 257), (700, 64), (17, 511),
          (4, 512), (5, 513), (1300, 100), (3, 1000), (3, 1024), (650, 1030), (2, 2048), (3, 4095), (310, 4096), (2, 4097),
-         (3, 8192), (2, 8200), (160, 16376), (3, 16383), (2, 16384)]
+         (3, 8192), (2, 8200), (160, 16376), (3, 16383), (2, 16384), (450, 1401), (700, 2500), (330, 6000), (200, 10300)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)
