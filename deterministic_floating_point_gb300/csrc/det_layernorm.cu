@@ -14,7 +14,7 @@
 // function of rows and cols, so the order of every sum is too.
 //
 // Bytes bound it: 16,384 x 4,096 in bf16 take 42 us (a copy of as many bytes 45), 60% of the issue slots,
-// the gradients 71 (5.7 TB/s); 65,536 x 4,096 in bf16 166 and 258 us, 6.5 and 6.2 TB/s.  A few rows: the launch and
+// the gradients 73 (5.5 TB/s); 65,536 x 4,096 in bf16 166 and 266 us, 6.5 and 6.1 TB/s.  A few rows: the launch and
 // one row's chain of a copy, two sums across the group (one in the gradient) and a store, about 6 us.
 #include "det_model.cuh"
 
@@ -25,27 +25,20 @@ namespace {
 
 // (A Two holds two adjacent columns.)
 
-// Leaves of the tree over a row's warps: the least power of two of that many and more.  MOST: threads of a
-// CTA, which a row takes more than half of if there may be more than 256.
-template <int MOST>
-__device__ __forceinline__ int leaves_of(int warps) { return MOST > 256 ? MOST / 32 : 1 << (32 - __clz(warps - 1)); }
-
-// The lanes' sums of a group, in every thread: a tree over lanes, then over
-// warps through `slot` (one float a warp).  A group of one warp needs no barrier.
-__device__ __forceinline__ void put_warp(float* slot, float v, int warp, int lane) {
-  if (lane == 0) slot[warp] = v;
-}
-template <int MOST>
-__device__ __forceinline__ float over_warps(const float* slot, int first_warp, int warps, int lane) {
-  if (MOST == 256 && warps == 8) {                    // the same tree as below, without shuffles
-    const float4 a = *reinterpret_cast<const float4*>(slot + first_warp), b = *reinterpret_cast<const float4*>(slot + first_warp + 4);
+// The lanes' sums of a group, in every thread: a tree over lanes, then over warps
+// through `slot`, where a group has LEAVES places (those of no warp are 0).  A group of
+// one warp needs no barrier.
+template <int LEAVES>
+__device__ __forceinline__ float over_warps(const float* slot, int lane) {
+  if constexpr (LEAVES == 8) {         // the same tree as below, without shuffles
+    const float4 a = *reinterpret_cast<const float4*>(slot), b = *reinterpret_cast<const float4*>(slot + 4);
     return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
-  }
-  const int leaves = leaves_of<MOST>(warps), j = lane & (leaves - 1);
-  float v = j < warps ? slot[first_warp + j] : 0.0f;
+  } else {
+    float v = slot[lane & (LEAVES - 1)];
 #pragma unroll
-  for (int s = 1; s < leaves; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  return v;
+    for (int s = 1; s < LEAVES; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    return v;
+  }
 }
 __device__ __forceinline__ float lanes(Two v) {
   return __fadd_rn(v.x, v.y);
@@ -57,19 +50,23 @@ __device__ __forceinline__ float inverse_root(float v) {
   return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0, infinite and NaN as they are
 }
 
-// A group's place: `threads` of them, whole warps, take a row.  ONE: it is the CTA.
-template <bool ONE>
+// A group's place: `threads` of them, whole warps, take a row, of a CTA of MOST threads and less.
+template <int MOST>
 struct Group {
-  int me, threads, warps, warp, first_warp, lane, index, count;
+  static constexpr int LEAVES = MOST / 32;       // of the tree over its warps (`leaves` of them are enough)
+  int me, threads, warps, warp, lane, index, count;
+  int leaves, first_leaf, leaf;
   __device__ __forceinline__ explicit Group(int threads_of_a_row) {
     threads = threads_of_a_row;
     warps = threads >> 5;
     warp = threadIdx.x >> 5;
-    index = ONE ? 0 : warp / warps;
+    index = warp / warps;
     me = threadIdx.x - index * threads;
     lane = threadIdx.x & 31;
-    first_warp = index * warps;
-    count = ONE ? 1 : (blockDim.x >> 5) / warps;
+    count = (blockDim.x >> 5) / warps;
+    leaves = 1 << (32 - __clz(warps - 1));
+    first_leaf = index * (MOST > 256 ? leaves : LEAVES);       // (four groups of two warps and more have 32)
+    leaf = first_leaf + (me >> 5);
   }
 };
 
@@ -80,8 +77,8 @@ struct Group {
 // Where rows or outputs do not all start on 16 bytes (VEC is false), the vectors that hold a
 // row's columns are copied and shifted as they are taken (what else such a first vector holds
 // is not the row's, but lies beside it in 16 bytes); outputs go through the warp's part of
-// shared memory to words in the order of memory.  (Gradient of 16,384 x 4,095 in bf16: 127 us; rows copied
-// word by word 133, read and written element by element 176.  16,384 x 4,096: 78.)
+// shared memory to words in the order of memory.  (Gradient of 16,384 x 4,095 in bf16: 125 us; rows copied
+// word by word 133, read and written element by element 176.  16,384 x 4,096: 80.)
 
 // Where a thread reads and writes in a row: its first column, and how many of each
 // of its eights there are.
@@ -333,7 +330,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
   extern __shared__ __align__(16) char s_dynamic[];
   dep_wait();
   dep_launch();
-  const Group<(MOST > 256)> g(threads);
+  const Group<MOST> g(threads);
   // weight and bias are in registers where CTAs of 256 threads leave enough of them (48 us for 16,384 x 4,096 in bf16 against
   // 52 with shared memory), else in shared memory
   constexpr bool HELD = MOST == 256;
@@ -365,6 +362,8 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
       keep_param(s_b, bias, g, k, cols, param_dtype, 0.0f);
     }
   }
+  if (threadIdx.x < 32) s_sum[threadIdx.x] = s_sq[threadIdx.x] = 0.0f;
+  __syncthreads();
   int stage = 0;
   // (every thread of the CTA makes as many rounds)
   for (unsigned first = blockIdx.x * g.count; first < rows; first += step, r += step, to += (long long)step * cols) {
@@ -385,9 +384,9 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
     if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sum = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
-      put_warp(s_sum, sum, g.warp, g.lane);
+      if (g.lane == 0) s_sum[g.leaf] = sum;
       __syncthreads();
-      sum = over_warps<MOST>(s_sum, g.first_warp, g.warps, g.lane);
+      sum = over_warps<MOST / 32>(s_sum + g.first_leaf, g.lane);
     }
     const float mean = sum * of;
     const Two minus_mean = twice(-mean);
@@ -403,9 +402,9 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
     if (K == 2) t[0] = add(t[0], t[K - 1]);
     float sq = warp_pt(lanes(t[0]));
     if (g.warps > 1) {
-      put_warp(s_sq, sq, g.warp, g.lane);
+      if (g.lane == 0) s_sq[g.leaf] = sq;
       __syncthreads();
-      sq = over_warps<MOST>(s_sq, g.first_warp, g.warps, g.lane);
+      sq = over_warps<MOST / 32>(s_sq + g.first_leaf, g.lane);
     }
     const float rstd = inverse_root(fmaf(sq, of, eps));
     const Two rstd2 = twice(rstd);
@@ -445,7 +444,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
   float* s_acc = reinterpret_cast<float*>(s_dynamic);
   dep_wait();
   dep_launch();
-  const Group<false> g(threads);
+  const Group<MOST> g(threads);
   float4* s_w = reinterpret_cast<float4*>(s_dynamic);
   char* mine_x = reinterpret_cast<char*>(s_w + 2 * K * g.threads) +
                  g.warp * (2 * feed_bytes<T, VEC, K>(stages) + turn_bytes<T, VEC>());
@@ -469,6 +468,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     from_grad += step * grad_stride;
   };
   for (int i = 0; i < stages; ++i) ask(i);
+  if (threadIdx.x < 64) s_sums[threadIdx.x >> 5][threadIdx.x & 31] = twice(0.0f);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (g.index == 0) keep_param(s_w, weight, g, k, cols, param_dtype, 1.0f);
@@ -524,17 +524,19 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
     for (int d = 1; d < 32; d <<= 1)
       sums = add(sums, two(__shfl_xor_sync(0xffffffffu, sums.x, d), __shfl_xor_sync(0xffffffffu, sums.y, d)));
     if (g.warps > 1) {
-      if (g.lane == 0) s_sums[parity][g.warp] = sums;
+      if (g.lane == 0) s_sums[parity][g.leaf] = sums;
       __syncthreads();
-      if (g.warps == 8) {              // the same tree, without shuffles
-        const float4* q = reinterpret_cast<const float4*>(&s_sums[parity][g.first_warp]);
+      if constexpr (MOST == 256) {     // the same tree as below, without shuffles
+        const float4* q = reinterpret_cast<const float4*>(&s_sums[parity][g.first_leaf]);
         Two t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = add(two(q[i].x, q[i].y), two(q[i].z, q[i].w));
         sums = add(add(t[0], t[1]), add(t[2], t[3]));
       } else {
-        const int leaves = leaves_of<256>(g.warps), j = g.lane & (leaves - 1);
-        sums = j < g.warps ? s_sums[parity][g.first_warp + j] : twice(0.0f);
+        // (with four eights a loop whose length is not known here: unrolled it took the registers of the columns' sums,
+        // 4,096 x 16,384 in bf16 98 us against 82)
+        const int leaves = K == 4 ? g.leaves : MOST / 32;
+        sums = s_sums[parity][g.first_leaf + (g.lane & (leaves - 1))];
         for (int d = 1; d < leaves; d <<= 1)
           sums = add(sums, two(__shfl_xor_sync(0xffffffffu, sums.x, d), __shfl_xor_sync(0xffffffffu, sums.y, d)));
       }
@@ -619,9 +621,9 @@ layer_norm_join_kernel(const float* part, int parts, int cols, void* grad_weight
 }
 
 // Eights of columns a thread takes (two keep a row's sums over lanes and warps short), and
-// the threads that take a row: as many warps as its columns need (13,107 x 5,120 in bf16, 10 warps: 53 and 98 us; with
+// the threads that take a row: as many warps as its columns need (13,107 x 5,120 in bf16, 10 warps: 53 and 92 us; with
 // the next power of two, 16 of them: 86 and 113).  The gradient of wide rows takes four eights: 1,024 threads of 64
-// registers each spill (4,096 x 16,384 in bf16: 182 us, 98 with 512 that take twice as much).
+// registers each spill (4,096 x 16,384 in bf16: 182 us, 82 with 512 that take twice as much).
 int eights(int64_t cols) { return cols > 256 ? 2 : 1; }
 int grad_eights(int64_t cols) { return cols > 8192 ? 4 : eights(cols); }
 int row_threads(int64_t cols, int eights) {
