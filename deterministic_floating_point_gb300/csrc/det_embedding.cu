@@ -18,7 +18,7 @@
 // sums are those of det_scatter_add_rows bit for bit.
 //
 // Bytes bound both.  16,384 rows of 2,048 in 32 bits to bf16: 20 us (116 MB, some rows many times: 17 at the copy's
-// rate), one launch.  The gradient of 16,384 x 2,048 for 65,536 rows in bf16 (332 MB, 50 us at that rate) takes 79:
+// rate), one launch.  The gradient of 16,384 x 2,048 for 65,536 rows in bf16 (332 MB, 50 us at that rate) takes 77:
 // 18 for the sort, which the clear of 96 MB fills, 49 for the sums and the rest of the clear, 5 for the join, and
 // starts and ends of launches.
 #include "det_sort.cuh"
