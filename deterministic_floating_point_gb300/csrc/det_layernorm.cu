@@ -542,8 +542,9 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       }
     }
     if (grad_x) {
-      // rstd (gw - sums.x / cols) - (x - mean) rstd^2 sums.y / cols
-      const Two minus_one = twice(-sums.x * of * rstd2.x), minus_two = twice(-sums.y * of * rstd2.x * rstd2.x);
+      // rstd (gw - sums.x / cols - (x - mean) rstd sums.y / cols).  (rstd^2 would pass 32 bits where rstd does not, at
+      // deviations below 5e-20 without an eps; rstd sums.y / cols is as large as the result.)
+      const Two minus_one = twice(-sums.x * of), minus_two = twice(-sums.y * of * rstd2.x);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Two xh[4], d[4], w[4];
@@ -553,7 +554,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = fma(add(xh[i], minus_mean), minus_two, fma(mul(d[i], w[i]), rstd2, minus_one));
+          const Two f = mul(fma(add(xh[i], minus_mean), minus_two, fma(d[i], w[i], minus_one)), rstd2);
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
         }
