@@ -345,10 +345,10 @@ struct GradArgs {
   int clear_from, clear_rows;         // the first row that is still to be cleared, and the rows of a warp (at most 32)
 };
 
+// (A row that is not added to counts as +0.0: a sum of -0.0 becomes +0.0, as det_scatter_add_rows has it.)
 template <typename O>
 __device__ __forceinline__ float finish(float sum, float scale, const O* old, bool accumulate) {
-  const float v = __fmul_rn(sum, scale);
-  return accumulate ? __fadd_rn(to_f32(*old), v) : v;
+  return __fadd_rn(accumulate ? to_f32(*old) : 0.0f, __fmul_rn(sum, scale));
 }
 
 // A lane's columns of a row: 16 bytes of T.  VEC: aligned, and all or none of them.
@@ -571,7 +571,6 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
 #pragma unroll
   for (int g = 0; g < kStages; ++g) asked = ask(asked, g);
   Two st[5][PAIRS];              // pending nodes of a block's tree: 1, 2, 4, 8, 16 rows
-  const Two scale = twice(a.scale);
   int stage = 0;
   for (int p = p0; p <= p1;) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -642,13 +641,11 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       if (last_node) {
         O* to = out + (long long)m.y * a.dim + c;
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], scale);
-        if (accumulate) {
-          float old[COLS];
-          load_cols<VEC>(old, to, nc);
+        for (int i = 0; i < PAIRS; ++i) v[i] = two(__fmul_rn(v[i].x, a.scale), __fmul_rn(v[i].y, a.scale));
+        float old[COLS] = {};          // (as in finish(); products of pairs would become one instruction with the sums)
+        if (accumulate) load_cols<VEC>(old, to, nc);
 #pragma unroll
-          for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);
-        }
+        for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);
         store_cols<VEC>(to, v, nc);
       } else {
         const long long start = w0 + q - rank;

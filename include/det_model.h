@@ -185,12 +185,12 @@ int det_embedding(const void* table, int table_dtype, int64_t vocab, int64_t dim
 
 /* ------------------------------------------------------------------------
  * det_embedding_backward -- the gradient of det_embedding's table:
- *   grad_table[v] = scale * PT(grad[i] : tokens[i] = v, i rising), per column,
+ *   grad_table[v] = old + scale * PT(grad[i] : tokens[i] = v, i rising), per column,
  * the canonical pairwise tree of det_scatter_add_rows in 32 bits, times scale,
- * rounded once to table_dtype: with DET_F32 and a scale of 1 the bits of
- * det_scatter_add_rows on a table of zeros.  Rows of no token are +0.0.  With
- * accumulate, what the row holds is added (in 32 bits, before the rounding), and
- * rows of no token are neither read nor written.
+ * plus +0.0 or, with accumulate, what the row holds (in 32 bits), rounded once to
+ * table_dtype: with DET_F32 and a scale of 1 the bits of det_scatter_add_rows, with
+ * accumulate on the same table, without on one of zeros.  Rows of no token are +0.0;
+ * with accumulate they are neither read nor written.
  *   grad        device, n x dim of dtype; row i starts at element i * grad_stride.
  *               Rows of tokens outside [0, vocab) are not read
  *   grad_table  device, vocab x dim of table_dtype, contiguous (written); must
