@@ -641,8 +641,8 @@ embedding_blocks_kernel(const T* grad, GradArgs a, O* out, int accumulate, int w
       if (last_node) {
         O* to = out + (long long)m.y * a.dim + c;
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) v[i] = two(__fmul_rn(v[i].x, a.scale), __fmul_rn(v[i].y, a.scale));
-        float old[COLS] = {};          // (as in finish(); products of pairs would become one instruction with the sums)
+        for (int i = 0; i < PAIRS; ++i) v[i] = mul(v[i], twice(a.scale));
+        float old[COLS] = {};          // (as in finish())
         if (accumulate) load_cols<VEC>(old, to, nc);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) v[i] = add(two(old[2 * i], old[2 * i + 1]), v[i]);

@@ -395,7 +395,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[k][i] = add(v[k][i], minus_mean);
       if (!whole) keep_first(v[k], cols - (g.me + k * g.threads) * 8);
-      t[k] = mul(v[k][0], v[k][0]);
+      t[k] = factor(v[k][0], v[k][0]);
 #pragma unroll
       for (int i = 1; i < 4; ++i) t[k] = fma(v[k][i], v[k][i], t[k]);
     }
@@ -418,7 +418,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = fma(mul(v[k][i], rstd2), HELD ? held_w[HELD ? k : 0][i] : w[i], HELD ? held_b[HELD ? k : 0][i] : b[i]);
+        const float2 f = fma(factor(v[k][i], rstd2), HELD ? held_w[HELD ? k : 0][i] : w[i], HELD ? held_b[HELD ? k : 0][i] : b[i]);
         y[2 * i] = f.x;
         y[2 * i + 1] = f.y;
       }
@@ -501,15 +501,15 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
       pairs_of(LATE ? feed_x.eight(stage, k, off_x, g.lane) : cx[k], xh);
       pairs_of(LATE ? feed_grad.eight(stage, k, off_grad, g.lane) : cg[k], d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = mul(add(xh[i], minus_mean), rstd2);
+      for (int i = 0; i < 4; ++i) xh[i] = factor(add(xh[i], minus_mean), rstd2);
       if (!whole) keep_first(xh, cols - (g.me + k * g.threads) * 8);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         aw[k][i] = fma(d[i], xh[i], aw[k][i]);
         ab[k][i] = add(ab[k][i], d[i]);
-        d[i] = mul(d[i], w[i]);
-        t1[k] = i ? add(t1[k], d[i]) : d[i];
-        t2[k] = i ? fma(d[i], xh[i], t2[k]) : mul(d[i], xh[i]);
+        const Two gw = factor(d[i], w[i]);
+        t1[k] = i ? fma(d[i], w[i], t1[k]) : gw;
+        t2[k] = i ? fma(gw, xh[i], t2[k]) : factor(gw, xh[i]);
       }
     }
 #pragma unroll
@@ -554,7 +554,7 @@ layer_norm_grad_kernel(const T* grad, long long grad_stride, const T* x, long lo
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const Two f = mul(fma(add(xh[i], minus_mean), minus_two, fma(d[i], w[i], minus_one)), rstd2);
+          const Two f = factor(fma(add(xh[i], minus_mean), minus_two, fma(d[i], w[i], minus_one)), rstd2);
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
         }
