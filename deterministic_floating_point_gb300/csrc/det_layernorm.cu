@@ -50,6 +50,17 @@ __device__ __forceinline__ float inverse_root(float v) {
   return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0, infinite and NaN as they are
 }
 
+// sum / n to nearest, for a whole number n below 2^15 and of = 1 / n to nearest (the product alone is a step off where n * of
+// rounds to less than 1: 1,000 in each of 41 columns had a mean of 999.99994).  The product q is off by less than 2 steps of
+// its last place; sum and n q are multiples of such a step, so what is left, n q from sum, is exact; and a quotient by n
+// lies no nearer than 1 / (2 n) steps to the middle between two values, where the last sum's error of 2^-22 of a step would
+// matter.  (Means below 2^-126 may be a step off.  A division instead: 87,381 x 768 in bf16 56.9 us against 54.1; the product
+// alone 53.7.)  NaN where the sum is infinite.
+__device__ __forceinline__ float mean_of(float sum, float n, float of) {
+  const float q = __fmul_rn(sum, of);
+  return fmaf(fmaf(-q, n, sum), of, q);
+}
+
 // A group's place: `threads` of them, whole warps, take a row, of a CTA of MOST threads and less.
 template <int MOST>
 struct Group {
@@ -388,7 +399,7 @@ layer_norm_kernel(const T* x, unsigned rows, int cols, long long x_stride, const
       __syncthreads();
       sum = over_warps<MOST / 32>(s_sum + g.first_leaf, g.lane);
     }
-    const float mean = sum * of;
+    const float mean = mean_of(sum, (float)cols, of);
     const Two minus_mean = twice(-mean);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
