@@ -44,10 +44,11 @@ __device__ __forceinline__ float lanes(Two v) {
   return __fadd_rn(v.x, v.y);
 }
 
-// 1 / sqrt(v) from the hardware's approximation by a step of Newton's method.
+// 1 / sqrt(v) from the hardware's approximation by a step of Newton's method.  NaN for an infinite v, a sum of squares that
+// has left 32 bits: 0 would make the row's results its bias.
 __device__ __forceinline__ float inverse_root(float v) {
   const float r = rsqrtf(v), e = fmaf(-0.5f * v * r, r, 0.5f);
-  return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0, infinite and NaN as they are
+  return v > 0.0f && r < 1e18f ? fmaf(r, e, r) : r;       // 0 and NaN as they are
 }
 
 // sum / n to nearest, for a whole number n below 2^15 and of = 1 / n to nearest (the product alone is a step off where n * of
@@ -754,7 +755,7 @@ extern "C" int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t co
                               const void* weight, const void* bias, int param_dtype, float eps, void* out,
                               float* mean_out, float* rstd_out, void* stream) {
   if (const int rc = check_rows(dtype, param_dtype, rows, cols)) return rc;
-  if (!(eps >= 0.0f) || x_stride < 0) return DET_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f && eps < INFINITY) || x_stride < 0) return DET_ERR_INVALID_ARG;
   if (rows == 0) return DET_OK;
   if (!x || !out) return DET_ERR_INVALID_ARG;
   if (misaligned(x, dtype) || misaligned(out, dtype) || misaligned(weight, param_dtype) ||

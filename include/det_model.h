@@ -212,10 +212,10 @@ int det_embedding_backward(const void* grad, int dtype, int64_t n, int64_t dim, 
  *   out     device, rows x cols of dtype, contiguous (written); may be x where
  *           x_stride is cols
  *   mean_out, rstd_out  device, rows floats each; either may be NULL
- * A row that holds NaN or an infinity has NaN results.  So may one whose sum, or whose
- * sum of squares, passes the range of 32 bits.
+ * A row that holds NaN or an infinity has NaN in out.  So has one whose sum, or whose
+ * sum of squares of x - mean (plus eps), passes the range of 32 bits.
  * Limits: rows < 2^31, 1 <= cols <= DET_MAX_NORM_COLS (rows of no columns are
- * refused unless there is no row), eps >= 0.
+ * refused unless there is no row), eps finite and not negative.
  */
 #define DET_MAX_NORM_COLS 16384
 int det_layer_norm(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_stride, const void* weight,
