@@ -31,6 +31,7 @@
 // 32-bit instructions, and whole pieces have no conditions.  8 x 4,096 x 2,048 in bf16: 80 us, 5.0 TB/s
 // (gradient 139 us, 4.8 TB/s), at 47% of the issue slots: a CTA fills the SM's shared memory, and its 18
 // warps wait for each other twice a round.
+#include "../../include/det_test_hooks.h"
 #include "det_model.cuh"
 
 #include <algorithm>
@@ -58,6 +59,8 @@ struct Shape {
   int time, channels;
   const int32_t* lengths;
   int log2_ranks;     // CTAs of a cluster
+  int withheld;       // the round whose message the cluster's first CTA never sends (test hook), else -1
+  unsigned long long wait_ns;
 };
 
 // ---------------------------------------------------------------------------
@@ -257,10 +260,10 @@ __device__ __forceinline__ void copy_to(int rank, void* to, const void* from, un
 }
 // Writes to shared memory before it are seen by copies after it.
 __device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Waits for a phase of messages, for about kWaitNs at most.  (The timer is read after
+// Waits for a phase of messages, for about wait_ns at most.  (The timer is read after
 // many polls only: reading it takes as long as a message.)
 template <bool CLUSTER>
-__device__ __forceinline__ bool messages_in(unsigned long long* bar, unsigned phase) {
+__device__ __forceinline__ bool messages_in(unsigned long long* bar, unsigned phase, unsigned long long wait_ns) {
   unsigned long long t0 = 0;
   for (unsigned polls = 1;; ++polls) {
     unsigned done;
@@ -278,7 +281,7 @@ __device__ __forceinline__ bool messages_in(unsigned long long* bar, unsigned ph
     if ((polls & 1023u) == 0) {
       const unsigned long long now = globaltimer();
       if (t0 == 0) t0 = now;
-      else if (now - t0 > kWaitNs) return false;
+      else if (now - t0 > wait_ns) return false;
     }
   }
 }
@@ -453,14 +456,25 @@ template <int VEC> struct Ring {
 // four rounds have places: a CTA may be told of round k + 2 while it still reads those
 // of k and k - 1.  (A CTA sends round k + 4 after it has heard of everyone's round k + 2, which
 // is sent after round k has been heard: by then its own place is free too.)
+// A wait that gives up is the CTA's last: it is `lost`, and waits no more.  It sends one round more at most (the argument above
+// holds for that one), so that no message can be taken for another round's.  The others run out of their own waits
+// then, if they have rounds left.
 template <typename V>
 struct Messages {
   alignas(16) Map<V> mine[4][32];
   Map<V> from[4][kMaxCluster][32];
   unsigned long long bar[4];
+  int lost;
 };
+// To how many CTAs the message of this round goes: all of the cluster's, or none.  (Asked for before the round's maps have come,
+// where the warp waits anyway, and used as a bound: a branch around the sending took 2% of a long sequence's time.)
 template <typename V, typename PLACE>
-__device__ __forceinline__ void send(Messages<V>& box, const PLACE& me, int round, const Map<V>& map) {
+__device__ __forceinline__ int receivers(const Messages<V>& box, const PLACE& me, int round, int withheld) {
+  const bool none = __shfl_sync(0xffffffffu, *(volatile const int*)&box.lost, 0) || (round == withheld && me.rank == 0);
+  return none ? 0 : me.ranks;
+}
+template <typename V, typename PLACE>
+__device__ __forceinline__ void send(Messages<V>& box, const PLACE& me, int round, const Map<V>& map, int to) {
   const int k = round & 3;
   if (me.ranks == 1) {                 // no cluster: its instructions must not be used
     box.from[k][0][me.lane] = map;
@@ -470,19 +484,24 @@ __device__ __forceinline__ void send(Messages<V>& box, const PLACE& me, int roun
   }
   box.mine[k][me.lane] = map;
   fence_copies();
-  if (me.lane == 0) mbar_arrive_expect_tx(&box.bar[k], me.ranks * 32 * (unsigned)sizeof(Map<V>));
+  if (me.lane < min(to, 1)) mbar_arrive_expect_tx(&box.bar[k], me.ranks * 32 * (unsigned)sizeof(Map<V>));
   __syncwarp();
-  if (me.lane < me.ranks)
+  if (me.lane < to)
     copy_to(me.lane, &box.from[k][me.rank][0], &box.mine[k][0], 32 * (unsigned)sizeof(Map<V>), &box.bar[k]);
 }
 // The state (or what comes back) at the CTA's block, from the one at the cluster's
 // blocks, v, which moves on past them.  BACK: from the last block to the first.
 template <int FORM, bool BACK, typename V, typename PLACE>
-__device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int round, V& v, bool& lost) {
+__device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int round, V& v, bool& lost,
+                                     unsigned long long wait_ns) {
   const int k = round & 3;
   const unsigned phase = round >> 2 & 1;
-  lost = lost || !(me.ranks == 1 ? messages_in<false>(&box.bar[k], phase) : messages_in<true>(&box.bar[k], phase));
-  if (lost) both(v, __int_as_float(0x7fffffff));
+  lost = lost || !(me.ranks == 1 ? messages_in<false>(&box.bar[k], phase, wait_ns)
+                                 : messages_in<true>(&box.bar[k], phase, wait_ns));
+  if (lost) {
+    both(v, __int_as_float(0x7fffffff));
+    if (me.lane == 0) box.lost = 1;
+  }
   V here = v;
   const int first = BACK ? me.ranks - 1 : 0, by = BACK ? -1 : 1;
   for (int j = 0, r = first; j < me.ranks; ++j, r += by) {
@@ -491,6 +510,17 @@ __device__ __forceinline__ V receive(Messages<V>& box, const PLACE& me, int roun
     v = after_block<FORM>(v, q.A, q.H);
   }
   return here;
+}
+
+// A cluster's end: no CTA leaves before what it was sent has come.  One that has heard every round has it all; a lost one
+// gives what was sent before the barrier a millisecond.
+template <typename V>
+__device__ __forceinline__ void leave(const Messages<V>& box) {
+  cluster_arrive();
+  cluster_wait();
+  if (box.lost)
+    for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -525,6 +555,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
   __shared__ Map<V> s_map[2][kWorkers][32];              // of the pieces; then A: the state a piece begins with
   __shared__ Messages<V> s_box;
   if (threadIdx.x < 4) mbar_init(&s_box.bar[threadIdx.x], 1);
+  if (threadIdx.x == 0) s_box.lost = 0;
   if (shape.log2_ranks > 0) cluster_arrive();            // a box is written only after its CTA has come here
   dep_wait();
   dep_launch();
@@ -542,6 +573,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
     // tells of the CTA's blocks
     each_round(me.rounds, [&](auto parity, int k) {
       constexpr int P = decltype(parity)::value;
+      const int to = receivers(s_box, me, k, shape.withheld);
       join<kMapsIn + P>(threads);
       Map<V> map;
       both(map.A, 1.0f);
@@ -559,7 +591,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
             map.A = mul(map.A, q[w].A);
           }
       }
-      send(s_box, me, k, map);
+      send(s_box, me, k, map, to);
     });
   } else if (me.warp > me.workers) {
     // hears of the cluster's, and hands out states
@@ -568,7 +600,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
     each_round(me.rounds, [&](auto parity, int k) {
       constexpr int P = decltype(parity)::value;
       join<kMapsIn + P>(threads);
-      V h = receive<FORM, false>(s_box, me, k, carry, lost);
+      V h = receive<FORM, false>(s_box, me, k, carry, lost, shape.wait_ns);
       const int block = k * me.ranks + me.rank;
       if (states && block < kept) store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, h, me.n);
 #pragma unroll 1
@@ -666,10 +698,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
       for (int i = 0; i < kSteps; ++i)
         if (me.n > 0 && t0 + i < time) store_word<T, VEC != 0>(out + ((long long)me.b * time + t0 + i) * channels + me.c, 0u, me.n);
   }
-  if (shape.log2_ranks > 0) {          // no CTA leaves before what it was sent has come
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (shape.log2_ranks > 0) leave(s_box);
 }
 
 // A thread's word of channels of a sequence of at most one piece: the same
@@ -793,6 +822,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
   __shared__ V s_back[2][kWorkers][32];                  // M; then what comes back behind a piece
   __shared__ Messages<V> s_box;                          // (A, M) of the CTAs' blocks
   if (threadIdx.x < 4) mbar_init(&s_box.bar[threadIdx.x], 1);
+  if (threadIdx.x == 0) s_box.lost = 0;
   if (shape.log2_ranks > 0) cluster_arrive();
   dep_wait();
   dep_launch();
@@ -806,6 +836,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
   if (me.warp == me.workers) {
     each_round(me.rounds, [&](auto parity, int k) {
       constexpr int P = decltype(parity)::value;
+      const int to = receivers(s_box, me, k, shape.withheld);
       join<kMapsIn + P>(threads);
       Map<V> map;
       both(map.A, 1.0f);
@@ -826,7 +857,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
             map.A = mul(map.A, A[w]);
           }
       }
-      send(s_box, me, k, map);
+      send(s_box, me, k, map, to);
     });
   } else if (me.warp > me.workers) {
     const int kept = (time + kBlock - 1) / kBlock;
@@ -858,7 +889,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
             h = after(h, q[w].A, q[w].H);
           }
       }
-      V m = receive<FORM, true>(s_box, me, k, carry, lost);
+      V m = receive<FORM, true>(s_box, me, k, carry, lost, shape.wait_ns);
 #pragma unroll 1
       for (int w0 = (me.workers - 1) & ~3; w0 >= 0; w0 -= 4) {
         V A[4], M[4];
@@ -954,10 +985,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
       give(parity, k);
     });
   }
-  if (shape.log2_ranks > 0) {
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (shape.log2_ranks > 0) leave(s_box);
 }
 
 template <typename T, int FORM, bool VEC>
@@ -1116,10 +1144,21 @@ int check_shape(int dtype, int form, int64_t batch, int64_t time, int64_t channe
 bool misaligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % model_elem_size(dtype) != 0; }
 bool misaligned_floats(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 != 0; }
 
+// Test hook state (det_test_hooks.h): host-side, read when a call is enqueued.
+int g_withheld = -1;
+unsigned long long g_wait_ns = kWaitNs;
+
 }  // namespace
 }  // namespace det
 
 using namespace det;
+
+extern "C" int det_test_recurrence_withhold(int64_t round, uint64_t timeout_ns) {
+  if (round >= 0 && (round > INT32_MAX || timeout_ns == 0 || timeout_ns > kWaitNs)) return DET_ERR_INVALID_ARG;
+  g_withheld = round < 0 ? -1 : (int)round;
+  g_wait_ns = round < 0 ? kWaitNs : timeout_ns;
+  return DET_OK;
+}
 
 #define DET_RECURRENCE_FORM(fn, T, VEC, ...) \
   (form == DET_GATE_DECAY ? fn<T, DET_GATE_DECAY, VEC>(__VA_ARGS__) : fn<T, DET_GATE_SIGMOID, VEC>(__VA_ARGS__))
@@ -1146,7 +1185,7 @@ extern "C" int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t 
     return DET_ERR_INVALID_ARG;
   const int how = reading(dtype, {x, gate, out}, {x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vx = {x, x_stride_b, x_stride_t}, vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0};
+  const Shape shape = {(int)time, (int)channels, lengths, 0, g_withheld, g_wait_ns};
   const cudaStream_t s = as_stream(stream);
   return DET_RECURRENCE_PICK(forward, vx, vg, shape, (int)batch, initial, out, final_out, states_out, s);
 }
@@ -1170,7 +1209,7 @@ extern "C" int det_linear_recurrence_backward(const void* grad, int64_t grad_str
                           {grad_stride_b, grad_stride_t, x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vd = {grad, grad_stride_b, grad_stride_t}, vx = {x, x_stride_b, x_stride_t},
              vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0};
+  const Shape shape = {(int)time, (int)channels, lengths, 0, g_withheld, g_wait_ns};
   const cudaStream_t s = as_stream(stream);
   return DET_RECURRENCE_PICK(backward, vd, vx, vg, shape, (int)batch, states, grad_final, grad_x, grad_gate, grad_initial, s);
 }

@@ -86,6 +86,7 @@ _SIGNATURES = {
     "det_profile_event_name": (ctypes.c_char_p, [_int]),
     "det_launch_count": (ctypes.c_ulonglong, []),
     "det_test_scan_withhold": (_int, [_i64, ctypes.c_uint64]),
+    "det_test_recurrence_withhold": (_int, [_i64, ctypes.c_uint64]),
     "det_profile_add_rate_probe": (_int, [_int, _int, _vp, _vp, ctypes.POINTER(ctypes.c_ulonglong)]),
     "det_atomic_sum": (_int, [_vp, _i64, _int, _vp, _vp]),
     "det_atomic_scatter_add": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _vp]),

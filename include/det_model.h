@@ -266,6 +266,8 @@ int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x
  * Products of up to DET_RECURRENCE_SPAN decays are formed: where one passes the
  * range of 32 bits (decays well above 1), states may become infinite or NaN before they
  * would step by step.  A state that is infinite or NaN leaves later states infinite or NaN.
+ * So does, as the only sign of it, a part of a sequence that was not told the states of the parts
+ * before it in time (2 s; the kernel ends all the same), here and in the gradient.
  * Limits: batch <= 65,535, time < 2^31 - 2^16, channels < 2^31 - 2^16; strides are not negative.
  */
 #define DET_GATE_DECAY 0
