@@ -59,6 +59,8 @@ struct Shape {
   int time, channels;
   const int32_t* lengths;
   int log2_ranks;     // CTAs of a cluster
+  float lowest_gate;  // -87, as a value that the compiler does not know: it would work out what belongs to it by itself,
+                      // and one step beside the hardware's approximations
   int withheld;       // the round whose message the cluster's first CTA never sends (test hook), else -1
   unsigned long long wait_ns;
 };
@@ -163,9 +165,10 @@ __device__ __forceinline__ void store_state(float* p, V v, int n) {
 //
 // Sigmoid: with e = exp(-z), a = 1 / (1 + e) and 1 - a = e a, which keeps the
 // relative accuracy of both where a difference from 1 would lose it.  In 16 bits e
-// and the reciprocal are the hardware's approximations (a and 1 - a off by at most
-// 8 + |z| units of 2^-24); z is held at -87 and more, so that e stays finite, and
-// the a that belongs to -87 is taken off (`floor`, 2^-125): a gate of -inf closes
+// and the reciprocal are the hardware's approximations: a and 1 - a are off by at most
+// 8 + 1.22 |z| units of 2^-24 of their own size (the rounded exponent counts |z| times; a step of a bf16 gate
+// changes them by 2^-9 |z|, and 12 instructions more a gate would be half of a step's).  z is held at -87 and more, so
+// that e stays finite, and the a that belongs to -87 is taken off (`floor`, below 2^-125): a gate of -inf closes
 // for good.  In 32 bits expf, and the smaller one of the two by a division.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -187,10 +190,10 @@ template <typename T, int FORM>
 struct Gates {
   using V = LaneV<T>;
   V floor;
-  __device__ __forceinline__ Gates() {
+  __device__ __forceinline__ explicit Gates(float lowest) {
     both(floor, 0.0f);
     if constexpr (FORM == DET_GATE_SIGMOID && sizeof(T) == 2) {
-      const float e = exp2_approx(__fmul_rn(kLowestGate, -kLog2e));
+      const float e = exp2_approx(__fmul_rn(lowest, -kLog2e));
       const float a = -rcp_approx(__fadd_rn(e, 1.0f));
       floor = two(a, a);
     }
@@ -623,7 +626,7 @@ recurrence_kernel(View x, View gate, Shape shape, const float* initial, T* out, 
         store_state<CH>(states + ((long long)me.b * kept + block) * channels + me.c, carry, me.n);
     if (final_out && len == 0 && me.rank == 0) store_state<CH>(final_out + row, carry, me.n);
   } else {
-    const Gates<T, FORM> gates;
+    const Gates<T, FORM> gates(shape.lowest_gate);
     const int at = me.rank * kBlock + me.warp * kSteps;
     // the rounds before this one have whole pieces here
     const int whole = me.whole && len >= at + kSteps ? (len - at - kSteps) / me.stride + 1 : 0;
@@ -731,7 +734,7 @@ recurrence_short_kernel(View x, View gate, Shape shape, const float* initial, T*
   constexpr int CH = Lane<T>::CH, STEPS = kSteps;
   dep_wait();
   dep_launch();
-  const Gates<T, FORM> gates;
+  const Gates<T, FORM> gates(shape.lowest_gate);
   const Word me(shape, T());
   if (me.n <= 0) return;
   const long long row = (long long)me.b * shape.channels + me.c;
@@ -910,7 +913,7 @@ recurrence_grad_kernel(View grad, View x, View gate, Shape shape, const float* s
     });
     if (grad_initial && len == 0 && me.rank == 0) store_state<CH>(grad_initial + row, carry, me.n);
   } else {
-    const Gates<T, FORM> gates;
+    const Gates<T, FORM> gates(shape.lowest_gate);
     const int at = me.rank * kBlock + me.warp * kSteps, last = (me.rounds - 1) * me.stride + at;
     // from this round on the pieces are whole
     const int whole = me.whole && len >= at + kSteps ? me.rounds - 1 - (len - at - kSteps) / me.stride : me.rounds;
@@ -996,7 +999,7 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
   constexpr int CH = Lane<T>::CH, STEPS = kSteps;
   dep_wait();
   dep_launch();
-  const Gates<T, FORM> gates;
+  const Gates<T, FORM> gates(shape.lowest_gate);
   const Word me(shape, T());
   if (me.n <= 0) return;
   const long long row = (long long)me.b * shape.channels + me.c;
@@ -1185,7 +1188,7 @@ extern "C" int det_linear_recurrence(const void* x, int64_t x_stride_b, int64_t 
     return DET_ERR_INVALID_ARG;
   const int how = reading(dtype, {x, gate, out}, {x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vx = {x, x_stride_b, x_stride_t}, vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0, g_withheld, g_wait_ns};
+  const Shape shape = {(int)time, (int)channels, lengths, 0, kLowestGate, g_withheld, g_wait_ns};
   const cudaStream_t s = as_stream(stream);
   return DET_RECURRENCE_PICK(forward, vx, vg, shape, (int)batch, initial, out, final_out, states_out, s);
 }
@@ -1209,7 +1212,7 @@ extern "C" int det_linear_recurrence_backward(const void* grad, int64_t grad_str
                           {grad_stride_b, grad_stride_t, x_stride_b, x_stride_t, gate_stride_b, gate_stride_t, channels});
   const View vd = {grad, grad_stride_b, grad_stride_t}, vx = {x, x_stride_b, x_stride_t},
              vg = {gate, gate_stride_b, gate_stride_t};
-  const Shape shape = {(int)time, (int)channels, lengths, 0, g_withheld, g_wait_ns};
+  const Shape shape = {(int)time, (int)channels, lengths, 0, kLowestGate, g_withheld, g_wait_ns};
   const cudaStream_t s = as_stream(stream);
   return DET_RECURRENCE_PICK(backward, vd, vx, vg, shape, (int)batch, states, grad_final, grad_x, grad_gate, grad_initial, s);
 }
