@@ -22,6 +22,9 @@
  *   caller's.
  * - There is no device status word: what a kernel finds out of range it
  *   skips, by the rule stated at the call.
+ * - "Not read" is said of values.  A row that starts inside an aligned 16-byte
+ *   vector may be fetched by the vectors, or 4-byte words, that hold it; what else
+ *   they hold, before the row and after it, is discarded.
  */
 #ifndef DET_MODEL_H
 #define DET_MODEL_H
@@ -250,6 +253,10 @@ int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x
  * in 32 bits; out is rounded once.  The bits of out[t] are a function of the initial
  * state and of the steps up to t alone: a sequence gives the same bits whatever
  * follows.  (One that is cut and resumed from its final state gives other roundings.)
+ * a and 1 - a of the sigmoid form are off by at most 8 units of 2^-24 of their size
+ * for DET_F32.  For 16-bit gates, whose own steps move them by far more, the
+ * exponential and the reciprocal are the hardware's: 8 + 1.22 |gate| units, and a is
+ * less by 2^-125 (0 from a gate of -87 down), in final_out and states_out too.
  *   x, gate   device, batch x time x channels of dtype; strides in elements, 1
  *             along channels
  *   initial   device, batch x channels floats, contiguous, or NULL (0)
@@ -263,9 +270,11 @@ int det_layer_norm_backward(const void* grad, int64_t grad_stride, const void* x
  *   states_out  device, batch x ceil(time / DET_RECURRENCE_KEEP) x channels floats:
  *             the state before every DET_RECURRENCE_KEEP-th step, for the gradient
  *             (past a sequence's end: its final state), or NULL
- * Products of up to DET_RECURRENCE_SPAN decays are formed: where one passes the
- * range of 32 bits (decays well above 1), states may become infinite or NaN before they
- * would step by step.  A state that is infinite or NaN leaves later states infinite or NaN.
+ * Products of up to DET_RECURRENCE_SPAN decays are formed, here and in the gradient: where
+ * one passes the range of 32 bits (decays well above 1), results may become infinite or NaN
+ * before they would step by step, and where one falls below it and decays well above 1
+ * follow, what came before is lost early.  A state that is infinite or NaN leaves later
+ * states infinite or NaN.
  * So does, as the only sign of it, a part of a sequence that was not told the states of the parts
  * before it in time (2 s; the kernel ends all the same), here and in the gradient.
  * Limits: batch <= 65,535, time < 2^31 - 2^16, channels < 2^31 - 2^16; strides are not negative.
