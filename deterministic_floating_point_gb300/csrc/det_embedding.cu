@@ -297,9 +297,9 @@ struct LongRun {
 };
 
 // The workspace: that of the library's sort, or a header and the order and runs of the
-// CTA's; then long runs and nodes.
+// small one's; then long runs and nodes.
 struct EmbedPlan {
-  bool one_cta;
+  bool small_sort;
   SortPlan sort;
   size_t perm, run_start, run_end, runs, nodes, total;
 };
@@ -307,9 +307,9 @@ EmbedPlan embed_plan(long long n, long long vocab, long long dim) {
   EmbedPlan p;
   // (gradient of 20,000 x 2,048 in bf16 for 65,536 rows: 97 us, 134 by the library's sort; of 32,768 places of one
   // token, which one CTA sorts alone, 107 against 48.)
-  p.one_cta = n <= kSortMost && vocab <= kSortVocab;
+  p.small_sort = n <= kSortMost && vocab <= kSortVocab;
   size_t at;
-  if (p.one_cta) {
+  if (p.small_sort) {
     p.perm = kHeaderBytes;
     p.run_start = align_up(p.perm + (size_t)n * 4, 256);
     p.run_end = align_up(p.run_start + (size_t)vocab * 4, 256);
@@ -787,7 +787,7 @@ int join(const GradArgs& a, int n, void* out, int accumulate, cudaStream_t s) {
   return e == cudaSuccess ? DET_OK : cuda_fail(e, "det_embedding_join");
 }
 
-int cta_sort(const GradArgs& a, int n, int vocab, void* table, size_t bytes, cudaStream_t s) {
+int small_sort(const GradArgs& a, int n, int vocab, void* table, size_t bytes, cudaStream_t s) {
   SortArgs g;
   g.tokens = a.tokens;
   g.n = n;
@@ -886,13 +886,13 @@ extern "C" int det_embedding_backward(const void* grad, int dtype, int64_t n, in
   a.n_valid = &header->n_valid;
   a.clear_from = (int)vocab;                                     // nothing
   a.long_runs = &header->long_segs;                              // cleared by either sort, neither of which uses it
-  if (plan.one_cta) {
+  if (plan.small_sort) {
     a.perm = reinterpret_cast<int32_t*>(w + plan.perm);
     a.run_start = reinterpret_cast<int32_t*>(w + plan.run_start);
     a.run_end = reinterpret_cast<int32_t*>(w + plan.run_end);
     const size_t row_bytes = (size_t)dim * model_elem_size(table_dtype);
     if (!accumulate) a.clear_from = (int)std::min<int64_t>(vocab, (int64_t)(kClearWithSort / row_bytes) + 1);
-    if (const int rc = cta_sort(a, (int)n, (int)vocab, accumulate ? nullptr : grad_table, a.clear_from * row_bytes, s)) return rc;
+    if (const int rc = small_sort(a, (int)n, (int)vocab, accumulate ? nullptr : grad_table, a.clear_from * row_bytes, s)) return rc;
   } else {
     int buffer = 0;
     if (const int rc = enqueue_sort(plan.sort, workspace, tokens, 0, nullptr, nullptr, s, &buffer)) return rc;

@@ -74,6 +74,19 @@ template <> struct Word<__half> {
   }
 };
 
+// Sums of two 32-bit lanes in a 64-bit register.
+__device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b,
+                                                        unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Word w of a row (elements N w, N w + 1), with masked logits past its end.
 template <typename T>
 __device__ __forceinline__ unsigned load_word(const T* row, long long w, long long vocab, bool words_aligned) {
