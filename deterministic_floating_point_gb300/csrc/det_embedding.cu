@@ -19,8 +19,9 @@
 //
 // Bytes bound both.  16,384 rows of 2,048 in 32 bits to bf16: 20 us (116 MB, some rows many times: 17 at the copy's
 // rate), one launch.  The gradient of 16,384 x 2,048 for 65,536 rows in bf16 (332 MB, 50 us at that rate) takes 77:
-// 18 for the sort, which the clear of 96 MB fills, 49 for the sums and the rest of the clear, 5 for the join, and
-// starts and ends of launches.
+// 18 for the sort, which the clear of 96 MB fills, 49 for the sums and the rest of the clear, and about 10 for the join,
+// whose launch overlaps the sums' end (11 to 17 by itself, by what the tokens are).  Added to a table in bf16, 73; at odd
+// widths (2,047) 109.  (Figures below that compare two ways were taken side by side when the choice was made.)
 #include "det_sort.cuh"
 #include "det_model.cuh"
 
@@ -305,8 +306,8 @@ struct EmbedPlan {
 };
 EmbedPlan embed_plan(long long n, long long vocab, long long dim) {
   EmbedPlan p;
-  // (gradient of 20,000 x 2,048 in bf16 for 65,536 rows: 97 us, 134 by the library's sort; of 32,768 places of one
-  // token, which one CTA sorts alone, 107 against 48.)
+  // (gradient of 20,000 x 2,048 in bf16 for 65,536 rows: 97 us, 134 by the library's sort.  32,768 places of one token,
+  // which one CTA sorts alone, 2,048 wide: 150 us for 65,536 rows and 123 for 3; by the library's sort 362 and 93.)
   p.small_sort = n <= kSortMost && vocab <= kSortVocab;
   size_t at;
   if (p.small_sort) {

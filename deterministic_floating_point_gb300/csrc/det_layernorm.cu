@@ -13,8 +13,9 @@
 // a second launch joins.  Row r belongs to partial sum r mod parts, and parts is a
 // function of rows and cols, so the order of every sum is too.
 //
-// Bytes bound it: 16,384 x 4,096 in bf16 take 42 us (a copy of as many bytes 45), 60% of the issue slots,
-// the gradients 73 (5.5 TB/s); 65,536 x 4,096 in bf16 166 and 266 us, 6.5 and 6.1 TB/s.  A few rows: the launch and
+// Bytes bound it: 16,384 x 4,096 in bf16 take 42 us (a copy of as many bytes 45), 56% of the issue slots,
+// the gradients 73 (5.5 TB/s); 65,536 x 4,096 in bf16 169 and 262 us, 6.4 and 6.1 TB/s.  (Figures
+// below that compare two ways were taken side by side when the choice was made.)  A few rows: the launch and
 // one row's chain of a copy, two sums across the group (one in the gradient) and a store, about 6 us.
 #include "det_model.cuh"
 

@@ -28,8 +28,8 @@
 // What bounds it: bytes, once an element costs few enough instructions (at the
 // copy's rate an SM's schedulers have 33 slots for each element forward and
 // twice that backward).  So two 16-bit channels of a word are worked on by packed
-// 32-bit instructions, and whole pieces have no conditions.  8 x 4,096 x 2,048 in bf16: 80 us, 5.0 TB/s
-// (gradient 139 us, 4.8 TB/s), at 47% of the issue slots: a CTA fills the SM's shared memory, and its 18
+// 32-bit instructions, and whole pieces have no conditions.  8 x 4,096 x 2,048 in bf16: 75 us, 5.4 TB/s
+// (gradient 135 us, 5.0 TB/s), at 47% of the issue slots: a CTA fills the SM's shared memory, and its 18
 // warps wait for each other twice a round.
 #include "../../include/det_test_hooks.h"
 #include "det_model.cuh"
@@ -166,8 +166,8 @@ __device__ __forceinline__ void store_state(float* p, V v, int n) {
 // Sigmoid: with e = exp(-z), a = 1 / (1 + e) and 1 - a = e a, which keeps the
 // relative accuracy of both where a difference from 1 would lose it.  In 16 bits e
 // and the reciprocal are the hardware's approximations: a and 1 - a are off by at most
-// 8 + 1.22 |z| units of 2^-24 of their own size (the rounded exponent counts |z| times; a step of a bf16 gate
-// changes them by 2^-9 |z|, and 12 instructions more a gate would be half of a step's).  z is held at -87 and more, so
+// 8 + 1.22 |z| units of 2^-24 of their own size (the rounded exponent counts |z| times; half a step of a bf16 gate
+// moves them by 2^-9 |z|, of an f16 one by 2^-12 |z|, so a reduction of every gate's range would show in nothing).  z is held at -87 and more, so
 // that e stays finite, and the a that belongs to -87 is taken off (`floor`, below 2^-125): a gate of -inf closes
 // for good.  In 32 bits expf, and the smaller one of the two by a division.
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -1023,8 +1023,8 @@ recurrence_grad_short_kernel(View grad, View x, View gate, Shape shape, const fl
 // CTAs that share a sequence (a cluster), as a logarithm: what costs the least in
 // rounds of blocks, with two more for a CTA's start, over the waves of clusters that
 // are resident at a time.  (Of 8 CTAs fewer clusters fit than the SMs' number lets
-// expect: 16 of them took two waves.)  The bits do not depend on it.  (1 x 65,536 x 256 in bf16 with 1, 2, 4, 8 CTAs:
-// 563, 311, 164, 92 us.)
+// expect: 16 of them took two waves.)  The bits do not depend on it.  (1 x 65,536 x 256 in bf16 with 1, 2, 4, 8 CTAs,
+// when this was chosen: 563, 311, 164, 92 us; with 8 now 84.)
 int choose_ranks(const void* kernel, cudaLaunchConfig_t cfg, long long sequences, int time) {
   static std::mutex mu;
   static std::map<std::tuple<const void*, int, int, unsigned, size_t>, int> cache;
@@ -1128,7 +1128,7 @@ int backward(const View& grad, const View& x, const View& gate, const Shape& sha
 }
 
 // How rows are read: 2 where all start on 16 bytes and are whole vectors, 1 where all
-// start on a word and are whole words, 0 else.  (8 x 4,096 steps in bf16: 2,048 channels 80 us, 2,046 121, 2,047 182.)
+// start on a word and are whole words, 0 else.  (8 x 4,096 steps in bf16: 2,048 channels 75 us, 2,046 116, 2,047 178.)
 int reading(int dtype, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> strides) {
   uintptr_t all = 0;
   for (const void* p : pointers) all |= reinterpret_cast<uintptr_t>(p);
