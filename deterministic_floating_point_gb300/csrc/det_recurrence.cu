@@ -166,10 +166,12 @@ __device__ __forceinline__ void store_state(float* p, V v, int n) {
 // Sigmoid: with e = exp(-z), a = 1 / (1 + e) and 1 - a = e a, which keeps the
 // relative accuracy of both where a difference from 1 would lose it.  In 16 bits e
 // and the reciprocal are the hardware's approximations: a and 1 - a are off by at most
-// 8 + 1.22 |z| units of 2^-24 of their own size (the rounded exponent counts |z| times; half a step of a bf16 gate
-// moves them by 2^-9 |z|, of an f16 one by 2^-12 |z|, so a reduction of every gate's range would show in nothing).  z is held at -87 and more, so
-// that e stays finite, and the a that belongs to -87 is taken off (`floor`, below 2^-125): a gate of -inf closes
-// for good.  In 32 bits expf, and the smaller one of the two by a division.
+// 8 + 1.22 |z| units of 2^-24 of their own size.  (The rounded exponent counts |z|
+// times.  Half a step of a bf16 gate moves them by 2^-9 |z|, of an f16 one by 2^-12 |z|,
+// so a reduction of every gate's range would show in nothing.)  z is held at -87 and
+// more, so that e stays finite, and the a that belongs to -87 is taken off (`floor`,
+// below 2^-125): a gate of -inf closes for good.  In 32 bits expf, and the smaller one
+// of the two by a division.
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -38,9 +38,9 @@ int det_test_scan_withhold(int64_t chunk, uint64_t timeout_ns);
  * det_linear_recurrence_backward call of more than 8 steps enqueued afterwards
  * never sends the message of round `round` from the first of the CTAs that share
  * a sequence (a round is one block of DET_RECURRENCE_KEEP steps for each of them;
- * where a sequence has one CTA nothing is withheld), and its waits give up after about `timeout_ns` nanoseconds instead
- * of 2 s.  The launch ends by itself, and results are NaN from that round on
- * (det_model.h).
+ * where a sequence has one CTA nothing is withheld), and its waits give up after
+ * about `timeout_ns` nanoseconds instead of 2 s.  The launch ends by itself, and
+ * results are NaN from that round on (det_model.h).
  *   round       >= 0 to set the hook; < 0 clears it
  *   timeout_ns  1 .. 2e9 when setting; ignored when clearing
  * Returns DET_OK, or DET_ERR_INVALID_ARG for values outside those ranges. */
